@@ -75,8 +75,13 @@ typedef enum mdw_status {
 typedef enum mdw_format {
   MDW_FMT_BF16 = 1,
   MDW_FMT_FP8_E4M3_ROWSCALE = 2,
-  MDW_FMT_MXFP4_E2M1_E8M0_B32 = 3
+  MDW_FMT_MXFP4_E2M1_E8M0_B32 = 3,
+  MDW_FMT_INT4_GROUP = 4,          /* mdw_w4_weights */
+  MDW_FMT_KV_PAGED = 5             /* mdw_kv_cache */
 } mdw_format;
+
+/* Element types of the attention sub-layer's tensors. */
+typedef enum mdw_dtype { MDW_DT_BF16 = 1, MDW_DT_F16 = 2, MDW_DT_F32 = 3, MDW_DT_E4M3 = 4 } mdw_dtype;
 
 #define MDW_MAGIC 0x3157444Du /* "MDW1" */
 
@@ -89,6 +94,11 @@ typedef enum mdw_format {
 #define MDW_MAX_TOPK 8
 #define MDW_MAX_M 32
 #define MDW_MAX_VOCAB_TOPK 32
+
+/* Limits of the attention sub-layer's calls. */
+#define MDW_MAX_REQUESTS 4096 /* requests of one mdw_kv_plan / mdw_tree_attention call */
+#define MDW_MAX_TREE 64       /* drafted tokens of one request's tree */
+#define MDW_MAX_GROUP 64      /* query heads per kv head */
 
 /* Weights of one MoE layer. Fill every field; set magic = MDW_MAGIC and
  * fmt = MDW_FMT_MXFP4_E2M1_E8M0_B32. The shared-expert pointers are all NULL (no shared
@@ -329,6 +339,128 @@ mdw_status lm_head_fp8_sample(const mdw_lm_head* head, int32_t M, const void* h_
                               int32_t topk, double temperature, double top_p, const double* u,
                               int32_t* token_out, int32_t* topk_idx, float* topk_val, void* ws,
                               size_t ws_bytes, mdw_stream_t stream);
+
+/* ---------------------------------------------------------------------------------- */
+/* The attention sub-layer of a verify window
+ *
+ * What a decode step runs around the MoE layers and the head for every window of drafted
+ * tokens: the dense projections on int4 weights, the plan of the paged key/value cache, the
+ * writer of the cache and the attention of a tree of drafted tokens over it.
+ *
+ * These calls follow the conventions above, with two additions:
+ *   - Row strides are in elements; a row starts on a 16-byte boundary unless said otherwise,
+ *     and its elements are contiguous, so q, k and v can be slices of one projection's rows.
+ *   - `status`: NULL, or a device uint32 that the CALLER clears. A call that meets bad data on
+ *     the device (lengths, page ids, slots, parents) stores an mdw_status there if the word is
+ *     still 0, computes nothing for what the bad data governs, and accesses nothing outside
+ *     the arrays it was given. No call clears the word, so one check serves a whole step
+ *     (mdw_device_status() reads it when it is 16-byte aligned). */
+
+/* A dense weight in int4 with group scales: w[n][k] = (code - zero) * scale, per group of
+ * `group` consecutive k. fmt MDW_FMT_INT4_GROUP. */
+typedef struct mdw_w4_weights {
+  uint32_t magic;
+  int32_t fmt;
+  int32_t n;             /* output features, >= 1 */
+  int32_t k;             /* input features, a multiple of group */
+  int32_t group;         /* 32, 64 or 128 */
+  int32_t dtype;         /* MDW_DT_BF16 or MDW_DT_F16: scale, x, bias and residual */
+  const void* q;         /* uint8 [n][k/2]: byte k/2 holds the code 0..15 of k in its low nibble (k even)
+                            or high nibble (k odd) */
+  const void* scale;     /* [n][k/group] in dtype */
+  const void* zero;      /* uint8 [n][k/group] zero codes 0..15, or NULL: 8 everywhere */
+} mdw_w4_weights;
+
+/* y[t][n] = sum_k x[t][k] * (code[n][k] - zero[n][k/group]) * scale[n][k/group]
+ *           (+ bias[n]) (+ residual[t][n])    for a window of 1 <= M <= MDW_MAX_M tokens.
+ * Products are exact, sums in fp32 in a fixed order (bit-reproducible), rounded once to y's type.
+ * x [M][k] (ldx), y [M][n] (ldy) in w->dtype or MDW_DT_F32, bias [n], residual [M][n] (ldr) in
+ * w->dtype. y, bias and residual need the alignment of their elements only. y may be the
+ * residual itself (same pointer, type and stride); it must not overlap any other argument. */
+mdw_status w4_linear(const mdw_w4_weights* w, int32_t M, const void* x, int64_t ldx, void* y, int64_t ldy,
+                     int32_t y_dtype, const void* bias, const void* residual, int64_t ldr, mdw_stream_t stream);
+
+/* A paged key/value cache: k and v are [num_pages][kv_heads][page_size][head_dim], pages
+ * page_stride elements apart (so both can share one allocation). Slot s is row s % page_size of
+ * page s / page_size. dtype MDW_DT_E4M3 stores x / scale[kv head] in E4M3 (round to nearest
+ * even, saturating). fmt MDW_FMT_KV_PAGED. */
+typedef struct mdw_kv_cache {
+  uint32_t magic;
+  int32_t fmt;
+  int32_t dtype;         /* MDW_DT_BF16, MDW_DT_F16 or MDW_DT_E4M3 */
+  int32_t num_pages;     /* >= 1 */
+  int32_t page_size;     /* 16, 32, 64, 128 or 256 tokens */
+  int32_t kv_heads;      /* >= 1 */
+  int32_t head_dim;      /* 64 or 128 */
+  int32_t reserved;
+  int64_t page_stride;   /* elements, >= kv_heads * page_size * head_dim, 16-byte multiple */
+  void* k;
+  void* v;
+  const float* k_scale;  /* device fp32 [kv_heads] > 0 (E4M3 caches), else NULL */
+  const float* v_scale;
+} mdw_kv_cache;
+
+/* Block tables, slot map, positions and tree masks from request lengths, in one launch.
+ * Request b (1 <= B <= MDW_MAX_REQUESTS) holds ctx_len[b] cached tokens and adds new_len[b]
+ * (either may be 0). With P = page_size, its pages ceil(ctx/P) .. ceil((ctx+new)/P) - 1 are
+ * taken from free_pages, request after request in order, and entered in
+ * block_table[b][0..max_pages); earlier entries are read and never written, later ones left as
+ * they are. The free list itself is not changed: *pages_taken entries at its front are used.
+ *   row_start   int32 [B+1]  prefix sums of new_len (rows of all requests, packed)
+ *   slot_map    int64 [T]    cache slot of each row
+ *   positions   int32 [T]    ctx + depth in the tree (ctx + index without parents)
+ *   tree_mask   NULL or uint64 [T]: bit j = the row sees node j of its request (itself and its
+ *               ancestors; all earlier nodes without parents)
+ *   parents     NULL (a chain) or int32 [T]: the index in the request of each row's parent,
+ *               smaller than the row's own, or -1
+ * With parents or tree_mask every new_len is at most MDW_MAX_TREE. Rows from row_start[B] to T
+ * get slot -1, position -1 and mask 0 (a captured launch can be padded).
+ * Bad lengths (negative, beyond max_pages * P, more rows than T, more pages than num_free,
+ * trees too large) fail the whole plan: status, row_start all 0, slots and positions -1, masks
+ * and pages_taken 0, table untouched. A page id outside [0, num_pages) is entered as -1, its
+ * rows get slot -1 and status is set; a bad parent does the same to its row (mask 0 too) and
+ * the rows below it. */
+mdw_status mdw_kv_plan(int32_t B, const int32_t* ctx_len, const int32_t* new_len, int32_t page_size,
+                       int32_t num_pages, int32_t* block_table, int32_t max_pages, const int32_t* free_pages,
+                       int32_t num_free, const int32_t* parents, int32_t T, int32_t* row_start,
+                       int64_t* slot_map, int32_t* positions, uint64_t* tree_mask, int32_t* pages_taken,
+                       uint32_t* status, mdw_stream_t stream);
+
+/* Writes T rows of keys and values [kv_heads][head_dim] (row strides ldk, ldv) to their slots.
+ * dtype (MDW_DT_BF16 / MDW_DT_F16) is the rows' type: the cache's own, or any of the two for an
+ * E4M3 cache. Slot -1 (padding) is skipped; a slot outside the cache is skipped and sets
+ * MDW_ERR_DEVICE_BOUNDS. The slots of one call are distinct: where one appears twice, which
+ * row's elements it holds afterwards is not defined. */
+mdw_status mdw_kv_write(const mdw_kv_cache* cache, int32_t T, const void* k, int64_t ldk, const void* v,
+                        int64_t ldv, int32_t dtype, const int64_t* slot_map, uint32_t* status,
+                        mdw_stream_t stream);
+
+/* Workspace bytes of mdw_tree_attention; 0 if the arguments are invalid. */
+size_t mdw_tree_attention_workspace_bytes(const mdw_kv_cache* cache, int32_t B, int32_t T, int32_t q_heads,
+                                          int32_t max_new);
+
+/* Attention of drafted tokens over the paged cache, after mdw_kv_write has stored their own
+ * keys and values. Rows row_start[b] .. row_start[b+1] - 1 of q [T][q_heads][head_dim] (row stride
+ * ldq) are the nodes of request b, at cache positions ctx_len[b] + index. A row sees the
+ * ctx_len[b] cached tokens and the nodes j whose bit is set in tree_mask[row] (uint64 [T]; NULL:
+ * the nodes up to itself). Query head h reads kv head h / (q_heads / kv_heads).
+ *   out[row][h] = sum_j softmax_j(scale * q . k_j) v_j    (row stride ldo, q's type)
+ *   lse[row][h] = log sum_j exp(scale * q . k_j)          (fp32 [T][q_heads], or NULL)
+ * over the keys the row sees. Keys it does not see contribute nothing, whatever they hold
+ * (NaN and infinities too); a row that sees none, or only scores of -inf, gives 0 and -inf.
+ * Scores, softmax sums and outputs are fp32; probabilities enter the second product in q's type
+ * (f16 for E4M3 caches).
+ * q_dtype is MDW_DT_BF16 / MDW_DT_F16 and the cache's own type, or any of the two for an E4M3
+ * cache. scale > 0, finite. Every request has at most max_new (1..MDW_MAX_TREE) rows. Rows before
+ * row_start[0] or from row_start[B] on are left as they were. A request with bad lengths or rows
+ * (outside [0, T), more than max_new, beyond max_pages * page_size) is skipped, keys on a page id
+ * outside [0, num_pages) are not seen; both set MDW_ERR_DEVICE_BOUNDS.
+ * ws: workspace, contents arbitrary; not to be shared by calls that may overlap. */
+mdw_status mdw_tree_attention(const mdw_kv_cache* cache, int32_t B, int32_t T, int32_t q_heads, int32_t max_new,
+                              const void* q, int64_t ldq, int32_t q_dtype, void* out, int64_t ldo, float* lse,
+                              const int32_t* block_table, int32_t max_pages, const int32_t* ctx_len,
+                              const int32_t* row_start, const uint64_t* tree_mask, float scale,
+                              uint32_t* status, void* ws, size_t ws_bytes, mdw_stream_t stream);
 
 /* Synchronises `stream`, then returns the device status word that the last call using
  * this workspace left (MDW_OK, MDW_ERR_TIMEOUT or MDW_ERR_DEVICE_BOUNDS), or MDW_ERR_CUDA

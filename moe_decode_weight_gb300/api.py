@@ -18,12 +18,14 @@ _PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_PKG, "libmdw.so")
 
 MDW_MAGIC = 0x3157444D
-FMT_BF16, FMT_FP8, FMT_MXFP4 = 1, 2, 3
+FMT_BF16, FMT_FP8, FMT_MXFP4, FMT_INT4_GROUP, FMT_KV_PAGED = 1, 2, 3, 4, 5
+DT_BF16, DT_F16, DT_F32, DT_E4M3 = 1, 2, 3, 4
 STATUS = {0: "MDW_OK", 1: "MDW_ERR_INVALID_ARG", 2: "MDW_ERR_UNSUPPORTED_SHAPE",
           3: "MDW_ERR_FORMAT_MISMATCH", 4: "MDW_ERR_WORKSPACE_TOO_SMALL", 5: "MDW_ERR_CUDA",
           6: "MDW_ERR_TIMEOUT", 7: "MDW_ERR_DEVICE_BOUNDS"}
 HIDDEN, INTER = 2560, 768
 MAX_M, MAX_TOPK, MAX_VOCAB_TOPK, MAX_EXPERTS = 32, 8, 32, 512
+MAX_REQUESTS, MAX_TREE, MAX_GROUP = 4096, 64, 64
 
 # exported symbols declared in include/moe_decode_weight.h
 SYMBOLS = ["mdw_status_string", "mdw_version", "mdw_moe_workspace_bytes", "mdw_moe_workspace_layout",
@@ -31,12 +33,14 @@ SYMBOLS = ["mdw_status_string", "mdw_version", "mdw_moe_workspace_bytes", "mdw_m
            "mdw_lm_head_workspace_bytes", "lm_head_fp8", "lm_head_bf16", "lm_head_fp8_rmsnorm",
            "mdw_stack_workspace_bytes",
            "moe_decode_stack", "mdw_device_status", "moe_decode_layer_noalloc", "mdw_sample_topk",
-           "lm_head_fp8_sample", "moe_decode_stack_routed", "mdw_debug_set_spin_budget"]
+           "lm_head_fp8_sample", "moe_decode_stack_routed", "mdw_debug_set_spin_budget",
+           "w4_linear", "mdw_kv_plan", "mdw_kv_write", "mdw_tree_attention_workspace_bytes",
+           "mdw_tree_attention"]
 
 
 class MdwError(RuntimeError):
-    def __init__(self, fn: str, code: int):
-        super().__init__(f"{fn} returned {STATUS.get(code, code)}")
+    def __init__(self, fn: str, code: int, detail: str = ""):
+        super().__init__(f"{fn} returned {STATUS.get(code, code)}" + (f": {detail}" if detail else ""))
         self.code = code
 
 
@@ -58,6 +62,19 @@ class MoeWsLayoutC(C.Structure):
     _fields_ = [(n, C.c_size_t) for n in ("header", "xq", "sx", "logits", "ids", "gates",
                                           "slot_expert", "pair_token", "pair_slot", "pair_gate",
                                           "h", "hq", "sh", "total")]
+
+
+class W4WeightsC(C.Structure):
+    _fields_ = [("magic", C.c_uint32), ("fmt", C.c_int32), ("n", C.c_int32), ("k", C.c_int32),
+                ("group", C.c_int32), ("dtype", C.c_int32), ("q", C.c_void_p), ("scale", C.c_void_p),
+                ("zero", C.c_void_p)]
+
+
+class KVCacheC(C.Structure):
+    _fields_ = [("magic", C.c_uint32), ("fmt", C.c_int32), ("dtype", C.c_int32), ("num_pages", C.c_int32),
+                ("page_size", C.c_int32), ("kv_heads", C.c_int32), ("head_dim", C.c_int32),
+                ("reserved", C.c_int32), ("page_stride", C.c_int64), ("k", C.c_void_p), ("v", C.c_void_p),
+                ("k_scale", C.c_void_p), ("v_scale", C.c_void_p)]
 
 
 _lib = None
@@ -110,6 +127,18 @@ def lib() -> C.CDLL:
     L.mdw_sample_topk.argtypes = [i32, i32, vp, vp, f64, f64, vp, vp, vp]
     L.lm_head_fp8_sample.restype = C.c_int
     L.lm_head_fp8_sample.argtypes = [C.POINTER(LMHeadC), i32, vp, i32, i32, f64, f64, vp, vp, vp, vp, vp, sz, vp]
+    f32 = C.c_float
+    L.w4_linear.restype = C.c_int
+    L.w4_linear.argtypes = [C.POINTER(W4WeightsC), i32, vp, i64, vp, i64, i32, vp, vp, i64, vp]
+    L.mdw_kv_plan.restype = C.c_int
+    L.mdw_kv_plan.argtypes = [i32, vp, vp, i32, i32, vp, i32, vp, i32, vp, i32, vp, vp, vp, vp, vp, vp, vp]
+    L.mdw_kv_write.restype = C.c_int
+    L.mdw_kv_write.argtypes = [C.POINTER(KVCacheC), i32, vp, i64, vp, i64, i32, vp, vp, vp]
+    L.mdw_tree_attention_workspace_bytes.restype = sz
+    L.mdw_tree_attention_workspace_bytes.argtypes = [C.POINTER(KVCacheC), i32, i32, i32, i32]
+    L.mdw_tree_attention.restype = C.c_int
+    L.mdw_tree_attention.argtypes = [C.POINTER(KVCacheC), i32, i32, i32, i32, vp, i64, i32, vp, i64, vp, vp, i32,
+                                     vp, vp, vp, f32, vp, vp, sz, vp]
     _lib = L
     return L
 
@@ -309,3 +338,183 @@ def moe_decode_stack_routed(layers, head, r0: torch.Tensor, argmax_out, ws: torc
 def mdw_device_status(ws: torch.Tensor, stream=None) -> int:
     """Synchronises the stream and returns the device status word of the workspace."""
     return lib().mdw_device_status(_ptr(ws), _stream(stream))
+
+
+# ------------------------------------------------------- the attention sub-layer of a window
+
+_DT = {torch.bfloat16: DT_BF16, torch.float16: DT_F16, torch.float32: DT_F32}
+_E4M3 = (torch.float8_e4m3fn, torch.uint8)
+
+
+class _On:
+    """What one call checks its tensors against: one CUDA device, made current for the launch."""
+
+    def __init__(self, fn: str, t: torch.Tensor):
+        if not t.is_cuda:
+            raise MdwError(fn, 1, "tensors must be on a CUDA device")
+        self.fn, self.device = fn, t.device
+
+    def bad(self, detail: str, code: int = 1):
+        return MdwError(self.fn, code, detail)
+
+    def array(self, t, name: str, dtypes, shape=None):
+        """Address of a contiguous tensor of one of `dtypes` (None stays None)."""
+        if t is None:
+            return None
+        if t.dtype not in dtypes:
+            raise self.bad(f"{name} has type {t.dtype}", 3)
+        if t.device != self.device or not t.is_contiguous() or (shape is not None and t.shape != shape):
+            raise self.bad(f"{name}: {tuple(t.shape)} on {t.device}, contiguous {t.is_contiguous()}; "
+                           f"wanted {shape or 'any shape'} on {self.device}")
+        return t.data_ptr()
+
+    def rows(self, t, name: str, dtypes, shape):
+        """Address and row stride of a tensor whose rows are contiguous."""
+        if t is None:
+            return None, 0
+        if t.dtype not in dtypes:
+            raise self.bad(f"{name} has type {t.dtype}", 3)
+        if t.device != self.device or t.shape != shape:
+            raise self.bad(f"{name}: {tuple(t.shape)} on {t.device}; wanted {tuple(shape)} on {self.device}")
+        st = t.stride()
+        width = 1
+        for i in range(len(shape) - 1, 0, -1):
+            if shape[i] != 1 and st[i] != width:
+                raise self.bad(f"{name}: the elements of a row must be contiguous (strides {st})")
+            width *= shape[i]
+        return t.data_ptr(), st[0] if shape[0] != 1 else -(-width // 8) * 8
+
+    def call(self, stream, *args):
+        f = getattr(lib(), self.fn)
+        if torch.cuda.current_device() != self.device.index:
+            with torch.cuda.device(self.device):
+                code = f(*args, (stream or torch.cuda.current_stream()).cuda_stream)
+        else:
+            code = f(*args, (stream or torch.cuda.current_stream()).cuda_stream)
+        if code != 0:
+            raise MdwError(self.fn, code)
+
+
+@dataclass
+class W4Weights:
+    """A dense weight in int4 with group scales (descriptor and the tensors it points at): q uint8
+    [N, K/2], scale bf16 or f16 [N, K/group], zero uint8 [N, K/group] or None (8 everywhere)."""
+    q: torch.Tensor
+    scale: torch.Tensor
+    zero: torch.Tensor | None = None
+    c: W4WeightsC = field(init=False)
+
+    def __post_init__(self):
+        on = _On("W4Weights", self.q)
+        if self.q.dim() != 2 or self.scale.dim() != 2 or self.scale.shape[0] != self.q.shape[0]:
+            raise on.bad("q is [N, K/2], scale [N, K/group]")
+        n, k, groups = self.q.shape[0], 2 * self.q.shape[1], self.scale.shape[1]
+        if n < 1 or groups < 1 or k % groups != 0 or k // groups not in (32, 64, 128):
+            raise on.bad(f"{k} input features in {groups} groups: groups are 32, 64 or 128 wide", 2)
+        self.c = W4WeightsC(MDW_MAGIC, FMT_INT4_GROUP, n, k, k // groups, _DT.get(self.scale.dtype, 0),
+                            on.array(self.q, "q", (torch.uint8,)),
+                            on.array(self.scale, "scale", (torch.bfloat16, torch.float16)),
+                            on.array(self.zero, "zero", (torch.uint8,), self.scale.shape))
+
+
+def w4_linear(w: W4Weights, x: torch.Tensor, y: torch.Tensor, bias=None, residual=None, stream=None) -> None:
+    """y = x . W^T (+ bias) (+ residual) for x [M, K], M <= 32; y [M, N] in x's type or float32."""
+    on, m, n, t = _On("w4_linear", x), x.shape[0], w.c.n, (w.scale.dtype,)
+    px, ldx = on.rows(x, "x", t, (m, w.c.k))
+    py, ldy = on.rows(y, "y", (t[0], torch.float32), (m, n))
+    pr, ldr = on.rows(residual, "residual", t, (m, n))
+    if w.q.device != on.device:
+        raise on.bad(f"weights on {w.q.device}, x on {on.device}")
+    on.call(stream, w.c, m, px, ldx, py, ldy, _DT[y.dtype], on.array(bias, "bias", t, (n,)), pr, ldr)
+
+
+@dataclass
+class KVCache:
+    """A paged key/value cache (descriptor and its tensors): k, v [pages, kv heads, page size, head dim] in
+    bf16, f16 or E4M3 (float8_e4m3fn or uint8, with k_scale, v_scale float32 [kv heads]); the pages
+    may be strided, what is inside one is contiguous."""
+    k: torch.Tensor
+    v: torch.Tensor
+    k_scale: torch.Tensor | None = None
+    v_scale: torch.Tensor | None = None
+    c: KVCacheC = field(init=False)
+
+    def __post_init__(self):
+        on, k, v = _On("KVCache", self.k), self.k, self.v
+        if k.dim() != 4:
+            raise on.bad("k and v are [pages, kv heads, page size, head dim]")
+        fp8 = k.dtype in _E4M3
+        dtypes = _E4M3 if fp8 else (torch.bfloat16, torch.float16)
+        pk, ldk = on.rows(k, "k", dtypes, k.shape)
+        pv, ldv = on.rows(v, "v", (k.dtype,), k.shape)
+        if ldk != ldv:
+            raise on.bad(f"k and v have page strides {ldk} and {ldv}")
+        one = (torch.float32,)
+        if fp8 != (self.k_scale is not None) or fp8 != (self.v_scale is not None):
+            raise on.bad("k_scale and v_scale belong to E4M3 caches, and to no other")
+        self.c = KVCacheC(MDW_MAGIC, FMT_KV_PAGED, DT_E4M3 if fp8 else _DT[k.dtype], k.shape[0], k.shape[2],
+                          k.shape[1], k.shape[3], 0, ldk, pk, pv,
+                          on.array(self.k_scale, "k_scale", one, (k.shape[1],)),
+                          on.array(self.v_scale, "v_scale", one, (k.shape[1],)))
+
+
+_I32, _I64, _MASK = (torch.int32,), (torch.int64,), (torch.int64, torch.uint64)
+
+
+def mdw_kv_plan(ctx_len: torch.Tensor, new_len: torch.Tensor, page_size: int, num_pages: int,
+                block_table: torch.Tensor, free_pages: torch.Tensor, row_start: torch.Tensor,
+                slot_map: torch.Tensor, positions: torch.Tensor, pages_taken: torch.Tensor, parents=None,
+                tree_mask=None, status=None, stream=None) -> None:
+    """Block tables, slot map, positions and tree masks from request lengths (see the C declaration):
+    ctx_len, new_len int32 [B]; block_table int32 [B, max pages]; free_pages int32 [F]; row_start int32
+    [B + 1]; slot_map int64 [T]; positions, parents int32 [T]; tree_mask int64 or uint64 [T]."""
+    on, b, t = _On("mdw_kv_plan", ctx_len), ctx_len.numel(), slot_map.numel()
+    if block_table.dim() != 2:
+        raise on.bad("block_table is [B, max pages]")
+    on.call(stream, b, on.array(ctx_len, "ctx_len", _I32, (b,)), on.array(new_len, "new_len", _I32, (b,)), page_size,
+            num_pages, on.array(block_table, "block_table", _I32, (b, block_table.shape[1])), block_table.shape[1],
+            on.array(free_pages, "free_pages", _I32), free_pages.numel(), on.array(parents, "parents", _I32, (t,)), t,
+            on.array(row_start, "row_start", _I32, (b + 1,)), on.array(slot_map, "slot_map", _I64, (t,)),
+            on.array(positions, "positions", _I32, (t,)), on.array(tree_mask, "tree_mask", _MASK, (t,)),
+            on.array(pages_taken, "pages_taken", _I32, (1,)), on.array(status, "status", _I32, (1,)))
+
+
+def mdw_kv_write(cache: KVCache, k: torch.Tensor, v: torch.Tensor, slot_map: torch.Tensor, status=None,
+                 stream=None) -> None:
+    """Rows k, v [T, kv heads, head dim] (rows may be strided) to the cache's slots slot_map int64 [T]."""
+    on, t = _On("mdw_kv_write", k), slot_map.numel()
+    shape, types = (t, cache.c.kv_heads, cache.c.head_dim), (torch.bfloat16, torch.float16)
+    pk, ldk = on.rows(k, "k", types, shape)
+    pv, ldv = on.rows(v, "v", (k.dtype,), shape)
+    if cache.k.device != on.device:
+        raise on.bad(f"cache on {cache.k.device}, k on {on.device}")
+    on.call(stream, cache.c, t, pk, ldk, pv, ldv, _DT[k.dtype], on.array(slot_map, "slot_map", _I64, (t,)),
+            on.array(status, "status", _I32, (1,)))
+
+
+def mdw_tree_attention_workspace_bytes(cache: KVCache, b: int, t: int, q_heads: int, max_new: int) -> int:
+    return lib().mdw_tree_attention_workspace_bytes(cache.c, b, t, q_heads, max_new)
+
+
+def mdw_tree_attention(cache: KVCache, q: torch.Tensor, out: torch.Tensor, block_table: torch.Tensor,
+                       ctx_len: torch.Tensor, row_start: torch.Tensor, max_new: int, ws: torch.Tensor,
+                       tree_mask=None, lse=None, scale: float | None = None, status=None, stream=None) -> None:
+    """Attention of the drafted rows q [T, query heads, head dim] over the paged cache (see the C
+    declaration); out like q, lse float32 [T, query heads] or None, scale head_dim ** -0.5 by default."""
+    on, b, c = _On("mdw_tree_attention", q), ctx_len.numel(), cache.c
+    if q.dim() != 3 or block_table.dim() != 2:
+        raise on.bad("q is [T, query heads, head dim], block_table [B, max pages]")
+    t, hq = q.shape[0], q.shape[1]
+    shape = (t, hq, c.head_dim)
+    pq, ldq = on.rows(q, "q", (torch.bfloat16, torch.float16), shape)
+    po, ldo = on.rows(out, "out", (q.dtype,), shape)
+    if cache.k.device != on.device:
+        raise on.bad(f"cache on {cache.k.device}, q on {on.device}")
+    if not ws.is_contiguous() or ws.device != on.device:
+        raise on.bad("ws must be contiguous and on q's device")
+    on.call(stream, c, b, t, hq, max_new, pq, ldq, _DT[q.dtype], po, ldo,
+            on.array(lse, "lse", (torch.float32,), (t, hq)),
+            on.array(block_table, "block_table", _I32, (b, block_table.shape[1])), block_table.shape[1],
+            on.array(ctx_len, "ctx_len", _I32, (b,)), on.array(row_start, "row_start", _I32, (b + 1,)),
+            on.array(tree_mask, "tree_mask", _MASK, (t,)), c.head_dim ** -0.5 if scale is None else scale,
+            on.array(status, "status", _I32, (1,)), ws.data_ptr(), ws.numel() * ws.element_size())

@@ -206,7 +206,7 @@ const char* mdw_status_string(mdw_status s) {
   return "MDW_ERR_UNKNOWN";
 }
 
-int32_t mdw_version(void) { return 200; }
+int32_t mdw_version(void) { return 300; }
 
 int64_t mdw_debug_set_spin_budget(int64_t cycles) {
   const long long v = cycles > 0 ? (long long)cycles : kSpinBudget;
