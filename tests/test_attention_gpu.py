@@ -333,7 +333,7 @@ class Attn:
         lse = torch.full(self.q.shape[:2], 5.0, device="cuda") if lse is True else lse
         max_new = max(1, int(self.new.max())) if max_new is None else max_new
         nbytes = api.mdw_tree_attention_workspace_bytes(self.cache, len(self.ctx), self.q.shape[0], self.q.shape[1], max_new)
-        ws = torch.full((nbytes,), 0xA5, dtype=torch.uint8, device="cuda") if ws is None else ws
+        ws = torch.full((nbytes,), 0xFF, dtype=torch.uint8, device="cuda") if ws is None else ws
         api.mdw_tree_attention(self.cache, q, out, i32(self.table if table is None else table), i32(self.ctx if ctx is None else ctx),
                                i32(self.start), max_new, ws, tree_mask=self.mask if mask is True else mask, lse=lse, scale=self.scale,
                                status=status, stream=stream)
@@ -670,3 +670,20 @@ def test_binding_refuses():
         api.KVCache(c.cache.k.view(torch.uint8), c.cache.v.view(torch.uint8))
     with pytest.raises(api.MdwError):
         api.KVCache(c.cache.k.transpose(1, 2), c.cache.v.transpose(1, 2))
+
+
+def test_attention_wait_that_runs_out_is_reported():
+    """A bounded wait of the copy pipeline that gives up ends in MDW_ERR_TIMEOUT, a clean exit and a usable
+    device; rows are then not stored."""
+    c = Attn(19, [3000, 500], [4, 2], 8, 2, 128, 16, BF, BF)
+    api.mdw_debug_set_spin_budget(1)
+    try:
+        status = i32([0])
+        c.call(status=status)
+        assert status.item() == 6
+    finally:
+        api.mdw_debug_set_spin_budget(0)
+    status = i32([0])
+    out, lse = c.call(status=status)
+    assert status.item() == 0
+    c.check(out, lse)
