@@ -31,7 +31,7 @@ def test_limits_match_the_header():
 
 @pytest.mark.parametrize("field,value,code", [
     ("magic", 0, 3), ("fmt", api.FMT_MXFP4, 3), ("dtype", F32, 3), ("group", 16, 2), ("group", 256, 2), ("n", 0, 2),
-    ("k", 2592, 2), ("k", 0, 2), ("q", FAKE + 8, 1), ("q", None, 1), ("scale", None, 1), ("scale", FAKE + 1, 1)])
+    ("k", 2592, 2), ("k", 0, 2), ("q", FAKE + 8, 1), ("q", None, 1), ("scale", None, 1), ("scale", FAKE + 8, 1), ("zero", FAKE + 8, 1)])
 def test_w4_rejects_weights(field, value, code):
     assert api.lib().w4_linear(_w4(**{field: value}), 1, FAKE, 2560, FAKE, 100, BF, None, None, 0, None) == code
 
