@@ -353,8 +353,10 @@ mdw_status lm_head_fp8_sample(const mdw_lm_head* head, int32_t M, const void* h_
  *   - `status`: NULL, or a device uint32 that the CALLER clears. A call that meets bad data on
  *     the device (lengths, page ids, slots, parents) stores an mdw_status there if the word is
  *     still 0, computes nothing for what the bad data governs, and accesses nothing outside
- *     the arrays it was given. No call clears the word, so one check serves a whole step
- *     (mdw_device_status() reads it when it is 16-byte aligned). */
+ *     the arrays it was given. A wait of a copy pipeline that runs out (it is bounded, see
+ *     mdw_debug_set_spin_budget) stores MDW_ERR_TIMEOUT; its block then stores no results. No
+ *     call clears the word, so one check serves a whole step (mdw_device_status() reads it
+ *     when it is 16-byte aligned). */
 
 /* A dense weight in int4 with group scales: w[n][k] = (code - zero) * scale, per group of
  * `group` consecutive k. fmt MDW_FMT_INT4_GROUP. */
@@ -378,7 +380,8 @@ typedef struct mdw_w4_weights {
  * w->dtype. y, bias and residual need the alignment of their elements only. y may be the
  * residual itself (same pointer, type and stride); it must not overlap any other argument. */
 mdw_status w4_linear(const mdw_w4_weights* w, int32_t M, const void* x, int64_t ldx, void* y, int64_t ldy,
-                     int32_t y_dtype, const void* bias, const void* residual, int64_t ldr, mdw_stream_t stream);
+                     int32_t y_dtype, const void* bias, const void* residual, int64_t ldr, uint32_t* status,
+                     mdw_stream_t stream);
 
 /* A paged key/value cache: k and v are [num_pages][kv_heads][page_size][head_dim], pages
  * page_stride elements apart (so both can share one allocation). Slot s is row s % page_size of

@@ -129,7 +129,7 @@ def lib() -> C.CDLL:
     L.lm_head_fp8_sample.argtypes = [C.POINTER(LMHeadC), i32, vp, i32, i32, f64, f64, vp, vp, vp, vp, vp, sz, vp]
     f32 = C.c_float
     L.w4_linear.restype = C.c_int
-    L.w4_linear.argtypes = [C.POINTER(W4WeightsC), i32, vp, i64, vp, i64, i32, vp, vp, i64, vp]
+    L.w4_linear.argtypes = [C.POINTER(W4WeightsC), i32, vp, i64, vp, i64, i32, vp, vp, i64, vp, vp]
     L.mdw_kv_plan.restype = C.c_int
     L.mdw_kv_plan.argtypes = [i32, vp, vp, i32, i32, vp, i32, vp, i32, vp, i32, vp, vp, vp, vp, vp, vp, vp]
     L.mdw_kv_write.restype = C.c_int
@@ -342,6 +342,8 @@ def mdw_device_status(ws: torch.Tensor, stream=None) -> int:
 
 # ------------------------------------------------------- the attention sub-layer of a window
 
+# The current stream's handle; torch.cuda.current_stream() builds a stream object, which costs more than a launch.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", lambda i: torch.cuda.current_stream(i).cuda_stream)
 _DT = {torch.bfloat16: DT_BF16, torch.float16: DT_F16, torch.float32: DT_F32}
 _E4M3 = (torch.float8_e4m3fn, torch.uint8)
 
@@ -388,9 +390,9 @@ class _On:
         f = getattr(lib(), self.fn)
         if torch.cuda.current_device() != self.device.index:
             with torch.cuda.device(self.device):
-                code = f(*args, (stream or torch.cuda.current_stream()).cuda_stream)
+                code = f(*args, stream.cuda_stream if stream is not None else _raw_stream(self.device.index))
         else:
-            code = f(*args, (stream or torch.cuda.current_stream()).cuda_stream)
+            code = f(*args, stream.cuda_stream if stream is not None else _raw_stream(self.device.index))
         if code != 0:
             raise MdwError(self.fn, code)
 
@@ -417,7 +419,8 @@ class W4Weights:
                             on.array(self.zero, "zero", (torch.uint8,), self.scale.shape))
 
 
-def w4_linear(w: W4Weights, x: torch.Tensor, y: torch.Tensor, bias=None, residual=None, stream=None) -> None:
+def w4_linear(w: W4Weights, x: torch.Tensor, y: torch.Tensor, bias=None, residual=None, status=None,
+              stream=None) -> None:
     """y = x . W^T (+ bias) (+ residual) for x [M, K], M <= 32; y [M, N] in x's type or float32."""
     on, m, n, t = _On("w4_linear", x), x.shape[0], w.c.n, (w.scale.dtype,)
     px, ldx = on.rows(x, "x", t, (m, w.c.k))
@@ -425,7 +428,8 @@ def w4_linear(w: W4Weights, x: torch.Tensor, y: torch.Tensor, bias=None, residua
     pr, ldr = on.rows(residual, "residual", t, (m, n))
     if w.q.device != on.device:
         raise on.bad(f"weights on {w.q.device}, x on {on.device}")
-    on.call(stream, w.c, m, px, ldx, py, ldy, _DT[y.dtype], on.array(bias, "bias", t, (n,)), pr, ldr)
+    on.call(stream, w.c, m, px, ldx, py, ldy, _DT[y.dtype], on.array(bias, "bias", t, (n,)), pr, ldr,
+            on.array(status, "status", _I32, (1,)))
 
 
 @dataclass

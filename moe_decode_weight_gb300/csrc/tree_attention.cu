@@ -150,45 +150,6 @@ struct Walk {
 
 // ------------------------------------------------------------------ barriers, copies, matrix steps
 
-__device__ __forceinline__ uint32_t smem_u32(const void* p) { return (uint32_t)__cvta_generic_to_shared(p); }
-__device__ __forceinline__ void mbar_init(uint32_t bar, uint32_t count) {
-  asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" :: "r"(bar), "r"(count) : "memory");
-}
-__device__ __forceinline__ void mbar_arrive(uint32_t bar) {
-  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" :: "r"(bar) : "memory");
-}
-__device__ __forceinline__ void mbar_arrive_tx(uint32_t bar, uint32_t bytes) {
-  asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" :: "r"(bar), "r"(bytes) : "memory");
-}
-__device__ __forceinline__ bool mbar_try(uint32_t bar, uint32_t parity) {
-  uint32_t ok;
-  asm volatile("{ .reg .pred p; mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2; selp.u32 %0, 1, 0, p; }"
-               : "=r"(ok) : "r"(bar), "r"(parity) : "memory");
-  return ok != 0;
-}
-__device__ __forceinline__ bool mbar_test(uint32_t bar, uint32_t parity) {
-  uint32_t ok;
-  asm volatile("{ .reg .pred p; mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2; selp.u32 %0, 1, 0, p; }"
-               : "=r"(ok) : "r"(bar), "r"(parity) : "memory");
-  return ok != 0;
-}
-// A wait that outlasts the budget marks the block dead: it and every later wait then give up at
-// once, so the block runs to its end (its results are not stored) and the status says so.
-__device__ __noinline__ void mbar_wait_slow(uint32_t bar, uint32_t parity, const AttnParams& p, volatile int* dead) {
-  const long long t0 = clock64();
-  for (;;) {
-    if (*dead) return;
-    if (clock64() - t0 > p.spin_budget) {
-      *dead = 1;
-      raise_status(p.status, MDW_ERR_TIMEOUT);
-      return;
-    }
-    if (mbar_try(bar, parity)) return;
-  }
-}
-__device__ __forceinline__ void mbar_wait(uint32_t bar, uint32_t parity, const AttnParams& p, volatile int* dead) {
-  if (!mbar_test(bar, parity)) mbar_wait_slow(bar, parity, p, dead);
-}
 __device__ __forceinline__ void tma_load(uint32_t dst, const CUtensorMap* map, uint32_t bar, int x, int row, int head, int page) {
   asm volatile("cp.async.bulk.tensor.4d.shared::cta.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], [%6];"
                :: "r"(dst), "l"(map), "r"(x), "r"(row), "r"(head), "r"(page), "r"(bar) : "memory");
@@ -449,7 +410,7 @@ tree_attention_kernel(const AttnParams p, const __grid_constant__ CUtensorMap km
       mbar_init(empty + 8 * i, kConsumers);
     }
     *dead = 0;
-    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    mbar_init_fence();
   }
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   Walk walk;
@@ -469,7 +430,7 @@ tree_attention_kernel(const AttnParams p, const __grid_constant__ CUtensorMap km
       const int id = wanted ? p.block_table[(size_t)walk.b * p.max_pages + (key >> p.page_shift)] : 0;
       const bool ok = wanted && id >= 0 && id < p.num_pages;
       const unsigned good = __ballot_sync(0xffffffffu, ok), bad = __ballot_sync(0xffffffffu, wanted && !ok);
-      mbar_wait(empty + 8 * stage, phase ^ 1, p, dead);
+      mbar_wait(empty + 8 * stage, phase ^ 1, p.spin_budget, p.status, dead);
       if (__any_sync(0xffffffffu, *dead)) break;
       const uint32_t bar = full + 8 * stage, kt = stages + stage * 2 * S::kTileBytes, vt = kt + S::kTileBytes;
       if (lane == 0) {
@@ -495,14 +456,8 @@ tree_attention_kernel(const AttnParams p, const __grid_constant__ CUtensorMap km
       if (--walk.left == 0) break;
       if (++walk.tile == walk.tiles) walk.next_item(p);
     }
-    if (*dead) {
-      // copies in flight end before the block does (each wait bounded by its own budget)
-      for (int i = 0; i < S::kStages; ++i) {
-        const uint32_t par = i < stage ? phase : phase ^ 1;
-        const long long t0 = clock64();
-        while (!mbar_try(full + 8 * i, par) && clock64() - t0 < (1ll << 28)) {}
-      }
-    }
+    if (__any_sync(0xffffffffu, *dead))
+      for (int i = 0; i < S::kStages; ++i) mbar_drain(full + 8 * i, i < stage ? phase : phase ^ 1);
     return;
   }
 
@@ -574,7 +529,7 @@ tree_attention_kernel(const AttnParams p, const __grid_constant__ CUtensorMap km
     for (int n = 0; n < D / 8; ++n) w.o[n][0] = w.o[n][1] = w.o[n][2] = w.o[n][3] = 0.f;
 
     for (int i = 0; i < count; ++i) {
-      mbar_wait(full + 8 * stage, phase, p, dead);
+      mbar_wait(full + 8 * stage, phase, p.spin_budget, p.status, dead);
       __syncwarp();
       if (live) {
         const uint32_t kt = stages + stage * 2 * S::kTileBytes, vt = kt + S::kTileBytes, bad = bad_pages[stage];
@@ -727,19 +682,6 @@ __global__ void __launch_bounds__(128) join_kernel(const AttnParams p, int block
 
 // ------------------------------------------------------------------ host
 
-using EncodeFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*, const cuuint64_t*,
-                              const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
-                              CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-EncodeFn encode_fn() {
-  static const EncodeFn fn = [] {
-    void* f = nullptr;
-    cudaDriverEntryPointQueryResult res;
-    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &res) != cudaSuccess) f = nullptr;
-    return reinterpret_cast<EncodeFn>(f);
-  }();
-  return fn;
-}
-
 // The cache as [pages][heads][page size][head dim]; a box is up to 128 rows of one page and head, 128 bytes (or
 // a whole 64-byte row) wide.
 bool encode_cache(CUtensorMap* map, const mdw_kv_cache* c, void* data) {
@@ -749,7 +691,7 @@ bool encode_cache(CUtensorMap* map, const mdw_kv_cache* c, void* data) {
   const cuuint64_t strides[3] = {d * e, d * ps * e, (cuuint64_t)c->page_stride * e};
   const cuuint32_t width = (cuuint32_t)(d * e < 128 ? d : 128 / e);
   const cuuint32_t box[4] = {width, (cuuint32_t)(ps < kTileKeys ? ps : kTileKeys), 1, 1}, ones[4] = {1, 1, 1, 1};
-  const EncodeFn fn = encode_fn();
+  const EncodeTiledFn fn = encode_tiled();
   return fn && fn(map, fp8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_UINT16, 4, data, dims, strides, box, ones,
                   CU_TENSOR_MAP_INTERLEAVE_NONE, width * e == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
                   CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
@@ -770,9 +712,9 @@ AttnWs attn_ws(int64_t items, int grid, int D) {
 int row_blocks_of(int32_t max_new, int group) { return (max_new * group + kTileRows - 1) / kTileRows; }
 
 template <typename T, bool kE4M3, int D>
-cudaError_t launch(const AttnParams& p, const CUtensorMap& km, const CUtensorMap& vm, int grid, cudaStream_t s) {
+cudaError_t launch(const AttnParams& p, const CUtensorMap& km, const CUtensorMap& vm, int grid, int dev, cudaStream_t s) {
   using S = Shape<T, kE4M3, D>;
-  cudaError_t e = cudaFuncSetAttribute(tree_attention_kernel<T, kE4M3, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kSmem);
+  cudaError_t e = allow_shared_memory<tree_attention_kernel<T, kE4M3, D>>(dev);
   if (e != cudaSuccess) return e;
   tree_attention_kernel<T, kE4M3, D><<<grid, kAttnThreads, S::kSmem, s>>>(p, km, vm);
   e = cudaGetLastError();
@@ -789,8 +731,8 @@ cudaError_t launch(const AttnParams& p, const CUtensorMap& km, const CUtensorMap
   return cudaLaunchKernelEx(&cfg, join_kernel<T, D>, p, grid);
 }
 template <typename T, bool kE4M3>
-cudaError_t launch(const AttnParams& p, int D, const CUtensorMap& km, const CUtensorMap& vm, int grid, cudaStream_t s) {
-  return D == 64 ? launch<T, kE4M3, 64>(p, km, vm, grid, s) : launch<T, kE4M3, 128>(p, km, vm, grid, s);
+cudaError_t launch(const AttnParams& p, int D, const CUtensorMap& km, const CUtensorMap& vm, int grid, int dev, cudaStream_t s) {
+  return D == 64 ? launch<T, kE4M3, 64>(p, km, vm, grid, dev, s) : launch<T, kE4M3, 128>(p, km, vm, grid, dev, s);
 }
 
 bool sizes_ok(const mdw_kv_cache* c, int32_t B, int32_t T, int32_t q_heads, int32_t max_new) {
@@ -806,7 +748,7 @@ using namespace mdw;
 extern "C" size_t mdw_tree_attention_workspace_bytes(const mdw_kv_cache* cache, int32_t B, int32_t T,
                                                      int32_t q_heads, int32_t max_new) {
   if (check_kv_cache(cache) != MDW_OK || !sizes_ok(cache, B, T, q_heads, max_new)) return 0;
-  const int grid = device_sm_count();
+  const int grid = sm_count(current_device());
   if (grid <= 0) return 0;
   const int64_t items = (int64_t)B * cache->kv_heads * row_blocks_of(max_new, q_heads / cache->kv_heads);
   return attn_ws(items, grid, cache->head_dim).total;
@@ -831,7 +773,7 @@ extern "C" mdw_status mdw_tree_attention(const mdw_kv_cache* cache, int32_t B, i
       !aligned_to(row_start, 4) || !null_or_aligned(tree_mask, 8) || !null_or_aligned(status, 4) || !aligned_to(ws, 16))
     return MDW_ERR_INVALID_ARG;
   if (!(scale > 0.f) || !std::isfinite(scale)) return MDW_ERR_INVALID_ARG;
-  const int grid = device_sm_count(), group = q_heads / cache->kv_heads, row_blocks = row_blocks_of(max_new, group);
+  const int dev = current_device(), grid = sm_count(dev), group = q_heads / cache->kv_heads, row_blocks = row_blocks_of(max_new, group);
   const int64_t items = (int64_t)B * cache->kv_heads * row_blocks;
   if (items > 0x7fffffffLL) return MDW_ERR_UNSUPPORTED_SHAPE;
   const AttnWs lay = attn_ws(items, std::max(grid, 1), cache->head_dim);
@@ -849,8 +791,8 @@ extern "C" mdw_status mdw_tree_attention(const mdw_kv_cache* cache, int32_t B, i
   const int D = cache->head_dim;
   cudaError_t e;
   if (q_dtype == MDW_DT_BF16)
-    e = fp8 ? launch<__nv_bfloat16, true>(p, D, km, vm, grid, s) : launch<__nv_bfloat16, false>(p, D, km, vm, grid, s);
+    e = fp8 ? launch<__nv_bfloat16, true>(p, D, km, vm, grid, dev, s) : launch<__nv_bfloat16, false>(p, D, km, vm, grid, dev, s);
   else
-    e = fp8 ? launch<__half, true>(p, D, km, vm, grid, s) : launch<__half, false>(p, D, km, vm, grid, s);
+    e = fp8 ? launch<__half, true>(p, D, km, vm, grid, dev, s) : launch<__half, false>(p, D, km, vm, grid, dev, s);
   return e == cudaSuccess ? MDW_OK : MDW_ERR_CUDA;
 }

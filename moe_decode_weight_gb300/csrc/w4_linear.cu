@@ -1,5 +1,17 @@
 // w4_linear: y = x . W^T (+ bias) (+ residual) with W in int4 codes and group scales, for windows of
 // up to MDW_MAX_M tokens.
+//
+// Mathematics. y[t][n] = sum over groups s[n][j] * sum over the group's k of (code - zero) x[t][k]: the inner sum on
+// the tensor cores (integers up to 15 times 16-bit elements, exact products, fp32 sums), the outer
+// one in fp32. m16n8k16 with 16 features as the rows and 8 tokens as the columns.
+//
+// Codes. A lane (g, q) holds features g and g + 8; of every 32-code block it takes word q (8 codes,
+// k = 8 q .. 8 q + 7), so the four lanes of a product always share a group, whatever its width. Masking
+// a word by 0x000f000f leaves codes j and j + 4 in its halves, under the exponent of 128 (bf16) or 1024
+// (f16) that is code + 128 or + 1024 exactly; subtracting 128 + zero or 1024 + zero leaves code - zero.
+// The token's elements are put in the same order once, when they enter shared memory.
+// This expansion bounds the kernels beside the codes' stream: 7 (bf16) or 5 (f16) operations of the integer
+// pipe for eight codes of a feature, whatever the number of tokens, so nothing else is left per code.
 #include <cstring>
 
 #include "mdw_attn.cuh"
@@ -17,17 +29,12 @@ struct W4Params {
   const void* bias;
   const void* residual;
   int64_t ldx, ldy, ldr;
-  int M, N, K, y_f32, sms;
+  uint32_t* status;
+  long long spin_budget;
+  int M, N, K, y_f32;
 };
 
-// ------------------------------------------------------------------ the matrix step
-//
-// y = W x^T on m16n8k16: 16 features are the rows, 8 tokens the columns. A lane (g, q) holds the codes of
-// features g and g + 8; of every 32-code block it takes word q (8 codes, k = 8 q .. 8 q + 7), so all four
-// lanes of a product stay inside one group. Masking a word by 0x000f000f leaves the codes j and
-// j + 4 of it in the two halves, under the exponent of 128 (bf16) or 1024 (f16) that is code + 128 or
-// + 1024 exactly; subtracting 128 + zero leaves code - zero, exact. The token's elements are
-// paired the same way. Groups are summed apart in fp32 and enter the result times their scale.
+constexpr int kUnit = 256;                     // codes of a row in one copy: 128 bytes, one swizzled line
 
 template <typename T> struct Int4;
 template <> struct Int4<__nv_bfloat16> {
@@ -67,12 +74,7 @@ template <> struct Int4<__half> {
   }
 };
 
-__device__ __forceinline__ void cp16(uint32_t dst, const void* src, bool on) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" :: "r"(dst), "l"(src), "r"(on ? 16 : 0) : "memory");
-}
-__device__ __forceinline__ void cp4(uint32_t dst, const void* src, int bytes) {
-  asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" :: "r"(dst), "l"(src), "r"(bytes) : "memory");
-}
+
 __device__ __forceinline__ uint32_t lds32(uint32_t a) {
   uint32_t v;
   asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(a) : "memory");
@@ -83,114 +85,104 @@ __device__ __forceinline__ uint4 lds128(uint32_t a) {
   asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a) : "memory");
   return v;
 }
-template <typename T>
-__device__ __forceinline__ float lds_elem(uint32_t a) {
-  unsigned short v;
-  asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(a) : "memory");
-  T t;
-  memcpy(&t, &v, 2);
-  return Elem<T>::to_float(t);
+// Eight elements of a token in the order of the expanded codes: pairs (j, j + 4).
+__device__ __forceinline__ void sts_paired(uint32_t a, uint4 v) {
+  asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" :: "r"(a), "r"(__byte_perm(v.x, v.z, 0x5410)), "r"(__byte_perm(v.x, v.z, 0x7632)),
+               "r"(__byte_perm(v.y, v.w, 0x5410)), "r"(__byte_perm(v.y, v.w, 0x7632)) : "memory");
 }
-__device__ __forceinline__ uint32_t lds8(uint32_t a) {
-  uint32_t v;
-  asm volatile("ld.shared.u8 %0, [%1];" : "=r"(v) : "r"(a) : "memory");
-  return v;
+__device__ __forceinline__ void tma_codes(uint32_t dst, const CUtensorMap* map, uint32_t bar, int byte, int row) {
+  asm volatile("cp.async.bulk.tensor.2d.shared::cta.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];"
+               :: "r"(dst), "l"(map), "r"(byte), "r"(row), "r"(bar) : "memory");
 }
 
-// A stage of 16 features x kU codes: code rows of kU / 2 bytes, 16 bytes apart more so that the eight
-// features of a load fall on different banks; the scales and zeros as the 4-byte words that cover
-// them (a row of an odd number of groups starts inside a word).
-template <int kU, int kGroup>
-struct Unit {
-  static constexpr int kGroups = kU / kGroup;
-  static constexpr int kCodePitch = kU / 2 + 16;
-  static constexpr int kScaleWords = kGroups / 2 + 1, kZeroWords = (kGroups + 6) / 4;
-  static constexpr int kXPitch = 2 * kU + 64;                   // two tokens of a 16-byte load on different banks
-  static __host__ __device__ constexpr int scales(int rows) { return rows * kCodePitch; }
-  static __host__ __device__ constexpr int zeros(int rows) { return scales(rows) + rows * kScaleWords * 4; }
-  static __host__ __device__ constexpr int tokens(int rows) { return (zeros(rows) + rows * kZeroWords * 4 + 15) / 16 * 16; }
-  static __host__ __device__ constexpr int bytes(int rows, int m) { return tokens(rows) + m * kXPitch; }
+// Scales and zeros of one unit for a lane's two features, requested two units ahead: the sectors come
+// from memory, and a load at the point of use would stall every unit.
+template <typename T, int kGroup>
+struct Scales {
+  static constexpr int kGroups = kUnit / kGroup;
+  uint32_t s[2][kGroups / 2], z[2][(kGroups + 3) / 4];
+
+  // Rows of whole units start on the boundary of a unit's scales, so one load serves a row; otherwise
+  // the scales are read one by one (and those behind the row's end not at all).
+  __device__ __forceinline__ void load(const W4Params& p, int n, int unit) {
+    const int groups = p.K / kGroup, first = unit * kGroups;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const size_t at = (size_t)min(n + 8 * i, p.N - 1) * groups + first;
+      const uint16_t* src = static_cast<const uint16_t*>(p.scale) + at;
+#pragma unroll
+      for (int j = 0; j < (kGroups + 3) / 4; ++j) z[i][j] = 0x08080808u;
+      if (p.K % kUnit == 0) {
+        if constexpr (kGroups == 2) {
+          s[i][0] = __ldg(reinterpret_cast<const uint32_t*>(src));
+          if (p.zero) z[i][0] = __ldg(reinterpret_cast<const uint16_t*>(p.zero + at));
+        } else if constexpr (kGroups == 4) {
+          const uint2 v = __ldg(reinterpret_cast<const uint2*>(src));
+          s[i][0] = v.x;
+          s[i][1] = v.y;
+          if (p.zero) z[i][0] = __ldg(reinterpret_cast<const uint32_t*>(p.zero + at));
+        } else {
+          const uint4 v = __ldg(reinterpret_cast<const uint4*>(src));
+          s[i][0] = v.x;
+          s[i][1] = v.y;
+          s[i][2] = v.z;
+          s[i][3] = v.w;
+          if (p.zero) {
+            const uint2 u = __ldg(reinterpret_cast<const uint2*>(p.zero + at));
+            z[i][0] = u.x;
+            z[i][1] = u.y;
+          }
+        }
+      } else {
+#pragma unroll
+        for (int j = 0; j < kGroups / 2; ++j) s[i][j] = 0u;
+#pragma unroll
+        for (int j = 0; j < kGroups; ++j) {
+          if (first + j >= groups) break;
+          s[i][j / 2] |= (uint32_t)__ldg(src + j) << (16 * (j & 1));
+          if (p.zero) z[i][j / 4] = (z[i][j / 4] & ~(0xffu << (8 * (j & 3)))) | (uint32_t)__ldg(p.zero + at + j) << (8 * (j & 3));
+        }
+      }
+    }
+  }
+  __device__ __forceinline__ float scale(int i, int j) const {
+    const unsigned short v = (unsigned short)(s[i][j / 2] >> (16 * (j & 1)));
+    T t;
+    memcpy(&t, &v, 2);
+    return Elem<T>::to_float(t);
+  }
+  __device__ __forceinline__ uint32_t zero2(int i, int j) const {
+    return Int4<T>::zero2((z[i][j / 4] >> (8 * (j & 3))) & 0xffu);
+  }
 };
 
-// Word window of `count` bytes from byte `at` on: word i starts at (at & ~3) + 4 i; src bytes are cut at `total`.
-__device__ __forceinline__ void cp_window(uint32_t dst, const uint8_t* base, int64_t at, int64_t total, int i) {
-  const int64_t pos = (at & ~int64_t{3}) + 4 * i;
-  const int64_t left = total - pos;
-  cp4(dst, base + (left > 0 ? pos : 0), left >= 4 ? 4 : (left > 0 ? (int)left : 0));
-}
-
-// Requests rows [n0, n0 + kRows) x codes [k0, k0 + kU) and the tokens' elements there; `id` of `threads`
-// takes part. Codes and elements behind K arrive as zeros, rows behind N repeat the last one.
-template <typename T, int kU, int kGroup, int kRows>
-__device__ __forceinline__ void request(const W4Params& p, uint32_t stage, int n0, int k0, int id, int threads) {
-  using U = Unit<kU, kGroup>;
-  const int groups = p.K / kGroup;
-  constexpr int kPieces = kU / 32;
+// 16 features x one unit x kTiles * 8 tokens: acc += scale * (codes - zero) . x. `code`: the lane's word of
+// feature g, block 0, in the swizzled line (feature g + 8 lies 1,024 bytes further; block b is at
+// code ^ 16 b); `x`: token g, elements 8 q of the unit, tokens `pitch` bytes apart. Codes and elements behind K
+// are zeros.
+template <typename T, int kGroup, int kTiles>
+__device__ __forceinline__ void multiply(uint32_t code, uint32_t x, uint32_t pitch, int g, int M, const Scales<T, kGroup>& sc,
+                                         float (&acc)[kTiles][4]) {
 #pragma unroll
-  for (int i = 0; i < kRows * kPieces; i += threads) {
-    const int at = i + id;
-    if (kRows * kPieces % threads != 0 && at >= kRows * kPieces) break;
-    const int row = at / kPieces, piece = at % kPieces, k = k0 + 32 * piece;
-    const int n = min(n0 + row, p.N - 1);
-    const bool on = k < p.K;
-    cp16(stage + row * U::kCodePitch + 16 * piece, p.q + (size_t)n * (p.K / 2) + (on ? k / 2 : 0), on);
-  }
-  const int64_t group0 = k0 / kGroup;
-  for (int at = id; at < kRows * U::kScaleWords; at += threads) {
-    const int row = at / U::kScaleWords, i = at - row * U::kScaleWords;
-    const int n = min(n0 + row, p.N - 1);
-    cp_window(stage + U::scales(kRows) + 4 * at, static_cast<const uint8_t*>(p.scale), ((int64_t)n * groups + group0) * 2,
-              (int64_t)p.N * groups * 2, i);
-  }
-  if (p.zero)
-    for (int at = id; at < kRows * U::kZeroWords; at += threads) {
-      const int row = at / U::kZeroWords, i = at - row * U::kZeroWords;
-      const int n = min(n0 + row, p.N - 1);
-      cp_window(stage + U::zeros(kRows) + 4 * at, p.zero, (int64_t)n * groups + group0, (int64_t)p.N * groups, i);
-    }
-  for (int at = id; at < p.M * (kU / 8); at += threads) {
-    const int t = at / (kU / 8), piece = at % (kU / 8), k = k0 + 8 * piece;
-    const bool on = k < p.K;
-    cp16(stage + U::tokens(kRows) + t * U::kXPitch + 16 * piece, static_cast<const T*>(p.x) + t * p.ldx + (on ? k : 0), on);
-  }
-}
-
-// The 16 features of a stage from row `row0` on, times kTiles x 8 tokens: acc += scale * (codes - zero) . x.
-template <typename T, int kU, int kGroup, int kRows, int kTiles>
-__device__ __forceinline__ void multiply(const W4Params& p, uint32_t stage, int n0, int row0, int k0, int lane, float (&acc)[kTiles][4]) {
-  using U = Unit<kU, kGroup>;
-  const int g = lane >> 2, q = lane & 3, groups = p.K / kGroup, group0 = k0 / kGroup;
-  const uint32_t code = stage + (row0 + g) * U::kCodePitch + 4 * q;
-  // byte offsets of the two features' first scale and zero in their windows
-  uint32_t scale[2], zero[2];
-#pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    const int row = row0 + g + 8 * i;
-    const uint32_t at = (uint32_t)min(n0 + row, p.N - 1) * (uint32_t)groups + (uint32_t)group0;
-    scale[i] = stage + U::scales(kRows) + row * U::kScaleWords * 4 + (at * 2 & 3);
-    zero[i] = stage + U::zeros(kRows) + row * U::kZeroWords * 4 + (at & 3);
-  }
-#pragma unroll
-  for (int s = 0; s < U::kGroups; ++s) {
-    if (group0 + s >= groups) break;
-    const uint32_t z0 = Int4<T>::zero2(p.zero ? lds8(zero[0] + s) : 8u), z1 = Int4<T>::zero2(p.zero ? lds8(zero[1] + s) : 8u);
+  for (int s = 0; s < kUnit / kGroup; ++s) {
+    const uint32_t z0 = sc.zero2(0, s), z1 = sc.zero2(1, s);
     float d[kTiles][4];
 #pragma unroll
     for (int t = 0; t < kTiles; ++t) d[t][0] = d[t][1] = d[t][2] = d[t][3] = 0.f;
 #pragma unroll
     for (int b = s * (kGroup / 32); b < (s + 1) * (kGroup / 32); ++b) {
       uint32_t lo[4], hi[4];
-      Int4<T>::expand(lds32(code + 16 * b), z0, lo);
-      Int4<T>::expand(lds32(code + 8 * U::kCodePitch + 16 * b), z1, hi);
+      Int4<T>::expand(lds32(code ^ (16 * b)), z0, lo);
+      Int4<T>::expand(lds32((code ^ (16 * b)) + 1024), z1, hi);
 #pragma unroll
       for (int t = 0; t < kTiles; ++t) {
-        uint4 x = make_uint4(0u, 0u, 0u, 0u);
-        if (8 * t + g < p.M) x = lds128(stage + U::tokens(kRows) + (8 * t + g) * U::kXPitch + 64 * b + 16 * q);
-        Int4<T>::mma(d[t], lo[0], hi[0], lo[1], hi[1], __byte_perm(x.x, x.z, 0x5410), __byte_perm(x.x, x.z, 0x7632));
-        Int4<T>::mma(d[t], lo[2], hi[2], lo[3], hi[3], __byte_perm(x.y, x.w, 0x5410), __byte_perm(x.y, x.w, 0x7632));
+        uint4 v = make_uint4(0u, 0u, 0u, 0u);
+        if (8 * t + g < M) v = lds128(x + 8 * t * pitch + 64 * b);
+        Int4<T>::mma(d[t], lo[0], hi[0], lo[1], hi[1], v.x, v.y);
+        Int4<T>::mma(d[t], lo[2], hi[2], lo[3], hi[3], v.z, v.w);
       }
     }
-    const float s0 = lds_elem<T>(scale[0] + 2 * s), s1 = lds_elem<T>(scale[1] + 2 * s);
+    const float s0 = sc.scale(0, s), s1 = sc.scale(1, s);
 #pragma unroll
     for (int t = 0; t < kTiles; ++t) {
       acc[t][0] = fmaf(s0, d[t][0], acc[t][0]);
@@ -219,51 +211,83 @@ __device__ __forceinline__ void store(const W4Params& p, int n0, int t0, int lan
 
 // ------------------------------------------------------------------ windows of up to 8 tokens
 //
-// Bound by the codes' stream. A block owns a contiguous range of 16-feature tiles and cuts its
-// (tile, unit of kU codes) sequence into eight equal contiguous shares, one per warp; each warp
-// streams its share through a ring of its own, with no barrier until the end. A tile cut between
-// warps is finished from their partial sums, in order.
-constexpr int kRowWarps = 8;
+// A block owns a contiguous range of 16-feature tiles and cuts its (tile, unit) sequence into eight equal
+// contiguous shares, one per warp; each warp streams its share through a ring of its own (one TMA box of
+// 16 x 128 bytes a unit), with no barrier between the first and the last. A tile cut between warps
+// is finished from their partial sums, in order. x stays in shared memory as a whole.
+constexpr int kRowWarps = 8, kRowStages = 4, kRowBytes = 16 * kUnit / 2;
+constexpr int kRowMaxX = 48 * 1024;            // bytes of x that leave room for two blocks on an SM
 
-template <typename T, int kU, int kGroup, int kStages>
-__global__ void __launch_bounds__(32 * kRowWarps) w4_rows_kernel(const W4Params p, int tiles) {
-  using U = Unit<kU, kGroup>;
-  extern __shared__ __align__(128) uint8_t smem[];
+__host__ __device__ inline int x_pitch(int K) { return (K + kUnit - 1) / kUnit * kUnit * 2 + 64; }   // two tokens' loads on other banks
+
+template <typename T, int kGroup>
+__global__ void __launch_bounds__(32 * kRowWarps, 2)
+w4_rows_kernel(const W4Params p, const __grid_constant__ CUtensorMap codes, int tiles) {
+  extern __shared__ uint8_t raw_smem[];
   __shared__ float part[kRowWarps][2][4][32];
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int units = (p.K + kU - 1) / kU;
+  __shared__ __align__(8) uint64_t bars[kRowWarps][kRowStages];
+  __shared__ int dead_flag;
+  volatile int* dead = &dead_flag;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, q = lane & 3;
+  const uint32_t base = (smem_u32(raw_smem) + 1023) & ~1023u;
+  const uint32_t ring = base + warp * kRowStages * kRowBytes, xs = base + kRowWarps * kRowStages * kRowBytes;
+  const uint32_t bar = smem_u32(&bars[warp][0]);
+  const int units = (p.K + kUnit - 1) / kUnit, pitch = x_pitch(p.K);
   const int t0 = (int)((int64_t)tiles * blockIdx.x / gridDim.x), t1 = (int)((int64_t)tiles * (blockIdx.x + 1) / gridDim.x);
   const int all = (t1 - t0) * units;                            // this block's units (the host bounds them)
-  const int u0 = (int)((int64_t)all * warp / kRowWarps), u1 = (int)((int64_t)all * (warp + 1) / kRowWarps);
-  const int bytes = U::bytes(16, p.M);
-  const uint32_t ring = (uint32_t)__cvta_generic_to_shared(smem) + warp * kStages * bytes;
-
-  int ask = u0, ask_tile = u0 / units, ask_unit = u0 - ask_tile * units;
-  uint32_t to = ring;
-  auto next = [&]() {
-    if (ask < u1) {
-      request<T, kU, kGroup, 16>(p, to, (t0 + ask_tile) * 16, ask_unit * kU, lane, 32);
-      ++ask;
-      if (++ask_unit == units) { ask_unit = 0; ++ask_tile; }
-      to = to + bytes == ring + kStages * bytes ? ring : to + bytes;
-    }
-    asm volatile("cp.async.commit_group;" ::: "memory");
-  };
-  for (int i = 0; i < kStages - 1; ++i) next();
+  auto share = [&](int w) { return (int)((int64_t)all * w / kRowWarps); };
+  const int u0 = share(warp), u1 = share(warp + 1);
 
   int tile = u0 / units, unit = u0 - tile * units;
+  int ask = u0, ask_tile = tile, ask_unit = unit;
+  auto request = [&](int stage) {                               // lane 0
+    mbar_arrive_tx(bar + 8 * stage, kRowBytes);
+    tma_codes(ring + stage * kRowBytes, &codes, bar + 8 * stage, ask_unit * (kUnit / 2), (t0 + ask_tile) * 16);
+    ++ask;
+    if (++ask_unit == units) { ask_unit = 0; ++ask_tile; }
+  };
+  if (threadIdx.x == 0) *dead = 0;
+  if (lane == 0) {
+    for (int i = 0; i < kRowStages; ++i) mbar_init(bar + 8 * i, 1);
+    mbar_init_fence();
+    for (int i = 0; i < kRowStages && ask < u1; ++i) request(i);
+  }
+  // the lane's scales of the next two units
+  Scales<T, kGroup> now, next;
+  int s_tile = tile, s_unit = unit, s_at = u0;
+  auto scales = [&](Scales<T, kGroup>& s) {
+    if (s_at < u1) s.load(p, (t0 + s_tile) * 16 + g, s_unit);
+    ++s_at;
+    if (++s_unit == units) { s_unit = 0; ++s_tile; }
+  };
+  scales(now);
+  scales(next);
+  for (int i = threadIdx.x; i < p.M * units * (kUnit / 8); i += 32 * kRowWarps) {
+    const int t = i / (units * (kUnit / 8)), k = (i - t * units * (kUnit / 8)) * 8;
+    const uint4 v = k < p.K ? *reinterpret_cast<const uint4*>(static_cast<const T*>(p.x) + t * p.ldx + k) : make_uint4(0u, 0u, 0u, 0u);
+    sts_paired(xs + t * pitch + 2 * k, v);
+  }
+  __syncthreads();
+
   bool from_start = unit == 0;
-  uint32_t at = ring;
+  int stage = 0;
+  uint32_t phase = 0;
   float acc[1][4] = {{0.f, 0.f, 0.f, 0.f}};
+  const uint32_t code = ring + g * 128 + (g << 4) + 4 * q, x = xs + g * pitch + 16 * q;
   for (int u = u0; u < u1; ++u) {
-    asm volatile("cp.async.wait_group %0;" :: "n"(kStages - 2) : "memory");
-    __syncwarp();                                               // all lanes' copies are here, and the oldest stage is read
-    next();
-    multiply<T, kU, kGroup, 16, 1>(p, at, (t0 + tile) * 16, 0, unit * kU, lane, acc);
-    at = at + bytes == ring + kStages * bytes ? ring : at + bytes;
+    Scales<T, kGroup> later;
+    scales(later);
+    mbar_wait(bar + 8 * stage, phase, p.spin_budget, p.status, dead);
+    __syncwarp();
+    multiply<T, kGroup, 1>(code + stage * kRowBytes, x + unit * (2 * kUnit), pitch, g, p.M, now, acc);
+    __syncwarp();
+    if (lane == 0 && ask < u1 && !*dead) request(stage);
+    now = next;
+    next = later;
+    if (++stage == kRowStages) { stage = 0; phase ^= 1; }
     if (++unit == units || u + 1 == u1) {
       if (from_start && unit == units) {
-        store<T>(p, (t0 + tile) * 16, 0, lane, acc[0]);
+        if (!*dead) store<T>(p, (t0 + tile) * 16, 0, lane, acc[0]);
       } else {
 #pragma unroll
         for (int e = 0; e < 4; ++e) part[warp][from_start ? 1 : 0][e][lane] = acc[0][e];
@@ -273,23 +297,27 @@ __global__ void __launch_bounds__(32 * kRowWarps) w4_rows_kernel(const W4Params 
       if (unit == units) { unit = 0; ++tile; }
     }
   }
-  asm volatile("cp.async.wait_all;" ::: "memory");
   __syncthreads();
+  if (*dead) {
+    // what this warp requested has arrived or arrives now: its i-th copy into a stage ends phase i
+    if (lane == 0)
+      for (int i = 0; i < kRowStages; ++i) {
+        const int n = (ask - u0 - i + kRowStages - 1) / kRowStages;
+        if (ask - u0 > i) mbar_drain(bar + 8 * i, (n - 1) & 1);
+      }
+    return;
+  }
   // the first warp whose share starts inside a tile finishes that tile
   if (u1 == u0 || u0 % units == 0) return;
   const int cut = u0 / units, begin = cut * units;
   int w = warp - 1;
-  while ((int64_t)all * w / kRowWarps > begin) {
-    if ((int)((int64_t)all * (w + 1) / kRowWarps) > (int)((int64_t)all * w / kRowWarps)) return;   // an earlier warp does
-    --w;
-  }
-  while ((int)((int64_t)all * (w + 1) / kRowWarps) <= begin) ++w;
+  for (; share(w) > begin; --w)
+    if (share(w + 1) > share(w)) return;                        // an earlier warp does
+  while (share(w + 1) <= begin) ++w;
 #pragma unroll
   for (int e = 0; e < 4; ++e) acc[0][e] = part[w][1][e][lane];
-  for (++w; w < kRowWarps; ++w) {
-    const int s0 = (int)((int64_t)all * w / kRowWarps), s1 = (int)((int64_t)all * (w + 1) / kRowWarps);
-    if (s0 >= begin + units) break;
-    if (s1 == s0) continue;
+  for (++w; w < kRowWarps && share(w) < begin + units; ++w) {
+    if (share(w + 1) == share(w)) continue;
 #pragma unroll
     for (int e = 0; e < 4; ++e) acc[0][e] += part[w][0][e][lane];
   }
@@ -298,53 +326,105 @@ __global__ void __launch_bounds__(32 * kRowWarps) w4_rows_kernel(const W4Params 
 
 // ------------------------------------------------------------------ wider windows
 //
-// With 9 to 32 tokens the elements of x outweigh the codes of 16 features, so eight warps (128
-// features) share them: one stage holds 128 features x 128 codes and the tokens' elements there.
-// Where there are few blocks of features, a cluster of blocks splits K and joins the sums
-// over distributed shared memory, in rank order.
-constexpr int kWideRows = 128, kWideUnit = 128, kWideStages = 4;
+// Where the window's x does not fit, eight warps of 128 features share its elements: a stage holds one
+// unit of 128 features (one TMA box) and of the tokens. A cluster of blocks splits K where
+// there are few blocks of features, and joins the sums over distributed shared memory, in rank order.
+constexpr int kWideRows = 128, kWideStages = 3, kWideCodes = kWideRows * kUnit / 2, kWidePitch = 2 * kUnit + 64;
 
 template <typename T, int kGroup, int kTiles>
-__global__ void __launch_bounds__(256) w4_wide_kernel(const W4Params p, int split) {
-  using U = Unit<kWideUnit, kGroup>;
-  extern __shared__ __align__(128) uint8_t smem[];
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+__global__ void __launch_bounds__(256, 2)
+w4_wide_kernel(const W4Params p, const __grid_constant__ CUtensorMap codes, int split) {
+  extern __shared__ uint8_t raw_smem[];
+  __shared__ __align__(8) uint64_t bars[kWideStages];
+  __shared__ int dead_flag;
+  volatile int* dead = &dead_flag;
+  constexpr int kChunks = 8 * kTiles * (kUnit / 8) / 256;       // 16-byte pieces of x per thread and stage
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, q = lane & 3;
   const int rank = blockIdx.x % split, n0 = blockIdx.x / split * kWideRows;
-  const int units = (p.K + kWideUnit - 1) / kWideUnit;
-  const int u0 = units * rank / split, u1 = units * (rank + 1) / split;
-  const int bytes = U::bytes(kWideRows, p.M);
-  const uint32_t ring = (uint32_t)__cvta_generic_to_shared(smem);
+  const int units = (p.K + kUnit - 1) / kUnit, u0 = units * rank / split, u1 = units * (rank + 1) / split;
+  const uint32_t base = (smem_u32(raw_smem) + 1023) & ~1023u, xs = base + kWideStages * kWideCodes, bar = smem_u32(bars);
+  const int x_bytes = p.M * kWidePitch;
+
+  auto request = [&](int u) {                                   // thread 0
+    const int stage = (u - u0) % kWideStages;
+    mbar_arrive_tx(bar + 8 * stage, kWideCodes);
+    tma_codes(base + stage * kWideCodes, &codes, bar + 8 * stage, u * (kUnit / 2), n0);
+  };
+  uint4 piece[kChunks];
+  auto load_x = [&](int u) {
+#pragma unroll
+    for (int i = 0; i < kChunks; ++i) {
+      const int at = threadIdx.x + 256 * i, t = at / (kUnit / 8), k = u * kUnit + at % (kUnit / 8) * 8;
+      piece[i] = t < p.M && k < p.K ? *reinterpret_cast<const uint4*>(static_cast<const T*>(p.x) + t * p.ldx + k) : make_uint4(0u, 0u, 0u, 0u);
+    }
+  };
+  auto store_x = [&](int u) {
+#pragma unroll
+    for (int i = 0; i < kChunks; ++i) {
+      const int at = threadIdx.x + 256 * i, t = at / (kUnit / 8);
+      if (t < p.M) sts_paired(xs + (u - u0) % kWideStages * x_bytes + t * kWidePitch + at % (kUnit / 8) * 16, piece[i]);
+    }
+  };
+  if (threadIdx.x == 0) {
+    *dead = 0;
+    for (int i = 0; i < kWideStages; ++i) mbar_init(bar + 8 * i, 1);
+    mbar_init_fence();
+    for (int u = u0; u < u1 && u < u0 + kWideStages - 1; ++u) request(u);
+  }
+  const int n = n0 + warp * 16 + g;
+  Scales<T, kGroup> now, next;
+  if (u0 < u1) now.load(p, n, u0);
+  if (u0 + 1 < u1) next.load(p, n, u0 + 1);
+  for (int u = u0; u < u1 && u < u0 + kWideStages - 1; ++u) {
+    load_x(u);
+    store_x(u);
+  }
   float acc[kTiles][4];
 #pragma unroll
   for (int t = 0; t < kTiles; ++t) acc[t][0] = acc[t][1] = acc[t][2] = acc[t][3] = 0.f;
-  auto ask = [&](int u) {
-    if (u < u1) request<T, kWideUnit, kGroup, kWideRows>(p, ring + (u - u0) % kWideStages * bytes, n0, u * kWideUnit, threadIdx.x, 256);
-    asm volatile("cp.async.commit_group;" ::: "memory");
-  };
-  for (int i = 0; i < kWideStages - 1; ++i) ask(u0 + i);
+  const uint32_t code = base + (warp * 16 + g) * 128 + (g << 4) + 4 * q, x = xs + g * kWidePitch + 16 * q;
+  __syncthreads();
   for (int u = u0; u < u1; ++u) {
-    asm volatile("cp.async.wait_group %0;" :: "n"(kWideStages - 2) : "memory");
+    const int stage = (u - u0) % kWideStages, far = u + kWideStages - 1;
+    // the stage of unit `far` was read last in the iteration before, which every warp has left
+    if (threadIdx.x == 0 && far < u1 && !*dead) request(far);
+    if (far < u1) load_x(far);
+    Scales<T, kGroup> later;
+    if (u + 2 < u1) later.load(p, n, u + 2);
+    mbar_wait(bar + 8 * stage, (u - u0) / kWideStages & 1, p.spin_budget, p.status, dead);
+    __syncwarp();
+    multiply<T, kGroup, kTiles>(code + stage * kWideCodes, x + stage * x_bytes, kWidePitch, g, p.M, now, acc);
+    if (far < u1) store_x(far);
+    now = next;
+    next = later;
     __syncthreads();
-    ask(u + kWideStages - 1);
-    multiply<T, kWideUnit, kGroup, kWideRows, kTiles>(p, ring + (u - u0) % kWideStages * bytes, n0, warp * 16, u * kWideUnit, lane, acc);
   }
+  if (*dead && threadIdx.x == 0)
+    for (int i = 0; i < kWideStages && u0 + i < u1; ++i) mbar_drain(bar + 8 * i, ((u1 - u0 - i + kWideStages - 1) / kWideStages - 1) & 1);
   if (split == 1) {
+    if (*dead) return;
 #pragma unroll
     for (int t = 0; t < kTiles; ++t) store<T>(p, n0 + warp * 16, 8 * t, lane, acc[t]);
     return;
   }
-  asm volatile("cp.async.wait_all;" ::: "memory");
-  __syncthreads();
-  float4* sums = reinterpret_cast<float4*>(smem);
 #pragma unroll
-  for (int t = 0; t < kTiles; ++t) sums[(warp * kTiles + t) * 32 + lane] = make_float4(acc[t][0], acc[t][1], acc[t][2], acc[t][3]);
+  for (int t = 0; t < kTiles; ++t)
+    asm volatile("st.shared.v4.f32 [%0], {%1,%2,%3,%4};" :: "r"(base + ((warp * kTiles + t) * 32 + lane) * 16), "f"(acc[t][0]), "f"(acc[t][1]),
+                 "f"(acc[t][2]), "f"(acc[t][3]) : "memory");
   asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
-  for (int i = rank * 8 + warp; i < 8 * kTiles; i += 8 * split) {
+  bool lost = false;                                            // a dead block anywhere in the cluster
+  for (int r = 0; r < split; ++r) {
+    uint32_t a, v;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_u32(&dead_flag)), "r"(r));
+    asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(a) : "memory");
+    lost |= v != 0;
+  }
+  for (int i = rank * 8 + warp; i < 8 * kTiles && !lost; i += 8 * split) {
     float sum[4] = {0.f, 0.f, 0.f, 0.f};
     for (int r = 0; r < split; ++r) {
       uint32_t a;
       float4 v;
-      asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(ring + (i * 32 + lane) * 16), "r"(r));
+      asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(base + (i * 32 + lane) * 16), "r"(r));
       asm volatile("ld.shared::cluster.v4.f32 {%0,%1,%2,%3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(a) : "memory");
       sum[0] += v.x;
       sum[1] += v.y;
@@ -358,34 +438,41 @@ __global__ void __launch_bounds__(256) w4_wide_kernel(const W4Params p, int spli
 
 // ------------------------------------------------------------------ launches
 
-template <typename K>
-cudaError_t allow_smem(K kernel, int bytes) {
-  return bytes > 48 * 1024 ? cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) : cudaSuccess;
+// The codes as [N][K / 2] bytes; a box is `rows` features x one unit, lines swizzled over 128 bytes.
+bool encode_codes(CUtensorMap* map, const W4Params& p, int rows) {
+  const cuuint64_t dims[2] = {(cuuint64_t)p.K / 2, (cuuint64_t)p.N}, strides[1] = {(cuuint64_t)p.K / 2};
+  const cuuint32_t box[2] = {kUnit / 2, (cuuint32_t)rows}, ones[2] = {1, 1};
+  const EncodeTiledFn fn = encode_tiled();
+  return fn && fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<uint8_t*>(p.q), dims, strides, box, ones,
+                  CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
+                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <typename T, int kU, int kGroup, int kStages>
-cudaError_t launch_rows(const W4Params& p, cudaStream_t s) {
-  const int tiles = (p.N + 15) / 16, smem = kRowWarps * kStages * Unit<kU, kGroup>::bytes(16, p.M);
-  const cudaError_t e = allow_smem(w4_rows_kernel<T, kU, kGroup, kStages>, smem);
+template <typename T, int kGroup>
+cudaError_t launch_rows(const W4Params& p, int dev, cudaStream_t s) {
+  const cudaError_t e = allow_shared_memory<w4_rows_kernel<T, kGroup>>(dev);
   if (e != cudaSuccess) return e;
-  const int grid = tiles < 2 * p.sms ? tiles : 2 * p.sms;
-  w4_rows_kernel<T, kU, kGroup, kStages><<<grid, 32 * kRowWarps, smem, s>>>(p, tiles);
+  CUtensorMap map;
+  if (!encode_codes(&map, p, 16)) return cudaErrorInvalidValue;
+  const int tiles = (p.N + 15) / 16, most = 2 * sm_count(dev);
+  const int smem = 1024 + kRowWarps * kRowStages * kRowBytes + p.M * x_pitch(p.K);
+  w4_rows_kernel<T, kGroup><<<tiles < most ? tiles : most, 32 * kRowWarps, smem, s>>>(p, map, tiles);
   return cudaGetLastError();
 }
 
 template <typename T, int kGroup, int kTiles>
-cudaError_t launch_wide(const W4Params& p, cudaStream_t s) {
-  const int blocks = (p.N + kWideRows - 1) / kWideRows, units = (p.K + kWideUnit - 1) / kWideUnit;
-  int split = 1;
-  while (split < 8 && blocks * split < p.sms && units >= 4 * split) split *= 2;
-  const int ring = kWideStages * Unit<kWideUnit, kGroup>::bytes(kWideRows, p.M), sums = 8 * kTiles * 32 * 16;
-  const int smem = ring > sums ? ring : sums;
-  cudaError_t e = allow_smem(w4_wide_kernel<T, kGroup, kTiles>, smem);
+cudaError_t launch_wide(const W4Params& p, int dev, cudaStream_t s) {
+  cudaError_t e = allow_shared_memory<w4_wide_kernel<T, kGroup, kTiles>>(dev);
   if (e != cudaSuccess) return e;
+  CUtensorMap map;
+  if (!encode_codes(&map, p, kWideRows)) return cudaErrorInvalidValue;
+  const int blocks = (p.N + kWideRows - 1) / kWideRows, units = (p.K + kUnit - 1) / kUnit;
+  int split = 1;
+  while (split < 8 && blocks * split < sm_count(dev) && units >= 4 * split) split *= 2;
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3((unsigned)(blocks * split));
   cfg.blockDim = dim3(256);
-  cfg.dynamicSmemBytes = smem;
+  cfg.dynamicSmemBytes = 1024 + kWideStages * (kWideCodes + p.M * kWidePitch);
   cfg.stream = s;
   cudaLaunchAttribute a{};
   a.id = cudaLaunchAttributeClusterDimension;
@@ -393,20 +480,18 @@ cudaError_t launch_wide(const W4Params& p, cudaStream_t s) {
   a.val.clusterDim.y = a.val.clusterDim.z = 1;
   cfg.attrs = &a;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, w4_wide_kernel<T, kGroup, kTiles>, p, split);
+  return cudaLaunchKernelEx(&cfg, w4_wide_kernel<T, kGroup, kTiles>, p, map, split);
 }
 
 template <typename T, int kGroup>
-cudaError_t launch(const W4Params& p, cudaStream_t s) {
-  if (p.M == 1) return launch_rows<T, 256, kGroup, 4>(p, s);
-  if (p.M == 2) return launch_rows<T, 256, kGroup, 3>(p, s);
-  if (p.M <= 4) return launch_rows<T, 128, kGroup, 4>(p, s);
-  if (p.M <= 8) return launch_rows<T, 128, kGroup, 3>(p, s);
-  return p.M <= 16 ? launch_wide<T, kGroup, 2>(p, s) : launch_wide<T, kGroup, 4>(p, s);
+cudaError_t launch(const W4Params& p, int dev, cudaStream_t s) {
+  if (p.M <= 8 && p.M * x_pitch(p.K) <= kRowMaxX) return launch_rows<T, kGroup>(p, dev, s);
+  if (p.M <= 8) return launch_wide<T, kGroup, 1>(p, dev, s);
+  return p.M <= 16 ? launch_wide<T, kGroup, 2>(p, dev, s) : launch_wide<T, kGroup, 4>(p, dev, s);
 }
 template <typename T>
-cudaError_t launch(const W4Params& p, int group, cudaStream_t s) {
-  return group == 32 ? launch<T, 32>(p, s) : (group == 64 ? launch<T, 64>(p, s) : launch<T, 128>(p, s));
+cudaError_t launch(const W4Params& p, int group, int dev, cudaStream_t s) {
+  return group == 32 ? launch<T, 32>(p, dev, s) : (group == 64 ? launch<T, 64>(p, dev, s) : launch<T, 128>(p, dev, s));
 }
 
 }  // namespace
@@ -416,7 +501,7 @@ using namespace mdw;
 
 extern "C" mdw_status w4_linear(const mdw_w4_weights* w, int32_t M, const void* x, int64_t ldx, void* y,
                                 int64_t ldy, int32_t y_dtype, const void* bias, const void* residual,
-                                int64_t ldr, mdw_stream_t stream) {
+                                int64_t ldr, uint32_t* status, mdw_stream_t stream) {
   if (!w) return MDW_ERR_INVALID_ARG;
   if (w->magic != MDW_MAGIC || w->fmt != MDW_FMT_INT4_GROUP) return MDW_ERR_FORMAT_MISMATCH;
   if (w->dtype != MDW_DT_BF16 && w->dtype != MDW_DT_F16) return MDW_ERR_FORMAT_MISMATCH;
@@ -427,15 +512,15 @@ extern "C" mdw_status w4_linear(const mdw_w4_weights* w, int32_t M, const void* 
     return MDW_ERR_INVALID_ARG;
   if (y_dtype != w->dtype && y_dtype != MDW_DT_F32) return MDW_ERR_FORMAT_MISMATCH;
   if (!aligned_to(y, y_dtype == MDW_DT_F32 ? 4 : 2) || ldy < w->n || !null_or_aligned(bias, 2) ||
-      !null_or_aligned(residual, 2) || (residual && ldr < w->n))
+      !null_or_aligned(residual, 2) || (residual && ldr < w->n) || !null_or_aligned(status, 4))
     return MDW_ERR_INVALID_ARG;
-  const int sms = device_sm_count();
+  const int dev = current_device(), sms = sm_count(dev);
   if (sms <= 0) return MDW_ERR_CUDA;
   // units of one block's share of the tiles stay far below 2^31
-  if ((int64_t)((w->n + 15) / 16 / sms + 1) * (w->k / 128 + 1) > 1 << 28) return MDW_ERR_UNSUPPORTED_SHAPE;
+  if ((int64_t)((w->n + 15) / 16 / sms + 1) * (w->k / kUnit + 1) > 1 << 28) return MDW_ERR_UNSUPPORTED_SHAPE;
   const W4Params p{static_cast<const uint8_t*>(w->q), w->scale, static_cast<const uint8_t*>(w->zero), x, y, bias,
-                   residual, ldx, ldy, ldr, M, w->n, w->k, y_dtype == MDW_DT_F32, sms};
+                   residual, ldx, ldy, ldr, status, mdw_spin_budget(), M, w->n, w->k, y_dtype == MDW_DT_F32};
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  const cudaError_t e = w->dtype == MDW_DT_BF16 ? launch<__nv_bfloat16>(p, w->group, s) : launch<__half>(p, w->group, s);
+  const cudaError_t e = w->dtype == MDW_DT_BF16 ? launch<__nv_bfloat16>(p, w->group, dev, s) : launch<__half>(p, w->group, dev, s);
   return e == cudaSuccess ? MDW_OK : MDW_ERR_CUDA;
 }

@@ -33,16 +33,16 @@ def test_limits_match_the_header():
     ("magic", 0, 3), ("fmt", api.FMT_MXFP4, 3), ("dtype", F32, 3), ("group", 16, 2), ("group", 256, 2), ("n", 0, 2),
     ("k", 2592, 2), ("k", 0, 2), ("q", FAKE + 8, 1), ("q", None, 1), ("scale", None, 1), ("scale", FAKE + 8, 1), ("zero", FAKE + 8, 1)])
 def test_w4_rejects_weights(field, value, code):
-    assert api.lib().w4_linear(_w4(**{field: value}), 1, FAKE, 2560, FAKE, 100, BF, None, None, 0, None) == code
+    assert api.lib().w4_linear(_w4(**{field: value}), 1, FAKE, 2560, FAKE, 100, BF, None, None, 0, None, None) == code
 
 
 @pytest.mark.parametrize("kw,code", [
     (dict(m=0), 1), (dict(m=33), 1), (dict(x=None), 1), (dict(x=FAKE + 2), 1), (dict(ldx=2552), 1), (dict(ldx=2561), 1),
     (dict(y=FAKE + 1), 1), (dict(y=None), 1), (dict(ldy=99), 1), (dict(yd=HF), 3), (dict(yd=0), 3), (dict(yd=F32, y=FAKE + 2), 1),
-    (dict(bias=FAKE + 1), 1), (dict(res=FAKE + 1, ldr=100), 1), (dict(res=FAKE, ldr=99), 1)])
+    (dict(bias=FAKE + 1), 1), (dict(res=FAKE + 1, ldr=100), 1), (dict(res=FAKE, ldr=99), 1), (dict(status=FAKE + 2), 1)])
 def test_w4_rejects_arguments(kw, code):
-    a = dict(m=1, x=FAKE, ldx=2560, y=FAKE, ldy=100, yd=BF, bias=None, res=None, ldr=0) | kw
-    assert api.lib().w4_linear(_w4(), a["m"], a["x"], a["ldx"], a["y"], a["ldy"], a["yd"], a["bias"], a["res"], a["ldr"], None) == code
+    a = dict(m=1, x=FAKE, ldx=2560, y=FAKE, ldy=100, yd=BF, bias=None, res=None, ldr=0, status=None) | kw
+    assert api.lib().w4_linear(_w4(), a["m"], a["x"], a["ldx"], a["y"], a["ldy"], a["yd"], a["bias"], a["res"], a["ldr"], a["status"], None) == code
 
 
 @pytest.mark.parametrize("kw,code", [

@@ -76,7 +76,8 @@ def test_w4_linear(m, n, k, group, zero, dtype, ydtype):
 
 
 @pytest.mark.parametrize("n,k,group", [(17, 32, 32), (1, 32, 32), (15, 96, 32), (16, 64, 64), (100, 192, 64), (48, 384, 128),
-                                       (31, 16384, 32), (2049, 640, 128), (10007, 512, 64), (7, 9984, 128)])
+                                       (31, 16384, 32), (2049, 640, 128), (10007, 512, 64), (7, 9984, 128),
+                                       (300, 2592, 32), (50, 2624, 64), (5000, 1024, 32)])
 @pytest.mark.parametrize("m", [1, 6, 32])
 def test_w4_linear_shapes(m, n, k, group):
     w = w4_case(n + k, n, k, group, n % 2 == 1, BF if k % 3 else HF)
