@@ -5,13 +5,13 @@
 // the tensor cores (integers up to 15 times 16-bit elements, exact products, fp32 sums), the outer
 // one in fp32. m16n8k16 with 16 features as the rows and 8 tokens as the columns.
 //
-// Codes. A lane (g, q) holds features g and g + 8; of every 32-code block it takes word q (8 codes,
-// k = 8 q .. 8 q + 7), so the four lanes of a product always share a group, whatever its width. Masking
-// a word by 0x000f000f leaves codes j and j + 4 in its halves, under the exponent of 128 (bf16) or 1024
-// (f16) that is code + 128 or + 1024 exactly; subtracting 128 + zero or 1024 + zero leaves code - zero.
-// The token's elements are put in the same order once, when they enter shared memory.
-// This expansion bounds the kernels beside the codes' stream: 7 (bf16) or 5 (f16) operations of the integer
-// pipe for eight codes of a feature, whatever the number of tokens, so nothing else is left per code.
+// Codes. A lane (g, q) of a product holds two features and a quarter of a group's codes (8, 16 or 32 of them, one
+// load), so the four lanes of a product always share a group. Masking a word by 0x000f000f leaves codes
+// j and j + 4 in its halves, under the exponent of 128 (bf16) or 1024 (f16) that is code + 128 or + 1024
+// exactly; subtracting 128 + zero or 1024 + zero leaves code - zero. The token's elements are put in the
+// same order once, when they enter shared memory. This expansion bounds the kernels beside the codes'
+// stream: 11 (bf16) or 9 (f16) operations for eight codes of a feature, whatever the number of tokens, of
+// which 7 or 5 on the integer pipe.
 #include <cstring>
 
 #include "mdw_attn.cuh"
@@ -34,7 +34,13 @@ struct W4Params {
   int M, N, K, y_f32;
 };
 
-constexpr int kUnit = 256;                     // codes of a row in one copy: 128 bytes, one swizzled line
+constexpr int kUnit = 256;                     // codes of a feature in one swizzled line of 128 bytes
+
+__device__ __forceinline__ uint32_t and_or(uint32_t v, uint32_t mask, uint32_t bits) {
+  uint32_t r;
+  asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(r) : "r"(v), "r"(mask), "r"(bits));   // (v & mask) | bits in one operation
+  return r;
+}
 
 template <typename T> struct Int4;
 template <> struct Int4<__nv_bfloat16> {
@@ -47,11 +53,12 @@ template <> struct Int4<__nv_bfloat16> {
   }
   static __device__ __forceinline__ void expand(uint32_t w, uint32_t z2, uint32_t (&p)[4]) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) p[i] = sub(((w >> (4 * i)) & 0x000f000fu) | 0x43004300u, z2);
+    for (int i = 0; i < 4; ++i) p[i] = sub(and_or(w >> (4 * i), 0x000f000fu, 0x43004300u), z2);
   }
-  static __device__ __forceinline__ void mma(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
-    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
-                 : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3]) : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+  static __device__ __forceinline__ void mma(float (&d)[4], const float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%11,%12,%13};"
+                 : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+                 : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(c[0]), "f"(c[1]), "f"(c[2]), "f"(c[3]));
   }
 };
 template <> struct Int4<__half> {
@@ -63,27 +70,29 @@ template <> struct Int4<__half> {
     const uint32_t nz = 0xd400d400u + ((z2 & 0x000f000fu) << 4);
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-      const uint32_t v = w >> (8 * i), lo = (v & 0x000f000fu) | 0x64006400u, hi = (v & 0x00f000f0u) | 0x64006400u;
+      const uint32_t v = w >> (8 * i), lo = and_or(v, 0x000f000fu, 0x64006400u), hi = and_or(v, 0x00f000f0u, 0x64006400u);
       asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(p[2 * i]) : "r"(lo), "r"(z2));
       asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(p[2 * i + 1]) : "r"(hi), "r"(0x2c002c00u), "r"(nz));
     }
   }
-  static __device__ __forceinline__ void mma(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
-    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
-                 : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3]) : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+  static __device__ __forceinline__ void mma(float (&d)[4], const float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%11,%12,%13};"
+                 : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+                 : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(c[0]), "f"(c[1]), "f"(c[2]), "f"(c[3]));
   }
 };
 
 
-__device__ __forceinline__ uint32_t lds32(uint32_t a) {
-  uint32_t v;
-  asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(a) : "memory");
-  return v;
-}
 __device__ __forceinline__ uint4 lds128(uint32_t a) {
   uint4 v;
   asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a) : "memory");
   return v;
+}
+template <int kWords> __device__ __forceinline__ void lds_words(uint32_t (&w)[kWords], uint32_t a) {
+  if constexpr (kWords == 1) asm volatile("ld.shared.u32 %0, [%1];" : "=r"(w[0]) : "r"(a) : "memory");
+  if constexpr (kWords == 2) asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];" : "=r"(w[0]), "=r"(w[1]) : "r"(a) : "memory");
+  if constexpr (kWords == 4)
+    asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]) : "r"(a) : "memory");
 }
 // Eight elements of a token in the order of the expanded codes: pairs (j, j + 4).
 __device__ __forceinline__ void sts_paired(uint32_t a, uint4 v) {
@@ -95,53 +104,82 @@ __device__ __forceinline__ void tma_codes(uint32_t dst, const CUtensorMap* map, 
                :: "r"(dst), "l"(map), "r"(byte), "r"(row), "r"(bar) : "memory");
 }
 
-// Scales and zeros of one unit for a lane's two features, requested two units ahead: the sectors come
+// Where a lane's two features' scales and zeros lie.
+template <typename T>
+struct ScaleRows {
+  const uint16_t* s[2];
+  const uint8_t* z[2];
+  __device__ __forceinline__ void begin(const W4Params& p, int n, int groups) {
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const size_t at = (size_t)min(n + 8 * i, p.N - 1) * groups;
+      s[i] = static_cast<const uint16_t*>(p.scale) + at;
+      z[i] = p.zero + at;                       // not read without zeros
+    }
+  }
+};
+
+// Scales and zeros of one unit for those features, requested one unit ahead: the sectors come
 // from memory, and a load at the point of use would stall every unit.
 template <typename T, int kGroup>
 struct Scales {
   static constexpr int kGroups = kUnit / kGroup;
   uint32_t s[2][kGroups / 2], z[2][(kGroups + 3) / 4];
 
-  // Rows of whole units start on the boundary of a unit's scales, so one load serves a row; otherwise
-  // the scales are read one by one (and those behind the row's end not at all).
-  __device__ __forceinline__ void load(const W4Params& p, int n, int unit) {
-    const int groups = p.K / kGroup, first = unit * kGroups;
+  // Rows of whole units start on the boundary of a unit's scales, so one load serves a row.
+  __device__ __forceinline__ void load(const W4Params& p, const ScaleRows<T>& rows, int unit) {
+    if (p.K % kUnit != 0) {
+      Scales part;
+      part.load_single(p, rows, unit);
+      *this = part;
+      return;
+    }
+    const int first = unit * kGroups;
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-      const size_t at = (size_t)min(n + 8 * i, p.N - 1) * groups + first;
-      const uint16_t* src = static_cast<const uint16_t*>(p.scale) + at;
-#pragma unroll
-      for (int j = 0; j < (kGroups + 3) / 4; ++j) z[i][j] = 0x08080808u;
-      if (p.K % kUnit == 0) {
-        if constexpr (kGroups == 2) {
-          s[i][0] = __ldg(reinterpret_cast<const uint32_t*>(src));
-          if (p.zero) z[i][0] = __ldg(reinterpret_cast<const uint16_t*>(p.zero + at));
-        } else if constexpr (kGroups == 4) {
-          const uint2 v = __ldg(reinterpret_cast<const uint2*>(src));
-          s[i][0] = v.x;
-          s[i][1] = v.y;
-          if (p.zero) z[i][0] = __ldg(reinterpret_cast<const uint32_t*>(p.zero + at));
-        } else {
-          const uint4 v = __ldg(reinterpret_cast<const uint4*>(src));
-          s[i][0] = v.x;
-          s[i][1] = v.y;
-          s[i][2] = v.z;
-          s[i][3] = v.w;
-          if (p.zero) {
-            const uint2 u = __ldg(reinterpret_cast<const uint2*>(p.zero + at));
-            z[i][0] = u.x;
-            z[i][1] = u.y;
-          }
-        }
+      const uint16_t* src = rows.s[i] + first;
+      if constexpr (kGroups == 2) {
+        s[i][0] = __ldg(reinterpret_cast<const uint32_t*>(src));
+      } else if constexpr (kGroups == 4) {
+        const uint2 v = __ldg(reinterpret_cast<const uint2*>(src));
+        s[i][0] = v.x;
+        s[i][1] = v.y;
       } else {
+        const uint4 v = __ldg(reinterpret_cast<const uint4*>(src));
+        s[i][0] = v.x;
+        s[i][1] = v.y;
+        s[i][2] = v.z;
+        s[i][3] = v.w;
+      }
+    }
+    if (p.zero) {
 #pragma unroll
-        for (int j = 0; j < kGroups / 2; ++j) s[i][j] = 0u;
-#pragma unroll
-        for (int j = 0; j < kGroups; ++j) {
-          if (first + j >= groups) break;
-          s[i][j / 2] |= (uint32_t)__ldg(src + j) << (16 * (j & 1));
-          if (p.zero) z[i][j / 4] = (z[i][j / 4] & ~(0xffu << (8 * (j & 3)))) | (uint32_t)__ldg(p.zero + at + j) << (8 * (j & 3));
+      for (int i = 0; i < 2; ++i) {
+        const uint8_t* zero = rows.z[i] + first;
+        if constexpr (kGroups == 2) {
+          z[i][0] = __ldg(reinterpret_cast<const uint16_t*>(zero));
+        } else if constexpr (kGroups == 4) {
+          z[i][0] = __ldg(reinterpret_cast<const uint32_t*>(zero));
+        } else {
+          const uint2 u = __ldg(reinterpret_cast<const uint2*>(zero));
+          z[i][0] = u.x;
+          z[i][1] = u.y;
         }
+      }
+    } else {
+#pragma unroll
+      for (int j = 0; j < (kGroups + 3) / 4; ++j) z[0][j] = z[1][j] = 0x08080808u;
+    }
+  }
+  // Otherwise the scales are read one by one, and those behind the row's end not at all.
+  __device__ __noinline__ void load_single(const W4Params& p, const ScaleRows<T>& rows, int unit) {
+    const int first = unit * kGroups, left = p.K / kGroup - first;
+    for (int i = 0; i < 2; ++i) {
+      for (int j = 0; j < (kGroups + 3) / 4; ++j) z[i][j] = 0x08080808u;
+      for (int j = 0; j < kGroups / 2; ++j) s[i][j] = 0u;
+      for (int j = 0; j < kGroups && j < left; ++j) {
+        s[i][j / 2] |= (uint32_t)__ldg(rows.s[i] + first + j) << (16 * (j & 1));
+        if (p.zero) z[i][j / 4] = (z[i][j / 4] & ~(0xffu << (8 * (j & 3)))) | (uint32_t)__ldg(rows.z[i] + first + j) << (8 * (j & 3));
       }
     }
   }
@@ -156,50 +194,74 @@ struct Scales {
   }
 };
 
-// 16 features x one unit x kTiles * 8 tokens: acc += scale * (codes - zero) . x. `code`: the lane's word of
-// feature g, block 0, in the swizzled line (feature g + 8 lies 1,024 bytes further; block b is at
-// code ^ 16 b); `x`: token g, elements 8 q of the unit, tokens `pitch` bytes apart. Codes and elements behind K
-// are zeros.
+// A lane's part of a line and of a token. Feature of product row g: bit-reversed g, so that the rows that one
+// phase of a 4-, 8- or 16-byte load touches lie in different banks of the swizzled lines.
+template <int kGroup>
+struct Lane {
+  static constexpr int kWords = kGroup / 32;                    // words of a group per lane
+  static __device__ __forceinline__ int feature(int lane) { return lane >> 4 | (lane >> 2 & 2) | (lane & 4); }
+  // Offset of group 0 in the line of `feature`; group s lies at this ^ (s * kGroup / 2).
+  static __device__ __forceinline__ uint32_t code(int lane) {
+    const int f = feature(lane), q = lane & 3;
+    return f * 128 + (((kWords == 4 ? q : kWords == 2 ? q >> 1 : 0) << 4) ^ (f << 4)) + (kWords == 2 ? (q & 1) * 8 : kWords == 1 ? q * 4 : 0);
+  }
+  // Where elements k .. k + 7 of a token go: word w of lane q of a group at 64 w + 16 q.
+  static __device__ __forceinline__ int element(int k) {
+    const int c = k % kGroup / 8;
+    return k / kGroup * (2 * kGroup) + c % kWords * 64 + c / kWords * 16;
+  }
+};
+
+// 16 features x kUnit codes x kTiles * 8 tokens: acc += scale * (codes - zero) . x. `code`: the lane's words of
+// group 0 (its second feature lies 1,024 bytes further). x[t]: the lane's elements of its token in tile
+// t; a column without a token repeats the last one's, its sums are not stored. Codes and elements behind
+// K are zeros.
 template <typename T, int kGroup, int kTiles>
-__device__ __forceinline__ void multiply(uint32_t code, uint32_t x, uint32_t pitch, int g, int M, const Scales<T, kGroup>& sc,
-                                         float (&acc)[kTiles][4]) {
+__device__ __forceinline__ void multiply(uint32_t code, const uint32_t (&x)[kTiles], const Scales<T, kGroup>& sc, float (&acc)[kTiles][4]) {
+  constexpr int kWords = Lane<kGroup>::kWords;
+  constexpr float kNone[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
   for (int s = 0; s < kUnit / kGroup; ++s) {
     const uint32_t z0 = sc.zero2(0, s), z1 = sc.zero2(1, s);
-    float d[kTiles][4];
+    // one tile's products are two chains, so that one need not wait for the other's result
+    constexpr int kChains = kTiles == 1 && kWords > 1 ? 2 : 1;
+    float d[kChains][kTiles][4];
+    uint32_t w0[kWords], w1[kWords];
+    lds_words<kWords>(w0, code ^ (s * kGroup / 2));
+    lds_words<kWords>(w1, (code ^ (s * kGroup / 2)) + 1024);
 #pragma unroll
-    for (int t = 0; t < kTiles; ++t) d[t][0] = d[t][1] = d[t][2] = d[t][3] = 0.f;
-#pragma unroll
-    for (int b = s * (kGroup / 32); b < (s + 1) * (kGroup / 32); ++b) {
+    for (int w = 0; w < kWords; ++w) {
       uint32_t lo[4], hi[4];
-      Int4<T>::expand(lds32(code ^ (16 * b)), z0, lo);
-      Int4<T>::expand(lds32((code ^ (16 * b)) + 1024), z1, hi);
+      Int4<T>::expand(w0[w], z0, lo);
+      Int4<T>::expand(w1[w], z1, hi);
 #pragma unroll
       for (int t = 0; t < kTiles; ++t) {
-        uint4 v = make_uint4(0u, 0u, 0u, 0u);
-        if (8 * t + g < M) v = lds128(x + 8 * t * pitch + 64 * b);
-        Int4<T>::mma(d[t], lo[0], hi[0], lo[1], hi[1], v.x, v.y);
-        Int4<T>::mma(d[t], lo[2], hi[2], lo[3], hi[3], v.z, v.w);
+        float (&sum)[4] = d[w % kChains][t];
+        const uint4 v = lds128(x[t] + s * (2 * kGroup) + 64 * w);
+        if (w < kChains) Int4<T>::mma(sum, kNone, lo[0], hi[0], lo[1], hi[1], v.x, v.y);
+        else Int4<T>::mma(sum, sum, lo[0], hi[0], lo[1], hi[1], v.x, v.y);
+        Int4<T>::mma(sum, sum, lo[2], hi[2], lo[3], hi[3], v.z, v.w);
       }
     }
     const float s0 = sc.scale(0, s), s1 = sc.scale(1, s);
 #pragma unroll
-    for (int t = 0; t < kTiles; ++t) {
-      acc[t][0] = fmaf(s0, d[t][0], acc[t][0]);
-      acc[t][1] = fmaf(s0, d[t][1], acc[t][1]);
-      acc[t][2] = fmaf(s1, d[t][2], acc[t][2]);
-      acc[t][3] = fmaf(s1, d[t][3], acc[t][3]);
-    }
+    for (int t = 0; t < kTiles; ++t)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        float sum = d[0][t][e];
+        if constexpr (kChains == 2) sum += d[1][t][e];
+        acc[t][e] = fmaf(e < 2 ? s0 : s1, sum, acc[t][e]);
+      }
   }
 }
 
-// Features n0 + {g, g + 8}, tokens t0 + 2 q + {0, 1}: bias, residual, one rounding.
+// The lane's two features of the 16 from n0 on, tokens t0 + 2 q + {0, 1}: bias, residual, one rounding.
 template <typename T>
 __device__ __forceinline__ void store(const W4Params& p, int n0, int t0, int lane, const float (&acc)[4]) {
-  const int g = lane >> 2, q = lane & 3;
+  const int f = Lane<32>::feature(lane), q = lane & 3;
 #pragma unroll
   for (int e = 0; e < 4; ++e) {
-    const int n = n0 + g + 8 * (e >> 1), t = t0 + 2 * q + (e & 1);
+    const int n = n0 + f + 8 * (e >> 1), t = t0 + 2 * q + (e & 1);
     if (n >= p.N || t >= p.M) continue;
     float v = acc[e];
     if (p.bias) v += Elem<T>::to_float(static_cast<const T*>(p.bias)[n]);
@@ -212,13 +274,14 @@ __device__ __forceinline__ void store(const W4Params& p, int n0, int t0, int lan
 // ------------------------------------------------------------------ windows of up to 8 tokens
 //
 // A block owns a contiguous range of 16-feature tiles and cuts its (tile, unit) sequence into eight equal
-// contiguous shares, one per warp; each warp streams its share through a ring of its own (one TMA box of
+// contiguous shares, one per warp; each warp streams its share through a ring of its own (two TMA boxes of
 // 16 x 128 bytes a unit), with no barrier between the first and the last. A tile cut between warps
 // is finished from their partial sums, in order. x stays in shared memory as a whole.
-constexpr int kRowWarps = 8, kRowStages = 4, kRowBytes = 16 * kUnit / 2;
-constexpr int kRowMaxX = 48 * 1024;            // bytes of x that leave room for two blocks on an SM
+constexpr int kRowWarps = 8, kRowStages = 2, kLineBytes = 16 * kUnit / 2, kRowUnit = 2 * kUnit, kRowBytes = 2 * kLineBytes;
+constexpr int kRowMaxX = 36 * 1024;            // bytes of x that leave room for two blocks on an SM
 
-__host__ __device__ inline int x_pitch(int K) { return (K + kUnit - 1) / kUnit * kUnit * 2 + 64; }   // two tokens' loads on other banks
+// Bytes of a token in shared memory, whole units; 64 more put two tokens' loads on different banks.
+__host__ __device__ inline int x_pitch(int K) { return (K + kRowUnit - 1) / kRowUnit * kRowUnit * 2 + 64; }
 
 template <typename T, int kGroup>
 __global__ void __launch_bounds__(32 * kRowWarps, 2)
@@ -228,11 +291,11 @@ w4_rows_kernel(const W4Params p, const __grid_constant__ CUtensorMap codes, int 
   __shared__ __align__(8) uint64_t bars[kRowWarps][kRowStages];
   __shared__ int dead_flag;
   volatile int* dead = &dead_flag;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, q = lane & 3;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, f = Lane<kGroup>::feature(lane);
   const uint32_t base = (smem_u32(raw_smem) + 1023) & ~1023u;
   const uint32_t ring = base + warp * kRowStages * kRowBytes, xs = base + kRowWarps * kRowStages * kRowBytes;
   const uint32_t bar = smem_u32(&bars[warp][0]);
-  const int units = (p.K + kUnit - 1) / kUnit, pitch = x_pitch(p.K);
+  const int units = (p.K + kRowUnit - 1) / kRowUnit, pitch = x_pitch(p.K);
   const int t0 = (int)((int64_t)tiles * blockIdx.x / gridDim.x), t1 = (int)((int64_t)tiles * (blockIdx.x + 1) / gridDim.x);
   const int all = (t1 - t0) * units;                            // this block's units (the host bounds them)
   auto share = [&](int w) { return (int)((int64_t)all * w / kRowWarps); };
@@ -242,7 +305,8 @@ w4_rows_kernel(const W4Params p, const __grid_constant__ CUtensorMap codes, int 
   int ask = u0, ask_tile = tile, ask_unit = unit;
   auto request = [&](int stage) {                               // lane 0
     mbar_arrive_tx(bar + 8 * stage, kRowBytes);
-    tma_codes(ring + stage * kRowBytes, &codes, bar + 8 * stage, ask_unit * (kUnit / 2), (t0 + ask_tile) * 16);
+    tma_codes(ring + stage * kRowBytes, &codes, bar + 8 * stage, ask_unit * (kRowUnit / 2), (t0 + ask_tile) * 16);
+    tma_codes(ring + stage * kRowBytes + kLineBytes, &codes, bar + 8 * stage, ask_unit * (kRowUnit / 2) + kUnit / 2, (t0 + ask_tile) * 16);
     ++ask;
     if (++ask_unit == units) { ask_unit = 0; ++ask_tile; }
   };
@@ -252,20 +316,35 @@ w4_rows_kernel(const W4Params p, const __grid_constant__ CUtensorMap codes, int 
     mbar_init_fence();
     for (int i = 0; i < kRowStages && ask < u1; ++i) request(i);
   }
-  // the lane's scales of the next two units
-  Scales<T, kGroup> now, next;
+  Scales<T, kGroup> now[2], next[2];
+  ScaleRows<T> rows;
   int s_tile = tile, s_unit = unit, s_at = u0;
-  auto scales = [&](Scales<T, kGroup>& s) {
-    if (s_at < u1) s.load(p, (t0 + s_tile) * 16 + g, s_unit);
+  rows.begin(p, (t0 + tile) * 16 + f, p.K / kGroup);
+  auto scales = [&](Scales<T, kGroup> (&s)[2]) {
+    if (s_at >= u1) return;
+    s[0].load(p, rows, 2 * s_unit);
+    if (s_unit * kRowUnit + kUnit < p.K) s[1].load(p, rows, 2 * s_unit + 1);
     ++s_at;
-    if (++s_unit == units) { s_unit = 0; ++s_tile; }
+    if (++s_unit == units) {
+      s_unit = 0;
+      ++s_tile;
+      rows.begin(p, (t0 + s_tile) * 16 + f, p.K / kGroup);
+    }
   };
   scales(now);
-  scales(next);
-  for (int i = threadIdx.x; i < p.M * units * (kUnit / 8); i += 32 * kRowWarps) {
-    const int t = i / (units * (kUnit / 8)), k = (i - t * units * (kUnit / 8)) * 8;
-    const uint4 v = k < p.K ? *reinterpret_cast<const uint4*>(static_cast<const T*>(p.x) + t * p.ldx + k) : make_uint4(0u, 0u, 0u, 0u);
-    sts_paired(xs + t * pitch + 2 * k, v);
+  const int pieces = units * (kRowUnit / 8), all_pieces = p.M * pieces;
+  for (int i = threadIdx.x; i < all_pieces; i += 4 * 32 * kRowWarps) {
+    uint4 v[4];
+    uint32_t to[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const int at = i + j * 32 * kRowWarps, t = at / pieces, k = (at - t * pieces) * 8;
+      to[j] = xs + t * pitch + Lane<kGroup>::element(k);
+      v[j] = at < all_pieces && k < p.K ? *reinterpret_cast<const uint4*>(static_cast<const T*>(p.x) + t * p.ldx + k) : make_uint4(0u, 0u, 0u, 0u);
+    }
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      if (i + j * 32 * kRowWarps < all_pieces) sts_paired(to[j], v[j]);
   }
   __syncthreads();
 
@@ -273,17 +352,18 @@ w4_rows_kernel(const W4Params p, const __grid_constant__ CUtensorMap codes, int 
   int stage = 0;
   uint32_t phase = 0;
   float acc[1][4] = {{0.f, 0.f, 0.f, 0.f}};
-  const uint32_t code = ring + g * 128 + (g << 4) + 4 * q, x = xs + g * pitch + 16 * q;
+  const uint32_t code = ring + Lane<kGroup>::code(lane), x = xs + min(lane >> 2, p.M - 1) * pitch + 16 * (lane & 3);
   for (int u = u0; u < u1; ++u) {
-    Scales<T, kGroup> later;
-    scales(later);
+    scales(next);
     mbar_wait(bar + 8 * stage, phase, p.spin_budget, p.status, dead);
     __syncwarp();
-    multiply<T, kGroup, 1>(code + stage * kRowBytes, x + unit * (2 * kUnit), pitch, g, p.M, now, acc);
+    const uint32_t at = code + stage * kRowBytes, x0[1] = {x + unit * (2 * kRowUnit)}, x1[1] = {x0[0] + 2 * kUnit};
+    multiply<T, kGroup, 1>(at, x0, now[0], acc);
+    if (unit * kRowUnit + kUnit < p.K) multiply<T, kGroup, 1>(at + kLineBytes, x1, now[1], acc);
     __syncwarp();
     if (lane == 0 && ask < u1 && !*dead) request(stage);
-    now = next;
-    next = later;
+    now[0] = next[0];
+    now[1] = next[1];
     if (++stage == kRowStages) { stage = 0; phase ^= 1; }
     if (++unit == units || u + 1 == u1) {
       if (from_start && unit == units) {
@@ -339,7 +419,7 @@ w4_wide_kernel(const W4Params p, const __grid_constant__ CUtensorMap codes, int 
   __shared__ int dead_flag;
   volatile int* dead = &dead_flag;
   constexpr int kChunks = 8 * kTiles * (kUnit / 8) / 256;       // 16-byte pieces of x per thread and stage
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, q = lane & 3;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, f = Lane<kGroup>::feature(lane);
   const int rank = blockIdx.x % split, n0 = blockIdx.x / split * kWideRows;
   const int units = (p.K + kUnit - 1) / kUnit, u0 = units * rank / split, u1 = units * (rank + 1) / split;
   const uint32_t base = (smem_u32(raw_smem) + 1023) & ~1023u, xs = base + kWideStages * kWideCodes, bar = smem_u32(bars);
@@ -350,20 +430,21 @@ w4_wide_kernel(const W4Params p, const __grid_constant__ CUtensorMap codes, int 
     mbar_arrive_tx(bar + 8 * stage, kWideCodes);
     tma_codes(base + stage * kWideCodes, &codes, bar + 8 * stage, u * (kUnit / 2), n0);
   };
+  // the thread's pieces of x: token t_x + 8 i, elements k_x .. k_x + 7 of the unit
+  const int t_x = threadIdx.x / (kUnit / 8), k_x = threadIdx.x % (kUnit / 8) * 8;
+  const T* x_src = static_cast<const T*>(p.x) + t_x * p.ldx + k_x;
+  const uint32_t x_dst = xs + t_x * kWidePitch + Lane<kGroup>::element(k_x);
   uint4 piece[kChunks];
   auto load_x = [&](int u) {
+    const bool in = u * kUnit + k_x < p.K;
 #pragma unroll
-    for (int i = 0; i < kChunks; ++i) {
-      const int at = threadIdx.x + 256 * i, t = at / (kUnit / 8), k = u * kUnit + at % (kUnit / 8) * 8;
-      piece[i] = t < p.M && k < p.K ? *reinterpret_cast<const uint4*>(static_cast<const T*>(p.x) + t * p.ldx + k) : make_uint4(0u, 0u, 0u, 0u);
-    }
+    for (int i = 0; i < kChunks; ++i)
+      piece[i] = in && t_x + 8 * i < p.M ? *reinterpret_cast<const uint4*>(x_src + u * kUnit + 8 * i * p.ldx) : make_uint4(0u, 0u, 0u, 0u);
   };
-  auto store_x = [&](int u) {
+  auto store_x = [&](int stage) {
 #pragma unroll
-    for (int i = 0; i < kChunks; ++i) {
-      const int at = threadIdx.x + 256 * i, t = at / (kUnit / 8);
-      if (t < p.M) sts_paired(xs + (u - u0) % kWideStages * x_bytes + t * kWidePitch + at % (kUnit / 8) * 16, piece[i]);
-    }
+    for (int i = 0; i < kChunks; ++i)
+      if (t_x + 8 * i < p.M) sts_paired(x_dst + stage * x_bytes + 8 * i * kWidePitch, piece[i]);
   };
   if (threadIdx.x == 0) {
     *dead = 0;
@@ -371,32 +452,41 @@ w4_wide_kernel(const W4Params p, const __grid_constant__ CUtensorMap codes, int 
     mbar_init_fence();
     for (int u = u0; u < u1 && u < u0 + kWideStages - 1; ++u) request(u);
   }
-  const int n = n0 + warp * 16 + g;
+  const int n = n0 + warp * 16 + f;
+  ScaleRows<T> rows;
+  rows.begin(p, n, p.K / kGroup);
   Scales<T, kGroup> now, next;
-  if (u0 < u1) now.load(p, n, u0);
-  if (u0 + 1 < u1) next.load(p, n, u0 + 1);
-  for (int u = u0; u < u1 && u < u0 + kWideStages - 1; ++u) {
-    load_x(u);
-    store_x(u);
+  if (u0 < u1) now.load(p, rows, u0);
+  for (int i = 0; i < kWideStages - 1 && u0 + i < u1; ++i) {
+    load_x(u0 + i);
+    store_x(i);
   }
   float acc[kTiles][4];
 #pragma unroll
   for (int t = 0; t < kTiles; ++t) acc[t][0] = acc[t][1] = acc[t][2] = acc[t][3] = 0.f;
-  const uint32_t code = base + (warp * 16 + g) * 128 + (g << 4) + 4 * q, x = xs + g * kWidePitch + 16 * q;
+  const uint32_t code = base + warp * 16 * 128 + Lane<kGroup>::code(lane);
+  uint32_t x[kTiles];
+#pragma unroll
+  for (int t = 0; t < kTiles; ++t) x[t] = xs + min(8 * t + (lane >> 2), p.M - 1) * kWidePitch + 16 * (lane & 3);
   __syncthreads();
+  int stage = 0, far_stage = kWideStages - 1;
+  uint32_t phase = 0;
   for (int u = u0; u < u1; ++u) {
-    const int stage = (u - u0) % kWideStages, far = u + kWideStages - 1;
+    const int far = u + kWideStages - 1;
     // the stage of unit `far` was read last in the iteration before, which every warp has left
     if (threadIdx.x == 0 && far < u1 && !*dead) request(far);
     if (far < u1) load_x(far);
-    Scales<T, kGroup> later;
-    if (u + 2 < u1) later.load(p, n, u + 2);
-    mbar_wait(bar + 8 * stage, (u - u0) / kWideStages & 1, p.spin_budget, p.status, dead);
+    if (u + 1 < u1) next.load(p, rows, u + 1);
+    mbar_wait(bar + 8 * stage, phase, p.spin_budget, p.status, dead);
     __syncwarp();
-    multiply<T, kGroup, kTiles>(code + stage * kWideCodes, x + stage * x_bytes, kWidePitch, g, p.M, now, acc);
-    if (far < u1) store_x(far);
+    uint32_t xu[kTiles];
+#pragma unroll
+    for (int t = 0; t < kTiles; ++t) xu[t] = x[t] + stage * x_bytes;
+    multiply<T, kGroup, kTiles>(code + stage * kWideCodes, xu, now, acc);
+    if (far < u1) store_x(far_stage);
     now = next;
-    next = later;
+    if (++stage == kWideStages) { stage = 0; phase ^= 1; }
+    if (++far_stage == kWideStages) far_stage = 0;
     __syncthreads();
   }
   if (*dead && threadIdx.x == 0)
@@ -454,8 +544,8 @@ cudaError_t launch_rows(const W4Params& p, int dev, cudaStream_t s) {
   if (e != cudaSuccess) return e;
   CUtensorMap map;
   if (!encode_codes(&map, p, 16)) return cudaErrorInvalidValue;
-  const int tiles = (p.N + 15) / 16, most = 2 * sm_count(dev);
   const int smem = 1024 + kRowWarps * kRowStages * kRowBytes + p.M * x_pitch(p.K);
+  const int tiles = (p.N + 15) / 16, most = 2 * sm_count(dev);
   w4_rows_kernel<T, kGroup><<<tiles < most ? tiles : most, 32 * kRowWarps, smem, s>>>(p, map, tiles);
   return cudaGetLastError();
 }
@@ -467,8 +557,10 @@ cudaError_t launch_wide(const W4Params& p, int dev, cudaStream_t s) {
   CUtensorMap map;
   if (!encode_codes(&map, p, kWideRows)) return cudaErrorInvalidValue;
   const int blocks = (p.N + kWideRows - 1) / kWideRows, units = (p.K + kUnit - 1) / kUnit;
-  int split = 1;
-  while (split < 8 && blocks * split < sm_count(dev) && units >= 4 * split) split *= 2;
+  // two blocks an SM, all resident at once
+  int split = 2 * sm_count(dev) / blocks;
+  split = split < 1 ? 1 : (split > 8 ? 8 : split);
+  if (split > units / 2) split = units < 2 ? 1 : units / 2;
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3((unsigned)(blocks * split));
   cfg.blockDim = dim3(256);
@@ -517,7 +609,7 @@ extern "C" mdw_status w4_linear(const mdw_w4_weights* w, int32_t M, const void* 
   const int dev = current_device(), sms = sm_count(dev);
   if (sms <= 0) return MDW_ERR_CUDA;
   // units of one block's share of the tiles stay far below 2^31
-  if ((int64_t)((w->n + 15) / 16 / sms + 1) * (w->k / kUnit + 1) > 1 << 28) return MDW_ERR_UNSUPPORTED_SHAPE;
+  if ((int64_t)((w->n + 15) / 16 / sms + 1) * (w->k / kRowUnit + 1) > 1 << 28) return MDW_ERR_UNSUPPORTED_SHAPE;
   const W4Params p{static_cast<const uint8_t*>(w->q), w->scale, static_cast<const uint8_t*>(w->zero), x, y, bias,
                    residual, ldx, ldy, ldr, status, mdw_spin_budget(), M, w->n, w->k, y_dtype == MDW_DT_F32};
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
