@@ -53,26 +53,52 @@ __device__ __forceinline__ int owner_of(const int32_t* start, int n, int v) {
 
 __global__ void __launch_bounds__(kPlanThreads) kv_plan_kernel(PlanParams p) {
   __shared__ int32_t start[MDW_MAX_REQUESTS + 1], first[MDW_MAX_REQUESTS + 1];
-  __shared__ int bad;
-  const int tid = threadIdx.x;
+  __shared__ int64_t sum_rows[kPlanThreads / 32], sum_pages[kPlanThreads / 32];
+  // Every block computes the whole prefix sums (a few kilobytes of lengths): no block waits for another.
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int64_t most = (int64_t)p.max_pages << p.page_shift;
   const int round = (1 << p.page_shift) - 1;
-  if (tid == 0) {
-    int64_t rows = 0, pages = 0;
-    int fail = 0;
-    for (int b = 0; b < p.B; ++b) {
-      const int64_t c = p.ctx_len[b], n = p.new_len[b];
-      if (c < 0 || n < 0 || c + n > most || ((p.parents || p.tree_mask) && n > MDW_MAX_TREE)) { fail = 1; break; }
-      start[b] = (int32_t)rows;
-      first[b] = (int32_t)pages;
-      rows += n;
-      pages += ((c + n + round) >> p.page_shift) - ((c + round) >> p.page_shift);
-      if (rows > p.T || pages > p.num_free) { fail = 1; break; }
+  const int per = (p.B + kPlanThreads - 1) / kPlanThreads, b0 = min(tid * per, p.B), b1 = min(b0 + per, p.B);
+  const int limit = p.parents || p.tree_mask ? MDW_MAX_TREE : 0x7fffffff;
+  int64_t rows = 0, pages = 0;
+  int fail = 0;
+  for (int b = b0; b < b1; ++b) {
+    const int64_t c = p.ctx_len[b], n = p.new_len[b];
+    if (c < 0 || n < 0 || c + n > most || n > limit) { fail = 1; break; }
+    start[b] = (int32_t)n;
+    first[b] = (int32_t)(((c + n + round) >> p.page_shift) - ((c + round) >> p.page_shift));
+    rows += n;
+    pages += first[b];
+  }
+  // inclusive sums over the warp's threads, then the warps before
+  int64_t rows_to = rows, pages_to = pages;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int64_t r = __shfl_up_sync(0xffffffffu, rows_to, o), g = __shfl_up_sync(0xffffffffu, pages_to, o);
+    if (lane >= o) { rows_to += r; pages_to += g; }
+  }
+  if (lane == 31) { sum_rows[warp] = rows_to; sum_pages[warp] = pages_to; }
+  fail = __syncthreads_or(fail);
+  int64_t all_rows = 0, all_pages = 0;
+#pragma unroll
+  for (int w = 0; w < kPlanThreads / 32; ++w) {
+    if (w < warp) { rows_to += sum_rows[w]; pages_to += sum_pages[w]; }
+    all_rows += sum_rows[w];
+    all_pages += sum_pages[w];
+  }
+  const bool bad = fail || all_rows > p.T || all_pages > p.num_free;
+  if (bad) {
+    if (tid == 0 && blockIdx.x == 0) raise_status(p.status, MDW_ERR_DEVICE_BOUNDS);
+  } else {
+    int32_t r = (int32_t)(rows_to - rows), g = (int32_t)(pages_to - pages);
+    for (int b = b0; b < b1; ++b) {
+      const int32_t n = start[b], f = first[b];
+      start[b] = r;
+      first[b] = g;
+      r += n;
+      g += f;
     }
-    start[p.B] = (int32_t)rows;
-    first[p.B] = (int32_t)pages;
-    bad = fail;
-    if (fail) raise_status(p.status, MDW_ERR_DEVICE_BOUNDS);
+    if (tid == 0) { start[p.B] = (int32_t)all_rows; first[p.B] = (int32_t)all_pages; }
   }
   __syncthreads();
   const int at = blockIdx.x * kPlanThreads + tid, step = gridDim.x * kPlanThreads;
@@ -137,43 +163,79 @@ struct WriteParams {
   const float* v_scale;
   const int64_t* slot_map;
   uint32_t* status;
-  int64_t items;
-  int chunks, dim_shift, page_shift;   // 16-byte pieces of one row's heads; log2 of pieces per head; of page size
+  int T, rows;                         // rows of the call, rows per block
+  int chunks, dim_shift, page_shift;   // 8-element pieces of a row; log2 of pieces per head; of page size
 };
 
-// One thread per 8 elements of one row's keys or values.
-template <typename T, bool kE4M3>
-__global__ void __launch_bounds__(256) kv_write_kernel(WriteParams p) {
-  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
-  if (i >= p.items) return;
-  const int chunk = (int)(i % p.chunks);
-  const int64_t row = i / p.chunks >> 1;
-  const bool is_v = (i / p.chunks) & 1;
-  const int64_t slot = p.slot_map[row];
-  if (slot < 0 || slot >= p.slots) {
-    if (slot != -1) raise_status(p.status, MDW_ERR_DEVICE_BOUNDS);
-    return;
-  }
-  const int head = chunk >> p.dim_shift, part = chunk & ((1 << p.dim_shift) - 1);
-  const int64_t in_page = slot & ((1 << p.page_shift) - 1);
-  const int64_t at = (slot >> p.page_shift) * p.page_stride +
-                     ((((int64_t)head << p.page_shift) + in_page) << (p.dim_shift + 3)) + 8 * part;
-  const T* src = static_cast<const T*>(is_v ? p.v : p.k) + row * (is_v ? p.ldv : p.ldk) + 8 * chunk;
-  const uint4 x = *reinterpret_cast<const uint4*>(src);
-  if constexpr (!kE4M3) {
-    *reinterpret_cast<uint4*>(static_cast<T*>(is_v ? p.vc : p.kc) + at) = x;
+__device__ __forceinline__ uint4 ld_once(const void* p) {
+  uint4 v;
+  asm volatile("ld.global.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p));
+  return v;
+}
+// Eight elements over their scale in E4M3: the code of the correctly rounded fp32 quotient, so that it depends
+// on nothing but x and scale. With y = RN(1 / s) and q = RN(x y), RN(q + (x - q s) y) is RN(x / s) (P. Markstein,
+// "Computation of elementary functions on the IBM RISC System/6000 processor", 1990) if the remainder
+// is exact and s has not the largest significand: scales of other magnitudes than 2^-64 .. 2^64 and that
+// significand are divided by, and quotients that saturate anyway are left as they are.
+template <typename T>
+__device__ __forceinline__ uint2 to_e4m3(uint4 x, float s) {
+  T e[8];
+  memcpy(e, &x, 16);
+  float v[8];
+  if (s >= 0x1p-64f && s <= 0x1p64f && (__float_as_uint(s) & 0x7fffffu) != 0x7fffffu) {
+    const float y = __frcp_rn(s);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const float f = Elem<T>::to_float(e[j]), q = __fmul_rn(f, y);
+      const float exact = __fmaf_rn(__fmaf_rn(-q, s, f), y, q);
+      v[j] = copysignf(fabsf(q) < 1024.f ? exact : q, f);          // -0 stays -0
+    }
   } else {
-    const float s = (is_v ? p.v_scale : p.k_scale)[head];
-    T e[8];
-    memcpy(e, &x, 16);
-    uint32_t out[2];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] = __fdiv_rn(Elem<T>::to_float(e[j]), s);
+  }
+  return make_uint2(f32x2_to_e4m3x2(v[0], v[1]) | f32x2_to_e4m3x2(v[2], v[3]) << 16,
+                    f32x2_to_e4m3x2(v[4], v[5]) | f32x2_to_e4m3x2(v[6], v[7]) << 16);
+}
+
+// A block takes `rows` rows; a thread moves 8 elements of the keys and of the values at a time, two such pairs in
+// flight. Neighbouring threads read and write neighbouring pieces; a head's row is the unit of the cache
+// that stays whole (64 to 256 bytes).
+template <typename T, bool kE4M3>
+__global__ void __launch_bounds__(256) kv_write_kernel(const WriteParams p) {
+  const int row0 = blockIdx.x * p.rows, pieces = min(p.rows, p.T - row0) * p.chunks;
+  for (int i = threadIdx.x; i < pieces; i += 512) {
+    uint4 k[2], v[2];
+    int64_t to[2];
+    int head[2];
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
-      const uint32_t lo = f32x2_to_e4m3x2(__fdiv_rn(Elem<T>::to_float(e[4 * j]), s), __fdiv_rn(Elem<T>::to_float(e[4 * j + 1]), s));
-      const uint32_t hi = f32x2_to_e4m3x2(__fdiv_rn(Elem<T>::to_float(e[4 * j + 2]), s), __fdiv_rn(Elem<T>::to_float(e[4 * j + 3]), s));
-      out[j] = lo | hi << 16;
+      const int at = i + 256 * j, r = at / p.chunks, chunk = at - r * p.chunks;
+      to[j] = -1;
+      if (at >= pieces) continue;
+      const int64_t slot = p.slot_map[row0 + r];
+      if (slot < 0 || slot >= p.slots) {
+        if (slot != -1) raise_status(p.status, MDW_ERR_DEVICE_BOUNDS);
+        continue;
+      }
+      k[j] = ld_once(static_cast<const T*>(p.k) + (row0 + r) * p.ldk + 8 * chunk);
+      v[j] = ld_once(static_cast<const T*>(p.v) + (row0 + r) * p.ldv + 8 * chunk);
+      head[j] = chunk >> p.dim_shift;
+      const int part = chunk & ((1 << p.dim_shift) - 1);
+      to[j] = (slot >> p.page_shift) * p.page_stride +
+              ((((int64_t)head[j] << p.page_shift) + (slot & ((1 << p.page_shift) - 1))) << (p.dim_shift + 3)) + 8 * part;
     }
-    *reinterpret_cast<uint2*>(static_cast<uint8_t*>(is_v ? p.vc : p.kc) + at) = make_uint2(out[0], out[1]);
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      if (to[j] < 0) continue;
+      if constexpr (!kE4M3) {
+        *reinterpret_cast<uint4*>(static_cast<T*>(p.kc) + to[j]) = k[j];
+        *reinterpret_cast<uint4*>(static_cast<T*>(p.vc) + to[j]) = v[j];
+      } else {
+        *reinterpret_cast<uint2*>(static_cast<uint8_t*>(p.kc) + to[j]) = to_e4m3<T>(k[j], p.k_scale[head[j]]);
+        *reinterpret_cast<uint2*>(static_cast<uint8_t*>(p.vc) + to[j]) = to_e4m3<T>(v[j], p.v_scale[head[j]]);
+      }
+    }
   }
 }
 
@@ -198,7 +260,9 @@ extern "C" mdw_status mdw_kv_plan(int32_t B, const int32_t* ctx_len, const int32
     return MDW_ERR_INVALID_ARG;
   PlanParams p{ctx_len, new_len, block_table, free_pages, parents, row_start, slot_map, positions, tree_mask,
                pages_taken, status, B, T, num_pages, max_pages, num_free, log2_of(page_size)};
-  const int blocks = (T + kPlanThreads - 1) / kPlanThreads;
+  const int dev = current_device(), most = 8 * sm_count(dev);
+  if (most <= 0) return MDW_ERR_CUDA;
+  const int wanted = (T + kPlanThreads - 1) / kPlanThreads, blocks = wanted < most ? wanted : most;
   kv_plan_kernel<<<blocks, kPlanThreads, 0, reinterpret_cast<cudaStream_t>(stream)>>>(p);
   return cudaGetLastError() == cudaSuccess ? MDW_OK : MDW_ERR_CUDA;
 }
@@ -215,19 +279,23 @@ extern "C" mdw_status mdw_kv_write(const mdw_kv_cache* cache, int32_t T, const v
   if (T < 1 || !aligned_to(k, 16) || !aligned_to(v, 16) || !row_stride_ok(ldk, width) || !row_stride_ok(ldv, width) ||
       !aligned_to(slot_map, 8) || !null_or_aligned(status, 4))
     return MDW_ERR_INVALID_ARG;
-  WriteParams p{k, v, ldk, ldv, cache->k, cache->v, cache->page_stride, (int64_t)cache->num_pages * cache->page_size,
-                cache->k_scale, cache->v_scale, slot_map, status, 0, (int)(width / 8), log2_of(cache->head_dim / 8),
-                log2_of(cache->page_size)};
-  p.items = (int64_t)T * 2 * p.chunks;
-  const int64_t blocks = (p.items + 255) / 256;
-  if (blocks > 0x7fffffffLL) return MDW_ERR_INVALID_ARG;
+  const int sms = sm_count(current_device());
+  if (sms <= 0) return MDW_ERR_CUDA;
+  // about 512 pieces a block (one round of its threads), fewer where that leaves SMs without a block
+  const int chunks = (int)(width / 8);
+  int rows = (512 + chunks - 1) / chunks;
+  if (T / rows < 4 * sms) rows = T / (4 * sms) < 1 ? 1 : T / (4 * sms);
+  const WriteParams p{k, v, ldk, ldv, cache->k, cache->v, cache->page_stride, (int64_t)cache->num_pages * cache->page_size,
+                      cache->k_scale, cache->v_scale, slot_map, status, T, rows, chunks, log2_of(cache->head_dim / 8),
+                      log2_of(cache->page_size)};
+  const unsigned blocks = (unsigned)((T + rows - 1) / rows);
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   if (dtype == MDW_DT_BF16) {
-    if (fp8) kv_write_kernel<__nv_bfloat16, true><<<(unsigned)blocks, 256, 0, s>>>(p);
-    else kv_write_kernel<__nv_bfloat16, false><<<(unsigned)blocks, 256, 0, s>>>(p);
+    if (fp8) kv_write_kernel<__nv_bfloat16, true><<<blocks, 256, 0, s>>>(p);
+    else kv_write_kernel<__nv_bfloat16, false><<<blocks, 256, 0, s>>>(p);
   } else {
-    if (fp8) kv_write_kernel<__half, true><<<(unsigned)blocks, 256, 0, s>>>(p);
-    else kv_write_kernel<__half, false><<<(unsigned)blocks, 256, 0, s>>>(p);
+    if (fp8) kv_write_kernel<__half, true><<<blocks, 256, 0, s>>>(p);
+    else kv_write_kernel<__half, false><<<blocks, 256, 0, s>>>(p);
   }
   return cudaGetLastError() == cudaSuccess ? MDW_OK : MDW_ERR_CUDA;
 }

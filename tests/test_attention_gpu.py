@@ -15,6 +15,7 @@ import torch
 
 from moe_decode_weight_gb300 import api
 from oracle import attention as OA
+from oracle import formats as OF
 
 pytestmark = pytest.mark.gpu
 BF, HF, F32, E4 = torch.bfloat16, torch.float16, torch.float32, torch.float8_e4m3fn
@@ -267,6 +268,30 @@ def test_kv_write(t, hkv, page, d, dtype, ctype):
                 if s >= 0:
                     want[s // page, :, s % page] = r
         assert np.array_equal(got, want)
+
+
+@pytest.mark.parametrize("dtype", [BF, HF])
+def test_kv_write_codes_of_every_element_at_many_scales(dtype):
+    """Every 16-bit element at scales of all magnitudes: the codes are those of the fp32 quotient, also where
+    it lies next to the middle of two codes, below E4M3's normal range or beyond its largest value."""
+    bits = torch.arange(1 << 16, dtype=torch.int32).to(torch.uint16).view(dtype)
+    x = bits[torch.isfinite(bits.float())]
+    x = torch.cat([x, x.new_zeros(-len(x) % 64)]).view(-1, 1, 64).cuda()
+    t = x.shape[0]
+    rng = np.random.default_rng(0)
+    scales = list(np.exp2(rng.uniform(-12, 12, 24))) + [1.0, 2.0 ** -9, 1.5, 1e-38, 3e38, 1e-45, 1 / 3, 0.99999994]
+    slots = torch.arange(t, device="cuda")
+    for s in scales:
+        shape = (t // 16 + 1, 1, 16, 64)
+        cache = api.KVCache(*(torch.zeros(shape, dtype=torch.uint8, device="cuda") for _ in range(2)),
+                            *(torch.full((1,), float(s), dtype=F32, device="cuda") for _ in range(2)))
+        api.mdw_kv_write(cache, x, -x, slots)
+        with np.errstate(over="ignore"):
+            q = x.float().cpu().numpy().reshape(t, 64) / np.float32(s)
+        for c, sign in ((cache.k, 1), (cache.v, -1)):
+            got = c.reshape(-1, 64)[:t].cpu().numpy()
+            want = OF.float_to_e4m3_rne_sat(np.clip(sign * q, -1e30, 1e30))
+            assert np.array_equal(got, want), (s, int((got != want).sum()))
 
 
 def test_kv_write_skips_slots_outside_the_cache():
