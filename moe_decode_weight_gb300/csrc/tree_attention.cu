@@ -12,11 +12,12 @@
 // per SM: ragged lengths balance, and only the first and last item of a share are partial. Their sums
 // go to the workspace and a second, dependent launch joins them.
 //
-// A block is one producer warp, which requests the pages of a tile by TMA (one box of 128 or 64 bytes per
-// key and head half, swizzled, so that ldmatrix reads it without bank conflicts) into a ring of
-// stages, and eight consumer warps, which share no barrier inside an item: each takes 16 rows and
-// a slice of the tile's keys (all 16-key slices of one row tile, or two or four row tiles with 32 or 64
-// keys each) and keeps its own maximum, sum and output in registers.
+// A block is eight warps, which share no barrier inside an item: each takes 16 rows and a slice of the
+// tile's keys (16 keys each of one row tile, or 32 or 64 of one of two or four row tiles) and keeps
+// its own maximum, sum and output in registers. The pages of a tile come by TMA (one box of 128 or 64
+// bytes per key and head half, swizzled, so that ldmatrix reads it without bank conflicts) into a
+// ring of stages that warp 0 keeps filled; a warp of its own for that would leave the others 168
+// registers, and they spill.
 #include <cuda.h>
 
 #include <algorithm>
@@ -32,8 +33,8 @@ namespace {
 
 constexpr int kTileKeys = 128;        // keys of a tile (one pipeline stage)
 constexpr int kTileRows = 64;         // rows of a row block
-constexpr int kConsumers = 8;         // consumer warps
-constexpr int kAttnThreads = 32 * (kConsumers + 1);
+constexpr int kConsumers = 8;         // warps, the first of which also requests the tiles
+constexpr int kAttnThreads = 32 * kConsumers;
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
 struct AttnParams {
@@ -50,12 +51,18 @@ struct AttnParams {
   uint32_t* status;
   long long spin_budget;
   float scale;
-  int B, T, Hq, Hkv, group, max_new, max_pages, num_pages, page_shift, row_blocks;
+  int B, T, Hq, Hkv, group, max_new, max_pages, num_pages, page_shift;
   // workspace
-  int64_t* total;          // [1] tiles of the whole call
-  int64_t* item_start;     // [B][Hkv][row_blocks] first tile of an item
+  int32_t* total;          // [2] tiles of the whole call, blocks with a share
+  struct Cut* cuts;        // [grid] the item that a block's share starts inside of
   float2* part_ml;         // [2 * grid][64] (c m, sum) of partial items
   float* part_o;           // [2 * grid][64][D] their unnormalised outputs
+};
+
+// An item that a share boundary cuts; rows = 0: the share starts with a whole item.
+struct Cut {
+  int row0, rows, first, h;        // request's first row, rows of the block (of rows x heads), its first one, kv head
+  int start, tiles;                // first tile of the item, its tiles
 };
 
 // ------------------------------------------------------------------ requests and shares
@@ -80,42 +87,70 @@ __device__ __forceinline__ Request load_request(const AttnParams& p, int b) {
   r.keys = (int)keys;
   return r;
 }
-__device__ __forceinline__ int64_t share_start(int64_t total, int c, int grid) { return total * c / grid; }
 
-// Blocks that have a share: none is empty, so every partial slot that a join reads was written.
-__device__ __forceinline__ int busy_blocks(int64_t total, int grid) { return total < grid ? (int)total : grid; }
+// Equal contiguous shares of `total` tiles: block c has tiles [start(c), start(c + 1)). No share is empty, so every
+// partial slot that a join reads was written.
+struct Shares {
+  int blocks, base, rest;
+  __device__ __forceinline__ Shares(int total, int grid) {
+    blocks = total < grid ? total : grid;
+    base = blocks > 0 ? total / blocks : 0;
+    rest = total - base * blocks;
+  }
+  __device__ __forceinline__ int start(int c) const { return c * base + min(c, rest); }
+  __device__ __forceinline__ int owner(int t) const {
+    const int wide = rest * (base + 1);
+    return t < wide ? t / (base + 1) : rest + (t - wide) / base;
+  }
+};
 
-// The walk of one warp over its block's share, tile by tile; every warp of a block sees the same.
+// The walk of one warp over its block's share, tile by tile; every warp of a block sees the same. A lane holds
+// one of 32 consecutive requests, so that the next one costs no load.
 struct Walk {
-  Request r;
+  Request mine, r;                 // the lane's request; the current item's
   int b, h, rb, tile, tiles;       // current item and tile, tiles of the item
-  int64_t left;                    // tiles left in the share
-  int64_t at;                      // global index of the current tile
+  int left;                        // tiles left in the share
 
+  __device__ __forceinline__ void take(int lane_) {
+    r.row0 = __shfl_sync(0xffffffffu, mine.row0, lane_);
+    r.rows = __shfl_sync(0xffffffffu, mine.rows, lane_);
+    r.ctx = __shfl_sync(0xffffffffu, mine.ctx, lane_);
+    r.keys = __shfl_sync(0xffffffffu, mine.keys, lane_);
+    tiles = r.tiles();
+  }
+  __device__ __forceinline__ void load32(const AttnParams& p, int first, int lane) {
+    mine.rows = 0;
+    if (first + lane < p.B) mine = load_request(p, first + lane);
+  }
   __device__ void begin(const AttnParams& p, int lane) {
+    left = 0;
     int64_t total = 0;
     for (int i = 0; i < p.B; i += 32) {
-      int64_t w = 0;
-      if (i + lane < p.B) {
-        const Request q = load_request(p, i + lane);
-        if (q.rows < 0 && blockIdx.x == 0) raise_status(p.status, MDW_ERR_DEVICE_BOUNDS);
-        w = q.work(p);
-      }
+      load32(p, i, lane);
+      if (mine.rows < 0 && blockIdx.x == 0) raise_status(p.status, MDW_ERR_DEVICE_BOUNDS);
+      int64_t w = mine.work(p);
+#pragma unroll
       for (int o = 16; o > 0; o >>= 1) w += __shfl_xor_sync(0xffffffffu, w, o);
       total += w;
     }
-    if (blockIdx.x == 0 && threadIdx.x == 0) *p.total = total;
-    const int blocks = busy_blocks(total, gridDim.x);
-    left = 0;
-    if ((int)blockIdx.x >= blocks) return;
-    at = share_start(total, blockIdx.x, blocks);
-    left = share_start(total, blockIdx.x + 1, blocks) - at;
-    int64_t before = 0;
+    const bool many = total > 0x7fffffff;       // beyond any real batch: nothing is computed
+    if (many && blockIdx.x == 0) raise_status(p.status, MDW_ERR_UNSUPPORTED_SHAPE);
+    const Shares shares(many ? 0 : (int)total, gridDim.x);
+    if (blockIdx.x == 0 && threadIdx.x == 0) {
+      p.total[0] = many ? 0 : (int)total;
+      p.total[1] = shares.blocks;
+    }
+    if ((int)blockIdx.x >= shares.blocks) return;
+    const int at = shares.start(blockIdx.x);
+    left = shares.start(blockIdx.x + 1) - at;
+    int before = 0;
     for (int i = 0; i < p.B; i += 32) {
-      const int64_t w = i + lane < p.B ? load_request(p, i + lane).work(p) : 0;
-      int64_t sum = w;
+      if (p.B > 32) load32(p, i, lane);
+      const int w = (int)mine.work(p);
+      int sum = w;
+#pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
-        const int64_t v = __shfl_up_sync(0xffffffffu, sum, o);
+        const int v = __shfl_up_sync(0xffffffffu, sum, o);
         if (lane >= o) sum += v;
       }
       const unsigned hit = __ballot_sync(0xffffffffu, before + sum > at);
@@ -123,32 +158,37 @@ struct Walk {
         const int l = __ffs(hit) - 1;
         before += __shfl_sync(0xffffffffu, sum - w, l);
         b = i + l;
+        take(l);
         break;
       }
       before += __shfl_sync(0xffffffffu, sum, 31);
     }
-    r = load_request(p, b);
-    tiles = r.tiles();
-    const int64_t in = at - before;
-    const int item = (int)(in / tiles);
-    tile = (int)(in - (int64_t)item * tiles);
+    const int in = at - before, item = in / tiles;
+    tile = in - item * tiles;
     h = item / r.blocks(p);
     rb = item - h * r.blocks(p);
+    if (threadIdx.x == 0) {
+      Cut cut{};
+      if (tile > 0) cut = Cut{r.row0, min(r.rows * p.group - rb * kTileRows, kTileRows), rb * kTileRows, h, at - tile, tiles};
+      p.cuts[blockIdx.x] = cut;
+    }
   }
-  __device__ __forceinline__ void next_item(const AttnParams& p) {
+  __device__ __forceinline__ void next_item(const AttnParams& p, int lane) {
     tile = 0;
     if (++rb == r.blocks(p)) {
       rb = 0;
       if (++h == p.Hkv) {
         h = 0;
-        do r = load_request(p, ++b); while (r.rows <= 0);
-        tiles = r.tiles();
+        do {
+          if ((++b & 31) == 0) load32(p, b, lane);
+          take(b & 31);
+        } while (r.rows <= 0);
       }
     }
   }
 };
 
-// ------------------------------------------------------------------ barriers, copies, matrix steps
+// ------------------------------------------------------------------ copies and matrix steps
 
 __device__ __forceinline__ void tma_load(uint32_t dst, const CUtensorMap* map, uint32_t bar, int x, int row, int head, int page) {
   asm volatile("cp.async.bulk.tensor.4d.shared::cta.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], [%6];"
@@ -350,41 +390,44 @@ __device__ __forceinline__ void attend(Rows<D>& w, uint32_t kt, uint32_t vt, int
   if constexpr (kTail) {
     if (__any_sync(0xffffffffu, odd != 0)) {
       // rare: some visible value is NaN or infinite; add such values key by key
+#pragma unroll 1
+      for (int k = 0; k < kKeys; ++k) {
+        const int in_tile = key0 + k, from = (lane & ~3) | (k >> 1 & 3);
+        float mine0 = 0.f, mine1 = 0.f;
 #pragma unroll
-      for (int j = 0; j < kKeys / 8; ++j)
-        for (int k = 0; k < 8; ++k) {
-          const int in_tile = key0 + 8 * j + k, from = (lane & ~3) | (k >> 1);
-          const float p0 = __shfl_sync(0xffffffffu, k & 1 ? s[j][1] : s[j][0], from);
-          const float p1 = __shfl_sync(0xffffffffu, k & 1 ? s[j][3] : s[j][2], from);
-          const bool on_page = !(bad_pages >> (in_tile >> page_shift) & 1);
-          const bool see0 = on_page && sees(w.bits[0], tile_key + in_tile, r.ctx);
-          const bool see1 = on_page && sees(w.bits[1], tile_key + in_tile, r.ctx);
-          if (tile_key + in_tile >= r.keys) continue;
+        for (int j = 0; j < kKeys / 8; ++j)
+          if (k >> 3 == j) {
+            mine0 = k & 1 ? s[j][1] : s[j][0];
+            mine1 = k & 1 ? s[j][3] : s[j][2];
+          }
+        const float p0 = __shfl_sync(0xffffffffu, mine0, from), p1 = __shfl_sync(0xffffffffu, mine1, from);
+        if (tile_key + in_tile >= r.keys || (bad_pages >> (in_tile >> page_shift) & 1)) continue;
+        const bool see0 = sees(w.bits[0], tile_key + in_tile, r.ctx), see1 = sees(w.bits[1], tile_key + in_tile, r.ctx);
 #pragma unroll
-          for (int n = 0; n < D / 8; ++n)
+        for (int n = 0; n < D / 8; ++n)
 #pragma unroll
-            for (int e = 0; e < 2; ++e) {
-              // the lane's output columns: 8 n + 2 q + e, or interleaved by fours over an E4M3 cache
-              const int d = kE4M3 ? 16 * (n >> 1) + 4 * q + 2 * e + (n & 1) : 8 * n + 2 * q + e;
-              const uint32_t at = S::piece(vt, in_tile, d * S::kBytes / 16) + (d * S::kBytes & 15);
-              float v;
-              if constexpr (kE4M3) {
-                uint32_t raw;
-                asm volatile("ld.shared.u8 %0, [%1];" : "=r"(raw) : "r"(at));
-                v = __half2float(__ushort_as_half((unsigned short)e4m3x2_to_f16x2(raw)));
-              } else {
-                unsigned short raw;
-                asm volatile("ld.shared.u16 %0, [%1];" : "=h"(raw) : "r"(at));
-                T t;
-                memcpy(&t, &raw, 2);
-                v = Elem<T>::to_float(t);
-              }
-              if (!isfinite(v)) {
-                if (see0) w.o[n][e] += p0 * v;
-                if (see1) w.o[n][2 + e] += p1 * v;
-              }
+          for (int e = 0; e < 2; ++e) {
+            // the lane's output columns: 8 n + 2 q + e, or interleaved by fours over an E4M3 cache
+            const int d = kE4M3 ? 16 * (n >> 1) + 4 * q + 2 * e + (n & 1) : 8 * n + 2 * q + e;
+            const uint32_t at = S::piece(vt, in_tile, d * S::kBytes / 16) + (d * S::kBytes & 15);
+            float v;
+            if constexpr (kE4M3) {
+              uint32_t raw;
+              asm volatile("ld.shared.u8 %0, [%1];" : "=r"(raw) : "r"(at));
+              v = __half2float(__ushort_as_half((unsigned short)e4m3x2_to_f16x2(raw)));
+            } else {
+              unsigned short raw;
+              asm volatile("ld.shared.u16 %0, [%1];" : "=h"(raw) : "r"(at));
+              T t;
+              memcpy(&t, &raw, 2);
+              v = Elem<T>::to_float(t);
             }
-        }
+            if (!isfinite(v)) {
+              if (see0) w.o[n][e] += p0 * v;
+              if (see1) w.o[n][2 + e] += p1 * v;
+            }
+          }
+      }
     }
   }
 }
@@ -418,50 +461,60 @@ tree_attention_kernel(const AttnParams p, const __grid_constant__ CUtensorMap km
   __syncthreads();
   if (walk.left == 0) return;
 
-  int stage = 0;
-  uint32_t phase = 0;
-  if (warp == kConsumers) {
-    // ---- producer: lane i serves the tile's i-th page
-    const int box_rows = min(1 << p.page_shift, kTileKeys), pages = kTileKeys / box_rows;
+  // Warp 0 requests the tiles, kStages ahead at first, then one for each that every warp has left: it
+  // asks for the stage of the tile before the one it has just done itself, so it seldom waits. Lane i
+  // serves a tile's i-th page; the page's number is loaded one tile ahead.
+  Walk ask = walk;
+  int asked = 0, ask_stage = 0;
+  uint32_t ask_phase = 0;
+  const int box_rows = min(1 << p.page_shift, kTileKeys), pages = kTileKeys / box_rows;
+  int page = -1;
+  bool wanted = false;
+  auto look = [&]() {
+    const int key = ask.tile * kTileKeys + lane * box_rows;
+    wanted = ask.left > 0 && lane < pages && key < ask.r.keys;
+    if (wanted) page = p.block_table[(size_t)ask.b * p.max_pages + (key >> p.page_shift)];
+  };
+  auto request = [&]() {
+    if (ask.left == 0) return;
+    if (asked >= S::kStages) mbar_wait(empty + 8 * ask_stage, ask_phase ^ 1, p.spin_budget, p.status, dead);
+    if (__any_sync(0xffffffffu, *dead)) return;
+    const bool ok = wanted && page >= 0 && page < p.num_pages;
+    const unsigned good = __ballot_sync(0xffffffffu, ok), bad = __ballot_sync(0xffffffffu, wanted && !ok);
+    const uint32_t bar = full + 8 * ask_stage, kt = stages + ask_stage * 2 * S::kTileBytes, vt = kt + S::kTileBytes;
     const uint32_t page_bytes = (uint32_t)box_rows * D * S::kBytes;
-    for (;;) {
-      const int key = walk.tile * kTileKeys + lane * box_rows;
-      const bool wanted = lane < pages && key < walk.r.keys;
-      const int id = wanted ? p.block_table[(size_t)walk.b * p.max_pages + (key >> p.page_shift)] : 0;
-      const bool ok = wanted && id >= 0 && id < p.num_pages;
-      const unsigned good = __ballot_sync(0xffffffffu, ok), bad = __ballot_sync(0xffffffffu, wanted && !ok);
-      mbar_wait(empty + 8 * stage, phase ^ 1, p.spin_budget, p.status, dead);
-      if (__any_sync(0xffffffffu, *dead)) break;
-      const uint32_t bar = full + 8 * stage, kt = stages + stage * 2 * S::kTileBytes, vt = kt + S::kTileBytes;
-      if (lane == 0) {
-        bad_pages[stage] = bad;
-        if (bad) raise_status(p.status, MDW_ERR_DEVICE_BOUNDS);
-        mbar_arrive_tx(bar, 2 * page_bytes * __popc(good));
-      }
-      __syncwarp();
-      if (ok) {
-        const int row = key & ((1 << p.page_shift) - 1);
-#pragma unroll
-        for (int i = 0; i < S::kHalves; ++i) {
-          const uint32_t off = i * (kTileKeys * S::kRowBytes) + lane * box_rows * S::kRowBytes;
-          tma_load(kt + off, &kmap, bar, i * (S::kRowBytes / S::kBytes), row, walk.h, id);
-        }
-#pragma unroll
-        for (int i = 0; i < S::kHalves; ++i) {
-          const uint32_t off = i * (kTileKeys * S::kRowBytes) + lane * box_rows * S::kRowBytes;
-          tma_load(vt + off, &vmap, bar, i * (S::kRowBytes / S::kBytes), row, walk.h, id);
-        }
-      }
-      if (++stage == S::kStages) { stage = 0; phase ^= 1; }
-      if (--walk.left == 0) break;
-      if (++walk.tile == walk.tiles) walk.next_item(p);
+    if (lane == 0) {
+      bad_pages[ask_stage] = bad;
+      if (bad) raise_status(p.status, MDW_ERR_DEVICE_BOUNDS);
+      mbar_arrive_tx(bar, 2 * page_bytes * __popc(good));
     }
-    if (__any_sync(0xffffffffu, *dead))
-      for (int i = 0; i < S::kStages; ++i) mbar_drain(full + 8 * i, i < stage ? phase : phase ^ 1);
-    return;
+    __syncwarp();
+    if (ok) {
+      const int row = (ask.tile * kTileKeys + lane * box_rows) & ((1 << p.page_shift) - 1);
+#pragma unroll
+      for (int i = 0; i < S::kHalves; ++i) {
+        const uint32_t off = i * (kTileKeys * S::kRowBytes) + lane * box_rows * S::kRowBytes;
+        tma_load(kt + off, &kmap, bar, i * (S::kRowBytes / S::kBytes), row, ask.h, page);
+      }
+#pragma unroll
+      for (int i = 0; i < S::kHalves; ++i) {
+        const uint32_t off = i * (kTileKeys * S::kRowBytes) + lane * box_rows * S::kRowBytes;
+        tma_load(vt + off, &vmap, bar, i * (S::kRowBytes / S::kBytes), row, ask.h, page);
+      }
+    }
+    ++asked;
+    if (++ask_stage == S::kStages) { ask_stage = 0; ask_phase ^= 1; }
+    if (--ask.left > 0 && ++ask.tile == ask.tiles) ask.next_item(p, lane);
+    look();
+  };
+  if (warp == 0) {
+    look();
+    for (int i = 0; i < S::kStages; ++i) request();
   }
 
-  // ---- consumers
+  int stage = 0;
+  uint32_t phase = 0;
+  bool behind = false;             // whether a tile has been done
   const int g = lane >> 2, q = lane & 3;
   while (walk.left > 0) {
     // one item: rows [first, first + rows) of the request, tiles [tile, tile + count)
@@ -469,9 +522,8 @@ tree_attention_kernel(const AttnParams p, const __grid_constant__ CUtensorMap km
     const int first = walk.rb * kTileRows, rows = min(r.rows * p.group - first, kTileRows);
     const int row_warps = rows <= 16 ? 1 : (rows <= 32 ? 2 : 4), slices = kConsumers / row_warps;
     const int wr = warp % row_warps, slice = warp / row_warps, h = walk.h;
-    const int tile0 = walk.tile, count = (int)min((int64_t)(walk.tiles - tile0), walk.left);
+    const int tile0 = walk.tile, count = min(walk.tiles - tile0, walk.left);
     const bool whole = count == walk.tiles;
-    if (tile0 == 0 && threadIdx.x == 0) p.item_start[((size_t)walk.b * p.Hkv + h) * p.row_blocks + walk.rb] = walk.at;
 
     Rows<D> w;
     const bool live = wr * 16 < rows;
@@ -535,22 +587,21 @@ tree_attention_kernel(const AttnParams p, const __grid_constant__ CUtensorMap km
         const uint32_t kt = stages + stage * 2 * S::kTileBytes, vt = kt + S::kTileBytes, bad = bad_pages[stage];
         const int tile_key = (tile0 + i) * kTileKeys;
         const bool all = tile_key + kTileKeys <= r.ctx && bad == 0;
-        if (row_warps == 1) {
-          if (all) attend<T, kE4M3, D, 16, false>(w, kt, vt, slice * 16, tile_key, r, bad, p.page_shift, lane);
-          else attend<T, kE4M3, D, 16, true>(w, kt, vt, slice * 16, tile_key, r, bad, p.page_shift, lane);
-        } else if (row_warps == 2) {
-          if (all) attend<T, kE4M3, D, 32, false>(w, kt, vt, slice * 32, tile_key, r, bad, p.page_shift, lane);
-          else
-            for (int k = 0; k < 32; k += 16) attend<T, kE4M3, D, 16, true>(w, kt, vt, slice * 32 + k, tile_key, r, bad, p.page_shift, lane);
-        } else {
-          if (all) attend<T, kE4M3, D, 64, false>(w, kt, vt, slice * 64, tile_key, r, bad, p.page_shift, lane);
-          else
-            for (int k = 0; k < 64; k += 16) attend<T, kE4M3, D, 16, true>(w, kt, vt, slice * 64 + k, tile_key, r, bad, p.page_shift, lane);
-        }
+        const int keys = 16 * row_warps, key0 = slice * keys;
+        if (!all)
+          for (int k = 0; k < keys; k += 16) attend<T, kE4M3, D, 16, true>(w, kt, vt, key0 + k, tile_key, r, bad, p.page_shift, lane);
+        else if (row_warps == 1)
+          attend<T, kE4M3, D, 16, false>(w, kt, vt, key0, tile_key, r, bad, p.page_shift, lane);
+        else
+          for (int k = 0; k < keys; k += 32) attend<T, kE4M3, D, 32, false>(w, kt, vt, key0 + k, tile_key, r, bad, p.page_shift, lane);
       }
       __syncwarp();
       if (lane == 0) mbar_arrive(empty + 8 * stage);
       if (++stage == S::kStages) { stage = 0; phase ^= 1; }
+      if (warp == 0) {
+        if (behind) request();
+        behind = true;
+      }
     }
 
     // join the slices of each row tile: halves, in a fixed order
@@ -636,48 +687,70 @@ tree_attention_kernel(const AttnParams p, const __grid_constant__ CUtensorMap km
       }
     }
     walk.left -= count;
-    walk.at += count;
-    if (walk.left > 0) walk.next_item(p);
+    if (walk.left > 0) walk.next_item(p, lane);
   }
+  if (warp == 0 && __any_sync(0xffffffffu, *dead))
+    for (int i = 0; i < S::kStages && i < asked; ++i) mbar_drain(full + 8 * i, ((asked - i + S::kStages - 1) / S::kStages - 1) & 1);
 }
 
-// Joins the partial items: one warp per row, a lane D / 32 columns, blocks in order.
+// Joins the partial items: block x belongs to the boundary before share x + 1, and works if it is the first one
+// inside its item. One warp per row, a lane D / 32 columns, the shares' sums in order.
 template <typename T, int D>
-__global__ void __launch_bounds__(128) join_kernel(const AttnParams p, int blocks) {
+__global__ void __launch_bounds__(128) join_kernel(const AttnParams p) {
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  const int rb = blockIdx.x % p.row_blocks, bh = blockIdx.x / p.row_blocks, b = bh / p.Hkv, h = bh - b * p.Hkv;
-  const int row = blockIdx.y * 4 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
-  const Request r = load_request(p, b);
-  const int flat = rb * kTileRows + row;
-  if (r.rows <= 0 || flat >= r.rows * p.group) return;
-  const int64_t total = *p.total, first = p.item_start[blockIdx.x], last = first + r.tiles() - 1;
-  const int grid = busy_blocks(total, blocks);
-  // block c owns tiles [total c / grid, total (c + 1) / grid)
-  const int c0 = (int)(((first + 1) * grid - 1) / total), c1 = (int)(((last + 1) * grid - 1) / total);
-  if (c0 == c1) return;
   constexpr int kPer = D / 32;
-  float o[kPer], l = 0.f, mc = -INFINITY;
-  for (int i = 0; i < kPer; ++i) o[i] = 0.f;
-  for (int c = c0; c <= c1; ++c)
-    mc = fmaxf(mc, p.part_ml[(size_t)(2 * c + (share_start(total, c, grid) > first ? 0 : 1)) * kTileRows + row].x);
+  const int row = blockIdx.y * 4 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
+  const int total = p.total[0], blocks = p.total[1];
+  if ((int)blockIdx.x + 1 >= blocks) return;
+  const Cut cut = p.cuts[blockIdx.x + 1];
+  if (row >= cut.rows) return;
+  const Shares shares(total, blocks);
+  if (shares.start(blockIdx.x) > cut.start) return;             // an earlier boundary is inside too
+  const int c0 = blockIdx.x, parts = shares.owner(cut.start + cut.tiles - 1) - c0 + 1;
+  // the item's first part is the last of its block's share, the others are the first of theirs
+  auto slot = [&](int i) { return (size_t)(2 * (c0 + i) + (i == 0 ? 1 : 0)) * kTileRows + row; };
+  float mc = -INFINITY;
+  for (int i = lane; i < parts; i += 32) mc = fmaxf(mc, p.part_ml[slot(i)].x);
+  mc = warp_max(mc);
   const float base = mc == -INFINITY ? 0.f : mc;
-#pragma unroll 4
-  for (int c = c0; c <= c1; ++c) {
-    const size_t at = (size_t)(2 * c + (share_start(total, c, grid) > first ? 0 : 1)) * kTileRows + row;
-    const float2 ml = p.part_ml[at];
-    const float f = exp2_fast(ml.x - base);
-    l = fmaf(ml.y, f, l);
-    const float* src = p.part_o + at * D + lane * kPer;
-    float v[kPer];
-    if constexpr (kPer == 4) *reinterpret_cast<float4*>(v) = *reinterpret_cast<const float4*>(src);
-    else *reinterpret_cast<float2*>(v) = *reinterpret_cast<const float2*>(src);
-    for (int i = 0; i < kPer; ++i) o[i] = fmaf(v[i], f, o[i]);
+  float o[kPer], l = 0.f;
+#pragma unroll
+  for (int j = 0; j < kPer; ++j) o[j] = 0.f;
+  for (int i0 = 0; i0 < parts; i0 += 32) {
+    float f = 0.f;
+    if (i0 + lane < parts) {
+      const float2 ml = p.part_ml[slot(i0 + lane)];
+      f = exp2_fast(ml.x - base);
+      l = fmaf(ml.y, f, l);
+    }
+    const int n = min(parts - i0, 32);
+    for (int i = 0; i < n; i += 8) {
+      float v[8][kPer];
+#pragma unroll
+      for (int u = 0; u < 8; ++u) {
+        const float* src = p.part_o + slot(i0 + min(i + u, n - 1)) * D + lane * kPer;
+        if constexpr (kPer == 4) *reinterpret_cast<float4*>(v[u]) = *reinterpret_cast<const float4*>(src);
+        else *reinterpret_cast<float2*>(v[u]) = *reinterpret_cast<const float2*>(src);
+      }
+#pragma unroll
+      for (int u = 0; u < 8; ++u) {
+        const float g = __shfl_sync(0xffffffffu, f, min(i + u, 31));
+        if (i + u < n)
+#pragma unroll
+          for (int j = 0; j < kPer; ++j) o[j] = fmaf(v[u][j], g, o[j]);
+      }
+    }
   }
-  const int node = flat / p.group, head = h * p.group + flat - node * p.group;
-  const float f = l == 0.f ? 0.f : (p.v_scale ? p.v_scale[h] : 1.f) / l;
-  T* dst = static_cast<T*>(p.out) + (int64_t)(r.row0 + node) * p.ldo + (int64_t)head * D + lane * kPer;
-  for (int i = 0; i < kPer; ++i) dst[i] = Elem<T>::from_float(l == 0.f ? 0.f : o[i] * f);
-  if (p.lse && lane == 0) p.lse[(int64_t)(r.row0 + node) * p.Hq + head] = l == 0.f ? -INFINITY : (mc + log2f(l)) * kLn2;
+  l = warp_sum(l);
+  const int flat = cut.first + row, node = flat / p.group, head = cut.h * p.group + flat - node * p.group;
+  const float f = l == 0.f ? 0.f : (p.v_scale ? p.v_scale[cut.h] : 1.f) / l;
+  T* dst = static_cast<T*>(p.out) + (int64_t)(cut.row0 + node) * p.ldo + (int64_t)head * D + lane * kPer;
+  uint32_t packed[kPer / 2];
+#pragma unroll
+  for (int j = 0; j < kPer; j += 2) packed[j / 2] = l == 0.f ? 0u : Mma<T>::pack(o[j] * f, o[j + 1] * f);
+  if constexpr (kPer == 4) *reinterpret_cast<uint2*>(dst) = make_uint2(packed[0], packed[1]);
+  else *reinterpret_cast<uint32_t*>(dst) = packed[0];
+  if (p.lse && lane == 0) p.lse[(int64_t)(cut.row0 + node) * p.Hq + head] = l == 0.f ? -INFINITY : (mc + log2f(l)) * kLn2;
 }
 
 // ------------------------------------------------------------------ host
@@ -698,18 +771,17 @@ bool encode_cache(CUtensorMap* map, const mdw_kv_cache* c, void* data) {
 }
 
 struct AttnWs {
-  size_t item_start, ml, o, total;
+  size_t cuts, ml, o, total;
 };
-AttnWs attn_ws(int64_t items, int grid, int D) {
+AttnWs attn_ws(int grid, int D) {
   AttnWs w;
   auto up = [](size_t v) { return (v + 255) / 256 * 256; };
-  w.item_start = 256;
-  w.ml = w.item_start + up((size_t)items * 8);
+  w.cuts = 256;
+  w.ml = w.cuts + up((size_t)grid * sizeof(Cut));
   w.o = w.ml + up((size_t)grid * 2 * kTileRows * 8);
   w.total = w.o + up((size_t)grid * 2 * kTileRows * D * 4);
   return w;
 }
-int row_blocks_of(int32_t max_new, int group) { return (max_new * group + kTileRows - 1) / kTileRows; }
 
 template <typename T, bool kE4M3, int D>
 cudaError_t launch(const AttnParams& p, const CUtensorMap& km, const CUtensorMap& vm, int grid, int dev, cudaStream_t s) {
@@ -719,8 +791,9 @@ cudaError_t launch(const AttnParams& p, const CUtensorMap& km, const CUtensorMap
   tree_attention_kernel<T, kE4M3, D><<<grid, kAttnThreads, S::kSmem, s>>>(p, km, vm);
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
+  if (grid == 1) return cudaSuccess;
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3((unsigned)(p.B * p.Hkv * p.row_blocks), (unsigned)((std::min(p.max_new * p.group, kTileRows) + 3) / 4));
+  cfg.gridDim = dim3((unsigned)(grid - 1), (unsigned)((std::min(p.max_new * p.group, kTileRows) + 3) / 4));
   cfg.blockDim = dim3(128);
   cfg.stream = s;
   cudaLaunchAttribute a{};
@@ -728,7 +801,7 @@ cudaError_t launch(const AttnParams& p, const CUtensorMap& km, const CUtensorMap
   a.val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = &a;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, join_kernel<T, D>, p, grid);
+  return cudaLaunchKernelEx(&cfg, join_kernel<T, D>, p);
 }
 template <typename T, bool kE4M3>
 cudaError_t launch(const AttnParams& p, int D, const CUtensorMap& km, const CUtensorMap& vm, int grid, int dev, cudaStream_t s) {
@@ -750,8 +823,7 @@ extern "C" size_t mdw_tree_attention_workspace_bytes(const mdw_kv_cache* cache, 
   if (check_kv_cache(cache) != MDW_OK || !sizes_ok(cache, B, T, q_heads, max_new)) return 0;
   const int grid = sm_count(current_device());
   if (grid <= 0) return 0;
-  const int64_t items = (int64_t)B * cache->kv_heads * row_blocks_of(max_new, q_heads / cache->kv_heads);
-  return attn_ws(items, grid, cache->head_dim).total;
+  return attn_ws(grid, cache->head_dim).total;
 }
 
 extern "C" mdw_status mdw_tree_attention(const mdw_kv_cache* cache, int32_t B, int32_t T, int32_t q_heads,
@@ -773,18 +845,16 @@ extern "C" mdw_status mdw_tree_attention(const mdw_kv_cache* cache, int32_t B, i
       !aligned_to(row_start, 4) || !null_or_aligned(tree_mask, 8) || !null_or_aligned(status, 4) || !aligned_to(ws, 16))
     return MDW_ERR_INVALID_ARG;
   if (!(scale > 0.f) || !std::isfinite(scale)) return MDW_ERR_INVALID_ARG;
-  const int dev = current_device(), grid = sm_count(dev), group = q_heads / cache->kv_heads, row_blocks = row_blocks_of(max_new, group);
-  const int64_t items = (int64_t)B * cache->kv_heads * row_blocks;
-  if (items > 0x7fffffffLL) return MDW_ERR_UNSUPPORTED_SHAPE;
-  const AttnWs lay = attn_ws(items, std::max(grid, 1), cache->head_dim);
+  const int dev = current_device(), grid = sm_count(dev);
+  const AttnWs lay = attn_ws(std::max(grid, 1), cache->head_dim);
   if (ws_bytes < lay.total) return MDW_ERR_WORKSPACE_TOO_SMALL;
   if (grid <= 0) return MDW_ERR_CUDA;
   uint8_t* base = static_cast<uint8_t*>(ws);
-  AttnParams p{cache->k_scale, cache->v_scale, q, out, lse, ldq, ldo, block_table, ctx_len, row_start, tree_mask, status,
-               mdw_spin_budget(), scale, B, T, q_heads, cache->kv_heads, group, max_new, max_pages, cache->num_pages,
-               log2_of(cache->page_size), row_blocks, reinterpret_cast<int64_t*>(base),
-               reinterpret_cast<int64_t*>(base + lay.item_start), reinterpret_cast<float2*>(base + lay.ml),
-               reinterpret_cast<float*>(base + lay.o)};
+  const AttnParams p{cache->k_scale, cache->v_scale, q, out, lse, ldq, ldo, block_table, ctx_len, row_start, tree_mask, status,
+                     mdw_spin_budget(), scale, B, T, q_heads, cache->kv_heads, q_heads / cache->kv_heads, max_new, max_pages,
+                     cache->num_pages, log2_of(cache->page_size), reinterpret_cast<int32_t*>(base),
+                     reinterpret_cast<Cut*>(base + lay.cuts), reinterpret_cast<float2*>(base + lay.ml),
+                     reinterpret_cast<float*>(base + lay.o)};
   CUtensorMap km, vm;
   if (!encode_cache(&km, cache, cache->k) || !encode_cache(&vm, cache, cache->v)) return MDW_ERR_CUDA;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
