@@ -7,17 +7,21 @@
 // split over warps and blocks and joined in a fixed order.
 //
 // Split. The query heads of one kv head and the nodes of one tree are the rows of one tile (node major,
-// up to 64 rows), so a key is read from memory once for all of them. The work is the list of
+// up to 128 rows), so a key is read from memory once for all of them. The work is the list of
 // (request, kv head, row block, 128-key tile), cut into equal contiguous shares, one per block, one block
 // per SM: ragged lengths balance, and only the first and last item of a share are partial. Their sums
 // go to the workspace and a second, dependent launch joins them.
 //
-// A block is eight warps, which share no barrier inside an item: each takes 16 rows and a slice of the
-// tile's keys (16 keys each of one row tile, or 32 or 64 of one of two or four row tiles) and keeps
-// its own maximum, sum and output in registers. The pages of a tile come by TMA (one box of 128 or 64
-// bytes per key and head half, swizzled, so that ldmatrix reads it without bank conflicts) into a
-// ring of stages that warp 0 keeps filled; a warp of its own for that would leave the others 168
-// registers, and they spill.
+// Both products run on tcgen05 with the rows as the 128 lanes of tensor memory (fewer rows cost the tensor
+// cores nothing that the memory stream would not hide): scores = rows x keys into 128 columns, then
+// probabilities x values onto D columns of output, the probabilities read from tensor memory. The
+// tiles of an item alternate between two streams with scores, output, maximum and sum of their own, so
+// that one stream's exponentials run while the tensor cores work for the other. The roles of a block:
+//   warp 0       requests the tiles by TMA (a box per page, head and 128 bytes of a row, swizzled)
+//   warp 1       issues the matrix products
+//   warps 2, 3   (and 12, 13 over an E4M3 cache) keep non-finite values that not every row sees out of the
+//                products, and turn E4M3 tiles into f16 ones, exactly
+//   warps 4-7    exponentials of the even tiles, one thread per row; warps 8-11 of the odd tiles
 #include <cuda.h>
 
 #include <algorithm>
@@ -32,12 +36,12 @@ namespace mdw {
 namespace {
 
 constexpr int kTileKeys = 128;        // keys of a tile (one pipeline stage)
-constexpr int kTileRows = 64;         // rows of a row block
-constexpr int kConsumers = 8;         // warps, the first of which also requests the tiles
-constexpr int kAttnThreads = 32 * kConsumers;
+constexpr int kTileRows = 128;        // rows of a row block
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
 struct AttnParams {
+  const void* v;             // the cache's values and page stride, for keys read on their own
+  int64_t page_stride;
   const float* k_scale;
   const float* v_scale;
   const void* q;
@@ -55,8 +59,8 @@ struct AttnParams {
   // workspace
   int32_t* total;          // [2] tiles of the whole call, blocks with a share
   struct Cut* cuts;        // [grid] the item that a block's share starts inside of
-  float2* part_ml;         // [2 * grid][64] (c m, sum) of partial items
-  float* part_o;           // [2 * grid][64][D] their unnormalised outputs
+  float2* part_ml;         // [2 * grid][128] (c m, sum) of partial items
+  float* part_o;           // [2 * grid][128][D] their unnormalised outputs
 };
 
 // An item that a share boundary cuts; rows = 0: the share starts with a whole item.
@@ -194,13 +198,64 @@ __device__ __forceinline__ void tma_load(uint32_t dst, const CUtensorMap* map, u
   asm volatile("cp.async.bulk.tensor.4d.shared::cta.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], [%6];"
                :: "r"(dst), "l"(map), "r"(x), "r"(row), "r"(head), "r"(page), "r"(bar) : "memory");
 }
-__device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t addr) {
-  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
-               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
+// ---- tensor memory and tcgen05 (one issuing thread; a column is 32 bits of each of 128 lanes)
+__device__ __forceinline__ void tc_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void tc_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
+// Arrives on the barrier when every product issued before is complete.
+__device__ __forceinline__ void tc_commit(uint32_t bar) {
+  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" :: "r"(bar) : "memory");
 }
-__device__ __forceinline__ void ldsm4_t(uint32_t (&r)[4], uint32_t addr) {
-  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
-               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
+__device__ __forceinline__ void tc_mma(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool add) {
+  asm volatile("{ .reg .pred p; setp.ne.b32 p, %4, 0; tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p; }"
+               :: "r"(d), "l"(a), "l"(b), "r"(idesc), "r"((uint32_t)add) : "memory");
+}
+__device__ __forceinline__ void tc_mma_tmem(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc) {
+  asm volatile("{ .reg .pred p; setp.ne.b32 p, 1, 0; tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p; }"
+               :: "r"(d), "r"(a), "l"(b), "r"(idesc) : "memory");
+}
+// Shared-memory operand, 128-byte swizzle: address and offsets in units of 16 bytes. K-major: `stride` between
+// groups of 8 rows. MN-major: `lead` between blocks of 64 columns, `stride` between groups of 8 k.
+__device__ __forceinline__ uint64_t smem_operand(uint32_t addr, uint32_t lead, uint32_t stride) {
+  return (uint64_t)((addr & 0x3ffff) >> 4) | (uint64_t)(lead >> 4) << 16 | (uint64_t)(stride >> 4) << 32 | 1ull << 46 | 2ull << 61;
+}
+// 128 x n, fp32 result, 16-bit operands of one type, b MN-major or K-major.
+__host__ __device__ constexpr uint32_t mma_shape(bool bf16, bool b_mn_major, int n) {
+  return 1u << 4 | (bf16 ? 1u : 0u) << 7 | (bf16 ? 1u : 0u) << 10 | (b_mn_major ? 1u : 0u) << 16 | (uint32_t)(n / 8) << 17 | (128u / 16) << 24;
+}
+__device__ __forceinline__ void tc_ld32(float (&v)[32], uint32_t addr) {
+  uint32_t* r = reinterpret_cast<uint32_t*>(v);
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+               "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]),
+                 "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]),
+                 "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]),
+                 "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31]) : "r"(addr));
+  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void tc_st32(uint32_t addr, const float (&v)[32]) {
+  const uint32_t* r = reinterpret_cast<const uint32_t*>(v);
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,"
+               "%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};"
+               :: "r"(addr), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+                 "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19]),
+                 "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]), "r"(r[29]),
+                 "r"(r[30]), "r"(r[31]) : "memory");
+}
+__device__ __forceinline__ void tc_st16(uint32_t addr, const uint32_t (&r)[16]) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};"
+               :: "r"(addr), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+                 "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]) : "memory");
+}
+__device__ __forceinline__ void tc_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+// Generic writes to shared memory before, reads by the tensor cores after.
+__device__ __forceinline__ void fence_async_proxy() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
+__device__ __forceinline__ uint4 lds16(uint32_t a) {
+  uint4 v;
+  asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a) : "memory");
+  return v;
+}
+__device__ __forceinline__ void sts16(uint32_t a, uint4 v) {
+  asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" :: "r"(a), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
 }
 __device__ __forceinline__ float exp2_fast(float x) {
   float y;
@@ -213,10 +268,7 @@ template <typename T> struct Mma;
 template <> struct Mma<__nv_bfloat16> {
   static constexpr uint32_t kExponent = 0x7F807F80u;
   static constexpr float kShift = 0.f;
-  static __device__ __forceinline__ void step(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
-                 : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3]) : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
-  }
+  static constexpr bool kBf16 = true;
   static __device__ __forceinline__ uint32_t pack(float lo, float hi) {
     uint32_t r;
     asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
@@ -225,18 +277,19 @@ template <> struct Mma<__nv_bfloat16> {
 };
 template <> struct Mma<__half> {
   static constexpr uint32_t kExponent = 0x7C007C00u;
-  // f16 probabilities are kept times 2^15, so that those below 2^-14 of the largest do not lose bits
-  static constexpr float kShift = 15.f;
-  static __device__ __forceinline__ void step(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
-                 : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3]) : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
-  }
+  // f16 probabilities are kept times 2^7, so that those below 2^-14 of the largest do not lose bits, and
+  // 2^8 more (kSlack) do not overflow
+  static constexpr float kShift = 7.f;
+  static constexpr bool kBf16 = false;
   static __device__ __forceinline__ uint32_t pack(float lo, float hi) {
     uint32_t r;
     asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
     return r;
   }
 };
+// The base of a row's exponents follows its maximum only when that has grown by more than this (log2): any
+// base gives the same result, and a new one costs a pass over the output in tensor memory.
+constexpr float kSlack = 8.f;
 
 // ------------------------------------------------------------------ the kernel
 
@@ -244,453 +297,529 @@ template <typename T, bool kE4M3, int D>
 struct Shape {
   using C = typename std::conditional<kE4M3, __half, T>::type;     // type of the products
   static constexpr int kBytes = kE4M3 ? 1 : 2;
-  static constexpr int kRowBytes = D * kBytes < 128 ? D * kBytes : 128;   // one key's row in shared memory
-  static constexpr int kHalves = D * kBytes / kRowBytes;                  // rows of a key (128-byte boxes)
-  static constexpr int kTileBytes = kTileKeys * D * kBytes;
-  static constexpr int kStages = kTileBytes == 32768 ? 3 : (kTileBytes == 16384 ? 5 : 8);
-  static constexpr int kMergeBytes = 4 * 16 * D * 4;                      // four warps' outputs
-  static constexpr int kSmem = 1024 + kStages * 2 * kTileBytes + kMergeBytes + 4 * 16 * 8 + 256;
-  // Address of the 16-byte piece `piece` of a key's row in its tile, as the TMA swizzle places it.
-  static __device__ __forceinline__ uint32_t piece(uint32_t tile, int key, int piece_) {
-    if constexpr (kRowBytes == 128)
-      return tile + (piece_ >> 3) * (kTileKeys * 128) + key * 128 + (((piece_ & 7) ^ (key & 7)) << 4);
-    else
-      return tile + key * 64 + ((piece_ ^ ((key >> 1) & 3)) << 4);
+  static constexpr int kRowBytes = D * kBytes < 128 ? D * kBytes : 128;   // one key's row in a copied tile
+  static constexpr int kHalves = D * kBytes / kRowBytes;                  // boxes of a page (128 bytes of each key)
+  static constexpr int kCopied = kTileKeys * D * kBytes;                  // a copied tile of keys or of values
+  static constexpr int kOperand = kTileKeys * D * 2;                      // a 16-bit one
+  static constexpr int kStages = kE4M3 ? (D == 128 ? 2 : 4) : (D == 128 ? 3 : 5);
+  static constexpr int kBuffers = kE4M3 ? 2 : 0;                          // converted tiles
+  static constexpr int kHelpers = kE4M3 ? 4 : 2;                          // warps 2, 3 (and 12, 13)
+  static constexpr int kThreads = 32 * (kE4M3 ? 14 : 12);
+  static constexpr int kRowsAt = 0, kStagesAt = kTileRows * D * 2, kBuffersAt = kStagesAt + kStages * 2 * kCopied;
+  static constexpr int kSmall = kBuffersAt + kBuffers * 2 * kOperand;     // barriers and small arrays
+  static constexpr int kSmem = kSmall + 2 * kTileRows * 8 + kTileRows * 4 + 512;
+  // tensor memory columns of a stream: scores (the probabilities take their first half when D = 128), output
+  static constexpr int kOut = 128, kProb = D == 128 ? 0 : 192, kStream = 256;
+
+  // 16-byte piece of a key's row in a copied tile, as the TMA swizzle places it.
+  static __device__ __forceinline__ uint32_t copied(uint32_t tile, int key, int piece) {
+    if constexpr (kRowBytes == 128) return tile + (piece >> 3) * (kTileKeys * 128) + key * 128 + (((piece & 7) ^ (key & 7)) << 4);
+    else return tile + key * 64 + ((piece ^ ((key >> 1) & 3)) << 4);
+  }
+  // The same in a 16-bit operand of 128 rows.
+  static __device__ __forceinline__ uint32_t operand(uint32_t tile, int row, int piece) {
+    return tile + (piece >> 3) * (128 * 128) + row * 128 + (((piece & 7) ^ (row & 7)) << 4);
   }
 };
 
-// One warp's state over an item: 16 rows, of which a lane (g, q) holds rows g and g + 8.
-template <int D>
-struct Rows {
-  uint32_t q[D / 16][4];
-  float o[D / 8][4];
-  float mc[2], l[2], c[2];         // c m, sum, c of the two rows
-  uint64_t bits[2];                // nodes they see
+// Barriers and small arrays of a block.
+struct Small {
+  uint32_t full, empty, clean;     // per stage: copied; free again; values fit for the product (or converted, per buffer)
+  uint32_t buffer_free;            // per buffer: the products with a converted tile are done
+  uint32_t rows_ready, rows_free;  // the item's rows are in shared memory; its last score product is done
+  uint32_t scores, probs, output;  // per stream: scores; probabilities; output of a tile complete
+  uint32_t end;
+  uint32_t* bad_pages;             // per stage: pages of the tile that lie outside the cache
+  uint32_t* tile_bad;              // the same per stage or buffer, for the exponentials
+  uint32_t (*odd)[4];              // per stage or buffer: keys with non-finite values (taken out)
+  volatile int* dead;
+  uint32_t* tmem;
+  float2* ml;                      // [2][128] (c m, sum) of the streams' rows
+  float* row_c;                    // [128] c of the rows
 };
 
-__device__ __forceinline__ bool sees(const uint64_t bits, int key, int ctx) {
-  return key < ctx || (key - ctx < 64 && (bits >> (key - ctx) & 1));
+// Visibility of 32 keys from `key` on (bit j: key + j) for a row with node mask `bits`.
+__device__ __forceinline__ uint32_t visible32(uint64_t bits, int key, int ctx) {
+  const int ahead = ctx - key;                                  // cached tokens among and after them
+  if (ahead >= 32) return 0xffffffffu;
+  if (ahead > 0) return ((1u << ahead) - 1u) | (uint32_t)(bits << ahead);
+  return -ahead < 64 ? (uint32_t)(bits >> -ahead) : 0u;
 }
-
-// kKeys keys of a tile, from key0 on: scores, softmax step, weighted values. kTail: the tile holds keys that
-// not every row sees; values of keys a row does not see must not reach it, whatever they hold, so
-// non-finite values enter the product as zeros and are added afterwards where they are seen.
-template <typename T, bool kE4M3, int D, int kKeys, bool kTail>
-__device__ __forceinline__ void attend(Rows<D>& w, uint32_t kt, uint32_t vt, int key0, int tile_key, const Request& r,
-                                       uint32_t bad_pages, int page_shift, int lane) {
-  using S = Shape<T, kE4M3, D>;
-  using M = Mma<typename S::C>;
-  constexpr int kSteps = D / 16;
-  const int q = lane & 3, mat = lane >> 3, in8 = lane & 7;
-  float s[kKeys / 8][4];
-#pragma unroll
-  for (int j = 0; j < kKeys / 8; ++j) s[j][0] = s[j][1] = s[j][2] = s[j][3] = 0.f;
-#pragma unroll
-  for (int j = 0; j < kKeys / 16; ++j) {
-    const int key = key0 + 16 * j + (mat >> 1) * 8 + in8;
-    if constexpr (!kE4M3) {
-#pragma unroll
-      for (int t = 0; t < kSteps; ++t) {
-        uint32_t f[4];
-        ldsm4(f, S::piece(kt, key, 2 * t + (mat & 1)));
-        M::step(s[2 * j], w.q[t], f[0], f[1]);
-        M::step(s[2 * j + 1], w.q[t], f[2], f[3]);
-      }
-    } else {
-#pragma unroll
-      for (int t = 0; t < kSteps; t += 2) {
-        uint32_t f[4];
-        ldsm4(f, S::piece(kt, key, t + (mat & 1)));
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-          M::step(s[2 * j + (i >> 1)], w.q[t + (i & 1)], e4m3x2_to_f16x2(f[i] & 0xffffu), e4m3x2_to_f16x2(f[i] >> 16));
-      }
-    }
-  }
-  if constexpr (kTail) {
-#pragma unroll
-    for (int j = 0; j < kKeys / 8; ++j)
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const int in_tile = key0 + 8 * j + 2 * q + (e & 1);
-        const bool on_page = !(bad_pages >> (in_tile >> page_shift) & 1);
-        if (!on_page || !sees(w.bits[e >> 1], tile_key + in_tile, r.ctx)) s[j][e] = -INFINITY;
-      }
-  }
-  float top[2] = {-INFINITY, -INFINITY};
-#pragma unroll
-  for (int j = 0; j < kKeys / 8; ++j)
-#pragma unroll
-    for (int e = 0; e < 4; ++e) top[e >> 1] = fmaxf(top[e >> 1], s[j][e]);
-  float base[2], keep[2];
-#pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    top[i] = fmaxf(top[i], __shfl_xor_sync(0xffffffffu, top[i], 1));
-    top[i] = fmaxf(top[i], __shfl_xor_sync(0xffffffffu, top[i], 2));
-    const float mc = top[i] == -INFINITY ? -INFINITY : fmaf(top[i], w.c[i], -M::kShift);
-    const float now = fmaxf(w.mc[i], mc);
-    base[i] = now == -INFINITY ? 0.f : now;
-    keep[i] = exp2_fast(w.mc[i] - base[i]);
-    w.mc[i] = now;
-    w.l[i] *= keep[i];
-  }
-#pragma unroll
-  for (int j = 0; j < kKeys / 8; ++j)
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      s[j][e] = exp2_fast(fmaf(s[j][e], w.c[e >> 1], -base[e >> 1]));
-      w.l[e >> 1] += s[j][e];
-    }
-  if (__any_sync(0xffffffffu, keep[0] != 1.f || keep[1] != 1.f)) {
-#pragma unroll
-    for (int j = 0; j < D / 8; ++j)
-#pragma unroll
-      for (int e = 0; e < 4; ++e) w.o[j][e] *= keep[e >> 1];
-  }
-  uint32_t odd = 0;
-#pragma unroll
-  for (int j = 0; j < kKeys / 16; ++j) {
-    const uint32_t a[4] = {M::pack(s[2 * j][0], s[2 * j][1]), M::pack(s[2 * j][2], s[2 * j][3]),
-                           M::pack(s[2 * j + 1][0], s[2 * j + 1][1]), M::pack(s[2 * j + 1][2], s[2 * j + 1][3])};
-    const int key = key0 + 16 * j + (mat & 1) * 8 + in8;
-    // the lane's values in a step: keys key0 + 16 j + {0, 8} + 2 q + {0, 1}
-    auto clean = [&](uint32_t v, int half) {
-      if constexpr (kTail) {
-        const uint32_t non = __vcmpeq2(v & M::kExponent, M::kExponent);
-        const int k = tile_key + key0 + 16 * j + 8 * half + 2 * q;
-        odd |= non & ((k < r.keys ? 0xffffu : 0u) | (k + 1 < r.keys ? 0xffff0000u : 0u));
-        return v & ~non;
-      } else {
-        return v;
-      }
-    };
-    if constexpr (!kE4M3) {
-#pragma unroll
-      for (int n = 0; n < D / 8; n += 2) {
-        uint32_t f[4];
-        ldsm4_t(f, S::piece(vt, key, n + (mat >> 1)));
-        M::step(w.o[n], a, clean(f[0], 0), clean(f[1], 1));
-        M::step(w.o[n + 1], a, clean(f[2], 0), clean(f[3], 1));
-      }
-    } else {
-#pragma unroll
-      for (int n = 0; n < D / 16; n += 2) {
-        uint32_t f[4];
-        ldsm4_t(f, S::piece(vt, key, n + (mat >> 1)));
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          const uint32_t a0 = e4m3x2_to_f16x2(f[2 * i] & 0xffffu), a1 = e4m3x2_to_f16x2(f[2 * i] >> 16);
-          const uint32_t b0 = e4m3x2_to_f16x2(f[2 * i + 1] & 0xffffu), b1 = e4m3x2_to_f16x2(f[2 * i + 1] >> 16);
-          M::step(w.o[2 * (n + i)], a, clean(__byte_perm(a0, a1, 0x5410), 0), clean(__byte_perm(b0, b1, 0x5410), 1));
-          M::step(w.o[2 * (n + i) + 1], a, clean(__byte_perm(a0, a1, 0x7632), 0), clean(__byte_perm(b0, b1, 0x7632), 1));
-        }
-      }
-    }
-  }
-  if constexpr (kTail) {
-    if (__any_sync(0xffffffffu, odd != 0)) {
-      // rare: some visible value is NaN or infinite; add such values key by key
-#pragma unroll 1
-      for (int k = 0; k < kKeys; ++k) {
-        const int in_tile = key0 + k, from = (lane & ~3) | (k >> 1 & 3);
-        float mine0 = 0.f, mine1 = 0.f;
-#pragma unroll
-        for (int j = 0; j < kKeys / 8; ++j)
-          if (k >> 3 == j) {
-            mine0 = k & 1 ? s[j][1] : s[j][0];
-            mine1 = k & 1 ? s[j][3] : s[j][2];
-          }
-        const float p0 = __shfl_sync(0xffffffffu, mine0, from), p1 = __shfl_sync(0xffffffffu, mine1, from);
-        if (tile_key + in_tile >= r.keys || (bad_pages >> (in_tile >> page_shift) & 1)) continue;
-        const bool see0 = sees(w.bits[0], tile_key + in_tile, r.ctx), see1 = sees(w.bits[1], tile_key + in_tile, r.ctx);
-#pragma unroll
-        for (int n = 0; n < D / 8; ++n)
-#pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            // the lane's output columns: 8 n + 2 q + e, or interleaved by fours over an E4M3 cache
-            const int d = kE4M3 ? 16 * (n >> 1) + 4 * q + 2 * e + (n & 1) : 8 * n + 2 * q + e;
-            const uint32_t at = S::piece(vt, in_tile, d * S::kBytes / 16) + (d * S::kBytes & 15);
-            float v;
-            if constexpr (kE4M3) {
-              uint32_t raw;
-              asm volatile("ld.shared.u8 %0, [%1];" : "=r"(raw) : "r"(at));
-              v = __half2float(__ushort_as_half((unsigned short)e4m3x2_to_f16x2(raw)));
-            } else {
-              unsigned short raw;
-              asm volatile("ld.shared.u16 %0, [%1];" : "=h"(raw) : "r"(at));
-              T t;
-              memcpy(&t, &raw, 2);
-              v = Elem<T>::to_float(t);
-            }
-            if (!isfinite(v)) {
-              if (see0) w.o[n][e] += p0 * v;
-              if (see1) w.o[n][2 + e] += p1 * v;
-            }
-          }
-      }
-    }
-  }
+// Those of 32 keys of a tile (from in_tile on) that lie on a page of the cache.
+__device__ __forceinline__ uint32_t on_pages32(uint32_t bad, int in_tile, int page_shift) {
+  uint32_t v = 0;
+  if (!(bad >> (in_tile >> page_shift) & 1)) v |= 0xffffu;
+  if (!(bad >> ((in_tile + 16) >> page_shift) & 1)) v |= 0xffff0000u;
+  return v;
 }
 
 template <typename T, bool kE4M3, int D>
-__global__ void __launch_bounds__(kAttnThreads, 1)
+__global__ void __launch_bounds__(Shape<T, kE4M3, D>::kThreads, 1)
 tree_attention_kernel(const AttnParams p, const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap) {
   using S = Shape<T, kE4M3, D>;
-  extern __shared__ uint8_t raw_smem[];
-  uint8_t* base = raw_smem + ((1024 - (smem_u32(raw_smem) & 1023)) & 1023);
-  const uint32_t stages = smem_u32(base);
-  float* merge_o = reinterpret_cast<float*>(base + S::kStages * 2 * S::kTileBytes);
-  float2* merge_ml = reinterpret_cast<float2*>(merge_o + 4 * 16 * D);
-  uint8_t* tail = reinterpret_cast<uint8_t*>(merge_ml + 4 * 16);
-  const uint32_t full = smem_u32(tail), empty = full + 8 * S::kStages;
-  uint32_t* bad_pages = reinterpret_cast<uint32_t*>(tail + 16 * S::kStages);
-  volatile int* dead = reinterpret_cast<volatile int*>(bad_pages + S::kStages);
+  using M = Mma<typename S::C>;
+  extern __shared__ __align__(1024) uint8_t smem[];
+  const uint32_t base = smem_u32(smem);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-
+  constexpr int kClean = kE4M3 ? S::kBuffers : S::kStages;
+  Small sm;
+  {
+    uint8_t* at = smem + S::kSmall;
+    sm.ml = reinterpret_cast<float2*>(at);
+    sm.row_c = reinterpret_cast<float*>(sm.ml + 2 * kTileRows);
+    uint32_t bar = smem_u32(sm.row_c + kTileRows);
+    auto take = [&](int n) { const uint32_t r = bar; bar += 8 * n; return r; };
+    sm.full = take(S::kStages);
+    sm.empty = take(S::kStages);
+    sm.clean = take(kClean);
+    sm.buffer_free = take(S::kBuffers);
+    sm.rows_ready = take(1);
+    sm.rows_free = take(1);
+    sm.scores = take(2);
+    sm.probs = take(2);
+    sm.output = take(2);
+    sm.end = take(1);
+    uint32_t* word = reinterpret_cast<uint32_t*>(smem + (bar - base));
+    sm.odd = reinterpret_cast<uint32_t (*)[4]>(word);
+    sm.bad_pages = word + 4 * kClean;
+    sm.tile_bad = sm.bad_pages + S::kStages;
+    sm.dead = reinterpret_cast<volatile int*>(sm.tile_bad + kClean);
+    sm.tmem = sm.tile_bad + kClean + 1;
+  }
+  if (base & 1023) {                                            // the swizzled tiles need the alignment asked for above
+    if (threadIdx.x == 0) raise_status(p.status, MDW_ERR_UNSUPPORTED_SHAPE);
+    if (blockIdx.x == 0 && threadIdx.x == 0) p.total[0] = p.total[1] = 0;
+    return;
+  }
   if (threadIdx.x == 0) {
     for (int i = 0; i < S::kStages; ++i) {
-      mbar_init(full + 8 * i, 1);
-      mbar_init(empty + 8 * i, kConsumers);
+      mbar_init(sm.full + 8 * i, 1);
+      mbar_init(sm.empty + 8 * i, kE4M3 ? 32 * S::kHelpers : 1);
     }
-    *dead = 0;
+    for (int i = 0; i < kClean; ++i) mbar_init(sm.clean + 8 * i, 32 * S::kHelpers);
+    for (int i = 0; i < S::kBuffers; ++i) mbar_init(sm.buffer_free + 8 * i, 1);
+    mbar_init(sm.rows_ready, 128);
+    mbar_init(sm.rows_free, 1);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(sm.scores + 8 * i, 1);
+      mbar_init(sm.probs + 8 * i, 4);
+      mbar_init(sm.output + 8 * i, 1);
+    }
+    mbar_init(sm.end, 1);
+    *sm.dead = 0;
     mbar_init_fence();
   }
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   Walk walk;
   walk.begin(p, lane);
+  if (walk.left == 0) return;                                   // the whole block
+  if (warp == 1) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" :: "r"(smem_u32(sm.tmem)) : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    tc_fence_before();
+  }
   __syncthreads();
-  if (walk.left == 0) return;
+  tc_fence_after();
+  const uint32_t tmem = *sm.tmem;
+  const uint32_t rows_at = base + S::kRowsAt;
+  auto wait = [&](uint32_t bar, uint32_t parity) { mbar_wait(bar, parity, p.spin_budget, p.status, sm.dead); };
+  auto stage_at = [&](int stage) { return base + S::kStagesAt + stage * 2 * S::kCopied; };
+  auto buffer_at = [&](int b) { return base + S::kBuffersAt + b * 2 * S::kOperand; };
 
-  // Warp 0 requests the tiles, kStages ahead at first, then one for each that every warp has left: it
-  // asks for the stage of the tile before the one it has just done itself, so it seldom waits. Lane i
-  // serves a tile's i-th page; the page's number is loaded one tile ahead.
-  Walk ask = walk;
-  int asked = 0, ask_stage = 0;
-  uint32_t ask_phase = 0;
-  const int box_rows = min(1 << p.page_shift, kTileKeys), pages = kTileKeys / box_rows;
-  int page = -1;
-  bool wanted = false;
-  auto look = [&]() {
-    const int key = ask.tile * kTileKeys + lane * box_rows;
-    wanted = ask.left > 0 && lane < pages && key < ask.r.keys;
-    if (wanted) page = p.block_table[(size_t)ask.b * p.max_pages + (key >> p.page_shift)];
-  };
-  auto request = [&]() {
-    if (ask.left == 0) return;
-    if (asked >= S::kStages) mbar_wait(empty + 8 * ask_stage, ask_phase ^ 1, p.spin_budget, p.status, dead);
-    if (__any_sync(0xffffffffu, *dead)) return;
-    const bool ok = wanted && page >= 0 && page < p.num_pages;
-    const unsigned good = __ballot_sync(0xffffffffu, ok), bad = __ballot_sync(0xffffffffu, wanted && !ok);
-    const uint32_t bar = full + 8 * ask_stage, kt = stages + ask_stage * 2 * S::kTileBytes, vt = kt + S::kTileBytes;
-    const uint32_t page_bytes = (uint32_t)box_rows * D * S::kBytes;
-    if (lane == 0) {
-      bad_pages[ask_stage] = bad;
-      if (bad) raise_status(p.status, MDW_ERR_DEVICE_BOUNDS);
-      mbar_arrive_tx(bar, 2 * page_bytes * __popc(good));
-    }
-    __syncwarp();
-    if (ok) {
-      const int row = (ask.tile * kTileKeys + lane * box_rows) & ((1 << p.page_shift) - 1);
-#pragma unroll
-      for (int i = 0; i < S::kHalves; ++i) {
-        const uint32_t off = i * (kTileKeys * S::kRowBytes) + lane * box_rows * S::kRowBytes;
-        tma_load(kt + off, &kmap, bar, i * (S::kRowBytes / S::kBytes), row, ask.h, page);
-      }
-#pragma unroll
-      for (int i = 0; i < S::kHalves; ++i) {
-        const uint32_t off = i * (kTileKeys * S::kRowBytes) + lane * box_rows * S::kRowBytes;
-        tma_load(vt + off, &vmap, bar, i * (S::kRowBytes / S::kBytes), row, ask.h, page);
-      }
-    }
-    ++asked;
-    if (++ask_stage == S::kStages) { ask_stage = 0; ask_phase ^= 1; }
-    if (--ask.left > 0 && ++ask.tile == ask.tiles) ask.next_item(p, lane);
-    look();
-  };
   if (warp == 0) {
+    // ---- copies: lane i serves the tile's i-th page, whose number is loaded one tile ahead
+    int stage = 0;
+    uint32_t phase = 0;
+    const int box_rows = min(1 << p.page_shift, kTileKeys), pages = kTileKeys / box_rows;
+    const uint32_t page_bytes = (uint32_t)box_rows * D * S::kBytes;
+    int page = -1, key = 0;
+    bool wanted = false;
+    auto look = [&]() {
+      key = walk.tile * kTileKeys + lane * box_rows;
+      wanted = lane < pages && key < walk.r.keys;
+      if (wanted) page = p.block_table[(size_t)walk.b * p.max_pages + (key >> p.page_shift)];
+    };
     look();
-    for (int i = 0; i < S::kStages; ++i) request();
-  }
-
-  int stage = 0;
-  uint32_t phase = 0;
-  bool behind = false;             // whether a tile has been done
-  const int g = lane >> 2, q = lane & 3;
-  while (walk.left > 0) {
-    // one item: rows [first, first + rows) of the request, tiles [tile, tile + count)
-    const Request r = walk.r;
-    const int first = walk.rb * kTileRows, rows = min(r.rows * p.group - first, kTileRows);
-    const int row_warps = rows <= 16 ? 1 : (rows <= 32 ? 2 : 4), slices = kConsumers / row_warps;
-    const int wr = warp % row_warps, slice = warp / row_warps, h = walk.h;
-    const int tile0 = walk.tile, count = min(walk.tiles - tile0, walk.left);
-    const bool whole = count == walk.tiles;
-
-    Rows<D> w;
-    const bool live = wr * 16 < rows;
-    const float c = p.scale * kLog2e * (kE4M3 ? p.k_scale[h] : 1.f);
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const int row = wr * 16 + g + 8 * i, flat = first + row;
-      const bool in = row < rows;
-      const int node = in ? flat / p.group : 0, head = h * p.group + (in ? flat - node * p.group : 0);
-      const T* src = static_cast<const T*>(p.q) + (int64_t)(r.row0 + node) * p.ldq + (int64_t)head * D;
-      w.bits[i] = 0;
-      if (in) {
-        w.bits[i] = p.tree_mask ? p.tree_mask[r.row0 + node] : ~0ull >> (63 - node);
-        if (r.rows < 64) w.bits[i] &= (1ull << r.rows) - 1;
+    for (;;) {
+      const bool ok = wanted && page >= 0 && page < p.num_pages;
+      const int id = page, row = key & ((1 << p.page_shift) - 1), head = walk.h;
+      const unsigned good = __ballot_sync(0xffffffffu, ok), bad = __ballot_sync(0xffffffffu, wanted && !ok);
+      const bool more = --walk.left > 0;
+      if (more) {
+        if (++walk.tile == walk.tiles) walk.next_item(p, lane);
+        look();
       }
-      w.c[i] = c;
-      w.mc[i] = -INFINITY;
-      w.l[i] = 0.f;
-      if constexpr (!kE4M3) {
-#pragma unroll
-        for (int t = 0; t < D / 16; ++t)
-#pragma unroll
-          for (int e = 0; e < 2; ++e)
-            w.q[t][i + 2 * e] = in ? *reinterpret_cast<const uint32_t*>(src + 16 * t + 8 * e + 2 * q) : 0u;
-      } else {
-        // E4M3 keys give a lane four consecutive elements; the order of a product's k is free
-        uint2 v[D / 16];
-        float top = 0.f;
-#pragma unroll
-        for (int t = 0; t < D / 16; ++t) {
-          v[t] = in ? *reinterpret_cast<const uint2*>(src + 16 * t + 4 * q) : make_uint2(0u, 0u);
-          T x[4];
-          memcpy(x, &v[t], 8);
-          for (int e = 0; e < 4; ++e) top = fmaxf(top, fabsf(Elem<T>::to_float(x[e])));
-        }
-        float f = 1.f;
-        if constexpr (std::is_same<T, __nv_bfloat16>::value) {
-          // bf16 rows enter f16 times a power of two that puts their largest element in [1, 4)
-          top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
-          top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
-          const int ex = top > 0.f && isfinite(top) ? min((int)(__float_as_uint(top) >> 23) - 127, 126) : 0;
-          f = __uint_as_float((uint32_t)(127 - ex) << 23);
-          w.c[i] = c * (ex >= -126 ? __uint_as_float((uint32_t)(127 + ex) << 23) : 5.877471754111438e-39f);
-        }
-#pragma unroll
-        for (int t = 0; t < D / 16; ++t) {
-          T x[4];
-          memcpy(x, &v[t], 8);
-          for (int e = 0; e < 2; ++e)
-            w.q[t][i + 2 * e] = Mma<__half>::pack(Elem<T>::to_float(x[2 * e]) * f, Elem<T>::to_float(x[2 * e + 1]) * f);
-        }
-      }
-    }
-#pragma unroll
-    for (int n = 0; n < D / 8; ++n) w.o[n][0] = w.o[n][1] = w.o[n][2] = w.o[n][3] = 0.f;
-
-    for (int i = 0; i < count; ++i) {
-      mbar_wait(full + 8 * stage, phase, p.spin_budget, p.status, dead);
-      __syncwarp();
-      if (live) {
-        const uint32_t kt = stages + stage * 2 * S::kTileBytes, vt = kt + S::kTileBytes, bad = bad_pages[stage];
-        const int tile_key = (tile0 + i) * kTileKeys;
-        const bool all = tile_key + kTileKeys <= r.ctx && bad == 0;
-        const int keys = 16 * row_warps, key0 = slice * keys;
-        if (!all)
-          for (int k = 0; k < keys; k += 16) attend<T, kE4M3, D, 16, true>(w, kt, vt, key0 + k, tile_key, r, bad, p.page_shift, lane);
-        else if (row_warps == 1)
-          attend<T, kE4M3, D, 16, false>(w, kt, vt, key0, tile_key, r, bad, p.page_shift, lane);
-        else
-          for (int k = 0; k < keys; k += 32) attend<T, kE4M3, D, 32, false>(w, kt, vt, key0 + k, tile_key, r, bad, p.page_shift, lane);
+      wait(sm.empty + 8 * stage, phase ^ 1);
+      if (__any_sync(0xffffffffu, *sm.dead)) break;
+      const uint32_t bar = sm.full + 8 * stage, kt = stage_at(stage), vt = kt + S::kCopied;
+      if (lane == 0) {
+        sm.bad_pages[stage] = bad;
+        if (bad) raise_status(p.status, MDW_ERR_DEVICE_BOUNDS);
+        mbar_arrive_tx(bar, 2 * page_bytes * __popc(good));
       }
       __syncwarp();
-      if (lane == 0) mbar_arrive(empty + 8 * stage);
+      if (ok) {
+#pragma unroll
+        for (int i = 0; i < S::kHalves; ++i) {
+          const uint32_t off = i * (kTileKeys * S::kRowBytes) + lane * box_rows * S::kRowBytes;
+          tma_load(kt + off, &kmap, bar, i * (S::kRowBytes / S::kBytes), row, head, id);
+        }
+#pragma unroll
+        for (int i = 0; i < S::kHalves; ++i) {
+          const uint32_t off = i * (kTileKeys * S::kRowBytes) + lane * box_rows * S::kRowBytes;
+          tma_load(vt + off, &vmap, bar, i * (S::kRowBytes / S::kBytes), row, head, id);
+        }
+      }
       if (++stage == S::kStages) { stage = 0; phase ^= 1; }
-      if (warp == 0) {
-        if (behind) request();
-        behind = true;
-      }
+      if (!more) break;
     }
-
-    // join the slices of each row tile: halves, in a fixed order
+    if (__any_sync(0xffffffffu, *sm.dead))
+      for (int i = 0; i < S::kStages; ++i) mbar_drain(sm.full + 8 * i, i < stage ? phase : phase ^ 1);
+  } else if (warp == 1) {
+    // ---- products. Scores of the first two tiles of an item, then in turn the output of tile i and the scores
+    // of tile i + 2, whose columns hold the probabilities that output reads.
+    constexpr int kSlots = kE4M3 ? S::kBuffers : S::kStages;    // where operands lie
+    int n = 0, items = 0, done[2] = {0, 0};                     // tiles before this item; items; outputs of each stream
+    while (walk.left > 0) {
+      const int count = min(walk.tiles - walk.tile, walk.left);
+      auto scores = [&](int i) {
+        const int at = (n + i) % kSlots, s = i & 1;
+        const uint32_t parity = ((n + i) / kSlots) & 1;
+        wait(kE4M3 ? sm.clean + 8 * at : sm.full + 8 * at, parity);
+        if (lane == 0) {
+          tc_fence_after();
+          const uint32_t kt = kE4M3 ? buffer_at(at) : stage_at(at);
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      w.l[i] += __shfl_xor_sync(0xffffffffu, w.l[i], 1);
-      w.l[i] += __shfl_xor_sync(0xffffffffu, w.l[i], 2);
-    }
-    for (int off = slices / 2; off > 0; off >>= 1) {
-      if (slice >= off && slice < 2 * off) {
-        const int at = (slice - off) * row_warps + wr;
-        float* o = merge_o + at * 16 * D + lane;
-#pragma unroll
-        for (int n = 0; n < D / 8; ++n)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) o[32 * (4 * n + e)] = w.o[n][e];
-        if (q == 0) {
-          merge_ml[at * 16 + g] = make_float2(w.mc[0], w.l[0]);
-          merge_ml[at * 16 + g + 8] = make_float2(w.mc[1], w.l[1]);
+          for (int t = 0; t < D / 16; ++t) {
+            const uint32_t off = (t >> 2) * (128 * 128) + (t & 3) * 32;
+            tc_mma(tmem + s * S::kStream, smem_operand(rows_at + off, 16, 1024), smem_operand(kt + off, 16, 1024),
+                   mma_shape(M::kBf16, false, kTileKeys), t > 0);
+          }
+          tc_commit(sm.scores + 8 * s);
+          if (i == count - 1) tc_commit(sm.rows_free);
         }
-      }
-      asm volatile("bar.sync 1, 256;" ::: "memory");
-      if (slice < off) {
-        const int at = slice * row_warps + wr;
-        const float* o = merge_o + at * 16 * D + lane;
-        float mine[2], other[2];
+        __syncwarp();
+      };
+      wait(sm.rows_ready, items & 1);
+      scores(0);
+      if (count > 1) scores(1);
+      for (int i = 0; i < count; ++i) {
+        const int at = (n + i) % kSlots, s = i & 1;
+        if (!kE4M3) wait(sm.clean + 8 * at, ((n + i) / kSlots) & 1);
+        wait(sm.probs + 8 * s, done[s] & 1);
+        if (lane == 0) {
+          tc_fence_after();
+          const uint32_t vt = kE4M3 ? buffer_at(at) + S::kOperand : stage_at(at) + S::kCopied;
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          const float2 ml = merge_ml[at * 16 + g + 8 * i];
-          const float top = fmaxf(w.mc[i], ml.x), safe = top == -INFINITY ? 0.f : top;
-          mine[i] = exp2_fast(w.mc[i] - safe);
-          other[i] = exp2_fast(ml.x - safe);
-          w.mc[i] = top;
-          w.l[i] = w.l[i] * mine[i] + ml.y * other[i];
+          for (int t = 0; t < kTileKeys / 16; ++t)
+            tc_mma_tmem(tmem + s * S::kStream + S::kOut, tmem + s * S::kStream + S::kProb + 8 * t,
+                        smem_operand(vt + t * 2048, 128 * 128, 1024), mma_shape(M::kBf16, true, D));
+          tc_commit(sm.output + 8 * s);
+          tc_commit(kE4M3 ? sm.buffer_free + 8 * at : sm.empty + 8 * at);
         }
-#pragma unroll
-        for (int n = 0; n < D / 8; ++n)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) w.o[n][e] = w.o[n][e] * mine[e >> 1] + o[32 * (4 * n + e)] * other[e >> 1];
+        __syncwarp();
+        if (i + 2 < count) {
+          wait(sm.output + 8 * s, done[s] & 1);
+          scores(i + 2);
+        }
+        ++done[s];
       }
-      asm volatile("bar.sync 1, 256;" ::: "memory");
+      n += count;
+      ++items;
+      walk.left -= count;
+      if (walk.left > 0) walk.next_item(p, lane);
     }
-    if (slice == 0 && live && !*dead) {
-      const int slot = 2 * blockIdx.x + (tile0 > 0 ? 0 : 1);
-      const float vs = kE4M3 ? p.v_scale[h] : 1.f;
+    if (lane == 0) tc_commit(sm.end);
+    __syncwarp();
+    mbar_drain(sm.end, 0);                                      // nothing is in flight when the columns are given back
+  } else if (warp < 4 || warp >= 12) {
+    // ---- values: in a tile that not every row sees as a whole, non-finite values are taken out and noted per
+    // key (the rows that see them add them); E4M3 tiles are converted
+    const int id = (warp < 4 ? warp - 2 : warp - 10) * 32 + lane;
+    constexpr int kAll = 32 * S::kHelpers;
+    int stage = 0, n = 0;
+    uint32_t phase = 0;
+    while (walk.left > 0) {
+      const Request r = walk.r;
+      const int tile_key = walk.tile * kTileKeys;
+      wait(sm.full + 8 * stage, phase);
+      const uint32_t bad = sm.bad_pages[stage];
+      const bool all = tile_key + kTileKeys <= r.ctx && bad == 0;
+      const int b = kE4M3 ? n % 2 : stage;
+      const uint32_t kt = stage_at(stage), vt = kt + S::kCopied;
+      if constexpr (kE4M3) wait(sm.buffer_free + 8 * b, (n / 2 & 1) ^ 1);
+      if (id == 0) sm.tile_bad[b] = bad;
+      if (!all) {
+        if (id < 4) sm.odd[b][id] = 0;
+        asm volatile("bar.sync 2, %0;" :: "n"(kAll) : "memory");
+      }
+      auto note = [&](uint32_t non, int key) {
+        if (non && tile_key + key < r.keys && !(bad >> (key >> p.page_shift) & 1)) atomicOr(&sm.odd[b][key >> 5], 1u << (key & 31));
+      };
+      if constexpr (!kE4M3) {
+        if (!all)
+          for (int i = id; i < kTileKeys * (D / 8); i += kAll) {
+            const int key = i / (D / 8);
+            const uint32_t at = S::copied(vt, key, i % (D / 8));
+            const uint4 v = lds16(at);
+            const uint32_t e = M::kExponent;
+            const uint4 non = make_uint4(__vcmpeq2(v.x & e, e), __vcmpeq2(v.y & e, e), __vcmpeq2(v.z & e, e), __vcmpeq2(v.w & e, e));
+            if (non.x | non.y | non.z | non.w) {
+              sts16(at, make_uint4(v.x & ~non.x, v.y & ~non.y, v.z & ~non.z, v.w & ~non.w));
+              note(1u, key);
+            }
+          }
+      } else {
+        const uint32_t to = buffer_at(b);
+        for (int i = id; i < 2 * kTileKeys * (D / 16); i += kAll) {
+          const int part = i / (kTileKeys * (D / 16)), key = i / (D / 16) % kTileKeys, piece = i % (D / 16);
+          uint4 v = lds16(S::copied(part ? vt : kt, key, piece));
+          if (part && !all) {
+            // the only non-finite code is S.1111.111
+            const uint32_t m = 0x7f7f7f7fu;
+            const uint4 non = make_uint4(__vcmpeq4(v.x & m, m), __vcmpeq4(v.y & m, m), __vcmpeq4(v.z & m, m), __vcmpeq4(v.w & m, m));
+            note(non.x | non.y | non.z | non.w, key);
+            v = make_uint4(v.x & ~non.x, v.y & ~non.y, v.z & ~non.z, v.w & ~non.w);
+          }
+          const uint32_t at = to + part * S::kOperand;
+          sts16(S::operand(at, key, 2 * piece), make_uint4(e4m3x2_to_f16x2(v.x & 0xffffu), e4m3x2_to_f16x2(v.x >> 16),
+                                                           e4m3x2_to_f16x2(v.y & 0xffffu), e4m3x2_to_f16x2(v.y >> 16)));
+          sts16(S::operand(at, key, 2 * piece + 1), make_uint4(e4m3x2_to_f16x2(v.z & 0xffffu), e4m3x2_to_f16x2(v.z >> 16),
+                                                               e4m3x2_to_f16x2(v.w & 0xffffu), e4m3x2_to_f16x2(v.w >> 16)));
+        }
+        mbar_arrive(sm.empty + 8 * stage);
+      }
+      fence_async_proxy();
+      mbar_arrive(sm.clean + 8 * b);
+      ++n;
+      if (++stage == S::kStages) { stage = 0; phase ^= 1; }
+      if (--walk.left > 0 && ++walk.tile == walk.tiles) walk.next_item(p, lane);
+    }
+  } else {
+    // ---- exponentials: thread = row
+    const int s = warp >= 8 ? 1 : 0, row = (warp & 3) * 32 + lane;
+    const uint32_t lanes = (uint32_t)(warp & 3) * 32 << 16;
+    const uint32_t scores = tmem + s * S::kStream + lanes, probs = scores + S::kProb, out = scores + S::kOut;
+    int n = 0, items = 0, done = 0;                             // tiles before this item; items; tiles of this stream
+    while (walk.left > 0) {
+      const Request r = walk.r;
+      const int first = walk.rb * kTileRows, rows = min(r.rows * p.group - first, kTileRows), h = walk.h;
+      const int tile0 = walk.tile, count = min(walk.tiles - tile0, walk.left);
+      const bool whole = count == walk.tiles, valid = row < rows, active = (warp & 3) * 32 < rows;
+      const int flat = first + (valid ? row : 0), node = flat / p.group, head = h * p.group + flat - node * p.group;
+      float c = p.scale * kLog2e * (kE4M3 ? p.k_scale[h] : 1.f);
+      if (s == 0) {
+        // the item's rows, after the products with the last item's
+        if (items > 0) wait(sm.rows_free, (items - 1) & 1);
+        if (valid) {
+          const T* src = static_cast<const T*>(p.q) + (int64_t)(r.row0 + node) * p.ldq + (int64_t)head * D;
+          if constexpr (!kE4M3) {
+#pragma unroll 8
+            for (int i = 0; i < D / 8; ++i) sts16(S::operand(rows_at, row, i), *reinterpret_cast<const uint4*>(src + 8 * i));
+          } else {
+            float f = 1.f;
+            if constexpr (std::is_same<T, __nv_bfloat16>::value) {
+              // bf16 rows enter f16 times a power of two that puts their largest element in [1, 4)
+              float top = 0.f;
+#pragma unroll 8
+              for (int i = 0; i < D / 8; ++i) {
+                T x[8];
+                const uint4 v = *reinterpret_cast<const uint4*>(src + 8 * i);
+                memcpy(x, &v, 16);
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const int row = wr * 16 + g + 8 * i, flat = first + row;
-        if (row >= rows) continue;
+                for (int e = 0; e < 8; ++e) top = fmaxf(top, fabsf(Elem<T>::to_float(x[e])));
+              }
+              const int ex = top > 0.f && isfinite(top) ? min((int)(__float_as_uint(top) >> 23) - 127, 126) : 0;
+              f = __uint_as_float((uint32_t)(127 - ex) << 23);
+              c *= ex >= -126 ? __uint_as_float((uint32_t)(127 + ex) << 23) : 5.877471754111438e-39f;
+            }
+#pragma unroll 8
+            for (int i = 0; i < D / 8; ++i) {
+              T x[8];
+              uint4 v = *reinterpret_cast<const uint4*>(src + 8 * i);
+              memcpy(x, &v, 16);
+              uint32_t* w = reinterpret_cast<uint32_t*>(&v);
+#pragma unroll
+              for (int e = 0; e < 4; ++e) w[e] = M::pack(Elem<T>::to_float(x[2 * e]) * f, Elem<T>::to_float(x[2 * e + 1]) * f);
+              sts16(S::operand(rows_at, row, i), v);
+            }
+          }
+        }
+        if (kE4M3) sm.row_c[row] = c;
+        fence_async_proxy();
+        mbar_arrive(sm.rows_ready);
+      }
+      uint64_t bits = 0;
+      if (valid) {
+        bits = p.tree_mask ? p.tree_mask[r.row0 + node] : ~0ull >> (63 - (flat / p.group));
+        if (r.rows < 64) bits &= (1ull << r.rows) - 1;
+      }
+      float mc = -INFINITY, l = 0.f;                            // base of the exponents (less kShift), sum
+      float v[32];
+      if (active) {
+#pragma unroll
+        for (int j = 0; j < 32; ++j) v[j] = 0.f;
+#pragma unroll
+        for (int i = 0; i < D; i += 32) tc_st32(out + i, v);
+        tc_wait_st();
+      }
+      if (kE4M3) {
+        asm volatile("bar.sync 1, 256;" ::: "memory");
+        c = sm.row_c[row];
+      }
+      for (int i = s; i < count; i += 2) {
+        const int at = (n + i) % kClean, tile_key = (tile0 + i) * kTileKeys;
+        wait(sm.clean + 8 * at, ((n + i) / kClean) & 1);
+        wait(sm.scores + 8 * s, done & 1);
+        __syncwarp();
+        if (active) {
+          tc_fence_after();
+          const uint32_t bad = sm.tile_bad[at];
+          const bool all = tile_key + kTileKeys <= r.ctx && bad == 0;
+          uint32_t see[4] = {~0u, ~0u, ~0u, ~0u};
+          if (!all)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) see[j] = visible32(bits, tile_key + 32 * j, r.ctx) & on_pages32(bad, 32 * j, p.page_shift);
+          float top = -INFINITY;
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            tc_ld32(v, scores + 32 * j);
+            if (!all)
+#pragma unroll
+              for (int e = 0; e < 32; ++e) v[e] = see[j] >> e & 1 ? v[e] : -INFINITY;
+#pragma unroll
+            for (int e = 0; e < 32; ++e) top = fmaxf(top, v[e]);
+          }
+          const float now = top == -INFINITY ? -INFINITY : fmaf(top, c, -M::kShift);
+          const bool grown = valid && now > mc + kSlack;        // also from -inf
+          if (__any_sync(0xffffffffu, grown)) {
+            const float f = grown ? (mc == -INFINITY ? 0.f : exp2_fast(mc - now)) : 1.f;
+            if (__any_sync(0xffffffffu, grown && l != 0.f)) {
+#pragma unroll 1
+              for (int i2 = 0; i2 < D; i2 += 32) {
+                tc_ld32(v, out + i2);
+#pragma unroll
+                for (int e = 0; e < 32; ++e) v[e] *= f;
+                tc_st32(out + i2, v);
+              }
+              tc_wait_st();
+            }
+            l *= f;
+            if (grown) mc = now;
+          }
+          const float from = mc == -INFINITY ? 0.f : mc;
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            tc_ld32(v, scores + 32 * j);
+            if (!all)
+#pragma unroll
+              for (int e = 0; e < 32; ++e) v[e] = see[j] >> e & 1 ? v[e] : -INFINITY;
+            float sum[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int e = 0; e < 32; ++e) {
+              v[e] = exp2_fast(fmaf(v[e], c, -from));
+              sum[e & 3] += v[e];
+            }
+            l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+            uint32_t packed[16];
+#pragma unroll
+            for (int e = 0; e < 16; ++e) packed[e] = M::pack(v[2 * e], v[2 * e + 1]);
+            tc_st16(probs + 16 * j, packed);
+            if (!all) {
+              // rare: keys with values that are NaN or infinite; the rows that see one add them themselves
+              for (uint32_t odd = sm.odd[at][j]; odd; odd &= odd - 1) {
+                const int k = __ffs(odd) - 1, key = tile_key + 32 * j + k;
+                float pk = 0.f;
+#pragma unroll
+                for (int e = 0; e < 32; ++e) pk = e == k ? v[e] : pk;
+                const bool seen = valid && (see[j] >> k & 1);
+                const int64_t page = p.block_table[(size_t)walk.b * p.max_pages + (key >> p.page_shift)];
+                const int64_t src = page * p.page_stride + (((int64_t)h << p.page_shift) + (key & ((1 << p.page_shift) - 1))) * D;
+                tc_wait_st();
+#pragma unroll 1
+                for (int i2 = 0; i2 < D; i2 += 32) {
+                  float o[32];
+                  tc_ld32(o, out + i2);
+#pragma unroll
+                  for (int e = 0; e < 32; ++e) {
+                    float x;
+                    if constexpr (kE4M3) x = __half2float(__ushort_as_half((unsigned short)e4m3x2_to_f16x2(static_cast<const uint8_t*>(p.v)[src + i2 + e])));
+                    else x = Elem<T>::to_float(static_cast<const T*>(p.v)[src + i2 + e]);
+                    if (seen && !isfinite(x)) o[e] += pk * x;
+                  }
+                  tc_st32(out + i2, o);
+                }
+              }
+            }
+          }
+          tc_wait_st();
+          tc_fence_before();
+        }
+        ++done;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(sm.probs + 8 * s);
+      }
+      // ---- the two streams' sums, each half of the columns by one of them
+      if (count > s) wait(sm.output + 8 * s, (done - 1) & 1);
+      __syncwarp();
+      tc_fence_after();
+      sm.ml[s * kTileRows + row] = make_float2(mc, l);
+      tc_fence_before();
+      asm volatile("bar.sync 1, 256;" ::: "memory");
+      tc_fence_after();
+      if (active && !*sm.dead) {
+        const float2 a = sm.ml[row], b = sm.ml[kTileRows + row];
+        const float m = fmaxf(a.x, b.x), from = m == -INFINITY ? 0.f : m;
+        float fa = exp2_fast(a.x - from), fb = exp2_fast(b.x - from);
+        const float sum = a.y * fa + b.y * fb;
+        const int slot = 2 * blockIdx.x + (tile0 > 0 ? 0 : 1);
         if (whole) {
-          const int node = flat / p.group, head = h * p.group + flat - node * p.group;
-          T* dst = static_cast<T*>(p.out) + (int64_t)(r.row0 + node) * p.ldo + (int64_t)head * D;
-          const float f = w.l[i] == 0.f ? 0.f : vs / w.l[i];
-          if constexpr (!kE4M3) {
+          const float f = sum == 0.f ? 0.f : (kE4M3 ? p.v_scale[h] : 1.f) / sum;
+          fa *= f;
+          fb *= f;
+        }
+#pragma unroll 1
+        for (int i = s * (D / 2); i < (s + 1) * (D / 2); i += 32) {
+          float w[32];
+          tc_ld32(v, tmem + lanes + S::kOut + i);
+          tc_ld32(w, tmem + lanes + S::kStream + S::kOut + i);
 #pragma unroll
-            for (int n = 0; n < D / 8; ++n)
-              *reinterpret_cast<uint32_t*>(dst + 8 * n + 2 * q) =
-                  Mma<T>::pack(w.l[i] == 0.f ? 0.f : w.o[n][2 * i] * f, w.l[i] == 0.f ? 0.f : w.o[n][2 * i + 1] * f);
-          } else {
+          for (int e = 0; e < 32; ++e) v[e] = fa * v[e] + fb * w[e];
+          if (valid && whole) {
+            T* dst = static_cast<T*>(p.out) + (int64_t)(r.row0 + node) * p.ldo + (int64_t)head * D + i;
 #pragma unroll
-            for (int n = 0; n < D / 8; n += 2)
-              *reinterpret_cast<uint2*>(dst + 8 * n + 4 * q) =
-                  w.l[i] == 0.f ? make_uint2(0u, 0u)
-                                : make_uint2(Mma<T>::pack(w.o[n][2 * i] * f, w.o[n + 1][2 * i] * f),
-                                             Mma<T>::pack(w.o[n][2 * i + 1] * f, w.o[n + 1][2 * i + 1] * f));
+            for (int e = 0; e < 32; e += 8)
+              *reinterpret_cast<uint4*>(dst + e) =
+                  sum == 0.f ? make_uint4(0u, 0u, 0u, 0u)
+                             : make_uint4(Mma<T>::pack(v[e], v[e + 1]), Mma<T>::pack(v[e + 2], v[e + 3]),
+                                          Mma<T>::pack(v[e + 4], v[e + 5]), Mma<T>::pack(v[e + 6], v[e + 7]));
+          } else if (valid) {
+            float* dst = p.part_o + ((size_t)slot * kTileRows + row) * D + i;
+#pragma unroll
+            for (int e = 0; e < 32; e += 4) *reinterpret_cast<float4*>(dst + e) = make_float4(v[e], v[e + 1], v[e + 2], v[e + 3]);
           }
-          if (p.lse && q == 0)
-            p.lse[(int64_t)(r.row0 + node) * p.Hq + head] = w.l[i] == 0.f ? -INFINITY : (w.mc[i] + log2f(w.l[i])) * kLn2;
-        } else {
-          float* o = p.part_o + ((size_t)slot * kTileRows + row) * D;
-          if constexpr (!kE4M3) {
-#pragma unroll
-            for (int n = 0; n < D / 8; ++n)
-              *reinterpret_cast<float2*>(o + 8 * n + 2 * q) = make_float2(w.o[n][2 * i], w.o[n][2 * i + 1]);
-          } else {
-#pragma unroll
-            for (int n = 0; n < D / 8; n += 2)
-              *reinterpret_cast<float4*>(o + 8 * n + 4 * q) =
-                  make_float4(w.o[n][2 * i], w.o[n + 1][2 * i], w.o[n][2 * i + 1], w.o[n + 1][2 * i + 1]);
-          }
-          if (q == 0) p.part_ml[(size_t)slot * kTileRows + row] = make_float2(w.mc[i], w.l[i]);
+          __syncwarp();                                         // the loads above are the whole warp's
+        }
+        if (s == 0 && valid) {
+          if (!whole) p.part_ml[(size_t)slot * kTileRows + row] = make_float2(m, sum);
+          else if (p.lse) p.lse[(int64_t)(r.row0 + node) * p.Hq + head] = sum == 0.f ? -INFINITY : (m + log2f(sum)) * kLn2;
         }
       }
+      tc_fence_before();
+      asm volatile("bar.sync 1, 256;" ::: "memory");
+      tc_fence_after();
+      n += count;
+      ++items;
+      walk.left -= count;
+      if (walk.left > 0) walk.next_item(p, lane);
     }
-    walk.left -= count;
-    if (walk.left > 0) walk.next_item(p, lane);
   }
-  if (warp == 0 && __any_sync(0xffffffffu, *dead))
-    for (int i = 0; i < S::kStages && i < asked; ++i) mbar_drain(full + 8 * i, ((asked - i + S::kStages - 1) / S::kStages - 1) & 1);
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" :: "r"(tmem) : "memory");
+  }
 }
 
 // Joins the partial items: block x belongs to the boundary before share x + 1, and works if it is the first one
@@ -788,7 +917,7 @@ cudaError_t launch(const AttnParams& p, const CUtensorMap& km, const CUtensorMap
   using S = Shape<T, kE4M3, D>;
   cudaError_t e = allow_shared_memory<tree_attention_kernel<T, kE4M3, D>>(dev);
   if (e != cudaSuccess) return e;
-  tree_attention_kernel<T, kE4M3, D><<<grid, kAttnThreads, S::kSmem, s>>>(p, km, vm);
+  tree_attention_kernel<T, kE4M3, D><<<grid, S::kThreads, S::kSmem, s>>>(p, km, vm);
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   if (grid == 1) return cudaSuccess;
@@ -850,7 +979,7 @@ extern "C" mdw_status mdw_tree_attention(const mdw_kv_cache* cache, int32_t B, i
   if (ws_bytes < lay.total) return MDW_ERR_WORKSPACE_TOO_SMALL;
   if (grid <= 0) return MDW_ERR_CUDA;
   uint8_t* base = static_cast<uint8_t*>(ws);
-  const AttnParams p{cache->k_scale, cache->v_scale, q, out, lse, ldq, ldo, block_table, ctx_len, row_start, tree_mask, status,
+  const AttnParams p{cache->v, cache->page_stride, cache->k_scale, cache->v_scale, q, out, lse, ldq, ldo, block_table, ctx_len, row_start, tree_mask, status,
                      mdw_spin_budget(), scale, B, T, q_heads, cache->kv_heads, q_heads / cache->kv_heads, max_new, max_pages,
                      cache->num_pages, log2_of(cache->page_size), reinterpret_cast<int32_t*>(base),
                      reinterpret_cast<Cut*>(base + lay.cuts), reinterpret_cast<float2*>(base + lay.ml),

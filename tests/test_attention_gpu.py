@@ -701,11 +701,13 @@ def test_binding_refuses():
 def test_attention_wait_that_runs_out_is_reported():
     """A bounded wait of the copy pipeline that gives up ends in MDW_ERR_TIMEOUT, a clean exit and a usable
     device; rows are then not stored."""
-    c = Attn(19, [3000, 500], [4, 2], 8, 2, 128, 16, BF, BF)
+    c = Attn(19, [40000, 500], [4, 2], 8, 2, 128, 16, BF, BF)
+    ws = torch.empty(api.mdw_tree_attention_workspace_bytes(c.cache, 2, c.t, 8, 4), dtype=torch.uint8, device="cuda")
     api.mdw_debug_set_spin_budget(1)
     try:
         status = i32([0])
-        c.call(status=status)
+        torch.zeros(1 << 28, dtype=torch.int32, device="cuda")  # the cache leaves the L2: its copies are waited for
+        c.call(status=status, ws=ws)
         assert status.item() == 6
     finally:
         api.mdw_debug_set_spin_budget(0)
