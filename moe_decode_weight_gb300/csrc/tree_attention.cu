@@ -12,16 +12,23 @@
 // per SM: ragged lengths balance, and only the first and last item of a share are partial. Their sums
 // go to the workspace and a second, dependent launch joins them.
 //
-// Both products run on tcgen05 with the rows as the 128 lanes of tensor memory (fewer rows cost the tensor
-// cores nothing that the memory stream would not hide): scores = rows x keys into 128 columns, then
-// probabilities x values onto D columns of output, the probabilities read from tensor memory. The
-// tiles of an item alternate between two streams with scores, output, maximum and sum of their own, so
-// that one stream's exponentials run while the tensor cores work for the other. The roles of a block:
+// Both products run on tcgen05 with the rows as the 128 lanes of tensor memory: scores = rows x keys into 128
+// columns, then probabilities x values onto D columns of output, the probabilities read from tensor memory.
+// Up to 64 (32) rows are laid down two (four) times, and every copy takes the exponentials of a half
+// (quarter) of the keys, so that all four schedulers share them; its other probabilities are zeros, and
+// the copies' outputs are joined at the end of the item. The tiles of an item alternate between
+// two streams with scores, output, maximum and sum of their own, so that one stream's exponentials run
+// while the tensor cores work for the other.
+//
+// What bounds it is the stream of keys and values: 152 SMs need about 128 KB each in flight to draw the
+// memory's full rate (a copy alone, with nothing done to the tiles, reaches 7.1 TB/s so, 16-token
+// pages in random order). Keys and values therefore share one ring in the order in which the products
+// free them (K0 K1 V0 K2 V1 K3 ...), and a tile is held only while its product runs. The roles of a block:
 //   warp 0       requests the tiles by TMA (a box per page, head and 128 bytes of a row, swizzled)
 //   warp 1       issues the matrix products
 //   warps 2, 3   (and 12, 13 over an E4M3 cache) keep non-finite values that not every row sees out of the
 //                products, and turn E4M3 tiles into f16 ones, exactly
-//   warps 4-7    exponentials of the even tiles, one thread per row; warps 8-11 of the odd tiles
+//   warps 4-7    exponentials of the even tiles, one thread per lane; warps 8-11 of the odd tiles
 #include <cuda.h>
 
 #include <algorithm>
@@ -230,8 +237,8 @@ __device__ __forceinline__ void tc_ld32(float (&v)[32], uint32_t addr) {
                  "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]),
                  "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]),
                  "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31]) : "r"(addr));
-  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
 }
+__device__ __forceinline__ void tc_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
 __device__ __forceinline__ void tc_st32(uint32_t addr, const float (&v)[32]) {
   const uint32_t* r = reinterpret_cast<const uint32_t*>(v);
   asm volatile("tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,"
@@ -301,13 +308,14 @@ struct Shape {
   static constexpr int kHalves = D * kBytes / kRowBytes;                  // boxes of a page (128 bytes of each key)
   static constexpr int kCopied = kTileKeys * D * kBytes;                  // a copied tile of keys or of values
   static constexpr int kOperand = kTileKeys * D * 2;                      // a 16-bit one
-  static constexpr int kStages = kE4M3 ? (D == 128 ? 2 : 4) : (D == 128 ? 3 : 5);
-  static constexpr int kBuffers = kE4M3 ? 2 : 0;                          // converted tiles
-  static constexpr int kHelpers = kE4M3 ? 4 : 2;                          // warps 2, 3 (and 12, 13)
+  static constexpr int kSlots = (kE4M3 ? 4 : 6) * (128 / D);              // copied tiles in the ring
+  static constexpr int kBuffers = kE4M3 ? 4 * (128 / D) : 0;              // converted tiles
+  static constexpr int kClean = kE4M3 ? kBuffers : kSlots;                // operands of the products
+  static constexpr int kHelpers = 32 * (kE4M3 ? 4 : 2);                   // threads of warps 2, 3 (and 12, 13)
   static constexpr int kThreads = 32 * (kE4M3 ? 14 : 12);
-  static constexpr int kRowsAt = 0, kStagesAt = kTileRows * D * 2, kBuffersAt = kStagesAt + kStages * 2 * kCopied;
-  static constexpr int kSmall = kBuffersAt + kBuffers * 2 * kOperand;     // barriers and small arrays
-  static constexpr int kSmem = kSmall + 2 * kTileRows * 8 + kTileRows * 4 + 512;
+  static constexpr int kRowsAt = 0, kSlotsAt = kTileRows * D * 2, kBuffersAt = kSlotsAt + kSlots * kCopied;
+  static constexpr int kSmall = kBuffersAt + kBuffers * kOperand;         // small arrays and barriers
+  static constexpr int kSmem = kSmall + 2 * kTileRows * 8 + kTileRows * 4 + (D == 128 ? 512 : 1024);
   // tensor memory columns of a stream: scores (the probabilities take their first half when D = 128), output
   static constexpr int kOut = 128, kProb = D == 128 ? 0 : 192, kStream = 256;
 
@@ -322,20 +330,28 @@ struct Shape {
   }
 };
 
+// Place of the keys and of the values of tile i in the order K0 K1 V0 K2 V1 K3 ... of an item of `count` tiles.
+__device__ __forceinline__ int keys_unit(int i) { return i < 2 ? i : 2 * i - 1; }
+__device__ __forceinline__ int values_unit(int i, int count) { return min(2 * i + 2, 2 * count - 1); }
+__device__ __forceinline__ bool is_keys(int unit, int count) {
+  return unit == 0 || (unit < 2 ? count > 1 : (unit & 1) && (unit + 1) / 2 < count);
+}
+
 // Barriers and small arrays of a block.
 struct Small {
-  uint32_t full, empty, clean;     // per stage: copied; free again; values fit for the product (or converted, per buffer)
-  uint32_t buffer_free;            // per buffer: the products with a converted tile are done
+  uint32_t full, empty;            // per slot: copied; free again
+  uint32_t clean, buffer_free;     // per operand: fit for the product; (converted ones) free again
   uint32_t rows_ready, rows_free;  // the item's rows are in shared memory; its last score product is done
   uint32_t scores, probs, output;  // per stream: scores; probabilities; output of a tile complete
   uint32_t end;
-  uint32_t* bad_pages;             // per stage: pages of the tile that lie outside the cache
-  uint32_t* tile_bad;              // the same per stage or buffer, for the exponentials
-  uint32_t (*odd)[4];              // per stage or buffer: keys with non-finite values (taken out)
+  uint32_t* bad_pages;             // per slot: pages of the tile that lie outside the cache
+  uint32_t* tile_bad;              // the same per operand, and then (last two) of the tile in each stream
+  uint32_t (*odd)[4];              // per operand: keys with non-finite values (taken out)
   volatile int* dead;
   uint32_t* tmem;
-  float2* ml;                      // [2][128] (c m, sum) of the streams' rows
-  float* row_c;                    // [128] c of the rows
+  float2* ml;                      // [2][128] (c m, sum) of the streams' lanes
+  float* row_c;                    // [128] c of the lanes (item's start)
+  float2* joined;                  // [64] (c m, sum) of joined lanes (item's end), in the same place
 };
 
 // Visibility of 32 keys from `key` on (bit j: key + j) for a row with node mask `bits`.
@@ -353,6 +369,123 @@ __device__ __forceinline__ uint32_t on_pages32(uint32_t bad, int in_tile, int pa
   return v;
 }
 
+// What a thread of the exponentials keeps of its lane over an item.
+struct Lane {
+  float c, mc, l;                  // c; base of the exponents (less kShift); sum
+  uint64_t bits;                   // nodes the row sees
+  int row, head;                   // of q, out and lse
+  bool valid;
+};
+
+// Exponentials of one tile for a lane: kCols keys from key0 on (the share of the lane's copy). The tile holds keys
+// that not every row sees unless `all`. Scores lie in the columns from `scores` on, probabilities go to `probs`
+// (two to a column), the output so far is in `out`.
+template <typename T, bool kE4M3, int D, int kCols>
+__device__ __forceinline__ void exponentials(const AttnParams& p, Lane& w, uint32_t scores, uint32_t probs, uint32_t out, int key0,
+                                             int tile_key, const Request& r, int b, int h, bool all, uint32_t bad, const uint32_t* odd) {
+  using S = Shape<T, kE4M3, D>;
+  using M = Mma<typename S::C>;
+  constexpr int kHeld = kCols == 64 ? 64 : 32;                  // scores held in registers at a time
+  float v[kHeld / 32][32];
+  uint32_t see[kCols / 32];
+#pragma unroll
+  for (int j = 0; j < kCols / 32; ++j) {
+    see[j] = ~0u;
+    if (!all) see[j] = visible32(w.bits, tile_key + key0 + 32 * j, r.ctx) & on_pages32(bad, key0 + 32 * j, p.page_shift);
+  }
+  auto load = [&](int at) {
+#pragma unroll
+    for (int j = 0; j < kHeld / 32; ++j) tc_ld32(v[j], scores + key0 + at + 32 * j);
+    tc_wait_ld();
+    if (!all)
+#pragma unroll
+      for (int j = 0; j < kHeld / 32; ++j)
+#pragma unroll
+        for (int e = 0; e < 32; ++e) v[j][e] = see[at / 32 + j] >> e & 1 ? v[j][e] : -INFINITY;
+  };
+  float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+  for (int at = kCols - kHeld; at >= 0; at -= kHeld) {          // the first part is held when the maximum is known
+    load(at);
+#pragma unroll
+    for (int j = 0; j < kHeld / 32; ++j)
+#pragma unroll
+      for (int e = 0; e < 32; ++e) top[e & 3] = fmaxf(top[e & 3], v[j][e]);
+  }
+  const float most = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
+  const float now = most == -INFINITY ? -INFINITY : fmaf(most, w.c, -M::kShift);
+  const bool grown = w.valid && now > w.mc + kSlack;            // also from -inf
+  if (__any_sync(0xffffffffu, grown)) {
+    const float f = grown ? (w.mc == -INFINITY ? 0.f : exp2_fast(w.mc - now)) : 1.f;
+    if (__any_sync(0xffffffffu, grown && w.l != 0.f)) {
+#pragma unroll 1
+      for (int i = 0; i < D; i += 32) {
+        float o[32];
+        tc_ld32(o, out + i);
+        tc_wait_ld();
+#pragma unroll
+        for (int e = 0; e < 32; ++e) o[e] *= f;
+        tc_st32(out + i, o);
+      }
+    }
+    w.l *= f;
+    if (grown) w.mc = now;
+  }
+  const float from = w.mc == -INFINITY ? 0.f : w.mc;
+  if constexpr (kCols < kTileKeys) {
+    const uint32_t none[16] = {0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0};
+#pragma unroll
+    for (int j = 0; j < kTileKeys; j += 32)
+      if (j < key0 || j >= key0 + kCols) tc_st16(probs + j / 2, none);
+  }
+#pragma unroll
+  for (int at = 0; at < kCols; at += kHeld) {
+    if (at > 0) load(at);
+#pragma unroll
+    for (int j = 0; j < kHeld / 32; ++j) {
+      float sum[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int e = 0; e < 32; ++e) {
+        v[j][e] = exp2_fast(fmaf(v[j][e], w.c, -from));
+        sum[e & 3] += v[j][e];
+      }
+      w.l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+      uint32_t packed[16];
+#pragma unroll
+      for (int e = 0; e < 16; ++e) packed[e] = M::pack(v[j][2 * e], v[j][2 * e + 1]);
+      tc_st16(probs + (key0 + at + 32 * j) / 2, packed);
+      if (!all) {
+        // rare: keys with values that are NaN or infinite; the rows that see one add them themselves
+        for (uint32_t left = odd[(key0 + at) / 32 + j]; left; left &= left - 1) {
+          const int k = __ffs(left) - 1, key = tile_key + key0 + at + 32 * j + k;
+          float pk = 0.f;
+#pragma unroll
+          for (int e = 0; e < 32; ++e) pk = e == k ? v[j][e] : pk;
+          const bool seen = w.valid && (see[at / 32 + j] >> k & 1);
+          const int64_t page = p.block_table[(size_t)b * p.max_pages + (key >> p.page_shift)];
+          const int64_t src = page * p.page_stride + (((int64_t)h << p.page_shift) + (key & ((1 << p.page_shift) - 1))) * D;
+#pragma unroll 1
+          for (int i = 0; i < D; i += 32) {
+            float o[32];
+            tc_wait_st();
+            tc_ld32(o, out + i);
+            tc_wait_ld();
+#pragma unroll
+            for (int e = 0; e < 32; ++e) {
+              float x;
+              if constexpr (kE4M3) x = __half2float(__ushort_as_half((unsigned short)e4m3x2_to_f16x2(static_cast<const uint8_t*>(p.v)[src + i + e])));
+              else x = Elem<T>::to_float(static_cast<const T*>(p.v)[src + i + e]);
+              if (seen && !isfinite(x)) o[e] += pk * x;
+            }
+            tc_st32(out + i, o);
+          }
+        }
+      }
+    }
+  }
+  tc_wait_st();
+}
+
 template <typename T, bool kE4M3, int D>
 __global__ void __launch_bounds__(Shape<T, kE4M3, D>::kThreads, 1)
 tree_attention_kernel(const AttnParams p, const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap) {
@@ -361,17 +494,17 @@ tree_attention_kernel(const AttnParams p, const __grid_constant__ CUtensorMap km
   extern __shared__ __align__(1024) uint8_t smem[];
   const uint32_t base = smem_u32(smem);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  constexpr int kClean = kE4M3 ? S::kBuffers : S::kStages;
   Small sm;
   {
     uint8_t* at = smem + S::kSmall;
     sm.ml = reinterpret_cast<float2*>(at);
     sm.row_c = reinterpret_cast<float*>(sm.ml + 2 * kTileRows);
+    sm.joined = reinterpret_cast<float2*>(sm.row_c);
     uint32_t bar = smem_u32(sm.row_c + kTileRows);
     auto take = [&](int n) { const uint32_t r = bar; bar += 8 * n; return r; };
-    sm.full = take(S::kStages);
-    sm.empty = take(S::kStages);
-    sm.clean = take(kClean);
+    sm.full = take(S::kSlots);
+    sm.empty = take(S::kSlots);
+    sm.clean = take(S::kClean);
     sm.buffer_free = take(S::kBuffers);
     sm.rows_ready = take(1);
     sm.rows_free = take(1);
@@ -381,10 +514,10 @@ tree_attention_kernel(const AttnParams p, const __grid_constant__ CUtensorMap km
     sm.end = take(1);
     uint32_t* word = reinterpret_cast<uint32_t*>(smem + (bar - base));
     sm.odd = reinterpret_cast<uint32_t (*)[4]>(word);
-    sm.bad_pages = word + 4 * kClean;
-    sm.tile_bad = sm.bad_pages + S::kStages;
-    sm.dead = reinterpret_cast<volatile int*>(sm.tile_bad + kClean);
-    sm.tmem = sm.tile_bad + kClean + 1;
+    sm.bad_pages = word + 4 * S::kClean;
+    sm.tile_bad = sm.bad_pages + S::kSlots;
+    sm.dead = reinterpret_cast<volatile int*>(sm.tile_bad + S::kClean + 2);
+    sm.tmem = sm.tile_bad + S::kClean + 3;
   }
   if (base & 1023) {                                            // the swizzled tiles need the alignment asked for above
     if (threadIdx.x == 0) raise_status(p.status, MDW_ERR_UNSUPPORTED_SHAPE);
@@ -392,16 +525,16 @@ tree_attention_kernel(const AttnParams p, const __grid_constant__ CUtensorMap km
     return;
   }
   if (threadIdx.x == 0) {
-    for (int i = 0; i < S::kStages; ++i) {
+    for (int i = 0; i < S::kSlots; ++i) {
       mbar_init(sm.full + 8 * i, 1);
-      mbar_init(sm.empty + 8 * i, kE4M3 ? 32 * S::kHelpers : 1);
+      mbar_init(sm.empty + 8 * i, kE4M3 ? S::kHelpers : 1);
     }
-    for (int i = 0; i < kClean; ++i) mbar_init(sm.clean + 8 * i, 32 * S::kHelpers);
+    for (int i = 0; i < S::kClean; ++i) mbar_init(sm.clean + 8 * i, S::kHelpers);
     for (int i = 0; i < S::kBuffers; ++i) mbar_init(sm.buffer_free + 8 * i, 1);
-    mbar_init(sm.rows_ready, 128);
+    mbar_init(sm.rows_ready, kTileRows);
     mbar_init(sm.rows_free, 1);
     for (int i = 0; i < 2; ++i) {
-      mbar_init(sm.scores + 8 * i, 1);
+      mbar_init(sm.scores + 8 * i, 2);
       mbar_init(sm.probs + 8 * i, 4);
       mbar_init(sm.output + 8 * i, 1);
     }
@@ -423,79 +556,81 @@ tree_attention_kernel(const AttnParams p, const __grid_constant__ CUtensorMap km
   const uint32_t tmem = *sm.tmem;
   const uint32_t rows_at = base + S::kRowsAt;
   auto wait = [&](uint32_t bar, uint32_t parity) { mbar_wait(bar, parity, p.spin_budget, p.status, sm.dead); };
-  auto stage_at = [&](int stage) { return base + S::kStagesAt + stage * 2 * S::kCopied; };
-  auto buffer_at = [&](int b) { return base + S::kBuffersAt + b * 2 * S::kOperand; };
+  auto slot_at = [&](int slot) { return base + S::kSlotsAt + slot * S::kCopied; };
+  auto operand_at = [&](int i) { return kE4M3 ? base + S::kBuffersAt + i * S::kOperand : slot_at(i); };
 
   if (warp == 0) {
-    // ---- copies: lane i serves the tile's i-th page, whose number is loaded one tile ahead
-    int stage = 0;
-    uint32_t phase = 0;
+    // ---- copies: lane i serves a tile's i-th page
     const int box_rows = min(1 << p.page_shift, kTileKeys), pages = kTileKeys / box_rows;
     const uint32_t page_bytes = (uint32_t)box_rows * D * S::kBytes;
-    int page = -1, key = 0;
-    bool wanted = false;
-    auto look = [&]() {
-      key = walk.tile * kTileKeys + lane * box_rows;
-      wanted = lane < pages && key < walk.r.keys;
-      if (wanted) page = p.block_table[(size_t)walk.b * p.max_pages + (key >> p.page_shift)];
-    };
-    look();
-    for (;;) {
-      const bool ok = wanted && page >= 0 && page < p.num_pages;
-      const int id = page, row = key & ((1 << p.page_shift) - 1), head = walk.h;
-      const unsigned good = __ballot_sync(0xffffffffu, ok), bad = __ballot_sync(0xffffffffu, wanted && !ok);
-      const bool more = --walk.left > 0;
-      if (more) {
-        if (++walk.tile == walk.tiles) walk.next_item(p, lane);
-        look();
-      }
-      wait(sm.empty + 8 * stage, phase ^ 1);
-      if (__any_sync(0xffffffffu, *sm.dead)) break;
-      const uint32_t bar = sm.full + 8 * stage, kt = stage_at(stage), vt = kt + S::kCopied;
-      if (lane == 0) {
-        sm.bad_pages[stage] = bad;
-        if (bad) raise_status(p.status, MDW_ERR_DEVICE_BOUNDS);
-        mbar_arrive_tx(bar, 2 * page_bytes * __popc(good));
-      }
-      __syncwarp();
-      if (ok) {
-#pragma unroll
-        for (int i = 0; i < S::kHalves; ++i) {
-          const uint32_t off = i * (kTileKeys * S::kRowBytes) + lane * box_rows * S::kRowBytes;
-          tma_load(kt + off, &kmap, bar, i * (S::kRowBytes / S::kBytes), row, head, id);
+    int slot = 0;
+    uint32_t phase = 0;
+    bool lost = false;
+    while (walk.left > 0 && !lost) {
+      const Request r = walk.r;
+      const int tile0 = walk.tile, count = min(walk.tiles - tile0, walk.left), head = walk.h;
+      const int32_t* table = p.block_table + (size_t)walk.b * p.max_pages;
+      auto look = [&](int i) {                                  // page of the lane in tile i; -1: none wanted, -2: outside the cache
+        const int key = (tile0 + i) * kTileKeys + lane * box_rows;
+        if (i >= count || lane >= pages || key >= r.keys) return -1;
+        const int id = table[key >> p.page_shift];
+        return id >= 0 && id < p.num_pages ? id : -2;
+      };
+      // pages of the tile whose values come next and of the two after it
+      int id0 = look(0), id1 = look(1), id2 = look(2);
+      for (int u = 0; u < 2 * count; ++u) {
+        const bool keys = is_keys(u, count);
+        const int id = keys && u > 0 ? id1 : id0, i = keys ? (u + 1) / 2 : (u == 2 * count - 1 ? count - 1 : u / 2 - 1);
+        const unsigned good = __ballot_sync(0xffffffffu, id >= 0), bad = __ballot_sync(0xffffffffu, id == -2);
+        wait(sm.empty + 8 * slot, phase ^ 1);
+        if (__any_sync(0xffffffffu, *sm.dead)) { lost = true; break; }
+        const uint32_t bar = sm.full + 8 * slot, to = slot_at(slot);
+        if (lane == 0) {
+          sm.bad_pages[slot] = bad;
+          if (bad) raise_status(p.status, MDW_ERR_DEVICE_BOUNDS);
+          mbar_arrive_tx(bar, page_bytes * __popc(good));
         }
+        __syncwarp();
+        if (id >= 0) {
+          const int row = ((tile0 + i) * kTileKeys + lane * box_rows) & ((1 << p.page_shift) - 1);
 #pragma unroll
-        for (int i = 0; i < S::kHalves; ++i) {
-          const uint32_t off = i * (kTileKeys * S::kRowBytes) + lane * box_rows * S::kRowBytes;
-          tma_load(vt + off, &vmap, bar, i * (S::kRowBytes / S::kBytes), row, head, id);
+          for (int k = 0; k < S::kHalves; ++k)
+            tma_load(to + k * (kTileKeys * S::kRowBytes) + lane * box_rows * S::kRowBytes, keys ? &kmap : &vmap, bar,
+                     k * (S::kRowBytes / S::kBytes), row, head, id);
+        }
+        if (++slot == S::kSlots) { slot = 0; phase ^= 1; }
+        if (!keys) {
+          id0 = id1;
+          id1 = id2;
+          id2 = look(i + 3);
         }
       }
-      if (++stage == S::kStages) { stage = 0; phase ^= 1; }
-      if (!more) break;
+      walk.left -= count;
+      if (walk.left > 0) walk.next_item(p, lane);
     }
-    if (__any_sync(0xffffffffu, *sm.dead))
-      for (int i = 0; i < S::kStages; ++i) mbar_drain(sm.full + 8 * i, i < stage ? phase : phase ^ 1);
+    if (lost)
+      for (int i = 0; i < S::kSlots; ++i) mbar_drain(sm.full + 8 * i, i < slot ? phase : phase ^ 1);
   } else if (warp == 1) {
     // ---- products. Scores of the first two tiles of an item, then in turn the output of tile i and the scores
     // of tile i + 2, whose columns hold the probabilities that output reads.
-    constexpr int kSlots = kE4M3 ? S::kBuffers : S::kStages;    // where operands lie
-    int n = 0, items = 0, done[2] = {0, 0};                     // tiles before this item; items; outputs of each stream
+    int unit0 = 0, items = 0, done[2] = {0, 0};                 // units before this item; items; outputs of each stream
     while (walk.left > 0) {
       const int count = min(walk.tiles - walk.tile, walk.left);
       auto scores = [&](int i) {
-        const int at = (n + i) % kSlots, s = i & 1;
-        const uint32_t parity = ((n + i) / kSlots) & 1;
-        wait(kE4M3 ? sm.clean + 8 * at : sm.full + 8 * at, parity);
+        const int unit = unit0 + keys_unit(i), at = unit % S::kClean, s = i & 1;
+        wait((kE4M3 ? sm.clean : sm.full) + 8 * at, unit / S::kClean & 1);
         if (lane == 0) {
           tc_fence_after();
-          const uint32_t kt = kE4M3 ? buffer_at(at) : stage_at(at);
 #pragma unroll
           for (int t = 0; t < D / 16; ++t) {
             const uint32_t off = (t >> 2) * (128 * 128) + (t & 3) * 32;
-            tc_mma(tmem + s * S::kStream, smem_operand(rows_at + off, 16, 1024), smem_operand(kt + off, 16, 1024),
+            tc_mma(tmem + s * S::kStream, smem_operand(rows_at + off, 16, 1024), smem_operand(operand_at(at) + off, 16, 1024),
                    mma_shape(M::kBf16, false, kTileKeys), t > 0);
           }
           tc_commit(sm.scores + 8 * s);
+          sm.tile_bad[S::kClean + s] = kE4M3 ? sm.tile_bad[at] : sm.bad_pages[at];
+          mbar_arrive(sm.scores + 8 * s);
+          tc_commit((kE4M3 ? sm.buffer_free : sm.empty) + 8 * at);
           if (i == count - 1) tc_commit(sm.rows_free);
         }
         __syncwarp();
@@ -504,18 +639,17 @@ tree_attention_kernel(const AttnParams p, const __grid_constant__ CUtensorMap km
       scores(0);
       if (count > 1) scores(1);
       for (int i = 0; i < count; ++i) {
-        const int at = (n + i) % kSlots, s = i & 1;
-        if (!kE4M3) wait(sm.clean + 8 * at, ((n + i) / kSlots) & 1);
+        const int unit = unit0 + values_unit(i, count), at = unit % S::kClean, s = i & 1;
+        wait(sm.clean + 8 * at, unit / S::kClean & 1);
         wait(sm.probs + 8 * s, done[s] & 1);
         if (lane == 0) {
           tc_fence_after();
-          const uint32_t vt = kE4M3 ? buffer_at(at) + S::kOperand : stage_at(at) + S::kCopied;
 #pragma unroll
           for (int t = 0; t < kTileKeys / 16; ++t)
             tc_mma_tmem(tmem + s * S::kStream + S::kOut, tmem + s * S::kStream + S::kProb + 8 * t,
-                        smem_operand(vt + t * 2048, 128 * 128, 1024), mma_shape(M::kBf16, true, D));
+                        smem_operand(operand_at(at) + t * 2048, 128 * 128, 1024), mma_shape(M::kBf16, true, D));
           tc_commit(sm.output + 8 * s);
-          tc_commit(kE4M3 ? sm.buffer_free + 8 * at : sm.empty + 8 * at);
+          tc_commit((kE4M3 ? sm.buffer_free : sm.empty) + 8 * at);
         }
         __syncwarp();
         if (i + 2 < count) {
@@ -524,7 +658,7 @@ tree_attention_kernel(const AttnParams p, const __grid_constant__ CUtensorMap km
         }
         ++done[s];
       }
-      n += count;
+      unit0 += 2 * count;
       ++items;
       walk.left -= count;
       if (walk.left > 0) walk.next_item(p, lane);
@@ -536,92 +670,100 @@ tree_attention_kernel(const AttnParams p, const __grid_constant__ CUtensorMap km
     // ---- values: in a tile that not every row sees as a whole, non-finite values are taken out and noted per
     // key (the rows that see them add them); E4M3 tiles are converted
     const int id = (warp < 4 ? warp - 2 : warp - 10) * 32 + lane;
-    constexpr int kAll = 32 * S::kHelpers;
-    int stage = 0, n = 0;
-    uint32_t phase = 0;
+    int slot = 0, buffer = 0;
+    uint32_t phase = 0, buffer_phase = 0;
     while (walk.left > 0) {
       const Request r = walk.r;
-      const int tile_key = walk.tile * kTileKeys;
-      wait(sm.full + 8 * stage, phase);
-      const uint32_t bad = sm.bad_pages[stage];
-      const bool all = tile_key + kTileKeys <= r.ctx && bad == 0;
-      const int b = kE4M3 ? n % 2 : stage;
-      const uint32_t kt = stage_at(stage), vt = kt + S::kCopied;
-      if constexpr (kE4M3) wait(sm.buffer_free + 8 * b, (n / 2 & 1) ^ 1);
-      if (id == 0) sm.tile_bad[b] = bad;
-      if (!all) {
-        if (id < 4) sm.odd[b][id] = 0;
-        asm volatile("bar.sync 2, %0;" :: "n"(kAll) : "memory");
-      }
-      auto note = [&](uint32_t non, int key) {
-        if (non && tile_key + key < r.keys && !(bad >> (key >> p.page_shift) & 1)) atomicOr(&sm.odd[b][key >> 5], 1u << (key & 31));
-      };
-      if constexpr (!kE4M3) {
-        if (!all)
-          for (int i = id; i < kTileKeys * (D / 8); i += kAll) {
-            const int key = i / (D / 8);
-            const uint32_t at = S::copied(vt, key, i % (D / 8));
-            const uint4 v = lds16(at);
-            const uint32_t e = M::kExponent;
-            const uint4 non = make_uint4(__vcmpeq2(v.x & e, e), __vcmpeq2(v.y & e, e), __vcmpeq2(v.z & e, e), __vcmpeq2(v.w & e, e));
-            if (non.x | non.y | non.z | non.w) {
-              sts16(at, make_uint4(v.x & ~non.x, v.y & ~non.y, v.z & ~non.z, v.w & ~non.w));
-              note(1u, key);
-            }
-          }
-      } else {
-        const uint32_t to = buffer_at(b);
-        for (int i = id; i < 2 * kTileKeys * (D / 16); i += kAll) {
-          const int part = i / (kTileKeys * (D / 16)), key = i / (D / 16) % kTileKeys, piece = i % (D / 16);
-          uint4 v = lds16(S::copied(part ? vt : kt, key, piece));
-          if (part && !all) {
-            // the only non-finite code is S.1111.111
-            const uint32_t m = 0x7f7f7f7fu;
-            const uint4 non = make_uint4(__vcmpeq4(v.x & m, m), __vcmpeq4(v.y & m, m), __vcmpeq4(v.z & m, m), __vcmpeq4(v.w & m, m));
-            note(non.x | non.y | non.z | non.w, key);
-            v = make_uint4(v.x & ~non.x, v.y & ~non.y, v.z & ~non.z, v.w & ~non.w);
-          }
-          const uint32_t at = to + part * S::kOperand;
-          sts16(S::operand(at, key, 2 * piece), make_uint4(e4m3x2_to_f16x2(v.x & 0xffffu), e4m3x2_to_f16x2(v.x >> 16),
-                                                           e4m3x2_to_f16x2(v.y & 0xffffu), e4m3x2_to_f16x2(v.y >> 16)));
-          sts16(S::operand(at, key, 2 * piece + 1), make_uint4(e4m3x2_to_f16x2(v.z & 0xffffu), e4m3x2_to_f16x2(v.z >> 16),
-                                                               e4m3x2_to_f16x2(v.w & 0xffffu), e4m3x2_to_f16x2(v.w >> 16)));
+      const int tile0 = walk.tile, count = min(walk.tiles - tile0, walk.left);
+      for (int u = 0; u < 2 * count; ++u) {
+        const bool keys = is_keys(u, count);
+        const int i = keys ? (u + 1) / 2 : (u == 2 * count - 1 ? count - 1 : u / 2 - 1), tile_key = (tile0 + i) * kTileKeys;
+        wait(sm.full + 8 * slot, phase);
+        const uint32_t bad = sm.bad_pages[slot], from = slot_at(slot);
+        const int b = kE4M3 ? buffer : slot;
+        const bool all = keys || (tile_key + kTileKeys <= r.ctx && bad == 0);
+        if constexpr (kE4M3) wait(sm.buffer_free + 8 * b, buffer_phase ^ 1);
+        if (id == 0) sm.tile_bad[b] = bad;
+        if (!all) {
+          if (id < 4) sm.odd[b][id] = 0;
+          asm volatile("bar.sync 2, %0;" :: "n"(S::kHelpers) : "memory");
         }
-        mbar_arrive(sm.empty + 8 * stage);
+        auto note = [&](uint32_t non, int key) {
+          if (non && tile_key + key < r.keys && !(bad >> (key >> p.page_shift) & 1)) atomicOr(&sm.odd[b][key >> 5], 1u << (key & 31));
+        };
+        if constexpr (!kE4M3) {
+          if (!all)
+            for (int j = id; j < kTileKeys * (D / 8); j += S::kHelpers) {
+              const int key = j / (D / 8);
+              const uint32_t at = S::copied(from, key, j % (D / 8));
+              const uint4 v = lds16(at);
+              const uint32_t e = M::kExponent;
+              const uint4 non = make_uint4(__vcmpeq2(v.x & e, e), __vcmpeq2(v.y & e, e), __vcmpeq2(v.z & e, e), __vcmpeq2(v.w & e, e));
+              if (non.x | non.y | non.z | non.w) {
+                sts16(at, make_uint4(v.x & ~non.x, v.y & ~non.y, v.z & ~non.z, v.w & ~non.w));
+                note(1u, key);
+              }
+            }
+        } else {
+          const uint32_t to = operand_at(b);
+#pragma unroll 4
+          for (int j = id; j < kTileKeys * (D / 16); j += S::kHelpers) {
+            const int key = j / (D / 16), piece = j % (D / 16);
+            uint4 v = lds16(S::copied(from, key, piece));
+            if (!all) {
+              // the only non-finite code is S.1111.111
+              const uint32_t m = 0x7f7f7f7fu;
+              const uint4 non = make_uint4(__vcmpeq4(v.x & m, m), __vcmpeq4(v.y & m, m), __vcmpeq4(v.z & m, m), __vcmpeq4(v.w & m, m));
+              note(non.x | non.y | non.z | non.w, key);
+              v = make_uint4(v.x & ~non.x, v.y & ~non.y, v.z & ~non.z, v.w & ~non.w);
+            }
+            sts16(S::operand(to, key, 2 * piece), make_uint4(e4m3x2_to_f16x2(v.x & 0xffffu), e4m3x2_to_f16x2(v.x >> 16),
+                                                             e4m3x2_to_f16x2(v.y & 0xffffu), e4m3x2_to_f16x2(v.y >> 16)));
+            sts16(S::operand(to, key, 2 * piece + 1), make_uint4(e4m3x2_to_f16x2(v.z & 0xffffu), e4m3x2_to_f16x2(v.z >> 16),
+                                                                 e4m3x2_to_f16x2(v.w & 0xffffu), e4m3x2_to_f16x2(v.w >> 16)));
+          }
+          mbar_arrive(sm.empty + 8 * slot);
+        }
+        if (kE4M3 || !all) fence_async_proxy();
+        mbar_arrive(sm.clean + 8 * b);
+        if (++slot == S::kSlots) { slot = 0; phase ^= 1; }
+        if (kE4M3 && ++buffer == S::kBuffers) { buffer = 0; buffer_phase ^= 1; }
       }
-      fence_async_proxy();
-      mbar_arrive(sm.clean + 8 * b);
-      ++n;
-      if (++stage == S::kStages) { stage = 0; phase ^= 1; }
-      if (--walk.left > 0 && ++walk.tile == walk.tiles) walk.next_item(p, lane);
+      walk.left -= count;
+      if (walk.left > 0) walk.next_item(p, lane);
     }
   } else {
-    // ---- exponentials: thread = row
-    const int s = warp >= 8 ? 1 : 0, row = (warp & 3) * 32 + lane;
+    // ---- exponentials: thread = lane of tensor memory
+    const int s = warp >= 8 ? 1 : 0, at_lane = (warp & 3) * 32 + lane;
     const uint32_t lanes = (uint32_t)(warp & 3) * 32 << 16;
     const uint32_t scores = tmem + s * S::kStream + lanes, probs = scores + S::kProb, out = scores + S::kOut;
-    int n = 0, items = 0, done = 0;                             // tiles before this item; items; tiles of this stream
+    int unit0 = 0, items = 0, done = 0;                         // units before this item; items; tiles of this stream
     while (walk.left > 0) {
       const Request r = walk.r;
       const int first = walk.rb * kTileRows, rows = min(r.rows * p.group - first, kTileRows), h = walk.h;
       const int tile0 = walk.tile, count = min(walk.tiles - tile0, walk.left);
-      const bool whole = count == walk.tiles, valid = row < rows, active = (warp & 3) * 32 < rows;
-      const int flat = first + (valid ? row : 0), node = flat / p.group, head = h * p.group + flat - node * p.group;
-      float c = p.scale * kLog2e * (kE4M3 ? p.k_scale[h] : 1.f);
+      const bool whole = count == walk.tiles;
+      // rows in a copy, the lane's row and the first key of its share of a tile
+      const int per = rows <= 32 ? 32 : (rows <= 64 ? 64 : 128), mine = at_lane & (per - 1), key0 = (at_lane / per) * per;
+      const bool active = (warp & 3) * 32 % per < rows;
+      Lane w;
+      w.valid = mine < rows;
+      const int flat = first + (w.valid ? mine : 0), node = flat / p.group;
+      w.row = r.row0 + node;
+      w.head = h * p.group + flat - node * p.group;
+      w.c = p.scale * kLog2e * (kE4M3 ? p.k_scale[h] : 1.f);
       if (s == 0) {
-        // the item's rows, after the products with the last item's
-        if (items > 0) wait(sm.rows_free, (items - 1) & 1);
-        if (valid) {
-          const T* src = static_cast<const T*>(p.q) + (int64_t)(r.row0 + node) * p.ldq + (int64_t)head * D;
+        if (w.valid) {
+          const T* src = static_cast<const T*>(p.q) + (int64_t)w.row * p.ldq + (int64_t)w.head * D;
           if constexpr (!kE4M3) {
-#pragma unroll 8
-            for (int i = 0; i < D / 8; ++i) sts16(S::operand(rows_at, row, i), *reinterpret_cast<const uint4*>(src + 8 * i));
+#pragma unroll
+            for (int i = 0; i < D / 8; ++i) sts16(S::operand(rows_at, at_lane, i), *reinterpret_cast<const uint4*>(src + 8 * i));
           } else {
             float f = 1.f;
             if constexpr (std::is_same<T, __nv_bfloat16>::value) {
               // bf16 rows enter f16 times a power of two that puts their largest element in [1, 4)
               float top = 0.f;
-#pragma unroll 8
+#pragma unroll
               for (int i = 0; i < D / 8; ++i) {
                 T x[8];
                 const uint4 v = *reinterpret_cast<const uint4*>(src + 8 * i);
@@ -631,184 +773,144 @@ tree_attention_kernel(const AttnParams p, const __grid_constant__ CUtensorMap km
               }
               const int ex = top > 0.f && isfinite(top) ? min((int)(__float_as_uint(top) >> 23) - 127, 126) : 0;
               f = __uint_as_float((uint32_t)(127 - ex) << 23);
-              c *= ex >= -126 ? __uint_as_float((uint32_t)(127 + ex) << 23) : 5.877471754111438e-39f;
+              w.c *= ex >= -126 ? __uint_as_float((uint32_t)(127 + ex) << 23) : 5.877471754111438e-39f;
             }
-#pragma unroll 8
+#pragma unroll
             for (int i = 0; i < D / 8; ++i) {
               T x[8];
               uint4 v = *reinterpret_cast<const uint4*>(src + 8 * i);
               memcpy(x, &v, 16);
-              uint32_t* w = reinterpret_cast<uint32_t*>(&v);
-#pragma unroll
-              for (int e = 0; e < 4; ++e) w[e] = M::pack(Elem<T>::to_float(x[2 * e]) * f, Elem<T>::to_float(x[2 * e + 1]) * f);
-              sts16(S::operand(rows_at, row, i), v);
+              v = make_uint4(M::pack(Elem<T>::to_float(x[0]) * f, Elem<T>::to_float(x[1]) * f), M::pack(Elem<T>::to_float(x[2]) * f, Elem<T>::to_float(x[3]) * f),
+                             M::pack(Elem<T>::to_float(x[4]) * f, Elem<T>::to_float(x[5]) * f), M::pack(Elem<T>::to_float(x[6]) * f, Elem<T>::to_float(x[7]) * f));
+              sts16(S::operand(rows_at, at_lane, i), v);
             }
           }
         }
-        if (kE4M3) sm.row_c[row] = c;
+        if (kE4M3) sm.row_c[at_lane] = w.c;
         fence_async_proxy();
         mbar_arrive(sm.rows_ready);
       }
-      uint64_t bits = 0;
-      if (valid) {
-        bits = p.tree_mask ? p.tree_mask[r.row0 + node] : ~0ull >> (63 - (flat / p.group));
-        if (r.rows < 64) bits &= (1ull << r.rows) - 1;
+      w.bits = 0;
+      if (w.valid) {
+        w.bits = p.tree_mask ? p.tree_mask[w.row] : ~0ull >> (63 - node);
+        if (r.rows < 64) w.bits &= (1ull << r.rows) - 1;
       }
-      float mc = -INFINITY, l = 0.f;                            // base of the exponents (less kShift), sum
-      float v[32];
+      w.mc = -INFINITY;
+      w.l = 0.f;
       if (active) {
+        float zero[32];
 #pragma unroll
-        for (int j = 0; j < 32; ++j) v[j] = 0.f;
+        for (int e = 0; e < 32; ++e) zero[e] = 0.f;
 #pragma unroll
-        for (int i = 0; i < D; i += 32) tc_st32(out + i, v);
+        for (int i = 0; i < D; i += 32) tc_st32(out + i, zero);
         tc_wait_st();
       }
       if (kE4M3) {
         asm volatile("bar.sync 1, 256;" ::: "memory");
-        c = sm.row_c[row];
+        w.c = sm.row_c[at_lane];
       }
       for (int i = s; i < count; i += 2) {
-        const int at = (n + i) % kClean, tile_key = (tile0 + i) * kTileKeys;
-        wait(sm.clean + 8 * at, ((n + i) / kClean) & 1);
+        const int tile_key = (tile0 + i) * kTileKeys;
         wait(sm.scores + 8 * s, done & 1);
+        const uint32_t bad = sm.tile_bad[S::kClean + s];
+        const bool all = tile_key + kTileKeys <= r.ctx && bad == 0;
+        const int value = unit0 + values_unit(i, count);
+        if (!all) wait(sm.clean + 8 * (value % S::kClean), value / S::kClean & 1);
         __syncwarp();
         if (active) {
           tc_fence_after();
-          const uint32_t bad = sm.tile_bad[at];
-          const bool all = tile_key + kTileKeys <= r.ctx && bad == 0;
-          uint32_t see[4] = {~0u, ~0u, ~0u, ~0u};
-          if (!all)
-#pragma unroll
-            for (int j = 0; j < 4; ++j) see[j] = visible32(bits, tile_key + 32 * j, r.ctx) & on_pages32(bad, 32 * j, p.page_shift);
-          float top = -INFINITY;
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            tc_ld32(v, scores + 32 * j);
-            if (!all)
-#pragma unroll
-              for (int e = 0; e < 32; ++e) v[e] = see[j] >> e & 1 ? v[e] : -INFINITY;
-#pragma unroll
-            for (int e = 0; e < 32; ++e) top = fmaxf(top, v[e]);
-          }
-          const float now = top == -INFINITY ? -INFINITY : fmaf(top, c, -M::kShift);
-          const bool grown = valid && now > mc + kSlack;        // also from -inf
-          if (__any_sync(0xffffffffu, grown)) {
-            const float f = grown ? (mc == -INFINITY ? 0.f : exp2_fast(mc - now)) : 1.f;
-            if (__any_sync(0xffffffffu, grown && l != 0.f)) {
-#pragma unroll 1
-              for (int i2 = 0; i2 < D; i2 += 32) {
-                tc_ld32(v, out + i2);
-#pragma unroll
-                for (int e = 0; e < 32; ++e) v[e] *= f;
-                tc_st32(out + i2, v);
-              }
-              tc_wait_st();
-            }
-            l *= f;
-            if (grown) mc = now;
-          }
-          const float from = mc == -INFINITY ? 0.f : mc;
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            tc_ld32(v, scores + 32 * j);
-            if (!all)
-#pragma unroll
-              for (int e = 0; e < 32; ++e) v[e] = see[j] >> e & 1 ? v[e] : -INFINITY;
-            float sum[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-            for (int e = 0; e < 32; ++e) {
-              v[e] = exp2_fast(fmaf(v[e], c, -from));
-              sum[e & 3] += v[e];
-            }
-            l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
-            uint32_t packed[16];
-#pragma unroll
-            for (int e = 0; e < 16; ++e) packed[e] = M::pack(v[2 * e], v[2 * e + 1]);
-            tc_st16(probs + 16 * j, packed);
-            if (!all) {
-              // rare: keys with values that are NaN or infinite; the rows that see one add them themselves
-              for (uint32_t odd = sm.odd[at][j]; odd; odd &= odd - 1) {
-                const int k = __ffs(odd) - 1, key = tile_key + 32 * j + k;
-                float pk = 0.f;
-#pragma unroll
-                for (int e = 0; e < 32; ++e) pk = e == k ? v[e] : pk;
-                const bool seen = valid && (see[j] >> k & 1);
-                const int64_t page = p.block_table[(size_t)walk.b * p.max_pages + (key >> p.page_shift)];
-                const int64_t src = page * p.page_stride + (((int64_t)h << p.page_shift) + (key & ((1 << p.page_shift) - 1))) * D;
-                tc_wait_st();
-#pragma unroll 1
-                for (int i2 = 0; i2 < D; i2 += 32) {
-                  float o[32];
-                  tc_ld32(o, out + i2);
-#pragma unroll
-                  for (int e = 0; e < 32; ++e) {
-                    float x;
-                    if constexpr (kE4M3) x = __half2float(__ushort_as_half((unsigned short)e4m3x2_to_f16x2(static_cast<const uint8_t*>(p.v)[src + i2 + e])));
-                    else x = Elem<T>::to_float(static_cast<const T*>(p.v)[src + i2 + e]);
-                    if (seen && !isfinite(x)) o[e] += pk * x;
-                  }
-                  tc_st32(out + i2, o);
-                }
-              }
-            }
-          }
-          tc_wait_st();
+          const uint32_t* odd = sm.odd[value % S::kClean];
+          if (per == 32) exponentials<T, kE4M3, D, 32>(p, w, scores, probs, out, key0, tile_key, r, walk.b, h, all, bad, odd);
+          else if (per == 64) exponentials<T, kE4M3, D, 64>(p, w, scores, probs, out, key0, tile_key, r, walk.b, h, all, bad, odd);
+          else exponentials<T, kE4M3, D, 128>(p, w, scores, probs, out, key0, tile_key, r, walk.b, h, all, bad, odd);
           tc_fence_before();
         }
         ++done;
         __syncwarp();
         if (lane == 0) mbar_arrive(sm.probs + 8 * s);
       }
-      // ---- the two streams' sums, each half of the columns by one of them
+
+      // ---- the item's result: the two streams of a lane (this thread takes half of the columns), then the copies
+      // of a row, whose sums pass through the place of the rows
+      constexpr int kHalf = D / 2;
       if (count > s) wait(sm.output + 8 * s, (done - 1) & 1);
+      wait(sm.rows_free, items & 1);
       __syncwarp();
       tc_fence_after();
-      sm.ml[s * kTileRows + row] = make_float2(mc, l);
+      sm.ml[s * kTileRows + at_lane] = make_float2(w.mc, w.l);
       tc_fence_before();
       asm volatile("bar.sync 1, 256;" ::: "memory");
       tc_fence_after();
-      if (active && !*sm.dead) {
-        const float2 a = sm.ml[row], b = sm.ml[kTileRows + row];
-        const float m = fmaxf(a.x, b.x), from = m == -INFINITY ? 0.f : m;
-        float fa = exp2_fast(a.x - from), fb = exp2_fast(b.x - from);
-        const float sum = a.y * fa + b.y * fb;
+      float m = -INFINITY, sum = 0.f, o[kHalf];
+      if (active) {
+        const float2 a = sm.ml[at_lane], b = sm.ml[kTileRows + at_lane];
+        m = fmaxf(a.x, b.x);
+        const float from = m == -INFINITY ? 0.f : m, fa = exp2_fast(a.x - from), fb = exp2_fast(b.x - from);
+        sum = a.y * fa + b.y * fb;
+#pragma unroll
+        for (int i = 0; i < kHalf; i += 32) {
+          float x[32];
+          tc_ld32(x, tmem + lanes + S::kOut + s * kHalf + i);
+          tc_wait_ld();
+#pragma unroll
+          for (int e = 0; e < 32; ++e) o[i + e] = fa * x[e];
+          tc_ld32(x, tmem + lanes + S::kStream + S::kOut + s * kHalf + i);
+          tc_wait_ld();
+#pragma unroll
+          for (int e = 0; e < 32; ++e) o[i + e] = fmaf(fb, x[e], o[i + e]);
+        }
+      }
+      for (int half = 64; half >= per; half >>= 1) {
+        // columns 4 c .. 4 c + 3 of lane x at (c * half + x) * 16 bytes
+        const uint32_t place = rows_at + (s * (kHalf / 4) * half + (at_lane & (half - 1))) * 16;
+        if (at_lane >= half && at_lane < 2 * half) {
+          if (s == 0) sm.joined[at_lane - half] = make_float2(m, sum);
+#pragma unroll
+          for (int i = 0; i < kHalf; i += 4)
+            sts16(place + i / 4 * half * 16, make_uint4(__float_as_uint(o[i]), __float_as_uint(o[i + 1]), __float_as_uint(o[i + 2]), __float_as_uint(o[i + 3])));
+        }
+        asm volatile("bar.sync 1, 256;" ::: "memory");
+        if (at_lane < half) {
+          const float2 a = sm.joined[at_lane];
+          const float both = fmaxf(m, a.x), from = both == -INFINITY ? 0.f : both, f0 = exp2_fast(m - from), f1 = exp2_fast(a.x - from);
+          m = both;
+          sum = sum * f0 + a.y * f1;
+#pragma unroll
+          for (int i = 0; i < kHalf; i += 4) {
+            const uint4 v = lds16(place + i / 4 * half * 16);
+            o[i] = o[i] * f0 + __uint_as_float(v.x) * f1;
+            o[i + 1] = o[i + 1] * f0 + __uint_as_float(v.y) * f1;
+            o[i + 2] = o[i + 2] * f0 + __uint_as_float(v.z) * f1;
+            o[i + 3] = o[i + 3] * f0 + __uint_as_float(v.w) * f1;
+          }
+        }
+        asm volatile("bar.sync 1, 256;" ::: "memory");
+      }
+      if (at_lane < per && w.valid && !*sm.dead) {
         const int slot = 2 * blockIdx.x + (tile0 > 0 ? 0 : 1);
         if (whole) {
           const float f = sum == 0.f ? 0.f : (kE4M3 ? p.v_scale[h] : 1.f) / sum;
-          fa *= f;
-          fb *= f;
-        }
-#pragma unroll 1
-        for (int i = s * (D / 2); i < (s + 1) * (D / 2); i += 32) {
-          float w[32];
-          tc_ld32(v, tmem + lanes + S::kOut + i);
-          tc_ld32(w, tmem + lanes + S::kStream + S::kOut + i);
+          T* dst = static_cast<T*>(p.out) + (int64_t)w.row * p.ldo + (int64_t)w.head * D + s * kHalf;
 #pragma unroll
-          for (int e = 0; e < 32; ++e) v[e] = fa * v[e] + fb * w[e];
-          if (valid && whole) {
-            T* dst = static_cast<T*>(p.out) + (int64_t)(r.row0 + node) * p.ldo + (int64_t)head * D + i;
-#pragma unroll
-            for (int e = 0; e < 32; e += 8)
-              *reinterpret_cast<uint4*>(dst + e) =
-                  sum == 0.f ? make_uint4(0u, 0u, 0u, 0u)
-                             : make_uint4(Mma<T>::pack(v[e], v[e + 1]), Mma<T>::pack(v[e + 2], v[e + 3]),
-                                          Mma<T>::pack(v[e + 4], v[e + 5]), Mma<T>::pack(v[e + 6], v[e + 7]));
-          } else if (valid) {
-            float* dst = p.part_o + ((size_t)slot * kTileRows + row) * D + i;
-#pragma unroll
-            for (int e = 0; e < 32; e += 4) *reinterpret_cast<float4*>(dst + e) = make_float4(v[e], v[e + 1], v[e + 2], v[e + 3]);
+          for (int i = 0; i < kHalf; i += 8) {
+            uint4 v = make_uint4(0u, 0u, 0u, 0u);
+            if (sum != 0.f)
+              v = make_uint4(Mma<T>::pack(o[i] * f, o[i + 1] * f), Mma<T>::pack(o[i + 2] * f, o[i + 3] * f),
+                             Mma<T>::pack(o[i + 4] * f, o[i + 5] * f), Mma<T>::pack(o[i + 6] * f, o[i + 7] * f));
+            *reinterpret_cast<uint4*>(dst + i) = v;
           }
-          __syncwarp();                                         // the loads above are the whole warp's
-        }
-        if (s == 0 && valid) {
-          if (!whole) p.part_ml[(size_t)slot * kTileRows + row] = make_float2(m, sum);
-          else if (p.lse) p.lse[(int64_t)(r.row0 + node) * p.Hq + head] = sum == 0.f ? -INFINITY : (m + log2f(sum)) * kLn2;
+          if (s == 0 && p.lse) p.lse[(int64_t)w.row * p.Hq + w.head] = sum == 0.f ? -INFINITY : (m + log2f(sum)) * kLn2;
+        } else {
+          float* dst = p.part_o + ((size_t)slot * kTileRows + mine) * D + s * kHalf;
+#pragma unroll
+          for (int i = 0; i < kHalf; i += 4) *reinterpret_cast<float4*>(dst + i) = make_float4(o[i], o[i + 1], o[i + 2], o[i + 3]);
+          if (s == 0) p.part_ml[(size_t)slot * kTileRows + mine] = make_float2(m, sum);
         }
       }
       tc_fence_before();
-      asm volatile("bar.sync 1, 256;" ::: "memory");
+      asm volatile("bar.sync 1, 256;" ::: "memory");            // outputs and sums are read; the next item may begin
       tc_fence_after();
-      n += count;
+      unit0 += 2 * count;
       ++items;
       walk.left -= count;
       if (walk.left > 0) walk.next_item(p, lane);
