@@ -26,8 +26,8 @@
 // free them (K0 K1 V0 K2 V1 K3 ...), and a tile is held only while its product runs. The roles of a block:
 //   warp 0       requests the tiles by TMA (a box per page, head and 128 bytes of a row, swizzled)
 //   warp 1       issues the matrix products
-//   warps 2, 3   (and 12, 13 over an E4M3 cache) keep non-finite values that not every row sees out of the
-//                products, and turn E4M3 tiles into f16 ones, exactly
+//   warps 2, 3   keep non-finite values that not every row sees out of the products, and turn E4M3 tiles into
+//                f16 ones, exactly
 //   warps 4-7    exponentials of the even tiles, one thread per lane; warps 8-11 of the odd tiles
 #include <cuda.h>
 
@@ -238,6 +238,14 @@ __device__ __forceinline__ void tc_ld32(float (&v)[32], uint32_t addr) {
                  "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]),
                  "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31]) : "r"(addr));
 }
+__device__ __forceinline__ void tc_ld16(float (&v)[16], uint32_t addr) {
+  uint32_t* r = reinterpret_cast<uint32_t*>(v);
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]),
+                 "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]) : "r"(addr));
+}
+__device__ __forceinline__ void tc_ld(float (&v)[16], uint32_t addr) { tc_ld16(v, addr); }
+__device__ __forceinline__ void tc_ld(float (&v)[32], uint32_t addr) { tc_ld32(v, addr); }
 __device__ __forceinline__ void tc_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
 __device__ __forceinline__ void tc_st32(uint32_t addr, const float (&v)[32]) {
   const uint32_t* r = reinterpret_cast<const uint32_t*>(v);
@@ -311,8 +319,7 @@ struct Shape {
   static constexpr int kSlots = (kE4M3 ? 4 : 6) * (128 / D);              // copied tiles in the ring
   static constexpr int kBuffers = kE4M3 ? 4 * (128 / D) : 0;              // converted tiles
   static constexpr int kClean = kE4M3 ? kBuffers : kSlots;                // operands of the products
-  static constexpr int kHelpers = 32 * (kE4M3 ? 4 : 2);                   // threads of warps 2, 3 (and 12, 13)
-  static constexpr int kThreads = 32 * (kE4M3 ? 14 : 12);
+  static constexpr int kHelpers = 64, kThreads = 32 * 12;                 // threads of warps 2 and 3; of all
   static constexpr int kRowsAt = 0, kSlotsAt = kTileRows * D * 2, kBuffersAt = kSlotsAt + kSlots * kCopied;
   static constexpr int kSmall = kBuffersAt + kBuffers * kOperand;         // small arrays and barriers
   static constexpr int kSmem = kSmall + 2 * kTileRows * 8 + kTileRows * 4 + (D == 128 ? 512 : 1024);
@@ -350,8 +357,7 @@ struct Small {
   volatile int* dead;
   uint32_t* tmem;
   float2* ml;                      // [2][128] (c m, sum) of the streams' lanes
-  float* row_c;                    // [128] c of the lanes (item's start)
-  float2* joined;                  // [64] (c m, sum) of joined lanes (item's end), in the same place
+  float* row_c;                    // [128] c of the lanes
 };
 
 // Visibility of 32 keys from `key` on (bit j: key + j) for a row with node mask `bits`.
@@ -385,7 +391,7 @@ __device__ __forceinline__ void exponentials(const AttnParams& p, Lane& w, uint3
                                              int tile_key, const Request& r, int b, int h, bool all, uint32_t bad, const uint32_t* odd) {
   using S = Shape<T, kE4M3, D>;
   using M = Mma<typename S::C>;
-  constexpr int kHeld = kCols == 64 ? 64 : 32;                  // scores held in registers at a time
+  constexpr int kHeld = 32;                  // scores held in registers at a time
   float v[kHeld / 32][32];
   uint32_t see[kCols / 32];
 #pragma unroll
@@ -432,12 +438,6 @@ __device__ __forceinline__ void exponentials(const AttnParams& p, Lane& w, uint3
     if (grown) w.mc = now;
   }
   const float from = w.mc == -INFINITY ? 0.f : w.mc;
-  if constexpr (kCols < kTileKeys) {
-    const uint32_t none[16] = {0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0};
-#pragma unroll
-    for (int j = 0; j < kTileKeys; j += 32)
-      if (j < key0 || j >= key0 + kCols) tc_st16(probs + j / 2, none);
-  }
 #pragma unroll
   for (int at = 0; at < kCols; at += kHeld) {
     if (at > 0) load(at);
@@ -483,6 +483,12 @@ __device__ __forceinline__ void exponentials(const AttnParams& p, Lane& w, uint3
       }
     }
   }
+  if constexpr (kCols < kTileKeys) {                           // (their columns may have held scores of this share until now)
+    const uint32_t none[16] = {0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0};
+#pragma unroll
+    for (int j = 0; j < kTileKeys; j += 32)
+      if (j < key0 || j >= key0 + kCols) tc_st16(probs + j / 2, none);
+  }
   tc_wait_st();
 }
 
@@ -499,7 +505,6 @@ tree_attention_kernel(const AttnParams p, const __grid_constant__ CUtensorMap km
     uint8_t* at = smem + S::kSmall;
     sm.ml = reinterpret_cast<float2*>(at);
     sm.row_c = reinterpret_cast<float*>(sm.ml + 2 * kTileRows);
-    sm.joined = reinterpret_cast<float2*>(sm.row_c);
     uint32_t bar = smem_u32(sm.row_c + kTileRows);
     auto take = [&](int n) { const uint32_t r = bar; bar += 8 * n; return r; };
     sm.full = take(S::kSlots);
@@ -666,10 +671,10 @@ tree_attention_kernel(const AttnParams p, const __grid_constant__ CUtensorMap km
     if (lane == 0) tc_commit(sm.end);
     __syncwarp();
     mbar_drain(sm.end, 0);                                      // nothing is in flight when the columns are given back
-  } else if (warp < 4 || warp >= 12) {
+  } else if (warp < 4) {
     // ---- values: in a tile that not every row sees as a whole, non-finite values are taken out and noted per
     // key (the rows that see them add them); E4M3 tiles are converted
-    const int id = (warp < 4 ? warp - 2 : warp - 10) * 32 + lane;
+    const int id = threadIdx.x - 64;
     int slot = 0, buffer = 0;
     uint32_t phase = 0, buffer_phase = 0;
     while (walk.left > 0) {
@@ -706,21 +711,29 @@ tree_attention_kernel(const AttnParams p, const __grid_constant__ CUtensorMap km
             }
         } else {
           const uint32_t to = operand_at(b);
-#pragma unroll 4
-          for (int j = id; j < kTileKeys * (D / 16); j += S::kHelpers) {
-            const int key = j / (D / 16), piece = j % (D / 16);
-            uint4 v = lds16(S::copied(from, key, piece));
-            if (!all) {
-              // the only non-finite code is S.1111.111
-              const uint32_t m = 0x7f7f7f7fu;
-              const uint4 non = make_uint4(__vcmpeq4(v.x & m, m), __vcmpeq4(v.y & m, m), __vcmpeq4(v.z & m, m), __vcmpeq4(v.w & m, m));
-              note(non.x | non.y | non.z | non.w, key);
-              v = make_uint4(v.x & ~non.x, v.y & ~non.y, v.z & ~non.z, v.w & ~non.w);
+          // thread: one 16-byte piece of every kStep-th key, at the same place of the swizzle each time
+          constexpr int kPieces = D / 16, kStep = S::kHelpers / kPieces;
+          const int key0 = id / kPieces, piece = id % kPieces;
+          const uint32_t src = S::copied(from, key0, piece), lo = S::operand(to, key0, 2 * piece), hi = S::operand(to, key0, 2 * piece + 1);
+#pragma unroll
+          for (int k0 = 0; k0 < kTileKeys / kStep; k0 += 4) {
+            uint4 v[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) v[k] = lds16(src + (k0 + k) * kStep * S::kRowBytes);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              if (!all) {
+                // the only non-finite code is S.1111.111
+                const uint32_t m = 0x7f7f7f7fu;
+                const uint4 non = make_uint4(__vcmpeq4(v[k].x & m, m), __vcmpeq4(v[k].y & m, m), __vcmpeq4(v[k].z & m, m), __vcmpeq4(v[k].w & m, m));
+                note(non.x | non.y | non.z | non.w, key0 + (k0 + k) * kStep);
+                v[k] = make_uint4(v[k].x & ~non.x, v[k].y & ~non.y, v[k].z & ~non.z, v[k].w & ~non.w);
+              }
+              sts16(lo + (k0 + k) * kStep * 128, make_uint4(e4m3x2_to_f16x2(v[k].x & 0xffffu), e4m3x2_to_f16x2(v[k].x >> 16),
+                                                            e4m3x2_to_f16x2(v[k].y & 0xffffu), e4m3x2_to_f16x2(v[k].y >> 16)));
+              sts16(hi + (k0 + k) * kStep * 128, make_uint4(e4m3x2_to_f16x2(v[k].z & 0xffffu), e4m3x2_to_f16x2(v[k].z >> 16),
+                                                            e4m3x2_to_f16x2(v[k].w & 0xffffu), e4m3x2_to_f16x2(v[k].w >> 16)));
             }
-            sts16(S::operand(to, key, 2 * piece), make_uint4(e4m3x2_to_f16x2(v.x & 0xffffu), e4m3x2_to_f16x2(v.x >> 16),
-                                                             e4m3x2_to_f16x2(v.y & 0xffffu), e4m3x2_to_f16x2(v.y >> 16)));
-            sts16(S::operand(to, key, 2 * piece + 1), make_uint4(e4m3x2_to_f16x2(v.z & 0xffffu), e4m3x2_to_f16x2(v.z >> 16),
-                                                                 e4m3x2_to_f16x2(v.w & 0xffffu), e4m3x2_to_f16x2(v.w >> 16)));
           }
           mbar_arrive(sm.empty + 8 * slot);
         }
@@ -756,14 +769,14 @@ tree_attention_kernel(const AttnParams p, const __grid_constant__ CUtensorMap km
         if (w.valid) {
           const T* src = static_cast<const T*>(p.q) + (int64_t)w.row * p.ldq + (int64_t)w.head * D;
           if constexpr (!kE4M3) {
-#pragma unroll
+#pragma unroll 8
             for (int i = 0; i < D / 8; ++i) sts16(S::operand(rows_at, at_lane, i), *reinterpret_cast<const uint4*>(src + 8 * i));
           } else {
             float f = 1.f;
             if constexpr (std::is_same<T, __nv_bfloat16>::value) {
               // bf16 rows enter f16 times a power of two that puts their largest element in [1, 4)
               float top = 0.f;
-#pragma unroll
+#pragma unroll 4
               for (int i = 0; i < D / 8; ++i) {
                 T x[8];
                 const uint4 v = *reinterpret_cast<const uint4*>(src + 8 * i);
@@ -775,7 +788,7 @@ tree_attention_kernel(const AttnParams p, const __grid_constant__ CUtensorMap km
               f = __uint_as_float((uint32_t)(127 - ex) << 23);
               w.c *= ex >= -126 ? __uint_as_float((uint32_t)(127 + ex) << 23) : 5.877471754111438e-39f;
             }
-#pragma unroll
+#pragma unroll 4
             for (int i = 0; i < D / 8; ++i) {
               T x[8];
               uint4 v = *reinterpret_cast<const uint4*>(src + 8 * i);
@@ -830,9 +843,9 @@ tree_attention_kernel(const AttnParams p, const __grid_constant__ CUtensorMap km
         if (lane == 0) mbar_arrive(sm.probs + 8 * s);
       }
 
-      // ---- the item's result: the two streams of a lane (this thread takes half of the columns), then the copies
-      // of a row, whose sums pass through the place of the rows
-      constexpr int kHalf = D / 2;
+      // ---- the item's result: the two streams of a lane and the copies of a row on one base; this thread adds the
+      // streams of half of the columns, and the copies add up in the place of the rows
+      constexpr int kHalf = D / 2, kPiece = D / 4;
       if (count > s) wait(sm.output + 8 * s, (done - 1) & 1);
       wait(sm.rows_free, items & 1);
       __syncwarp();
@@ -841,71 +854,69 @@ tree_attention_kernel(const AttnParams p, const __grid_constant__ CUtensorMap km
       tc_fence_before();
       asm volatile("bar.sync 1, 256;" ::: "memory");
       tc_fence_after();
-      float m = -INFINITY, sum = 0.f, o[kHalf];
-      if (active) {
-        const float2 a = sm.ml[at_lane], b = sm.ml[kTileRows + at_lane];
-        m = fmaxf(a.x, b.x);
-        const float from = m == -INFINITY ? 0.f : m, fa = exp2_fast(a.x - from), fb = exp2_fast(b.x - from);
-        sum = a.y * fa + b.y * fb;
-#pragma unroll
-        for (int i = 0; i < kHalf; i += 32) {
-          float x[32];
-          tc_ld32(x, tmem + lanes + S::kOut + s * kHalf + i);
+      float m = -INFINITY, sum = 0.f;
+      for (int i = mine; i < 2 * kTileRows; i += per) m = fmaxf(m, sm.ml[i].x);
+      const float from = m == -INFINITY ? 0.f : m;
+      for (int i = mine; i < 2 * kTileRows; i += per) sum += sm.ml[i].y * exp2_fast(sm.ml[i].x - from);
+      float fa = exp2_fast(sm.ml[at_lane].x - from), fb = exp2_fast(sm.ml[kTileRows + at_lane].x - from);
+      if (whole) {
+        const float f = sum == 0.f ? 0.f : (kE4M3 ? p.v_scale[h] : 1.f) / sum;
+        fa *= f;
+        fb *= f;
+      }
+      const int slot = 2 * blockIdx.x + (tile0 > 0 ? 0 : 1);
+#pragma unroll 1
+      for (int i = s * kHalf; i < (s + 1) * kHalf; i += kPiece) {
+        float o[kPiece];
+        if (active) {
+          float x[kPiece];
+          tc_ld(x, tmem + lanes + S::kOut + i);
+          tc_ld(o, tmem + lanes + S::kStream + S::kOut + i);
           tc_wait_ld();
 #pragma unroll
-          for (int e = 0; e < 32; ++e) o[i + e] = fa * x[e];
-          tc_ld32(x, tmem + lanes + S::kStream + S::kOut + s * kHalf + i);
-          tc_wait_ld();
-#pragma unroll
-          for (int e = 0; e < 32; ++e) o[i + e] = fmaf(fb, x[e], o[i + e]);
+          for (int e = 0; e < kPiece; ++e) o[e] = fa * x[e] + fb * o[e];
         }
-      }
-      for (int half = 64; half >= per; half >>= 1) {
-        // columns 4 c .. 4 c + 3 of lane x at (c * half + x) * 16 bytes
-        const uint32_t place = rows_at + (s * (kHalf / 4) * half + (at_lane & (half - 1))) * 16;
-        if (at_lane >= half && at_lane < 2 * half) {
-          if (s == 0) sm.joined[at_lane - half] = make_float2(m, sum);
+        // columns 4 c .. 4 c + 3 of lane x at (128 c + x) * 16 bytes
+        const uint32_t place = rows_at + s * (kPiece / 4 * kTileRows * 16) + at_lane * 16;
+        if (per < kTileRows) {
+          if (at_lane >= per)
 #pragma unroll
-          for (int i = 0; i < kHalf; i += 4)
-            sts16(place + i / 4 * half * 16, make_uint4(__float_as_uint(o[i]), __float_as_uint(o[i + 1]), __float_as_uint(o[i + 2]), __float_as_uint(o[i + 3])));
+            for (int e = 0; e < kPiece; e += 4)
+              sts16(place + e / 4 * kTileRows * 16, make_uint4(__float_as_uint(o[e]), __float_as_uint(o[e + 1]), __float_as_uint(o[e + 2]), __float_as_uint(o[e + 3])));
+          asm volatile("bar.sync 1, 256;" ::: "memory");
+          if (at_lane < per)
+            for (int copy = per; copy < kTileRows; copy += per)
+#pragma unroll
+              for (int e = 0; e < kPiece; e += 4) {
+                const uint4 v = lds16(place + copy * 16 + e / 4 * kTileRows * 16);
+                o[e] += __uint_as_float(v.x);
+                o[e + 1] += __uint_as_float(v.y);
+                o[e + 2] += __uint_as_float(v.z);
+                o[e + 3] += __uint_as_float(v.w);
+              }
+          asm volatile("bar.sync 1, 256;" ::: "memory");
         }
-        asm volatile("bar.sync 1, 256;" ::: "memory");
-        if (at_lane < half) {
-          const float2 a = sm.joined[at_lane];
-          const float both = fmaxf(m, a.x), from = both == -INFINITY ? 0.f : both, f0 = exp2_fast(m - from), f1 = exp2_fast(a.x - from);
-          m = both;
-          sum = sum * f0 + a.y * f1;
+        if (at_lane < per && w.valid && !*sm.dead) {
+          if (whole) {
+            T* dst = static_cast<T*>(p.out) + (int64_t)w.row * p.ldo + (int64_t)w.head * D + i;
 #pragma unroll
-          for (int i = 0; i < kHalf; i += 4) {
-            const uint4 v = lds16(place + i / 4 * half * 16);
-            o[i] = o[i] * f0 + __uint_as_float(v.x) * f1;
-            o[i + 1] = o[i + 1] * f0 + __uint_as_float(v.y) * f1;
-            o[i + 2] = o[i + 2] * f0 + __uint_as_float(v.z) * f1;
-            o[i + 3] = o[i + 3] * f0 + __uint_as_float(v.w) * f1;
+            for (int e = 0; e < kPiece; e += 8) {
+              uint4 v = make_uint4(0u, 0u, 0u, 0u);
+              if (sum != 0.f)
+                v = make_uint4(Mma<T>::pack(o[e], o[e + 1]), Mma<T>::pack(o[e + 2], o[e + 3]), Mma<T>::pack(o[e + 4], o[e + 5]), Mma<T>::pack(o[e + 6], o[e + 7]));
+              *reinterpret_cast<uint4*>(dst + e) = v;
+            }
+          } else {
+            float* dst = p.part_o + ((size_t)slot * kTileRows + mine) * D + i;
+#pragma unroll
+            for (int e = 0; e < kPiece; e += 4) *reinterpret_cast<float4*>(dst + e) = make_float4(o[e], o[e + 1], o[e + 2], o[e + 3]);
           }
         }
-        asm volatile("bar.sync 1, 256;" ::: "memory");
+        __syncwarp();
       }
-      if (at_lane < per && w.valid && !*sm.dead) {
-        const int slot = 2 * blockIdx.x + (tile0 > 0 ? 0 : 1);
-        if (whole) {
-          const float f = sum == 0.f ? 0.f : (kE4M3 ? p.v_scale[h] : 1.f) / sum;
-          T* dst = static_cast<T*>(p.out) + (int64_t)w.row * p.ldo + (int64_t)w.head * D + s * kHalf;
-#pragma unroll
-          for (int i = 0; i < kHalf; i += 8) {
-            uint4 v = make_uint4(0u, 0u, 0u, 0u);
-            if (sum != 0.f)
-              v = make_uint4(Mma<T>::pack(o[i] * f, o[i + 1] * f), Mma<T>::pack(o[i + 2] * f, o[i + 3] * f),
-                             Mma<T>::pack(o[i + 4] * f, o[i + 5] * f), Mma<T>::pack(o[i + 6] * f, o[i + 7] * f));
-            *reinterpret_cast<uint4*>(dst + i) = v;
-          }
-          if (s == 0 && p.lse) p.lse[(int64_t)w.row * p.Hq + w.head] = sum == 0.f ? -INFINITY : (m + log2f(sum)) * kLn2;
-        } else {
-          float* dst = p.part_o + ((size_t)slot * kTileRows + mine) * D + s * kHalf;
-#pragma unroll
-          for (int i = 0; i < kHalf; i += 4) *reinterpret_cast<float4*>(dst + i) = make_float4(o[i], o[i + 1], o[i + 2], o[i + 3]);
-          if (s == 0) p.part_ml[(size_t)slot * kTileRows + mine] = make_float2(m, sum);
-        }
+      if (s == 0 && at_lane < per && w.valid && !*sm.dead) {
+        if (!whole) p.part_ml[(size_t)slot * kTileRows + mine] = make_float2(m, sum);
+        else if (p.lse) p.lse[(int64_t)w.row * p.Hq + w.head] = sum == 0.f ? -INFINITY : (m + log2f(sum)) * kLn2;
       }
       tc_fence_before();
       asm volatile("bar.sync 1, 256;" ::: "memory");            // outputs and sums are read; the next item may begin
