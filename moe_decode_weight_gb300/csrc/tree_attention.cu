@@ -26,8 +26,9 @@
 // free them (K0 K1 V0 K2 V1 K3 ...), and a tile is held only while its product runs. The roles of a block:
 //   warp 0       requests the tiles by TMA (a box per page, head and 128 bytes of a row, swizzled)
 //   warp 1       issues the matrix products
-//   warps 2, 3   keep non-finite values that not every row sees out of the products, and turn E4M3 tiles into
-//                f16 ones, exactly
+//   warps 2, 3   lay down the rows of the next item while the last one's are in the exponentials, keep
+//                non-finite values that not every row sees out of the products, and turn E4M3 tiles
+//                into f16 ones, exactly
 //   warps 4-7    exponentials of the even tiles, one thread per lane; warps 8-11 of the odd tiles
 #include <cuda.h>
 
@@ -78,12 +79,16 @@ struct Cut {
 
 // ------------------------------------------------------------------ requests and shares
 
+// An item costs its tiles and, for its rows, its first scores and its result, as much time as this many more
+// (measured between 2 and 4): they count when the work is cut into shares.
+constexpr int kItemCost = 3;
+
 struct Request {
   int row0, rows, ctx, keys;       // first row, rows, cached tokens, keys; rows < 0: not valid
   __device__ __forceinline__ int blocks(const AttnParams& p) const { return (rows * p.group + kTileRows - 1) / kTileRows; }
   __device__ __forceinline__ int tiles() const { return (keys + kTileKeys - 1) / kTileKeys; }
   __device__ __forceinline__ int64_t work(const AttnParams& p) const {
-    return rows <= 0 ? 0 : (int64_t)p.Hkv * blocks(p) * tiles();
+    return rows <= 0 ? 0 : (int64_t)p.Hkv * blocks(p) * (tiles() + kItemCost);
   }
 };
 __device__ __forceinline__ Request load_request(const AttnParams& p, int b) {
@@ -99,8 +104,9 @@ __device__ __forceinline__ Request load_request(const AttnParams& p, int b) {
   return r;
 }
 
-// Equal contiguous shares of `total` tiles: block c has tiles [start(c), start(c + 1)). No share is empty, so every
-// partial slot that a join reads was written.
+// Equal contiguous shares of `total` units: block c has [start(c), start(c + 1)). An item's units are its tiles and
+// then its kItemCost; a share that has tiles of an item writes a partial result of it, one that ends
+// among its last units has the whole rest.
 struct Shares {
   int blocks, base, rest;
   __device__ __forceinline__ Shares(int total, int grid) {
@@ -120,7 +126,7 @@ struct Shares {
 struct Walk {
   Request mine, r;                 // the lane's request; the current item's
   int b, h, rb, tile, tiles;       // current item and tile, tiles of the item
-  int left;                        // tiles left in the share
+  int units;                       // units left in the share, the current item's from `tile` on first
 
   __device__ __forceinline__ void take(int lane_) {
     r.row0 = __shfl_sync(0xffffffffu, mine.row0, lane_);
@@ -134,7 +140,7 @@ struct Walk {
     if (first + lane < p.B) mine = load_request(p, first + lane);
   }
   __device__ void begin(const AttnParams& p, int lane) {
-    left = 0;
+    units = 0;
     int64_t total = 0;
     for (int i = 0; i < p.B; i += 32) {
       load32(p, i, lane);
@@ -153,7 +159,7 @@ struct Walk {
     }
     if ((int)blockIdx.x >= shares.blocks) return;
     const int at = shares.start(blockIdx.x);
-    left = shares.start(blockIdx.x + 1) - at;
+    units = shares.start(blockIdx.x + 1) - at;
     int before = 0;
     for (int i = 0; i < p.B; i += 32) {
       if (p.B > 32) load32(p, i, lane);
@@ -174,15 +180,24 @@ struct Walk {
       }
       before += __shfl_sync(0xffffffffu, sum, 31);
     }
-    const int in = at - before, item = in / tiles;
-    tile = in - item * tiles;
+    const int in = at - before, whole = tiles + kItemCost, item = in / whole;
+    tile = in - item * whole;
     h = item / r.blocks(p);
     rb = item - h * r.blocks(p);
-    if (threadIdx.x == 0) {
-      Cut cut{};
-      if (tile > 0) cut = Cut{r.row0, min(r.rows * p.group - rb * kTileRows, kTileRows), rb * kTileRows, h, at - tile, tiles};
-      p.cuts[blockIdx.x] = cut;
+    Cut cut{};
+    if (tile > 0 && tile < tiles) cut = Cut{r.row0, min(r.rows * p.group - rb * kTileRows, kTileRows), rb * kTileRows, h, at - tile, tiles};
+    if (threadIdx.x == 0) p.cuts[blockIdx.x] = cut;
+    if (tile >= tiles) {                        // the tiles before belong to the last share
+      units -= whole - tile;
+      if (units > 0) next_item(p, lane);
     }
+  }
+  // Tiles of the current item in the share; afterwards done() moves on.
+  __device__ __forceinline__ int count() const { return min(tiles - tile, units); }
+  __device__ __forceinline__ bool more() const { return units > 0; }
+  __device__ __forceinline__ void done(const AttnParams& p, int lane) {
+    units -= tiles + kItemCost - tile;
+    if (units > 0) next_item(p, lane);
   }
   __device__ __forceinline__ void next_item(const AttnParams& p, int lane) {
     tile = 0;
@@ -316,13 +331,14 @@ struct Shape {
   static constexpr int kHalves = D * kBytes / kRowBytes;                  // boxes of a page (128 bytes of each key)
   static constexpr int kCopied = kTileKeys * D * kBytes;                  // a copied tile of keys or of values
   static constexpr int kOperand = kTileKeys * D * 2;                      // a 16-bit one
-  static constexpr int kSlots = (kE4M3 ? 4 : 6) * (128 / D);              // copied tiles in the ring
-  static constexpr int kBuffers = kE4M3 ? 4 * (128 / D) : 0;              // converted tiles
+  static constexpr int kSlots = (kE4M3 ? 4 : 5) * (128 / D);              // copied tiles in the ring
+  static constexpr int kBuffers = kE4M3 ? 3 * (128 / D) : 0;              // converted tiles
   static constexpr int kClean = kE4M3 ? kBuffers : kSlots;                // operands of the products
   static constexpr int kHelpers = 64, kThreads = 32 * 12;                 // threads of warps 2 and 3; of all
   static constexpr int kRowsAt = 0, kSlotsAt = kTileRows * D * 2, kBuffersAt = kSlotsAt + kSlots * kCopied;
-  static constexpr int kSmall = kBuffersAt + kBuffers * kOperand;         // small arrays and barriers
-  static constexpr int kSmem = kSmall + 2 * kTileRows * 8 + kTileRows * 4 + (D == 128 ? 512 : 1024);
+  static constexpr int kPiece = 16, kJoinAt = kBuffersAt + kBuffers * kOperand;   // columns of an output that join at a time
+  static constexpr int kSmall = kJoinAt + 2 * kTileRows * kPiece * 4;     // small arrays and barriers
+  static constexpr int kSmem = kSmall + 2 * kTileRows * 8 + 3 * kTileRows * 4 + 1024;
   // tensor memory columns of a stream: scores (the probabilities take their first half when D = 128), output
   static constexpr int kOut = 128, kProb = D == 128 ? 0 : 192, kStream = 256;
 
@@ -357,7 +373,8 @@ struct Small {
   volatile int* dead;
   uint32_t* tmem;
   float2* ml;                      // [2][128] (c m, sum) of the streams' lanes
-  float* row_c;                    // [128] c of the lanes
+  float* row_c;                    // [3][128] c of the lanes, by item mod 3: when the rows of item k + 3 are laid
+                                   // down, the first tile of item k + 2 has its scores, so item k is done
 };
 
 // Visibility of 32 keys from `key` on (bit j: key + j) for a row with node mask `bits`.
@@ -374,6 +391,9 @@ __device__ __forceinline__ uint32_t on_pages32(uint32_t bad, int in_tile, int pa
   if (!(bad >> ((in_tile + 16) >> page_shift) & 1)) v |= 0xffff0000u;
   return v;
 }
+
+// Rows are laid down 128 / copy_rows times.
+__device__ __forceinline__ int copy_rows(int rows) { return rows <= 32 ? 32 : (rows <= 64 ? 64 : 128); }
 
 // What a thread of the exponentials keeps of its lane over an item.
 struct Lane {
@@ -505,7 +525,7 @@ tree_attention_kernel(const AttnParams p, const __grid_constant__ CUtensorMap km
     uint8_t* at = smem + S::kSmall;
     sm.ml = reinterpret_cast<float2*>(at);
     sm.row_c = reinterpret_cast<float*>(sm.ml + 2 * kTileRows);
-    uint32_t bar = smem_u32(sm.row_c + kTileRows);
+    uint32_t bar = smem_u32(sm.row_c + 3 * kTileRows);
     auto take = [&](int n) { const uint32_t r = bar; bar += 8 * n; return r; };
     sm.full = take(S::kSlots);
     sm.empty = take(S::kSlots);
@@ -536,7 +556,7 @@ tree_attention_kernel(const AttnParams p, const __grid_constant__ CUtensorMap km
     }
     for (int i = 0; i < S::kClean; ++i) mbar_init(sm.clean + 8 * i, S::kHelpers);
     for (int i = 0; i < S::kBuffers; ++i) mbar_init(sm.buffer_free + 8 * i, 1);
-    mbar_init(sm.rows_ready, kTileRows);
+    mbar_init(sm.rows_ready, S::kHelpers);
     mbar_init(sm.rows_free, 1);
     for (int i = 0; i < 2; ++i) {
       mbar_init(sm.scores + 8 * i, 2);
@@ -550,7 +570,7 @@ tree_attention_kernel(const AttnParams p, const __grid_constant__ CUtensorMap km
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   Walk walk;
   walk.begin(p, lane);
-  if (walk.left == 0) return;                                   // the whole block
+  if (!walk.more()) return;                                     // the whole block
   if (warp == 1) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" :: "r"(smem_u32(sm.tmem)) : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
@@ -571,9 +591,9 @@ tree_attention_kernel(const AttnParams p, const __grid_constant__ CUtensorMap km
     int slot = 0;
     uint32_t phase = 0;
     bool lost = false;
-    while (walk.left > 0 && !lost) {
+    while (walk.more() && !lost) {
       const Request r = walk.r;
-      const int tile0 = walk.tile, count = min(walk.tiles - tile0, walk.left), head = walk.h;
+      const int tile0 = walk.tile, count = walk.count(), head = walk.h;
       const int32_t* table = p.block_table + (size_t)walk.b * p.max_pages;
       auto look = [&](int i) {                                  // page of the lane in tile i; -1: none wanted, -2: outside the cache
         const int key = (tile0 + i) * kTileKeys + lane * box_rows;
@@ -610,8 +630,7 @@ tree_attention_kernel(const AttnParams p, const __grid_constant__ CUtensorMap km
           id2 = look(i + 3);
         }
       }
-      walk.left -= count;
-      if (walk.left > 0) walk.next_item(p, lane);
+      walk.done(p, lane);
     }
     if (lost)
       for (int i = 0; i < S::kSlots; ++i) mbar_drain(sm.full + 8 * i, i < slot ? phase : phase ^ 1);
@@ -619,8 +638,8 @@ tree_attention_kernel(const AttnParams p, const __grid_constant__ CUtensorMap km
     // ---- products. Scores of the first two tiles of an item, then in turn the output of tile i and the scores
     // of tile i + 2, whose columns hold the probabilities that output reads.
     int unit0 = 0, items = 0, done[2] = {0, 0};                 // units before this item; items; outputs of each stream
-    while (walk.left > 0) {
-      const int count = min(walk.tiles - walk.tile, walk.left);
+    while (walk.more()) {
+      const int count = walk.count();
       auto scores = [&](int i) {
         const int unit = unit0 + keys_unit(i), at = unit % S::kClean, s = i & 1;
         wait((kE4M3 ? sm.clean : sm.full) + 8 * at, unit / S::kClean & 1);
@@ -641,8 +660,11 @@ tree_attention_kernel(const AttnParams p, const __grid_constant__ CUtensorMap km
         __syncwarp();
       };
       wait(sm.rows_ready, items & 1);
-      scores(0);
-      if (count > 1) scores(1);
+      // the columns of the scores hold probabilities until the last output that reads them is complete
+      for (int i = 0; i < 2 && i < count; ++i) {
+        if (done[i] > 0) wait(sm.output + 8 * i, (done[i] - 1) & 1);
+        scores(i);
+      }
       for (int i = 0; i < count; ++i) {
         const int unit = unit0 + values_unit(i, count), at = unit % S::kClean, s = i & 1;
         wait(sm.clean + 8 * at, unit / S::kClean & 1);
@@ -665,8 +687,7 @@ tree_attention_kernel(const AttnParams p, const __grid_constant__ CUtensorMap km
       }
       unit0 += 2 * count;
       ++items;
-      walk.left -= count;
-      if (walk.left > 0) walk.next_item(p, lane);
+      walk.done(p, lane);
     }
     if (lane == 0) tc_commit(sm.end);
     __syncwarp();
@@ -675,11 +696,54 @@ tree_attention_kernel(const AttnParams p, const __grid_constant__ CUtensorMap km
     // ---- values: in a tile that not every row sees as a whole, non-finite values are taken out and noted per
     // key (the rows that see them add them); E4M3 tiles are converted
     const int id = threadIdx.x - 64;
-    int slot = 0, buffer = 0;
+    int slot = 0, buffer = 0, items = 0;
     uint32_t phase = 0, buffer_phase = 0;
-    while (walk.left > 0) {
+    while (walk.more()) {
       const Request r = walk.r;
-      const int tile0 = walk.tile, count = min(walk.tiles - tile0, walk.left);
+      const int tile0 = walk.tile, count = walk.count(), h = walk.h;
+      // the item's rows, as soon as the last item's scores are complete
+      if (items > 0) wait(sm.rows_free, (items - 1) & 1);
+      const int first = walk.rb * kTileRows, rows = min(r.rows * p.group - first, kTileRows), per = copy_rows(rows);
+#pragma unroll 1
+      for (int at = id; at < kTileRows; at += S::kHelpers) {
+        const int mine = at & (per - 1), flat = first + mine, node = flat / p.group;
+        if (mine >= rows) continue;
+        const T* src = static_cast<const T*>(p.q) + (int64_t)(r.row0 + node) * p.ldq + (int64_t)(h * p.group + flat - node * p.group) * D;
+        if constexpr (!kE4M3) {
+#pragma unroll 8
+          for (int i = 0; i < D / 8; ++i) sts16(S::operand(rows_at, at, i), *reinterpret_cast<const uint4*>(src + 8 * i));
+        } else {
+          float f = 1.f, c = p.scale * kLog2e * p.k_scale[h];
+          if constexpr (std::is_same<T, __nv_bfloat16>::value) {
+            // bf16 rows enter f16 times a power of two that puts their largest element in [1, 4)
+            float top = 0.f;
+#pragma unroll 8
+            for (int i = 0; i < D / 8; ++i) {
+              T x[8];
+              const uint4 v = *reinterpret_cast<const uint4*>(src + 8 * i);
+              memcpy(x, &v, 16);
+#pragma unroll
+              for (int e = 0; e < 8; ++e) top = fmaxf(top, fabsf(Elem<T>::to_float(x[e])));
+            }
+            const int ex = top > 0.f && isfinite(top) ? min((int)(__float_as_uint(top) >> 23) - 127, 126) : 0;
+            f = __uint_as_float((uint32_t)(127 - ex) << 23);
+            c *= ex >= -126 ? __uint_as_float((uint32_t)(127 + ex) << 23) : 5.877471754111438e-39f;
+          }
+#pragma unroll 8
+          for (int i = 0; i < D / 8; ++i) {
+            T x[8];
+            uint4 v = *reinterpret_cast<const uint4*>(src + 8 * i);
+            memcpy(x, &v, 16);
+            v = make_uint4(M::pack(Elem<T>::to_float(x[0]) * f, Elem<T>::to_float(x[1]) * f), M::pack(Elem<T>::to_float(x[2]) * f, Elem<T>::to_float(x[3]) * f),
+                           M::pack(Elem<T>::to_float(x[4]) * f, Elem<T>::to_float(x[5]) * f), M::pack(Elem<T>::to_float(x[6]) * f, Elem<T>::to_float(x[7]) * f));
+            sts16(S::operand(rows_at, at, i), v);
+          }
+          sm.row_c[items % 3 * kTileRows + at] = c;
+        }
+      }
+      fence_async_proxy();
+      mbar_arrive(sm.rows_ready);
+      ++items;
       for (int u = 0; u < 2 * count; ++u) {
         const bool keys = is_keys(u, count);
         const int i = keys ? (u + 1) / 2 : (u == 2 * count - 1 ? count - 1 : u / 2 - 1), tile_key = (tile0 + i) * kTileKeys;
@@ -742,8 +806,7 @@ tree_attention_kernel(const AttnParams p, const __grid_constant__ CUtensorMap km
         if (++slot == S::kSlots) { slot = 0; phase ^= 1; }
         if (kE4M3 && ++buffer == S::kBuffers) { buffer = 0; buffer_phase ^= 1; }
       }
-      walk.left -= count;
-      if (walk.left > 0) walk.next_item(p, lane);
+      walk.done(p, lane);
     }
   } else {
     // ---- exponentials: thread = lane of tensor memory
@@ -751,13 +814,13 @@ tree_attention_kernel(const AttnParams p, const __grid_constant__ CUtensorMap km
     const uint32_t lanes = (uint32_t)(warp & 3) * 32 << 16;
     const uint32_t scores = tmem + s * S::kStream + lanes, probs = scores + S::kProb, out = scores + S::kOut;
     int unit0 = 0, items = 0, done = 0;                         // units before this item; items; tiles of this stream
-    while (walk.left > 0) {
+    while (walk.more()) {
       const Request r = walk.r;
       const int first = walk.rb * kTileRows, rows = min(r.rows * p.group - first, kTileRows), h = walk.h;
-      const int tile0 = walk.tile, count = min(walk.tiles - tile0, walk.left);
+      const int tile0 = walk.tile, count = walk.count();
       const bool whole = count == walk.tiles;
       // rows in a copy, the lane's row and the first key of its share of a tile
-      const int per = rows <= 32 ? 32 : (rows <= 64 ? 64 : 128), mine = at_lane & (per - 1), key0 = (at_lane / per) * per;
+      const int per = copy_rows(rows), mine = at_lane & (per - 1), key0 = at_lane & ~(per - 1);
       const bool active = (warp & 3) * 32 % per < rows;
       Lane w;
       w.valid = mine < rows;
@@ -765,44 +828,6 @@ tree_attention_kernel(const AttnParams p, const __grid_constant__ CUtensorMap km
       w.row = r.row0 + node;
       w.head = h * p.group + flat - node * p.group;
       w.c = p.scale * kLog2e * (kE4M3 ? p.k_scale[h] : 1.f);
-      if (s == 0) {
-        if (w.valid) {
-          const T* src = static_cast<const T*>(p.q) + (int64_t)w.row * p.ldq + (int64_t)w.head * D;
-          if constexpr (!kE4M3) {
-#pragma unroll 8
-            for (int i = 0; i < D / 8; ++i) sts16(S::operand(rows_at, at_lane, i), *reinterpret_cast<const uint4*>(src + 8 * i));
-          } else {
-            float f = 1.f;
-            if constexpr (std::is_same<T, __nv_bfloat16>::value) {
-              // bf16 rows enter f16 times a power of two that puts their largest element in [1, 4)
-              float top = 0.f;
-#pragma unroll 4
-              for (int i = 0; i < D / 8; ++i) {
-                T x[8];
-                const uint4 v = *reinterpret_cast<const uint4*>(src + 8 * i);
-                memcpy(x, &v, 16);
-#pragma unroll
-                for (int e = 0; e < 8; ++e) top = fmaxf(top, fabsf(Elem<T>::to_float(x[e])));
-              }
-              const int ex = top > 0.f && isfinite(top) ? min((int)(__float_as_uint(top) >> 23) - 127, 126) : 0;
-              f = __uint_as_float((uint32_t)(127 - ex) << 23);
-              w.c *= ex >= -126 ? __uint_as_float((uint32_t)(127 + ex) << 23) : 5.877471754111438e-39f;
-            }
-#pragma unroll 4
-            for (int i = 0; i < D / 8; ++i) {
-              T x[8];
-              uint4 v = *reinterpret_cast<const uint4*>(src + 8 * i);
-              memcpy(x, &v, 16);
-              v = make_uint4(M::pack(Elem<T>::to_float(x[0]) * f, Elem<T>::to_float(x[1]) * f), M::pack(Elem<T>::to_float(x[2]) * f, Elem<T>::to_float(x[3]) * f),
-                             M::pack(Elem<T>::to_float(x[4]) * f, Elem<T>::to_float(x[5]) * f), M::pack(Elem<T>::to_float(x[6]) * f, Elem<T>::to_float(x[7]) * f));
-              sts16(S::operand(rows_at, at_lane, i), v);
-            }
-          }
-        }
-        if (kE4M3) sm.row_c[at_lane] = w.c;
-        fence_async_proxy();
-        mbar_arrive(sm.rows_ready);
-      }
       w.bits = 0;
       if (w.valid) {
         w.bits = p.tree_mask ? p.tree_mask[w.row] : ~0ull >> (63 - node);
@@ -818,13 +843,10 @@ tree_attention_kernel(const AttnParams p, const __grid_constant__ CUtensorMap km
         for (int i = 0; i < D; i += 32) tc_st32(out + i, zero);
         tc_wait_st();
       }
-      if (kE4M3) {
-        asm volatile("bar.sync 1, 256;" ::: "memory");
-        w.c = sm.row_c[at_lane];
-      }
       for (int i = s; i < count; i += 2) {
         const int tile_key = (tile0 + i) * kTileKeys;
         wait(sm.scores + 8 * s, done & 1);
+        if (kE4M3 && i == s) w.c = sm.row_c[items % 3 * kTileRows + at_lane];
         const uint32_t bad = sm.tile_bad[S::kClean + s];
         const bool all = tile_key + kTileKeys <= r.ctx && bad == 0;
         const int value = unit0 + values_unit(i, count);
@@ -844,10 +866,9 @@ tree_attention_kernel(const AttnParams p, const __grid_constant__ CUtensorMap km
       }
 
       // ---- the item's result: the two streams of a lane and the copies of a row on one base; this thread adds the
-      // streams of half of the columns, and the copies add up in the place of the rows
-      constexpr int kHalf = D / 2, kPiece = D / 4;
+      // streams of half of the columns, and the copies add up over shared memory
+      constexpr int kHalf = D / 2, kPiece = S::kPiece;
       if (count > s) wait(sm.output + 8 * s, (done - 1) & 1);
-      wait(sm.rows_free, items & 1);
       __syncwarp();
       tc_fence_after();
       sm.ml[s * kTileRows + at_lane] = make_float2(w.mc, w.l);
@@ -877,7 +898,7 @@ tree_attention_kernel(const AttnParams p, const __grid_constant__ CUtensorMap km
           for (int e = 0; e < kPiece; ++e) o[e] = fa * x[e] + fb * o[e];
         }
         // columns 4 c .. 4 c + 3 of lane x at (128 c + x) * 16 bytes
-        const uint32_t place = rows_at + s * (kPiece / 4 * kTileRows * 16) + at_lane * 16;
+        const uint32_t place = base + S::kJoinAt + s * (kPiece / 4 * kTileRows * 16) + at_lane * 16;
         if (per < kTileRows) {
           if (at_lane >= per)
 #pragma unroll
@@ -923,8 +944,7 @@ tree_attention_kernel(const AttnParams p, const __grid_constant__ CUtensorMap km
       tc_fence_after();
       unit0 += 2 * count;
       ++items;
-      walk.left -= count;
-      if (walk.left > 0) walk.next_item(p, lane);
+      walk.done(p, lane);
     }
   }
   tc_fence_before();
@@ -941,58 +961,58 @@ template <typename T, int D>
 __global__ void __launch_bounds__(128) join_kernel(const AttnParams p) {
   asm volatile("griddepcontrol.wait;" ::: "memory");
   constexpr int kPer = D / 32;
-  const int row = blockIdx.y * 4 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
+  const int lane = threadIdx.x & 31;
   const int total = p.total[0], blocks = p.total[1];
   if ((int)blockIdx.x + 1 >= blocks) return;
   const Cut cut = p.cuts[blockIdx.x + 1];
-  if (row >= cut.rows) return;
   const Shares shares(total, blocks);
   if (shares.start(blockIdx.x) > cut.start) return;             // an earlier boundary is inside too
   const int c0 = blockIdx.x, parts = shares.owner(cut.start + cut.tiles - 1) - c0 + 1;
-  // the item's first part is the last of its block's share, the others are the first of theirs
-  auto slot = [&](int i) { return (size_t)(2 * (c0 + i) + (i == 0 ? 1 : 0)) * kTileRows + row; };
-  float mc = -INFINITY;
-  for (int i = lane; i < parts; i += 32) mc = fmaxf(mc, p.part_ml[slot(i)].x);
-  mc = warp_max(mc);
-  const float base = mc == -INFINITY ? 0.f : mc;
-  float o[kPer], l = 0.f;
+  for (int row = blockIdx.y * 4 + (threadIdx.x >> 5); row < cut.rows; row += 4 * gridDim.y) {
+    // the item's first part is the last of its block's share, the others are the first of theirs
+    auto slot = [&](int i) { return (size_t)(2 * (c0 + i) + (i == 0 ? 1 : 0)) * kTileRows + row; };
+    float mc = -INFINITY;
+    for (int i = lane; i < parts; i += 32) mc = fmaxf(mc, p.part_ml[slot(i)].x);
+    mc = warp_max(mc);
+    const float base = mc == -INFINITY ? 0.f : mc;
+    float o[kPer], l = 0.f;
 #pragma unroll
-  for (int j = 0; j < kPer; ++j) o[j] = 0.f;
-  for (int i0 = 0; i0 < parts; i0 += 32) {
-    float f = 0.f;
-    if (i0 + lane < parts) {
-      const float2 ml = p.part_ml[slot(i0 + lane)];
-      f = exp2_fast(ml.x - base);
-      l = fmaf(ml.y, f, l);
-    }
-    const int n = min(parts - i0, 32);
-    for (int i = 0; i < n; i += 8) {
-      float v[8][kPer];
-#pragma unroll
-      for (int u = 0; u < 8; ++u) {
-        const float* src = p.part_o + slot(i0 + min(i + u, n - 1)) * D + lane * kPer;
-        if constexpr (kPer == 4) *reinterpret_cast<float4*>(v[u]) = *reinterpret_cast<const float4*>(src);
-        else *reinterpret_cast<float2*>(v[u]) = *reinterpret_cast<const float2*>(src);
+    for (int j = 0; j < kPer; ++j) o[j] = 0.f;
+    for (int i0 = 0; i0 < parts; i0 += 32) {
+      float f = 0.f;
+      if (i0 + lane < parts) {
+        const float2 ml = p.part_ml[slot(i0 + lane)];
+        f = exp2_fast(ml.x - base);
+        l = fmaf(ml.y, f, l);
       }
+      const int n = min(parts - i0, 32);
+      for (int i = 0; i < n; i += 4) {
+        float v[4][kPer];
 #pragma unroll
-      for (int u = 0; u < 8; ++u) {
-        const float g = __shfl_sync(0xffffffffu, f, min(i + u, 31));
-        if (i + u < n)
+        for (int u = 0; u < 4; ++u) {
+          const float* src = p.part_o + slot(i0 + min(i + u, n - 1)) * D + lane * kPer;
+          if constexpr (kPer == 4) *reinterpret_cast<float4*>(v[u]) = __ldcg(reinterpret_cast<const float4*>(src));
+          else *reinterpret_cast<float2*>(v[u]) = __ldcg(reinterpret_cast<const float2*>(src));
+        }
 #pragma unroll
-          for (int j = 0; j < kPer; ++j) o[j] = fmaf(v[u][j], g, o[j]);
+        for (int u = 0; u < 4; ++u) {
+          const float g = __shfl_sync(0xffffffffu, f, min(i + u, 31));
+#pragma unroll
+          for (int j = 0; j < kPer; ++j) o[j] = i + u < n ? fmaf(v[u][j], g, o[j]) : o[j];
+        }
       }
     }
+    l = warp_sum(l);
+    const int flat = cut.first + row, node = flat / p.group, head = cut.h * p.group + flat - node * p.group;
+    const float f = l == 0.f ? 0.f : (p.v_scale ? p.v_scale[cut.h] : 1.f) / l;
+    T* dst = static_cast<T*>(p.out) + (int64_t)(cut.row0 + node) * p.ldo + (int64_t)head * D + lane * kPer;
+    uint32_t packed[kPer / 2];
+#pragma unroll
+    for (int j = 0; j < kPer; j += 2) packed[j / 2] = l == 0.f ? 0u : Mma<T>::pack(o[j] * f, o[j + 1] * f);
+    if constexpr (kPer == 4) *reinterpret_cast<uint2*>(dst) = make_uint2(packed[0], packed[1]);
+    else *reinterpret_cast<uint32_t*>(dst) = packed[0];
+    if (p.lse && lane == 0) p.lse[(int64_t)(cut.row0 + node) * p.Hq + head] = l == 0.f ? -INFINITY : (mc + log2f(l)) * kLn2;
   }
-  l = warp_sum(l);
-  const int flat = cut.first + row, node = flat / p.group, head = cut.h * p.group + flat - node * p.group;
-  const float f = l == 0.f ? 0.f : (p.v_scale ? p.v_scale[cut.h] : 1.f) / l;
-  T* dst = static_cast<T*>(p.out) + (int64_t)(cut.row0 + node) * p.ldo + (int64_t)head * D + lane * kPer;
-  uint32_t packed[kPer / 2];
-#pragma unroll
-  for (int j = 0; j < kPer; j += 2) packed[j / 2] = l == 0.f ? 0u : Mma<T>::pack(o[j] * f, o[j + 1] * f);
-  if constexpr (kPer == 4) *reinterpret_cast<uint2*>(dst) = make_uint2(packed[0], packed[1]);
-  else *reinterpret_cast<uint32_t*>(dst) = packed[0];
-  if (p.lse && lane == 0) p.lse[(int64_t)(cut.row0 + node) * p.Hq + head] = l == 0.f ? -INFINITY : (mc + log2f(l)) * kLn2;
 }
 
 // ------------------------------------------------------------------ host
@@ -1035,7 +1055,7 @@ cudaError_t launch(const AttnParams& p, const CUtensorMap& km, const CUtensorMap
   if (e != cudaSuccess) return e;
   if (grid == 1) return cudaSuccess;
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3((unsigned)(grid - 1), (unsigned)((std::min(p.max_new * p.group, kTileRows) + 3) / 4));
+  cfg.gridDim = dim3((unsigned)(grid - 1), (unsigned)std::min((std::min(p.max_new * p.group, kTileRows) + 3) / 4, 8));
   cfg.blockDim = dim3(128);
   cfg.stream = s;
   cudaLaunchAttribute a{};
