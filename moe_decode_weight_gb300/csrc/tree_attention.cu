@@ -26,9 +26,9 @@
 // free them (K0 K1 V0 K2 V1 K3 ...), and a tile is held only while its product runs. The roles of a block:
 //   warp 0       requests the tiles by TMA (a box per page, head and 128 bytes of a row, swizzled)
 //   warp 1       issues the matrix products
-//   warps 2, 3   lay down the rows of the next item while the last one's are in the exponentials, keep
-//                non-finite values that not every row sees out of the products, and turn E4M3 tiles
-//                into f16 ones, exactly
+//   warps 2, 3   lay down the rows of the next item while the last one's are in the exponentials, and keep
+//                non-finite values that not every row sees out of the products
+//   warps 12-15  over an E4M3 cache only: do the latter and turn the tiles into f16 ones, exactly
 //   warps 4-7    exponentials of the even tiles, one thread per lane; warps 8-11 of the odd tiles
 #include <cuda.h>
 
@@ -227,18 +227,27 @@ __device__ __forceinline__ void tc_fence_after() { asm volatile("tcgen05.fence::
 __device__ __forceinline__ void tc_commit(uint32_t bar) {
   asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" :: "r"(bar) : "memory");
 }
-__device__ __forceinline__ void tc_mma(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool add) {
-  asm volatile("{ .reg .pred p; setp.ne.b32 p, %4, 0; tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p; }"
-               :: "r"(d), "l"(a), "l"(b), "r"(idesc), "r"((uint32_t)add) : "memory");
+// Shared-memory operand with 128-byte swizzle, in two words: address and offsets in units of 16 bytes. K-major:
+// kStride between groups of 8 rows. MN-major: `lead` between blocks of 64 columns, kStride between
+// groups of 8 k. The second word is the same for all (stride, version, swizzle); a product's steps along k
+// add to the first one only, which keeps their issue short.
+constexpr uint32_t kOperandHigh = (1024u >> 4) | 1u << 14 | 2u << 29;
+__device__ __forceinline__ uint32_t operand_low(uint32_t addr, uint32_t lead) { return (addr & 0x3ffff) >> 4 | (lead >> 4) << 16; }
+__device__ __forceinline__ void tc_mma(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, bool add) {
+  asm volatile("{ .reg .pred p; .reg .b64 a, b; setp.ne.b32 p, %4, 0; mov.b64 a, {%1, %5}; mov.b64 b, {%2, %5};"
+               " tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, p; }"
+               :: "r"(d), "r"(a), "r"(b), "r"(idesc), "r"((uint32_t)add), "r"(kOperandHigh) : "memory");
 }
-__device__ __forceinline__ void tc_mma_tmem(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc) {
-  asm volatile("{ .reg .pred p; setp.ne.b32 p, 1, 0; tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p; }"
-               :: "r"(d), "r"(a), "l"(b), "r"(idesc) : "memory");
+__device__ __forceinline__ void tc_mma_tmem(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc) {
+  asm volatile("{ .reg .pred p; .reg .b64 b; setp.ne.b32 p, 1, 0; mov.b64 b, {%2, %4};"
+               " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], b, %3, p; }"
+               :: "r"(d), "r"(a), "r"(b), "r"(idesc), "r"(kOperandHigh) : "memory");
 }
-// Shared-memory operand, 128-byte swizzle: address and offsets in units of 16 bytes. K-major: `stride` between
-// groups of 8 rows. MN-major: `lead` between blocks of 64 columns, `stride` between groups of 8 k.
-__device__ __forceinline__ uint64_t smem_operand(uint32_t addr, uint32_t lead, uint32_t stride) {
-  return (uint64_t)((addr & 0x3ffff) >> 4) | (uint64_t)(lead >> 4) << 16 | (uint64_t)(stride >> 4) << 32 | 1ull << 46 | 2ull << 61;
+// One lane of a converged warp.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t one;
+  asm volatile("{ .reg .pred p; elect.sync _|p, 0xffffffff; selp.u32 %0, 1, 0, p; }" : "=r"(one));
+  return one != 0;
 }
 // 128 x n, fp32 result, 16-bit operands of one type, b MN-major or K-major.
 __host__ __device__ constexpr uint32_t mma_shape(bool bf16, bool b_mn_major, int n) {
@@ -260,7 +269,6 @@ __device__ __forceinline__ void tc_ld16(float (&v)[16], uint32_t addr) {
                  "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]) : "r"(addr));
 }
 __device__ __forceinline__ void tc_ld(float (&v)[16], uint32_t addr) { tc_ld16(v, addr); }
-__device__ __forceinline__ void tc_ld(float (&v)[32], uint32_t addr) { tc_ld32(v, addr); }
 __device__ __forceinline__ void tc_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
 __device__ __forceinline__ void tc_st32(uint32_t addr, const float (&v)[32]) {
   const uint32_t* r = reinterpret_cast<const uint32_t*>(v);
@@ -334,7 +342,8 @@ struct Shape {
   static constexpr int kSlots = (kE4M3 ? 4 : 5) * (128 / D);              // copied tiles in the ring
   static constexpr int kBuffers = kE4M3 ? 3 * (128 / D) : 0;              // converted tiles
   static constexpr int kClean = kE4M3 ? kBuffers : kSlots;                // operands of the products
-  static constexpr int kHelpers = 64, kThreads = 32 * 12;                 // threads of warps 2 and 3; of all
+  static constexpr int kHelpers = kE4M3 ? 128 : 64;                       // threads of warps 12-15, or of 2 and 3
+  static constexpr int kThreads = 32 * (kE4M3 ? 16 : 12);
   static constexpr int kRowsAt = 0, kSlotsAt = kTileRows * D * 2, kBuffersAt = kSlotsAt + kSlots * kCopied;
   static constexpr int kPiece = 16, kJoinAt = kBuffersAt + kBuffers * kOperand;   // columns of an output that join at a time
   static constexpr int kSmall = kJoinAt + 2 * kTileRows * kPiece * 4;     // small arrays and barriers
@@ -411,7 +420,7 @@ __device__ __forceinline__ void exponentials(const AttnParams& p, Lane& w, uint3
                                              int tile_key, const Request& r, int b, int h, bool all, uint32_t bad, const uint32_t* odd) {
   using S = Shape<T, kE4M3, D>;
   using M = Mma<typename S::C>;
-  constexpr int kHeld = 32;                  // scores held in registers at a time
+  constexpr int kHeld = kCols < 64 || kE4M3 ? 32 : 64;         // scores held in registers at a time
   float v[kHeld / 32][32];
   uint32_t see[kCols / 32];
 #pragma unroll
@@ -519,7 +528,7 @@ tree_attention_kernel(const AttnParams p, const __grid_constant__ CUtensorMap km
   using M = Mma<typename S::C>;
   extern __shared__ __align__(1024) uint8_t smem[];
   const uint32_t base = smem_u32(smem);
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   Small sm;
   {
     uint8_t* at = smem + S::kSmall;
@@ -556,7 +565,7 @@ tree_attention_kernel(const AttnParams p, const __grid_constant__ CUtensorMap km
     }
     for (int i = 0; i < S::kClean; ++i) mbar_init(sm.clean + 8 * i, S::kHelpers);
     for (int i = 0; i < S::kBuffers; ++i) mbar_init(sm.buffer_free + 8 * i, 1);
-    mbar_init(sm.rows_ready, S::kHelpers);
+    mbar_init(sm.rows_ready, 64);
     mbar_init(sm.rows_free, 1);
     for (int i = 0; i < 2; ++i) {
       mbar_init(sm.scores + 8 * i, 2);
@@ -578,7 +587,7 @@ tree_attention_kernel(const AttnParams p, const __grid_constant__ CUtensorMap km
   }
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = *sm.tmem;
+  const uint32_t tmem = __shfl_sync(0xffffffffu, *sm.tmem, 0);
   const uint32_t rows_at = base + S::kRowsAt;
   auto wait = [&](uint32_t bar, uint32_t parity) { mbar_wait(bar, parity, p.spin_budget, p.status, sm.dead); };
   auto slot_at = [&](int slot) { return base + S::kSlotsAt + slot * S::kCopied; };
@@ -643,13 +652,13 @@ tree_attention_kernel(const AttnParams p, const __grid_constant__ CUtensorMap km
       auto scores = [&](int i) {
         const int unit = unit0 + keys_unit(i), at = unit % S::kClean, s = i & 1;
         wait((kE4M3 ? sm.clean : sm.full) + 8 * at, unit / S::kClean & 1);
-        if (lane == 0) {
-          tc_fence_after();
+        tc_fence_after();
+        const uint32_t rows_low = operand_low(rows_at, 16), keys_low = operand_low(operand_at(at), 16), to = tmem + s * S::kStream;
+        if (elect_one()) {
 #pragma unroll
           for (int t = 0; t < D / 16; ++t) {
-            const uint32_t off = (t >> 2) * (128 * 128) + (t & 3) * 32;
-            tc_mma(tmem + s * S::kStream, smem_operand(rows_at + off, 16, 1024), smem_operand(operand_at(at) + off, 16, 1024),
-                   mma_shape(M::kBf16, false, kTileKeys), t > 0);
+            const uint32_t off = ((t >> 2) * (128 * 128) + (t & 3) * 32) >> 4;
+            tc_mma(to, rows_low + off, keys_low + off, mma_shape(M::kBf16, false, kTileKeys), t > 0);
           }
           tc_commit(sm.scores + 8 * s);
           sm.tile_bad[S::kClean + s] = kE4M3 ? sm.tile_bad[at] : sm.bad_pages[at];
@@ -669,18 +678,20 @@ tree_attention_kernel(const AttnParams p, const __grid_constant__ CUtensorMap km
         const int unit = unit0 + values_unit(i, count), at = unit % S::kClean, s = i & 1;
         wait(sm.clean + 8 * at, unit / S::kClean & 1);
         wait(sm.probs + 8 * s, done[s] & 1);
-        if (lane == 0) {
-          tc_fence_after();
+        tc_fence_after();
+        const uint32_t values_low = operand_low(operand_at(at), 128 * 128), stream = tmem + s * S::kStream;
+        if (elect_one()) {
 #pragma unroll
           for (int t = 0; t < kTileKeys / 16; ++t)
-            tc_mma_tmem(tmem + s * S::kStream + S::kOut, tmem + s * S::kStream + S::kProb + 8 * t,
-                        smem_operand(operand_at(at) + t * 2048, 128 * 128, 1024), mma_shape(M::kBf16, true, D));
+            tc_mma_tmem(stream + S::kOut, stream + S::kProb + 8 * t, values_low + t * (2048 >> 4), mma_shape(M::kBf16, true, D));
           tc_commit(sm.output + 8 * s);
           tc_commit((kE4M3 ? sm.buffer_free : sm.empty) + 8 * at);
         }
         __syncwarp();
         if (i + 2 < count) {
-          wait(sm.output + 8 * s, done[s] & 1);
+          // where the probabilities have columns of their own, the scores may follow at once: their completion
+          // includes the output's
+          if (S::kProb < kTileKeys) wait(sm.output + 8 * s, done[s] & 1);
           scores(i + 2);
         }
         ++done[s];
@@ -692,58 +703,64 @@ tree_attention_kernel(const AttnParams p, const __grid_constant__ CUtensorMap km
     if (lane == 0) tc_commit(sm.end);
     __syncwarp();
     mbar_drain(sm.end, 0);                                      // nothing is in flight when the columns are given back
-  } else if (warp < 4) {
-    // ---- values: in a tile that not every row sees as a whole, non-finite values are taken out and noted per
-    // key (the rows that see them add them); E4M3 tiles are converted
-    const int id = threadIdx.x - 64;
+  } else if (warp < 4 || warp >= 12) {
+    // ---- warps 2, 3: the rows of an item, as soon as the last item's scores are complete. They (or warps 12-15 over
+    // an E4M3 cache) also go over the tiles: where not every row sees all of a tile, non-finite values are
+    // taken out and noted per key (the rows that see them add them); E4M3 tiles are converted
+    const int id = kE4M3 ? threadIdx.x - 384 : threadIdx.x - 64;
     int slot = 0, buffer = 0, items = 0;
     uint32_t phase = 0, buffer_phase = 0;
     while (walk.more()) {
       const Request r = walk.r;
       const int tile0 = walk.tile, count = walk.count(), h = walk.h;
-      // the item's rows, as soon as the last item's scores are complete
-      if (items > 0) wait(sm.rows_free, (items - 1) & 1);
-      const int first = walk.rb * kTileRows, rows = min(r.rows * p.group - first, kTileRows), per = copy_rows(rows);
+      if (warp < 4) {
+        if (items > 0) wait(sm.rows_free, (items - 1) & 1);
+        const int first = walk.rb * kTileRows, rows = min(r.rows * p.group - first, kTileRows), per = copy_rows(rows);
 #pragma unroll 1
-      for (int at = id; at < kTileRows; at += S::kHelpers) {
-        const int mine = at & (per - 1), flat = first + mine, node = flat / p.group;
-        if (mine >= rows) continue;
-        const T* src = static_cast<const T*>(p.q) + (int64_t)(r.row0 + node) * p.ldq + (int64_t)(h * p.group + flat - node * p.group) * D;
-        if constexpr (!kE4M3) {
+        for (int at = threadIdx.x - 64; at < kTileRows; at += 64) {
+          const int mine = at & (per - 1), flat = first + mine, node = flat / p.group;
+          if (mine >= rows) continue;
+          const T* src = static_cast<const T*>(p.q) + (int64_t)(r.row0 + node) * p.ldq + (int64_t)(h * p.group + flat - node * p.group) * D;
+          if constexpr (!kE4M3) {
 #pragma unroll 8
-          for (int i = 0; i < D / 8; ++i) sts16(S::operand(rows_at, at, i), *reinterpret_cast<const uint4*>(src + 8 * i));
-        } else {
-          float f = 1.f, c = p.scale * kLog2e * p.k_scale[h];
-          if constexpr (std::is_same<T, __nv_bfloat16>::value) {
-            // bf16 rows enter f16 times a power of two that puts their largest element in [1, 4)
-            float top = 0.f;
+            for (int i = 0; i < D / 8; ++i) sts16(S::operand(rows_at, at, i), *reinterpret_cast<const uint4*>(src + 8 * i));
+          } else {
+            float f = 1.f, c = p.scale * kLog2e * p.k_scale[h];
+            if constexpr (std::is_same<T, __nv_bfloat16>::value) {
+              // bf16 rows enter f16 times a power of two that puts their largest element in [1, 4)
+              float top = 0.f;
+#pragma unroll 8
+              for (int i = 0; i < D / 8; ++i) {
+                T x[8];
+                const uint4 v = *reinterpret_cast<const uint4*>(src + 8 * i);
+                memcpy(x, &v, 16);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) top = fmaxf(top, fabsf(Elem<T>::to_float(x[e])));
+              }
+              const int ex = top > 0.f && isfinite(top) ? min((int)(__float_as_uint(top) >> 23) - 127, 126) : 0;
+              f = __uint_as_float((uint32_t)(127 - ex) << 23);
+              c *= ex >= -126 ? __uint_as_float((uint32_t)(127 + ex) << 23) : 5.877471754111438e-39f;
+            }
 #pragma unroll 8
             for (int i = 0; i < D / 8; ++i) {
               T x[8];
-              const uint4 v = *reinterpret_cast<const uint4*>(src + 8 * i);
+              uint4 v = *reinterpret_cast<const uint4*>(src + 8 * i);
               memcpy(x, &v, 16);
-#pragma unroll
-              for (int e = 0; e < 8; ++e) top = fmaxf(top, fabsf(Elem<T>::to_float(x[e])));
+              v = make_uint4(M::pack(Elem<T>::to_float(x[0]) * f, Elem<T>::to_float(x[1]) * f), M::pack(Elem<T>::to_float(x[2]) * f, Elem<T>::to_float(x[3]) * f),
+                             M::pack(Elem<T>::to_float(x[4]) * f, Elem<T>::to_float(x[5]) * f), M::pack(Elem<T>::to_float(x[6]) * f, Elem<T>::to_float(x[7]) * f));
+              sts16(S::operand(rows_at, at, i), v);
             }
-            const int ex = top > 0.f && isfinite(top) ? min((int)(__float_as_uint(top) >> 23) - 127, 126) : 0;
-            f = __uint_as_float((uint32_t)(127 - ex) << 23);
-            c *= ex >= -126 ? __uint_as_float((uint32_t)(127 + ex) << 23) : 5.877471754111438e-39f;
+            sm.row_c[items % 3 * kTileRows + at] = c;
           }
-#pragma unroll 8
-          for (int i = 0; i < D / 8; ++i) {
-            T x[8];
-            uint4 v = *reinterpret_cast<const uint4*>(src + 8 * i);
-            memcpy(x, &v, 16);
-            v = make_uint4(M::pack(Elem<T>::to_float(x[0]) * f, Elem<T>::to_float(x[1]) * f), M::pack(Elem<T>::to_float(x[2]) * f, Elem<T>::to_float(x[3]) * f),
-                           M::pack(Elem<T>::to_float(x[4]) * f, Elem<T>::to_float(x[5]) * f), M::pack(Elem<T>::to_float(x[6]) * f, Elem<T>::to_float(x[7]) * f));
-            sts16(S::operand(rows_at, at, i), v);
-          }
-          sm.row_c[items % 3 * kTileRows + at] = c;
+        }
+        fence_async_proxy();
+        mbar_arrive(sm.rows_ready);
+        ++items;
+        if (kE4M3) {
+          walk.done(p, lane);
+          continue;
         }
       }
-      fence_async_proxy();
-      mbar_arrive(sm.rows_ready);
-      ++items;
       for (int u = 0; u < 2 * count; ++u) {
         const bool keys = is_keys(u, count);
         const int i = keys ? (u + 1) / 2 : (u == 2 * count - 1 ? count - 1 : u / 2 - 1), tile_key = (tile0 + i) * kTileKeys;
@@ -778,6 +795,7 @@ tree_attention_kernel(const AttnParams p, const __grid_constant__ CUtensorMap km
           // thread: one 16-byte piece of every kStep-th key, at the same place of the swizzle each time
           constexpr int kPieces = D / 16, kStep = S::kHelpers / kPieces;
           const int key0 = id / kPieces, piece = id % kPieces;
+          const bool swap = piece >= 4;                         // the two halves of an operand share banks: even pieces of one with odd ones of the other
           const uint32_t src = S::copied(from, key0, piece), lo = S::operand(to, key0, 2 * piece), hi = S::operand(to, key0, 2 * piece + 1);
 #pragma unroll
           for (int k0 = 0; k0 < kTileKeys / kStep; k0 += 4) {
@@ -793,10 +811,11 @@ tree_attention_kernel(const AttnParams p, const __grid_constant__ CUtensorMap km
                 note(non.x | non.y | non.z | non.w, key0 + (k0 + k) * kStep);
                 v[k] = make_uint4(v[k].x & ~non.x, v[k].y & ~non.y, v[k].z & ~non.z, v[k].w & ~non.w);
               }
-              sts16(lo + (k0 + k) * kStep * 128, make_uint4(e4m3x2_to_f16x2(v[k].x & 0xffffu), e4m3x2_to_f16x2(v[k].x >> 16),
-                                                            e4m3x2_to_f16x2(v[k].y & 0xffffu), e4m3x2_to_f16x2(v[k].y >> 16)));
-              sts16(hi + (k0 + k) * kStep * 128, make_uint4(e4m3x2_to_f16x2(v[k].z & 0xffffu), e4m3x2_to_f16x2(v[k].z >> 16),
-                                                            e4m3x2_to_f16x2(v[k].w & 0xffffu), e4m3x2_to_f16x2(v[k].w >> 16)));
+              const uint32_t a0 = swap ? v[k].z : v[k].x, a1 = swap ? v[k].w : v[k].y, b0 = swap ? v[k].x : v[k].z, b1 = swap ? v[k].y : v[k].w;
+              sts16((swap ? hi : lo) + (k0 + k) * kStep * 128, make_uint4(e4m3x2_to_f16x2(a0 & 0xffffu), e4m3x2_to_f16x2(a0 >> 16),
+                                                                          e4m3x2_to_f16x2(a1 & 0xffffu), e4m3x2_to_f16x2(a1 >> 16)));
+              sts16((swap ? lo : hi) + (k0 + k) * kStep * 128, make_uint4(e4m3x2_to_f16x2(b0 & 0xffffu), e4m3x2_to_f16x2(b0 >> 16),
+                                                                          e4m3x2_to_f16x2(b1 & 0xffffu), e4m3x2_to_f16x2(b1 >> 16)));
             }
           }
           mbar_arrive(sm.empty + 8 * slot);
