@@ -9,6 +9,8 @@ this module raises; there is no CPU fallback.
 from __future__ import annotations
 
 import ctypes as C
+import importlib.machinery
+import importlib.util
 import os
 from dataclasses import dataclass, field
 
@@ -342,59 +344,47 @@ def mdw_device_status(ws: torch.Tensor, stream=None) -> int:
 
 # ------------------------------------------------------- the attention sub-layer of a window
 
-# The current stream's handle; torch.cuda.current_stream() builds a stream object, which costs more than a launch.
-_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", lambda i: torch.cuda.current_stream(i).cuda_stream)
 _DT = {torch.bfloat16: DT_BF16, torch.float16: DT_F16, torch.float32: DT_F32}
 _E4M3 = (torch.float8_e4m3fn, torch.uint8)
+_bound = None
 
 
-class _On:
-    """What one call checks its tensors against: one CUDA device, made current for the launch."""
+def _binding():
+    """The extension that reads the tensors of the calls below and makes them (loaded once)."""
+    global _bound
+    if _bound is not None:
+        return _bound
+    path = os.path.join(_PKG, "_binding.so")
+    if not os.path.exists(path):
+        raise RuntimeError(f"{path} is missing: build it with moe_decode_weight_gb300.build.build()")
+    L = lib()
+    loader = importlib.machinery.ExtensionFileLoader("_binding", path)
+    m = importlib.util.module_from_spec(importlib.util.spec_from_file_location("_binding", path, loader=loader))
+    loader.exec_module(m)
+    # the raw handles: the objects that torch.cuda.current_stream() builds cost as much as a launch
+    device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+    stream = getattr(torch._C, "_cuda_getCurrentRawStream", lambda i: torch.cuda.current_stream(i).cuda_stream)
+    m.setup((torch.bfloat16, torch.float16, torch.float32, torch.float8_e4m3fn, torch.uint8, torch.int32, torch.int64, torch.uint64),
+            MdwError, device, stream, tuple(C.cast(f, C.c_void_p).value for f in
+                                            (L.w4_linear, L.mdw_kv_plan, L.mdw_kv_write, L.mdw_tree_attention)))
+    _bound = m
+    return m
 
-    def __init__(self, fn: str, t: torch.Tensor):
-        if not t.is_cuda:
-            raise MdwError(fn, 1, "tensors must be on a CUDA device")
-        self.fn, self.device = fn, t.device
 
-    def bad(self, detail: str, code: int = 1):
-        return MdwError(self.fn, code, detail)
+def _on_device(fn, device, *args):
+    """A call whose tensors are on another device than the current one."""
+    if device is not None:
+        with torch.cuda.device(device):
+            fn(*args)
 
-    def array(self, t, name: str, dtypes, shape=None):
-        """Address of a contiguous tensor of one of `dtypes` (None stays None)."""
-        if t is None:
-            return None
-        if t.dtype not in dtypes:
-            raise self.bad(f"{name} has type {t.dtype}", 3)
-        if t.device != self.device or not t.is_contiguous() or (shape is not None and t.shape != shape):
-            raise self.bad(f"{name}: {tuple(t.shape)} on {t.device}, contiguous {t.is_contiguous()}; "
-                           f"wanted {shape or 'any shape'} on {self.device}")
-        return t.data_ptr()
 
-    def rows(self, t, name: str, dtypes, shape):
-        """Address and row stride of a tensor whose rows are contiguous."""
-        if t is None:
-            return None, 0
-        if t.dtype not in dtypes:
-            raise self.bad(f"{name} has type {t.dtype}", 3)
-        if t.device != self.device or t.shape != shape:
-            raise self.bad(f"{name}: {tuple(t.shape)} on {t.device}; wanted {tuple(shape)} on {self.device}")
-        st = t.stride()
-        width = 1
-        for i in range(len(shape) - 1, 0, -1):
-            if shape[i] != 1 and st[i] != width:
-                raise self.bad(f"{name}: the elements of a row must be contiguous (strides {st})")
-            width *= shape[i]
-        return t.data_ptr(), st[0] if shape[0] != 1 else -(-width // 8) * 8
-
-    def call(self, stream, *args):
-        f = getattr(lib(), self.fn)
-        if torch.cuda.current_device() != self.device.index:
-            with torch.cuda.device(self.device):
-                code = f(*args, stream.cuda_stream if stream is not None else _raw_stream(self.device.index))
-        else:
-            code = f(*args, stream.cuda_stream if stream is not None else _raw_stream(self.device.index))
-        if code != 0:
-            raise MdwError(self.fn, code)
+def _address(fn: str, t: torch.Tensor, name: str, dtypes, device, shape=None) -> int:
+    """Address of a handle's tensor, contiguous from its second dimension on."""
+    if not t.is_cuda or t.device != device or (shape is not None and t.shape != shape) or not (t.numel() == 0 or t[0].is_contiguous()):
+        raise MdwError(fn, 1, f"{name}: {tuple(t.shape)} on {t.device}, strides {t.stride()}; wanted {shape or 'its'} shape on {device}")
+    if t.dtype not in dtypes:
+        raise MdwError(fn, 3, f"{name} has type {t.dtype}")
+    return t.data_ptr()
 
 
 @dataclass
@@ -405,31 +395,32 @@ class W4Weights:
     scale: torch.Tensor
     zero: torch.Tensor | None = None
     c: W4WeightsC = field(init=False)
+    address: int = field(init=False)
 
     def __post_init__(self):
-        on = _On("W4Weights", self.q)
-        if self.q.dim() != 2 or self.scale.dim() != 2 or self.scale.shape[0] != self.q.shape[0]:
-            raise on.bad("q is [N, K/2], scale [N, K/group]")
-        n, k, groups = self.q.shape[0], 2 * self.q.shape[1], self.scale.shape[1]
+        fn, q, scale = "W4Weights", self.q, self.scale
+        if q.dim() != 2 or scale.dim() != 2 or scale.shape[0] != q.shape[0]:
+            raise MdwError(fn, 1, "q is [N, K/2], scale [N, K/group]")
+        n, k, groups = q.shape[0], 2 * q.shape[1], scale.shape[1]
         if n < 1 or groups < 1 or k % groups != 0 or k // groups not in (32, 64, 128):
-            raise on.bad(f"{k} input features in {groups} groups: groups are 32, 64 or 128 wide", 2)
-        self.c = W4WeightsC(MDW_MAGIC, FMT_INT4_GROUP, n, k, k // groups, _DT.get(self.scale.dtype, 0),
-                            on.array(self.q, "q", (torch.uint8,)),
-                            on.array(self.scale, "scale", (torch.bfloat16, torch.float16)),
-                            on.array(self.zero, "zero", (torch.uint8,), self.scale.shape))
+            raise MdwError(fn, 2, f"{k} input features in {groups} groups: groups are 32, 64 or 128 wide")
+        for t in (q, scale, self.zero):
+            if t is not None and not t.is_contiguous():
+                raise MdwError(fn, 1, "weights are contiguous")
+        self.c = W4WeightsC(MDW_MAGIC, FMT_INT4_GROUP, n, k, k // groups, _DT.get(scale.dtype, 0),
+                            _address(fn, q, "q", (torch.uint8,), q.device),
+                            _address(fn, scale, "scale", (torch.bfloat16, torch.float16), q.device),
+                            None if self.zero is None else _address(fn, self.zero, "zero", (torch.uint8,), q.device, scale.shape))
+        self.address = C.addressof(self.c)
 
 
 def w4_linear(w: W4Weights, x: torch.Tensor, y: torch.Tensor, bias=None, residual=None, status=None,
               stream=None) -> None:
     """y = x . W^T (+ bias) (+ residual) for x [M, K], M <= 32; y [M, N] in x's type or float32."""
-    on, m, n, t = _On("w4_linear", x), x.shape[0], w.c.n, (w.scale.dtype,)
-    px, ldx = on.rows(x, "x", t, (m, w.c.k))
-    py, ldy = on.rows(y, "y", (t[0], torch.float32), (m, n))
-    pr, ldr = on.rows(residual, "residual", t, (m, n))
-    if w.q.device != on.device:
-        raise on.bad(f"weights on {w.q.device}, x on {on.device}")
-    on.call(stream, w.c, m, px, ldx, py, ldy, _DT[y.dtype], on.array(bias, "bias", t, (n,)), pr, ldr,
-            on.array(status, "status", _I32, (1,)))
+    if x.device != w.q.device:
+        raise MdwError("w4_linear", 1, f"weights on {w.q.device}, x on {x.device}")
+    f, args = _binding().w4_linear, (w, x, y, bias, residual, status, stream)
+    _on_device(f, f(*args), *args)
 
 
 @dataclass
@@ -442,27 +433,27 @@ class KVCache:
     k_scale: torch.Tensor | None = None
     v_scale: torch.Tensor | None = None
     c: KVCacheC = field(init=False)
+    address: int = field(init=False)
 
     def __post_init__(self):
-        on, k, v = _On("KVCache", self.k), self.k, self.v
+        fn, k, v = "KVCache", self.k, self.v
         if k.dim() != 4:
-            raise on.bad("k and v are [pages, kv heads, page size, head dim]")
+            raise MdwError(fn, 1, "k and v are [pages, kv heads, page size, head dim]")
         fp8 = k.dtype in _E4M3
-        dtypes = _E4M3 if fp8 else (torch.bfloat16, torch.float16)
-        pk, ldk = on.rows(k, "k", dtypes, k.shape)
-        pv, ldv = on.rows(v, "v", (k.dtype,), k.shape)
-        if ldk != ldv:
-            raise on.bad(f"k and v have page strides {ldk} and {ldv}")
-        one = (torch.float32,)
+        pk = _address(fn, k, "k", _E4M3 if fp8 else (torch.bfloat16, torch.float16), k.device)
+        pv = _address(fn, v, "v", (k.dtype,), k.device, k.shape)
+        strides = {t.stride(0) for t in (k, v)} if k.shape[0] > 1 else {k[0].numel()}
+        if len(strides) > 1:
+            raise MdwError(fn, 1, f"k and v have page strides {strides}")
         if fp8 != (self.k_scale is not None) or fp8 != (self.v_scale is not None):
-            raise on.bad("k_scale and v_scale belong to E4M3 caches, and to no other")
+            raise MdwError(fn, 1, "k_scale and v_scale belong to E4M3 caches, and to no other")
+        scales = [None, None]
+        if fp8:
+            scales = [_address(fn, t.view(1, -1), n, (torch.float32,), k.device, (1, k.shape[1]))
+                      for t, n in ((self.k_scale, "k_scale"), (self.v_scale, "v_scale"))]
         self.c = KVCacheC(MDW_MAGIC, FMT_KV_PAGED, DT_E4M3 if fp8 else _DT[k.dtype], k.shape[0], k.shape[2],
-                          k.shape[1], k.shape[3], 0, ldk, pk, pv,
-                          on.array(self.k_scale, "k_scale", one, (k.shape[1],)),
-                          on.array(self.v_scale, "v_scale", one, (k.shape[1],)))
-
-
-_I32, _I64, _MASK = (torch.int32,), (torch.int64,), (torch.int64, torch.uint64)
+                          k.shape[1], k.shape[3], 0, strides.pop(), pk, pv, *scales)
+        self.address = C.addressof(self.c)
 
 
 def mdw_kv_plan(ctx_len: torch.Tensor, new_len: torch.Tensor, page_size: int, num_pages: int,
@@ -471,54 +462,35 @@ def mdw_kv_plan(ctx_len: torch.Tensor, new_len: torch.Tensor, page_size: int, nu
                 tree_mask=None, status=None, stream=None) -> None:
     """Block tables, slot map, positions and tree masks from request lengths (see the C declaration):
     ctx_len, new_len int32 [B]; block_table int32 [B, max pages]; free_pages int32 [F]; row_start int32
-    [B + 1]; slot_map int64 [T]; positions, parents int32 [T]; tree_mask int64 or uint64 [T]."""
-    on, b, t = _On("mdw_kv_plan", ctx_len), ctx_len.numel(), slot_map.numel()
-    if block_table.dim() != 2:
-        raise on.bad("block_table is [B, max pages]")
-    on.call(stream, b, on.array(ctx_len, "ctx_len", _I32, (b,)), on.array(new_len, "new_len", _I32, (b,)), page_size,
-            num_pages, on.array(block_table, "block_table", _I32, (b, block_table.shape[1])), block_table.shape[1],
-            on.array(free_pages, "free_pages", _I32), free_pages.numel(), on.array(parents, "parents", _I32, (t,)), t,
-            on.array(row_start, "row_start", _I32, (b + 1,)), on.array(slot_map, "slot_map", _I64, (t,)),
-            on.array(positions, "positions", _I32, (t,)), on.array(tree_mask, "tree_mask", _MASK, (t,)),
-            on.array(pages_taken, "pages_taken", _I32, (1,)), on.array(status, "status", _I32, (1,)))
+    [B + 1]; slot_map int64 [T]; positions, parents int32 [T]; tree_mask int64 or uint64 [T];
+    pages_taken, status int32 [1]."""
+    f, args = _binding().kv_plan, (ctx_len, new_len, page_size, num_pages, block_table, free_pages, row_start, slot_map, positions,
+                                   pages_taken, parents, tree_mask, status, stream)
+    _on_device(f, f(*args), *args)
 
 
 def mdw_kv_write(cache: KVCache, k: torch.Tensor, v: torch.Tensor, slot_map: torch.Tensor, status=None,
                  stream=None) -> None:
     """Rows k, v [T, kv heads, head dim] (rows may be strided) to the cache's slots slot_map int64 [T]."""
-    on, t = _On("mdw_kv_write", k), slot_map.numel()
-    shape, types = (t, cache.c.kv_heads, cache.c.head_dim), (torch.bfloat16, torch.float16)
-    pk, ldk = on.rows(k, "k", types, shape)
-    pv, ldv = on.rows(v, "v", (k.dtype,), shape)
-    if cache.k.device != on.device:
-        raise on.bad(f"cache on {cache.k.device}, k on {on.device}")
-    on.call(stream, cache.c, t, pk, ldk, pv, ldv, _DT[k.dtype], on.array(slot_map, "slot_map", _I64, (t,)),
-            on.array(status, "status", _I32, (1,)))
+    if k.device != cache.k.device:
+        raise MdwError("mdw_kv_write", 1, f"cache on {cache.k.device}, k on {k.device}")
+    f, args = _binding().kv_write, (cache, k, v, slot_map, status, stream)
+    _on_device(f, f(*args), *args)
 
 
 def mdw_tree_attention_workspace_bytes(cache: KVCache, b: int, t: int, q_heads: int, max_new: int) -> int:
-    return lib().mdw_tree_attention_workspace_bytes(cache.c, b, t, q_heads, max_new)
+    with torch.cuda.device(cache.k.device):
+        return lib().mdw_tree_attention_workspace_bytes(cache.c, b, t, q_heads, max_new)
 
 
 def mdw_tree_attention(cache: KVCache, q: torch.Tensor, out: torch.Tensor, block_table: torch.Tensor,
                        ctx_len: torch.Tensor, row_start: torch.Tensor, max_new: int, ws: torch.Tensor,
                        tree_mask=None, lse=None, scale: float | None = None, status=None, stream=None) -> None:
     """Attention of the drafted rows q [T, query heads, head dim] over the paged cache (see the C
-    declaration); out like q, lse float32 [T, query heads] or None, scale head_dim ** -0.5 by default."""
-    on, b, c = _On("mdw_tree_attention", q), ctx_len.numel(), cache.c
-    if q.dim() != 3 or block_table.dim() != 2:
-        raise on.bad("q is [T, query heads, head dim], block_table [B, max pages]")
-    t, hq = q.shape[0], q.shape[1]
-    shape = (t, hq, c.head_dim)
-    pq, ldq = on.rows(q, "q", (torch.bfloat16, torch.float16), shape)
-    po, ldo = on.rows(out, "out", (q.dtype,), shape)
-    if cache.k.device != on.device:
-        raise on.bad(f"cache on {cache.k.device}, q on {on.device}")
-    if not ws.is_contiguous() or ws.device != on.device:
-        raise on.bad("ws must be contiguous and on q's device")
-    on.call(stream, c, b, t, hq, max_new, pq, ldq, _DT[q.dtype], po, ldo,
-            on.array(lse, "lse", (torch.float32,), (t, hq)),
-            on.array(block_table, "block_table", _I32, (b, block_table.shape[1])), block_table.shape[1],
-            on.array(ctx_len, "ctx_len", _I32, (b,)), on.array(row_start, "row_start", _I32, (b + 1,)),
-            on.array(tree_mask, "tree_mask", _MASK, (t,)), c.head_dim ** -0.5 if scale is None else scale,
-            on.array(status, "status", _I32, (1,)), ws.data_ptr(), ws.numel() * ws.element_size())
+    declaration); out like q, lse float32 [T, query heads] or None, scale head_dim ** -0.5 by default, ws
+    uint8 of at least mdw_tree_attention_workspace_bytes."""
+    if q.device != cache.k.device:
+        raise MdwError("mdw_tree_attention", 1, f"cache on {cache.k.device}, q on {q.device}")
+    f, args = _binding().tree_attention, (cache, q, out, block_table, ctx_len, row_start, max_new, ws, tree_mask, lse,
+                                          cache.c.head_dim ** -0.5 if scale is None else scale, status, stream)
+    _on_device(f, f(*args), *args)

@@ -11,6 +11,7 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -18,6 +19,7 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libmdw.so")
+BINDING = os.path.join(PKG, "_binding.so")            # CPython extension: argument marshalling (csrc/binding.c)
 TRACE_LIB = os.path.join(PKG, "libmdw_trace.so")     # profiling build (-DMDW_TRACE), never loaded by the API
 SOURCES = ["moe.cu", "lm_head.cu", "abi.cu", "noalloc.cu", "sampler.cu", "w4_linear.cu",
            "kv_cache.cu", "tree_attention.cu"]
@@ -43,13 +45,25 @@ def _compile(src: str, trace: bool = False) -> str:
     return obj
 
 
+def _binding() -> None:
+    tmp = BINDING + ".tmp"
+    cmd = [shutil.which("gcc") or "cc", "-O2", "-std=c11", "-Wall", "-shared", "-fPIC", "-I" + sysconfig.get_paths()["include"],
+           "-I" + INCLUDE, os.path.join(CSRC, "binding.c"), "-o", tmp]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"gcc failed on binding.c:\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, BINDING)
+
+
 def build(verbose: bool = False, trace: bool = False) -> str:
-    """Build libmdw.so (always rebuilds); returns its path. trace=True builds the profiling
+    """Build libmdw.so and _binding.so (always rebuilds); returns the library's path. trace=True builds the profiling
     library libmdw_trace.so instead: the same kernels with %globaltimer stamps at their phase
     boundaries (read by moe_decode_weight_gb300.phase_trace); the product library is untouched."""
     os.makedirs(BUILD, exist_ok=True)
     with cf.ThreadPoolExecutor(max_workers=len(SOURCES)) as ex:
         objs = list(ex.map(lambda src: _compile(src, trace), SOURCES))
+    if not trace:
+        _binding()
     out = TRACE_LIB if trace else LIB
     tmp = out + ".tmp"
     cmd = [nvcc(), *ARCH, "-shared", "-o", tmp, *objs, "-cudart", "static"]

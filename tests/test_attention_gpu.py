@@ -715,3 +715,19 @@ def test_attention_wait_that_runs_out_is_reported():
     out, lse = c.call(status=status)
     assert status.item() == 0
     c.check(out, lse)
+
+
+# ---- the binding ----------------------------------------------------------------------------------
+def test_handles_of_another_kind_are_refused():
+    kv = torch.zeros(2, 1, 16, 64, dtype=torch.bfloat16, device="cuda")
+    cache = api.KVCache(kv, kv.clone())
+    w = api.W4Weights(torch.zeros(64, 32, dtype=torch.uint8, device="cuda"), torch.zeros(64, 1, dtype=torch.bfloat16, device="cuda"))
+    x = torch.zeros(1, 64, dtype=torch.bfloat16, device="cuda")
+    rows = torch.zeros(1, 1, 64, dtype=torch.bfloat16, device="cuda")
+    cache.q, w.k = x, rows
+    with pytest.raises(api.MdwError) as e:
+        api.w4_linear(cache, x, x.clone())
+    assert e.value.code == 3
+    with pytest.raises(api.MdwError) as e:
+        api.mdw_kv_write(w, rows, rows, torch.zeros(1, dtype=torch.int64, device="cuda"))
+    assert e.value.code == 3
