@@ -22,7 +22,7 @@ LIB = os.path.join(PKG, "libmdw.so")
 BINDING = os.path.join(PKG, "_binding.so")            # CPython extension: argument marshalling (csrc/binding.c)
 TRACE_LIB = os.path.join(PKG, "libmdw_trace.so")     # profiling build (-DMDW_TRACE), never loaded by the API
 SOURCES = ["moe.cu", "lm_head.cu", "abi.cu", "noalloc.cu", "sampler.cu", "w4_linear.cu",
-           "kv_cache.cu", "tree_attention.cu"]
+           "kv_cache.cu", "tree_attention.cu", "tree_attention_rows.cu"]
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-std=c++17", "-O3", "-lineinfo", "-Xcompiler", "-fPIC", "-Xcompiler", "-fvisibility=default",

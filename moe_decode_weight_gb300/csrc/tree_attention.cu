@@ -36,190 +36,14 @@
 #include <cmath>
 #include <type_traits>
 
-#include "mdw_attn.cuh"
-#include "mdw_device.cuh"
 #include "mdw_internal.h"
+#include "tree_attention.cuh"
 
 namespace mdw {
 namespace {
 
-constexpr int kTileKeys = 128;        // keys of a tile (one pipeline stage)
-constexpr int kTileRows = 128;        // rows of a row block
-constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
-
-struct AttnParams {
-  const void* v;             // the cache's values and page stride, for keys read on their own
-  int64_t page_stride;
-  const float* k_scale;
-  const float* v_scale;
-  const void* q;
-  void* out;
-  float* lse;
-  int64_t ldq, ldo;
-  const int32_t* block_table;
-  const int32_t* ctx_len;
-  const int32_t* row_start;
-  const uint64_t* tree_mask;
-  uint32_t* status;
-  long long spin_budget;
-  float scale;
-  int B, T, Hq, Hkv, group, max_new, max_pages, num_pages, page_shift;
-  // workspace
-  int32_t* total;          // [2] tiles of the whole call, blocks with a share
-  struct Cut* cuts;        // [grid] the item that a block's share starts inside of
-  float2* part_ml;         // [2 * grid][128] (c m, sum) of partial items
-  float* part_o;           // [2 * grid][128][D] their unnormalised outputs
-};
-
-// An item that a share boundary cuts; rows = 0: the share starts with a whole item.
-struct Cut {
-  int row0, rows, first, h;        // request's first row, rows of the block (of rows x heads), its first one, kv head
-  int start, tiles;                // first tile of the item, its tiles
-};
-
-// ------------------------------------------------------------------ requests and shares
-
-// An item costs its tiles and, for its rows, its first scores and its result, as much time as this many more
-// (measured between 2 and 4): they count when the work is cut into shares.
-constexpr int kItemCost = 3;
-
-struct Request {
-  int row0, rows, ctx, keys;       // first row, rows, cached tokens, keys; rows < 0: not valid
-  __device__ __forceinline__ int blocks(const AttnParams& p) const { return (rows * p.group + kTileRows - 1) / kTileRows; }
-  __device__ __forceinline__ int tiles() const { return (keys + kTileKeys - 1) / kTileKeys; }
-  __device__ __forceinline__ int64_t work(const AttnParams& p) const {
-    return rows <= 0 ? 0 : (int64_t)p.Hkv * blocks(p) * (tiles() + kItemCost);
-  }
-};
-__device__ __forceinline__ Request load_request(const AttnParams& p, int b) {
-  Request r;
-  r.row0 = p.row_start[b];
-  const int64_t rows = (int64_t)p.row_start[b + 1] - r.row0;
-  r.ctx = p.ctx_len[b];
-  const int64_t keys = r.ctx + rows;
-  const bool ok = r.row0 >= 0 && rows >= 0 && r.row0 + rows <= p.T && rows <= p.max_new && r.ctx >= 0 &&
-                  keys <= (int64_t)p.max_pages << p.page_shift;
-  r.rows = ok ? (int)rows : -1;
-  r.keys = (int)keys;
-  return r;
-}
-
-// Equal contiguous shares of `total` units: block c has [start(c), start(c + 1)). An item's units are its tiles and
-// then its kItemCost; a share that has tiles of an item writes a partial result of it, one that ends
-// among its last units has the whole rest.
-struct Shares {
-  int blocks, base, rest;
-  __device__ __forceinline__ Shares(int total, int grid) {
-    blocks = total < grid ? total : grid;
-    base = blocks > 0 ? total / blocks : 0;
-    rest = total - base * blocks;
-  }
-  __device__ __forceinline__ int start(int c) const { return c * base + min(c, rest); }
-  __device__ __forceinline__ int owner(int t) const {
-    const int wide = rest * (base + 1);
-    return t < wide ? t / (base + 1) : rest + (t - wide) / base;
-  }
-};
-
-// The walk of one warp over its block's share, tile by tile; every warp of a block sees the same. A lane holds
-// one of 32 consecutive requests, so that the next one costs no load.
-struct Walk {
-  Request mine, r;                 // the lane's request; the current item's
-  int b, h, rb, tile, tiles;       // current item and tile, tiles of the item
-  int units;                       // units left in the share, the current item's from `tile` on first
-
-  __device__ __forceinline__ void take(int lane_) {
-    r.row0 = __shfl_sync(0xffffffffu, mine.row0, lane_);
-    r.rows = __shfl_sync(0xffffffffu, mine.rows, lane_);
-    r.ctx = __shfl_sync(0xffffffffu, mine.ctx, lane_);
-    r.keys = __shfl_sync(0xffffffffu, mine.keys, lane_);
-    tiles = r.tiles();
-  }
-  __device__ __forceinline__ void load32(const AttnParams& p, int first, int lane) {
-    mine.rows = 0;
-    if (first + lane < p.B) mine = load_request(p, first + lane);
-  }
-  __device__ void begin(const AttnParams& p, int lane) {
-    units = 0;
-    int64_t total = 0;
-    for (int i = 0; i < p.B; i += 32) {
-      load32(p, i, lane);
-      if (mine.rows < 0 && blockIdx.x == 0) raise_status(p.status, MDW_ERR_DEVICE_BOUNDS);
-      int64_t w = mine.work(p);
-#pragma unroll
-      for (int o = 16; o > 0; o >>= 1) w += __shfl_xor_sync(0xffffffffu, w, o);
-      total += w;
-    }
-    const bool many = total > 0x7fffffff;       // beyond any real batch: nothing is computed
-    if (many && blockIdx.x == 0) raise_status(p.status, MDW_ERR_UNSUPPORTED_SHAPE);
-    const Shares shares(many ? 0 : (int)total, gridDim.x);
-    if (blockIdx.x == 0 && threadIdx.x == 0) {
-      p.total[0] = many ? 0 : (int)total;
-      p.total[1] = shares.blocks;
-    }
-    if ((int)blockIdx.x >= shares.blocks) return;
-    const int at = shares.start(blockIdx.x);
-    units = shares.start(blockIdx.x + 1) - at;
-    int before = 0;
-    for (int i = 0; i < p.B; i += 32) {
-      if (p.B > 32) load32(p, i, lane);
-      const int w = (int)mine.work(p);
-      int sum = w;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int v = __shfl_up_sync(0xffffffffu, sum, o);
-        if (lane >= o) sum += v;
-      }
-      const unsigned hit = __ballot_sync(0xffffffffu, before + sum > at);
-      if (hit) {
-        const int l = __ffs(hit) - 1;
-        before += __shfl_sync(0xffffffffu, sum - w, l);
-        b = i + l;
-        take(l);
-        break;
-      }
-      before += __shfl_sync(0xffffffffu, sum, 31);
-    }
-    const int in = at - before, whole = tiles + kItemCost, item = in / whole;
-    tile = in - item * whole;
-    h = item / r.blocks(p);
-    rb = item - h * r.blocks(p);
-    Cut cut{};
-    if (tile > 0 && tile < tiles) cut = Cut{r.row0, min(r.rows * p.group - rb * kTileRows, kTileRows), rb * kTileRows, h, at - tile, tiles};
-    if (threadIdx.x == 0) p.cuts[blockIdx.x] = cut;
-    if (tile >= tiles) {                        // the tiles before belong to the last share
-      units -= whole - tile;
-      if (units > 0) next_item(p, lane);
-    }
-  }
-  // Tiles of the current item in the share; afterwards done() moves on.
-  __device__ __forceinline__ int count() const { return min(tiles - tile, units); }
-  __device__ __forceinline__ bool more() const { return units > 0; }
-  __device__ __forceinline__ void done(const AttnParams& p, int lane) {
-    units -= tiles + kItemCost - tile;
-    if (units > 0) next_item(p, lane);
-  }
-  __device__ __forceinline__ void next_item(const AttnParams& p, int lane) {
-    tile = 0;
-    if (++rb == r.blocks(p)) {
-      rb = 0;
-      if (++h == p.Hkv) {
-        h = 0;
-        do {
-          if ((++b & 31) == 0) load32(p, b, lane);
-          take(b & 31);
-        } while (r.rows <= 0);
-      }
-    }
-  }
-};
-
 // ------------------------------------------------------------------ copies and matrix steps
 
-__device__ __forceinline__ void tma_load(uint32_t dst, const CUtensorMap* map, uint32_t bar, int x, int row, int head, int page) {
-  asm volatile("cp.async.bulk.tensor.4d.shared::cta.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], [%6];"
-               :: "r"(dst), "l"(map), "r"(x), "r"(row), "r"(head), "r"(page), "r"(bar) : "memory");
-}
 // ---- tensor memory and tcgen05 (one issuing thread; a column is 32 bits of each of 128 lanes)
 __device__ __forceinline__ void tc_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void tc_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
@@ -287,48 +111,6 @@ __device__ __forceinline__ void tc_st16(uint32_t addr, const uint32_t (&r)[16]) 
 __device__ __forceinline__ void tc_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 // Generic writes to shared memory before, reads by the tensor cores after.
 __device__ __forceinline__ void fence_async_proxy() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
-__device__ __forceinline__ uint4 lds16(uint32_t a) {
-  uint4 v;
-  asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a) : "memory");
-  return v;
-}
-__device__ __forceinline__ void sts16(uint32_t a, uint4 v) {
-  asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" :: "r"(a), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
-}
-__device__ __forceinline__ float exp2_fast(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-
-// Types of the two matrix products: the query's own, f16 over an E4M3 cache (exact for its values).
-template <typename T> struct Mma;
-template <> struct Mma<__nv_bfloat16> {
-  static constexpr uint32_t kExponent = 0x7F807F80u;
-  static constexpr float kShift = 0.f;
-  static constexpr bool kBf16 = true;
-  static __device__ __forceinline__ uint32_t pack(float lo, float hi) {
-    uint32_t r;
-    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-    return r;
-  }
-};
-template <> struct Mma<__half> {
-  static constexpr uint32_t kExponent = 0x7C007C00u;
-  // f16 probabilities are kept times 2^7, so that those below 2^-14 of the largest do not lose bits, and
-  // 2^8 more (kSlack) do not overflow
-  static constexpr float kShift = 7.f;
-  static constexpr bool kBf16 = false;
-  static __device__ __forceinline__ uint32_t pack(float lo, float hi) {
-    uint32_t r;
-    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-    return r;
-  }
-};
-// The base of a row's exponents follows its maximum only when that has grown by more than this (log2): any
-// base gives the same result, and a new one costs a pass over the output in tensor memory.
-constexpr float kSlack = 8.f;
-
 // ------------------------------------------------------------------ the kernel
 
 template <typename T, bool kE4M3, int D>
@@ -386,13 +168,6 @@ struct Small {
                                    // down, the first tile of item k + 2 has its scores, so item k is done
 };
 
-// Visibility of 32 keys from `key` on (bit j: key + j) for a row with node mask `bits`.
-__device__ __forceinline__ uint32_t visible32(uint64_t bits, int key, int ctx) {
-  const int ahead = ctx - key;                                  // cached tokens among and after them
-  if (ahead >= 32) return 0xffffffffu;
-  if (ahead > 0) return ((1u << ahead) - 1u) | (uint32_t)(bits << ahead);
-  return -ahead < 64 ? (uint32_t)(bits >> -ahead) : 0u;
-}
 // Those of 32 keys of a tile (from in_tile on) that lie on a page of the cache.
 __device__ __forceinline__ uint32_t on_pages32(uint32_t bad, int in_tile, int page_shift) {
   uint32_t v = 0;
@@ -1036,15 +811,17 @@ __global__ void __launch_bounds__(128) join_kernel(const AttnParams p) {
 
 // ------------------------------------------------------------------ host
 
-// The cache as [pages][heads][page size][head dim]; a box is up to 128 rows of one page and head, 128 bytes (or
+bool few_rows(const AttnParams& p) { return p.max_new * p.group <= kFewRows; }
+
+// The cache as [pages][heads][page size][head dim]; a box is up to `most` rows of one page and head, 128 bytes (or
 // a whole 64-byte row) wide.
-bool encode_cache(CUtensorMap* map, const mdw_kv_cache* c, void* data) {
+bool encode_cache(CUtensorMap* map, const mdw_kv_cache* c, void* data, int most) {
   const bool fp8 = c->dtype == MDW_DT_E4M3;
   const cuuint64_t e = fp8 ? 1 : 2, d = c->head_dim, ps = c->page_size;
   const cuuint64_t dims[4] = {d, ps, (cuuint64_t)c->kv_heads, (cuuint64_t)c->num_pages};
   const cuuint64_t strides[3] = {d * e, d * ps * e, (cuuint64_t)c->page_stride * e};
   const cuuint32_t width = (cuuint32_t)(d * e < 128 ? d : 128 / e);
-  const cuuint32_t box[4] = {width, (cuuint32_t)(ps < kTileKeys ? ps : kTileKeys), 1, 1}, ones[4] = {1, 1, 1, 1};
+  const cuuint32_t box[4] = {width, std::min((cuuint32_t)ps, (cuuint32_t)most), 1, 1}, ones[4] = {1, 1, 1, 1};
   const EncodeTiledFn fn = encode_tiled();
   return fn && fn(map, fp8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_UINT16, 4, data, dims, strides, box, ones,
                   CU_TENSOR_MAP_INTERLEAVE_NONE, width * e == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
@@ -1067,11 +844,17 @@ AttnWs attn_ws(int grid, int D) {
 template <typename T, bool kE4M3, int D>
 cudaError_t launch(const AttnParams& p, const CUtensorMap& km, const CUtensorMap& vm, int grid, int dev, cudaStream_t s) {
   using S = Shape<T, kE4M3, D>;
-  cudaError_t e = allow_shared_memory<tree_attention_kernel<T, kE4M3, D>>(dev);
-  if (e != cudaSuccess) return e;
-  tree_attention_kernel<T, kE4M3, D><<<grid, S::kThreads, S::kSmem, s>>>(p, km, vm);
-  e = cudaGetLastError();
-  if (e != cudaSuccess) return e;
+  cudaError_t e;
+  if (few_rows(p)) {
+    e = launch_few_rows(p, std::is_same<T, __nv_bfloat16>::value, kE4M3, D, km, vm, grid, dev, s);
+    if (e != cudaSuccess) return e;
+  } else {
+    e = allow_shared_memory<tree_attention_kernel<T, kE4M3, D>>(dev);
+    if (e != cudaSuccess) return e;
+    tree_attention_kernel<T, kE4M3, D><<<grid, S::kThreads, S::kSmem, s>>>(p, km, vm);
+    e = cudaGetLastError();
+    if (e != cudaSuccess) return e;
+  }
   if (grid == 1) return cudaSuccess;
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3((unsigned)(grid - 1), (unsigned)std::min((std::min(p.max_new * p.group, kTileRows) + 3) / 4, 8));
@@ -1137,9 +920,9 @@ extern "C" mdw_status mdw_tree_attention(const mdw_kv_cache* cache, int32_t B, i
                      reinterpret_cast<Cut*>(base + lay.cuts), reinterpret_cast<float2*>(base + lay.ml),
                      reinterpret_cast<float*>(base + lay.o)};
   CUtensorMap km, vm;
-  if (!encode_cache(&km, cache, cache->k) || !encode_cache(&vm, cache, cache->v)) return MDW_ERR_CUDA;
+  const int D = cache->head_dim, most = few_rows(p) ? kFewBytes / (D * (fp8 ? 1 : 2)) : kTileKeys;
+  if (!encode_cache(&km, cache, cache->k, most) || !encode_cache(&vm, cache, cache->v, most)) return MDW_ERR_CUDA;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  const int D = cache->head_dim;
   cudaError_t e;
   if (q_dtype == MDW_DT_BF16)
     e = fp8 ? launch<__nv_bfloat16, true>(p, D, km, vm, grid, dev, s) : launch<__nv_bfloat16, false>(p, D, km, vm, grid, dev, s);

@@ -1,0 +1,502 @@
+// mdw_tree_attention for up to 16 rows a request and kv head: single tokens and short windows.
+//
+// Mathematics as in tree_attention.cu. With so few rows the tensor-memory form wastes its products (128 lanes a
+// tile, whatever the rows: 2,700 cycles a tile pair against 1,400 of an E4M3 tile's stream), and E4M3 tiles
+// would be converted in shared memory. Here one warp does everything for its keys: it copies them, forms
+// scores and outputs with m16n8k16 (16 rows x 8 keys x 16 elements), converts E4M3 codes in registers on the way
+// into the products, and keeps maximum, sum and output of its own. Nothing is shared before the end of an
+// item, so there is no barrier in the loop: the eight warps of a block take the item's stages (4 KB of keys and of
+// values, three of them in flight per warp, 192 KB per SM) in turn, and join once per item.
+//
+// Order of elements and keys. A contraction may take its index in any order if both operands do: lane (g, q) of a
+// product (g = 0..7, q = 0..3) has keys q and q + 4 of eight as its two columns, and 16 bytes in a row of a key as
+// its elements, so that every load of keys or values is 16 bytes wide and without bank conflicts in the
+// swizzled tiles.
+#include <type_traits>
+
+#include "mdw_internal.h"
+#include "tree_attention.cuh"
+
+namespace mdw {
+namespace {
+
+constexpr int kWarps = 8, kStages = 3;
+
+template <typename T, bool kE4M3, int D>
+struct Few {
+  using C = typename std::conditional<kE4M3, __half, T>::type;     // type of the products
+  static constexpr int kBytes = kE4M3 ? 1 : 2;
+  static constexpr int kKeys = kFewBytes / (D * kBytes);           // keys of a stage
+  static constexpr int kRowBytes = D * kBytes < 128 ? D * kBytes : 128, kHalves = D * kBytes / kRowBytes;
+  static constexpr int kStageBytes = 2 * kFewBytes;                // keys, then values
+  static constexpr int kPitch = D + 4;                             // floats of a joined row
+  static constexpr int kJoinAt = kWarps * kStages * kStageBytes, kSmall = kJoinAt + kWarps / 2 * kFewRows * kPitch * 4;
+  static constexpr int kSmem = kSmall + kWarps * kFewRows * 8 + kWarps * kStages * 8 + 16;
+
+  static __device__ __forceinline__ uint32_t piece(uint32_t tile, int key, int i) {   // 16 bytes of a key's row
+    if constexpr (kRowBytes == 128) return tile + (i >> 3) * (kKeys * 128) + key * 128 + (((i & 7) ^ (key & 7)) << 4);
+    else return tile + key * 64 + ((i ^ ((key >> 1) & 3)) << 4);
+  }
+  // Element that output column g of tile t holds; the lanes of a pair of columns are far apart for the loads' sake.
+  static __device__ __forceinline__ int element(int t, int g) {
+    if constexpr (kE4M3) return (D / 8) * ((g & 1) << 2 | g >> 1) + t;
+    else return 8 * t + g;
+  }
+};
+
+template <typename C>
+__device__ __forceinline__ void mma16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  if constexpr (std::is_same<C, __nv_bfloat16>::value)
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3]) : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+  else
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3]) : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ void load_transposed(uint32_t (&v)[4], uint32_t a) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]) : "r"(a) : "memory");
+}
+__device__ __forceinline__ uint2 lds8(uint32_t a) {
+  uint2 v;
+  asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(a) : "memory");
+  return v;
+}
+
+// Stages of the walk's current item that lie in the block's share, and the warp's place among them: stages go to the
+// warps in turn, on from where the item before stopped.
+template <int kKeys>
+struct Stages {
+  int n, i, before;                // stages of the item; the warp's next one; stages of the items before
+  __device__ __forceinline__ void item(const Walk& w, int warp) {
+    const int keys = min(w.r.keys, (w.tile + w.count()) * kTileKeys) - w.tile * kTileKeys;
+    n = (keys + kKeys - 1) / kKeys;
+    i = (warp - before) & (kWarps - 1);
+  }
+};
+
+template <typename T, bool kE4M3, int D>
+__global__ void __launch_bounds__(32 * kWarps, 1)
+few_rows_kernel(const AttnParams p, const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap) {
+  using S = Few<T, kE4M3, D>;
+  using C = typename S::C;
+  using M = Mma<C>;
+  constexpr int kOctets = S::kKeys / 8, kOut = D / 8, kSteps = D / 16;
+  extern __shared__ __align__(1024) uint8_t smem[];
+  const uint32_t base = smem_u32(smem);
+  const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31, g = lane >> 2, q = lane & 3;
+  float2* ml = reinterpret_cast<float2*>(smem + S::kSmall);     // [warp][16] (c m, sum)
+  const uint32_t bars = base + S::kSmall + kWarps * kFewRows * 8 + warp * kStages * 8;
+  volatile int* dead = reinterpret_cast<volatile int*>(smem + S::kSmall + kWarps * kFewRows * 8 + kWarps * kStages * 8);
+  const uint32_t ring = base + warp * kStages * S::kStageBytes;
+  if (base & 1023) {                                            // the swizzled tiles need the alignment asked for above
+    if (threadIdx.x == 0) raise_status(p.status, MDW_ERR_UNSUPPORTED_SHAPE);
+    if (blockIdx.x == 0 && threadIdx.x == 0) p.total[0] = p.total[1] = 0;
+    return;
+  }
+  if (threadIdx.x == 0) *dead = 0;
+  if (lane == 0) {
+    for (int i = 0; i < kStages; ++i) mbar_init(bars + 8 * i, 1);
+    mbar_init_fence();
+  }
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  Walk walk;
+  walk.begin(p, lane);
+  if (!walk.more()) return;                                     // the whole block
+  __syncthreads();                                              // *dead
+
+  // ---- copies, ahead of the products by the ring's stages: a walk of their own. The lanes hold the page ids of the
+  // item's next stages (kPages of them a stage), loaded a batch early.
+  const int box_rows = min(1 << p.page_shift, S::kKeys), pages = S::kKeys / box_rows, batch = 32 / pages;
+  const uint32_t page_bytes = (uint32_t)box_rows * D * S::kBytes;
+  Walk ask = walk;
+  Stages<S::kKeys> to;
+  to.before = 0;
+  int asked = 0, slot_to = 0, in_batch = 0, ids = -1, next_ids = -1;
+  uint32_t bads = 0;                                            // 4 bits per slot: pages outside the cache
+  auto look = [&](int first) {                                  // stage `first` of the item and the warp's next ones
+    const int key = ask.tile * kTileKeys + (first + lane / pages * kWarps) * S::kKeys + lane % pages * box_rows;
+    if (first + lane / pages * kWarps >= to.n || key >= ask.r.keys) return -1;
+    const int id = p.block_table[(size_t)ask.b * p.max_pages + (key >> p.page_shift)];
+    return id >= 0 && id < p.num_pages ? id : -2;
+  };
+  auto ask_item = [&]() {                                       // the first item on from here with a stage for this warp
+    for (;;) {
+      to.item(ask, warp);
+      if (to.i < to.n) break;
+      to.before += to.n;
+      ask.done(p, lane);
+      if (!ask.more()) return;
+    }
+    ids = look(to.i);
+    next_ids = look(to.i + batch * kWarps);
+    in_batch = 0;
+  };
+  auto request = [&]() {
+    const int id = __shfl_sync(0xffffffffu, ids, (in_batch * pages + lane) & 31);
+    const bool mine = lane < pages;
+    const unsigned good = __ballot_sync(0xffffffffu, mine && id >= 0), bad = __ballot_sync(0xffffffffu, mine && id == -2);
+    const uint32_t bar = bars + 8 * slot_to, at = ring + slot_to * S::kStageBytes;
+    if (lane == 0) {
+      if (bad) raise_status(p.status, MDW_ERR_DEVICE_BOUNDS);
+      mbar_arrive_tx(bar, 2 * page_bytes * __popc(good));
+    }
+    __syncwarp();
+    bads = (bads & ~(15u << 4 * slot_to)) | bad << 4 * slot_to;
+    if (mine && id >= 0) {
+      const int row = (ask.tile * kTileKeys + to.i * S::kKeys + lane * box_rows) & ((1 << p.page_shift) - 1);
+#pragma unroll
+      for (int k = 0; k < S::kHalves; ++k) {
+        const uint32_t dst = at + k * (S::kKeys * S::kRowBytes) + lane * box_rows * S::kRowBytes;
+        tma_load(dst, &kmap, bar, k * (S::kRowBytes / S::kBytes), row, ask.h, id);
+        tma_load(dst + kFewBytes, &vmap, bar, k * (S::kRowBytes / S::kBytes), row, ask.h, id);
+      }
+    }
+    __syncwarp();
+    ++asked;
+    if (++slot_to == kStages) slot_to = 0;
+    to.i += kWarps;
+    if (to.i >= to.n) {
+      to.before += to.n;
+      ask.done(p, lane);
+      if (ask.more()) ask_item();
+    } else if (++in_batch == batch) {
+      in_batch = 0;
+      ids = next_ids;
+      next_ids = look(to.i + batch * kWarps);
+    }
+  };
+  ask_item();
+  for (int i = 0; i < kStages && ask.more(); ++i) request();
+
+  Stages<S::kKeys> at;
+  at.before = 0;
+  int slot = 0;
+  uint32_t phase = 0;
+  while (walk.more()) {
+    const Request r = walk.r;
+    const int rows = r.rows * p.group, tile0 = walk.tile, count = walk.count(), h = walk.h;
+    const bool whole = count == walk.tiles;
+    at.item(walk, warp);
+    // ---- rows g and g + 8 of the item, four elements of each per step; the nodes they see; c
+    uint32_t qf[kSteps][4];
+    uint64_t bits[2];
+    float c[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int row = g + 8 * i, node = row / p.group;
+      const bool valid = row < rows;
+      bits[i] = 0;
+      if (valid) {
+        bits[i] = (p.tree_mask ? p.tree_mask[r.row0 + node] : ~0ull >> (63 - node)) & ((1ull << r.rows) - 1);
+      }
+      c[i] = p.scale * kLog2e * (kE4M3 ? p.k_scale[h] : 1.f);
+      const T* src = static_cast<const T*>(p.q) + (valid ? (int64_t)(r.row0 + node) * p.ldq + (int64_t)(h * p.group + row - node * p.group) * D : 0);
+#pragma unroll
+      for (int st = 0; st < kSteps; ++st) {
+        const int d = kE4M3 ? 16 * (q + 4 * (st >> 2)) + 4 * (st & 3) : 64 * (st >> 2) + 8 * (q + 4 * (st >> 1 & 1)) + 4 * (st & 1);
+        const uint2 v = valid ? *reinterpret_cast<const uint2*>(src + d) : make_uint2(0u, 0u);
+        qf[st][i] = v.x;
+        qf[st][2 + i] = v.y;
+      }
+      if constexpr (kE4M3 && std::is_same<T, __nv_bfloat16>::value) {
+        // bf16 rows enter f16 times a power of two that puts their largest element in [1, 4)
+        auto low = [](uint32_t v) { return __uint_as_float(v << 16); };
+        auto high = [](uint32_t v) { return __uint_as_float(v & 0xffff0000u); };
+        float top = 0.f;
+#pragma unroll
+        for (int st = 0; st < kSteps; ++st)
+#pragma unroll
+          for (int j = i; j < 4; j += 2) top = fmaxf(top, fmaxf(fabsf(low(qf[st][j])), fabsf(high(qf[st][j]))));
+        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+        const int ex = top > 0.f && isfinite(top) ? min((int)(__float_as_uint(top) >> 23) - 127, 126) : 0;
+        const float f = __uint_as_float((uint32_t)(127 - ex) << 23);
+        c[i] *= ex >= -126 ? __uint_as_float((uint32_t)(127 + ex) << 23) : 5.877471754111438e-39f;
+#pragma unroll
+        for (int st = 0; st < kSteps; ++st)
+#pragma unroll
+          for (int j = i; j < 4; j += 2) qf[st][j] = M::pack(low(qf[st][j]) * f, high(qf[st][j]) * f);
+      }
+    }
+    float o[kOut][4], mc[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
+#pragma unroll
+    for (int t = 0; t < kOut; ++t) o[t][0] = o[t][1] = o[t][2] = o[t][3] = 0.f;
+
+    for (; at.i < at.n; at.i += kWarps) {
+      const int key0 = tile0 * kTileKeys + at.i * S::kKeys;
+      mbar_wait(bars + 8 * slot, phase, p.spin_budget, p.status, dead);
+      __syncwarp();
+      const uint32_t bad = bads >> 4 * slot & 15, keys = ring + slot * S::kStageBytes, values = keys + kFewBytes;
+      const bool all = key0 + S::kKeys <= r.ctx && bad == 0;    // every row sees every key
+      // ---- scores; columns 2 q and 2 q + 1 of octet n: keys 8 n + q and 8 n + q + 4
+      float s[kOctets][4];
+#pragma unroll
+      for (int n = 0; n < kOctets; ++n) {
+        const int key = 8 * n + ((g & 1) << 2 | g >> 1);
+        s[n][0] = s[n][1] = s[n][2] = s[n][3] = 0.f;
+        if constexpr (kE4M3) {
+#pragma unroll
+          for (int j = 0; j < kSteps / 4; ++j) {
+            const uint4 v = lds16(S::piece(keys, key, q + 4 * j));
+            const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+            for (int i = 0; i < 4; ++i) mma16<C>(s[n], qf[4 * j + i], e4m3x2_to_f16x2(w[i] & 0xffffu), e4m3x2_to_f16x2(w[i] >> 16));
+          }
+        } else {
+#pragma unroll
+          for (int j = 0; j < kSteps / 2; ++j) {
+            const uint4 v = lds16(S::piece(keys, key, 8 * (j >> 1) + q + 4 * (j & 1)));
+            mma16<C>(s[n], qf[2 * j], v.x, v.y);
+            mma16<C>(s[n], qf[2 * j + 1], v.z, v.w);
+          }
+        }
+      }
+      uint32_t see[2][(S::kKeys + 31) / 32], there[(S::kKeys + 31) / 32];   // keys that the rows see; that exist
+      if (!all) {
+#pragma unroll
+        for (int j = 0; j < (S::kKeys + 31) / 32; ++j) {
+          uint32_t on = 0;                                      // keys on pages of the cache
+#pragma unroll
+          for (int k = 0; k < 32 && k < S::kKeys; k += 16)
+            if (!(bad >> (32 * j + k) / box_rows & 1)) on |= 0xffffu << k;
+          there[j] = on & visible32((1ull << r.rows) - 1, key0 + 32 * j, r.ctx);
+#pragma unroll
+          for (int i = 0; i < 2; ++i) see[i][j] = on & visible32(bits[i], key0 + 32 * j, r.ctx);
+        }
+#pragma unroll
+        for (int n = 0; n < kOctets; ++n)
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            if (!(see[e >> 1][n / 4] >> (8 * (n & 3) + q + 4 * (e & 1)) & 1)) s[n][e] = -INFINITY;
+      }
+      // ---- exponentials; the base of a row's exponents moves only when its maximum has grown by more than kSlack
+      float now[2];
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        float top = -INFINITY;
+#pragma unroll
+        for (int n = 0; n < kOctets; ++n) top = fmaxf(top, fmaxf(s[n][2 * i], s[n][2 * i + 1]));
+        now[i] = top == -INFINITY ? -INFINITY : fmaf(top, c[i], -M::kShift);
+      }
+      if (__any_sync(0xffffffffu, now[0] > mc[0] + kSlack || now[1] > mc[1] + kSlack)) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          now[i] = fmaxf(now[i], __shfl_xor_sync(0xffffffffu, now[i], 1));
+          now[i] = fmaxf(now[i], __shfl_xor_sync(0xffffffffu, now[i], 2));
+          const bool grown = now[i] > mc[i] + kSlack;           // also from -inf
+          const float f = grown ? (mc[i] == -INFINITY ? 0.f : exp2_fast(mc[i] - now[i])) : 1.f;
+          if (grown) mc[i] = now[i];
+          l[i] *= f;
+#pragma unroll
+          for (int t = 0; t < kOut; ++t) {
+            o[t][2 * i] *= f;
+            o[t][2 * i + 1] *= f;
+          }
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const float from = mc[i] == -INFINITY ? 0.f : mc[i];
+        float sum[2] = {0.f, 0.f};
+#pragma unroll
+        for (int n = 0; n < kOctets; ++n)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            s[n][2 * i + e] = exp2_fast(fmaf(s[n][2 * i + e], c[i], -from));
+            sum[e] += s[n][2 * i + e];
+          }
+        l[i] += sum[0] + sum[1];
+      }
+      // ---- outputs, 16 keys at a time. The probabilities are rounded to the products' type, as the values are
+#pragma unroll
+      for (int k = 0; k < kOctets / 2; ++k) {
+        const uint32_t pf[4] = {M::pack(s[2 * k][0], s[2 * k][1]), M::pack(s[2 * k][2], s[2 * k][3]),
+                                M::pack(s[2 * k + 1][0], s[2 * k + 1][1]), M::pack(s[2 * k + 1][2], s[2 * k + 1][3])};
+        uint32_t odd = 0;                                       // keys (of the 16) with values that are not finite, where not every row sees all
+        if constexpr (kE4M3) {
+          constexpr int kWords = D / 32;
+          uint32_t v[4][kWords];
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const int key = 16 * k + 4 * j + q, unit = (g & 1) << 2 | g >> 1;
+            if constexpr (D == 128) {
+              const uint4 x = lds16(S::piece(values, key, unit));
+              v[j][0] = x.x, v[j][1] = x.y, v[j][2] = x.z, v[j][3] = x.w;
+            } else {
+              const uint2 x = lds8(S::piece(values, key, unit >> 1) + (unit & 1) * 8);
+              v[j][0] = x.x, v[j][1] = x.y;
+            }
+            if (!all)
+#pragma unroll
+              for (int w = 0; w < kWords; ++w) {
+                const uint32_t non = __vcmpeq4(v[j][w] & 0x7f7f7f7fu, 0x7f7f7f7fu);   // the only non-finite code is S.1111.111
+                v[j][w] &= ~non;
+                if (non) odd |= 1u << (4 * j + q);
+              }
+          }
+#pragma unroll
+          for (int w = 0; w < kWords; ++w)
+#pragma unroll
+            for (int b = 0; b < 4; b += 2) {
+              const uint32_t x = __byte_perm(v[0][w], v[1][w], b == 0 ? 0x5140 : 0x7362), y = __byte_perm(v[2][w], v[3][w], b == 0 ? 0x5140 : 0x7362);
+              mma16<C>(o[4 * w + b], pf, e4m3x2_to_f16x2(x & 0xffffu), e4m3x2_to_f16x2(y & 0xffffu));
+              mma16<C>(o[4 * w + b + 1], pf, e4m3x2_to_f16x2(x >> 16), e4m3x2_to_f16x2(y >> 16));
+            }
+        } else {
+          const int key = 16 * k + (lane & 8) + ((lane & 7) >> 1) + 4 * (lane & 1);
+#pragma unroll
+          for (int t = 0; t < kOut; t += 2) {
+            uint32_t v[4];
+            load_transposed(v, S::piece(values, key, t + (lane >> 4)));
+            if (!all)
+#pragma unroll
+              for (int j = 0; j < 4; ++j) {
+                const uint32_t non = __vcmpeq2(v[j] & M::kExponent, M::kExponent);
+                v[j] &= ~non;
+                if (non & 0xffffu) odd |= 1u << (8 * (j & 1) + q);
+                if (non >> 16) odd |= 1u << (8 * (j & 1) + q + 4);
+              }
+            mma16<C>(o[t], pf, v[0], v[1]);
+            mma16<C>(o[t + 1], pf, v[2], v[3]);
+          }
+        }
+        if (!all) {
+          odd = __reduce_or_sync(0xffffffffu, odd) & there[k / 2] >> (16 * (k & 1));
+          // rare: the rows that see such a key add what was taken out
+          for (; odd; odd &= odd - 1) {
+            const int x = __ffs(odd) - 1, from = (lane & ~3) | (x & 3);
+            const float up = x & 8 ? (x & 4 ? s[2 * k + 1][1] : s[2 * k + 1][0]) : (x & 4 ? s[2 * k][1] : s[2 * k][0]);
+            const float down = x & 8 ? (x & 4 ? s[2 * k + 1][3] : s[2 * k + 1][2]) : (x & 4 ? s[2 * k][3] : s[2 * k][2]);
+            const float pk[2] = {__shfl_sync(0xffffffffu, up, from), __shfl_sync(0xffffffffu, down, from)};
+#pragma unroll
+            for (int t = 0; t < kOut; ++t)
+#pragma unroll
+              for (int e = 0; e < 2; ++e) {
+                const int d = S::element(t, 2 * q + e), key = 16 * k + x;
+                const uint32_t a = S::piece(values, key, d * S::kBytes / 16) + d * S::kBytes % 16;
+                float f;
+                if constexpr (kE4M3) {
+                  uint32_t code;
+                  asm volatile("ld.shared.u8 %0, [%1];" : "=r"(code) : "r"(a) : "memory");
+                  f = __half2float(__ushort_as_half((unsigned short)e4m3x2_to_f16x2(code)));
+                } else {
+                  T y;
+                  unsigned short code;
+                  asm volatile("ld.shared.u16 %0, [%1];" : "=h"(code) : "r"(a) : "memory");
+                  memcpy(&y, &code, 2);
+                  f = Elem<T>::to_float(y);
+                }
+#pragma unroll
+                for (int i = 0; i < 2; ++i)
+                  if (!isfinite(f) && (see[i][k / 2] >> (16 * (k & 1) + x) & 1)) o[t][2 * i + e] += pk[i] * f;
+              }
+          }
+        }
+      }
+      __syncwarp();                                             // the slot is read
+      if (++slot == kStages) { slot = 0; phase ^= 1; }
+      if (ask.more() && !__any_sync(0xffffffffu, *dead)) request();
+    }
+    at.before += at.n;
+
+    // ---- the item's result: the warps' outputs on one base, four at a time added up in shared memory
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      l[i] += __shfl_xor_sync(0xffffffffu, l[i], 1);
+      l[i] += __shfl_xor_sync(0xffffffffu, l[i], 2);
+      if (q == 0) ml[warp * kFewRows + g + 8 * i] = make_float2(mc[i], l[i]);
+    }
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      float m = -INFINITY;
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) m = fmaxf(m, ml[w * kFewRows + g + 8 * i].x);
+      const float f = exp2_fast(mc[i] - (m == -INFINITY ? 0.f : m));
+#pragma unroll
+      for (int t = 0; t < kOut; ++t) {
+        o[t][2 * i] *= f;
+        o[t][2 * i + 1] *= f;
+      }
+    }
+    float* place = reinterpret_cast<float*>(smem + S::kJoinAt) + (warp & 3) * (kFewRows * S::kPitch);
+    auto each = [&](auto&& f) {                                 // the lane's outputs and their place
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+#pragma unroll
+        for (int t = 0; t < kOut; ++t)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) f(o[t][2 * i + e], place[(g + 8 * i) * S::kPitch + S::element(t, 2 * q + e)]);
+    };
+    if (warp >= 4) each([](float& mine, float& there) { there = mine; });
+    __syncthreads();
+    if (warp < 4) each([](float& mine, float& there) { there += mine; });
+    __syncthreads();
+    {
+      constexpr int kCols = D / 16;
+      const int row = threadIdx.x >> 4, d = (threadIdx.x & 15) * kCols, node = row / p.group;
+      float m = -INFINITY, sum = 0.f, v[kCols];
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) m = fmaxf(m, ml[w * kFewRows + row].x);
+      const float from = m == -INFINITY ? 0.f : m;
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) sum += ml[w * kFewRows + row].y * exp2_fast(ml[w * kFewRows + row].x - from);
+      const float* joined = reinterpret_cast<const float*>(smem + S::kJoinAt) + row * S::kPitch + d;
+#pragma unroll
+      for (int j = 0; j < kCols; j += 4) {
+        float4 x = *reinterpret_cast<const float4*>(joined + j);
+#pragma unroll
+        for (int w = 1; w < 4; ++w) {
+          const float4 y = *reinterpret_cast<const float4*>(joined + w * kFewRows * S::kPitch + j);
+          x.x += y.x, x.y += y.y, x.z += y.z, x.w += y.w;
+        }
+        v[j] = x.x, v[j + 1] = x.y, v[j + 2] = x.z, v[j + 3] = x.w;
+      }
+      if (row < rows && !*dead) {
+        if (whole) {
+          const float f = sum == 0.f ? 0.f : (kE4M3 ? p.v_scale[h] : 1.f) / sum;
+          const int head = h * p.group + row - node * p.group;
+          T* dst = static_cast<T*>(p.out) + (int64_t)(r.row0 + node) * p.ldo + (int64_t)head * D + d;
+          uint32_t packed[kCols / 2];
+#pragma unroll
+          for (int j = 0; j < kCols; j += 2) packed[j / 2] = sum == 0.f ? 0u : Mma<T>::pack(v[j] * f, v[j + 1] * f);
+          if constexpr (kCols == 8) *reinterpret_cast<uint4*>(dst) = make_uint4(packed[0], packed[1], packed[2], packed[3]);
+          else *reinterpret_cast<uint2*>(dst) = make_uint2(packed[0], packed[1]);
+          if (p.lse && d == 0) p.lse[(int64_t)(r.row0 + node) * p.Hq + head] = sum == 0.f ? -INFINITY : (m + log2f(sum)) * kLn2;
+        } else {
+          const size_t part = (size_t)(2 * blockIdx.x + (tile0 > 0 ? 0 : 1)) * kTileRows + row;
+#pragma unroll
+          for (int j = 0; j < kCols; j += 4) *reinterpret_cast<float4*>(p.part_o + part * D + d + j) = make_float4(v[j], v[j + 1], v[j + 2], v[j + 3]);
+          if (d == 0) p.part_ml[part] = make_float2(m, sum);
+        }
+      }
+    }
+    walk.done(p, lane);
+    __syncthreads();                                            // sums and outputs are read; the next item may write
+  }
+  // copies that a block given up did not wait for
+  if (*dead)
+    for (int i = max(asked - kStages, 0); i < asked; ++i) mbar_drain(bars + 8 * (i % kStages), i / kStages & 1);
+}
+
+template <typename T, bool kE4M3, int D>
+cudaError_t launch(const AttnParams& p, const CUtensorMap& km, const CUtensorMap& vm, int grid, int dev, cudaStream_t s) {
+  const cudaError_t e = allow_shared_memory<few_rows_kernel<T, kE4M3, D>>(dev);
+  if (e != cudaSuccess) return e;
+  few_rows_kernel<T, kE4M3, D><<<grid, 32 * kWarps, Few<T, kE4M3, D>::kSmem, s>>>(p, km, vm);
+  return cudaGetLastError();
+}
+template <typename T>
+cudaError_t launch(const AttnParams& p, bool e4m3, int D, const CUtensorMap& km, const CUtensorMap& vm, int grid, int dev, cudaStream_t s) {
+  if (D == 64) return e4m3 ? launch<T, true, 64>(p, km, vm, grid, dev, s) : launch<T, false, 64>(p, km, vm, grid, dev, s);
+  return e4m3 ? launch<T, true, 128>(p, km, vm, grid, dev, s) : launch<T, false, 128>(p, km, vm, grid, dev, s);
+}
+
+}  // namespace
+
+cudaError_t launch_few_rows(const AttnParams& p, bool bf16, bool e4m3, int D, const CUtensorMap& km, const CUtensorMap& vm, int grid, int dev, cudaStream_t s) {
+  return bf16 ? launch<__nv_bfloat16>(p, e4m3, D, km, vm, grid, dev, s) : launch<__half>(p, e4m3, D, km, vm, grid, dev, s);
+}
+
+}  // namespace mdw
