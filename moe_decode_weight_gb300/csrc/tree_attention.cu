@@ -920,7 +920,8 @@ extern "C" mdw_status mdw_tree_attention(const mdw_kv_cache* cache, int32_t B, i
                      reinterpret_cast<Cut*>(base + lay.cuts), reinterpret_cast<float2*>(base + lay.ml),
                      reinterpret_cast<float*>(base + lay.o)};
   CUtensorMap km, vm;
-  const int D = cache->head_dim, most = few_rows(p) ? kFewBytes / (D * (fp8 ? 1 : 2)) : kTileKeys;
+  const int D = cache->head_dim, key_bytes = D * (fp8 ? 1 : 2);
+  const int most = few_rows(p) ? few_rows_operand(key_bytes, few_rows_blocks(p)) / key_bytes : kTileKeys;
   if (!encode_cache(&km, cache, cache->k, most) || !encode_cache(&vm, cache, cache->v, most)) return MDW_ERR_CUDA;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   cudaError_t e;

@@ -20,18 +20,21 @@
 namespace mdw {
 namespace {
 
-constexpr int kWarps = 8, kStages = 3;
+constexpr int kWarps = 8;
 
-template <typename T, bool kE4M3, int D>
+// kBlocks warps share the copies of a ring and have 16 rows each.
+template <typename T, bool kE4M3, int D, int kBlocks>
 struct Few {
   using C = typename std::conditional<kE4M3, __half, T>::type;     // type of the products
   static constexpr int kBytes = kE4M3 ? 1 : 2;
-  static constexpr int kKeys = kFewBytes / (D * kBytes);           // keys of a stage
+  static constexpr int kOperand = few_rows_operand(D * kBytes, kBlocks), kKeys = kOperand / (D * kBytes);   // of a stage: bytes of keys; keys
   static constexpr int kRowBytes = D * kBytes < 128 ? D * kBytes : 128, kHalves = D * kBytes / kRowBytes;
-  static constexpr int kStageBytes = 2 * kFewBytes;                // keys, then values
+  static constexpr int kStageBytes = 2 * kOperand;                 // keys, then values
+  static constexpr int kRings = kWarps / kBlocks, kStages = 3 * kBlocks * 4096 / kOperand, kRows = 16 * kBlocks;
   static constexpr int kPitch = D + 4;                             // floats of a joined row
-  static constexpr int kJoinAt = kWarps * kStages * kStageBytes, kSmall = kJoinAt + kWarps / 2 * kFewRows * kPitch * 4;
-  static constexpr int kSmem = kSmall + kWarps * kFewRows * 8 + kWarps * kStages * 8 + 16;
+  static constexpr int kJoinAt = kRings * kStages * kStageBytes, kSmall = kJoinAt + kWarps / 2 * 16 * kPitch * 4;
+  static constexpr int kBarsAt = kSmall + kWarps * 16 * 8, kBadAt = kBarsAt + 2 * kRings * kStages * 8;
+  static constexpr int kSmem = kBadAt + kRings * kStages * 4 + 16;
 
   static __device__ __forceinline__ uint32_t piece(uint32_t tile, int key, int i) {   // 16 bytes of a key's row
     if constexpr (kRowBytes == 128) return tile + (i >> 3) * (kKeys * 128) + key * 128 + (((i & 7) ^ (key & 7)) << 4);
@@ -63,99 +66,103 @@ __device__ __forceinline__ uint2 lds8(uint32_t a) {
   return v;
 }
 
-// Stages of the walk's current item that lie in the block's share, and the warp's place among them: stages go to the
-// warps in turn, on from where the item before stopped.
-template <int kKeys>
+// Stages of the walk's current item that lie in the block's share, and the ring's place among them: stages go to the
+// rings in turn, on from where the item before stopped.
+template <int kKeys, int kRings>
 struct Stages {
-  int n, i, before;                // stages of the item; the warp's next one; stages of the items before
-  __device__ __forceinline__ void item(const Walk& w, int warp) {
+  int n, i, before;                // stages of the item; the ring's next one; stages of the items before
+  __device__ __forceinline__ void item(const Walk& w, int ring) {
     const int keys = min(w.r.keys, (w.tile + w.count()) * kTileKeys) - w.tile * kTileKeys;
     n = (keys + kKeys - 1) / kKeys;
-    i = (warp - before) & (kWarps - 1);
+    i = (ring - before) & (kRings - 1);
   }
 };
 
-template <typename T, bool kE4M3, int D>
+template <typename T, bool kE4M3, int D, int kBlocks>
 __global__ void __launch_bounds__(32 * kWarps, 1)
 few_rows_kernel(const AttnParams p, const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap) {
-  using S = Few<T, kE4M3, D>;
+  using S = Few<T, kE4M3, D, kBlocks>;
   using C = typename S::C;
   using M = Mma<C>;
-  constexpr int kOctets = S::kKeys / 8, kOut = D / 8, kSteps = D / 16;
+  constexpr int kOctets = S::kKeys / 8, kOut = D / 8, kSteps = D / 16, kStages = S::kStages, kRings = S::kRings;
   extern __shared__ __align__(1024) uint8_t smem[];
   const uint32_t base = smem_u32(smem);
   const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31, g = lane >> 2, q = lane & 3;
+  const int mine = warp / kBlocks, row0 = warp % kBlocks * 16;  // the warp's ring; first of its rows
   float2* ml = reinterpret_cast<float2*>(smem + S::kSmall);     // [warp][16] (c m, sum)
-  const uint32_t bars = base + S::kSmall + kWarps * kFewRows * 8 + warp * kStages * 8;
-  volatile int* dead = reinterpret_cast<volatile int*>(smem + S::kSmall + kWarps * kFewRows * 8 + kWarps * kStages * 8);
-  const uint32_t ring = base + warp * kStages * S::kStageBytes;
+  const uint32_t full = base + S::kBarsAt + mine * kStages * 16, empty = full + kStages * 8;
+  volatile uint32_t* bads = reinterpret_cast<volatile uint32_t*>(smem + S::kBadAt) + mine * kStages;   // per slot: pages outside the cache
+  volatile int* dead = reinterpret_cast<volatile int*>(smem + S::kBadAt + kRings * kStages * 4);
+  const uint32_t ring = base + mine * kStages * S::kStageBytes;
   if (base & 1023) {                                            // the swizzled tiles need the alignment asked for above
     if (threadIdx.x == 0) raise_status(p.status, MDW_ERR_UNSUPPORTED_SHAPE);
     if (blockIdx.x == 0 && threadIdx.x == 0) p.total[0] = p.total[1] = 0;
     return;
   }
   if (threadIdx.x == 0) *dead = 0;
-  if (lane == 0) {
-    for (int i = 0; i < kStages; ++i) mbar_init(bars + 8 * i, 1);
+  if (row0 == 0 && lane == 0) {
+    for (int i = 0; i < kStages; ++i) {
+      mbar_init(full + 8 * i, 1);
+      mbar_init(empty + 8 * i, kBlocks);
+    }
     mbar_init_fence();
   }
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   Walk walk;
   walk.begin(p, lane);
   if (!walk.more()) return;                                     // the whole block
-  __syncthreads();                                              // *dead
+  __syncthreads();                                              // barriers, *dead
 
-  // ---- copies, ahead of the products by the ring's stages: a walk of their own. The lanes hold the page ids of the
-  // item's next stages (kPages of them a stage), loaded a batch early.
+  // ---- copies, ahead of the products by the ring's stages: a walk of their own, by the ring's first warp. The lanes
+  // hold the page ids of the item's next stages (`pages` of them a stage), loaded a batch early.
   const int box_rows = min(1 << p.page_shift, S::kKeys), pages = S::kKeys / box_rows, batch = 32 / pages;
   const uint32_t page_bytes = (uint32_t)box_rows * D * S::kBytes;
   Walk ask = walk;
-  Stages<S::kKeys> to;
+  Stages<S::kKeys, kRings> to;
   to.before = 0;
   int asked = 0, slot_to = 0, in_batch = 0, ids = -1, next_ids = -1;
-  uint32_t bads = 0;                                            // 4 bits per slot: pages outside the cache
-  auto look = [&](int first) {                                  // stage `first` of the item and the warp's next ones
-    const int key = ask.tile * kTileKeys + (first + lane / pages * kWarps) * S::kKeys + lane % pages * box_rows;
-    if (first + lane / pages * kWarps >= to.n || key >= ask.r.keys) return -1;
+  auto look = [&](int first) {                                  // stage `first` of the item and the ring's next ones
+    const int key = ask.tile * kTileKeys + (first + lane / pages * kRings) * S::kKeys + lane % pages * box_rows;
+    if (first + lane / pages * kRings >= to.n || key >= ask.r.keys) return -1;
     const int id = p.block_table[(size_t)ask.b * p.max_pages + (key >> p.page_shift)];
     return id >= 0 && id < p.num_pages ? id : -2;
   };
-  auto ask_item = [&]() {                                       // the first item on from here with a stage for this warp
+  auto ask_item = [&]() {                                       // the first item on from here with a stage for this ring
     for (;;) {
-      to.item(ask, warp);
+      to.item(ask, mine);
       if (to.i < to.n) break;
       to.before += to.n;
       ask.done(p, lane);
       if (!ask.more()) return;
     }
     ids = look(to.i);
-    next_ids = look(to.i + batch * kWarps);
+    next_ids = look(to.i + batch * kRings);
     in_batch = 0;
   };
   auto request = [&]() {
     const int id = __shfl_sync(0xffffffffu, ids, (in_batch * pages + lane) & 31);
-    const bool mine = lane < pages;
-    const unsigned good = __ballot_sync(0xffffffffu, mine && id >= 0), bad = __ballot_sync(0xffffffffu, mine && id == -2);
-    const uint32_t bar = bars + 8 * slot_to, at = ring + slot_to * S::kStageBytes;
+    const bool wanted = lane < pages;
+    const unsigned good = __ballot_sync(0xffffffffu, wanted && id >= 0), bad = __ballot_sync(0xffffffffu, wanted && id == -2);
+    const uint32_t bar = full + 8 * slot_to, at = ring + slot_to * S::kStageBytes;
     if (lane == 0) {
+      bads[slot_to] = bad;
       if (bad) raise_status(p.status, MDW_ERR_DEVICE_BOUNDS);
       mbar_arrive_tx(bar, 2 * page_bytes * __popc(good));
     }
     __syncwarp();
-    bads = (bads & ~(15u << 4 * slot_to)) | bad << 4 * slot_to;
-    if (mine && id >= 0) {
+    if (wanted && id >= 0) {
       const int row = (ask.tile * kTileKeys + to.i * S::kKeys + lane * box_rows) & ((1 << p.page_shift) - 1);
 #pragma unroll
       for (int k = 0; k < S::kHalves; ++k) {
         const uint32_t dst = at + k * (S::kKeys * S::kRowBytes) + lane * box_rows * S::kRowBytes;
         tma_load(dst, &kmap, bar, k * (S::kRowBytes / S::kBytes), row, ask.h, id);
-        tma_load(dst + kFewBytes, &vmap, bar, k * (S::kRowBytes / S::kBytes), row, ask.h, id);
+        tma_load(dst + S::kOperand, &vmap, bar, k * (S::kRowBytes / S::kBytes), row, ask.h, id);
       }
     }
     __syncwarp();
     ++asked;
     if (++slot_to == kStages) slot_to = 0;
-    to.i += kWarps;
+    to.i += kRings;
     if (to.i >= to.n) {
       to.before += to.n;
       ask.done(p, lane);
@@ -163,28 +170,31 @@ few_rows_kernel(const AttnParams p, const __grid_constant__ CUtensorMap kmap, co
     } else if (++in_batch == batch) {
       in_batch = 0;
       ids = next_ids;
-      next_ids = look(to.i + batch * kWarps);
+      next_ids = look(to.i + batch * kRings);
     }
   };
-  ask_item();
-  for (int i = 0; i < kStages && ask.more(); ++i) request();
+  if (row0 == 0) {
+    ask_item();
+    for (int i = 0; i < kStages && ask.more(); ++i) request();
+  }
 
-  Stages<S::kKeys> at;
+  Stages<S::kKeys, kRings> at;
   at.before = 0;
-  int slot = 0;
+  int slot = 0, used = 0;
   uint32_t phase = 0;
   while (walk.more()) {
     const Request r = walk.r;
     const int rows = r.rows * p.group, tile0 = walk.tile, count = walk.count(), h = walk.h;
     const bool whole = count == walk.tiles;
-    at.item(walk, warp);
-    // ---- rows g and g + 8 of the item, four elements of each per step; the nodes they see; c
+    at.item(walk, mine);
+    const bool active = kBlocks == 1 || row0 < rows;
+    // ---- rows g and g + 8 of the warp, four elements of each per step; the nodes they see; c
     uint32_t qf[kSteps][4];
     uint64_t bits[2];
     float c[2];
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-      const int row = g + 8 * i, node = row / p.group;
+      const int row = row0 + g + 8 * i, node = row / p.group;
       const bool valid = row < rows;
       bits[i] = 0;
       if (valid) {
@@ -223,34 +233,33 @@ few_rows_kernel(const AttnParams p, const __grid_constant__ CUtensorMap kmap, co
 #pragma unroll
     for (int t = 0; t < kOut; ++t) o[t][0] = o[t][1] = o[t][2] = o[t][3] = 0.f;
 
-    for (; at.i < at.n; at.i += kWarps) {
-      const int key0 = tile0 * kTileKeys + at.i * S::kKeys;
-      mbar_wait(bars + 8 * slot, phase, p.spin_budget, p.status, dead);
-      __syncwarp();
-      const uint32_t bad = bads >> 4 * slot & 15, keys = ring + slot * S::kStageBytes, values = keys + kFewBytes;
+    auto stage = [&](const int key0) {
+      const uint32_t bad = bads[slot], keys = ring + slot * S::kStageBytes, values = keys + S::kOperand;
       const bool all = key0 + S::kKeys <= r.ctx && bad == 0;    // every row sees every key
       // ---- scores; columns 2 q and 2 q + 1 of octet n: keys 8 n + q and 8 n + q + 4
       float s[kOctets][4];
 #pragma unroll
       for (int n = 0; n < kOctets; ++n) {
         const int key = 8 * n + ((g & 1) << 2 | g >> 1);
-        s[n][0] = s[n][1] = s[n][2] = s[n][3] = 0.f;
+        float part[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};   // two chains, shorter than one
         if constexpr (kE4M3) {
 #pragma unroll
           for (int j = 0; j < kSteps / 4; ++j) {
             const uint4 v = lds16(S::piece(keys, key, q + 4 * j));
             const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-            for (int i = 0; i < 4; ++i) mma16<C>(s[n], qf[4 * j + i], e4m3x2_to_f16x2(w[i] & 0xffffu), e4m3x2_to_f16x2(w[i] >> 16));
+            for (int i = 0; i < 4; ++i) mma16<C>(part[i & 1], qf[4 * j + i], e4m3x2_to_f16x2(w[i] & 0xffffu), e4m3x2_to_f16x2(w[i] >> 16));
           }
         } else {
 #pragma unroll
           for (int j = 0; j < kSteps / 2; ++j) {
             const uint4 v = lds16(S::piece(keys, key, 8 * (j >> 1) + q + 4 * (j & 1)));
-            mma16<C>(s[n], qf[2 * j], v.x, v.y);
-            mma16<C>(s[n], qf[2 * j + 1], v.z, v.w);
+            mma16<C>(part[0], qf[2 * j], v.x, v.y);
+            mma16<C>(part[1], qf[2 * j + 1], v.z, v.w);
           }
         }
+#pragma unroll
+        for (int e = 0; e < 4; ++e) s[n][e] = part[0][e] + part[1][e];
       }
       uint32_t see[2][(S::kKeys + 31) / 32], there[(S::kKeys + 31) / 32];   // keys that the rows see; that exist
       if (!all) {
@@ -394,9 +403,22 @@ few_rows_kernel(const AttnParams p, const __grid_constant__ CUtensorMap kmap, co
           }
         }
       }
-      __syncwarp();                                             // the slot is read
+    };
+    for (; at.i < at.n; at.i += kRings) {
+      mbar_wait(full + 8 * slot, phase, p.spin_budget, p.status, dead);
+      __syncwarp();
+      if (active) stage(tile0 * kTileKeys + at.i * S::kKeys);
+      __syncwarp();                                             // the slot is read by this warp
+      if constexpr (kBlocks > 1) {
+        if (lane == 0) mbar_arrive(empty + 8 * slot);
+      }
+      // the slot's next copies; where warps share it those of the slot before, which the others have left by now
+      if (row0 == 0 && ask.more() && used >= kBlocks - 1) {
+        if constexpr (kBlocks > 1) mbar_wait(empty + 8 * slot_to, (asked / kStages & 1) ^ 1, p.spin_budget, p.status, dead);
+        if (!__any_sync(0xffffffffu, *dead)) request();
+      }
+      ++used;
       if (++slot == kStages) { slot = 0; phase ^= 1; }
-      if (ask.more() && !__any_sync(0xffffffffu, *dead)) request();
     }
     at.before += at.n;
 
@@ -405,14 +427,14 @@ few_rows_kernel(const AttnParams p, const __grid_constant__ CUtensorMap kmap, co
     for (int i = 0; i < 2; ++i) {
       l[i] += __shfl_xor_sync(0xffffffffu, l[i], 1);
       l[i] += __shfl_xor_sync(0xffffffffu, l[i], 2);
-      if (q == 0) ml[warp * kFewRows + g + 8 * i] = make_float2(mc[i], l[i]);
+      if (q == 0) ml[warp * 16 + g + 8 * i] = make_float2(mc[i], l[i]);
     }
     __syncthreads();
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       float m = -INFINITY;
 #pragma unroll
-      for (int w = 0; w < kWarps; ++w) m = fmaxf(m, ml[w * kFewRows + g + 8 * i].x);
+      for (int w = 0; w < kRings; ++w) m = fmaxf(m, ml[(w * kBlocks + warp % kBlocks) * 16 + g + 8 * i].x);
       const float f = exp2_fast(mc[i] - (m == -INFINITY ? 0.f : m));
 #pragma unroll
       for (int t = 0; t < kOut; ++t) {
@@ -420,7 +442,7 @@ few_rows_kernel(const AttnParams p, const __grid_constant__ CUtensorMap kmap, co
         o[t][2 * i + 1] *= f;
       }
     }
-    float* place = reinterpret_cast<float*>(smem + S::kJoinAt) + (warp & 3) * (kFewRows * S::kPitch);
+    float* place = reinterpret_cast<float*>(smem + S::kJoinAt) + (warp & 3) * (16 * S::kPitch);
     auto each = [&](auto&& f) {                                 // the lane's outputs and their place
 #pragma unroll
       for (int i = 0; i < 2; ++i)
@@ -434,21 +456,22 @@ few_rows_kernel(const AttnParams p, const __grid_constant__ CUtensorMap kmap, co
     if (warp < 4) each([](float& mine, float& there) { there += mine; });
     __syncthreads();
     {
-      constexpr int kCols = D / 16;
-      const int row = threadIdx.x >> 4, d = (threadIdx.x & 15) * kCols, node = row / p.group;
+      constexpr int kCols = D * kBlocks / 16, kPer = D / kCols;  // columns of a thread, threads of a row
+      const int row = threadIdx.x / kPer, d = threadIdx.x % kPer * kCols, node = row / p.group;
+      const float2* of_row = ml + row;                          // [ring][kRows]: a block's warps are those of its rows
       float m = -INFINITY, sum = 0.f, v[kCols];
 #pragma unroll
-      for (int w = 0; w < kWarps; ++w) m = fmaxf(m, ml[w * kFewRows + row].x);
+      for (int w = 0; w < kRings; ++w) m = fmaxf(m, of_row[w * S::kRows].x);
       const float from = m == -INFINITY ? 0.f : m;
 #pragma unroll
-      for (int w = 0; w < kWarps; ++w) sum += ml[w * kFewRows + row].y * exp2_fast(ml[w * kFewRows + row].x - from);
+      for (int w = 0; w < kRings; ++w) sum += of_row[w * S::kRows].y * exp2_fast(of_row[w * S::kRows].x - from);
       const float* joined = reinterpret_cast<const float*>(smem + S::kJoinAt) + row * S::kPitch + d;
 #pragma unroll
       for (int j = 0; j < kCols; j += 4) {
         float4 x = *reinterpret_cast<const float4*>(joined + j);
 #pragma unroll
-        for (int w = 1; w < 4; ++w) {
-          const float4 y = *reinterpret_cast<const float4*>(joined + w * kFewRows * S::kPitch + j);
+        for (int w = kBlocks; w < 4; w += kBlocks) {
+          const float4 y = *reinterpret_cast<const float4*>(joined + w * 16 * S::kPitch + j);
           x.x += y.x, x.y += y.y, x.z += y.z, x.w += y.w;
         }
         v[j] = x.x, v[j + 1] = x.y, v[j + 2] = x.z, v[j + 3] = x.w;
@@ -461,8 +484,10 @@ few_rows_kernel(const AttnParams p, const __grid_constant__ CUtensorMap kmap, co
           uint32_t packed[kCols / 2];
 #pragma unroll
           for (int j = 0; j < kCols; j += 2) packed[j / 2] = sum == 0.f ? 0u : Mma<T>::pack(v[j] * f, v[j + 1] * f);
-          if constexpr (kCols == 8) *reinterpret_cast<uint4*>(dst) = make_uint4(packed[0], packed[1], packed[2], packed[3]);
-          else *reinterpret_cast<uint2*>(dst) = make_uint2(packed[0], packed[1]);
+          if constexpr (kCols == 4) *reinterpret_cast<uint2*>(dst) = make_uint2(packed[0], packed[1]);
+          else
+#pragma unroll
+            for (int j = 0; j < kCols / 2; j += 4) *reinterpret_cast<uint4*>(dst + 2 * j) = make_uint4(packed[j], packed[j + 1], packed[j + 2], packed[j + 3]);
           if (p.lse && d == 0) p.lse[(int64_t)(r.row0 + node) * p.Hq + head] = sum == 0.f ? -INFINITY : (m + log2f(sum)) * kLn2;
         } else {
           const size_t part = (size_t)(2 * blockIdx.x + (tile0 > 0 ? 0 : 1)) * kTileRows + row;
@@ -477,15 +502,19 @@ few_rows_kernel(const AttnParams p, const __grid_constant__ CUtensorMap kmap, co
   }
   // copies that a block given up did not wait for
   if (*dead)
-    for (int i = max(asked - kStages, 0); i < asked; ++i) mbar_drain(bars + 8 * (i % kStages), i / kStages & 1);
+    for (int i = max(asked - kStages, 0); i < asked; ++i) mbar_drain(full + 8 * (i % kStages), i / kStages & 1);
 }
 
+template <typename T, bool kE4M3, int D, int kBlocks>
+cudaError_t launch(const AttnParams& p, const CUtensorMap& km, const CUtensorMap& vm, int grid, int dev, cudaStream_t s) {
+  const cudaError_t e = allow_shared_memory<few_rows_kernel<T, kE4M3, D, kBlocks>>(dev);
+  if (e != cudaSuccess) return e;
+  few_rows_kernel<T, kE4M3, D, kBlocks><<<grid, 32 * kWarps, Few<T, kE4M3, D, kBlocks>::kSmem, s>>>(p, km, vm);
+  return cudaGetLastError();
+}
 template <typename T, bool kE4M3, int D>
 cudaError_t launch(const AttnParams& p, const CUtensorMap& km, const CUtensorMap& vm, int grid, int dev, cudaStream_t s) {
-  const cudaError_t e = allow_shared_memory<few_rows_kernel<T, kE4M3, D>>(dev);
-  if (e != cudaSuccess) return e;
-  few_rows_kernel<T, kE4M3, D><<<grid, 32 * kWarps, Few<T, kE4M3, D>::kSmem, s>>>(p, km, vm);
-  return cudaGetLastError();
+  return few_rows_blocks(p) == 1 ? launch<T, kE4M3, D, 1>(p, km, vm, grid, dev, s) : launch<T, kE4M3, D, 2>(p, km, vm, grid, dev, s);
 }
 template <typename T>
 cudaError_t launch(const AttnParams& p, bool e4m3, int D, const CUtensorMap& km, const CUtensorMap& vm, int grid, int dev, cudaStream_t s) {
