@@ -80,10 +80,11 @@ __device__ __forceinline__ void mbar_wait(uint32_t bar, uint32_t parity, long lo
   if (!mbar_test(bar, parity)) mbar_wait_slow(bar, parity, budget, status, dead);
 }
 // A dead block's copies in flight end before the block does (bounded as well).
-static __device__ __noinline__ void mbar_drain(uint32_t bar, uint32_t parity) {
+__device__ __forceinline__ void mbar_drain_inline(uint32_t bar, uint32_t parity) {
   const long long t0 = clock64();
   while (!mbar_try(bar, parity) && clock64() - t0 < (1ll << 28)) {}
 }
+static __device__ __noinline__ void mbar_drain(uint32_t bar, uint32_t parity) { mbar_drain_inline(bar, parity); }
 
 // ------------------------------------------------------------------ host
 

@@ -20,7 +20,9 @@
 namespace mdw {
 namespace {
 
-constexpr int kWarps = 8;
+// Warps of the products; a third warpgroup, of which one warp works, makes the copies. The groups share the registers
+// that the launch gives each thread (168) as 40 + 2 x 232.
+constexpr int kWarps = 8, kThreads = 32 * kWarps + 128;
 
 // kBlocks warps share the copies of a ring and have 16 rows each.
 template <typename T, bool kE4M3, int D, int kBlocks>
@@ -66,20 +68,15 @@ __device__ __forceinline__ uint2 lds8(uint32_t a) {
   return v;
 }
 
-// Stages of the walk's current item that lie in the block's share, and the ring's place among them: stages go to the
-// rings in turn, on from where the item before stopped.
-template <int kKeys, int kRings>
-struct Stages {
-  int n, i, before;                // stages of the item; the ring's next one; stages of the items before
-  __device__ __forceinline__ void item(const Walk& w, int ring) {
-    const int keys = min(w.r.keys, (w.tile + w.count()) * kTileKeys) - w.tile * kTileKeys;
-    n = (keys + kKeys - 1) / kKeys;
-    i = (ring - before) & (kRings - 1);
-  }
-};
+// Stages of the walk's current item that lie in the block's share.
+template <int kKeys>
+__device__ __forceinline__ int stages(const Walk& w) {
+  const int keys = min(w.r.keys, (w.tile + w.count()) * kTileKeys) - w.tile * kTileKeys;
+  return (keys + kKeys - 1) / kKeys;
+}
 
 template <typename T, bool kE4M3, int D, int kBlocks>
-__global__ void __launch_bounds__(32 * kWarps, 1)
+__global__ void __launch_bounds__(kThreads, 1)
 few_rows_kernel(const AttnParams p, const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap) {
   using S = Few<T, kE4M3, D, kBlocks>;
   using C = typename S::C;
@@ -88,23 +85,20 @@ few_rows_kernel(const AttnParams p, const __grid_constant__ CUtensorMap kmap, co
   extern __shared__ __align__(1024) uint8_t smem[];
   const uint32_t base = smem_u32(smem);
   const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31, g = lane >> 2, q = lane & 3;
-  const int mine = warp / kBlocks, row0 = warp % kBlocks * 16;  // the warp's ring; first of its rows
   float2* ml = reinterpret_cast<float2*>(smem + S::kSmall);     // [warp][16] (c m, sum)
-  const uint32_t full = base + S::kBarsAt + mine * kStages * 16, empty = full + kStages * 8;
-  volatile uint32_t* bads = reinterpret_cast<volatile uint32_t*>(smem + S::kBadAt) + mine * kStages;   // per slot: pages outside the cache
+  // barriers of ring x, slot i at 8 (kStages x + i); pages of its stage outside the cache
+  const uint32_t full = base + S::kBarsAt, empty = full + kRings * kStages * 8;
+  volatile uint32_t* bads = reinterpret_cast<volatile uint32_t*>(smem + S::kBadAt);
   volatile int* dead = reinterpret_cast<volatile int*>(smem + S::kBadAt + kRings * kStages * 4);
-  const uint32_t ring = base + mine * kStages * S::kStageBytes;
   if (base & 1023) {                                            // the swizzled tiles need the alignment asked for above
     if (threadIdx.x == 0) raise_status(p.status, MDW_ERR_UNSUPPORTED_SHAPE);
     if (blockIdx.x == 0 && threadIdx.x == 0) p.total[0] = p.total[1] = 0;
     return;
   }
   if (threadIdx.x == 0) *dead = 0;
-  if (row0 == 0 && lane == 0) {
-    for (int i = 0; i < kStages; ++i) {
-      mbar_init(full + 8 * i, 1);
-      mbar_init(empty + 8 * i, kBlocks);
-    }
+  if (threadIdx.x < kRings * kStages) {
+    mbar_init(full + 8 * threadIdx.x, 1);
+    mbar_init(empty + 8 * threadIdx.x, kBlocks);
     mbar_init_fence();
   }
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
@@ -113,80 +107,83 @@ few_rows_kernel(const AttnParams p, const __grid_constant__ CUtensorMap kmap, co
   if (!walk.more()) return;                                     // the whole block
   __syncthreads();                                              // barriers, *dead
 
-  // ---- copies, ahead of the products by the ring's stages: a walk of their own, by the ring's first warp. The lanes
-  // hold the page ids of the item's next stages (`pages` of them a stage), loaded a batch early.
-  const int box_rows = min(1 << p.page_shift, S::kKeys), pages = S::kKeys / box_rows, batch = 32 / pages;
-  const uint32_t page_bytes = (uint32_t)box_rows * D * S::kBytes;
-  Walk ask = walk;
-  Stages<S::kKeys, kRings> to;
-  to.before = 0;
-  int asked = 0, slot_to = 0, in_batch = 0, ids = -1, next_ids = -1;
-  auto look = [&](int first) {                                  // stage `first` of the item and the ring's next ones
-    const int key = ask.tile * kTileKeys + (first + lane / pages * kRings) * S::kKeys + lane % pages * box_rows;
-    if (first + lane / pages * kRings >= to.n || key >= ask.r.keys) return -1;
-    const int id = p.block_table[(size_t)ask.b * p.max_pages + (key >> p.page_shift)];
-    return id >= 0 && id < p.num_pages ? id : -2;
-  };
-  auto ask_item = [&]() {                                       // the first item on from here with a stage for this ring
-    for (;;) {
-      to.item(ask, mine);
-      if (to.i < to.n) break;
-      to.before += to.n;
-      ask.done(p, lane);
-      if (!ask.more()) return;
-    }
-    ids = look(to.i);
-    next_ids = look(to.i + batch * kRings);
-    in_batch = 0;
-  };
-  auto request = [&]() {
-    const int id = __shfl_sync(0xffffffffu, ids, (in_batch * pages + lane) & 31);
-    const bool wanted = lane < pages;
-    const unsigned good = __ballot_sync(0xffffffffu, wanted && id >= 0), bad = __ballot_sync(0xffffffffu, wanted && id == -2);
-    const uint32_t bar = full + 8 * slot_to, at = ring + slot_to * S::kStageBytes;
-    if (lane == 0) {
-      bads[slot_to] = bad;
-      if (bad) raise_status(p.status, MDW_ERR_DEVICE_BOUNDS);
-      mbar_arrive_tx(bar, 2 * page_bytes * __popc(good));
-    }
-    __syncwarp();
-    if (wanted && id >= 0) {
-      const int row = (ask.tile * kTileKeys + to.i * S::kKeys + lane * box_rows) & ((1 << p.page_shift) - 1);
+  if (warp >= kWarps) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 40;");
+    if (warp > kWarps) return;
+    // ---- copies. Stages go to the rings in turn, across items; a lane has one page of one ring's next stage. Within an
+    // item the rings advance on their own, each as its slots become free.
+    const int box_rows = min(1 << p.page_shift, S::kKeys), pages = S::kKeys / box_rows;
+    const uint32_t page_bytes = (uint32_t)box_rows * D * S::kBytes, of_stage = (1u << pages) - 1u;
+    const int x = lane / pages, sub = lane - x * pages, low = x * pages;   // ring, page of the stage, ring's first lane
+    int before = 0, asked = 0;                                  // stages before the item; copies of this lane's ring
+    while (walk.more() && !__any_sync(0xffffffffu, *dead)) {
+      const Request r = walk.r;
+      const int n = stages<S::kKeys>(walk), first = walk.tile * kTileKeys + sub * box_rows, h = walk.h;
+      const int32_t* table = p.block_table + (size_t)walk.b * p.max_pages;
+      int i = x < kRings ? (x - before) & (kRings - 1) : n;     // the ring's next stage of the item
+      auto wanted = [&](int i) { return i < n && first + i * S::kKeys < r.keys; };
+      // the lane's page of it, not looked at before its copy: the load is on its way meanwhile
+      auto look = [&](int i) { return wanted(i) ? table[(first + i * S::kKeys) >> p.page_shift] : 0; };
+      int id = look(i), next_id = look(i + kRings);
+      long long t0 = clock64();
+      while (__any_sync(0xffffffffu, i < n)) {
+        if (__any_sync(0xffffffffu, *dead)) break;
+        const int slot = x * kStages + asked % kStages;
+        const unsigned free = __ballot_sync(0xffffffffu, i < n && mbar_test(empty + 8 * slot, (asked / kStages & 1) ^ 1));
+        const bool go = i < n && (free >> low & of_stage) == of_stage;
+        const bool want = go && wanted(i), there = want && id >= 0 && id < p.num_pages;
+        const unsigned good = __ballot_sync(0xffffffffu, there), bad = __ballot_sync(0xffffffffu, want && !there);
+        if (!__any_sync(0xffffffffu, go)) {
+          if (clock64() - t0 > p.spin_budget) {
+            *dead = 1;
+            raise_status(p.status, MDW_ERR_TIMEOUT);
+          }
+          __nanosleep(40);
+          continue;
+        }
+        const uint32_t bar = full + 8 * slot, to = base + slot * S::kStageBytes + sub * box_rows * S::kRowBytes;
+        if (go && sub == 0) {
+          bads[slot] = bad >> low & of_stage;
+          if (bad >> low & of_stage) raise_status(p.status, MDW_ERR_DEVICE_BOUNDS);
+          mbar_arrive_tx(bar, 2 * page_bytes * __popc(good >> low & of_stage));
+        }
+        __syncwarp();
+        if (go) {
+          if (there) {
+            const int row = (first + i * S::kKeys) & ((1 << p.page_shift) - 1);
 #pragma unroll
-      for (int k = 0; k < S::kHalves; ++k) {
-        const uint32_t dst = at + k * (S::kKeys * S::kRowBytes) + lane * box_rows * S::kRowBytes;
-        tma_load(dst, &kmap, bar, k * (S::kRowBytes / S::kBytes), row, ask.h, id);
-        tma_load(dst + S::kOperand, &vmap, bar, k * (S::kRowBytes / S::kBytes), row, ask.h, id);
+            for (int k = 0; k < S::kHalves; ++k) {
+              tma_load(to + k * (S::kKeys * S::kRowBytes), &kmap, bar, k * (S::kRowBytes / S::kBytes), row, h, id);
+              tma_load(to + k * (S::kKeys * S::kRowBytes) + S::kOperand, &vmap, bar, k * (S::kRowBytes / S::kBytes), row, h, id);
+            }
+          }
+          ++asked;
+          i += kRings;
+          id = next_id;
+          next_id = look(i + kRings);
+        }
+        __syncwarp();
+        t0 = clock64();
       }
+      before += n;
+      walk.done(p, lane);
     }
-    __syncwarp();
-    ++asked;
-    if (++slot_to == kStages) slot_to = 0;
-    to.i += kRings;
-    if (to.i >= to.n) {
-      to.before += to.n;
-      ask.done(p, lane);
-      if (ask.more()) ask_item();
-    } else if (++in_batch == batch) {
-      in_batch = 0;
-      ids = next_ids;
-      next_ids = look(to.i + batch * kRings);
-    }
-  };
-  if (row0 == 0) {
-    ask_item();
-    for (int i = 0; i < kStages && ask.more(); ++i) request();
+    // a block given up: its copies in flight end before it does
+    if (*dead && x < kRings && sub == 0)
+      for (int i = max(asked - kStages, 0); i < asked; ++i) mbar_drain_inline(full + 8 * (x * kStages + i % kStages), i / kStages & 1);
+    return;
   }
 
-  Stages<S::kKeys, kRings> at;
-  at.before = 0;
-  int slot = 0, used = 0;
+  auto join_barrier = [] { asm volatile("bar.sync 1, %0;" :: "n"(32 * kWarps) : "memory"); };
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 232;");
+  const int mine = warp / kBlocks, row0 = warp % kBlocks * 16;  // the warp's ring; first of its rows
+  const uint32_t ring = base + mine * kStages * S::kStageBytes, full0 = full + 8 * mine * kStages, empty0 = empty + 8 * mine * kStages;
+  int slot = 0, before = 0;
   uint32_t phase = 0;
   while (walk.more()) {
     const Request r = walk.r;
     const int rows = r.rows * p.group, tile0 = walk.tile, count = walk.count(), h = walk.h;
     const bool whole = count == walk.tiles;
-    at.item(walk, mine);
     const bool active = kBlocks == 1 || row0 < rows;
     // ---- rows g and g + 8 of the warp, four elements of each per step; the nodes they see; c
     uint32_t qf[kSteps][4];
@@ -234,7 +231,8 @@ few_rows_kernel(const AttnParams p, const __grid_constant__ CUtensorMap kmap, co
     for (int t = 0; t < kOut; ++t) o[t][0] = o[t][1] = o[t][2] = o[t][3] = 0.f;
 
     auto stage = [&](const int key0) {
-      const uint32_t bad = bads[slot], keys = ring + slot * S::kStageBytes, values = keys + S::kOperand;
+      const uint32_t bad = bads[mine * kStages + slot], keys = ring + slot * S::kStageBytes, values = keys + S::kOperand;
+      const int box_rows = min(1 << p.page_shift, S::kKeys);
       const bool all = key0 + S::kKeys <= r.ctx && bad == 0;    // every row sees every key
       // ---- scores; columns 2 q and 2 q + 1 of octet n: keys 8 n + q and 8 n + q + 4
       float s[kOctets][4];
@@ -404,23 +402,16 @@ few_rows_kernel(const AttnParams p, const __grid_constant__ CUtensorMap kmap, co
         }
       }
     };
-    for (; at.i < at.n; at.i += kRings) {
-      mbar_wait(full + 8 * slot, phase, p.spin_budget, p.status, dead);
+    const int n = stages<S::kKeys>(walk);
+    for (int i = (mine - before) & (kRings - 1); i < n; i += kRings) {
+      mbar_wait(full0 + 8 * slot, phase, p.spin_budget, p.status, dead);
       __syncwarp();
-      if (active) stage(tile0 * kTileKeys + at.i * S::kKeys);
-      __syncwarp();                                             // the slot is read by this warp
-      if constexpr (kBlocks > 1) {
-        if (lane == 0) mbar_arrive(empty + 8 * slot);
-      }
-      // the slot's next copies; where warps share it those of the slot before, which the others have left by now
-      if (row0 == 0 && ask.more() && used >= kBlocks - 1) {
-        if constexpr (kBlocks > 1) mbar_wait(empty + 8 * slot_to, (asked / kStages & 1) ^ 1, p.spin_budget, p.status, dead);
-        if (!__any_sync(0xffffffffu, *dead)) request();
-      }
-      ++used;
+      if (active) stage(tile0 * kTileKeys + i * S::kKeys);
+      __syncwarp();
+      if (lane == 0) mbar_arrive(empty0 + 8 * slot);
       if (++slot == kStages) { slot = 0; phase ^= 1; }
     }
-    at.before += at.n;
+    before += n;
 
     // ---- the item's result: the warps' outputs on one base, four at a time added up in shared memory
 #pragma unroll
@@ -429,7 +420,7 @@ few_rows_kernel(const AttnParams p, const __grid_constant__ CUtensorMap kmap, co
       l[i] += __shfl_xor_sync(0xffffffffu, l[i], 2);
       if (q == 0) ml[warp * 16 + g + 8 * i] = make_float2(mc[i], l[i]);
     }
-    __syncthreads();
+    join_barrier();
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       float m = -INFINITY;
@@ -452,9 +443,9 @@ few_rows_kernel(const AttnParams p, const __grid_constant__ CUtensorMap kmap, co
           for (int e = 0; e < 2; ++e) f(o[t][2 * i + e], place[(g + 8 * i) * S::kPitch + S::element(t, 2 * q + e)]);
     };
     if (warp >= 4) each([](float& mine, float& there) { there = mine; });
-    __syncthreads();
+    join_barrier();
     if (warp < 4) each([](float& mine, float& there) { there += mine; });
-    __syncthreads();
+    join_barrier();
     {
       constexpr int kCols = D * kBlocks / 16, kPer = D / kCols;  // columns of a thread, threads of a row
       const int row = threadIdx.x / kPer, d = threadIdx.x % kPer * kCols, node = row / p.group;
@@ -498,18 +489,15 @@ few_rows_kernel(const AttnParams p, const __grid_constant__ CUtensorMap kmap, co
       }
     }
     walk.done(p, lane);
-    __syncthreads();                                            // sums and outputs are read; the next item may write
+    join_barrier();                                            // sums and outputs are read; the next item may write
   }
-  // copies that a block given up did not wait for
-  if (*dead)
-    for (int i = max(asked - kStages, 0); i < asked; ++i) mbar_drain(full + 8 * (i % kStages), i / kStages & 1);
 }
 
 template <typename T, bool kE4M3, int D, int kBlocks>
 cudaError_t launch(const AttnParams& p, const CUtensorMap& km, const CUtensorMap& vm, int grid, int dev, cudaStream_t s) {
   const cudaError_t e = allow_shared_memory<few_rows_kernel<T, kE4M3, D, kBlocks>>(dev);
   if (e != cudaSuccess) return e;
-  few_rows_kernel<T, kE4M3, D, kBlocks><<<grid, 32 * kWarps, Few<T, kE4M3, D, kBlocks>::kSmem, s>>>(p, km, vm);
+  few_rows_kernel<T, kE4M3, D, kBlocks><<<grid, kThreads, Few<T, kE4M3, D, kBlocks>::kSmem, s>>>(p, km, vm);
   return cudaGetLastError();
 }
 template <typename T, bool kE4M3, int D>
