@@ -62,6 +62,8 @@ __device__ __forceinline__ bool mbar_test(uint32_t bar, uint32_t parity) {
                : "=r"(ok) : "r"(bar), "r"(parity) : "memory");
   return ok != 0;
 }
+// Brings a copy's descriptor in before the first copy needs it.
+__device__ __forceinline__ void prefetch_map(const CUtensorMap* map) { asm volatile("prefetch.tensormap [%0];" :: "l"(map) : "memory"); }
 // A wait that outlasts the budget marks the block dead: it and every later wait then give up at
 // once, so the block runs to its end (its results are not stored) and the status says so.
 static __device__ __noinline__ void mbar_wait_slow(uint32_t bar, uint32_t parity, long long budget, uint32_t* status, volatile int* dead) {

@@ -334,6 +334,8 @@ tree_attention_kernel(const AttnParams p, const __grid_constant__ CUtensorMap km
     return;
   }
   if (threadIdx.x == 0) {
+    prefetch_map(&kmap);
+    prefetch_map(&vmap);
     for (int i = 0; i < S::kSlots; ++i) {
       mbar_init(sm.full + 8 * i, 1);
       mbar_init(sm.empty + 8 * i, kE4M3 ? S::kHelpers : 1);
@@ -756,53 +758,57 @@ __global__ void __launch_bounds__(128) join_kernel(const AttnParams p) {
   asm volatile("griddepcontrol.wait;" ::: "memory");
   constexpr int kPer = D / 32;
   const int lane = threadIdx.x & 31;
+  // (loaded together: cuts of blocks without a share hold what an earlier call left, and are not used)
   const int total = p.total[0], blocks = p.total[1];
-  if ((int)blockIdx.x + 1 >= blocks) return;
   const Cut cut = p.cuts[blockIdx.x + 1];
+  if ((int)blockIdx.x + 1 >= blocks || cut.rows == 0) return;
   const Shares shares(total, blocks);
   if (shares.start(blockIdx.x) > cut.start) return;             // an earlier boundary is inside too
   const int c0 = blockIdx.x, parts = shares.owner(cut.start + cut.tiles - 1) - c0 + 1;
   for (int row = blockIdx.y * 4 + (threadIdx.x >> 5); row < cut.rows; row += 4 * gridDim.y) {
     // the item's first part is the last of its block's share, the others are the first of theirs
     auto slot = [&](int i) { return (size_t)(2 * (c0 + i) + (i == 0 ? 1 : 0)) * kTileRows + row; };
-    float mc = -INFINITY;
-    for (int i = lane; i < parts; i += 32) mc = fmaxf(mc, p.part_ml[slot(i)].x);
+    float2 ml = make_float2(-INFINITY, 0.f);                    // of part `lane`
+    if (lane < parts) ml = p.part_ml[slot(lane)];
+    constexpr int kAhead = 8;                                   // parts whose outputs are loaded with the sums
+    float v[kAhead][kPer];
+    auto load = [&](int first) {
+#pragma unroll
+      for (int u = 0; u < kAhead; ++u) {
+        const float* src = p.part_o + slot(min(first + u, parts - 1)) * D + lane * kPer;
+        if constexpr (kPer == 4) *reinterpret_cast<float4*>(v[u]) = __ldcg(reinterpret_cast<const float4*>(src));
+        else *reinterpret_cast<float2*>(v[u]) = __ldcg(reinterpret_cast<const float2*>(src));
+      }
+    };
+    load(0);
+    float mc = ml.x;
+    for (int i = lane + 32; i < parts; i += 32) mc = fmaxf(mc, p.part_ml[slot(i)].x);
     mc = warp_max(mc);
     const float base = mc == -INFINITY ? 0.f : mc;
-    float o[kPer], l = 0.f;
+    float o[kPer], f = 0.f, l = 0.f;
 #pragma unroll
     for (int j = 0; j < kPer; ++j) o[j] = 0.f;
-    for (int i0 = 0; i0 < parts; i0 += 32) {
-      float f = 0.f;
-      if (i0 + lane < parts) {
-        const float2 ml = p.part_ml[slot(i0 + lane)];
+    for (int i = 0; i < parts; i += kAhead) {
+      if (i % 32 == 0) {
+        if (i > 0) ml = i + lane < parts ? p.part_ml[slot(i + lane)] : make_float2(-INFINITY, 0.f);
         f = exp2_fast(ml.x - base);
         l = fmaf(ml.y, f, l);
       }
-      const int n = min(parts - i0, 32);
-      for (int i = 0; i < n; i += 4) {
-        float v[4][kPer];
+      if (i > 0) load(i);
 #pragma unroll
-        for (int u = 0; u < 4; ++u) {
-          const float* src = p.part_o + slot(i0 + min(i + u, n - 1)) * D + lane * kPer;
-          if constexpr (kPer == 4) *reinterpret_cast<float4*>(v[u]) = __ldcg(reinterpret_cast<const float4*>(src));
-          else *reinterpret_cast<float2*>(v[u]) = __ldcg(reinterpret_cast<const float2*>(src));
-        }
+      for (int u = 0; u < kAhead; ++u) {
+        const float g = __shfl_sync(0xffffffffu, f, (i + u) & 31);
 #pragma unroll
-        for (int u = 0; u < 4; ++u) {
-          const float g = __shfl_sync(0xffffffffu, f, min(i + u, 31));
-#pragma unroll
-          for (int j = 0; j < kPer; ++j) o[j] = i + u < n ? fmaf(v[u][j], g, o[j]) : o[j];
-        }
+        for (int j = 0; j < kPer; ++j) o[j] = i + u < parts ? fmaf(v[u][j], g, o[j]) : o[j];
       }
     }
     l = warp_sum(l);
     const int flat = cut.first + row, node = flat / p.group, head = cut.h * p.group + flat - node * p.group;
-    const float f = l == 0.f ? 0.f : (p.v_scale ? p.v_scale[cut.h] : 1.f) / l;
+    const float norm = l == 0.f ? 0.f : (p.v_scale ? p.v_scale[cut.h] : 1.f) / l;
     T* dst = static_cast<T*>(p.out) + (int64_t)(cut.row0 + node) * p.ldo + (int64_t)head * D + lane * kPer;
     uint32_t packed[kPer / 2];
 #pragma unroll
-    for (int j = 0; j < kPer; j += 2) packed[j / 2] = l == 0.f ? 0u : Mma<T>::pack(o[j] * f, o[j + 1] * f);
+    for (int j = 0; j < kPer; j += 2) packed[j / 2] = l == 0.f ? 0u : Mma<T>::pack(o[j] * norm, o[j + 1] * norm);
     if constexpr (kPer == 4) *reinterpret_cast<uint2*>(dst) = make_uint2(packed[0], packed[1]);
     else *reinterpret_cast<uint32_t*>(dst) = packed[0];
     if (p.lse && lane == 0) p.lse[(int64_t)(cut.row0 + node) * p.Hq + head] = l == 0.f ? -INFINITY : (mc + log2f(l)) * kLn2;
@@ -811,7 +817,17 @@ __global__ void __launch_bounds__(128) join_kernel(const AttnParams p) {
 
 // ------------------------------------------------------------------ host
 
-bool few_rows(const AttnParams& p) { return p.max_new * p.group <= kFewRows; }
+// Which kernel. Up to 16 rows: few_rows_kernel (one token over 131k E4M3 keys 51 us, the other kernel 87; 1,500 16-bit keys
+// 10.4 and 15.4; 131k 16-bit keys 91 and 88). Up to 32 rows, of which two warps share the copies: the same over E4M3 caches and
+// heads of 64 (batches of trees 74 and 80 us, 54 and 66, 54 and 56), over a 16-bit cache with heads of 128 where the block
+// table leaves room for two tiles a block at most (1,500 keys 11.6 and 15.6 us, but a batch of trees 88 and 78).
+bool few_rows(const AttnParams& p, int key_bytes, int grid) {
+  const int rows = p.max_new * p.group;
+  if (rows <= 16) return true;
+  if (rows > kFewRows) return false;
+  const int64_t tiles = (((int64_t)p.max_pages << p.page_shift) + kTileKeys - 1) / kTileKeys * p.B * p.Hkv;
+  return key_bytes < 256 || tiles <= 2 * grid;
+}
 
 // The cache as [pages][heads][page size][head dim]; a box is up to `most` rows of one page and head, 128 bytes (or
 // a whole 64-byte row) wide.
@@ -845,7 +861,7 @@ template <typename T, bool kE4M3, int D>
 cudaError_t launch(const AttnParams& p, const CUtensorMap& km, const CUtensorMap& vm, int grid, int dev, cudaStream_t s) {
   using S = Shape<T, kE4M3, D>;
   cudaError_t e;
-  if (few_rows(p)) {
+  if (few_rows(p, D * S::kBytes, grid)) {
     e = launch_few_rows(p, std::is_same<T, __nv_bfloat16>::value, kE4M3, D, km, vm, grid, dev, s);
     if (e != cudaSuccess) return e;
   } else {
@@ -921,7 +937,7 @@ extern "C" mdw_status mdw_tree_attention(const mdw_kv_cache* cache, int32_t B, i
                      reinterpret_cast<float*>(base + lay.o)};
   CUtensorMap km, vm;
   const int D = cache->head_dim, key_bytes = D * (fp8 ? 1 : 2);
-  const int most = few_rows(p) ? few_rows_operand(key_bytes, few_rows_blocks(p)) / key_bytes : kTileKeys;
+  const int most = few_rows(p, key_bytes, grid) ? kFewBytes / key_bytes : kTileKeys;
   if (!encode_cache(&km, cache, cache->k, most) || !encode_cache(&vm, cache, cache->v, most)) return MDW_ERR_CUDA;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   cudaError_t e;

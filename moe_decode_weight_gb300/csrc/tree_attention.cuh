@@ -239,11 +239,9 @@ __device__ __forceinline__ uint32_t visible32(uint64_t bits, int key, int ctx) {
   return -ahead < 64 ? (uint32_t)(bits >> -ahead) : 0u;
 }
 
-// Up to kFewRows rows a request and kv head: the kernel of tree_attention_rows.cu. A stage of its copies has as many
-// bytes of keys, and a box as many rows of a page at most, as few_rows_operand says.
-constexpr int kFewRows = 32;
-constexpr int few_rows_operand(int key_bytes, int blocks) { return key_bytes == 256 ? 4096 * blocks : 4096; }
-inline int few_rows_blocks(const AttnParams& p) { return p.max_new * p.group <= 16 ? 1 : 2; }
+// Up to kFewRows rows a request and kv head: the kernel of tree_attention_rows.cu. A stage of its copies, and so a box
+// of them, has kFewBytes of keys at most.
+constexpr int kFewRows = 32, kFewBytes = 4096;
 cudaError_t launch_few_rows(const AttnParams& p, bool bf16, bool e4m3, int D, const CUtensorMap& km, const CUtensorMap& vm, int grid, int dev,
                             cudaStream_t s);
 

@@ -29,10 +29,10 @@ template <typename T, bool kE4M3, int D, int kBlocks>
 struct Few {
   using C = typename std::conditional<kE4M3, __half, T>::type;     // type of the products
   static constexpr int kBytes = kE4M3 ? 1 : 2;
-  static constexpr int kOperand = few_rows_operand(D * kBytes, kBlocks), kKeys = kOperand / (D * kBytes);   // of a stage: bytes of keys; keys
+  static constexpr int kKeys = kFewBytes / (D * kBytes);           // keys of a stage
   static constexpr int kRowBytes = D * kBytes < 128 ? D * kBytes : 128, kHalves = D * kBytes / kRowBytes;
-  static constexpr int kStageBytes = 2 * kOperand;                 // keys, then values
-  static constexpr int kRings = kWarps / kBlocks, kStages = 3 * kBlocks * 4096 / kOperand, kRows = 16 * kBlocks;
+  static constexpr int kStageBytes = 2 * kFewBytes;                // keys, then values
+  static constexpr int kRings = kWarps / kBlocks, kStages = 3 * kBlocks, kRows = 16 * kBlocks;
   static constexpr int kPitch = D + 4;                             // floats of a joined row
   static constexpr int kJoinAt = kRings * kStages * kStageBytes, kSmall = kJoinAt + kWarps / 2 * 16 * kPitch * 4;
   static constexpr int kBarsAt = kSmall + kWarps * 16 * 8, kBadAt = kBarsAt + 2 * kRings * kStages * 8;
@@ -95,7 +95,11 @@ few_rows_kernel(const AttnParams p, const __grid_constant__ CUtensorMap kmap, co
     if (blockIdx.x == 0 && threadIdx.x == 0) p.total[0] = p.total[1] = 0;
     return;
   }
-  if (threadIdx.x == 0) *dead = 0;
+  if (threadIdx.x == 0) {
+    *dead = 0;
+    prefetch_map(&kmap);
+    prefetch_map(&vmap);
+  }
   if (threadIdx.x < kRings * kStages) {
     mbar_init(full + 8 * threadIdx.x, 1);
     mbar_init(empty + 8 * threadIdx.x, kBlocks);
@@ -154,7 +158,7 @@ few_rows_kernel(const AttnParams p, const __grid_constant__ CUtensorMap kmap, co
 #pragma unroll
             for (int k = 0; k < S::kHalves; ++k) {
               tma_load(to + k * (S::kKeys * S::kRowBytes), &kmap, bar, k * (S::kRowBytes / S::kBytes), row, h, id);
-              tma_load(to + k * (S::kKeys * S::kRowBytes) + S::kOperand, &vmap, bar, k * (S::kRowBytes / S::kBytes), row, h, id);
+              tma_load(to + k * (S::kKeys * S::kRowBytes) + kFewBytes, &vmap, bar, k * (S::kRowBytes / S::kBytes), row, h, id);
             }
           }
           ++asked;
@@ -231,7 +235,7 @@ few_rows_kernel(const AttnParams p, const __grid_constant__ CUtensorMap kmap, co
     for (int t = 0; t < kOut; ++t) o[t][0] = o[t][1] = o[t][2] = o[t][3] = 0.f;
 
     auto stage = [&](const int key0) {
-      const uint32_t bad = bads[mine * kStages + slot], keys = ring + slot * S::kStageBytes, values = keys + S::kOperand;
+      const uint32_t bad = bads[mine * kStages + slot], keys = ring + slot * S::kStageBytes, values = keys + kFewBytes;
       const int box_rows = min(1 << p.page_shift, S::kKeys);
       const bool all = key0 + S::kKeys <= r.ctx && bad == 0;    // every row sees every key
       // ---- scores; columns 2 q and 2 q + 1 of octet n: keys 8 n + q and 8 n + q + 4
@@ -502,7 +506,7 @@ cudaError_t launch(const AttnParams& p, const CUtensorMap& km, const CUtensorMap
 }
 template <typename T, bool kE4M3, int D>
 cudaError_t launch(const AttnParams& p, const CUtensorMap& km, const CUtensorMap& vm, int grid, int dev, cudaStream_t s) {
-  return few_rows_blocks(p) == 1 ? launch<T, kE4M3, D, 1>(p, km, vm, grid, dev, s) : launch<T, kE4M3, D, 2>(p, km, vm, grid, dev, s);
+  return p.max_new * p.group <= 16 ? launch<T, kE4M3, D, 1>(p, km, vm, grid, dev, s) : launch<T, kE4M3, D, 2>(p, km, vm, grid, dev, s);
 }
 template <typename T>
 cudaError_t launch(const AttnParams& p, bool e4m3, int D, const CUtensorMap& km, const CUtensorMap& vm, int grid, int dev, cudaStream_t s) {
