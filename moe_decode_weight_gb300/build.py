@@ -21,7 +21,7 @@ BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libmdw.so")
 BINDING = os.path.join(PKG, "_binding.so")            # CPython extension: argument marshalling (csrc/binding.c)
 TRACE_LIB = os.path.join(PKG, "libmdw_trace.so")     # profiling build (-DMDW_TRACE), never loaded by the API
-SOURCES = ["moe.cu", "lm_head.cu", "abi.cu", "noalloc.cu", "sampler.cu", "w4_linear.cu",
+SOURCES = ["moe.cu", "lm_head.cu", "abi.cu", "noalloc.cu", "sampler.cu", "w4_linear.cu", "w4_tensor.cu",
            "kv_cache.cu", "tree_attention.cu", "tree_attention_rows.cu"]
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]

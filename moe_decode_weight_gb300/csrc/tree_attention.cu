@@ -37,80 +37,12 @@
 #include <type_traits>
 
 #include "mdw_internal.h"
+#include "mdw_tcgen05.cuh"
 #include "tree_attention.cuh"
 
 namespace mdw {
 namespace {
 
-// ------------------------------------------------------------------ copies and matrix steps
-
-// ---- tensor memory and tcgen05 (one issuing thread; a column is 32 bits of each of 128 lanes)
-__device__ __forceinline__ void tc_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
-__device__ __forceinline__ void tc_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
-// Arrives on the barrier when every product issued before is complete.
-__device__ __forceinline__ void tc_commit(uint32_t bar) {
-  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" :: "r"(bar) : "memory");
-}
-// Shared-memory operand with 128-byte swizzle, in two words: address and offsets in units of 16 bytes. K-major:
-// kStride between groups of 8 rows. MN-major: `lead` between blocks of 64 columns, kStride between
-// groups of 8 k. The second word is the same for all (stride, version, swizzle); a product's steps along k
-// add to the first one only, which keeps their issue short.
-constexpr uint32_t kOperandHigh = (1024u >> 4) | 1u << 14 | 2u << 29;
-__device__ __forceinline__ uint32_t operand_low(uint32_t addr, uint32_t lead) { return (addr & 0x3ffff) >> 4 | (lead >> 4) << 16; }
-__device__ __forceinline__ void tc_mma(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, bool add) {
-  asm volatile("{ .reg .pred p; .reg .b64 a, b; setp.ne.b32 p, %4, 0; mov.b64 a, {%1, %5}; mov.b64 b, {%2, %5};"
-               " tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, p; }"
-               :: "r"(d), "r"(a), "r"(b), "r"(idesc), "r"((uint32_t)add), "r"(kOperandHigh) : "memory");
-}
-__device__ __forceinline__ void tc_mma_tmem(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc) {
-  asm volatile("{ .reg .pred p; .reg .b64 b; setp.ne.b32 p, 1, 0; mov.b64 b, {%2, %4};"
-               " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], b, %3, p; }"
-               :: "r"(d), "r"(a), "r"(b), "r"(idesc), "r"(kOperandHigh) : "memory");
-}
-// One lane of a converged warp.
-__device__ __forceinline__ bool elect_one() {
-  uint32_t one;
-  asm volatile("{ .reg .pred p; elect.sync _|p, 0xffffffff; selp.u32 %0, 1, 0, p; }" : "=r"(one));
-  return one != 0;
-}
-// 128 x n, fp32 result, 16-bit operands of one type, b MN-major or K-major.
-__host__ __device__ constexpr uint32_t mma_shape(bool bf16, bool b_mn_major, int n) {
-  return 1u << 4 | (bf16 ? 1u : 0u) << 7 | (bf16 ? 1u : 0u) << 10 | (b_mn_major ? 1u : 0u) << 16 | (uint32_t)(n / 8) << 17 | (128u / 16) << 24;
-}
-__device__ __forceinline__ void tc_ld32(float (&v)[32], uint32_t addr) {
-  uint32_t* r = reinterpret_cast<uint32_t*>(v);
-  asm volatile("tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
-               "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
-               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]),
-                 "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]),
-                 "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]),
-                 "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31]) : "r"(addr));
-}
-__device__ __forceinline__ void tc_ld16(float (&v)[16], uint32_t addr) {
-  uint32_t* r = reinterpret_cast<uint32_t*>(v);
-  asm volatile("tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
-               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]),
-                 "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]) : "r"(addr));
-}
-__device__ __forceinline__ void tc_ld(float (&v)[16], uint32_t addr) { tc_ld16(v, addr); }
-__device__ __forceinline__ void tc_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
-__device__ __forceinline__ void tc_st32(uint32_t addr, const float (&v)[32]) {
-  const uint32_t* r = reinterpret_cast<const uint32_t*>(v);
-  asm volatile("tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,"
-               "%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};"
-               :: "r"(addr), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
-                 "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19]),
-                 "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]), "r"(r[29]),
-                 "r"(r[30]), "r"(r[31]) : "memory");
-}
-__device__ __forceinline__ void tc_st16(uint32_t addr, const uint32_t (&r)[16]) {
-  asm volatile("tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};"
-               :: "r"(addr), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
-                 "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]) : "memory");
-}
-__device__ __forceinline__ void tc_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
-// Generic writes to shared memory before, reads by the tensor cores after.
-__device__ __forceinline__ void fence_async_proxy() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
 // ------------------------------------------------------------------ the kernel
 
 template <typename T, bool kE4M3, int D>
@@ -460,7 +392,7 @@ tree_attention_kernel(const AttnParams p, const __grid_constant__ CUtensorMap km
         if (elect_one()) {
 #pragma unroll
           for (int t = 0; t < kTileKeys / 16; ++t)
-            tc_mma_tmem(stream + S::kOut, stream + S::kProb + 8 * t, values_low + t * (2048 >> 4), mma_shape(M::kBf16, true, D));
+            tc_mma_tmem(stream + S::kOut, stream + S::kProb + 8 * t, values_low + t * (2048 >> 4), mma_shape(M::kBf16, true, D), true);
           tc_commit(sm.output + 8 * s);
           tc_commit((kE4M3 ? sm.buffer_free : sm.empty) + 8 * at);
         }

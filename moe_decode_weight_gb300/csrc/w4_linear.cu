@@ -12,98 +12,20 @@
 // same order once, when they enter shared memory. This expansion bounds the kernels beside the codes'
 // stream: 11 (bf16) or 9 (f16) operations for eight codes of a feature, whatever the number of tokens, of
 // which 7 or 5 on the integer pipe.
-#include <cstring>
+#include <type_traits>
 
-#include "mdw_attn.cuh"
 #include "mdw_internal.h"
+#include "w4_linear.cuh"
 
 namespace mdw {
 namespace {
 
-struct W4Params {
-  const uint8_t* q;
-  const void* scale;
-  const uint8_t* zero;
-  const void* x;
-  void* y;
-  const void* bias;
-  const void* residual;
-  int64_t ldx, ldy, ldr;
-  uint32_t* status;
-  long long spin_budget;
-  int M, N, K, y_f32;
-};
-
-constexpr int kUnit = 256;                     // codes of a feature in one swizzled line of 128 bytes
-
-__device__ __forceinline__ uint32_t and_or(uint32_t v, uint32_t mask, uint32_t bits) {
-  uint32_t r;
-  asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(r) : "r"(v), "r"(mask), "r"(bits));   // (v & mask) | bits in one operation
-  return r;
-}
-
-template <typename T> struct Int4;
-template <> struct Int4<__nv_bfloat16> {
-  // z2: 128 + zero in both halves
-  static __device__ __forceinline__ uint32_t zero2(uint32_t z) { return (0x4300u + z) * 0x00010001u; }
-  static __device__ __forceinline__ uint32_t sub(uint32_t v, uint32_t z2) {
-    uint32_t r;
-    asm("sub.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(v), "r"(z2));
-    return r;
-  }
-  static __device__ __forceinline__ void expand(uint32_t w, uint32_t z2, uint32_t (&p)[4]) {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) p[i] = sub(and_or(w >> (4 * i), 0x000f000fu, 0x43004300u), z2);
-  }
-  static __device__ __forceinline__ void mma(float (&d)[4], const float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
-    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%11,%12,%13};"
-                 : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
-                 : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(c[0]), "f"(c[1]), "f"(c[2]), "f"(c[3]));
-  }
-};
-template <> struct Int4<__half> {
-  // low half: 1024 + zero; the odd codes stay in their upper nibble as 1024 + 16 code and are brought
-  // down by one exact multiply-add: (1024 + 16 code) / 16 - (64 + zero)
-  static __device__ __forceinline__ uint32_t zero2(uint32_t z) { return (0x6400u + z) * 0x00010001u; }
-  static __device__ __forceinline__ void expand(uint32_t w, uint32_t z2, uint32_t (&p)[4]) {
-    // -(64 + zero) in f16: 0xd400 is -64, whose unit in the last place is 1 / 16
-    const uint32_t nz = 0xd400d400u + ((z2 & 0x000f000fu) << 4);
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const uint32_t v = w >> (8 * i), lo = and_or(v, 0x000f000fu, 0x64006400u), hi = and_or(v, 0x00f000f0u, 0x64006400u);
-      asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(p[2 * i]) : "r"(lo), "r"(z2));
-      asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(p[2 * i + 1]) : "r"(hi), "r"(0x2c002c00u), "r"(nz));
-    }
-  }
-  static __device__ __forceinline__ void mma(float (&d)[4], const float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
-    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%11,%12,%13};"
-                 : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
-                 : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(c[0]), "f"(c[1]), "f"(c[2]), "f"(c[3]));
-  }
-};
-
-
-__device__ __forceinline__ uint4 lds128(uint32_t a) {
-  uint4 v;
-  asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a) : "memory");
-  return v;
-}
 template <int kWords> __device__ __forceinline__ void lds_words(uint32_t (&w)[kWords], uint32_t a) {
   if constexpr (kWords == 1) asm volatile("ld.shared.u32 %0, [%1];" : "=r"(w[0]) : "r"(a) : "memory");
   if constexpr (kWords == 2) asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];" : "=r"(w[0]), "=r"(w[1]) : "r"(a) : "memory");
   if constexpr (kWords == 4)
     asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]) : "r"(a) : "memory");
 }
-// Eight elements of a token in the order of the expanded codes: pairs (j, j + 4).
-__device__ __forceinline__ void sts_paired(uint32_t a, uint4 v) {
-  asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" :: "r"(a), "r"(__byte_perm(v.x, v.z, 0x5410)), "r"(__byte_perm(v.x, v.z, 0x7632)),
-               "r"(__byte_perm(v.y, v.w, 0x5410)), "r"(__byte_perm(v.y, v.w, 0x7632)) : "memory");
-}
-__device__ __forceinline__ void tma_codes(uint32_t dst, const CUtensorMap* map, uint32_t bar, int byte, int row) {
-  asm volatile("cp.async.bulk.tensor.2d.shared::cta.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];"
-               :: "r"(dst), "l"(map), "r"(byte), "r"(row), "r"(bar) : "memory");
-}
-
 // Where a lane's two features' scales and zeros lie.
 template <typename T>
 struct ScaleRows {
@@ -575,9 +497,16 @@ cudaError_t launch_wide(const W4Params& p, int dev, cudaStream_t s) {
   return cudaLaunchKernelEx(&cfg, w4_wide_kernel<T, kGroup, kTiles>, p, map, split);
 }
 
+constexpr int kTensorTiles = 64;
 template <typename T, int kGroup>
 cudaError_t launch(const W4Params& p, int dev, cudaStream_t s) {
+  const int tiles = (p.N + kTensorRows - 1) / kTensorRows;
   if (p.M <= 8 && p.M * x_pitch(p.K) <= kRowMaxX) return launch_rows<T, kGroup>(p, dev, s);
+  if (tiles >= kTensorTiles) {
+    CUtensorMap map;
+    if (!encode_codes(&map, p, kTensorRows)) return cudaErrorInvalidValue;
+    return launch_w4_tensor(p, map, std::is_same<T, __nv_bfloat16>::value, kGroup, dev, s);
+  }
   if (p.M <= 8) return launch_wide<T, kGroup, 1>(p, dev, s);
   return p.M <= 16 ? launch_wide<T, kGroup, 2>(p, dev, s) : launch_wide<T, kGroup, 4>(p, dev, s);
 }

@@ -731,3 +731,22 @@ def test_handles_of_another_kind_are_refused():
     with pytest.raises(api.MdwError) as e:
         api.mdw_kv_write(w, rows, rows, torch.zeros(1, dtype=torch.int64, device="cuda"))
     assert e.value.code == 3
+
+
+@pytest.mark.parametrize("m,n,k,group,zero,dtype,ydtype", [
+    (9, 8192, 256, 32, True, BF, BF), (16, 8200, 320, 32, True, HF, F32), (17, 8193, 384, 128, True, BF, F32), (32, 20000, 2560, 64, False, HF, HF),
+    (32, 8321, 2880, 32, True, BF, BF), (31, 8200, 5120, 128, False, BF, F32), (13, 9001, 6400, 64, True, HF, F32), (8, 8192, 12800, 128, True, BF, F32)])
+def test_w4_linear_many_features(m, n, k, group, zero, dtype, ydtype):
+    """Features for every block and more, with tokens that fit a block's shared memory and ones that do not."""
+    w = w4_case(m + n, n, k, group, zero, dtype)
+    x = torch.randn((m, k), generator=gen(2), device="cuda").to(dtype)
+    bias = torch.randn(n, generator=gen(3), device="cuda").to(dtype)
+    res = torch.randn((m, n), generator=gen(4), device="cuda").to(dtype)
+    y = torch.full((m + 1, n), 7.0, dtype=ydtype, device="cuda")
+    api.w4_linear(w, x, y[:m], bias=bias, residual=res)
+    want, tol = w4_want(w, x, bias, res)
+    assert_close(host(y[:m]), want, tol + half_step(ydtype) * np.abs(want))
+    assert (y[m] == 7.0).all()
+    again = torch.empty_like(y[:m])
+    api.w4_linear(w, x, again, bias=bias, residual=res)
+    assert torch.equal(again, y[:m])
