@@ -134,20 +134,19 @@ struct Lane {
   }
 };
 
-// 16 features x kUnit codes x kTiles * 8 tokens: acc += scale * (codes - zero) . x. `code`: the lane's words of
-// group 0 (its second feature lies 1,024 bytes further). x[t]: the lane's elements of its token in tile
-// t; a column without a token repeats the last one's, its sums are not stored. Codes and elements behind
-// K are zeros.
-template <typename T, int kGroup, int kTiles>
-__device__ __forceinline__ void multiply(uint32_t code, const uint32_t (&x)[kTiles], const Scales<T, kGroup>& sc, float (&acc)[kTiles][4]) {
+// 16 features x kUnit codes x 8 tokens: acc += scale * (codes - zero) . x. `code`: the lane's words of group 0 (its
+// second feature lies 1,024 bytes further). x: the lane's elements of its token; a column without a token
+// repeats the last one's, its sums are not stored. Codes and elements behind K are zeros.
+template <typename T, int kGroup>
+__device__ __forceinline__ void multiply(uint32_t code, uint32_t x, const Scales<T, kGroup>& sc, float (&acc)[4]) {
   constexpr int kWords = Lane<kGroup>::kWords;
   constexpr float kNone[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
   for (int s = 0; s < kUnit / kGroup; ++s) {
     const uint32_t z0 = sc.zero2(0, s), z1 = sc.zero2(1, s);
-    // one tile's products are two chains, so that one need not wait for the other's result
-    constexpr int kChains = kTiles == 1 && kWords > 1 ? 2 : 1;
-    float d[kChains][kTiles][4];
+    // two chains of products, so that one need not wait for the other's result
+    constexpr int kChains = kWords > 1 ? 2 : 1;
+    float d[kChains][4];
     uint32_t w0[kWords], w1[kWords];
     lds_words<kWords>(w0, code ^ (s * kGroup / 2));
     lds_words<kWords>(w1, (code ^ (s * kGroup / 2)) + 1024);
@@ -156,34 +155,29 @@ __device__ __forceinline__ void multiply(uint32_t code, const uint32_t (&x)[kTil
       uint32_t lo[4], hi[4];
       Int4<T>::expand(w0[w], z0, lo);
       Int4<T>::expand(w1[w], z1, hi);
-#pragma unroll
-      for (int t = 0; t < kTiles; ++t) {
-        float (&sum)[4] = d[w % kChains][t];
-        const uint4 v = lds128(x[t] + s * (2 * kGroup) + 64 * w);
-        if (w < kChains) Int4<T>::mma(sum, kNone, lo[0], hi[0], lo[1], hi[1], v.x, v.y);
-        else Int4<T>::mma(sum, sum, lo[0], hi[0], lo[1], hi[1], v.x, v.y);
-        Int4<T>::mma(sum, sum, lo[2], hi[2], lo[3], hi[3], v.z, v.w);
-      }
+      float (&sum)[4] = d[w % kChains];
+      const uint4 v = lds128(x + s * (2 * kGroup) + 64 * w);
+      if (w < kChains) Int4<T>::mma(sum, kNone, lo[0], hi[0], lo[1], hi[1], v.x, v.y);
+      else Int4<T>::mma(sum, sum, lo[0], hi[0], lo[1], hi[1], v.x, v.y);
+      Int4<T>::mma(sum, sum, lo[2], hi[2], lo[3], hi[3], v.z, v.w);
     }
     const float s0 = sc.scale(0, s), s1 = sc.scale(1, s);
 #pragma unroll
-    for (int t = 0; t < kTiles; ++t)
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        float sum = d[0][t][e];
-        if constexpr (kChains == 2) sum += d[1][t][e];
-        acc[t][e] = fmaf(e < 2 ? s0 : s1, sum, acc[t][e]);
-      }
+    for (int e = 0; e < 4; ++e) {
+      float sum = d[0][e];
+      if constexpr (kChains == 2) sum += d[1][e];
+      acc[e] = fmaf(e < 2 ? s0 : s1, sum, acc[e]);
+    }
   }
 }
 
-// The lane's two features of the 16 from n0 on, tokens t0 + 2 q + {0, 1}: bias, residual, one rounding.
+// The lane's two features of the 16 from n0 on, tokens 2 q + {0, 1}: bias, residual, one rounding.
 template <typename T>
-__device__ __forceinline__ void store(const W4Params& p, int n0, int t0, int lane, const float (&acc)[4]) {
+__device__ __forceinline__ void store(const W4Params& p, int n0, int lane, const float (&acc)[4]) {
   const int f = Lane<32>::feature(lane), q = lane & 3;
 #pragma unroll
   for (int e = 0; e < 4; ++e) {
-    const int n = n0 + f + 8 * (e >> 1), t = t0 + 2 * q + (e & 1);
+    const int n = n0 + f + 8 * (e >> 1), t = 2 * q + (e & 1);
     if (n >= p.N || t >= p.M) continue;
     float v = acc[e];
     if (p.bias) v += Elem<T>::to_float(static_cast<const T*>(p.bias)[n]);
@@ -273,15 +267,15 @@ w4_rows_kernel(const W4Params p, const __grid_constant__ CUtensorMap codes, int 
   bool from_start = unit == 0;
   int stage = 0;
   uint32_t phase = 0;
-  float acc[1][4] = {{0.f, 0.f, 0.f, 0.f}};
+  float acc[4] = {0.f, 0.f, 0.f, 0.f};
   const uint32_t code = ring + Lane<kGroup>::code(lane), x = xs + min(lane >> 2, p.M - 1) * pitch + 16 * (lane & 3);
   for (int u = u0; u < u1; ++u) {
     scales(next);
     mbar_wait(bar + 8 * stage, phase, p.spin_budget, p.status, dead);
     __syncwarp();
-    const uint32_t at = code + stage * kRowBytes, x0[1] = {x + unit * (2 * kRowUnit)}, x1[1] = {x0[0] + 2 * kUnit};
-    multiply<T, kGroup, 1>(at, x0, now[0], acc);
-    if (unit * kRowUnit + kUnit < p.K) multiply<T, kGroup, 1>(at + kLineBytes, x1, now[1], acc);
+    const uint32_t at = code + stage * kRowBytes, x0 = x + unit * (2 * kRowUnit);
+    multiply<T, kGroup>(at, x0, now[0], acc);
+    if (unit * kRowUnit + kUnit < p.K) multiply<T, kGroup>(at + kLineBytes, x0 + 2 * kUnit, now[1], acc);
     __syncwarp();
     if (lane == 0 && ask < u1 && !*dead) request(stage);
     now[0] = next[0];
@@ -289,12 +283,12 @@ w4_rows_kernel(const W4Params p, const __grid_constant__ CUtensorMap codes, int 
     if (++stage == kRowStages) { stage = 0; phase ^= 1; }
     if (++unit == units || u + 1 == u1) {
       if (from_start && unit == units) {
-        if (!*dead) store<T>(p, (t0 + tile) * 16, 0, lane, acc[0]);
+        if (!*dead) store<T>(p, (t0 + tile) * 16, lane, acc);
       } else {
 #pragma unroll
-        for (int e = 0; e < 4; ++e) part[warp][from_start ? 1 : 0][e][lane] = acc[0][e];
+        for (int e = 0; e < 4; ++e) part[warp][from_start ? 1 : 0][e][lane] = acc[e];
       }
-      acc[0][0] = acc[0][1] = acc[0][2] = acc[0][3] = 0.f;
+      acc[0] = acc[1] = acc[2] = acc[3] = 0.f;
       from_start = true;
       if (unit == units) { unit = 0; ++tile; }
     }
@@ -317,135 +311,13 @@ w4_rows_kernel(const W4Params p, const __grid_constant__ CUtensorMap codes, int 
     if (share(w + 1) > share(w)) return;                        // an earlier warp does
   while (share(w + 1) <= begin) ++w;
 #pragma unroll
-  for (int e = 0; e < 4; ++e) acc[0][e] = part[w][1][e][lane];
+  for (int e = 0; e < 4; ++e) acc[e] = part[w][1][e][lane];
   for (++w; w < kRowWarps && share(w) < begin + units; ++w) {
     if (share(w + 1) == share(w)) continue;
 #pragma unroll
-    for (int e = 0; e < 4; ++e) acc[0][e] += part[w][0][e][lane];
+    for (int e = 0; e < 4; ++e) acc[e] += part[w][0][e][lane];
   }
-  store<T>(p, (t0 + cut) * 16, 0, lane, acc[0]);
-}
-
-// ------------------------------------------------------------------ wider windows
-//
-// Where the window's x does not fit, eight warps of 128 features share its elements: a stage holds one
-// unit of 128 features (one TMA box) and of the tokens. A cluster of blocks splits K where
-// there are few blocks of features, and joins the sums over distributed shared memory, in rank order.
-constexpr int kWideRows = 128, kWideStages = 3, kWideCodes = kWideRows * kUnit / 2, kWidePitch = 2 * kUnit + 64;
-
-template <typename T, int kGroup, int kTiles>
-__global__ void __launch_bounds__(256, 2)
-w4_wide_kernel(const W4Params p, const __grid_constant__ CUtensorMap codes, int split) {
-  extern __shared__ uint8_t raw_smem[];
-  __shared__ __align__(8) uint64_t bars[kWideStages];
-  __shared__ int dead_flag;
-  volatile int* dead = &dead_flag;
-  constexpr int kChunks = 8 * kTiles * (kUnit / 8) / 256;       // 16-byte pieces of x per thread and stage
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, f = Lane<kGroup>::feature(lane);
-  const int rank = blockIdx.x % split, n0 = blockIdx.x / split * kWideRows;
-  const int units = (p.K + kUnit - 1) / kUnit, u0 = units * rank / split, u1 = units * (rank + 1) / split;
-  const uint32_t base = (smem_u32(raw_smem) + 1023) & ~1023u, xs = base + kWideStages * kWideCodes, bar = smem_u32(bars);
-  const int x_bytes = p.M * kWidePitch;
-
-  auto request = [&](int u) {                                   // thread 0
-    const int stage = (u - u0) % kWideStages;
-    mbar_arrive_tx(bar + 8 * stage, kWideCodes);
-    tma_codes(base + stage * kWideCodes, &codes, bar + 8 * stage, u * (kUnit / 2), n0);
-  };
-  // the thread's pieces of x: token t_x + 8 i, elements k_x .. k_x + 7 of the unit
-  const int t_x = threadIdx.x / (kUnit / 8), k_x = threadIdx.x % (kUnit / 8) * 8;
-  const T* x_src = static_cast<const T*>(p.x) + t_x * p.ldx + k_x;
-  const uint32_t x_dst = xs + t_x * kWidePitch + Lane<kGroup>::element(k_x);
-  uint4 piece[kChunks];
-  auto load_x = [&](int u) {
-    const bool in = u * kUnit + k_x < p.K;
-#pragma unroll
-    for (int i = 0; i < kChunks; ++i)
-      piece[i] = in && t_x + 8 * i < p.M ? *reinterpret_cast<const uint4*>(x_src + u * kUnit + 8 * i * p.ldx) : make_uint4(0u, 0u, 0u, 0u);
-  };
-  auto store_x = [&](int stage) {
-#pragma unroll
-    for (int i = 0; i < kChunks; ++i)
-      if (t_x + 8 * i < p.M) sts_paired(x_dst + stage * x_bytes + 8 * i * kWidePitch, piece[i]);
-  };
-  if (threadIdx.x == 0) {
-    *dead = 0;
-    for (int i = 0; i < kWideStages; ++i) mbar_init(bar + 8 * i, 1);
-    mbar_init_fence();
-    for (int u = u0; u < u1 && u < u0 + kWideStages - 1; ++u) request(u);
-  }
-  const int n = n0 + warp * 16 + f;
-  ScaleRows<T> rows;
-  rows.begin(p, n, p.K / kGroup);
-  Scales<T, kGroup> now, next;
-  if (u0 < u1) now.load(p, rows, u0);
-  for (int i = 0; i < kWideStages - 1 && u0 + i < u1; ++i) {
-    load_x(u0 + i);
-    store_x(i);
-  }
-  float acc[kTiles][4];
-#pragma unroll
-  for (int t = 0; t < kTiles; ++t) acc[t][0] = acc[t][1] = acc[t][2] = acc[t][3] = 0.f;
-  const uint32_t code = base + warp * 16 * 128 + Lane<kGroup>::code(lane);
-  uint32_t x[kTiles];
-#pragma unroll
-  for (int t = 0; t < kTiles; ++t) x[t] = xs + min(8 * t + (lane >> 2), p.M - 1) * kWidePitch + 16 * (lane & 3);
-  __syncthreads();
-  int stage = 0, far_stage = kWideStages - 1;
-  uint32_t phase = 0;
-  for (int u = u0; u < u1; ++u) {
-    const int far = u + kWideStages - 1;
-    // the stage of unit `far` was read last in the iteration before, which every warp has left
-    if (threadIdx.x == 0 && far < u1 && !*dead) request(far);
-    if (far < u1) load_x(far);
-    if (u + 1 < u1) next.load(p, rows, u + 1);
-    mbar_wait(bar + 8 * stage, phase, p.spin_budget, p.status, dead);
-    __syncwarp();
-    uint32_t xu[kTiles];
-#pragma unroll
-    for (int t = 0; t < kTiles; ++t) xu[t] = x[t] + stage * x_bytes;
-    multiply<T, kGroup, kTiles>(code + stage * kWideCodes, xu, now, acc);
-    if (far < u1) store_x(far_stage);
-    now = next;
-    if (++stage == kWideStages) { stage = 0; phase ^= 1; }
-    if (++far_stage == kWideStages) far_stage = 0;
-    __syncthreads();
-  }
-  if (*dead && threadIdx.x == 0)
-    for (int i = 0; i < kWideStages && u0 + i < u1; ++i) mbar_drain(bar + 8 * i, ((u1 - u0 - i + kWideStages - 1) / kWideStages - 1) & 1);
-  if (split == 1) {
-    if (*dead) return;
-#pragma unroll
-    for (int t = 0; t < kTiles; ++t) store<T>(p, n0 + warp * 16, 8 * t, lane, acc[t]);
-    return;
-  }
-#pragma unroll
-  for (int t = 0; t < kTiles; ++t)
-    asm volatile("st.shared.v4.f32 [%0], {%1,%2,%3,%4};" :: "r"(base + ((warp * kTiles + t) * 32 + lane) * 16), "f"(acc[t][0]), "f"(acc[t][1]),
-                 "f"(acc[t][2]), "f"(acc[t][3]) : "memory");
-  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
-  bool lost = false;                                            // a dead block anywhere in the cluster
-  for (int r = 0; r < split; ++r) {
-    uint32_t a, v;
-    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_u32(&dead_flag)), "r"(r));
-    asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(a) : "memory");
-    lost |= v != 0;
-  }
-  for (int i = rank * 8 + warp; i < 8 * kTiles && !lost; i += 8 * split) {
-    float sum[4] = {0.f, 0.f, 0.f, 0.f};
-    for (int r = 0; r < split; ++r) {
-      uint32_t a;
-      float4 v;
-      asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(base + (i * 32 + lane) * 16), "r"(r));
-      asm volatile("ld.shared::cluster.v4.f32 {%0,%1,%2,%3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(a) : "memory");
-      sum[0] += v.x;
-      sum[1] += v.y;
-      sum[2] += v.z;
-      sum[3] += v.w;
-    }
-    store<T>(p, n0 + i / kTiles * 16, i % kTiles * 8, lane, sum);
-  }
-  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+  store<T>(p, (t0 + cut) * 16, lane, acc);
 }
 
 // ------------------------------------------------------------------ launches
@@ -472,43 +344,14 @@ cudaError_t launch_rows(const W4Params& p, int dev, cudaStream_t s) {
   return cudaGetLastError();
 }
 
-template <typename T, int kGroup, int kTiles>
-cudaError_t launch_wide(const W4Params& p, int dev, cudaStream_t s) {
-  cudaError_t e = allow_shared_memory<w4_wide_kernel<T, kGroup, kTiles>>(dev);
-  if (e != cudaSuccess) return e;
-  CUtensorMap map;
-  if (!encode_codes(&map, p, kWideRows)) return cudaErrorInvalidValue;
-  const int blocks = (p.N + kWideRows - 1) / kWideRows, units = (p.K + kUnit - 1) / kUnit;
-  // two blocks an SM, all resident at once
-  int split = 2 * sm_count(dev) / blocks;
-  split = split < 1 ? 1 : (split > 8 ? 8 : split);
-  if (split > units / 2) split = units < 2 ? 1 : units / 2;
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3((unsigned)(blocks * split));
-  cfg.blockDim = dim3(256);
-  cfg.dynamicSmemBytes = 1024 + kWideStages * (kWideCodes + p.M * kWidePitch);
-  cfg.stream = s;
-  cudaLaunchAttribute a{};
-  a.id = cudaLaunchAttributeClusterDimension;
-  a.val.clusterDim.x = split;
-  a.val.clusterDim.y = a.val.clusterDim.z = 1;
-  cfg.attrs = &a;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, w4_wide_kernel<T, kGroup, kTiles>, p, map, split);
-}
-
-constexpr int kTensorTiles = 64;
+// Up to 8 tokens whose elements leave two blocks a SM's shared memory: the rows' kernel (8 tokens x 2560 elements do not: at
+// 157184 features 52 us on tcgen05; one token 47 us, against 57).
 template <typename T, int kGroup>
 cudaError_t launch(const W4Params& p, int dev, cudaStream_t s) {
-  const int tiles = (p.N + kTensorRows - 1) / kTensorRows;
   if (p.M <= 8 && p.M * x_pitch(p.K) <= kRowMaxX) return launch_rows<T, kGroup>(p, dev, s);
-  if (tiles >= kTensorTiles) {
-    CUtensorMap map;
-    if (!encode_codes(&map, p, kTensorRows)) return cudaErrorInvalidValue;
-    return launch_w4_tensor(p, map, std::is_same<T, __nv_bfloat16>::value, kGroup, dev, s);
-  }
-  if (p.M <= 8) return launch_wide<T, kGroup, 1>(p, dev, s);
-  return p.M <= 16 ? launch_wide<T, kGroup, 2>(p, dev, s) : launch_wide<T, kGroup, 4>(p, dev, s);
+  CUtensorMap map;
+  if (!encode_codes(&map, p, kTensorRows)) return cudaErrorInvalidValue;
+  return launch_w4_tensor(p, map, std::is_same<T, __nv_bfloat16>::value, kGroup, dev, s);
 }
 template <typename T>
 cudaError_t launch(const W4Params& p, int group, int dev, cudaStream_t s) {

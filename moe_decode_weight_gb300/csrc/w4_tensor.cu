@@ -17,6 +17,7 @@
 // them, 1024 + code and 1024 + 16 code. bf16 has too few of those, but its numbers up to 255 * 2^-133, subnormal
 // and the first normal ones, are the integers times 2^-133; the product with 2^127 (2^123) makes them
 // code * 2^-6, and the factor 64 goes into the scale. 12 operations for eight codes of a feature, done once for all tokens.
+#include <atomic>
 #include <type_traits>
 
 #include "mdw_internal.h"
@@ -26,6 +27,7 @@
 namespace mdw {
 namespace {
 
+constexpr int kMostSplit = 8, kJoinUnits = 3;
 constexpr int kThreads = 512, kCodeBytes = kTensorRows * kUnit / 2, kHalf = kUnit / 2;
 constexpr int kOperands = 4;                   // halves of a unit in tensor memory, expanded, 64 columns each
 
@@ -38,10 +40,10 @@ struct WideSmem {
   static __device__ __forceinline__ int place(int n, int half) { return n % kIssuers * kRing + (2 * (n / kIssuers) + half) % kRing; }
   static __device__ __forceinline__ int round(int n, int half) { return (2 * (n / kIssuers) + half) / kRing & 1; }
   static constexpr int kXBlock = kTokens * 128, kStageBytes = kCodeBytes + 4 * kXBlock;   // 64 elements of the tokens; codes and tokens of a unit
-  static constexpr int kStages = 224 * 1024 / kStageBytes, kBars = kStages * kStageBytes;
-  static constexpr int kFull = kBars, kEmpty = kFull + 8 * kStages, kOperand = kEmpty + 8 * kStages, kOperandFree = kOperand + 8 * 2;
+  static constexpr int kStages = 200 * 1024 / kStageBytes, kJoin = kStages * kStageBytes, kBars = kJoin + kTokens * kTensorRows * 4;
+  static constexpr int kFull = kBars, kEmpty = kFull + 8 * kStages, kOperand = kEmpty + 8 * kStages, kOperandFree = kOperand + 8 * kOperands;
   static constexpr int kResult = kOperandFree + 8 * kOperands, kResultFree = kResult + 8 * kResults, kEnd = kResultFree + 8 * kResults;
-  static constexpr int kDead = kEnd + 8, kTmem = kDead + 4, kTotal = kTmem + 4 + 1024;   // (and the alignment of the swizzled tiles)
+  static constexpr int kJoinReady = kEnd + 8, kJoinFree = kJoinReady + 8, kDead = kJoinFree + 8, kTmem = kDead + 4, kTotal = kTmem + 4 + 1024;   // (and the alignment of the swizzled tiles)
 };
 
 // Eight codes, neighbours in the halves of a word.
@@ -66,17 +68,43 @@ template <> struct Neighbours<__half> {
   }
 };
 
-// Position in the sequence of (tile, unit) that every role of a block walks over.
+// Position in the sequence of (tile, unit) that every role of a block walks over: units first .. last - 1 of each tile.
 struct Units {
-  int tile, unit, units, tiles, step;
+  int tile, unit, first, last, tiles, step;
   __device__ __forceinline__ bool more() const { return tile < tiles; }
   __device__ __forceinline__ void next() {
-    if (++unit == units) {
-      unit = 0;
+    if (++unit == last) {
+      unit = first;
       tile += step;
     }
   }
 };
+
+// Blocks of a cluster: address of another block's shared memory, arrival there, a wait for arrivals from there.
+__device__ __forceinline__ uint32_t in_block(uint32_t a, int rank) {
+  uint32_t r;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(rank));
+  return r;
+}
+__device__ __forceinline__ void arrive_cluster(uint32_t bar) {
+  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" :: "r"(bar) : "memory");
+}
+__device__ __forceinline__ void wait_cluster(uint32_t bar, uint32_t parity, const W4Params& p, volatile int* dead) {
+  const long long t0 = clock64();
+  uint32_t ok = 0;
+  while (!*dead) {
+    asm volatile("{ .reg .pred p; mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2; selp.u32 %0, 1, 0, p; }"
+                 : "=r"(ok) : "r"(bar), "r"(parity) : "memory");
+    if (ok) return;
+    if (clock64() - t0 > p.spin_budget) {
+      *dead = 1;
+      raise_status(p.status, MDW_ERR_TIMEOUT);
+    }
+  }
+}
+__device__ __forceinline__ void sync_cluster() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
 
 // Scales or zeros of one unit (256 / kGroup of them) for one feature.
 template <int kGroup>
@@ -146,7 +174,7 @@ __device__ __forceinline__ void prefetch_scales(const W4Params& p, const Units& 
 
 template <typename T, int kGroup, int kTokens>
 __global__ void __launch_bounds__(kThreads, 1)
-w4_tensor_kernel(const W4Params p, const __grid_constant__ CUtensorMap codes, const __grid_constant__ CUtensorMap tokens) {
+w4_tensor_kernel(const W4Params p, const __grid_constant__ CUtensorMap codes, const __grid_constant__ CUtensorMap tokens, int split) {
   using L = WideSmem<kGroup, kTokens>;
   extern __shared__ uint8_t raw_smem[];
   const uint32_t base = (smem_u32(raw_smem) + 1023) & ~1023u;
@@ -163,14 +191,16 @@ w4_tensor_kernel(const W4Params p, const __grid_constant__ CUtensorMap codes, co
       mbar_init(bar(L::kEmpty, i), 5);                          // four warps that expand; the products
     }
     for (int i = 0; i < kOperands; ++i) {
+      mbar_init(bar(L::kOperand, i), 4);
       mbar_init(bar(L::kOperandFree, i), 1);
     }
-    for (int i = 0; i < 2; ++i) mbar_init(bar(L::kOperand, i), 4);
     for (int i = 0; i < L::kResults; ++i) {
       mbar_init(bar(L::kResult, i), 1);
       mbar_init(bar(L::kResultFree, i), 4);
     }
     mbar_init(bar(L::kEnd, 0), L::kIssuers);
+    mbar_init(bar(L::kJoinReady, 0), 4 * split);
+    mbar_init(bar(L::kJoinFree, 0), 4 * split);
     *dead = 0;
     mbar_init_fence();
   }
@@ -182,8 +212,9 @@ w4_tensor_kernel(const W4Params p, const __grid_constant__ CUtensorMap codes, co
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = __shfl_sync(0xffffffffu, *reinterpret_cast<volatile uint32_t*>(smem + L::kTmem), 0);
-  const int units = (p.K + kUnit - 1) / kUnit;
-  Units at{(int)blockIdx.x, 0, units, (p.N + kTensorRows - 1) / kTensorRows, (int)gridDim.x};
+  if (split > 1) sync_cluster();                                // the others' barriers are there
+  const int units = (p.K + kUnit - 1) / kUnit, rank = blockIdx.x % split, u0 = units * rank / split;
+  Units at{(int)blockIdx.x / split, u0, u0, units * (rank + 1) / split, (p.N + kTensorRows - 1) / kTensorRows, (int)gridDim.x / split};
 
   if (warp == 0) {
     // ---- copies
@@ -208,14 +239,14 @@ w4_tensor_kernel(const W4Params p, const __grid_constant__ CUtensorMap codes, co
     if (warp == 2) at.next();
     for (int n = warp - 1; at.more(); n += L::kIssuers) {
       const int stage = n % L::kStages;
-      // the unit's codes are expanded, so its copies, the tokens among them, are there as well
-      wait(bar(L::kOperand, n & 1), n / 2 & 1);
 #pragma unroll
       for (int half = 0; half < 2; ++half) {
         const int from = (2 * n + half) % kOperands, to = L::place(n, half);
         const uint32_t a = tmem + from * 64, d = tmem + kOperands * 64 + to * L::kHalfColumns;
         const uint32_t x = operand_low(base + stage * L::kStageBytes + kCodeBytes + half * 2 * L::kXBlock, 16);
         wait(bar(L::kResultFree, to), L::round(n, half) ^ 1);
+        // the codes are expanded, so the unit's copies, the tokens among them, are there as well
+        wait(bar(L::kOperand, from), n / 2 & 1);
         tc_fence_after();
         if (elect_one()) {
 #pragma unroll
@@ -269,13 +300,13 @@ w4_tensor_kernel(const W4Params p, const __grid_constant__ CUtensorMap codes, co
           for (int j = 0; j < 16; ++j) e[j] = Neighbours<T>::expand(__byte_perm(w[j / 4], 0u, 0x4040u + 0x0101u * (j % 4)), z);
           tc_st16(tmem + lanes + to * 64 + 16 * i, e);
         }
-      }
-      tc_wait_st();
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) {
-        mbar_arrive(bar(L::kEmpty, stage));
-        mbar_arrive(bar(L::kOperand, set));
+        tc_wait_st();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive(bar(L::kOperand, to));
+          if (half == 1) mbar_arrive(bar(L::kEmpty, stage));
+        }
       }
     }
   } else if (warp >= 12) {
@@ -292,6 +323,7 @@ w4_tensor_kernel(const W4Params p, const __grid_constant__ CUtensorMap codes, co
     float acc[kTokens];
 #pragma unroll
     for (int t = 0; t < kTokens; ++t) acc[t] = 0.f;
+    int round = 0;                                              // tiles joined
     for (int n = 0; at.more(); ++n) {
       const int feature = at.tile * kTensorRows + row, unit = at.unit;
       now = next;
@@ -331,18 +363,53 @@ w4_tensor_kernel(const W4Params p, const __grid_constant__ CUtensorMap codes, co
           }
         }
       }
-      if (unit + 1 < units) continue;
-      if (feature < p.N && !*dead) {
-        const float b = p.bias ? Elem<T>::to_float(static_cast<const T*>(p.bias)[feature]) : 0.f;
+      if (unit + 1 < at.last) continue;
+      auto store = [&](int t, float v) {
+        if (p.bias) v += Elem<T>::to_float(static_cast<const T*>(p.bias)[feature]);
+        if (p.residual) v += Elem<T>::to_float(static_cast<const T*>(p.residual)[t * p.ldr + feature]);
+        if (p.y_f32) static_cast<float*>(p.y)[t * p.ldy + feature] = v;
+        else static_cast<T*>(p.y)[t * p.ldy + feature] = Elem<T>::from_float(v);
+      };
+      if (split == 1) {
+        if (feature < p.N && !*dead) {
 #pragma unroll
-        for (int t = 0; t < kTokens; ++t) {
-          if (t >= p.M) break;
-          float v = acc[t];
-          if (p.bias) v += b;
-          if (p.residual) v += Elem<T>::to_float(static_cast<const T*>(p.residual)[t * p.ldr + feature]);
-          if (p.y_f32) static_cast<float*>(p.y)[t * p.ldy + feature] = v;
-          else static_cast<T*>(p.y)[t * p.ldy + feature] = Elem<T>::from_float(v);
+          for (int t = 0; t < kTokens; ++t)
+            if (t < p.M) store(t, acc[t]);
         }
+      } else {
+        // the blocks of a cluster have a part of K each: every one adds up some of the tokens, in the blocks' order
+        const uint32_t place = base + L::kJoin + row * 4;
+        wait_cluster(bar(L::kJoinFree, 0), (round & 1) ^ 1, p, dead);
+#pragma unroll
+        for (int t = 0; t < kTokens; ++t) asm volatile("st.shared.f32 [%0], %1;" :: "r"(place + t * (kTensorRows * 4)), "f"(acc[t]) : "memory");
+        __syncwarp();
+        if (lane < split && !*dead) arrive_cluster(in_block(bar(L::kJoinReady, 0), lane));
+        wait_cluster(bar(L::kJoinReady, 0), round & 1, p, dead);
+        __syncwarp();
+        if (!*dead) {
+          for (int t0 = rank; t0 < p.M; t0 += 2 * split) {
+            float part[2][kMostSplit];                          // requested together: each takes some 250 cycles
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+#pragma unroll
+              for (int r = 0; r < kMostSplit; ++r) {
+                part[i][r] = 0.f;
+                const int t = t0 + i * split;
+                if (r < split && t < p.M)
+                  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(part[i][r]) : "r"(in_block(place + t * (kTensorRows * 4), r)) : "memory");
+              }
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+              float v = 0.f;
+#pragma unroll
+              for (int r = 0; r < kMostSplit; ++r) v += part[i][r];
+              if (feature < p.N && t0 + i * split < p.M) store(t0 + i * split, v);
+            }
+          }
+        }
+        __syncwarp();
+        if (lane < split && !*dead) arrive_cluster(in_block(bar(L::kJoinFree, 0), lane));
+        ++round;
       }
 #pragma unroll
       for (int t = 0; t < kTokens; ++t) acc[t] = 0.f;
@@ -353,6 +420,10 @@ w4_tensor_kernel(const W4Params p, const __grid_constant__ CUtensorMap codes, co
   if (warp == 1) {
     tc_fence_after();
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" :: "r"(tmem) : "memory");
+  }
+  if (split > 1) {
+    __syncthreads();
+    sync_cluster();                                             // no block ends while another reads its sums
   }
 }
 
@@ -365,15 +436,56 @@ bool encode_tokens(CUtensorMap* map, const W4Params& p, int tokens) {
                   CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_128B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// Clusters of `split` blocks that a device runs at once, asked once.
+template <auto kKernel>
+int clusters(const cudaLaunchConfig_t& cfg, int split, int dev) {
+  static std::atomic<int> known[kMaxDevices][kMostSplit + 1];
+  int n = known[dev][split].load(std::memory_order_relaxed);
+  if (n == 0) {
+    if (cudaOccupancyMaxActiveClusters(&n, kKernel, &cfg) != cudaSuccess || n < 1) {
+      cudaGetLastError();
+      n = -1;
+    }
+    known[dev][split].store(n, std::memory_order_relaxed);
+  }
+  return n;
+}
+
 template <typename T, int kGroup, int kTokens>
 cudaError_t launch(const W4Params& p, const CUtensorMap& codes, int dev, cudaStream_t s) {
-  const cudaError_t e = allow_shared_memory<w4_tensor_kernel<T, kGroup, kTokens>>(dev);
+  constexpr auto kKernel = w4_tensor_kernel<T, kGroup, kTokens>;
+  const cudaError_t e = allow_shared_memory<kKernel>(dev);
   if (e != cudaSuccess) return e;
   CUtensorMap tokens;
   if (!encode_tokens(&tokens, p, kTokens)) return cudaErrorInvalidValue;
-  const int tiles = (p.N + kTensorRows - 1) / kTensorRows, sms = sm_count(dev);
-  w4_tensor_kernel<T, kGroup, kTokens><<<tiles < sms ? tiles : sms, kThreads, WideSmem<kGroup, kTokens>::kTotal, s>>>(p, codes, tokens);
-  return cudaGetLastError();
+  const int tiles = (p.N + kTensorRows - 1) / kTensorRows, units = (p.K + kUnit - 1) / kUnit;
+  cudaLaunchConfig_t cfg{};
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = WideSmem<kGroup, kTokens>::kTotal;
+  cfg.stream = s;
+  cudaLaunchAttribute a{};
+  a.id = cudaLaunchAttributeClusterDimension;
+  a.val.clusterDim.y = a.val.clusterDim.z = 1;
+  cfg.attrs = &a;
+  cfg.numAttrs = 1;
+  // Blocks to a tile, each with a part of K: the fewest units that a block goes through one after the other, a join counted
+  // as kJoinUnits of them.
+  int split = 1, many = sm_count(dev), best = (tiles + many - 1) / many * units;
+  for (int n = 2; n <= kMostSplit && n <= units; ++n) {
+    a.val.clusterDim.x = n;
+    cfg.gridDim = dim3((unsigned)n);
+    const int fit = clusters<kKernel>(cfg, n, dev);
+    if (fit < 1) continue;
+    const int cost = (tiles + fit - 1) / fit * ((units + n - 1) / n + kJoinUnits);
+    if (cost < best) {
+      best = cost;
+      split = n;
+      many = fit;
+    }
+  }
+  a.val.clusterDim.x = split;
+  cfg.gridDim = dim3((unsigned)(split * (tiles < many ? tiles : many)));
+  return cudaLaunchKernelEx(&cfg, kKernel, p, codes, tokens, split);
 }
 template <typename T, int kGroup>
 cudaError_t launch(const W4Params& p, const CUtensorMap& codes, int dev, cudaStream_t s) {
