@@ -17,6 +17,7 @@
 // them, 1024 + code and 1024 + 16 code. bf16 has too few of those, but its numbers up to 255 * 2^-133, subnormal
 // and the first normal ones, are the integers times 2^-133; the product with 2^127 (2^123) makes them
 // code * 2^-6, and the factor 64 goes into the scale. 12 operations for eight codes of a feature, done once for all tokens.
+#include <algorithm>
 #include <atomic>
 #include <type_traits>
 
@@ -27,7 +28,7 @@
 namespace mdw {
 namespace {
 
-constexpr int kMostSplit = 8, kJoinUnits = 3;
+constexpr int kMostCluster = 8;
 constexpr int kThreads = 512, kCodeBytes = kTensorRows * kUnit / 2, kHalf = kUnit / 2;
 constexpr int kOperands = 4;                   // halves of a unit in tensor memory, expanded, 64 columns each
 
@@ -39,11 +40,13 @@ struct WideSmem {
   // Place of a half of unit n, and the parity of its round.
   static __device__ __forceinline__ int place(int n, int half) { return n % kIssuers * kRing + (2 * (n / kIssuers) + half) % kRing; }
   static __device__ __forceinline__ int round(int n, int half) { return (2 * (n / kIssuers) + half) / kRing & 1; }
+  // Sums of a tile that other blocks continue (which = 1), or that this one continues (0).
+  static __device__ __forceinline__ int part(int which, int t, int row) { return kJoin + ((which * kTokens + t) * kTensorRows + row) * 4; }
   static constexpr int kXBlock = kTokens * 128, kStageBytes = kCodeBytes + 4 * kXBlock;   // 64 elements of the tokens; codes and tokens of a unit
-  static constexpr int kStages = 200 * 1024 / kStageBytes, kJoin = kStages * kStageBytes, kBars = kJoin + kTokens * kTensorRows * 4;
+  static constexpr int kStages = 192 * 1024 / kStageBytes, kJoin = kStages * kStageBytes, kBars = kJoin + 2 * kTokens * kTensorRows * 4;
   static constexpr int kFull = kBars, kEmpty = kFull + 8 * kStages, kOperand = kEmpty + 8 * kStages, kOperandFree = kOperand + 8 * kOperands;
   static constexpr int kResult = kOperandFree + 8 * kOperands, kResultFree = kResult + 8 * kResults, kEnd = kResultFree + 8 * kResults;
-  static constexpr int kJoinReady = kEnd + 8, kJoinFree = kJoinReady + 8, kDead = kJoinFree + 8, kTmem = kDead + 4, kTotal = kTmem + 4 + 1024;   // (and the alignment of the swizzled tiles)
+  static constexpr int kDead = kEnd + 8, kTmem = kDead + 4, kTotal = kTmem + 4 + 1024;   // (and the alignment of the swizzled tiles)
 };
 
 // Eight codes, neighbours in the halves of a word.
@@ -68,43 +71,41 @@ template <> struct Neighbours<__half> {
   }
 };
 
-// Position in the sequence of (tile, unit) that every role of a block walks over: units first .. last - 1 of each tile.
+// Position in the block's share of the sequence of (tile, unit), over which every role walks.
 struct Units {
-  int tile, unit, first, last, tiles, step;
-  __device__ __forceinline__ bool more() const { return tile < tiles; }
+  int tile, unit, units, left;     // units of a tile; units left in the share
+  __device__ __forceinline__ bool more() const { return left > 0; }
   __device__ __forceinline__ void next() {
-    if (++unit == last) {
-      unit = first;
-      tile += step;
+    --left;
+    if (++unit == units) {
+      unit = 0;
+      ++tile;
     }
   }
 };
 
-// Blocks of a cluster: address of another block's shared memory, arrival there, a wait for arrivals from there.
+// Address of another block's shared memory in the cluster.
 __device__ __forceinline__ uint32_t in_block(uint32_t a, int rank) {
   uint32_t r;
   asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(rank));
   return r;
 }
-__device__ __forceinline__ void arrive_cluster(uint32_t bar) {
-  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" :: "r"(bar) : "memory");
-}
-__device__ __forceinline__ void wait_cluster(uint32_t bar, uint32_t parity, const W4Params& p, volatile int* dead) {
-  const long long t0 = clock64();
-  uint32_t ok = 0;
-  while (!*dead) {
-    asm volatile("{ .reg .pred p; mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2; selp.u32 %0, 1, 0, p; }"
-                 : "=r"(ok) : "r"(bar), "r"(parity) : "memory");
-    if (ok) return;
-    if (clock64() - t0 > p.spin_budget) {
-      *dead = 1;
-      raise_status(p.status, MDW_ERR_TIMEOUT);
-    }
-  }
-}
 __device__ __forceinline__ void sync_cluster() {
   asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
+
+// The tiles are divided among the clusters, and the (tile, unit) sequence of a cluster into equal contiguous shares of its
+// blocks: a tile cut between blocks is finished from their sums, in order, when all are done.
+struct Share {
+  int t0, units, all, blocks;      // cluster's first tile, units of a tile, units of the cluster
+  __device__ __forceinline__ Share(const W4Params& p, int blocks_) : blocks(blocks_) {
+    const int tiles = (p.N + kTensorRows - 1) / kTensorRows, clusters = gridDim.x / blocks, c = blockIdx.x / blocks;
+    units = (p.K + kUnit - 1) / kUnit;
+    t0 = (int)((int64_t)tiles * c / clusters);
+    all = ((int)((int64_t)tiles * (c + 1) / clusters) - t0) * units;
+  }
+  __device__ __forceinline__ int start(int rank) const { return (int)((int64_t)all * rank / blocks); }
+};
 
 // Scales or zeros of one unit (256 / kGroup of them) for one feature.
 template <int kGroup>
@@ -172,9 +173,18 @@ __device__ __forceinline__ void prefetch_scales(const W4Params& p, const Units& 
   if (p.zero) asm volatile("prefetch.global.L2 [%0];" :: "l"(p.zero + first));
 }
 
+// One rounding of a token's feature, after bias and residual.
+template <typename T>
+__device__ __forceinline__ void store(const W4Params& p, int t, int feature, float v) {
+  if (p.bias) v += Elem<T>::to_float(static_cast<const T*>(p.bias)[feature]);
+  if (p.residual) v += Elem<T>::to_float(static_cast<const T*>(p.residual)[t * p.ldr + feature]);
+  if (p.y_f32) static_cast<float*>(p.y)[t * p.ldy + feature] = v;
+  else static_cast<T*>(p.y)[t * p.ldy + feature] = Elem<T>::from_float(v);
+}
+
 template <typename T, int kGroup, int kTokens>
 __global__ void __launch_bounds__(kThreads, 1)
-w4_tensor_kernel(const W4Params p, const __grid_constant__ CUtensorMap codes, const __grid_constant__ CUtensorMap tokens, int split) {
+w4_tensor_kernel(const W4Params p, const __grid_constant__ CUtensorMap codes, const __grid_constant__ CUtensorMap tokens, int blocks) {
   using L = WideSmem<kGroup, kTokens>;
   extern __shared__ uint8_t raw_smem[];
   const uint32_t base = (smem_u32(raw_smem) + 1023) & ~1023u;
@@ -199,8 +209,6 @@ w4_tensor_kernel(const W4Params p, const __grid_constant__ CUtensorMap codes, co
       mbar_init(bar(L::kResultFree, i), 4);
     }
     mbar_init(bar(L::kEnd, 0), L::kIssuers);
-    mbar_init(bar(L::kJoinReady, 0), 4 * split);
-    mbar_init(bar(L::kJoinFree, 0), 4 * split);
     *dead = 0;
     mbar_init_fence();
   }
@@ -212,9 +220,9 @@ w4_tensor_kernel(const W4Params p, const __grid_constant__ CUtensorMap codes, co
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = __shfl_sync(0xffffffffu, *reinterpret_cast<volatile uint32_t*>(smem + L::kTmem), 0);
-  if (split > 1) sync_cluster();                                // the others' barriers are there
-  const int units = (p.K + kUnit - 1) / kUnit, rank = blockIdx.x % split, u0 = units * rank / split;
-  Units at{(int)blockIdx.x / split, u0, u0, units * (rank + 1) / split, (p.N + kTensorRows - 1) / kTensorRows, (int)gridDim.x / split};
+  const Share share(p, blocks);
+  const int rank = blockIdx.x % blocks, units = share.units, u0 = share.start(rank), u1 = share.start(rank + 1);
+  Units at{share.t0 + u0 / units, u0 % units, units, u1 - u0};
 
   if (warp == 0) {
     // ---- copies
@@ -323,7 +331,7 @@ w4_tensor_kernel(const W4Params p, const __grid_constant__ CUtensorMap codes, co
     float acc[kTokens];
 #pragma unroll
     for (int t = 0; t < kTokens; ++t) acc[t] = 0.f;
-    int round = 0;                                              // tiles joined
+    bool from_start = at.unit == 0;                             // of the tile
     for (int n = 0; at.more(); ++n) {
       const int feature = at.tile * kTensorRows + row, unit = at.unit;
       now = next;
@@ -363,54 +371,19 @@ w4_tensor_kernel(const W4Params p, const __grid_constant__ CUtensorMap codes, co
           }
         }
       }
-      if (unit + 1 < at.last) continue;
-      auto store = [&](int t, float v) {
-        if (p.bias) v += Elem<T>::to_float(static_cast<const T*>(p.bias)[feature]);
-        if (p.residual) v += Elem<T>::to_float(static_cast<const T*>(p.residual)[t * p.ldr + feature]);
-        if (p.y_f32) static_cast<float*>(p.y)[t * p.ldy + feature] = v;
-        else static_cast<T*>(p.y)[t * p.ldy + feature] = Elem<T>::from_float(v);
-      };
-      if (split == 1) {
+      if (unit + 1 < units && at.more()) continue;
+      if (unit + 1 == units && from_start) {
         if (feature < p.N && !*dead) {
 #pragma unroll
           for (int t = 0; t < kTokens; ++t)
-            if (t < p.M) store(t, acc[t]);
+            if (t < p.M) store<T>(p, t, feature, acc[t]);
         }
       } else {
-        // the blocks of a cluster have a part of K each: every one adds up some of the tokens, in the blocks' order
-        const uint32_t place = base + L::kJoin + row * 4;
-        wait_cluster(bar(L::kJoinFree, 0), (round & 1) ^ 1, p, dead);
 #pragma unroll
-        for (int t = 0; t < kTokens; ++t) asm volatile("st.shared.f32 [%0], %1;" :: "r"(place + t * (kTensorRows * 4)), "f"(acc[t]) : "memory");
-        __syncwarp();
-        if (lane < split && !*dead) arrive_cluster(in_block(bar(L::kJoinReady, 0), lane));
-        wait_cluster(bar(L::kJoinReady, 0), round & 1, p, dead);
-        __syncwarp();
-        if (!*dead) {
-          for (int t0 = rank; t0 < p.M; t0 += 2 * split) {
-            float part[2][kMostSplit];                          // requested together: each takes some 250 cycles
-#pragma unroll
-            for (int i = 0; i < 2; ++i)
-#pragma unroll
-              for (int r = 0; r < kMostSplit; ++r) {
-                part[i][r] = 0.f;
-                const int t = t0 + i * split;
-                if (r < split && t < p.M)
-                  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(part[i][r]) : "r"(in_block(place + t * (kTensorRows * 4), r)) : "memory");
-              }
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-              float v = 0.f;
-#pragma unroll
-              for (int r = 0; r < kMostSplit; ++r) v += part[i][r];
-              if (feature < p.N && t0 + i * split < p.M) store(t0 + i * split, v);
-            }
-          }
-        }
-        __syncwarp();
-        if (lane < split && !*dead) arrive_cluster(in_block(bar(L::kJoinFree, 0), lane));
-        ++round;
+        for (int t = 0; t < kTokens; ++t)
+          asm volatile("st.shared.f32 [%0], %1;" :: "r"(base + L::part(from_start, t, row)), "f"(acc[t]) : "memory");
       }
+      from_start = true;
 #pragma unroll
       for (int t = 0; t < kTokens; ++t) acc[t] = 0.f;
     }
@@ -421,10 +394,40 @@ w4_tensor_kernel(const W4Params p, const __grid_constant__ CUtensorMap codes, co
     tc_fence_after();
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" :: "r"(tmem) : "memory");
   }
-  if (split > 1) {
-    __syncthreads();
-    sync_cluster();                                             // no block ends while another reads its sums
+  if (blocks == 1) return;
+  sync_cluster();
+  // the first block whose share starts inside a tile finishes that tile
+  const int cut = u0 / units, begin = cut * units;
+  if (u0 > begin && share.start(rank - 1) <= begin) {
+    bool lost = false;                                          // a dead block anywhere in the cluster
+    for (int r = 0; r < blocks; ++r) {
+      uint32_t v;
+      asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(in_block(base + L::kDead, r)) : "memory");
+      lost |= v != 0;
+    }
+    int end = rank;                                             // blocks rank - 1 .. end have a part of it
+    while (end + 1 < blocks && share.start(end + 1) < begin + units) ++end;
+    const int row = (warp & 3) * 32 + lane, feature = (share.t0 + cut) * kTensorRows + row;
+    constexpr int kEach = kTokens / 4;                          // tokens of a thread
+    float sum[kEach];
+#pragma unroll
+    for (int i = 0; i < kEach; ++i)
+      asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(sum[i]) : "r"(in_block(base + L::part(1, (warp >> 2) + 4 * i, row), rank - 1)) : "memory");
+    for (int r = rank; r <= end; ++r) {
+      float v[kEach];
+#pragma unroll
+      for (int i = 0; i < kEach; ++i)
+        asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v[i]) : "r"(in_block(base + L::part(0, (warp >> 2) + 4 * i, row), r)) : "memory");
+#pragma unroll
+      for (int i = 0; i < kEach; ++i) sum[i] += v[i];
+    }
+    if (feature < p.N && !lost) {
+#pragma unroll
+      for (int i = 0; i < kEach; ++i)
+        if ((warp >> 2) + 4 * i < p.M) store<T>(p, (warp >> 2) + 4 * i, feature, sum[i]);
+    }
   }
+  sync_cluster();                                               // no block ends while another reads its sums
 }
 
 // The tokens as [M][K] elements; a box is 64 elements of all of them, those that are missing zeros.
@@ -436,17 +439,19 @@ bool encode_tokens(CUtensorMap* map, const W4Params& p, int tokens) {
                   CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_128B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// Clusters of `split` blocks that a device runs at once, asked once.
+constexpr int kJoinUnits = 2;
+
+// Clusters of `blocks` blocks that a device runs at once, asked once.
 template <auto kKernel>
-int clusters(const cudaLaunchConfig_t& cfg, int split, int dev) {
-  static std::atomic<int> known[kMaxDevices][kMostSplit + 1];
-  int n = known[dev][split].load(std::memory_order_relaxed);
+int clusters(const cudaLaunchConfig_t& cfg, int blocks, int dev) {
+  static std::atomic<int> known[kMaxDevices][kMostCluster + 1];
+  int n = known[dev][blocks].load(std::memory_order_relaxed);
   if (n == 0) {
     if (cudaOccupancyMaxActiveClusters(&n, kKernel, &cfg) != cudaSuccess || n < 1) {
       cudaGetLastError();
       n = -1;
     }
-    known[dev][split].store(n, std::memory_order_relaxed);
+    known[dev][blocks].store(n, std::memory_order_relaxed);
   }
   return n;
 }
@@ -468,24 +473,23 @@ cudaError_t launch(const W4Params& p, const CUtensorMap& codes, int dev, cudaStr
   a.val.clusterDim.y = a.val.clusterDim.z = 1;
   cfg.attrs = &a;
   cfg.numAttrs = 1;
-  // Blocks to a tile, each with a part of K: the fewest units that a block goes through one after the other, a join counted
-  // as kJoinUnits of them.
-  int split = 1, many = sm_count(dev), best = (tiles + many - 1) / many * units;
-  for (int n = 2; n <= kMostSplit && n <= units; ++n) {
+  // Blocks to a cluster: the fewest units in a block's share, a join counted as kJoinUnits of them.
+  int blocks = 1, many = std::min(sm_count(dev), tiles), best = (tiles + many - 1) / many * units;
+  for (int n = 2; n <= kMostCluster && n <= units; ++n) {
     a.val.clusterDim.x = n;
     cfg.gridDim = dim3((unsigned)n);
-    const int fit = clusters<kKernel>(cfg, n, dev);
+    const int fit = std::min(clusters<kKernel>(cfg, n, dev), tiles);
     if (fit < 1) continue;
-    const int cost = (tiles + fit - 1) / fit * ((units + n - 1) / n + kJoinUnits);
+    const int cost = ((tiles + fit - 1) / fit * units + n - 1) / n + kJoinUnits;
     if (cost < best) {
       best = cost;
-      split = n;
+      blocks = n;
       many = fit;
     }
   }
-  a.val.clusterDim.x = split;
-  cfg.gridDim = dim3((unsigned)(split * (tiles < many ? tiles : many)));
-  return cudaLaunchKernelEx(&cfg, kKernel, p, codes, tokens, split);
+  a.val.clusterDim.x = blocks;
+  cfg.gridDim = dim3((unsigned)(blocks * many));
+  return cudaLaunchKernelEx(&cfg, kKernel, p, codes, tokens, blocks);
 }
 template <typename T, int kGroup>
 cudaError_t launch(const W4Params& p, const CUtensorMap& codes, int dev, cudaStream_t s) {
