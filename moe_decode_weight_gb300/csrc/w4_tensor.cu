@@ -396,35 +396,47 @@ w4_tensor_kernel(const W4Params p, const __grid_constant__ CUtensorMap codes, co
   }
   if (blocks == 1) return;
   sync_cluster();
-  // the first block whose share starts inside a tile finishes that tile
-  const int cut = u0 / units, begin = cut * units;
-  if (u0 > begin && share.start(rank - 1) <= begin) {
-    bool lost = false;                                          // a dead block anywhere in the cluster
-    for (int r = 0; r < blocks; ++r) {
-      uint32_t v;
-      asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(in_block(base + L::kDead, r)) : "memory");
-      lost |= v != 0;
-    }
-    int end = rank;                                             // blocks rank - 1 .. end have a part of it
-    while (end + 1 < blocks && share.start(end + 1) < begin + units) ++end;
-    const int row = (warp & 3) * 32 + lane, feature = (share.t0 + cut) * kTensorRows + row;
-    constexpr int kEach = kTokens / 4;                          // tokens of a thread
-    float sum[kEach];
+  bool lost = false;                                            // a dead block anywhere in the cluster
+  for (int r = 0; r < blocks; ++r) {
+    uint32_t v;
+    asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(in_block(base + L::kDead, r)) : "memory");
+    lost |= v != 0;
+  }
+  // Tiles that this share starts inside of or ends inside of. Of up to three blocks with parts of one the second adds
+  // them up; of more each adds up some of the tokens.
+  const int row = (warp & 3) * 32 + lane;
+  auto part = [&](int rank, int which, int t) {
+    float v;
+    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(in_block(base + L::part(which, t, row), rank)) : "memory");
+    return v;
+  };
+#pragma unroll 1
+  for (int which = 0; which < 2; ++which) {
+    const int u = which ? u1 : u0, tile = u / units, begin = tile * units, feature = (share.t0 + tile) * kTensorRows + row;
+    if (u == begin || (which == 1 && u0 > begin)) continue;
+    int first = rank, end = rank;                               // blocks with a part of it
+    while (share.start(first) > begin) --first;
+    while (share.start(end + 1) < begin + units) ++end;
+    const int n = end - first + 1;
+    if (n <= 3) {
+      if (rank != first + 1) continue;
+      float v[3][kTokens / 4];                                  // requested together: each takes some 250 cycles
 #pragma unroll
-    for (int i = 0; i < kEach; ++i)
-      asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(sum[i]) : "r"(in_block(base + L::part(1, (warp >> 2) + 4 * i, row), rank - 1)) : "memory");
-    for (int r = rank; r <= end; ++r) {
-      float v[kEach];
+      for (int i = 0; i < 3; ++i)
 #pragma unroll
-      for (int i = 0; i < kEach; ++i)
-        asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v[i]) : "r"(in_block(base + L::part(0, (warp >> 2) + 4 * i, row), r)) : "memory");
+        for (int j = 0; j < kTokens / 4; ++j) v[i][j] = i < n ? part(first + i, i == 0, (warp >> 2) + 4 * j) : 0.f;
 #pragma unroll
-      for (int i = 0; i < kEach; ++i) sum[i] += v[i];
-    }
-    if (feature < p.N && !lost) {
+      for (int j = 0; j < kTokens / 4; ++j)
+        if (feature < p.N && (warp >> 2) + 4 * j < p.M && !lost) store<T>(p, (warp >> 2) + 4 * j, feature, v[0][j] + v[1][j] + v[2][j]);
+    } else {
+      for (int t = rank - first + n * (warp >> 2); t < p.M; t += 4 * n) {
+        float v[kMostCluster], sum = 0.f;
 #pragma unroll
-      for (int i = 0; i < kEach; ++i)
-        if ((warp >> 2) + 4 * i < p.M) store<T>(p, (warp >> 2) + 4 * i, feature, sum[i]);
+        for (int i = 0; i < kMostCluster; ++i) v[i] = i < n ? part(first + i, i == 0, t) : 0.f;
+#pragma unroll
+        for (int i = 0; i < kMostCluster; ++i) sum += v[i];
+        if (feature < p.N && !lost) store<T>(p, t, feature, sum);
+      }
     }
   }
   sync_cluster();                                               // no block ends while another reads its sums
@@ -439,7 +451,7 @@ bool encode_tokens(CUtensorMap* map, const W4Params& p, int tokens) {
                   CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_128B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-constexpr int kJoinUnits = 2;
+constexpr int kJoinUnits = 4;
 
 // Clusters of `blocks` blocks that a device runs at once, asked once.
 template <auto kKernel>
