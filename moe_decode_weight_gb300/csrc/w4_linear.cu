@@ -7,11 +7,11 @@
 //
 // Codes. A lane (g, q) of a product holds two features and a quarter of a group's codes (8, 16 or 32 of them, one
 // load), so the four lanes of a product always share a group. Masking a word by 0x000f000f leaves codes
-// j and j + 4 in its halves, under the exponent of 128 (bf16) or 1024 (f16) that is code + 128 or + 1024
-// exactly; subtracting 128 + zero or 1024 + zero leaves code - zero. The token's elements are put in the
-// same order once, when they enter shared memory. This expansion bounds the kernels beside the codes'
-// stream: 11 (bf16) or 9 (f16) operations for eight codes of a feature, whatever the number of tokens, of
-// which 7 or 5 on the integer pipe.
+// j and j + 4 in its halves, by 0x00f000f0 codes j + 1 and j + 5, times 16. Under the exponent of 1024 that is a
+// f16 number, and as it is a bf16 one (see Int4); one more operation, exact, leaves code - zero. The
+// token's elements are put in the same order once, when they enter shared memory. This expansion
+// bounds the kernel beside the codes' stream: 9 operations for eight codes of a feature, whatever the number
+// of tokens, of which 5 on the integer pipe (157184 features x 2560, one token: 43.5 us, 4.8 TB/s).
 #include <type_traits>
 
 #include "mdw_internal.h"
@@ -109,7 +109,7 @@ struct Scales {
     const unsigned short v = (unsigned short)(s[i][j / 2] >> (16 * (j & 1)));
     T t;
     memcpy(&t, &v, 2);
-    return Elem<T>::to_float(t);
+    return Int4<T>::kFactor * Elem<T>::to_float(t);
   }
   __device__ __forceinline__ uint32_t zero2(int i, int j) const {
     return Int4<T>::zero2((z[i][j / 4] >> (8 * (j & 3))) & 0xffu);

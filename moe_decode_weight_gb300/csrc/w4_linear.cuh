@@ -31,16 +31,23 @@ __device__ __forceinline__ uint32_t and_or(uint32_t v, uint32_t mask, uint32_t b
 
 template <typename T> struct Int4;
 template <> struct Int4<__nv_bfloat16> {
-  // z2: 128 + zero in both halves
-  static __device__ __forceinline__ uint32_t zero2(uint32_t z) { return (0x4300u + z) * 0x00010001u; }
-  static __device__ __forceinline__ uint32_t sub(uint32_t v, uint32_t z2) {
+  // The numbers up to 255 * 2^-133, subnormal and the first normal ones, are the integers times 2^-133: a code in the low
+  // nibble of a half is one, a code in the next nibble 16 times one. A product with 2^127 (2^123), with the zero
+  // taken out by the same operation, makes them (code - zero) * 2^-6 exactly; kFactor goes into the scale.
+  static constexpr float kFactor = 64.f;
+  static __device__ __forceinline__ uint32_t fma2(uint32_t a, uint32_t b, uint32_t c) {
     uint32_t r;
-    asm("sub.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(v), "r"(z2));
+    asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(r) : "r"(a), "r"(b), "r"(c));
     return r;
   }
+  static __device__ __forceinline__ uint32_t zero2(uint32_t z) { return fma2(z * 0x00010001u, 0xff00ff00u, 0u); }   // -zero * 2^-6
   static __device__ __forceinline__ void expand(uint32_t w, uint32_t z2, uint32_t (&p)[4]) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) p[i] = sub(and_or(w >> (4 * i), 0x000f000fu, 0x43004300u), z2);
+    for (int i = 0; i < 2; ++i) {
+      const uint32_t v = w >> (8 * i);
+      p[2 * i] = fma2(v & 0x000f000fu, 0x7f007f00u, z2);
+      p[2 * i + 1] = fma2(v & 0x00f000f0u, 0x7d007d00u, z2);
+    }
   }
   static __device__ __forceinline__ void mma(float (&d)[4], const float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
     asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%11,%12,%13};"
@@ -49,6 +56,7 @@ template <> struct Int4<__nv_bfloat16> {
   }
 };
 template <> struct Int4<__half> {
+  static constexpr float kFactor = 1.f;
   // low half: 1024 + zero; the odd codes stay in their upper nibble as 1024 + 16 code and are brought
   // down by one exact multiply-add: (1024 + 16 code) / 16 - (64 + zero)
   static __device__ __forceinline__ uint32_t zero2(uint32_t z) { return (0x6400u + z) * 0x00010001u; }
