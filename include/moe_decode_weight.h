@@ -363,7 +363,7 @@ mdw_status lm_head_fp8_sample(const mdw_lm_head* head, int32_t M, const void* h_
 typedef struct mdw_w4_weights {
   uint32_t magic;
   int32_t fmt;
-  int32_t n;             /* output features, >= 1 */
+  int32_t n;             /* output features, 1 .. 2^31 - 256 */
   int32_t k;             /* input features, a multiple of group */
   int32_t group;         /* 32, 64 or 128 */
   int32_t dtype;         /* MDW_DT_BF16 or MDW_DT_F16: scale, x, bias and residual */
@@ -375,7 +375,8 @@ typedef struct mdw_w4_weights {
 
 /* y[t][n] = sum_k x[t][k] * (code[n][k] - zero[n][k/group]) * scale[n][k/group]
  *           (+ bias[n]) (+ residual[t][n])    for a window of 1 <= M <= MDW_MAX_M tokens.
- * Products are exact, sums in fp32 in a fixed order (bit-reproducible), rounded once to y's type.
+ * Products are exact (bf16: of elements from 2^-100 on, with scales below 2^121), sums in fp32 in
+ * a fixed order (bit-reproducible), rounded once to y's type.
  * x [M][k] (ldx), y [M][n] (ldy) in w->dtype or MDW_DT_F32, bias [n], residual [M][n] (ldr) in
  * w->dtype. y, bias and residual need the alignment of their elements only. y may be the
  * residual itself (same pointer, type and stride); it must not overlap any other argument. */

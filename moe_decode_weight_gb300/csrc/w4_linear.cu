@@ -370,7 +370,7 @@ extern "C" mdw_status w4_linear(const mdw_w4_weights* w, int32_t M, const void* 
   if (w->magic != MDW_MAGIC || w->fmt != MDW_FMT_INT4_GROUP) return MDW_ERR_FORMAT_MISMATCH;
   if (w->dtype != MDW_DT_BF16 && w->dtype != MDW_DT_F16) return MDW_ERR_FORMAT_MISMATCH;
   if (w->group != 32 && w->group != 64 && w->group != 128) return MDW_ERR_UNSUPPORTED_SHAPE;
-  if (w->n < 1 || w->k < w->group || w->k % w->group != 0) return MDW_ERR_UNSUPPORTED_SHAPE;
+  if (w->n < 1 || w->n > 0x7fffff00 || w->k < w->group || w->k % w->group != 0) return MDW_ERR_UNSUPPORTED_SHAPE;   // (rows of a tile past n are int32)
   if (M < 1 || M > MDW_MAX_M) return MDW_ERR_INVALID_ARG;
   if (!aligned_to(w->q, 16) || !aligned_to(w->scale, 16) || !null_or_aligned(w->zero, 16) || !aligned_to(x, 16) || !row_stride_ok(ldx, w->k))
     return MDW_ERR_INVALID_ARG;

@@ -102,3 +102,8 @@ def test_binding_refuses_host_tensors():
         api.KVCache(torch.zeros((1, 1, 16, 64)), torch.zeros((1, 1, 16, 64)))
     with pytest.raises(api.MdwError):
         api.mdw_kv_plan(*(torch.zeros(1, dtype=torch.int32),) * 2, 16, 1, *(torch.zeros((1, 1), dtype=torch.int32),) * 6)
+
+
+@pytest.mark.parametrize("n", [(1 << 31) - 255, (1 << 31) - 1])
+def test_w4_rejects_features_whose_tiles_pass_int32(n):
+    assert api.lib().w4_linear(_w4(n=n, k=128), 1, FAKE, 128, FAKE, n, BF, None, None, 0, None, None) == 2

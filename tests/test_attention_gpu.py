@@ -750,3 +750,180 @@ def test_w4_linear_many_features(m, n, k, group, zero, dtype, ydtype):
     again = torch.empty_like(y[:m])
     api.w4_linear(w, x, again, bias=bias, residual=res)
     assert torch.equal(again, y[:m])
+
+
+# ---- every kernel of mdw_tree_attention: up to 16 rows a request and kv head, up to 32, more
+PATHS = [(8, BF, BF, 128), (8, BF, E4, 128), (8, HF, HF, 64), (8, HF, E4, 64), (16, BF, BF, 128), (16, BF, E4, 128), (16, HF, HF, 64),
+         (16, HF, E4, 64), (64, BF, BF, 128), (64, BF, E4, 128), (64, HF, HF, 64), (64, HF, E4, 64)]   # query heads over 2 kv heads
+
+
+@pytest.mark.parametrize("hq,dtype,ctype,d", PATHS)
+def test_attention_bad_pages_on_every_path(hq, dtype, ctype, d):
+    c = Attn(30, [400, 40, 16], [4, 3, 1], hq, 2, d, 16, dtype, ctype)
+    table = c.table.copy()
+    table[0, 2], table[0, 6], table[0, 20], table[1, 0] = 1 << 30, -3, -1, c.cache.k.shape[0]
+    status = i32([0])
+    out, lse = c.call(table=table, status=status)
+    assert status.item() == 7
+    hide = [np.zeros(404, bool), np.zeros(43, bool), np.zeros(17, bool)]
+    hide[0][32:48], hide[0][96:112], hide[0][320:336], hide[1][:16] = True, True, True, True
+    c.check(out, lse, hide=hide)
+
+
+@pytest.mark.parametrize("hq,dtype,ctype,d", PATHS)
+def test_attention_bad_lengths_and_empty_requests_on_every_path(hq, dtype, ctype, d):
+    c = Attn(31, [30, 40, 50, 0, 300], [2, 4, 2, 0, 1], hq, 2, d, 32, dtype, ctype, pad=3)
+    for ctx, bad in (([30, -1, 50, 0, 300], [1]), ([30, 40, 2147483647, 0, 300], [2]), ([2000, 40, 50, 0, 300], [0])):
+        status = i32([0])
+        out, lse = c.call(ctx=ctx, status=status)
+        assert status.item() == 7
+        c.check(out, lse, requests=[b for b in range(5) if b not in bad])
+        for b in bad:
+            rows = slice(int(c.start[b]), int(c.start[b + 1]))
+            assert (out[rows] == 5).all() and (lse[rows] == 5).all()
+        assert (out[9:] == 5).all() and (lse[9:] == 5).all()
+
+
+@pytest.mark.parametrize("hq,dtype,ctype,d", PATHS)
+def test_attention_nothing_seen_on_every_path(hq, dtype, ctype, d):
+    c = Attn(32, [0, 0, 40], [4, 1, 2], hq, 2, d, 16, dtype, ctype)
+    for s in c.seen[:2]:
+        s[:] = False
+    c.mask[:5] = 0
+    out, lse = c.call()
+    assert not out[:5].any() and (lse[:5] == -float("inf")).all()
+    c.check(out, lse, requests=[2])
+
+
+@pytest.mark.parametrize("page", [16, 64])
+@pytest.mark.parametrize("hq,dtype,ctype,d", [(2, BF, BF, 128), (2, HF, E4, 128), (2, HF, HF, 64), (2, BF, E4, 64), (8, BF, BF, 128), (8, HF, E4, 128),
+                                              (8, HF, HF, 64), (8, BF, E4, 64), (32, BF, BF, 128), (32, HF, E4, 64)])
+def test_attention_ignores_what_masked_keys_hold_on_every_path(hq, dtype, ctype, d, page):
+    """NaN and infinities behind the sequence, in spare pages and in nodes that a row does not see; rows that see
+    NaN values are NaN there."""
+    ctx, new = [70, 0, 1029], [8, 7, 8]
+    c = Attn(33, ctx, new, hq, 2, d, page, dtype, ctype, masks="random", spare=4)
+    for s in c.seen:
+        s[0], s[1], s[2] = False, False, False
+        s[0, 0], s[2, 3] = True, True
+    bits = [sum(1 << int(j) for j in np.nonzero(r)[0]) for s in c.seen for r in s]
+    c.mask = torch.tensor(np.array(bits, np.uint64).view(np.int64), device="cuda")
+    clean = [c.keys(b) for b in range(3)]
+    raw = torch.uint8 if ctype == E4 else torch.int16
+    nan, inf = (127, 255) if ctype == E4 else (0x7FC0, 0x7F80) if dtype == BF else (0x7E00, 0x7C00)
+
+    def spoil(page_id, off, node):
+        c.cache.v.view(raw)[page_id, :, off, ::3] = nan if node == 3 else inf
+        if node != 3:
+            c.cache.k.view(raw)[page_id, :, off, 1::5] = nan
+
+    used = set(c.table[c.table >= 0].tolist())
+    for b in range(3):
+        for node in (3, 5):
+            key = ctx[b] + node
+            spoil(int(c.table[b, key // page]), key % page, node)
+        n = ctx[b] + new[b]
+        for off in range(n % page, page if n % page else 0):
+            spoil(int(c.table[b, n // page]), off, 5)
+    for page_id in set(range(c.cache.k.shape[0])) - used:
+        for off in range(page):
+            spoil(page_id, off, 5)
+    out, lse = c.call()
+    for b in range(3):
+        keep = np.nonzero(~(c.seen[b][:, 3] | c.seen[b][:, 5]))[0]
+        assert {0, 1} <= set(keep.tolist())
+        rows = torch.tensor(keep + c.start[b], device="cuda")
+        sub = Attn.__new__(Attn)
+        seen = np.concatenate([np.ones((len(keep), ctx[b]), bool), c.seen[b][keep]], 1)
+        sub.__dict__.update(c.__dict__, ctx=np.array([0]), new=np.array([len(keep)]), start=np.array([0, len(keep)]), q=c.q[rows], seen=[seen])
+        sub.check(out[rows], lse[rows], k_v=lambda _: clean[b])
+        row = out[int(c.start[b]) + 2].float()
+        assert torch.isnan(row[:, ::3]).all() and torch.isfinite(row[:, 1::3]).all()
+
+
+def test_calls_on_two_streams_do_not_disturb_each_other():
+    cs = [Attn(34 + i, [900, 40], [4, 2], 16 * (1 + 3 * i), 4, 128, 16, BF, BF) for i in range(2)]
+    ws = [w4_case(40 + i, 2000, 2560, 64, True, BF) for i in range(2)]
+    xs = [torch.randn((3 + 20 * i, 2560), generator=gen(i), device="cuda").to(BF) for i in range(2)]
+    want = [c.call()[0] for c in cs]
+    ys = [torch.empty((x.shape[0], 2000), dtype=BF, device="cuda") for x in xs]
+    for w, x, y in zip(ws, xs, ys):
+        api.w4_linear(w, x, y)
+    got = [[torch.empty_like(y) for _ in range(8)] for y in ys]
+    outs = [[torch.empty_like(c.q) for _ in range(8)] for c in cs]
+    space = [torch.empty(api.mdw_tree_attention_workspace_bytes(c.cache, 2, c.t, c.q.shape[1], 4), dtype=torch.uint8, device="cuda") for c in cs]
+    fixed = [(i32(c.table), i32(c.ctx), i32(c.start)) for c in cs]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    for k in range(8):
+        for i, (c, s) in enumerate(zip(cs, streams)):
+            api.w4_linear(ws[i], xs[i], got[i][k], stream=s)
+            api.mdw_tree_attention(c.cache, c.q, outs[i][k], *fixed[i], 4, space[i], tree_mask=c.mask, scale=c.scale, stream=s)
+    torch.cuda.synchronize()
+    for i in range(2):
+        assert all(torch.equal(g, ys[i]) for g in got[i]) and all(torch.equal(o, want[i]) for o in outs[i])
+
+
+def test_w4_linear_wait_that_runs_out_is_reported():
+    w = w4_case(50, 3000, 5120, 64, False, BF)
+    x = torch.randn((20, 5120), generator=gen(0), device="cuda").to(BF)
+    y, status = torch.empty((20, 3000), dtype=BF, device="cuda"), i32([0])
+    api.mdw_debug_set_spin_budget(1)
+    try:
+        api.w4_linear(w, x, y, status=status)
+        assert status.item() == 6
+    finally:
+        api.mdw_debug_set_spin_budget(0)
+    status = i32([0])
+    api.w4_linear(w, x, y, status=status)
+    want, tol = w4_want(w, x)
+    assert status.item() == 0
+    assert_close(host(y), want, tol + half_step(BF) * np.abs(want))
+
+
+FIRST_CALLS_CAPTURED = """
+import sys; sys.path[:0] = [{root!r}, {tests!r}]
+import torch
+import test_attention_gpu as t
+from moe_decode_weight_gb300 import api
+c = [t.Attn(60 + i, [300, 20], [4, 2], hq, 2, 64, 16, t.HF, t.HF) for i, hq in enumerate((4, 16, 64))]
+w = t.w4_case(61, 900, 640, 64, True, t.HF)
+x = [torch.randn((m, 640), device="cuda").half() for m in (2, 12, 25)]
+y = [torch.zeros((v.shape[0], 900), dtype=torch.half, device="cuda") for v in x]
+out = [torch.zeros_like(v.q) for v in c]
+args = [(t.i32(v.table), t.i32(v.ctx), t.i32(v.start)) for v in c]
+ws = [torch.empty(api.mdw_tree_attention_workspace_bytes(v.cache, 2, v.t, v.q.shape[1], 4), dtype=torch.uint8, device="cuda") for v in c]
+slot = torch.arange(6, device="cuda")
+ctx, new, free, table = t.i32([3, 20]), t.i32([2, 4]), t.i32([5, 6, 7]), t.i32([[1, -1, -1], [2, 3, -1]])
+start, slots, pos, taken = t.i32([0] * 3), torch.zeros(6, dtype=torch.int64, device="cuda"), t.i32([0] * 6), t.i32([0])
+keys = torch.randn((6, 2, 64), device="cuda").half()
+torch.cuda.synchronize()
+g = torch.cuda.CUDAGraph()
+with torch.cuda.graph(g):
+    api.mdw_kv_plan(ctx, new, 16, 8, table, free, start, slots, pos, taken)
+    api.mdw_kv_write(c[0].cache, keys, keys, slot)
+    for a, b in zip(x, y):
+        api.w4_linear(w, a, b)
+    for v, o, a, s in zip(c, out, args, ws):
+        api.mdw_tree_attention(v.cache, v.q, o, *a, 4, s, tree_mask=v.mask, scale=v.scale)
+g.replay()
+g.replay()
+torch.cuda.synchronize()
+assert slots.tolist() == [19, 20, 52, 53, 54, 55] and start.tolist() == [0, 2, 6], (slots, start)
+for a, b in zip(x, y):
+    want, tol = t.w4_want(w, a)
+    t.assert_close(t.host(b), want, tol + t.half_step(t.HF) * abs(want))
+for v, o in zip(c, out):
+    v.check(o, None)
+print("ok")
+"""
+
+
+def test_first_calls_of_a_process_can_be_captured():
+    import os
+    import subprocess
+    import sys
+    here = os.path.dirname(os.path.abspath(__file__))
+    code = FIRST_CALLS_CAPTURED.format(root=os.path.dirname(here), tests=here)
+    r = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0 and r.stdout.strip().endswith("ok"), r.stderr[-2000:]
