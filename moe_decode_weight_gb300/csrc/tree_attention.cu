@@ -20,7 +20,11 @@
 // two streams with scores, output, maximum and sum of their own, so that one stream's exponentials run
 // while the tensor cores work for the other.
 //
-// What bounds it is the stream of keys and values: 152 SMs need about 128 KB each in flight to draw the
+// Requests of up to 32 rows a kv head have a kernel of their own (tree_attention_rows.cu; few_rows() below chooses).
+//
+// What bounds it is the stream of keys and values up to 64 rows a block (16 ragged trees of up to 16 nodes x 4 heads, 12k
+// keys: 84 us, 4.9 TB/s), and the exponentials above (64-node trees of 8 heads: 56 us; a tile of 128 rows
+// takes a stream 6,100 cycles, 4,300 of them exponentials). 152 SMs need about 128 KB each in flight to draw the
 // memory's full rate (a copy alone, with nothing done to the tiles, reaches 7.1 TB/s so, 16-token
 // pages in random order). Keys and values therefore share one ring in the order in which the products
 // free them (K0 K1 V0 K2 V1 K3 ...), and a tile is held only while its product runs. The roles of a block:
