@@ -378,9 +378,19 @@ def _on_device(fn, device, *args):
             fn(*args)
 
 
+def _packed_rows(shape, stride) -> bool:
+    """Whether a tensor is contiguous from its second dimension on."""
+    width = 1
+    for n, step in zip(reversed(shape[1:]), reversed(stride[1:])):
+        if n != 1 and step != width:
+            return False
+        width *= n
+    return True
+
+
 def _address(fn: str, t: torch.Tensor, name: str, dtypes, device, shape=None) -> int:
     """Address of a handle's tensor, contiguous from its second dimension on."""
-    if not t.is_cuda or t.device != device or (shape is not None and t.shape != shape) or not (t.numel() == 0 or t[0].is_contiguous()):
+    if not t.is_cuda or t.device != device or (shape is not None and t.shape != shape) or not _packed_rows(t.shape, t.stride()):
         raise MdwError(fn, 1, f"{name}: {tuple(t.shape)} on {t.device}, strides {t.stride()}; wanted {shape or 'its'} shape on {device}")
     if t.dtype not in dtypes:
         raise MdwError(fn, 3, f"{name} has type {t.dtype}")
@@ -442,7 +452,7 @@ class KVCache:
         fp8 = k.dtype in _E4M3
         pk = _address(fn, k, "k", _E4M3 if fp8 else (torch.bfloat16, torch.float16), k.device)
         pv = _address(fn, v, "v", (k.dtype,), k.device, k.shape)
-        strides = {t.stride(0) for t in (k, v)} if k.shape[0] > 1 else {k[0].numel()}
+        strides = {k.stride(0), v.stride(0)} if k.shape[0] > 1 else {k.shape[1] * k.shape[2] * k.shape[3]}
         if len(strides) > 1:
             raise MdwError(fn, 1, f"k and v have page strides {strides}")
         if fp8 != (self.k_scale is not None) or fp8 != (self.v_scale is not None):
@@ -479,6 +489,8 @@ def mdw_kv_write(cache: KVCache, k: torch.Tensor, v: torch.Tensor, slot_map: tor
 
 
 def mdw_tree_attention_workspace_bytes(cache: KVCache, b: int, t: int, q_heads: int, max_new: int) -> int:
+    if cache.k.get_device() == torch.cuda.current_device():
+        return lib().mdw_tree_attention_workspace_bytes(cache.c, b, t, q_heads, max_new)
     with torch.cuda.device(cache.k.device):
         return lib().mdw_tree_attention_workspace_bytes(cache.c, b, t, q_heads, max_new)
 
