@@ -23,8 +23,8 @@
 // Requests of up to 32 rows a kv head have a kernel of their own (tree_attention_rows.cu; few_rows() below chooses).
 //
 // What bounds it is the stream of keys and values up to 64 rows a block (16 ragged trees of up to 16 nodes x 4 heads, 12k
-// keys: 84 us, 4.9 TB/s), and the exponentials above (64-node trees of 8 heads: 56 us; a tile of 128 rows
-// takes a stream 6,100 cycles, 4,300 of them exponentials). 152 SMs need about 128 KB each in flight to draw the
+// keys: 84 us, 4.9 TB/s), and the exponentials above (64-node trees of 8 heads: 50 us; a tile of 128 rows
+// takes a stream some 5,000 cycles, most of them exponentials). 152 SMs need about 128 KB each in flight to draw the
 // memory's full rate (a copy alone, with nothing done to the tiles, reaches 7.1 TB/s so, 16-token
 // pages in random order). Keys and values therefore share one ring in the order in which the products
 // free them (K0 K1 V0 K2 V1 K3 ...), and a tile is held only while its product runs. The roles of a block:
@@ -123,40 +123,33 @@ struct Lane {
   bool valid;
 };
 
-// Exponentials of one tile for a lane: kCols keys from key0 on (the share of the lane's copy). The tile holds keys
+// Exponentials of one tile for a lane: `cols` keys from key0 on (the share of the lane's copy). The tile holds keys
 // that not every row sees unless `all`. Scores lie in the columns from `scores` on, probabilities go to `probs`
-// (two to a column), the output so far is in `out`.
-template <typename T, bool kE4M3, int D, int kCols>
-__device__ __forceinline__ void exponentials(const AttnParams& p, Lane& w, uint32_t scores, uint32_t probs, uint32_t out, int key0,
+// (two to a column), the output so far is in `out`. 32 keys at a time, in loops that stay rolled: the warps of the two
+// streams are at different places of this code, and unrolled over the tile it did not stay in the instruction cache
+// (64-node trees 56 us instead of 50).
+template <typename T, bool kE4M3, int D>
+__device__ __forceinline__ void exponentials(const AttnParams& p, Lane& w, uint32_t scores, uint32_t probs, uint32_t out, int key0, int cols,
                                              int tile_key, const Request& r, int b, int h, bool all, uint32_t bad, const uint32_t* odd) {
   using S = Shape<T, kE4M3, D>;
   using M = Mma<typename S::C>;
-  constexpr int kHeld = kCols < 64 || kE4M3 ? 32 : 64;         // scores held in registers at a time
-  float v[kHeld / 32][32];
-  uint32_t see[kCols / 32];
-#pragma unroll
-  for (int j = 0; j < kCols / 32; ++j) {
-    see[j] = ~0u;
-    if (!all) see[j] = visible32(w.bits, tile_key + key0 + 32 * j, r.ctx) & on_pages32(bad, key0 + 32 * j, p.page_shift);
-  }
+  float v[32];
+  uint32_t see = ~0u;
   auto load = [&](int at) {
-#pragma unroll
-    for (int j = 0; j < kHeld / 32; ++j) tc_ld32(v[j], scores + key0 + at + 32 * j);
+    tc_ld32(v, scores + key0 + at);
     tc_wait_ld();
-    if (!all)
+    if (!all) {
+      see = visible32(w.bits, tile_key + key0 + at, r.ctx) & on_pages32(bad, key0 + at, p.page_shift);
 #pragma unroll
-      for (int j = 0; j < kHeld / 32; ++j)
-#pragma unroll
-        for (int e = 0; e < 32; ++e) v[j][e] = see[at / 32 + j] >> e & 1 ? v[j][e] : -INFINITY;
+      for (int e = 0; e < 32; ++e) v[e] = see >> e & 1 ? v[e] : -INFINITY;
+    }
   };
   float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll
-  for (int at = kCols - kHeld; at >= 0; at -= kHeld) {          // the first part is held when the maximum is known
+#pragma unroll 1
+  for (int at = cols - 32; at >= 0; at -= 32) {                // the first part is held when the maximum is known
     load(at);
 #pragma unroll
-    for (int j = 0; j < kHeld / 32; ++j)
-#pragma unroll
-      for (int e = 0; e < 32; ++e) top[e & 3] = fmaxf(top[e & 3], v[j][e]);
+    for (int e = 0; e < 32; ++e) top[e & 3] = fmaxf(top[e & 3], v[e]);
   }
   const float most = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
   const float now = most == -INFINITY ? -INFINITY : fmaf(most, w.c, -M::kShift);
@@ -178,56 +171,53 @@ __device__ __forceinline__ void exponentials(const AttnParams& p, Lane& w, uint3
     if (grown) w.mc = now;
   }
   const float from = w.mc == -INFINITY ? 0.f : w.mc;
-#pragma unroll
-  for (int at = 0; at < kCols; at += kHeld) {
-    if (at > 0) load(at);
-#pragma unroll
-    for (int j = 0; j < kHeld / 32; ++j) {
-      float sum[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-      for (int e = 0; e < 32; ++e) {
-        v[j][e] = exp2_fast(fmaf(v[j][e], w.c, -from));
-        sum[e & 3] += v[j][e];
-      }
-      w.l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
-      uint32_t packed[16];
-#pragma unroll
-      for (int e = 0; e < 16; ++e) packed[e] = M::pack(v[j][2 * e], v[j][2 * e + 1]);
-      tc_st16(probs + (key0 + at + 32 * j) / 2, packed);
-      if (!all) {
-        // rare: keys with values that are NaN or infinite; the rows that see one add them themselves
-        for (uint32_t left = odd[(key0 + at) / 32 + j]; left; left &= left - 1) {
-          const int k = __ffs(left) - 1, key = tile_key + key0 + at + 32 * j + k;
-          float pk = 0.f;
-#pragma unroll
-          for (int e = 0; e < 32; ++e) pk = e == k ? v[j][e] : pk;
-          const bool seen = w.valid && (see[at / 32 + j] >> k & 1);
-          const int64_t page = p.block_table[(size_t)b * p.max_pages + (key >> p.page_shift)];
-          const int64_t src = page * p.page_stride + (((int64_t)h << p.page_shift) + (key & ((1 << p.page_shift) - 1))) * D;
 #pragma unroll 1
-          for (int i = 0; i < D; i += 32) {
-            float o[32];
-            tc_wait_st();
-            tc_ld32(o, out + i);
-            tc_wait_ld();
+  for (int at = 0; at < cols; at += 32) {
+    if (at > 0) load(at);
+    float sum[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-            for (int e = 0; e < 32; ++e) {
-              float x;
-              if constexpr (kE4M3) x = __half2float(__ushort_as_half((unsigned short)e4m3x2_to_f16x2(static_cast<const uint8_t*>(p.v)[src + i + e])));
-              else x = Elem<T>::to_float(static_cast<const T*>(p.v)[src + i + e]);
-              if (seen && !isfinite(x)) o[e] += pk * x;
-            }
-            tc_st32(out + i, o);
+    for (int e = 0; e < 32; ++e) {
+      v[e] = exp2_fast(fmaf(v[e], w.c, -from));
+      sum[e & 3] += v[e];
+    }
+    w.l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+    uint32_t packed[16];
+#pragma unroll
+    for (int e = 0; e < 16; ++e) packed[e] = M::pack(v[2 * e], v[2 * e + 1]);
+    tc_st16(probs + (key0 + at) / 2, packed);
+    if (!all) {
+      // rare: keys with values that are NaN or infinite; the rows that see one add them themselves
+      for (uint32_t left = odd[(key0 + at) / 32]; left; left &= left - 1) {
+        const int k = __ffs(left) - 1, key = tile_key + key0 + at + k;
+        float pk = 0.f;
+#pragma unroll
+        for (int e = 0; e < 32; ++e) pk = e == k ? v[e] : pk;
+        const bool seen = w.valid && (see >> k & 1);
+        const int64_t page = p.block_table[(size_t)b * p.max_pages + (key >> p.page_shift)];
+        const int64_t src = page * p.page_stride + (((int64_t)h << p.page_shift) + (key & ((1 << p.page_shift) - 1))) * D;
+#pragma unroll 1
+        for (int i = 0; i < D; i += 32) {
+          float o[32];
+          tc_wait_st();
+          tc_ld32(o, out + i);
+          tc_wait_ld();
+#pragma unroll
+          for (int e = 0; e < 32; ++e) {
+            float x;
+            if constexpr (kE4M3) x = __half2float(__ushort_as_half((unsigned short)e4m3x2_to_f16x2(static_cast<const uint8_t*>(p.v)[src + i + e])));
+            else x = Elem<T>::to_float(static_cast<const T*>(p.v)[src + i + e]);
+            if (seen && !isfinite(x)) o[e] += pk * x;
           }
+          tc_st32(out + i, o);
         }
       }
     }
   }
-  if constexpr (kCols < kTileKeys) {                           // (their columns may have held scores of this share until now)
+  if (cols < kTileKeys) {                                       // (their columns may have held scores of this share until now)
     const uint32_t none[16] = {0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0};
-#pragma unroll
+#pragma unroll 1
     for (int j = 0; j < kTileKeys; j += 32)
-      if (j < key0 || j >= key0 + kCols) tc_st16(probs + j / 2, none);
+      if (j < key0 || j >= key0 + cols) tc_st16(probs + j / 2, none);
   }
   tc_wait_st();
 }
@@ -587,9 +577,7 @@ tree_attention_kernel(const AttnParams p, const __grid_constant__ CUtensorMap km
         if (active) {
           tc_fence_after();
           const uint32_t* odd = sm.odd[value % S::kClean];
-          if (per == 32) exponentials<T, kE4M3, D, 32>(p, w, scores, probs, out, key0, tile_key, r, walk.b, h, all, bad, odd);
-          else if (per == 64) exponentials<T, kE4M3, D, 64>(p, w, scores, probs, out, key0, tile_key, r, walk.b, h, all, bad, odd);
-          else exponentials<T, kE4M3, D, 128>(p, w, scores, probs, out, key0, tile_key, r, walk.b, h, all, bad, odd);
+          exponentials<T, kE4M3, D>(p, w, scores, probs, out, key0, per, tile_key, r, walk.b, h, all, bad, odd);
           tc_fence_before();
         }
         ++done;
