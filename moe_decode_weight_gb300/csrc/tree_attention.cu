@@ -133,25 +133,25 @@ __device__ __forceinline__ void exponentials(const AttnParams& p, Lane& w, uint3
                                              int tile_key, const Request& r, int b, int h, bool all, uint32_t bad, const uint32_t* odd) {
   using S = Shape<T, kE4M3, D>;
   using M = Mma<typename S::C>;
-  float v[32];
+  float v[32], most = -INFINITY;
   uint32_t see = ~0u;
-  auto load = [&](int at) {
-    tc_ld32(v, scores + key0 + at);
-    tc_wait_ld();
-    if (!all) {
-      see = visible32(w.bits, tile_key + key0 + at, r.ctx) & on_pages32(bad, key0 + at, p.page_shift);
+  auto hide = [&](int at) {
+    see = visible32(w.bits, tile_key + key0 + at, r.ctx) & on_pages32(bad, key0 + at, p.page_shift);
 #pragma unroll
-      for (int e = 0; e < 32; ++e) v[e] = see >> e & 1 ? v[e] : -INFINITY;
-    }
+    for (int e = 0; e < 32; ++e) v[e] = see >> e & 1 ? v[e] : -INFINITY;
   };
-  float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll 1
   for (int at = cols - 32; at >= 0; at -= 32) {                // the first part is held when the maximum is known
-    load(at);
+    float top = tc_ld32_max(v, scores + key0 + at);
+    tc_wait_ld();
+    if (!all) {
+      hide(at);
+      top = -INFINITY;
 #pragma unroll
-    for (int e = 0; e < 32; ++e) top[e & 3] = fmaxf(top[e & 3], v[e]);
+      for (int e = 0; e < 32; ++e) top = fmaxf(top, v[e]);
+    }
+    most = fmaxf(most, top);
   }
-  const float most = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
   const float now = most == -INFINITY ? -INFINITY : fmaf(most, w.c, -M::kShift);
   const bool grown = w.valid && now > w.mc + kSlack;            // also from -inf
   if (__any_sync(0xffffffffu, grown)) {
@@ -173,7 +173,11 @@ __device__ __forceinline__ void exponentials(const AttnParams& p, Lane& w, uint3
   const float from = w.mc == -INFINITY ? 0.f : w.mc;
 #pragma unroll 1
   for (int at = 0; at < cols; at += 32) {
-    if (at > 0) load(at);
+    if (at > 0) {
+      tc_ld32(v, scores + key0 + at);
+      tc_wait_ld();
+      if (!all) hide(at);
+    }
     float sum[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
     for (int e = 0; e < 32; ++e) {
