@@ -23,7 +23,7 @@
 // Requests of up to 32 rows a kv head have a kernel of their own (tree_attention_rows.cu; few_rows() below chooses).
 //
 // What bounds it is the stream of keys and values up to 64 rows a block (16 ragged trees of up to 16 nodes x 4 heads, 12k
-// keys: 84 us, 4.9 TB/s), and the exponentials above (64-node trees of 8 heads: 50 us; a tile of 128 rows
+// keys: 79 us, 5.2 TB/s), and the exponentials above (64-node trees of 8 heads: 48 us; a tile of 128 rows
 // takes a stream some 5,000 cycles, most of them exponentials). 152 SMs need about 128 KB each in flight to draw the
 // memory's full rate (a copy alone, with nothing done to the tiles, reaches 7.1 TB/s so, 16-token
 // pages in random order). Keys and values therefore share one ring in the order in which the products
@@ -745,10 +745,10 @@ __global__ void __launch_bounds__(128) join_kernel(const AttnParams p) {
 
 // ------------------------------------------------------------------ host
 
-// Which kernel. Up to 16 rows: few_rows_kernel (one token over 131k E4M3 keys 51 us, the other kernel 87; 1,500 16-bit keys
-// 10.4 and 15.4; 131k 16-bit keys 91 and 88). Up to 32 rows, of which two warps share the copies: the same over E4M3 caches and
-// heads of 64 (batches of trees 74 and 80 us, 54 and 66, 54 and 56), over a 16-bit cache with heads of 128 where the block
-// table leaves room for two tiles a block at most (1,500 keys 11.6 and 15.6 us, but a batch of trees 88 and 78).
+// Which kernel. Up to 16 rows: few_rows_kernel (one token over 131k E4M3 keys 51 us, the other kernel 86; 1,500 16-bit keys
+// 10.4 and 14.7; 131k 16-bit keys 90 and 88). Up to 32 rows, of which two warps share the copies: the same over E4M3 caches
+// and heads of 64 (batches of trees 72 and 79 us, 51 and 64, 51 and 59), over a 16-bit cache with heads of 128 where
+// the block table leaves room for two tiles a block at most (1,500 keys 11.5 and 14.9 us, but a batch of trees 88 and 77).
 bool few_rows(const AttnParams& p, int key_bytes, int grid) {
   const int rows = p.max_new * p.group;
   if (rows <= 16) return true;
@@ -858,14 +858,16 @@ extern "C" mdw_status mdw_tree_attention(const mdw_kv_cache* cache, int32_t B, i
   if (ws_bytes < lay.total) return MDW_ERR_WORKSPACE_TOO_SMALL;
   if (grid <= 0) return MDW_ERR_CUDA;
   uint8_t* base = static_cast<uint8_t*>(ws);
-  const AttnParams p{cache->v, cache->page_stride, cache->k_scale, cache->v_scale, q, out, lse, ldq, ldo, block_table, ctx_len, row_start, tree_mask, status,
+  AttnParams p{cache->v, cache->page_stride, cache->k_scale, cache->v_scale, q, out, lse, ldq, ldo, block_table, ctx_len, row_start, tree_mask, status,
                      mdw_spin_budget(), scale, B, T, q_heads, cache->kv_heads, q_heads / cache->kv_heads, max_new, max_pages,
-                     cache->num_pages, log2_of(cache->page_size), reinterpret_cast<int32_t*>(base),
+                     cache->num_pages, log2_of(cache->page_size), kItemCost, reinterpret_cast<int32_t*>(base),
                      reinterpret_cast<Cut*>(base + lay.cuts), reinterpret_cast<float2*>(base + lay.ml),
                      reinterpret_cast<float*>(base + lay.o)};
   CUtensorMap km, vm;
   const int D = cache->head_dim, key_bytes = D * (fp8 ? 1 : 2);
-  const int most = few_rows(p, key_bytes, grid) ? kFewBytes / key_bytes : kTileKeys;
+  const bool few = few_rows(p, key_bytes, grid);
+  const int most = few ? kFewBytes / key_bytes : kTileKeys;
+  if (few) p.item_cost = p.max_new * p.group <= 16 ? kItemCost16 : kItemCost32;
   if (!encode_cache(&km, cache, cache->k, most) || !encode_cache(&vm, cache, cache->v, most)) return MDW_ERR_CUDA;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   cudaError_t e;

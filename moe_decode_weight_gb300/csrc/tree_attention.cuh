@@ -32,7 +32,7 @@ struct AttnParams {
   uint32_t* status;
   long long spin_budget;
   float scale;
-  int B, T, Hq, Hkv, group, max_new, max_pages, num_pages, page_shift;
+  int B, T, Hq, Hkv, group, max_new, max_pages, num_pages, page_shift, item_cost;
   // workspace
   int32_t* total;          // [2] tiles of the whole call, blocks with a share
   struct Cut* cuts;        // [grid] the item that a block's share starts inside of
@@ -48,16 +48,17 @@ struct Cut {
 
 // ------------------------------------------------------------------ requests and shares
 
-// An item costs its tiles and, for its rows, its first scores and its result, as much time as this many more
-// (measured between 2 and 4): they count when the work is cut into shares.
-constexpr int kItemCost = 3;
+// An item costs its tiles and, for its rows, its first scores and its result, as much time as so many more: they count
+// when the work is cut into shares. 16 ragged trees: 84 us at 3, 79 to 81 at 5 to 7, 85 at 9; the kernel for few rows,
+// 32 of them over E4M3: 79 us at 2, 72 at 4, 75 at 7; one token in 64 requests 66 us at 1, 64 at 2, 68 at 5.
+constexpr int kItemCost = 6, kItemCost32 = 4, kItemCost16 = 2;
 
 struct Request {
   int row0, rows, ctx, keys;       // first row, rows, cached tokens, keys; rows < 0: not valid
   __device__ __forceinline__ int blocks(const AttnParams& p) const { return (rows * p.group + kTileRows - 1) / kTileRows; }
   __device__ __forceinline__ int tiles() const { return (keys + kTileKeys - 1) / kTileKeys; }
   __device__ __forceinline__ int64_t work(const AttnParams& p) const {
-    return rows <= 0 ? 0 : (int64_t)p.Hkv * blocks(p) * (tiles() + kItemCost);
+    return rows <= 0 ? 0 : (int64_t)p.Hkv * blocks(p) * (tiles() + p.item_cost);
   }
 };
 __device__ __forceinline__ Request load_request(const AttnParams& p, int b) {
@@ -74,7 +75,7 @@ __device__ __forceinline__ Request load_request(const AttnParams& p, int b) {
 }
 
 // Equal contiguous shares of `total` units: block c has [start(c), start(c + 1)). An item's units are its tiles and
-// then its kItemCost; a share that has tiles of an item writes a partial result of it, one that ends
+// then its item cost; a share that has tiles of an item writes a partial result of it, one that ends
 // among its last units has the whole rest.
 struct Shares {
   int blocks, base, rest;
@@ -149,7 +150,7 @@ struct Walk {
       }
       before += __shfl_sync(0xffffffffu, sum, 31);
     }
-    const int in = at - before, whole = tiles + kItemCost, item = in / whole;
+    const int in = at - before, whole = tiles + p.item_cost, item = in / whole;
     tile = in - item * whole;
     h = item / r.blocks(p);
     rb = item - h * r.blocks(p);
@@ -165,7 +166,7 @@ struct Walk {
   __device__ __forceinline__ int count() const { return min(tiles - tile, units); }
   __device__ __forceinline__ bool more() const { return units > 0; }
   __device__ __forceinline__ void done(const AttnParams& p, int lane) {
-    units -= tiles + kItemCost - tile;
+    units -= tiles + p.item_cost - tile;
     if (units > 0) next_item(p, lane);
   }
   __device__ __forceinline__ void next_item(const AttnParams& p, int lane) {

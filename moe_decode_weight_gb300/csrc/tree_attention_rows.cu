@@ -12,7 +12,7 @@
 // E4M3 caches). All lanes' page ids are loaded one stage early and looked at when they are used.
 //
 // Measured: one token over 131k E4M3 keys of 8 kv heads 51 us (5.2 TB/s; the stream alone 38, then begin 4, end 2
-// and join 3), 16-bit keys 91 us (5.9 TB/s), the 20 rows of a 4-token window over 1,500 keys 11.6 us, of which
+// and join 3), 16-bit keys 90 us (5.9 TB/s), the 20 rows of a 4-token window over 1,500 keys 11.5 us, of which
 // launch, first copies, end and join are all but 2. What bounds it is the keys' stream; over E4M3 with more than
 // 16 rows the conversion, which every 16 rows repeat (5.2 -> 3.2 TB/s).
 //
