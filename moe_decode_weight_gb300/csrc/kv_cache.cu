@@ -260,7 +260,9 @@ extern "C" mdw_status mdw_kv_plan(int32_t B, const int32_t* ctx_len, const int32
     return MDW_ERR_INVALID_ARG;
   PlanParams p{ctx_len, new_len, block_table, free_pages, parents, row_start, slot_map, positions, tree_mask,
                pages_taken, status, B, T, num_pages, max_pages, num_free, log2_of(page_size)};
-  const int dev = current_device(), most = 8 * sm_count(dev);
+  // four blocks an SM: more repeat the prefix sums, fewer have too few stores on their way (199 prompts with 390k rows 5.9 us; 8:
+  // 7.3, 3: 6.3, 2: 7.7)
+  const int dev = current_device(), most = 4 * sm_count(dev);
   if (most <= 0) return MDW_ERR_CUDA;
   const int wanted = (T + kPlanThreads - 1) / kPlanThreads, blocks = wanted < most ? wanted : most;
   kv_plan_kernel<<<blocks, kPlanThreads, 0, reinterpret_cast<cudaStream_t>(stream)>>>(p);
