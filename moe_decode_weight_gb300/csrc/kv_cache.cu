@@ -172,23 +172,34 @@ __device__ __forceinline__ uint4 ld_once(const void* p) {
   asm volatile("ld.global.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p));
   return v;
 }
+// The largest magnitude of two elements in each half (NaN counts as small).
+__device__ __forceinline__ __nv_bfloat162 most2(__nv_bfloat162 a, __nv_bfloat162 b) { return __hmax2(__habs2(a), __habs2(b)); }
+__device__ __forceinline__ __half2 most2(__half2 a, __half2 b) { return __hmax2(__habs2(a), __habs2(b)); }
+template <typename T> struct Two;
+template <> struct Two<__nv_bfloat16> { using type = __nv_bfloat162; };
+template <> struct Two<__half> { using type = __half2; };
+
 // Eight elements over their scale in E4M3: the code of the correctly rounded fp32 quotient, so that it depends
 // on nothing but x and scale. With y = RN(1 / s) and q = RN(x y), RN(q + (x - q s) y) is RN(x / s) (P. Markstein,
 // "Computation of elementary functions on the IBM RISC System/6000 processor", 1990) if the remainder
 // is exact and s has not the largest significand: scales of other magnitudes than 2^-64 .. 2^64 and that
-// significand are divided by, and quotients that saturate anyway are left as they are.
+// significand are divided by, and so are eight elements of which one is beyond 1024 s (far above what saturates; infinite
+// ones among them). The remainder is taken as q s - x, whose sign leaves -0 as it is.
 template <typename T>
 __device__ __forceinline__ uint2 to_e4m3(uint4 x, float s) {
+  using T2 = typename Two<T>::type;
   T e[8];
+  T2 two[4];
   memcpy(e, &x, 16);
+  memcpy(two, &x, 16);
+  const T2 most = most2(most2(two[0], two[1]), most2(two[2], two[3]));
+  const float top = fmaxf(Elem<T>::to_float(most.x), Elem<T>::to_float(most.y)), y = __frcp_rn(s);
   float v[8];
-  if (s >= 0x1p-64f && s <= 0x1p64f && (__float_as_uint(s) & 0x7fffffu) != 0x7fffffu) {
-    const float y = __frcp_rn(s);
+  if (s >= 0x1p-64f && s <= 0x1p64f && (__float_as_uint(s) & 0x7fffffu) != 0x7fffffu && top * y < 1024.f) {
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
       const float f = Elem<T>::to_float(e[j]), q = __fmul_rn(f, y);
-      const float exact = __fmaf_rn(__fmaf_rn(-q, s, f), y, q);
-      v[j] = copysignf(fabsf(q) < 1024.f ? exact : q, f);          // -0 stays -0
+      v[j] = __fmaf_rn(-__fmaf_rn(q, s, -f), y, q);
     }
   } else {
 #pragma unroll
@@ -200,9 +211,10 @@ __device__ __forceinline__ uint2 to_e4m3(uint4 x, float s) {
 
 // A block takes `rows` rows; a thread moves 8 elements of the keys and of the values at a time, two such pairs in
 // flight. Neighbouring threads read and write neighbouring pieces; a head's row is the unit of the cache
-// that stays whole (64 to 256 bytes).
+// that stays whole (64 to 256 bytes). 16381 rows of 8 heads of 128, 16-bit: 22.1 us, 6.1 TB/s; to E4M3: 21.9 us, 4.6 TB/s
+// (six blocks an SM; five 22.9, eight 24.0: their registers no longer hold two pairs).
 template <typename T, bool kE4M3>
-__global__ void __launch_bounds__(256) kv_write_kernel(const WriteParams p) {
+__global__ void __launch_bounds__(256, 6) kv_write_kernel(const WriteParams p) {
   const int row0 = blockIdx.x * p.rows, pieces = min(p.rows, p.T - row0) * p.chunks;
   for (int i = threadIdx.x; i < pieces; i += 512) {
     uint4 k[2], v[2];
