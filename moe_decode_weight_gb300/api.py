@@ -371,8 +371,9 @@ def _binding():
     return m
 
 
-def _on_device(fn, device, *args):
-    """A call whose tensors are on another device than the current one."""
+def _call(fn, *args):
+    """fn(*args); it answers with a device where its tensors are on another one than the current."""
+    device = fn(*args)
     if device is not None:
         with torch.cuda.device(device):
             fn(*args)
@@ -406,6 +407,7 @@ class W4Weights:
     zero: torch.Tensor | None = None
     c: W4WeightsC = field(init=False)
     address: int = field(init=False)
+    device_index: int = field(init=False)
 
     def __post_init__(self):
         fn, q, scale = "W4Weights", self.q, self.scale
@@ -422,15 +424,13 @@ class W4Weights:
                             _address(fn, scale, "scale", (torch.bfloat16, torch.float16), q.device),
                             None if self.zero is None else _address(fn, self.zero, "zero", (torch.uint8,), q.device, scale.shape))
         self.address = C.addressof(self.c)
+        self.device_index = q.get_device()
 
 
 def w4_linear(w: W4Weights, x: torch.Tensor, y: torch.Tensor, bias=None, residual=None, status=None,
               stream=None) -> None:
     """y = x . W^T (+ bias) (+ residual) for x [M, K], M <= 32; y [M, N] in x's type or float32."""
-    if x.device != w.q.device:
-        raise MdwError("w4_linear", 1, f"weights on {w.q.device}, x on {x.device}")
-    f, args = _binding().w4_linear, (w, x, y, bias, residual, status, stream)
-    _on_device(f, f(*args), *args)
+    _call((_bound or _binding()).w4_linear, w, x, y, bias, residual, status, stream)
 
 
 @dataclass
@@ -444,6 +444,7 @@ class KVCache:
     v_scale: torch.Tensor | None = None
     c: KVCacheC = field(init=False)
     address: int = field(init=False)
+    device_index: int = field(init=False)
 
     def __post_init__(self):
         fn, k, v = "KVCache", self.k, self.v
@@ -464,6 +465,7 @@ class KVCache:
         self.c = KVCacheC(MDW_MAGIC, FMT_KV_PAGED, DT_E4M3 if fp8 else _DT[k.dtype], k.shape[0], k.shape[2],
                           k.shape[1], k.shape[3], 0, strides.pop(), pk, pv, *scales)
         self.address = C.addressof(self.c)
+        self.device_index = k.get_device()
 
 
 def mdw_kv_plan(ctx_len: torch.Tensor, new_len: torch.Tensor, page_size: int, num_pages: int,
@@ -474,18 +476,14 @@ def mdw_kv_plan(ctx_len: torch.Tensor, new_len: torch.Tensor, page_size: int, nu
     ctx_len, new_len int32 [B]; block_table int32 [B, max pages]; free_pages int32 [F]; row_start int32
     [B + 1]; slot_map int64 [T]; positions, parents int32 [T]; tree_mask int64 or uint64 [T];
     pages_taken, status int32 [1]."""
-    f, args = _binding().kv_plan, (ctx_len, new_len, page_size, num_pages, block_table, free_pages, row_start, slot_map, positions,
-                                   pages_taken, parents, tree_mask, status, stream)
-    _on_device(f, f(*args), *args)
+    _call((_bound or _binding()).kv_plan, ctx_len, new_len, page_size, num_pages, block_table, free_pages, row_start, slot_map,
+          positions, pages_taken, parents, tree_mask, status, stream)
 
 
 def mdw_kv_write(cache: KVCache, k: torch.Tensor, v: torch.Tensor, slot_map: torch.Tensor, status=None,
                  stream=None) -> None:
     """Rows k, v [T, kv heads, head dim] (rows may be strided) to the cache's slots slot_map int64 [T]."""
-    if k.device != cache.k.device:
-        raise MdwError("mdw_kv_write", 1, f"cache on {cache.k.device}, k on {k.device}")
-    f, args = _binding().kv_write, (cache, k, v, slot_map, status, stream)
-    _on_device(f, f(*args), *args)
+    _call((_bound or _binding()).kv_write, cache, k, v, slot_map, status, stream)
 
 
 def mdw_tree_attention_workspace_bytes(cache: KVCache, b: int, t: int, q_heads: int, max_new: int) -> int:
@@ -501,8 +499,5 @@ def mdw_tree_attention(cache: KVCache, q: torch.Tensor, out: torch.Tensor, block
     """Attention of the drafted rows q [T, query heads, head dim] over the paged cache (see the C
     declaration); out like q, lse float32 [T, query heads] or None, scale head_dim ** -0.5 by default, ws
     uint8 of at least mdw_tree_attention_workspace_bytes."""
-    if q.device != cache.k.device:
-        raise MdwError("mdw_tree_attention", 1, f"cache on {cache.k.device}, q on {q.device}")
-    f, args = _binding().tree_attention, (cache, q, out, block_table, ctx_len, row_start, max_new, ws, tree_mask, lse,
-                                          cache.c.head_dim ** -0.5 if scale is None else scale, status, stream)
-    _on_device(f, f(*args), *args)
+    _call((_bound or _binding()).tree_attention, cache, q, out, block_table, ctx_len, row_start, max_new, ws, tree_mask, lse,
+          scale, status, stream)

@@ -48,7 +48,7 @@ def _compile(src: str, trace: bool = False) -> str:
 def _binding() -> None:
     tmp = BINDING + ".tmp"
     cmd = [shutil.which("gcc") or "cc", "-O2", "-std=c11", "-Wall", "-shared", "-fPIC", "-I" + sysconfig.get_paths()["include"],
-           "-I" + INCLUDE, os.path.join(CSRC, "binding.c"), "-o", tmp]
+           "-I" + INCLUDE, os.path.join(CSRC, "binding.c"), "-o", tmp, "-lm"]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"gcc failed on binding.c:\n{r.stdout}\n{r.stderr}")

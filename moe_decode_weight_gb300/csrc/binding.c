@@ -2,11 +2,12 @@
  *
  * A window's calls take a few microseconds on the GPU, and reading ten tensors' types, shapes, strides and
  * addresses from Python takes longer than that: a call of mdw_kv_plan took 10.1 us, of which the library's
- * part was 3.2 us, and takes 6.8 us through this module (mdw_tree_attention 13.3 -> 9.1, w4_linear 7.5 -> 4.6,
- * mdw_kv_write 7.1 -> 4.5). It does the checks that the Python code did and calls the library's entry points, whose addresses
+ * part was 3.2 us, and takes 6.0 us through this module (mdw_tree_attention 13.3 -> 7.6, w4_linear 7.5 -> 4.1,
+ * mdw_kv_write 7.1 -> 4.1). It does the checks that the Python code did and calls the library's entry points, whose addresses
  * the package hands it; it holds no arithmetic and keeps nothing of its arguments. */
 #define PY_SSIZE_T_CLEAN
 #include <Python.h>
+#include <math.h>
 #include <stdint.h>
 #include <string.h>
 
@@ -15,7 +16,7 @@
 enum { T_BF16 = 1, T_F16 = 2, T_F32 = 4, T_E4M3 = 8, T_U8 = 16, T_I32 = 32, T_I64 = 64, T_U64 = 128, T_KINDS = 8 };
 
 static PyObject *g_types[T_KINDS], *g_refuse, *g_device, *g_stream;
-static PyObject *s_dtype, *s_data_ptr, *s_get_device, *s_shape, *s_stride, *s_address, *s_cuda_stream;
+static PyObject *s_dtype, *s_data_ptr, *s_get_device, *s_shape, *s_stride, *s_address, *s_device_index, *s_cuda_stream, *s_is_contiguous;
 
 typedef mdw_status (*w4_fn)(const mdw_w4_weights*, int32_t, const void*, int64_t, void*, int64_t, int32_t, const void*, const void*,
                             int64_t, uint32_t*, mdw_stream_t);
@@ -31,7 +32,7 @@ static plan_fn g_plan;
 static write_fn g_write;
 static attention_fn g_attention;
 
-/* One call's state: the device of its first tensor, which the others have to share. */
+/* One call's state: the device of its handle or first tensor, which the others have to share. */
 typedef struct {
   const char* fn;
   long device;
@@ -71,8 +72,8 @@ static int numbers(PyObject* tuple, int64_t* out, int* n) {
   return !PyErr_Occurred();
 }
 
-/* Reads a tensor of one of the `types`; None (if `optional`) gives a null pointer. */
-static int tensor(Call* c, PyObject* t, const char* name, int types, int optional, Tensor* out) {
+/* Reads a tensor of one of the `types`, with or without its strides; None (if `optional`) gives a null pointer. */
+static int tensor(Call* c, PyObject* t, const char* name, int types, int optional, int strides, Tensor* out) {
   memset(out, 0, sizeof *out);
   if (t == Py_None && optional) return 1;
   PyObject* type = PyObject_GetAttr(t, s_dtype);
@@ -83,7 +84,8 @@ static int tensor(Call* c, PyObject* t, const char* name, int types, int optiona
   int64_t device, p;
   int n;
   if (!number(PyObject_CallMethodNoArgs(t, s_get_device), &device) || !number(PyObject_CallMethodNoArgs(t, s_data_ptr), &p) ||
-      !numbers(PyObject_GetAttr(t, s_shape), out->size, &out->dims) || !numbers(PyObject_CallMethodNoArgs(t, s_stride), out->stride, &n))
+      !numbers(PyObject_GetAttr(t, s_shape), out->size, &out->dims) ||
+      (strides && !numbers(PyObject_CallMethodNoArgs(t, s_stride), out->stride, &n)))
     return 0;
   if (device < 0) return refuse(c, MDW_ERR_INVALID_ARG, name, "has to be on a CUDA device");
   if (!(out->type & types)) return refuse(c, MDW_ERR_FORMAT_MISMATCH, name, "has another type than the call takes");
@@ -93,10 +95,10 @@ static int tensor(Call* c, PyObject* t, const char* name, int types, int optiona
   out->p = (void*)(intptr_t)p;
   return 1;
 }
-/* Whether dimensions from `first` on are laid out without gaps. */
-static int packed(const Tensor* t, int first) {
+/* Whether the elements of a row are laid out without gaps. */
+static int packed_rows(const Tensor* t) {
   int64_t width = 1;
-  for (int i = t->dims - 1; i >= first; --i) {
+  for (int i = t->dims - 1; i > 0; --i) {
     if (t->size[i] != 1 && t->stride[i] != width) return 0;
     width *= t->size[i];
   }
@@ -104,9 +106,13 @@ static int packed(const Tensor* t, int first) {
 }
 /* A contiguous array; want: its sizes (-1: any), of which there are `dims`. */
 static int array(Call* c, PyObject* o, const char* name, int types, int optional, int dims, int64_t d0, int64_t d1, Tensor* out) {
-  if (!tensor(c, o, name, types, optional, out)) return 0;
-  if (!out->p && o == Py_None) return 1;
-  if (out->dims != dims || (d0 >= 0 && out->size[0] != d0) || (dims > 1 && d1 >= 0 && out->size[1] != d1) || !packed(out, 0))
+  if (!tensor(c, o, name, types, optional, 0, out)) return 0;
+  if (o == Py_None) return 1;
+  PyObject* r = PyObject_CallMethodNoArgs(o, s_is_contiguous);
+  if (!r) return 0;
+  const int contiguous = r == Py_True;
+  Py_DECREF(r);
+  if (out->dims != dims || (d0 >= 0 && out->size[0] != d0) || (dims > 1 && d1 >= 0 && out->size[1] != d1) || !contiguous)
     return refuse(c, MDW_ERR_INVALID_ARG, name, "has another shape, or is not contiguous");
   return 1;
 }
@@ -114,19 +120,21 @@ static int array(Call* c, PyObject* o, const char* name, int types, int optional
 static int rows(Call* c, PyObject* o, const char* name, int types, int optional, int dims, int64_t d0, int64_t d1, int64_t d2, Tensor* out,
                 int64_t* ld) {
   *ld = 0;
-  if (!tensor(c, o, name, types, optional, out)) return 0;
+  if (!tensor(c, o, name, types, optional, 1, out)) return 0;
   if (o == Py_None) return 1;
   if (out->dims != dims || (d0 >= 0 && out->size[0] != d0) || (d1 >= 0 && out->size[1] != d1) || (dims > 2 && d2 >= 0 && out->size[2] != d2) ||
-      !packed(out, 1))
+      !packed_rows(out))
     return refuse(c, MDW_ERR_INVALID_ARG, name, "has another shape, or rows whose elements are not contiguous");
   const int64_t width = out->size[1] * (dims > 2 ? out->size[2] : 1);
   *ld = out->size[0] != 1 ? out->stride[0] : (width + 7) / 8 * 8;
   return 1;
 }
-/* Address of a weight or cache handle's descriptor, whose first two words are the magic and the format. */
-static const void* handle(const Call* c, PyObject* o, uint32_t format) {
-  int64_t a;
-  if (!number(PyObject_GetAttr(o, s_address), &a)) return NULL;
+/* Address of a weight or cache handle's descriptor, whose first two words are the magic and the format; the call's
+ * tensors have to be on its device. */
+static const void* handle(Call* c, PyObject* o, uint32_t format) {
+  int64_t a, device;
+  if (!number(PyObject_GetAttr(o, s_address), &a) || !number(PyObject_GetAttr(o, s_device_index), &device)) return NULL;
+  c->device = (long)device;
   const uint32_t* d = (const uint32_t*)(intptr_t)a;
   if (d[0] == MDW_MAGIC && d[1] == format) return d;
   refuse(c, MDW_ERR_FORMAT_MISMATCH, "the handle", "is of another kind");
@@ -268,7 +276,7 @@ static PyObject* b_tree_attention(PyObject* self, PyObject* const* a, Py_ssize_t
       !array(&c, a[9], "lse", T_F32, 1, 2, q.size[0], q.size[1], &lse) || !array(&c, a[11], "status", T_I32, 1, 1, 1, 0, &status))
     return NULL;
   const int64_t most = PyLong_AsLongLong(a[6]);
-  const double scale = PyFloat_AsDouble(a[10]);
+  const double scale = a[10] == Py_None ? 1.0 / sqrt((double)h->head_dim) : PyFloat_AsDouble(a[10]);
   if (PyErr_Occurred()) return NULL;
   mdw_stream_t s;
   int elsewhere;
@@ -318,6 +326,8 @@ PyMODINIT_FUNC PyInit__binding(void) {
   s_shape = PyUnicode_InternFromString("shape");
   s_stride = PyUnicode_InternFromString("stride");
   s_address = PyUnicode_InternFromString("address");
+  s_device_index = PyUnicode_InternFromString("device_index");
+  s_is_contiguous = PyUnicode_InternFromString("is_contiguous");
   s_cuda_stream = PyUnicode_InternFromString("cuda_stream");
   return PyModule_Create(&module);
 }

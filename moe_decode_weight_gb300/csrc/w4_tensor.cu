@@ -161,7 +161,7 @@ struct UnitZeros {
 };
 
 // A unit's scales and zeros, kFar units ahead: under load memory answers later than one unit takes.
-constexpr int kFar = 8;
+constexpr int kFar = 4;
 template <int kGroup>
 __device__ __forceinline__ void prefetch_scales(const W4Params& p, const Units& at, int row) {
   const size_t first = (size_t)min(at.tile * kTensorRows + row, p.N - 1) * (p.K / kGroup) + at.unit * (kUnit / kGroup);
