@@ -23,7 +23,7 @@
 // Requests of up to 32 rows a kv head have a kernel of their own (tree_attention_rows.cu; few_rows() below chooses).
 //
 // What bounds it is the stream of keys and values up to 64 rows a block (16 ragged trees of up to 16 nodes x 4 heads, 12k
-// keys: 79 us, 5.2 TB/s), and the exponentials above (64-node trees of 8 heads: 48 us; a tile of 128 rows
+// keys: 79 us, 5.2 TB/s), and the exponentials above (64-node trees of 8 heads: 46 us; a tile of 128 rows
 // takes a stream some 5,000 cycles, most of them exponentials). 152 SMs need about 128 KB each in flight to draw the
 // memory's full rate (a copy alone, with nothing done to the tiles, reaches 7.1 TB/s so, 16-token
 // pages in random order). Keys and values therefore share one ring in the order in which the products
@@ -63,7 +63,9 @@ struct Shape {
   static constexpr int kHelpers = kE4M3 ? 128 : 64;                       // threads of warps 12-15, or of 2 and 3
   static constexpr int kThreads = 32 * (kE4M3 ? 16 : 12);
   static constexpr int kRowsAt = 0, kSlotsAt = kTileRows * D * 2, kBuffersAt = kSlotsAt + kSlots * kCopied;
-  static constexpr int kPiece = 16, kJoinAt = kBuffersAt + kBuffers * kOperand;   // columns of an output that join at a time
+  // columns of an output that join at a time: few registers over E4M3 (a batch of trees 80 us, with 16 84) and for heads of 64
+  // (64-node trees 46.6, 47.6), fewer barriers otherwise (64 requests 75, with 8 77)
+  static constexpr int kPiece = kE4M3 || D == 64 ? 8 : 16, kJoinAt = kBuffersAt + kBuffers * kOperand;
   static constexpr int kSmall = kJoinAt + 2 * kTileRows * kPiece * 4;     // small arrays and barriers
   static constexpr int kSmem = kSmall + 2 * kTileRows * 8 + 3 * kTileRows * 4 + 1024;
   // tensor memory columns of a stream: scores (the probabilities take their first half when D = 128), output
@@ -600,9 +602,13 @@ tree_attention_kernel(const AttnParams p, const __grid_constant__ CUtensorMap km
       asm volatile("bar.sync 1, 256;" ::: "memory");
       tc_fence_after();
       float m = -INFINITY, sum = 0.f;
-      for (int i = mine; i < 2 * kTileRows; i += per) m = fmaxf(m, sm.ml[i].x);
+#pragma unroll
+      for (int j = 0; j < 2 * kTileRows / 32; ++j)
+        if (32 * j % per == 0) m = fmaxf(m, sm.ml[mine + 32 * j].x);
       const float from = m == -INFINITY ? 0.f : m;
-      for (int i = mine; i < 2 * kTileRows; i += per) sum += sm.ml[i].y * exp2_fast(sm.ml[i].x - from);
+#pragma unroll
+      for (int j = 0; j < 2 * kTileRows / 32; ++j)
+        if (32 * j % per == 0) sum += sm.ml[mine + 32 * j].y * exp2_fast(sm.ml[mine + 32 * j].x - from);
       float fa = exp2_fast(sm.ml[at_lane].x - from), fb = exp2_fast(sm.ml[kTileRows + at_lane].x - from);
       if (whole) {
         const float f = sum == 0.f ? 0.f : (kE4M3 ? p.v_scale[h] : 1.f) / sum;
