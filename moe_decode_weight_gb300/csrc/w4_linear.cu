@@ -11,7 +11,7 @@
 // f16 number, and as it is a bf16 one (see Int4); one more operation, exact, leaves code - zero. The
 // token's elements are put in the same order once, when they enter shared memory. This expansion
 // bounds the kernel beside the codes' stream: 9 operations for eight codes of a feature, whatever the number
-// of tokens, of which 5 on the integer pipe (157184 features x 2560, one token: 43.5 us, 4.8 TB/s).
+// of tokens, of which 5 on the integer pipe (157184 features x 2560, one token: 43.0 us, 4.8 TB/s).
 #include <type_traits>
 
 #include "mdw_internal.h"
@@ -189,11 +189,12 @@ __device__ __forceinline__ void store(const W4Params& p, int n0, int lane, const
 
 // ------------------------------------------------------------------ windows of up to 8 tokens
 //
-// A block owns a contiguous range of 16-feature tiles and cuts its (tile, unit) sequence into eight equal
-// contiguous shares, one per warp; each warp streams its share through a ring of its own (two TMA boxes of
-// 16 x 128 bytes a unit), with no barrier between the first and the last. A tile cut between warps
-// is finished from their partial sums, in order. x stays in shared memory as a whole.
+// A cluster of blocks (most often of one) owns a contiguous range of 16-feature tiles and cuts its (tile, unit) sequence into
+// equal contiguous shares, one per warp; each warp streams its share through a ring of its own (two TMA boxes of
+// 16 x 128 bytes a unit), with no barrier between the first and the last. A tile cut between warps is
+// finished from their partial sums, in order. x stays in each block's shared memory as a whole.
 constexpr int kRowWarps = 8, kRowStages = 2, kLineBytes = 16 * kUnit / 2, kRowUnit = 2 * kUnit, kRowBytes = 2 * kLineBytes;
+constexpr int kRowJoin = 10;
 constexpr int kRowMaxX = 36 * 1024;            // bytes of x that leave room for two blocks on an SM
 
 // Bytes of a token in shared memory, whole units; 64 more put two tokens' loads on different banks.
@@ -201,7 +202,7 @@ __host__ __device__ inline int x_pitch(int K) { return (K + kRowUnit - 1) / kRow
 
 template <typename T, int kGroup>
 __global__ void __launch_bounds__(32 * kRowWarps, 2)
-w4_rows_kernel(const W4Params p, const __grid_constant__ CUtensorMap codes, int tiles) {
+w4_rows_kernel(const W4Params p, const __grid_constant__ CUtensorMap codes, int tiles, int blocks) {
   extern __shared__ uint8_t raw_smem[];
   __shared__ float part[kRowWarps][2][4][32];
   __shared__ __align__(8) uint64_t bars[kRowWarps][kRowStages];
@@ -212,10 +213,15 @@ w4_rows_kernel(const W4Params p, const __grid_constant__ CUtensorMap codes, int 
   const uint32_t ring = base + warp * kRowStages * kRowBytes, xs = base + kRowWarps * kRowStages * kRowBytes;
   const uint32_t bar = smem_u32(&bars[warp][0]);
   const int units = (p.K + kRowUnit - 1) / kRowUnit, pitch = x_pitch(p.K);
-  const int t0 = (int)((int64_t)tiles * blockIdx.x / gridDim.x), t1 = (int)((int64_t)tiles * (blockIdx.x + 1) / gridDim.x);
-  const int all = (t1 - t0) * units;                            // this block's units (the host bounds them)
-  auto share = [&](int w) { return (int)((int64_t)all * w / kRowWarps); };
-  const int u0 = share(warp), u1 = share(warp + 1);
+  // (32-bit divisions, and few: a warp that starts with 64-bit ones starts a microsecond later)
+  const unsigned clusters = blocks == 1 ? gridDim.x : gridDim.x / (unsigned)blocks, cluster = blocks == 1 ? blockIdx.x : blockIdx.x / (unsigned)blocks;
+  const int all_warps = kRowWarps * blocks, mine = ((int)blockIdx.x - (int)cluster * blocks) * kRowWarps + warp;   // the warp's place in the cluster
+  const int some = (unsigned)tiles / clusters, more = tiles - some * (int)clusters;
+  const int t0 = (int)cluster * some + min((int)cluster, more), n_tiles = some + ((int)cluster < more);
+  const int all = n_tiles * units;                              // the cluster's units (the host bounds them)
+  const int per = (unsigned)all / (unsigned)all_warps, rest = all - per * all_warps;
+  auto share = [&](int w) { return w * per + min(w, rest); };
+  const int u0 = share(mine), u1 = share(mine + 1);
 
   int tile = u0 / units, unit = u0 - tile * units;
   int ask = u0, ask_tile = tile, ask_unit = unit;
@@ -293,31 +299,54 @@ w4_rows_kernel(const W4Params p, const __grid_constant__ CUtensorMap codes, int 
       if (unit == units) { unit = 0; ++tile; }
     }
   }
-  __syncthreads();
-  if (*dead) {
+  if (*dead && lane == 0)
     // what this warp requested has arrived or arrives now: its i-th copy into a stage ends phase i
-    if (lane == 0)
-      for (int i = 0; i < kRowStages; ++i) {
-        const int n = (ask - u0 - i + kRowStages - 1) / kRowStages;
-        if (ask - u0 > i) mbar_drain(bar + 8 * i, (n - 1) & 1);
-      }
-    return;
+    for (int i = 0; i < kRowStages; ++i) {
+      const int n = (ask - u0 - i + kRowStages - 1) / kRowStages;
+      if (ask - u0 > i) mbar_drain(bar + 8 * i, (n - 1) & 1);
+    }
+  __syncwarp();
+  bool lost;                                                    // a dead block anywhere in the cluster
+  if (blocks == 1) {
+    __syncthreads();
+    lost = *dead;
+  } else {
+    sync_cluster();
+    lost = false;
+    for (int r = 0; r < blocks; ++r) {
+      uint32_t v;
+      asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(in_block(smem_u32(&dead_flag), r)) : "memory");
+      lost |= v != 0;
+    }
   }
-  // the first warp whose share starts inside a tile finishes that tile
-  if (u1 == u0 || u0 % units == 0) return;
-  const int cut = u0 / units, begin = cut * units;
-  int w = warp - 1;
-  for (; share(w) > begin; --w)
-    if (share(w + 1) > share(w)) return;                        // an earlier warp does
-  while (share(w + 1) <= begin) ++w;
+  auto partial = [&](int w, int which, int e) {                 // of warp w of the cluster
+    if (blocks == 1) return part[w][which][e][lane];
+    float v;
+    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(in_block(smem_u32(&part[w % kRowWarps][which][e][lane]), w / kRowWarps)) : "memory");
+    return v;
+  };
+  auto finish = [&]() {
+    // the first warp whose share starts inside a tile finishes that tile
+    if (lost || u1 == u0 || u0 % units == 0) return;
+    const int cut = u0 / units, begin = cut * units;
+    int w = mine - 1;
+    for (; share(w) > begin; --w)
+      if (share(w + 1) > share(w)) return;                      // an earlier warp does
+    while (share(w + 1) <= begin) ++w;
 #pragma unroll
-  for (int e = 0; e < 4; ++e) acc[e] = part[w][1][e][lane];
-  for (++w; w < kRowWarps && share(w) < begin + units; ++w) {
-    if (share(w + 1) == share(w)) continue;
+    for (int e = 0; e < 4; ++e) acc[e] = partial(w, 1, e);
+    for (++w; w < all_warps && share(w) < begin + units; ++w) {
+      if (share(w + 1) == share(w)) continue;
 #pragma unroll
-    for (int e = 0; e < 4; ++e) acc[e] += part[w][0][e][lane];
+      for (int e = 0; e < 4; ++e) acc[e] += partial(w, 0, e);
+    }
+    store<T>(p, (t0 + cut) * 16, lane, acc);
+  };
+  finish();
+  if (blocks > 1) {
+    __syncwarp();
+    sync_cluster();                                             // no block ends while another reads its sums
   }
-  store<T>(p, (t0 + cut) * 16, lane, acc);
 }
 
 // ------------------------------------------------------------------ launches
@@ -339,13 +368,39 @@ cudaError_t launch_rows(const W4Params& p, int dev, cudaStream_t s) {
   CUtensorMap map;
   if (!encode_codes(&map, p, 16)) return cudaErrorInvalidValue;
   const int smem = 1024 + kRowWarps * kRowStages * kRowBytes + p.M * x_pitch(p.K);
-  const int tiles = (p.N + 15) / 16, most = 2 * sm_count(dev);
-  w4_rows_kernel<T, kGroup><<<tiles < most ? tiles : most, 32 * kRowWarps, smem, s>>>(p, map, tiles);
-  return cudaGetLastError();
+  const int tiles = (p.N + 15) / 16, most = 2 * sm_count(dev), units = (p.K + kRowUnit - 1) / kRowUnit;
+  cudaLaunchConfig_t cfg{};
+  cfg.blockDim = dim3(32 * kRowWarps);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute a{};
+  a.id = cudaLaunchAttributeClusterDimension;
+  a.val.clusterDim.y = a.val.clusterDim.z = 1;
+  cfg.attrs = &a;
+  // Blocks to a cluster: the fewest units in a block's share, a join of a cluster counted as kRowJoin of them (one token, 10007
+  // features: 16384 elements 32.9 us in clusters, 41.6 without; 5120 elements 13.0 and 12.0).
+  int blocks = 1, many = tiles < most ? tiles : most, best = (tiles + many - 1) / many * units;
+  for (int n = 2; n <= kMostCluster && tiles > most; n *= 2) {
+    a.val.clusterDim.x = n;
+    cfg.numAttrs = 1;
+    cfg.gridDim = dim3((unsigned)n);
+    const int fit = clusters<w4_rows_kernel<T, kGroup>>(cfg, n, dev);
+    if (fit < 1) continue;
+    const int cost = ((tiles + fit - 1) / fit * units + n - 1) / n + kRowJoin;
+    if (cost < best) {
+      best = cost;
+      blocks = n;
+      many = fit;
+    }
+  }
+  a.val.clusterDim.x = blocks;
+  cfg.numAttrs = blocks > 1 ? 1 : 0;
+  cfg.gridDim = dim3((unsigned)(blocks * many));
+  return cudaLaunchKernelEx(&cfg, w4_rows_kernel<T, kGroup>, p, map, tiles, blocks);
 }
 
-// Up to 8 tokens whose elements leave two blocks a SM's shared memory: the rows' kernel (8 tokens x 2560 elements do not: at
-// 157184 features 52 us on tcgen05; one token 47 us, against 57).
+// Up to 8 tokens whose elements leave two blocks a SM's shared memory: the rows' kernel (157184 features x 2560, one token: 43 us, on
+// tcgen05 51; 8 tokens x 2048: 38 and 43; 4000 features x 4096, 4 tokens: 7.7 and 7.8). 8 tokens x 2560 elements do not fit.
 template <typename T, int kGroup>
 cudaError_t launch(const W4Params& p, int dev, cudaStream_t s) {
   if (p.M <= 8 && p.M * x_pitch(p.K) <= kRowMaxX) return launch_rows<T, kGroup>(p, dev, s);

@@ -1,6 +1,7 @@
 // What the kernels of w4_linear share: the call's parameters, the expansion of the codes, small steps.
 #pragma once
 
+#include <atomic>
 #include <cstring>
 
 #include "mdw_attn.cuh"
@@ -90,6 +91,34 @@ __device__ __forceinline__ void sts_paired(uint32_t a, uint4 v) {
 __device__ __forceinline__ void tma_codes(uint32_t dst, const CUtensorMap* map, uint32_t bar, int byte, int row) {
   asm volatile("cp.async.bulk.tensor.2d.shared::cta.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];"
                :: "r"(dst), "l"(map), "r"(byte), "r"(row), "r"(bar) : "memory");
+}
+
+// ------------------------------------------------------------------ clusters
+
+constexpr int kMostCluster = 8;
+
+// Address of another block's shared memory in the cluster.
+__device__ __forceinline__ uint32_t in_block(uint32_t a, int rank) {
+  uint32_t r;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(rank));
+  return r;
+}
+__device__ __forceinline__ void sync_cluster() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+// Clusters of `blocks` blocks that a device runs at once, asked once.
+template <auto kKernel>
+int clusters(const cudaLaunchConfig_t& cfg, int blocks, int dev) {
+  static std::atomic<int> known[kMaxDevices][kMostCluster + 1];
+  int n = known[dev][blocks].load(std::memory_order_relaxed);
+  if (n == 0) {
+    if (cudaOccupancyMaxActiveClusters(&n, kKernel, &cfg) != cudaSuccess || n < 1) {
+      cudaGetLastError();
+      n = -1;
+    }
+    known[dev][blocks].store(n, std::memory_order_relaxed);
+  }
+  return n;
 }
 
 // Windows of up to 32 tokens on the tensor cores' own memory (w4_tensor.cu); codes: boxes of kTensorRows features x one unit.

@@ -16,7 +16,7 @@
 // and a fused multiply-add, exact in both halves, takes 16 and the zero out, as in Int4. 12 operations for eight
 // codes of a feature, done once for all tokens.
 //
-// Measured, 157184 features x 2560 in groups of 128: 9 tokens 52 us, 32 tokens 61 us (3.7 TB/s; m16n8k16 products fed from
+// Measured, 157184 features x 2560 in groups of 128: 9 tokens 51.5 us, 32 tokens 60 us (3.8 TB/s; m16n8k16 products fed from
 // shared memory took 63 and 104). What bounds it is the way of a half unit through its stages, expansion, products and
 // sums, of which each takes 600 to 900 cycles and waits for the others' barriers, not one of them alone: without
 // the expansion it is 15 % faster, without the products 8 %, from L2 2 %.
@@ -31,7 +31,6 @@
 namespace mdw {
 namespace {
 
-constexpr int kMostCluster = 8;
 constexpr int kThreads = 512, kCodeBytes = kTensorRows * kUnit / 2, kHalf = kUnit / 2;
 constexpr int kOperands = 4;                   // halves of a unit in tensor memory, expanded, 64 columns each
 
@@ -80,27 +79,20 @@ struct Units {
   }
 };
 
-// Address of another block's shared memory in the cluster.
-__device__ __forceinline__ uint32_t in_block(uint32_t a, int rank) {
-  uint32_t r;
-  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(rank));
-  return r;
-}
-__device__ __forceinline__ void sync_cluster() {
-  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
-}
-
 // The tiles are divided among the clusters, and the (tile, unit) sequence of a cluster into equal contiguous shares of its
 // blocks: a tile cut between blocks is finished from their sums, in order, when all are done.
 struct Share {
-  int t0, units, all, blocks;      // cluster's first tile, units of a tile, units of the cluster
-  __device__ __forceinline__ Share(const W4Params& p, int blocks_) : blocks(blocks_) {
-    const int tiles = (p.N + kTensorRows - 1) / kTensorRows, clusters = gridDim.x / blocks, c = blockIdx.x / blocks;
+  int t0, units, per, rest;        // cluster's first tile, units of a tile; of a block of it (the first `rest` blocks have one more)
+  __device__ __forceinline__ Share(const W4Params& p, int blocks) {
+    const int tiles = (p.N + kTensorRows - 1) / kTensorRows, clusters = (unsigned)gridDim.x / (unsigned)blocks, c = (unsigned)blockIdx.x / (unsigned)blocks;
+    const int some = (unsigned)tiles / (unsigned)clusters, more = tiles - some * clusters;
     units = (p.K + kUnit - 1) / kUnit;
-    t0 = (int)((int64_t)tiles * c / clusters);
-    all = ((int)((int64_t)tiles * (c + 1) / clusters) - t0) * units;
+    t0 = c * some + min(c, more);
+    const int all = (some + (c < more)) * units;
+    per = (unsigned)all / (unsigned)blocks;
+    rest = all - per * blocks;
   }
-  __device__ __forceinline__ int start(int rank) const { return (int)((int64_t)all * rank / blocks); }
+  __device__ __forceinline__ int start(int rank) const { return rank * per + min(rank, rest); }
 };
 
 // Scales or zeros of one unit (256 / kGroup of them) for one feature.
@@ -448,21 +440,6 @@ bool encode_tokens(CUtensorMap* map, const W4Params& p, int tokens) {
 }
 
 constexpr int kJoinUnits = 4;
-
-// Clusters of `blocks` blocks that a device runs at once, asked once.
-template <auto kKernel>
-int clusters(const cudaLaunchConfig_t& cfg, int blocks, int dev) {
-  static std::atomic<int> known[kMaxDevices][kMostCluster + 1];
-  int n = known[dev][blocks].load(std::memory_order_relaxed);
-  if (n == 0) {
-    if (cudaOccupancyMaxActiveClusters(&n, kKernel, &cfg) != cudaSuccess || n < 1) {
-      cudaGetLastError();
-      n = -1;
-    }
-    known[dev][blocks].store(n, std::memory_order_relaxed);
-  }
-  return n;
-}
 
 template <typename T, int kGroup, int kTokens>
 cudaError_t launch(const W4Params& p, const CUtensorMap& codes, int dev, cudaStream_t s) {

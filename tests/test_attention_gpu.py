@@ -927,3 +927,21 @@ def test_first_calls_of_a_process_can_be_captured():
     code = FIRST_CALLS_CAPTURED.format(root=os.path.dirname(here), tests=here)
     r = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True, timeout=300)
     assert r.returncode == 0 and r.stdout.strip().endswith("ok"), r.stderr[-2000:]
+
+
+@pytest.mark.parametrize("m,n,k,group,zero,dtype,ydtype", [
+    (1, 5000, 512, 128, False, BF, F32), (3, 5130, 2560, 64, True, HF, HF), (8, 9001, 640, 32, True, BF, BF), (2, 20011, 1152, 128, False, BF, F32),
+    (1, 7001, 16384, 32, True, HF, F32), (4, 4880, 4096, 128, True, BF, BF), (1, 12001, 96, 32, False, BF, F32)])
+def test_w4_linear_few_tokens_many_features(m, n, k, group, zero, dtype, ydtype):
+    """More tiles of features than blocks, whose units clusters of blocks share out."""
+    w = w4_case(m + n, n, k, group, zero, dtype)
+    x = torch.randn((m, k), generator=gen(2), device="cuda").to(dtype)
+    res = torch.randn((m, n), generator=gen(4), device="cuda").to(dtype)
+    y = torch.full((m + 1, n), 7.0, dtype=ydtype, device="cuda")
+    api.w4_linear(w, x, y[:m], residual=res)
+    want, tol = w4_want(w, x, residual=res)
+    assert_close(host(y[:m]), want, tol + half_step(ydtype) * np.abs(want))
+    assert (y[m] == 7.0).all()
+    again = torch.empty_like(y[:m])
+    api.w4_linear(w, x, again, residual=res)
+    assert torch.equal(again, y[:m])
