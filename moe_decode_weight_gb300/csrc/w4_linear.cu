@@ -400,7 +400,7 @@ cudaError_t launch_rows(const W4Params& p, int dev, cudaStream_t s) {
 }
 
 // Up to 8 tokens whose elements leave two blocks a SM's shared memory: the rows' kernel (157184 features x 2560, one token: 43 us, on
-// tcgen05 51; 8 tokens x 2048: 38 and 43; 4000 features x 4096, 4 tokens: 7.7 and 7.8). 8 tokens x 2560 elements do not fit.
+// tcgen05 51; 8 tokens x 2048: 38 and 43; 4000 features x 4096, 4 tokens: 7.8 and 7.9). 8 tokens x 2560 elements do not fit.
 template <typename T, int kGroup>
 cudaError_t launch(const W4Params& p, int dev, cudaStream_t s) {
   if (p.M <= 8 && p.M * x_pitch(p.K) <= kRowMaxX) return launch_rows<T, kGroup>(p, dev, s);
