@@ -81,7 +81,8 @@ static __device__ __noinline__ void mbar_wait_slow(uint32_t bar, uint32_t parity
 __device__ __forceinline__ void mbar_wait(uint32_t bar, uint32_t parity, long long budget, uint32_t* status, volatile int* dead) {
   if (!mbar_test(bar, parity)) mbar_wait_slow(bar, parity, budget, status, dead);
 }
-// A dead block's copies in flight end before the block does (bounded as well).
+// Waits for a copy's arrival whether or not the block is dead (bounded as well): a block does not end before its copies, which
+// would write into the shared memory of the one that follows.
 __device__ __forceinline__ void mbar_drain_inline(uint32_t bar, uint32_t parity) {
   const long long t0 = clock64();
   while (!mbar_try(bar, parity) && clock64() - t0 < (1ll << 28)) {}

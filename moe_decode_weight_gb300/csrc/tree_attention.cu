@@ -350,8 +350,9 @@ tree_attention_kernel(const AttnParams p, const __grid_constant__ CUtensorMap km
       }
       walk.done(p, lane);
     }
-    if (lost)
-      for (int i = 0; i < S::kSlots; ++i) mbar_drain(sm.full + 8 * i, i < slot ? phase : phase ^ 1);
+    // Every copy arrives before the block ends, also where a wait runs out after the last one was requested: warp 0 waits
+    // for each slot's last one (a slot that was never filled has its phase before the first, which is over).
+    for (int i = 0; i < S::kSlots; ++i) mbar_drain(sm.full + 8 * i, i < slot ? phase : phase ^ 1);
   } else if (warp == 1) {
     // ---- products. Scores of the first two tiles of an item, then in turn the output of tile i and the scores
     // of tile i + 2, whose columns hold the probabilities that output reads.

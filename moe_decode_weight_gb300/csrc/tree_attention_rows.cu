@@ -180,8 +180,9 @@ few_rows_kernel(const AttnParams p, const __grid_constant__ CUtensorMap kmap, co
       before += n;
       walk.done(p, lane);
     }
-    // a block given up: its copies in flight end before it does
-    if (*dead && x < kRings && sub == 0)
+    // Every copy arrives before the block ends, also where a wait runs out after the last one was requested: the block is not
+    // over before this warp has waited for each ring's last ones.
+    if (x < kRings && sub == 0)
       for (int i = max(asked - kStages, 0); i < asked; ++i) mbar_drain_inline(full + 8 * (x * kStages + i % kStages), i / kStages & 1);
     return;
   }

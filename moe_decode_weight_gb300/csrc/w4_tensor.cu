@@ -226,8 +226,8 @@ w4_tensor_kernel(const W4Params p, const __grid_constant__ CUtensorMap codes, co
 #pragma unroll
         for (int i = 0; i < kUnit / 64; ++i) tma_codes(to + kCodeBytes + i * L::kXBlock, &tokens, full, at.unit * kUnit + 64 * i, 0);
       }
-      if (*dead)                                                // what was requested arrives before the block ends
-        for (int i = n > L::kStages ? n - L::kStages : 0; i < n; ++i) mbar_drain(bar(L::kFull, i % L::kStages), i / L::kStages & 1);
+      // what was requested arrives before the block ends, also where a wait runs out after the last request
+      for (int i = n > L::kStages ? n - L::kStages : 0; i < n; ++i) mbar_drain(bar(L::kFull, i % L::kStages), i / L::kStages & 1);
     }
     __syncwarp();
   } else if (warp <= L::kIssuers) {

@@ -945,3 +945,49 @@ def test_w4_linear_few_tokens_many_features(m, n, k, group, zero, dtype, ydtype)
     again = torch.empty_like(y[:m])
     api.w4_linear(w, x, again, residual=res)
     assert torch.equal(again, y[:m])
+
+
+# ---- waits that run out: every copy arrives before its block ends, whenever the wait runs out
+
+
+@pytest.mark.parametrize("hq,dtype,ctype,d", PATHS)
+def test_attention_is_right_after_waits_that_ran_out(hq, dtype, ctype, d):
+    """Shares of a few tiles, whose copies are all requested at once: those of a block that gave up do not reach
+    into the shared memory of the next call's blocks, which follow at once."""
+    c = Attn(70, [900, 0, 300, 140], [4, 3, 1, 4], hq, 2, d, 16, dtype, ctype)
+    want = c.call()
+    args = i32(c.table), i32(c.ctx), i32(c.start)
+    ws = [torch.empty(api.mdw_tree_attention_workspace_bytes(c.cache, 4, c.t, hq, 4), dtype=torch.uint8, device="cuda") for _ in range(2)]
+    junk, lse = torch.empty_like(c.q), torch.empty(c.q.shape[:2], device="cuda")
+    outs = [torch.empty_like(c.q) for _ in range(16)]
+    lost, good = i32([0]), i32([0])
+    try:
+        for out in outs:
+            api.mdw_debug_set_spin_budget(1)
+            api.mdw_tree_attention(c.cache, c.q, junk, *args, 4, ws[0], tree_mask=c.mask, lse=lse, scale=c.scale, status=lost)
+            api.mdw_debug_set_spin_budget(0)
+            api.mdw_tree_attention(c.cache, c.q, out, *args, 4, ws[1], tree_mask=c.mask, lse=lse, scale=c.scale, status=good)
+    finally:
+        api.mdw_debug_set_spin_budget(0)
+    assert lost.item() == 6 and good.item() == 0
+    assert all(torch.equal(out, want[0]) for out in outs) and torch.equal(lse, want[1])
+
+
+@pytest.mark.parametrize("m,n,k,group,dtype", [(2, 3000, 2560, 64, BF), (12, 3000, 640, 32, HF), (12, 40000, 640, 128, BF), (32, 3000, 5120, 32, BF)])
+def test_w4_linear_is_right_after_waits_that_ran_out(m, n, k, group, dtype):
+    w = w4_case(71, n, k, group, True, dtype)
+    x = torch.randn((m, k), generator=gen(1), device="cuda").to(dtype)
+    want, junk = torch.empty((m, n), dtype=F32, device="cuda"), torch.empty((m, n), dtype=F32, device="cuda")
+    api.w4_linear(w, x, want)
+    outs = [torch.empty_like(want) for _ in range(16)]
+    lost, good = i32([0]), i32([0])
+    try:
+        for out in outs:
+            api.mdw_debug_set_spin_budget(1)
+            api.w4_linear(w, x, junk, status=lost)
+            api.mdw_debug_set_spin_budget(0)
+            api.w4_linear(w, x, out, status=good)
+    finally:
+        api.mdw_debug_set_spin_budget(0)
+    assert good.item() == 0 and (m <= 8 or lost.item() == 6)
+    assert all(torch.equal(out, want) for out in outs)
