@@ -199,7 +199,10 @@ __device__ __forceinline__ void exponentials(const AttnParams& p, Lane& w, uint3
 #pragma unroll
         for (int e = 0; e < 32; ++e) pk = e == k ? v[e] : pk;
         const bool seen = w.valid && (see >> k & 1);
+        // (a block that gave up comes here with notes of another tile: keys behind the sequence or on pages outside the cache)
+        if (key >= r.keys) break;
         const int64_t page = p.block_table[(size_t)b * p.max_pages + (key >> p.page_shift)];
+        if (page < 0 || page >= p.num_pages) continue;
         const int64_t src = page * p.page_stride + (((int64_t)h << p.page_shift) + (key & ((1 << p.page_shift) - 1))) * D;
 #pragma unroll 1
         for (int i = 0; i < D; i += 32) {

@@ -991,3 +991,24 @@ def test_w4_linear_is_right_after_waits_that_ran_out(m, n, k, group, dtype):
         api.mdw_debug_set_spin_budget(0)
     assert good.item() == 0 and (m <= 8 or lost.item() == 6)
     assert all(torch.equal(out, want) for out in outs)
+
+
+@pytest.mark.parametrize("hq,dtype,ctype,d", PATHS)
+def test_attention_that_gives_up_reads_no_bad_page(hq, dtype, ctype, d):
+    """A block whose wait runs out goes on with what its shared memory holds, here NaN of the same tiles' other
+    pages: it reads neither pages outside the cache nor behind the table's end."""
+    c = Attn(72, [900, 90], [4, 3], hq, 2, d, 16, dtype, ctype)
+    table = c.table.copy()
+    table[0, 1::2], table[1, 3:] = 1 << 30, -(1 << 30)
+    c.cache.v.view(torch.uint8 if ctype == E4 else torch.int16).fill_(127 if ctype == E4 else -1)
+    ws = torch.empty(api.mdw_tree_attention_workspace_bytes(c.cache, 2, c.t, hq, 4), dtype=torch.uint8, device="cuda")
+    for budget in (0, 1, 1, 1):                       # the first call leaves its tiles in shared memory
+        api.mdw_debug_set_spin_budget(budget)
+        try:
+            status = i32([0])
+            out, _ = c.call(table=table, ws=ws, status=status)
+            assert status.item() in ((7,) if budget == 0 else (6, 7))
+        finally:
+            api.mdw_debug_set_spin_budget(0)
+    c = Attn(73, [900, 90], [4, 3], hq, 2, d, 16, dtype, ctype)
+    c.check(*c.call())
