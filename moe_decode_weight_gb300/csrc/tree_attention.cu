@@ -364,7 +364,9 @@ tree_attention_kernel(const AttnParams p, const __grid_constant__ CUtensorMap km
       const int count = walk.count();
       auto scores = [&](int i) {
         const int unit = unit0 + keys_unit(i), at = unit % S::kClean, s = i & 1;
-        wait((kE4M3 ? sm.clean : sm.full) + 8 * at, unit / S::kClean & 1);
+        // (also where nothing is done to keys: the helper warps wait for every copy, and one that came to a slot after its
+        // next copy would wait for the one after that, and hold up everything)
+        wait(sm.clean + 8 * at, unit / S::kClean & 1);
         tc_fence_after();
         const uint32_t rows_low = operand_low(rows_at, 16), keys_low = operand_low(operand_at(at), 16), to = tmem + s * S::kStream;
         if (elect_one()) {

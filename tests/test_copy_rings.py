@@ -17,6 +17,20 @@ def source(name):
         return re.sub(r"//[^\n]*", "", f.read())
 
 
+def ends(start, moves):
+    """The states that can be reached from `start` and from which nothing moves any more."""
+    seen, todo, last = {start}, [start], []
+    while todo:
+        s = todo.pop()
+        after = list(moves(s))
+        last += [] if after else [s]
+        for t in after:
+            if t not in seen:
+                seen.add(t)
+                todo.append(t)
+    return last
+
+
 # ------------------------------------------------------------- a block does not end before its copies
 
 
@@ -66,3 +80,61 @@ def test_copying_warps_wait_for_their_copies_unconditionally(name, drain):
     assert len(at) == 1 and lines[at[0]].startswith("for (")
     before = lines[at[0] - 1]
     assert not re.match(r"if \(.*(dead|lost)", before), before
+
+
+# ------------------------------------------------------- every warp that waits for a copy sees its phase
+
+
+def keys_first(count):
+    """The units of an item: K0 K1 V0 K2 V1 ... with their tiles."""
+    order = [("K", 0)]
+    for i in range(count):
+        order += [("K", i + 1)] if i + 1 < count else []
+        order += [("V", i)]
+    return order
+
+
+def stuck(scores_wait, slots, count):
+    """Whether the ring of 16-bit tiles can come to a halt: a copying warp, the warp of the products (which frees a slot) and
+    two helper warps, that wait for every unit's copy and then arrive. A barrier is the number of its completed
+    phases, and a wait for phase n by parity returns while that is n + 1, n + 3, ..."""
+    order = keys_first(count)
+    place = {u: n for n, u in enumerate(order)}
+    products = [("K", 0)] + ([("K", 1)] if count > 1 else [])
+    for i in range(count):
+        products += [("V", i)] + ([("K", i + 2)] if i + 2 < count else [])
+    n = len(order)
+    assert sorted(products) == sorted(order)
+
+    def over(done, phase):
+        return done > phase and (done - phase) % 2 == 1
+
+    # asked, arrived: copies; freed per slot; place of the products; places of the helpers
+    def moves(s):
+        asked, arrived, used, helpers = s
+        freed = [sum(1 for u in products[:used] if place[u] % slots == x) for x in range(slots)]
+        full = [sum(1 for u in range(arrived) if u % slots == x) for x in range(slots)]
+        clean = [min(sum(1 for u in range(h) if u % slots == x) for h in helpers) for x in range(slots)]
+        if asked < n and freed[asked % slots] >= asked // slots:
+            yield asked + 1, arrived, used, helpers
+        if arrived < asked:
+            yield asked, arrived + 1, used, helpers
+        if used < n:
+            u = place[products[used]]
+            done = full if products[used][0] == "K" and scores_wait == "full" else clean
+            if over(done[u % slots], u // slots):
+                yield asked, arrived, used + 1, helpers
+        for j, h in enumerate(helpers):
+            if h < n and over(full[h % slots], h // slots):
+                yield asked, arrived, used, helpers[:j] + (h + 1,) + helpers[j + 1:]
+
+    return any(s != (n, n, n, (n, n)) for s in ends((0, 0, 0, (0, 0)), moves))
+
+
+@pytest.mark.parametrize("slots,count", [(3, 6), (4, 7), (5, 8)])
+def test_ring_of_tiles_cannot_come_to_a_halt(slots, count):
+    """The products wait for the helpers' arrival for keys as for values; waiting for the copy alone lets a slot be
+    filled again before a helper has seen that its last copy is there."""
+    assert stuck("full", slots, count) and not stuck("clean", slots, count)
+    scores = re.search(r"auto scores = \[&\]\(int i\) \{(.*?)tc_fence_after", source("tree_attention.cu"), re.S).group(1)
+    assert re.findall(r"wait\(([^;]*?) \+ 8 \* at", scores) == ["sm.clean"]
