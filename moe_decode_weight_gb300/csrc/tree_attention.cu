@@ -199,10 +199,7 @@ __device__ __forceinline__ void exponentials(const AttnParams& p, Lane& w, uint3
 #pragma unroll
         for (int e = 0; e < 32; ++e) pk = e == k ? v[e] : pk;
         const bool seen = w.valid && (see >> k & 1);
-        // (a block that gave up comes here with notes of another tile: keys behind the sequence or on pages outside the cache)
-        if (key >= r.keys) break;
         const int64_t page = p.block_table[(size_t)b * p.max_pages + (key >> p.page_shift)];
-        if (page < 0 || page >= p.num_pages) continue;
         const int64_t src = page * p.page_stride + (((int64_t)h << p.page_shift) + (key & ((1 << p.page_shift) - 1))) * D;
 #pragma unroll 1
         for (int i = 0; i < D; i += 32) {
@@ -585,8 +582,9 @@ tree_attention_kernel(const AttnParams p, const __grid_constant__ CUtensorMap km
         const bool all = tile_key + kTileKeys <= r.ctx && bad == 0;
         const int value = unit0 + values_unit(i, count);
         if (!all) wait(sm.clean + 8 * (value % S::kClean), value / S::kClean & 1);
-        __syncwarp();
-        if (active) {
+        // (the notes of a block that gave up are another tile's: they name keys behind the sequence, or pages outside the cache)
+        const bool lost = __any_sync(0xffffffffu, !all && *sm.dead);
+        if (active && !lost) {
           tc_fence_after();
           const uint32_t* odd = sm.odd[value % S::kClean];
           exponentials<T, kE4M3, D>(p, w, scores, probs, out, key0, per, tile_key, r, walk.b, h, all, bad, odd);
