@@ -354,9 +354,9 @@ mdw_status lm_head_fp8_sample(const mdw_lm_head* head, int32_t M, const void* h_
  *     the device (lengths, page ids, slots, parents) stores an mdw_status there if the word is
  *     still 0, computes nothing for what the bad data governs, and accesses nothing outside
  *     the arrays it was given. A wait of a copy pipeline that runs out (it is bounded, see
- *     mdw_debug_set_spin_budget) stores MDW_ERR_TIMEOUT; its block then stores no results. No
- *     call clears the word, so one check serves a whole step (mdw_device_status() reads it
- *     when it is 16-byte aligned). */
+ *     mdw_debug_set_spin_budget) stores MDW_ERR_TIMEOUT; results that its block has a part in
+ *     and has not stored yet are then left as they were. No call clears the word, so one check
+ *     serves a whole step (mdw_device_status() reads it when it is 16-byte aligned). */
 
 /* A dense weight in int4 with group scales: w[n][k] = (code - zero) * scale, per group of
  * `group` consecutive k. fmt MDW_FMT_INT4_GROUP. */

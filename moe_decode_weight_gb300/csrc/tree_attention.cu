@@ -683,6 +683,7 @@ tree_attention_kernel(const AttnParams p, const __grid_constant__ CUtensorMap km
   }
   tc_fence_before();
   __syncthreads();
+  if (threadIdx.x == 0 && *sm.dead) p.lost[blockIdx.x] = 1;
   if (warp == 1) {
     tc_fence_after();
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" :: "r"(tmem) : "memory");
@@ -703,6 +704,8 @@ __global__ void __launch_bounds__(128) join_kernel(const AttnParams p) {
   const Shares shares(total, blocks);
   if (shares.start(blockIdx.x) > cut.start) return;             // an earlier boundary is inside too
   const int c0 = blockIdx.x, parts = shares.owner(cut.start + cut.tiles - 1) - c0 + 1;
+  int lost = lane < parts ? p.lost[c0 + lane] : 0;              // (looked at when the sums are there)
+  for (int i = lane + 32; i < parts; i += 32) lost |= p.lost[c0 + i];
   for (int row = blockIdx.y * 4 + (threadIdx.x >> 5); row < cut.rows; row += 4 * gridDim.y) {
     // the item's first part is the last of its block's share, the others are the first of theirs
     auto slot = [&](int i) { return (size_t)(2 * (c0 + i) + (i == 0 ? 1 : 0)) * kTileRows + row; };
@@ -741,6 +744,7 @@ __global__ void __launch_bounds__(128) join_kernel(const AttnParams p) {
       }
     }
     l = warp_sum(l);
+    if (__any_sync(0xffffffffu, lost)) return;                  // a part is missing
     const int flat = cut.first + row, node = flat / p.group, head = cut.h * p.group + flat - node * p.group;
     const float norm = l == 0.f ? 0.f : (p.v_scale ? p.v_scale[cut.h] : 1.f) / l;
     T* dst = static_cast<T*>(p.out) + (int64_t)(cut.row0 + node) * p.ldo + (int64_t)head * D + lane * kPer;
@@ -783,13 +787,14 @@ bool encode_cache(CUtensorMap* map, const mdw_kv_cache* c, void* data, int most)
 }
 
 struct AttnWs {
-  size_t cuts, ml, o, total;
+  size_t cuts, lost, ml, o, total;
 };
 AttnWs attn_ws(int grid, int D) {
   AttnWs w;
   auto up = [](size_t v) { return (v + 255) / 256 * 256; };
   w.cuts = 256;
-  w.ml = w.cuts + up((size_t)grid * sizeof(Cut));
+  w.lost = w.cuts + up((size_t)grid * sizeof(Cut));
+  w.ml = w.lost + up((size_t)grid * 4);
   w.o = w.ml + up((size_t)grid * 2 * kTileRows * 8);
   w.total = w.o + up((size_t)grid * 2 * kTileRows * D * 4);
   return w;
@@ -871,7 +876,7 @@ extern "C" mdw_status mdw_tree_attention(const mdw_kv_cache* cache, int32_t B, i
   AttnParams p{cache->v, cache->page_stride, cache->k_scale, cache->v_scale, q, out, lse, ldq, ldo, block_table, ctx_len, row_start, tree_mask, status,
                      mdw_spin_budget(), scale, B, T, q_heads, cache->kv_heads, q_heads / cache->kv_heads, max_new, max_pages,
                      cache->num_pages, log2_of(cache->page_size), kItemCost, reinterpret_cast<int32_t*>(base),
-                     reinterpret_cast<Cut*>(base + lay.cuts), reinterpret_cast<float2*>(base + lay.ml),
+                     reinterpret_cast<Cut*>(base + lay.cuts), reinterpret_cast<int32_t*>(base + lay.lost), reinterpret_cast<float2*>(base + lay.ml),
                      reinterpret_cast<float*>(base + lay.o)};
   CUtensorMap km, vm;
   const int D = cache->head_dim, key_bytes = D * (fp8 ? 1 : 2);

@@ -36,6 +36,7 @@ struct AttnParams {
   // workspace
   int32_t* total;          // [2] tiles of the whole call, blocks with a share
   struct Cut* cuts;        // [grid] the item that a block's share starts inside of
+  int32_t* lost;           // [grid] whether a block gave up: what its part belongs to is not stored
   float2* part_ml;         // [2 * grid][128] (c m, sum) of partial items
   float* part_o;           // [2 * grid][128][D] their unnormalised outputs
 };
@@ -156,7 +157,10 @@ struct Walk {
     rb = item - h * r.blocks(p);
     Cut cut{};
     if (tile > 0 && tile < tiles) cut = Cut{r.row0, min(r.rows * p.group - rb * kTileRows, kTileRows), rb * kTileRows, h, at - tile, tiles};
-    if (threadIdx.x == 0) p.cuts[blockIdx.x] = cut;
+    if (threadIdx.x == 0) {
+      p.cuts[blockIdx.x] = cut;
+      p.lost[blockIdx.x] = 0;                   // (the same thread sets it when the block ends)
+    }
     if (tile >= tiles) {                        // the tiles before belong to the last share
       units -= whole - tile;
       if (units > 0) next_item(p, lane);

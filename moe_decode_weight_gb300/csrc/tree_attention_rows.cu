@@ -504,6 +504,7 @@ few_rows_kernel(const AttnParams p, const __grid_constant__ CUtensorMap kmap, co
     walk.done(p, lane);
     join_barrier();                                            // sums and outputs are read; the next item may write
   }
+  if (threadIdx.x == 0 && *dead) p.lost[blockIdx.x] = 1;
 }
 
 template <typename T, bool kE4M3, int D, int kBlocks>

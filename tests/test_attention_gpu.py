@@ -1012,3 +1012,25 @@ def test_attention_that_gives_up_reads_no_bad_page(hq, dtype, ctype, d):
             api.mdw_debug_set_spin_budget(0)
     c = Attn(73, [900, 90], [4, 3], hq, 2, d, 16, dtype, ctype)
     c.check(*c.call())
+
+
+@pytest.mark.parametrize("hq,dtype,ctype,d", PATHS + [(32, BF, BF, 128), (32, HF, HF, 64), (32, HF, E4, 128)])
+def test_attention_stores_nothing_of_items_with_a_lost_part(hq, dtype, ctype, d):
+    """Requests cut between blocks of which some give up: rows are right or left as they were, not joined from what
+    the workspace holds (finite sums here)."""
+    c = Attn(74, [40000, 500], [4, 2], hq, 2, d, 16, dtype, ctype)
+    want, want_lse = c.call()
+    nbytes = api.mdw_tree_attention_workspace_bytes(c.cache, 2, c.t, hq, 4)
+    flush = torch.empty(1 << 28, dtype=torch.int32, device="cuda")
+    for _ in range(4):
+        ws = torch.full((nbytes // 4,), 1.0, device="cuda").view(torch.uint8)
+        out, lse, status = torch.full_like(c.q, 5.0), torch.full(c.q.shape[:2], 5.0, device="cuda"), i32([0])
+        flush.zero_()                                # the cache leaves the L2: its first copies are waited for
+        api.mdw_debug_set_spin_budget(1)
+        try:
+            c.call(out=out, lse=lse, ws=ws, status=status)
+        finally:
+            api.mdw_debug_set_spin_budget(0)
+        assert status.item() == 6
+        kept = (out == 5).all(2) & (lse == 5)        # (blocks whose copies were always there in time have not given up)
+        assert torch.equal(out[~kept], want[~kept]) and torch.equal(lse[~kept], want_lse[~kept])
