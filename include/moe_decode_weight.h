@@ -364,7 +364,7 @@ typedef struct mdw_w4_weights {
   uint32_t magic;
   int32_t fmt;
   int32_t n;             /* output features, 1 .. 2^31 - 256 */
-  int32_t k;             /* input features, a multiple of group */
+  int32_t k;             /* input features, a multiple of group, up to 2^31 - 256 */
   int32_t group;         /* 32, 64 or 128 */
   int32_t dtype;         /* MDW_DT_BF16 or MDW_DT_F16: scale, x, bias and residual */
   const void* q;         /* uint8 [n][k/2]: byte k/2 holds the code 0..15 of k in its low nibble (k even)

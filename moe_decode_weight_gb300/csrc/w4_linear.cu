@@ -198,7 +198,7 @@ constexpr int kRowJoin = 10;
 constexpr int kRowMaxX = 36 * 1024;            // bytes of x that leave room for two blocks on an SM
 
 // Bytes of a token in shared memory, whole units; 64 more put two tokens' loads on different banks.
-__host__ __device__ inline int x_pitch(int K) { return (K + kRowUnit - 1) / kRowUnit * kRowUnit * 2 + 64; }
+__host__ __device__ constexpr int x_pitch(int K) { return (K + kRowUnit - 1) / kRowUnit * kRowUnit * 2 + 64; }
 
 template <typename T, int kGroup>
 __global__ void __launch_bounds__(32 * kRowWarps, 2)
@@ -401,9 +401,14 @@ cudaError_t launch_rows(const W4Params& p, int dev, cudaStream_t s) {
 
 // Up to 8 tokens whose elements leave two blocks a SM's shared memory: the rows' kernel (157184 features x 2560, one token: 43 us, on
 // tcgen05 51; 8 tokens x 2048: 38 and 43; 4000 features x 4096, 4 tokens: 7.8 and 7.9). 8 tokens x 2560 elements do not fit.
+constexpr bool fits_rows(int M, int64_t K) { return M <= 8 && K <= kRowMaxX / 2 && M * x_pitch((int)K) <= kRowMaxX; }
+// (a K that is compared as it is: tokens of 2^28 elements and more pass 32 bits in bytes)
+static_assert(fits_rows(1, 17920) && !fits_rows(1, 17952) && fits_rows(8, 2048) && !fits_rows(8, 2560));
+static_assert(!fits_rows(8, 1 << 28) && !fits_rows(4, 1 << 29) && !fits_rows(1, 1 << 30) && !fits_rows(2, 1 << 30) && !fits_rows(1, 0x7fffff00));
+
 template <typename T, int kGroup>
 cudaError_t launch(const W4Params& p, int dev, cudaStream_t s) {
-  if (p.M <= 8 && p.M * x_pitch(p.K) <= kRowMaxX) return launch_rows<T, kGroup>(p, dev, s);
+  if (fits_rows(p.M, p.K)) return launch_rows<T, kGroup>(p, dev, s);
   CUtensorMap map;
   if (!encode_codes(&map, p, kTensorRows)) return cudaErrorInvalidValue;
   return launch_w4_tensor(p, map, std::is_same<T, __nv_bfloat16>::value, kGroup, dev, s);
@@ -425,7 +430,8 @@ extern "C" mdw_status w4_linear(const mdw_w4_weights* w, int32_t M, const void* 
   if (w->magic != MDW_MAGIC || w->fmt != MDW_FMT_INT4_GROUP) return MDW_ERR_FORMAT_MISMATCH;
   if (w->dtype != MDW_DT_BF16 && w->dtype != MDW_DT_F16) return MDW_ERR_FORMAT_MISMATCH;
   if (w->group != 32 && w->group != 64 && w->group != 128) return MDW_ERR_UNSUPPORTED_SHAPE;
-  if (w->n < 1 || w->n > 0x7fffff00 || w->k < w->group || w->k % w->group != 0) return MDW_ERR_UNSUPPORTED_SHAPE;   // (rows of a tile past n are int32)
+  // (rows of a tile past n are int32, and so are elements of a unit past k)
+  if (w->n < 1 || w->n > 0x7fffff00 || w->k < w->group || w->k > 0x7fffff00 || w->k % w->group != 0) return MDW_ERR_UNSUPPORTED_SHAPE;
   if (M < 1 || M > MDW_MAX_M) return MDW_ERR_INVALID_ARG;
   if (!aligned_to(w->q, 16) || !aligned_to(w->scale, 16) || !null_or_aligned(w->zero, 16) || !aligned_to(x, 16) || !row_stride_ok(ldx, w->k))
     return MDW_ERR_INVALID_ARG;

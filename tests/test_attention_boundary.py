@@ -107,3 +107,10 @@ def test_binding_refuses_host_tensors():
 @pytest.mark.parametrize("n", [(1 << 31) - 255, (1 << 31) - 1])
 def test_w4_rejects_features_whose_tiles_pass_int32(n):
     assert api.lib().w4_linear(_w4(n=n, k=128), 1, FAKE, 128, FAKE, n, BF, None, None, 0, None, None) == 2
+
+
+@pytest.mark.parametrize("m", [1, 8])
+@pytest.mark.parametrize("k", [(1 << 31) - 128, (1 << 31) - 224])
+def test_w4_rejects_elements_whose_units_pass_int32(m, k):
+    k = k // 32 * 32
+    assert api.lib().w4_linear(_w4(n=1, k=k, group=32), m, FAKE, k, FAKE, 1, BF, None, None, 0, None, None) == 2
