@@ -455,10 +455,11 @@ size_t mdw_tree_attention_workspace_bytes(const mdw_kv_cache* cache, int32_t B, 
  * Scores, softmax sums and outputs are fp32; probabilities enter the second product in q's type
  * (f16 for E4M3 caches).
  * q_dtype is MDW_DT_BF16 / MDW_DT_F16 and the cache's own type, or any of the two for an E4M3
- * cache. scale > 0, finite. Every request has at most max_new (1..MDW_MAX_TREE) rows. Rows before
- * row_start[0] or from row_start[B] on are left as they were. A request with bad lengths or rows
- * (outside [0, T), more than max_new, beyond max_pages * page_size) is skipped, keys on a page id
- * outside [0, num_pages) are not seen; both set MDW_ERR_DEVICE_BOUNDS.
+ * cache. scale > 0, finite. max_pages * page_size is at most 2^31 - 65536. Every request has at
+ * most max_new (1..MDW_MAX_TREE) rows. Rows before row_start[0] or from row_start[B] on are left as
+ * they were. A request with bad lengths or rows (outside [0, T), more than max_new, beyond
+ * max_pages * page_size) is skipped, keys on a page id outside [0, num_pages) are not seen; both
+ * set MDW_ERR_DEVICE_BOUNDS.
  * ws: workspace, contents arbitrary; not to be shared by calls that may overlap. */
 mdw_status mdw_tree_attention(const mdw_kv_cache* cache, int32_t B, int32_t T, int32_t q_heads, int32_t max_new,
                               const void* q, int64_t ldq, int32_t q_dtype, void* out, int64_t ldo, float* lse,

@@ -861,7 +861,7 @@ extern "C" mdw_status mdw_tree_attention(const mdw_kv_cache* cache, int32_t B, i
   const bool fp8 = cache->dtype == MDW_DT_E4M3;
   if (!fp8 && q_dtype != cache->dtype) return MDW_ERR_FORMAT_MISMATCH;
   if (!sizes_ok(cache, B, T, q_heads, max_new)) return MDW_ERR_INVALID_ARG;
-  if (max_pages < 1 || (int64_t)max_pages * cache->page_size > 0x7fffffffLL) return MDW_ERR_UNSUPPORTED_SHAPE;
+  if (max_pages < 1 || (int64_t)max_pages * cache->page_size > 0x7fff0000LL) return MDW_ERR_UNSUPPORTED_SHAPE;   // (keys of a tile past the last are int32)
   const int64_t width = (int64_t)q_heads * cache->head_dim;
   if (!aligned_to(q, 16) || !row_stride_ok(ldq, width) || !aligned_to(out, 16) || !row_stride_ok(ldo, width) ||
       !null_or_aligned(lse, 4) || !aligned_to(block_table, 4) || !aligned_to(ctx_len, 4) ||

@@ -114,3 +114,10 @@ def test_w4_rejects_features_whose_tiles_pass_int32(n):
 def test_w4_rejects_elements_whose_units_pass_int32(m, k):
     k = k // 32 * 32
     assert api.lib().w4_linear(_w4(n=1, k=k, group=32), m, FAKE, k, FAKE, 1, BF, None, None, 0, None, None) == 2
+
+
+@pytest.mark.parametrize("page,width", [(16, (1 << 27) - 1), (256, (1 << 23) - 1), (256, (1 << 23) - 255)])
+def test_attention_rejects_tables_whose_tiles_pass_int32(page, width):
+    c = _cache(page_size=page, page_stride=4 * page * 128)
+    assert api.lib().mdw_tree_attention(c, 1, 4, 8, 4, FAKE, 1024, BF, FAKE, 1024, None, FAKE, width, FAKE, FAKE, None, 0.1, None,
+                                        FAKE, 1 << 40, None) == 2
