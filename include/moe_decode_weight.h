@@ -452,6 +452,8 @@ size_t mdw_tree_attention_workspace_bytes(const mdw_kv_cache* cache, int32_t B, 
  *   lse[row][h] = log sum_j exp(scale * q . k_j)          (fp32 [T][q_heads], or NULL)
  * over the keys the row sees. Keys it does not see contribute nothing, whatever they hold
  * (NaN and infinities too); a row that sees none, or only scores of -inf, gives 0 and -inf.
+ * A value that is not finite counts in every row that sees its key, also where the rounded
+ * probability is 0: +-inf, or NaN where one is NaN or both infinities meet.
  * Scores, softmax sums and outputs are fp32; probabilities enter the second product in q's type
  * (f16 for E4M3 caches).
  * q_dtype is MDW_DT_BF16 / MDW_DT_F16 and the cache's own type, or any of the two for an E4M3

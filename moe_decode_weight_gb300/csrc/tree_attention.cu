@@ -620,6 +620,7 @@ tree_attention_kernel(const AttnParams p, const __grid_constant__ CUtensorMap km
         fb *= f;
       }
       const int slot = 2 * blockIdx.x + (tile0 > 0 ? 0 : 1);
+      bool nan = false;
 #pragma unroll 1
       for (int i = s * kHalf; i < (s + 1) * kHalf; i += kPiece) {
         float o[kPiece];
@@ -652,6 +653,9 @@ tree_attention_kernel(const AttnParams p, const __grid_constant__ CUtensorMap km
           asm volatile("bar.sync 1, 256;" ::: "memory");
         }
         if (at_lane < per && w.valid && !*sm.dead) {
+          if constexpr (!kE4M3)
+#pragma unroll
+            for (int e = 0; e < kPiece; ++e) nan |= isnan(o[e]);
           if (whole) {
             T* dst = static_cast<T*>(p.out) + (int64_t)w.row * p.ldo + (int64_t)w.head * D + i;
 #pragma unroll
@@ -668,6 +672,11 @@ tree_attention_kernel(const AttnParams p, const __grid_constant__ CUtensorMap km
           }
         }
         __syncwarp();
+      }
+      if (nan && isfinite(sum)) {
+        const int i = s * kHalf;
+        mend_columns<T>(p, whole ? static_cast<T*>(p.out) + (int64_t)w.row * p.ldo + (int64_t)w.head * D + i : nullptr,
+                        p.part_o + ((size_t)slot * kTileRows + mine) * D + i, i, kHalf, walk, w.bits, D);
       }
       if (s == 0 && at_lane < per && w.valid && !*sm.dead) {
         if (!whole) p.part_ml[(size_t)slot * kTileRows + mine] = make_float2(m, sum);

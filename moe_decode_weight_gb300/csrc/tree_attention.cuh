@@ -244,6 +244,50 @@ __device__ __forceinline__ uint32_t visible32(uint64_t bits, int key, int ctx) {
   return -ahead < 64 ? (uint32_t)(bits >> -ahead) : 0u;
 }
 
+// Values that are not finite. A product with a probability of zero makes NaN of an infinite value: one that f16 rounds to zero, one that
+// exp2 does, the zeros of the keys of other copies. The sum of such values with positive weights is the infinity, or NaN if one of them is
+// NaN or both infinities occur: the columns that came out as NaN in a thread's results (stored in out or part, from `column` on) are
+// looked up in the keys [key, end) that the row sees. v: the head's values of page 0. Rare, and so after everything else: finite caches
+// cost a comparison per output.
+template <typename T>
+static __device__ __noinline__ void mend_columns(T* out, float* part, int column, int columns, const uint16_t* v, int64_t page_stride, const int32_t* table,
+                                                 int page_shift, int num_pages, int width, int ctx, uint64_t bits, int first, int end) {
+  constexpr uint32_t kExponent = Mma<T>::kExponent & 0xffffu;
+  for (int i = 0; i < columns; i += 4) {
+    bool odd = false;
+    for (int j = i; j < i + 4; ++j) odd |= isnan(out ? Elem<T>::to_float(out[j]) : part[j]);
+    if (!odd) continue;
+    uint32_t found = 0;                                         // which of the four hold +inf (bits 0-3), -inf (bits 4-7); NaN is both
+#pragma unroll 4
+    for (int key = first; key < end; ++key) {
+      const bool sees = key < ctx || bits >> (key - ctx) & 1;
+      const int page = table[key >> page_shift];
+      if (!sees || page < 0 || page >= num_pages) continue;
+      const uint2 x = *reinterpret_cast<const uint2*>(v + page * page_stride + (int64_t)(key & ((1 << page_shift) - 1)) * width + column + i);
+      const uint32_t e[4] = {x.x & 0xffffu, x.x >> 16, x.y & 0xffffu, x.y >> 16};
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        if ((e[j] & kExponent) != kExponent) continue;
+        const bool nan = (e[j] & 0x7fffu) != kExponent;
+        if (nan || !(e[j] >> 15)) found |= 1u << j;
+        if (nan || e[j] >> 15) found |= 16u << j;
+      }
+    }
+    for (int j = 0; j < 4; ++j) {
+      if ((found >> j & 1) == (found >> (4 + j) & 1)) continue;
+      const float x = found >> j & 1 ? INFINITY : -INFINITY;
+      if (out) out[i + j] = Elem<T>::from_float(x);
+      else part[i + j] = x;
+    }
+  }
+}
+template <typename T>
+__device__ __forceinline__ void mend_columns(const AttnParams& p, T* out, float* part, int column, int columns, const Walk& w, uint64_t bits, int width) {
+  mend_columns<T>(out, part, column, columns, static_cast<const uint16_t*>(p.v) + ((int64_t)w.h << p.page_shift) * width, p.page_stride,
+                  p.block_table + (size_t)w.b * p.max_pages, p.page_shift, p.num_pages, width, w.r.ctx, bits, w.tile * kTileKeys,
+                  min(w.r.keys, (w.tile + w.count()) * kTileKeys));
+}
+
 // Up to kFewRows rows a request and kv head: the kernel of tree_attention_rows.cu. A stage of its copies, and so a box
 // of them, has kFewBytes of keys at most.
 constexpr int kFewRows = 32, kFewBytes = 4096;

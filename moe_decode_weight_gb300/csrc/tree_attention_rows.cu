@@ -499,6 +499,17 @@ few_rows_kernel(const AttnParams p, const __grid_constant__ CUtensorMap kmap, co
           for (int j = 0; j < kCols; j += 4) *reinterpret_cast<float4*>(p.part_o + part * D + d + j) = make_float4(v[j], v[j + 1], v[j + 2], v[j + 3]);
           if (d == 0) p.part_ml[part] = make_float2(m, sum);
         }
+        if constexpr (!kE4M3) {
+          bool nan = false;
+#pragma unroll
+          for (int j = 0; j < kCols; ++j) nan |= isnan(v[j]);
+          if (nan && isfinite(sum)) {
+            const int head = h * p.group + row - node * p.group;
+            mend_columns<T>(p, whole ? static_cast<T*>(p.out) + (int64_t)(r.row0 + node) * p.ldo + (int64_t)head * D + d : nullptr,
+                            p.part_o + ((size_t)(2 * blockIdx.x + (tile0 > 0 ? 0 : 1)) * kTileRows + row) * D + d, d, kCols, walk,
+                            (p.tree_mask ? p.tree_mask[r.row0 + node] : ~0ull >> (63 - node)) & ((1ull << r.rows) - 1), D);
+          }
+        }
       }
     }
     walk.done(p, lane);

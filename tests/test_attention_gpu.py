@@ -1034,3 +1034,46 @@ def test_attention_stores_nothing_of_items_with_a_lost_part(hq, dtype, ctype, d)
         assert status.item() == 6
         kept = (out == 5).all(2) & (lse == 5)        # (blocks whose copies were always there in time have not given up)
         assert torch.equal(out[~kept], want[~kept]) and torch.equal(lse[~kept], want_lse[~kept])
+
+
+# ---- values that are not finite and are seen: the infinity, or NaN where one is NaN or both infinities meet
+SEEN = [(hq, dtype, d) for hq in (2, 8, 16, 24, 32, 64) for dtype, d in ((BF, 128), (HF, 128), (BF, 64), (HF, 64))]   # 4 to 128 rows
+
+
+@pytest.mark.parametrize("hq,dtype,d", SEEN)
+@pytest.mark.parametrize("ctx", [[300, 1029, 130], [20000, 5, 130]])
+def test_attention_gives_the_infinities_that_a_row_sees(hq, dtype, d, ctx):
+    c = Attn(80, ctx, [4, 3, 4], hq, 2, d, 16, dtype, dtype)
+    clean, clean_lse = c.call()
+    c.check(clean, clean_lse)
+    inf = float("inf")
+
+    def put(b, key, column, value):
+        c.cache.v[int(c.table[b, key // 16]), :, key % 16, column::5] = value
+
+    # request 0: in full tiles of the context, far from and near its end; request 2: in a node and in the partial tile
+    first, second = 37, ctx[0] - 180
+    put(0, first, 0, inf), put(0, second, 1, -inf), put(0, first, 2, inf), put(0, second, 2, -inf), put(0, second, 3, float("nan"))
+    put(2, ctx[2] + 1, 0, inf), put(2, ctx[2] - 1, 1, -inf)
+    out, lse = c.call()
+    assert torch.equal(lse, clean_lse)
+    assert (out[:4, :, 0::5] == inf).all() and (out[:4, :, 1::5] == -inf).all()
+    assert torch.isnan(out[:4, :, 2::5]).all() and torch.isnan(out[:4, :, 3::5]).all() and torch.equal(out[:4, :, 4::5], clean[:4, :, 4::5])
+    assert torch.equal(out[4:7], clean[4:7])
+    sees = torch.tensor(c.seen[2][:, 1], device="cuda")
+    assert (out[7:][sees][:, :, 0::5] == inf).all() and torch.equal(out[7:][~sees][:, :, 0::5], clean[7:][~sees][:, :, 0::5])
+    assert (out[7:, :, 1::5] == -inf).all() and all(torch.equal(out[7:, :, i::5], clean[7:, :, i::5]) for i in (2, 3, 4))
+
+
+@pytest.mark.parametrize("hq,dtype,d", SEEN)
+def test_attention_gives_an_infinity_of_small_probability(hq, dtype, d):
+    """e^-30 of the largest: f16 rounds such a probability to zero, fp32 does not."""
+    c = Attn(81, [700], [4], hq, 2, d, 16, dtype, dtype)
+    c.cache.k.zero_(), c.q.fill_(1.0)
+    page, at = int(c.table[0, 203 // 16]), 203 % 16
+    c.cache.k[page, :, at] = -30.0 / (c.scale * d)
+    clean, _ = c.call()
+    c.cache.v[page, :, at, ::3] = float("inf")
+    out, lse = c.call()
+    assert (out[:, :, ::3] == float("inf")).all() and torch.isfinite(lse).all()
+    assert torch.equal(out[:, :, 1::3], clean[:, :, 1::3])
