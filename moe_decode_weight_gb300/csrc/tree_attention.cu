@@ -462,7 +462,7 @@ tree_attention_kernel(const AttnParams p, const __grid_constant__ CUtensorMap km
                              M::pack(Elem<T>::to_float(x[4]) * f, Elem<T>::to_float(x[5]) * f), M::pack(Elem<T>::to_float(x[6]) * f, Elem<T>::to_float(x[7]) * f));
               sts16(S::operand(rows_at, at, i), v);
             }
-            sm.row_c[items % 3 * kTileRows + at] = c;
+            sm.row_c[items % 3 * kTileRows + at] = positive(c);
           }
         }
         fence_async_proxy();

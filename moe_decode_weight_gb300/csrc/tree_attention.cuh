@@ -208,6 +208,10 @@ __device__ __forceinline__ float exp2_fast(float x) {
   return y;
 }
 
+// c of a row over an E4M3 cache, which holds the scales of the keys and of the row's elements: where it falls below fp32 it stays
+// positive, for a key that a row does not see is one with a score of -inf times c.
+__device__ __forceinline__ float positive(float c) { return c == 0.f ? 1.401298464e-45f : c; }
+
 // Types of the two matrix products: the query's own, f16 over an E4M3 cache (exact for its values).
 template <typename T> struct Mma;
 template <> struct Mma<__nv_bfloat16> {

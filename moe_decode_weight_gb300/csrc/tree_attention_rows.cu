@@ -238,6 +238,7 @@ few_rows_kernel(const AttnParams p, const __grid_constant__ CUtensorMap kmap, co
 #pragma unroll
           for (int j = i; j < 4; j += 2) qf[st][j] = M::pack(low(qf[st][j]) * f, high(qf[st][j]) * f);
       }
+      if constexpr (kE4M3) c[i] = positive(c[i]);
     }
     float o[kOut][4], mc[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
 #pragma unroll

@@ -1077,3 +1077,14 @@ def test_attention_gives_an_infinity_of_small_probability(hq, dtype, d):
     out, lse = c.call()
     assert (out[:, :, ::3] == float("inf")).all() and torch.isfinite(lse).all()
     assert torch.equal(out[:, :, 1::3], clean[:, :, 1::3])
+
+
+@pytest.mark.parametrize("hq,dtype,ctype,d", [x for x in PATHS if x[2] == E4] + [(32, BF, E4, 128)])
+@pytest.mark.parametrize("k_scale", [1e-45, 1e-38])
+def test_attention_with_scales_below_fp32(hq, dtype, ctype, d, k_scale):
+    """Keys whose scale times the softmax's is 0 in fp32 have equal scores; keys that a row does not see stay out."""
+    c = Attn(82, [300, 0, 20], [4, 3, 4], hq, 2, d, 16, dtype, ctype, masks="random")
+    c.cache.k_scale.fill_(k_scale)
+    c.check(*c.call())
+    c.q *= 2.0 ** -14                                # (bf16 rows enter f16 times a power of two)
+    c.check(*c.call())
