@@ -370,7 +370,8 @@ typedef struct mdw_w4_weights {
   const void* q;         /* uint8 [n][k/2]: byte k/2 holds the code 0..15 of k in its low nibble (k even)
                             or high nibble (k odd) */
   const void* scale;     /* [n][k/group] in dtype */
-  const void* zero;      /* uint8 [n][k/group] zero codes 0..15, or NULL: 8 everywhere */
+  const void* zero;      /* uint8 [n][k/group], any value (16 too, as weights converted from "zero - 1" have), or
+                            NULL: 8 everywhere */
 } mdw_w4_weights;
 
 /* y[t][n] = sum_k x[t][k] * (code[n][k] - zero[n][k/group]) * scale[n][k/group]

@@ -62,8 +62,8 @@ template <> struct Int4<__half> {
   // down by one exact multiply-add: (1024 + 16 code) / 16 - (64 + zero)
   static __device__ __forceinline__ uint32_t zero2(uint32_t z) { return (0x6400u + z) * 0x00010001u; }
   static __device__ __forceinline__ void expand(uint32_t w, uint32_t z2, uint32_t (&p)[4]) {
-    // -(64 + zero) in f16: 0xd400 is -64, whose unit in the last place is 1 / 16
-    const uint32_t nz = 0xd400d400u + ((z2 & 0x000f000fu) << 4);
+    uint32_t nz;                                                // 960 - (1024 + zero) = -(64 + zero), exactly
+    asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(nz) : "r"(0x63806380u), "r"(z2));
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       const uint32_t v = w >> (8 * i), lo = and_or(v, 0x000f000fu, 0x64006400u), hi = and_or(v, 0x00f000f0u, 0x64006400u);

@@ -58,7 +58,12 @@ template <> struct Neighbours<__nv_bfloat16> {
   static __device__ __forceinline__ uint32_t expand(uint32_t two, uint32_t z) { return Int4<__nv_bfloat16>::fma2(two & 0x00f0000fu, 0x7d007f00u, z); }
 };
 template <> struct Neighbours<__half> {
-  static __device__ __forceinline__ uint32_t zero(uint32_t z) { return 0xd400e400u + z * 0x00100001u; }            // -(64 + z), -(1024 + z)
+  // -(64 + z), -(1024 + z): (960, 0) - (1024 + z), exactly
+  static __device__ __forceinline__ uint32_t zero(uint32_t z) {
+    uint32_t r;
+    asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(0x63800000u), "r"(0x64006400u + z * 0x00010001u));
+    return r;
+  }
   static __device__ __forceinline__ uint32_t expand(uint32_t two, uint32_t z) {
     uint32_t r;
     asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(r) : "r"(and_or(two, 0x00f0000fu, 0x64006400u)), "r"(0x2c003c00u), "r"(z));

@@ -1088,3 +1088,22 @@ def test_attention_with_scales_below_fp32(hq, dtype, ctype, d, k_scale):
     c.check(*c.call())
     c.q *= 2.0 ** -14                                # (bf16 rows enter f16 times a power of two)
     c.check(*c.call())
+
+
+@pytest.mark.parametrize("m,n,k,group,dtype", [(m, 1000, 2048, g, t) for m in (1, 8, 9, 32) for g in (32, 64, 128) for t in (BF, HF)])
+def test_w4_linear_takes_every_zero(m, n, k, group, dtype):
+    """Zeros of 0 to 255, not those of a code alone, in every kernel; bit for bit with x of one element at a time, for
+    which nothing is rounded."""
+    w = w4_case(83 + m, n, k, group, False, dtype)
+    w = api.W4Weights(w.q, w.scale, torch.arange(n * (k // group), device="cuda").remainder(256).to(torch.uint8).view(n, -1))
+    x = torch.randn((m, k), generator=gen(m), device="cuda").to(dtype)
+    y = torch.empty((m, n), dtype=F32, device="cuda")
+    api.w4_linear(w, x, y)
+    want, tol = w4_want(w, x)
+    assert_close(host(y), want, tol + half_step(F32) * np.abs(want))
+    weight = OA.w4_weight(w.q.cpu().numpy(), host(w.scale), w.zero.cpu().numpy(), group)
+    for first in (0, 77, k - m):
+        x.zero_()
+        x[torch.arange(m), torch.arange(first, first + m)] = 1.0
+        api.w4_linear(w, x, y)
+        assert np.array_equal(host(y), weight[:, first:first + m].T)
