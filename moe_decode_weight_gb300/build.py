@@ -12,6 +12,7 @@ import shutil
 import subprocess
 import sys
 import sysconfig
+import warnings
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -46,8 +47,17 @@ def _compile(src: str, trace: bool = False) -> str:
 
 
 def _binding() -> None:
+    """The extension is not needed for the C library or the decode step's calls: without a C compiler or
+    Python's headers a warning says so, and the calls that want it raise."""
     tmp = BINDING + ".tmp"
-    cmd = [shutil.which("gcc") or "cc", "-O2", "-std=c11", "-Wall", "-shared", "-fPIC", "-I" + sysconfig.get_paths()["include"],
+    cc, headers = shutil.which("gcc") or shutil.which("cc"), sysconfig.get_paths()["include"]
+    if cc is None or not os.path.exists(os.path.join(headers, "Python.h")):
+        if os.path.exists(BINDING):
+            os.remove(BINDING)                        # an earlier build's may not match the library
+        warnings.warn(f"no C compiler or no Python.h in {headers}: {os.path.basename(BINDING)} is not built, "
+                      "and the attention sub-layer's calls from Python are not available")
+        return
+    cmd = [cc, "-O2", "-std=c11", "-Wall", "-shared", "-fPIC", "-I" + headers,
            "-I" + INCLUDE, os.path.join(CSRC, "binding.c"), "-o", tmp, "-lm"]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
@@ -62,8 +72,6 @@ def build(verbose: bool = False, trace: bool = False) -> str:
     os.makedirs(BUILD, exist_ok=True)
     with cf.ThreadPoolExecutor(max_workers=len(SOURCES)) as ex:
         objs = list(ex.map(lambda src: _compile(src, trace), SOURCES))
-    if not trace:
-        _binding()
     out = TRACE_LIB if trace else LIB
     tmp = out + ".tmp"
     cmd = [nvcc(), *ARCH, "-shared", "-o", tmp, *objs, "-cudart", "static"]
@@ -71,6 +79,8 @@ def build(verbose: bool = False, trace: bool = False) -> str:
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, out)
+    if not trace:
+        _binding()
     if verbose:
         print(f"built {out}")
     return out
