@@ -1107,3 +1107,25 @@ def test_w4_linear_takes_every_zero(m, n, k, group, dtype):
         x[torch.arange(m), torch.arange(first, first + m)] = 1.0
         api.w4_linear(w, x, y)
         assert np.array_equal(host(y), weight[:, first:first + m].T)
+
+
+@pytest.mark.parametrize("m", [1, 8, 9, 32])
+@pytest.mark.parametrize("group", [32, 128])
+def test_w4_linear_products_are_exact_at_the_ends_of_bf16(m, group):
+    """Elements of 2^-100 and scales just below 2^121: one element a token, so that the scale's product alone is rounded."""
+    n, k = 500, 1024
+    w = w4_case(84, n, k, group, True, BF)
+    top = 2.0 ** 120 * (1 + 127 / 128)
+    w.scale.copy_(torch.where(torch.rand(w.scale.shape, generator=gen(1), device="cuda") < 0.5, top, 1.0).to(BF))
+    x = torch.zeros((m, k), dtype=BF, device="cuda")
+    at = torch.randint(0, k, (m,), generator=gen(2), device="cuda")
+    x[torch.arange(m, device="cuda"), at] = (2.0 ** -100 * (1 + torch.randint(0, 128, (m,), generator=gen(3), device="cuda") / 128)).to(BF)
+    y = torch.empty((m, n), dtype=F32, device="cuda")
+    api.w4_linear(w, x, y)
+    want, _ = w4_want(w, x)
+    assert_close(host(y), want, half_step(F32) * np.abs(want))
+    x *= 2.0 ** 100
+    w.scale.fill_(2.0 ** -100)
+    api.w4_linear(w, x, y)
+    want, _ = w4_want(w, x)
+    assert_close(host(y), want, half_step(F32) * np.abs(want))
