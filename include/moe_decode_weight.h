@@ -395,10 +395,10 @@ typedef struct mdw_kv_cache {
   int32_t dtype;         /* MDW_DT_BF16, MDW_DT_F16 or MDW_DT_E4M3 */
   int32_t num_pages;     /* >= 1 */
   int32_t page_size;     /* 16, 32, 64, 128 or 256 tokens */
-  int32_t kv_heads;      /* >= 1 */
+  int32_t kv_heads;      /* 1 .. 1024 */
   int32_t head_dim;      /* 64 or 128 */
   int32_t reserved;
-  int64_t page_stride;   /* elements, >= kv_heads * page_size * head_dim, 16-byte multiple */
+  int64_t page_stride;   /* elements, kv_heads * page_size * head_dim .. 2^32, 16-byte multiple */
   void* k;
   void* v;
   const float* k_scale;  /* device fp32 [kv_heads] > 0 (E4M3 caches), else NULL */
@@ -456,7 +456,9 @@ size_t mdw_tree_attention_workspace_bytes(const mdw_kv_cache* cache, int32_t B, 
  * A value that is not finite counts in every row that sees its key, also where the rounded
  * probability is 0: +-inf, or NaN where one is NaN or both infinities meet.
  * Scores, softmax sums and outputs are fp32; probabilities enter the second product in q's type
- * (f16 for E4M3 caches).
+ * (f16 for E4M3 caches). Over an E4M3 cache the elements of a bf16 row enter the first product in
+ * f16, off by at most 2^-25 of the row's largest. The order of the sums, and so the last bits,
+ * depends on the lengths and on the call's sizes (max_new and max_pages among them), not on timing.
  * q_dtype is MDW_DT_BF16 / MDW_DT_F16 and the cache's own type, or any of the two for an E4M3
  * cache. scale > 0, finite. max_pages * page_size is at most 2^31 - 65536. Every request has at
  * most max_new (1..MDW_MAX_TREE) rows. Rows before row_start[0] or from row_start[B] on are left as

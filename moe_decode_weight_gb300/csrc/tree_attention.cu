@@ -4,7 +4,10 @@
 //   o = sum_j 2^(c z_j - c m) v_j / sum_j 2^(c z_j - c m),   lse = ln2 (c m + log2 sum_j 2^(c z_j - c m)),
 // for any m; a running maximum keeps the exponents below 0. Partial results (c m, sum, weighted
 // values) over disjoint key sets join by rescaling to the larger c m, so the keys of a row can be
-// split over warps and blocks and joined in a fixed order.
+// split over warps and blocks and joined in a fixed order. Scores, sums and outputs are fp32. The probabilities
+// are rounded to 16 bits for the second product, since an instruction multiplies operands of one type
+// and a second product for the rest would double its work: outputs are off by 0.0022 of their norm instead of 0.0017, which is
+// their own rounding to bf16 (4-token window; f16, 64-node trees: 0.00029 instead of 0.00021).
 //
 // Split. The query heads of one kv head and the nodes of one tree are the rows of one tile (node major,
 // up to 128 rows), so a key is read from memory once for all of them. The work is the list of
@@ -439,7 +442,8 @@ tree_attention_kernel(const AttnParams p, const __grid_constant__ CUtensorMap km
           } else {
             float f = 1.f, c = p.scale * kLog2e * p.k_scale[h];
             if constexpr (std::is_same<T, __nv_bfloat16>::value) {
-              // bf16 rows enter f16 times a power of two that puts their largest element in [1, 4)
+              // bf16 rows enter f16, the type of the converted keys, times a power of two that puts their largest element in [1, 4):
+              // elements below 2^-17 of it are off by up to 2^-25 of it, far below the fp32 sums' own error
               float top = 0.f;
 #pragma unroll 8
               for (int i = 0; i < D / 8; ++i) {
@@ -770,8 +774,11 @@ __global__ void __launch_bounds__(128) join_kernel(const AttnParams p) {
 
 // Which kernel. Up to 16 rows: few_rows_kernel (one token over 131k E4M3 keys 51 us, the other kernel 86; 1,500 16-bit keys
 // 10.4 and 14.7; 131k 16-bit keys 90 and 88). Up to 32 rows, of which two warps share the copies: the same over E4M3 caches
-// and heads of 64 (batches of trees 72 and 79 us, 51 and 64, 51 and 59), over a 16-bit cache with heads of 128 where
-// the block table leaves room for two tiles a block at most (1,500 keys 11.5 and 14.9 us, but a batch of trees 88 and 77).
+// and heads of 64 (batches of trees 72 and 79 us, 51 and 64, 51 and 59). Over a 16-bit cache with heads of 128 neither is always the
+// faster one: a window of 20 rows over 1,500 keys takes 11.5 and 14.8 us, over 9,600 keys (two tiles a block) 17.8 and
+// 18.2, over 40,000 31.5 and 29.5, a batch of trees 88 and 77. The lengths are on the device, so the choice goes by what the
+// block table has room for, two tiles a block: a short window with a table of 32k tokens takes the slower kernel, and its
+// last bits follow the table's width.
 bool few_rows(const AttnParams& p, int key_bytes, int grid) {
   const int rows = p.max_new * p.group;
   if (rows <= 16) return true;

@@ -1,6 +1,6 @@
 // What the two kernels of mdw_tree_attention share: the call's parameters, the cut of its work into shares, types
 // and small steps. tree_attention.cu has the kernel for many rows, the join and the entry points,
-// tree_attention_rows.cu the kernel for up to 16 rows.
+// tree_attention_rows.cu the kernel for up to 32 rows.
 #pragma once
 
 #include <cuda.h>

@@ -378,7 +378,9 @@ cudaError_t launch_rows(const W4Params& p, int dev, cudaStream_t s) {
   a.val.clusterDim.y = a.val.clusterDim.z = 1;
   cfg.attrs = &a;
   // Blocks to a cluster: the fewest units in a block's share, a join of a cluster counted as kRowJoin of them (one token, 10007
-  // features: 16384 elements 32.9 us in clusters, 41.6 without; 5120 elements 13.0 and 12.0).
+  // features: 16384 elements 32.9 us in clusters, 41.6 without; 5120 elements 13.0 and 12.0). Only where there are more tiles than
+  // blocks: with fewer, each tile's block brings in the token for itself, which more blocks repeat (1000 features x 16384: 12.8 us in
+  // clusters, 9.2 without; x 5120 5.6 and 5.7; 2560 x 16384 13.9 and 13.3).
   int blocks = 1, many = tiles < most ? tiles : most, best = (tiles + many - 1) / many * units;
   for (int n = 2; n <= kMostCluster && tiles > most; n *= 2) {
     a.val.clusterDim.x = n;
