@@ -211,7 +211,7 @@ __device__ __forceinline__ uint2 to_e4m3(uint4 x, float s) {
 
 // A block takes `rows` rows; a thread moves 8 elements of the keys and of the values at a time, two such pairs in
 // flight. Neighbouring threads read and write neighbouring pieces; a head's row is the unit of the cache
-// that stays whole (64 to 256 bytes). 16381 rows of 8 heads of 128, 16-bit: 22.1 us, 6.1 TB/s; to E4M3: 21.9 us, 4.6 TB/s
+// that stays whole (64 to 256 bytes). 16381 rows of 8 heads of 128, 16-bit: 22.1 us, 6.1 TB/s; to E4M3: 22.3 us, 4.5 TB/s
 // (six blocks an SM; five 22.9, eight 24.0: their registers no longer hold two pairs).
 template <typename T, bool kE4M3>
 __global__ void __launch_bounds__(256, 6) kv_write_kernel(const WriteParams p) {
@@ -272,7 +272,7 @@ extern "C" mdw_status mdw_kv_plan(int32_t B, const int32_t* ctx_len, const int32
     return MDW_ERR_INVALID_ARG;
   PlanParams p{ctx_len, new_len, block_table, free_pages, parents, row_start, slot_map, positions, tree_mask,
                pages_taken, status, B, T, num_pages, max_pages, num_free, log2_of(page_size)};
-  // four blocks an SM: more repeat the prefix sums, fewer have too few stores on their way (199 prompts with 390k rows 5.9 us; 8:
+  // four blocks an SM: more repeat the prefix sums, fewer have too few stores on their way (199 prompts with 390k rows 6.1 us; 8:
   // 7.3, 3: 6.3, 2: 7.7)
   const int dev = current_device(), most = 4 * sm_count(dev);
   if (most <= 0) return MDW_ERR_CUDA;

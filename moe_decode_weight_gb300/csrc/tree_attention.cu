@@ -26,8 +26,8 @@
 // Requests of up to 32 rows a kv head have a kernel of their own (tree_attention_rows.cu; few_rows() below chooses).
 //
 // What bounds it is the stream of keys and values up to 64 rows a block (16 ragged trees of up to 16 nodes x 4 heads, 12k
-// keys: 79 us, 5.2 TB/s), and the exponentials above (64-node trees of 8 heads: 46 us; a tile of 128 rows
-// takes a stream some 5,000 cycles, most of them exponentials). 152 SMs need about 128 KB each in flight to draw the
+// keys: 80 us, 5.1 TB/s), and the chain of a tile above (64-node trees of 8 heads: 47 us; a tile of 128 rows
+// takes a stream some 5,000 cycles: scores, maximum, exponentials, output). 152 SMs need about 128 KB each in flight to draw the
 // memory's full rate (a copy alone, with nothing done to the tiles, reaches 7.1 TB/s so, 16-token
 // pages in random order). Keys and values therefore share one ring in the order in which the products
 // free them (K0 K1 V0 K2 V1 K3 ...), and a tile is held only while its product runs. The roles of a block:
