@@ -677,17 +677,20 @@ tree_attention_kernel(const AttnParams p, const __grid_constant__ CUtensorMap km
         }
         __syncwarp();
       }
-      if (nan && isfinite(sum)) {
-        const int i = s * kHalf;
-        mend_columns<T>(p, whole ? static_cast<T*>(p.out) + (int64_t)w.row * p.ldo + (int64_t)w.head * D + i : nullptr,
-                        p.part_o + ((size_t)slot * kTileRows + mine) * D + i, i, kHalf, walk, w.bits, D);
-      }
       if (s == 0 && at_lane < per && w.valid && !*sm.dead) {
         if (!whole) p.part_ml[(size_t)slot * kTileRows + mine] = make_float2(m, sum);
         else if (p.lse) p.lse[(int64_t)w.row * p.Hq + w.head] = sum == 0.f ? -INFINITY : (m + log2f(sum)) * kLn2;
       }
+      __syncwarp();
       tc_fence_before();
-      asm volatile("bar.sync 1, 256;" ::: "memory");            // outputs and sums are read; the next item may begin
+      // outputs and sums are read; the next item may begin
+      if constexpr (kE4M3) {
+        asm volatile("bar.sync 1, 256;" ::: "memory");
+      } else if (const bool odd = nan && isfinite(sum); join_barrier_or(odd)) {
+        T* out = whole ? static_cast<T*>(p.out) + (int64_t)w.row * p.ldo + (int64_t)w.head * D + s * kHalf : nullptr;
+        mend_item<T, D>(p, walk, reinterpret_cast<uint32_t*>(smem + S::kJoinAt), threadIdx.x - 128, odd, out,
+                        p.part_o + ((size_t)slot * kTileRows + mine) * D + s * kHalf, s * kHalf, kHalf, w.bits);
+      }
       tc_fence_after();
       unit0 += 2 * count;
       ++items;

@@ -250,46 +250,87 @@ __device__ __forceinline__ uint32_t visible32(uint64_t bits, int key, int ctx) {
 
 // Values that are not finite. A product with a probability of zero makes NaN of an infinite value: one that f16 rounds to zero, one that
 // exp2 does, the zeros of the keys of other copies. The sum of such values with positive weights is the infinity, or NaN if one of them is
-// NaN or both infinities occur: the columns that came out as NaN in a thread's results (stored in out or part, from `column` on) are
-// looked up in the keys [key, end) that the row sees. v: the head's values of page 0. Rare, and so after everything else: finite caches
-// cost a comparison per output.
-template <typename T>
-static __device__ __noinline__ void mend_columns(T* out, float* part, int column, int columns, const uint16_t* v, int64_t page_stride, const int32_t* table,
-                                                 int page_shift, int num_pages, int width, int ctx, uint64_t bits, int first, int end) {
-  constexpr uint32_t kExponent = Mma<T>::kExponent & 0xffffu;
-  for (int i = 0; i < columns; i += 4) {
-    bool odd = false;
-    for (int j = i; j < i + 4; ++j) odd |= isnan(out ? Elem<T>::to_float(out[j]) : part[j]);
-    if (!odd) continue;
-    uint32_t found = 0;                                         // which of the four hold +inf (bits 0-3), -inf (bits 4-7); NaN is both
-#pragma unroll 4
-    for (int key = first; key < end; ++key) {
-      const bool sees = key < ctx || bits >> (key - ctx) & 1;
-      const int page = table[key >> page_shift];
-      if (!sees || page < 0 || page >= num_pages) continue;
-      const uint2 x = *reinterpret_cast<const uint2*>(v + page * page_stride + (int64_t)(key & ((1 << page_shift) - 1)) * width + column + i);
-      const uint32_t e[4] = {x.x & 0xffffu, x.x >> 16, x.y & 0xffffu, x.y >> 16};
+// NaN or both infinities occur. So where a column of an item came out as NaN over finite sums, the block looks its values up: which
+// columns meet +inf and -inf (NaN is both) in the context, and in each node. Rare, and so after the item's results are stored:
+// finite caches cost a comparison per output, a token of NaN in the longest of 16 requests 94 -> 270 us (a search by every thread for
+// itself took 8 ms).
+constexpr int kJoinThreads = 256;    // threads that join an item's results, in both kernels, on barrier 1
+__device__ __forceinline__ bool join_barrier_or(bool mine) {
+  uint32_t any;
+  asm volatile("{ .reg .pred p, q; setp.ne.u32 q, %1, 0; bar.red.or.pred p, 1, %2, q; selp.u32 %0, 1, 0, p; }"
+               : "=r"(any) : "r"((uint32_t)mine), "n"(kJoinThreads) : "memory");
+  return any != 0;
+}
+// Words of found [1 + nodes][D / 32][+inf, -inf]; row 0 is the context.
+template <int D> __device__ __forceinline__ constexpr int found_words(int nodes) { return (1 + nodes) * (D / 32) * 2; }
+// All kJoinThreads threads; v: the head's values of page 0; keys [first, end).
+template <typename T, int D>
+static __device__ __noinline__ void find_infinities(uint32_t* found, int id, const uint16_t* v, int64_t page_stride, const int32_t* table, int page_shift,
+                                                    int num_pages, int ctx, int first, int end) {
+  constexpr uint32_t kExponent = Mma<T>::kExponent;
+  constexpr int kPieces = D / 8, kStep = kJoinThreads / kPieces;
+  const int piece = id % kPieces;
+  uint32_t seen[2] = {0, 0};                                    // of the context
+#pragma unroll 8
+  for (int key = first + id / kPieces; key < end; key += kStep) {
+    const int page = table[key >> page_shift];
+    if (page < 0 || page >= num_pages) continue;
+    const uint4 x = *reinterpret_cast<const uint4*>(v + page * page_stride + (int64_t)(key & ((1 << page_shift) - 1)) * D + 8 * piece);
+    const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+    uint32_t here[2] = {0, 0};
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        if ((e[j] & kExponent) != kExponent) continue;
-        const bool nan = (e[j] & 0x7fffu) != kExponent;
-        if (nan || !(e[j] >> 15)) found |= 1u << j;
-        if (nan || e[j] >> 15) found |= 16u << j;
-      }
+    for (int j = 0; j < 8; ++j) {
+      const uint32_t e = w[j / 2] >> (16 * (j & 1)) & 0xffffu, size = e & 0x7fffu, inf = kExponent & 0xffffu;
+      here[0] |= (uint32_t)(size > inf || e == inf) << j;
+      here[1] |= (uint32_t)(size > inf || e == (inf | 0x8000u)) << j;
     }
-    for (int j = 0; j < 4; ++j) {
-      if ((found >> j & 1) == (found >> (4 + j) & 1)) continue;
-      const float x = found >> j & 1 ? INFINITY : -INFINITY;
-      if (out) out[i + j] = Elem<T>::from_float(x);
-      else part[i + j] = x;
+    if (key < ctx) {
+      seen[0] |= here[0];
+      seen[1] |= here[1];
+    } else {
+      for (int k = 0; k < 2; ++k)
+        if (here[k]) atomicOr(&found[((1 + key - ctx) * (D / 32) + piece / 4) * 2 + k], here[k] << (piece % 4 * 8));
     }
   }
+  for (int k = 0; k < 2; ++k)
+    if (seen[k]) atomicOr(&found[piece / 4 * 2 + k], seen[k] << (piece % 4 * 8));
 }
-template <typename T>
-__device__ __forceinline__ void mend_columns(const AttnParams& p, T* out, float* part, int column, int columns, const Walk& w, uint64_t bits, int width) {
-  mend_columns<T>(out, part, column, columns, static_cast<const uint16_t*>(p.v) + ((int64_t)w.h << p.page_shift) * width, p.page_stride,
-                  p.block_table + (size_t)w.b * p.max_pages, p.page_shift, p.num_pages, width, w.r.ctx, bits, w.tile * kTileKeys,
-                  min(w.r.keys, (w.tile + w.count()) * kTileKeys));
+// A thread's columns of a row that sees the nodes `bits`, in out or part: those that meet one of the infinities (and are it, or NaN).
+template <typename T, int D>
+static __device__ __noinline__ void mend_columns(T* out, float* part, int column, int columns, const uint32_t* found, uint64_t bits) {
+  uint32_t high = 0, low = 0;
+  for (int i = 0; i < columns; ++i) {
+    const int word = (column + i) / 32, bit = (column + i) % 32;
+    if (i == 0 || bit == 0) {
+      high = found[2 * word];
+      low = found[2 * word + 1];
+      for (uint64_t left = bits; left; left &= left - 1) {
+        const int row = __ffsll(left) * (D / 32) + word;
+        high |= found[2 * row];
+        low |= found[2 * row + 1];
+      }
+    }
+    if (!((high ^ low) >> bit & 1)) continue;
+    const float x = high >> bit & 1 ? INFINITY : -INFINITY;
+    if (out) out[i] = Elem<T>::from_float(x);
+    else part[i] = x;
+  }
+}
+// After an item's results are stored and join_barrier_or() of the threads that have NaN over finite sums (odd).
+template <typename T, int D>
+__device__ __forceinline__ void mend_item(const AttnParams& p, const Walk& w, uint32_t* found, int id, bool odd, T* out, float* part, int column, int columns,
+                                          uint64_t bits) {
+  for (int i = id; i < found_words<D>(w.r.rows); i += kJoinThreads) found[i] = 0;
+  __syncwarp();
+  join_barrier_or(false);
+  find_infinities<T, D>(found, id, static_cast<const uint16_t*>(p.v) + ((int64_t)w.h << p.page_shift) * D, p.page_stride,
+                        p.block_table + (size_t)w.b * p.max_pages, p.page_shift, p.num_pages, w.r.ctx, w.tile * kTileKeys,
+                        min(w.r.keys, (w.tile + w.count()) * kTileKeys));
+  __syncwarp();
+  join_barrier_or(false);
+  if (odd) mend_columns<T, D>(out, part, column, columns, found, bits);
+  __syncwarp();
+  join_barrier_or(false);
 }
 
 // Up to kFewRows rows a request and kv head: the kernel of tree_attention_rows.cu. A stage of its copies, and so a box

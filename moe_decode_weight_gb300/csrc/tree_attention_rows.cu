@@ -482,7 +482,8 @@ few_rows_kernel(const AttnParams p, const __grid_constant__ CUtensorMap kmap, co
         }
         v[j] = x.x, v[j + 1] = x.y, v[j + 2] = x.z, v[j + 3] = x.w;
       }
-      if (row < rows && !*dead) {
+      const bool stored = row < rows && !*dead;
+      if (stored) {
         if (whole) {
           const float f = sum == 0.f ? 0.f : (kE4M3 ? p.v_scale[h] : 1.f) / sum;
           const int head = h * p.group + row - node * p.group;
@@ -501,21 +502,25 @@ few_rows_kernel(const AttnParams p, const __grid_constant__ CUtensorMap kmap, co
           for (int j = 0; j < kCols; j += 4) *reinterpret_cast<float4*>(p.part_o + part * D + d + j) = make_float4(v[j], v[j + 1], v[j + 2], v[j + 3]);
           if (d == 0) p.part_ml[part] = make_float2(m, sum);
         }
-        if constexpr (!kE4M3) {
-          bool nan = false;
+      }
+      if constexpr (kE4M3) {
+        join_barrier();
+      } else {
+        bool odd = false;
 #pragma unroll
-          for (int j = 0; j < kCols; ++j) nan |= isnan(v[j]);
-          if (nan && isfinite(sum)) {
-            const int head = h * p.group + row - node * p.group;
-            mend_columns<T>(p, whole ? static_cast<T*>(p.out) + (int64_t)(r.row0 + node) * p.ldo + (int64_t)head * D + d : nullptr,
-                            p.part_o + ((size_t)(2 * blockIdx.x + (tile0 > 0 ? 0 : 1)) * kTileRows + row) * D + d, d, kCols, walk,
-                            (p.tree_mask ? p.tree_mask[r.row0 + node] : ~0ull >> (63 - node)) & ((1ull << r.rows) - 1), D);
-          }
+        for (int j = 0; j < kCols; ++j) odd |= isnan(v[j]);
+        odd &= stored && isfinite(sum);
+        __syncwarp();
+        if (join_barrier_or(odd)) {
+          T* out = whole ? static_cast<T*>(p.out) + (int64_t)(r.row0 + node) * p.ldo + (int64_t)(h * p.group + row - node * p.group) * D + d : nullptr;
+          uint64_t sees = 0;
+          if (odd) sees = (p.tree_mask ? p.tree_mask[r.row0 + node] : ~0ull >> (63 - node)) & ((1ull << r.rows) - 1);
+          mend_item<T, D>(p, walk, reinterpret_cast<uint32_t*>(smem + S::kJoinAt), threadIdx.x, odd, out,
+                          p.part_o + ((size_t)(2 * blockIdx.x + (tile0 > 0 ? 0 : 1)) * kTileRows + row) * D + d, d, kCols, sees);
         }
       }
     }
-    walk.done(p, lane);
-    join_barrier();                                            // sums and outputs are read; the next item may write
+    walk.done(p, lane);                                         // sums and outputs are read; the next item may write
   }
   if (threadIdx.x == 0 && *dead) p.lost[blockIdx.x] = 1;
 }

@@ -1129,3 +1129,23 @@ def test_w4_linear_products_are_exact_at_the_ends_of_bf16(m, group):
     api.w4_linear(w, x, y)
     want, _ = w4_want(w, x)
     assert_close(host(y), want, half_step(F32) * np.abs(want))
+
+
+@pytest.mark.parametrize("hq,dtype,d", SEEN)
+def test_attention_infinities_without_a_mask_and_on_bad_pages(hq, dtype, d):
+    """Chains without a mask; infinities on a page that no row sees any more stay out."""
+    c = Attn(85, [600, 40], [4, 2], hq, 2, d, 32, dtype, dtype, masks="chain")
+    clean, clean_lse = c.call()
+    inf, t = float("inf"), c.table
+    c.cache.v[int(t[0, 3]), :, 5, ::4] = -inf
+    c.cache.v[int(t[1, 40 // 32]), :, 40 % 32, 1::4] = inf       # node 0 of request 1: seen by both rows
+    c.cache.v[int(t[1, 41 // 32]), :, 41 % 32, 2::4] = inf       # node 1: by itself
+    out, lse = c.call(mask=None)
+    assert torch.equal(lse, clean_lse)
+    assert (out[:4, :, ::4] == -inf).all() and all(torch.equal(out[:4, :, i::4], clean[:4, :, i::4]) for i in (1, 2, 3))
+    assert (out[4:, :, 1::4] == inf).all() and all(torch.equal(out[4:, :, i::4], clean[4:, :, i::4]) for i in (0, 3))
+    assert (out[5, :, 2::4] == inf).all() and torch.equal(out[4, :, 2::4], clean[4, :, 2::4])
+    table = t.copy()
+    table[0, 3] = -1
+    hidden, _ = c.call(mask=None, table=table, status=i32([0]))
+    assert torch.isfinite(hidden[:4]).all()
