@@ -376,8 +376,8 @@ typedef struct mdw_w4_weights {
 
 /* y[t][n] = sum_k x[t][k] * (code[n][k] - zero[n][k/group]) * scale[n][k/group]
  *           (+ bias[n]) (+ residual[t][n])    for a window of 1 <= M <= MDW_MAX_M tokens.
- * Products are exact (bf16: of elements from 2^-100 on, with scales below 2^121), sums in fp32 in
- * a fixed order (bit-reproducible), rounded once to y's type.
+ * Products are exact (bf16: of elements between 2^-100 and 2^118, with scales below 2^121), sums
+ * in fp32 in a fixed order (bit-reproducible), a group's before its scale, rounded once to y's type.
  * x [M][k] (ldx), y [M][n] (ldy) in w->dtype or MDW_DT_F32, bias [n], residual [M][n] (ldr) in
  * w->dtype. y, bias and residual need the alignment of their elements only. y may be the
  * residual itself (same pointer, type and stride); it must not overlap any other argument. */
