@@ -382,6 +382,7 @@ cudaError_t launch_rows(const W4Params& p, int dev, cudaStream_t s) {
   // features: 16384 elements 32.9 us in clusters, 41.6 without; 5120 elements 13.0 and 12.0). Only where there are more tiles than
   // blocks: with fewer, each tile's block brings in the token for itself, which more blocks repeat (1000 features x 16384: 12.8 us in
   // clusters, 9.2 without; x 5120 5.6 and 5.7; 2560 x 16384 13.9 and 13.3).
+  // (How many clusters fit is asked once: registers and shared memory leave two blocks an SM for every window of this kernel.)
   int blocks = 1, many = tiles < most ? tiles : most, best = (tiles + many - 1) / many * units;
   for (int n = 2; n <= kMostCluster && tiles > most; n *= 2) {
     a.val.clusterDim.x = n;
