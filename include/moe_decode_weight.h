@@ -77,11 +77,15 @@ typedef enum mdw_format {
   MDW_FMT_FP8_E4M3_ROWSCALE = 2,
   MDW_FMT_MXFP4_E2M1_E8M0_B32 = 3,
   MDW_FMT_INT4_GROUP = 4,          /* mdw_w4_weights */
-  MDW_FMT_KV_PAGED = 5             /* mdw_kv_cache */
+  MDW_FMT_KV_PAGED = 5,            /* mdw_kv_cache */
+  MDW_FMT_LINEAR_STATE = 6         /* mdw_linear_state */
 } mdw_format;
 
 /* Element types of the attention sub-layer's tensors. */
 typedef enum mdw_dtype { MDW_DT_BF16 = 1, MDW_DT_F16 = 2, MDW_DT_F32 = 3, MDW_DT_E4M3 = 4 } mdw_dtype;
+
+/* Gates of mdw_block_norm: none, the gate itself, its sigmoid, the gate times its sigmoid. */
+typedef enum mdw_gate { MDW_GATE_NONE = 0, MDW_GATE_MUL = 1, MDW_GATE_SIGMOID = 2, MDW_GATE_SILU = 3 } mdw_gate;
 
 #define MDW_MAGIC 0x3157444Du /* "MDW1" */
 
@@ -99,6 +103,7 @@ typedef enum mdw_dtype { MDW_DT_BF16 = 1, MDW_DT_F16 = 2, MDW_DT_F32 = 3, MDW_DT
 #define MDW_MAX_REQUESTS 4096 /* requests of one mdw_kv_plan / mdw_tree_attention call */
 #define MDW_MAX_TREE 64       /* drafted tokens of one request's tree */
 #define MDW_MAX_GROUP 64      /* query heads per kv head */
+#define MDW_MAX_NORM_WIDTH 16384 /* elements of a row of mdw_block_norm */
 
 /* Weights of one MoE layer. Fill every field; set magic = MDW_MAGIC and
  * fmt = MDW_FMT_MXFP4_E2M1_E8M0_B32. The shared-expert pointers are all NULL (no shared
@@ -471,6 +476,89 @@ mdw_status mdw_tree_attention(const mdw_kv_cache* cache, int32_t B, int32_t T, i
                               const int32_t* block_table, int32_t max_pages, const int32_t* ctx_len,
                               const int32_t* row_start, const uint64_t* tree_mask, float scale,
                               uint32_t* status, void* ws, size_t ws_bytes, mdw_stream_t stream);
+
+/* ---------------------------------------------------------------------------------- */
+/* The linear-attention sub-layer of a window, and what stands between two sub-layers
+ *
+ * Layers of a hybrid decoder whose attention is linear hold a matrix S for each request and value head
+ * instead of a cache that grows. With the log decay g (natural logarithm) of a token and head,
+ *   S_t = exp(g_t) S_(t-1) + k_t v_t^T,     o_t = scale * S_t^T q_t.
+ * The conventions of the attention sub-layer above hold (row strides, status words), and these:
+ *   - q and k are rows [qk_heads][head_dim], v and out rows [heads][head_dim] of bf16; value head h uses query and
+ *     key head h / (heads / qk_heads) (at most MDW_MAX_GROUP value heads to one).
+ *   - log_decay: fp32 [T][heads] (row stride ldd), or [heads] for all rows with ldd = 0; 4-byte aligned. -inf forgets what
+ *     was before.
+ *   - Rows row_start[b] .. row_start[b+1] - 1 are those of request b, in order. Rows before row_start[0] or from
+ *     row_start[B] on are left as they were.
+ *   - slot_in[b] (-1: zeros) is the slot of the state before, slot_out[b] (-1: not stored) of the one after; they
+ *     may be the same. A request is skipped, with MDW_ERR_DEVICE_BOUNDS, if its rows or slots are bad (outside
+ *     [0, T), more than max_new rows, slots from num_slots on) or if another request stores to the slot that it
+ *     reads or stores to.
+ *   - States and sums are fp32, in a fixed order, which depends on the lengths and the call's sizes and not on timing.
+ *   - Values that are not finite make results of their own row and later ones of the request NaN or infinite (which,
+ *     is not defined), and reach no earlier row and no other request. */
+
+/* The states of a layer. fmt MDW_FMT_LINEAR_STATE. */
+typedef struct mdw_linear_state {
+  uint32_t magic;
+  int32_t fmt;
+  int32_t num_slots;     /* >= 1 */
+  int32_t heads;         /* value heads, 1 .. 1024 */
+  int32_t head_dim;      /* 64 or 128 */
+  int32_t reserved;
+  int64_t slot_stride;   /* elements, heads * head_dim^2 .. 2^32, a multiple of 4 */
+  float* s;              /* [num_slots][heads][head_dim of k][head_dim of v] */
+} mdw_linear_state;
+
+/* Workspace bytes of mdw_linear_attention; 0 if the arguments are invalid. */
+size_t mdw_linear_attention_workspace_bytes(const mdw_linear_state* state, int32_t B, int32_t T, int32_t qk_heads,
+                                            int32_t max_new);
+
+/* Outputs of the rows of B requests and the states after them: one token each, whole prompts, or both in one call.
+ * A request without rows copies its state. max_new >= 1 is an upper bound of a request's rows (more make it
+ * bad), as near as the host knows it: the kernels are chosen by it. ws: workspace, contents arbitrary; not to be
+ * shared by calls that may overlap. scale is finite. */
+mdw_status mdw_linear_attention(const mdw_linear_state* state, int32_t B, int32_t T, int32_t qk_heads, int32_t max_new,
+                                const void* q, int64_t ldq, const void* k, int64_t ldk, const void* v, int64_t ldv,
+                                const float* log_decay, int64_t ldd, void* out, int64_t ldo,
+                                const int32_t* row_start, const int32_t* slot_in, const int32_t* slot_out,
+                                float scale, uint32_t* status, void* ws, size_t ws_bytes, mdw_stream_t stream);
+
+/* Outputs of trees of drafted tokens: each request has up to max_new (1..MDW_MAX_TREE) rows, and a row comes after
+ * the nodes j of its request whose bit is set in tree_mask[row] (as mdw_kv_plan gives them; its own bit counts as
+ * set, bits above it are not looked at; NULL: a chain). No state is stored. */
+mdw_status mdw_linear_tree_attention(const mdw_linear_state* state, int32_t B, int32_t T, int32_t qk_heads,
+                                     int32_t max_new, const void* q, int64_t ldq, const void* k, int64_t ldk,
+                                     const void* v, int64_t ldv, const float* log_decay, int64_t ldd, void* out,
+                                     int64_t ldo, const int32_t* row_start, const int32_t* slot_in,
+                                     const uint64_t* tree_mask, float scale, uint32_t* status, mdw_stream_t stream);
+
+/* The states after the accepted rows of each request, in order: those whose bits are set in accepted[b] (a node's
+ * tree_mask is the path to it; 0 copies the state). Bits from the request's rows on are not looked at. max_new is
+ * 1..MDW_MAX_TREE. */
+mdw_status mdw_linear_state_advance(const mdw_linear_state* state, int32_t B, int32_t T, int32_t qk_heads,
+                                    int32_t max_new, const void* k, int64_t ldk, const void* v, int64_t ldv,
+                                    const float* log_decay, int64_t ldd, const int32_t* row_start,
+                                    const uint64_t* accepted, const int32_t* slot_in, const int32_t* slot_out,
+                                    uint32_t* status, mdw_stream_t stream);
+
+/* Between two sub-layers, for T rows of `width` (1..MDW_MAX_NORM_WIDTH) elements:
+ *   z   = y, or where post_w is given y / sqrt(mean(y^2) + eps) * post_w, the mean over groups of `group` elements
+ *         (width, or 64 or 128 that divide it; post_w [group] serves all groups)
+ *   z   = z * gate | sigmoid(gate) | gate * sigmoid(gate)   (gate [T][width], or [width] for all rows with ldg = 0)
+ *   sum = residual_scale * residual + branch_scale * z      (residual NULL: branch_scale * z)
+ *   x   = sum / sqrt(mean(sum^2) + eps) * pre_w             of the sum as rounded to sum_dtype
+ * in fp32, each output rounded once. x and pre_w are both given or both NULL; sum may be NULL where x is given. dtype
+ * (MDW_DT_BF16 / MDW_DT_F16) is the type of post_w, gate, pre_w and x; y is in dtype or MDW_DT_F32, residual and sum
+ * in sum_dtype, which is dtype or MDW_DT_F32. Tensors and row strides need the alignment of their elements only (rows on
+ * 16-byte boundaries are faster). sum may be the residual itself and x or sum y itself (same pointer, type and stride);
+ * otherwise outputs overlap nothing. branch_scale and residual_scale are finite, eps is finite and > 0. Squares
+ * are summed in fp32: elements above 2^63 / sqrt(width) may overflow them. */
+mdw_status mdw_block_norm(int32_t T, int32_t width, int32_t dtype, const void* y, int64_t ldy, int32_t y_dtype,
+                          const void* post_w, int32_t group, const void* gate, int64_t ldg, int32_t gate_kind,
+                          float branch_scale, const void* residual, int64_t ldr, float residual_scale, void* sum,
+                          int64_t lds, int32_t sum_dtype, const void* pre_w, void* x, int64_t ldx, float eps,
+                          mdw_stream_t stream);
 
 /* Synchronises `stream`, then returns the device status word that the last call using
  * this workspace left (MDW_OK, MDW_ERR_TIMEOUT or MDW_ERR_DEVICE_BOUNDS), or MDW_ERR_CUDA

@@ -20,14 +20,15 @@ _PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_PKG, "libmdw.so")
 
 MDW_MAGIC = 0x3157444D
-FMT_BF16, FMT_FP8, FMT_MXFP4, FMT_INT4_GROUP, FMT_KV_PAGED = 1, 2, 3, 4, 5
+FMT_BF16, FMT_FP8, FMT_MXFP4, FMT_INT4_GROUP, FMT_KV_PAGED, FMT_LINEAR_STATE = 1, 2, 3, 4, 5, 6
 DT_BF16, DT_F16, DT_F32, DT_E4M3 = 1, 2, 3, 4
 STATUS = {0: "MDW_OK", 1: "MDW_ERR_INVALID_ARG", 2: "MDW_ERR_UNSUPPORTED_SHAPE",
           3: "MDW_ERR_FORMAT_MISMATCH", 4: "MDW_ERR_WORKSPACE_TOO_SMALL", 5: "MDW_ERR_CUDA",
           6: "MDW_ERR_TIMEOUT", 7: "MDW_ERR_DEVICE_BOUNDS"}
 HIDDEN, INTER = 2560, 768
 MAX_M, MAX_TOPK, MAX_VOCAB_TOPK, MAX_EXPERTS = 32, 8, 32, 512
-MAX_REQUESTS, MAX_TREE, MAX_GROUP = 4096, 64, 64
+MAX_REQUESTS, MAX_TREE, MAX_GROUP, MAX_NORM_WIDTH = 4096, 64, 64, 16384
+GATES = {"none": 0, "mul": 1, "sigmoid": 2, "silu": 3}
 
 # exported symbols declared in include/moe_decode_weight.h
 SYMBOLS = ["mdw_status_string", "mdw_version", "mdw_moe_workspace_bytes", "mdw_moe_workspace_layout",
@@ -37,7 +38,8 @@ SYMBOLS = ["mdw_status_string", "mdw_version", "mdw_moe_workspace_bytes", "mdw_m
            "moe_decode_stack", "mdw_device_status", "moe_decode_layer_noalloc", "mdw_sample_topk",
            "lm_head_fp8_sample", "moe_decode_stack_routed", "mdw_debug_set_spin_budget",
            "w4_linear", "mdw_kv_plan", "mdw_kv_write", "mdw_tree_attention_workspace_bytes",
-           "mdw_tree_attention"]
+           "mdw_tree_attention", "mdw_linear_attention_workspace_bytes", "mdw_linear_attention",
+           "mdw_linear_tree_attention", "mdw_linear_state_advance", "mdw_block_norm"]
 
 
 class MdwError(RuntimeError):
@@ -77,6 +79,11 @@ class KVCacheC(C.Structure):
                 ("page_size", C.c_int32), ("kv_heads", C.c_int32), ("head_dim", C.c_int32),
                 ("reserved", C.c_int32), ("page_stride", C.c_int64), ("k", C.c_void_p), ("v", C.c_void_p),
                 ("k_scale", C.c_void_p), ("v_scale", C.c_void_p)]
+
+
+class LinearStateC(C.Structure):
+    _fields_ = [("magic", C.c_uint32), ("fmt", C.c_int32), ("num_slots", C.c_int32), ("heads", C.c_int32),
+                ("head_dim", C.c_int32), ("reserved", C.c_int32), ("slot_stride", C.c_int64), ("s", C.c_void_p)]
 
 
 _lib = None
@@ -141,6 +148,18 @@ def lib() -> C.CDLL:
     L.mdw_tree_attention.restype = C.c_int
     L.mdw_tree_attention.argtypes = [C.POINTER(KVCacheC), i32, i32, i32, i32, vp, i64, i32, vp, i64, vp, vp, i32,
                                      vp, vp, vp, f32, vp, vp, sz, vp]
+    L.mdw_linear_attention_workspace_bytes.restype = sz
+    L.mdw_linear_attention_workspace_bytes.argtypes = [C.POINTER(LinearStateC), i32, i32, i32, i32]
+    L.mdw_linear_attention.restype = C.c_int
+    L.mdw_linear_attention.argtypes = [C.POINTER(LinearStateC), i32, i32, i32, i32, vp, i64, vp, i64, vp, i64, vp, i64, vp, i64,
+                                       vp, vp, vp, f32, vp, vp, sz, vp]
+    L.mdw_linear_tree_attention.restype = C.c_int
+    L.mdw_linear_tree_attention.argtypes = [C.POINTER(LinearStateC), i32, i32, i32, i32, vp, i64, vp, i64, vp, i64, vp, i64, vp, i64,
+                                            vp, vp, vp, f32, vp, vp]
+    L.mdw_linear_state_advance.restype = C.c_int
+    L.mdw_linear_state_advance.argtypes = [C.POINTER(LinearStateC), i32, i32, i32, i32, vp, i64, vp, i64, vp, i64, vp, vp, vp, vp, vp, vp]
+    L.mdw_block_norm.restype = C.c_int
+    L.mdw_block_norm.argtypes = [i32, i32, i32, vp, i64, i32, vp, i32, vp, i64, i32, f32, vp, i64, f32, vp, i64, i32, vp, vp, i64, f32, vp]
     _lib = L
     return L
 
@@ -366,7 +385,8 @@ def _binding():
     stream = getattr(torch._C, "_cuda_getCurrentRawStream", lambda i: torch.cuda.current_stream(i).cuda_stream)
     m.setup((torch.bfloat16, torch.float16, torch.float32, torch.float8_e4m3fn, torch.uint8, torch.int32, torch.int64, torch.uint64),
             MdwError, device, stream, tuple(C.cast(f, C.c_void_p).value for f in
-                                            (L.w4_linear, L.mdw_kv_plan, L.mdw_kv_write, L.mdw_tree_attention)))
+                                            (L.w4_linear, L.mdw_kv_plan, L.mdw_kv_write, L.mdw_tree_attention, L.mdw_linear_attention,
+                                             L.mdw_linear_tree_attention, L.mdw_linear_state_advance, L.mdw_block_norm)))
     _bound = m
     return m
 
@@ -501,3 +521,74 @@ def mdw_tree_attention(cache: KVCache, q: torch.Tensor, out: torch.Tensor, block
     uint8 of at least mdw_tree_attention_workspace_bytes."""
     _call((_bound or _binding()).tree_attention, cache, q, out, block_table, ctx_len, row_start, max_new, ws, tree_mask, lse,
           scale, status, stream)
+
+
+# ------------------------------------------- the linear-attention sub-layer, and between sub-layers
+
+
+@dataclass
+class LinearState:
+    """The states of a linear-attention layer (descriptor and its tensor): s float32 [slots, value heads, head
+    dim, head dim]; the slots may be strided, what is inside one is contiguous."""
+    s: torch.Tensor
+    c: LinearStateC = field(init=False)
+    address: int = field(init=False)
+    device_index: int = field(init=False)
+
+    def __post_init__(self):
+        fn, s = "LinearState", self.s
+        if s.dim() != 4 or s.shape[2] != s.shape[3]:
+            raise MdwError(fn, 1, "s is [slots, value heads, head dim, head dim]")
+        p = _address(fn, s, "s", (torch.float32,), s.device)
+        stride = s.stride(0) if s.shape[0] > 1 else s.shape[1] * s.shape[2] * s.shape[3]
+        self.c = LinearStateC(MDW_MAGIC, FMT_LINEAR_STATE, s.shape[0], s.shape[1], s.shape[2], 0, stride, p)
+        self.address = C.addressof(self.c)
+        self.device_index = s.get_device()
+
+
+def mdw_linear_attention_workspace_bytes(state: LinearState, b: int, t: int, qk_heads: int, max_new: int) -> int:
+    if state.s.get_device() == torch.cuda.current_device():
+        return lib().mdw_linear_attention_workspace_bytes(state.c, b, t, qk_heads, max_new)
+    with torch.cuda.device(state.s.device):
+        return lib().mdw_linear_attention_workspace_bytes(state.c, b, t, qk_heads, max_new)
+
+
+def mdw_linear_attention(state: LinearState, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, log_decay: torch.Tensor,
+                         out: torch.Tensor, row_start: torch.Tensor, slot_in: torch.Tensor, slot_out: torch.Tensor,
+                         max_new: int, ws: torch.Tensor, scale: float | None = None, status=None, stream=None) -> None:
+    """Linear attention with a decay for each head over the rows of B requests, from the states slot_in to the
+    states slot_out (see the C declaration): q, k bf16 [T, key heads, head dim], v, out bf16 [T, value heads, head
+    dim] (rows may be strided), log_decay float32 [T, value heads] or [value heads], row_start int32 [B + 1],
+    slot_in, slot_out int32 [B], scale head_dim ** -0.5 by default, ws uint8 of at least
+    mdw_linear_attention_workspace_bytes."""
+    _call((_bound or _binding()).linear_attention, state, q, k, v, log_decay, out, row_start, slot_in, slot_out, max_new, ws,
+          scale, status, stream)
+
+
+def mdw_linear_tree_attention(state: LinearState, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, log_decay: torch.Tensor,
+                              out: torch.Tensor, row_start: torch.Tensor, slot_in: torch.Tensor, max_new: int,
+                              tree_mask=None, scale: float | None = None, status=None, stream=None) -> None:
+    """The same for trees of drafted tokens (tree_mask int64 or uint64 [T], as mdw_kv_plan gives it; None: chains); the
+    states stay as they are."""
+    _call((_bound or _binding()).linear_tree_attention, state, q, k, v, log_decay, out, row_start, slot_in, max_new, tree_mask,
+          scale, status, stream)
+
+
+def mdw_linear_state_advance(state: LinearState, k: torch.Tensor, v: torch.Tensor, log_decay: torch.Tensor,
+                             row_start: torch.Tensor, accepted: torch.Tensor, slot_in: torch.Tensor, slot_out: torch.Tensor,
+                             max_new: int, status=None, stream=None) -> None:
+    """The states after the accepted rows of each request: accepted int64 or uint64 [B], a bit per row."""
+    _call((_bound or _binding()).linear_state_advance, state, k, v, log_decay, row_start, accepted, slot_in, slot_out, max_new,
+          status, stream)
+
+
+def mdw_block_norm(y: torch.Tensor, sum: torch.Tensor | None, post_weight=None, group: int | None = None, gate=None,
+                   gate_kind: str = "none", residual=None, pre_weight=None, x=None, branch_scale: float = 1.0,
+                   residual_scale: float = 1.0, eps: float = 1e-6, stream=None) -> None:
+    """Norm after a sub-layer, gate, scaled residual and norm before the next (see the C declaration): y [T, W];
+    sum = residual_scale * residual + branch_scale * act(gate) * norm(y) and x = norm(sum) * pre_weight, both [T, W];
+    post_weight [group] (W by default), gate [T, W] or [W], gate_kind "none", "mul", "sigmoid" or "silu"."""
+    if gate_kind not in GATES:
+        raise MdwError("mdw_block_norm", 1, f"gate_kind {gate_kind!r} is none of {sorted(GATES)}")
+    _call((_bound or _binding()).block_norm, y, sum, post_weight, group, gate, GATES[gate_kind], residual, pre_weight, x,
+          branch_scale, residual_scale, eps, stream)

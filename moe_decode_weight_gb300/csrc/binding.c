@@ -1,4 +1,4 @@
-/* Marshalling of the attention sub-layer's calls, as a CPython extension (module _binding).
+/* Marshalling of the calls of the attention sub-layers and the norm between them, as a CPython extension (module _binding).
  *
  * A window's calls take a few microseconds on the GPU, and reading ten tensors' types, shapes, strides and
  * addresses from Python takes longer than that: a call of mdw_kv_plan took 10.1 us, of which the library's
@@ -27,10 +27,26 @@ typedef mdw_status (*write_fn)(const mdw_kv_cache*, int32_t, const void*, int64_
 typedef mdw_status (*attention_fn)(const mdw_kv_cache*, int32_t, int32_t, int32_t, int32_t, const void*, int64_t, int32_t, void*,
                                    int64_t, float*, const int32_t*, int32_t, const int32_t*, const int32_t*, const uint64_t*, float,
                                    uint32_t*, void*, size_t, mdw_stream_t);
+typedef mdw_status (*linear_fn)(const mdw_linear_state*, int32_t, int32_t, int32_t, int32_t, const void*, int64_t, const void*, int64_t,
+                                const void*, int64_t, const float*, int64_t, void*, int64_t, const int32_t*, const int32_t*,
+                                const int32_t*, float, uint32_t*, void*, size_t, mdw_stream_t);
+typedef mdw_status (*linear_tree_fn)(const mdw_linear_state*, int32_t, int32_t, int32_t, int32_t, const void*, int64_t, const void*,
+                                     int64_t, const void*, int64_t, const float*, int64_t, void*, int64_t, const int32_t*,
+                                     const int32_t*, const uint64_t*, float, uint32_t*, mdw_stream_t);
+typedef mdw_status (*advance_fn)(const mdw_linear_state*, int32_t, int32_t, int32_t, int32_t, const void*, int64_t, const void*, int64_t,
+                                 const float*, int64_t, const int32_t*, const uint64_t*, const int32_t*, const int32_t*, uint32_t*,
+                                 mdw_stream_t);
+typedef mdw_status (*norm_fn)(int32_t, int32_t, int32_t, const void*, int64_t, int32_t, const void*, int32_t, const void*, int64_t,
+                              int32_t, float, const void*, int64_t, float, void*, int64_t, int32_t, const void*, void*, int64_t, float,
+                              mdw_stream_t);
 static w4_fn g_w4;
 static plan_fn g_plan;
 static write_fn g_write;
 static attention_fn g_attention;
+static linear_fn g_linear;
+static linear_tree_fn g_linear_tree;
+static advance_fn g_advance;
+static norm_fn g_norm;
 
 /* One call's state: the device of its handle or first tensor, which the others have to share. */
 typedef struct {
@@ -290,15 +306,165 @@ static PyObject* b_tree_attention(PyObject* self, PyObject* const* a, Py_ssize_t
   return result(&c, 0, st);
 }
 
-/* setup(types, refuse, current device, current stream, addresses of the four entry points) */
-static PyObject* b_setup(PyObject* self, PyObject* const* a, Py_ssize_t n) {
-  if (!arguments("setup", n, 5)) return NULL;
-  if (!PyTuple_Check(a[0]) || PyTuple_GET_SIZE(a[0]) != T_KINDS || !PyTuple_Check(a[4]) || PyTuple_GET_SIZE(a[4]) != 4) {
-    PyErr_SetString(PyExc_TypeError, "setup: types and addresses are tuples of 8 and 4");
+/* Log decays [T][heads] with contiguous elements, or [heads] for all rows (*ld = 0). */
+static int decays(Call* c, PyObject* o, int64_t t, int64_t heads, Tensor* out, int64_t* ld) {
+  *ld = 0;
+  if (!tensor(c, o, "log_decay", T_F32, 0, 1, out)) return 0;
+  const int one = out->dims == 1;
+  if ((out->dims != 1 && out->dims != 2) || out->size[out->dims - 1] != heads || (heads > 1 && out->stride[out->dims - 1] != 1) ||
+      (!one && out->size[0] != t))
+    return refuse(c, MDW_ERR_INVALID_ARG, "log_decay", "has another shape, or heads that are not contiguous");
+  if (!one) *ld = t == 1 ? heads : out->stride[0];
+  return 1;
+}
+
+/* linear_attention(handle, q, k, v, log_decay, out, row_start, slot_in, slot_out, max_new, ws, scale, status, stream) */
+static PyObject* b_linear_attention(PyObject* self, PyObject* const* a, Py_ssize_t n) {
+  Call c = {"mdw_linear_attention", -1};
+  Tensor q, k, v, g, out, start, in, to, ws, status;
+  int64_t ldq, ldk, ldv, ldd, ldo;
+  const mdw_linear_state* h;
+  if (!arguments(c.fn, n, 14) || !(h = handle(&c, a[0], MDW_FMT_LINEAR_STATE))) return NULL;
+  if (!rows(&c, a[1], "q", T_BF16, 0, 3, -1, -1, h->head_dim, &q, &ldq)) return NULL;
+  const int64_t t = q.size[0];
+  if (!rows(&c, a[2], "k", T_BF16, 0, 3, t, q.size[1], h->head_dim, &k, &ldk) ||
+      !rows(&c, a[3], "v", T_BF16, 0, 3, t, h->heads, h->head_dim, &v, &ldv) || !decays(&c, a[4], t, h->heads, &g, &ldd) ||
+      !rows(&c, a[5], "out", T_BF16, 0, 3, t, h->heads, h->head_dim, &out, &ldo) ||
+      !array(&c, a[7], "slot_in", T_I32, 0, 1, -1, 0, &in) || !array(&c, a[6], "row_start", T_I32, 0, 1, in.size[0] + 1, 0, &start) ||
+      !array(&c, a[8], "slot_out", T_I32, 0, 1, in.size[0], 0, &to) || !array(&c, a[10], "ws", T_U8, 0, 1, -1, 0, &ws) ||
+      !array(&c, a[12], "status", T_I32, 1, 1, 1, 0, &status))
+    return NULL;
+  const int64_t most = PyLong_AsLongLong(a[9]);
+  const double scale = a[11] == Py_None ? 1.0 / sqrt((double)h->head_dim) : PyFloat_AsDouble(a[11]);
+  if (PyErr_Occurred()) return NULL;
+  mdw_stream_t s;
+  int elsewhere;
+  if (!stream_of(&c, a[13], &s, &elsewhere)) return elsewhere ? result(&c, 1, MDW_OK) : NULL;
+  if (!fits32(in.size[0]) || !fits32(t) || !fits32(q.size[1]) || !fits32(most)) return result(&c, 0, MDW_ERR_INVALID_ARG);
+  mdw_status st;
+  Py_BEGIN_ALLOW_THREADS;
+  st = g_linear(h, (int)in.size[0], (int)t, (int)q.size[1], (int)most, q.p, ldq, k.p, ldk, v.p, ldv, g.p, ldd, out.p, ldo, start.p, in.p,
+                to.p, (float)scale, status.p, ws.p, (size_t)ws.size[0], s);
+  Py_END_ALLOW_THREADS;
+  return result(&c, 0, st);
+}
+
+/* linear_tree_attention(handle, q, k, v, log_decay, out, row_start, slot_in, max_new, tree_mask, scale, status, stream) */
+static PyObject* b_linear_tree(PyObject* self, PyObject* const* a, Py_ssize_t n) {
+  Call c = {"mdw_linear_tree_attention", -1};
+  Tensor q, k, v, g, out, start, in, mask, status;
+  int64_t ldq, ldk, ldv, ldd, ldo;
+  const mdw_linear_state* h;
+  if (!arguments(c.fn, n, 13) || !(h = handle(&c, a[0], MDW_FMT_LINEAR_STATE))) return NULL;
+  if (!rows(&c, a[1], "q", T_BF16, 0, 3, -1, -1, h->head_dim, &q, &ldq)) return NULL;
+  const int64_t t = q.size[0];
+  if (!rows(&c, a[2], "k", T_BF16, 0, 3, t, q.size[1], h->head_dim, &k, &ldk) ||
+      !rows(&c, a[3], "v", T_BF16, 0, 3, t, h->heads, h->head_dim, &v, &ldv) || !decays(&c, a[4], t, h->heads, &g, &ldd) ||
+      !rows(&c, a[5], "out", T_BF16, 0, 3, t, h->heads, h->head_dim, &out, &ldo) ||
+      !array(&c, a[7], "slot_in", T_I32, 0, 1, -1, 0, &in) || !array(&c, a[6], "row_start", T_I32, 0, 1, in.size[0] + 1, 0, &start) ||
+      !array(&c, a[9], "tree_mask", T_I64 | T_U64, 1, 1, t, 0, &mask) || !array(&c, a[11], "status", T_I32, 1, 1, 1, 0, &status))
+    return NULL;
+  const int64_t most = PyLong_AsLongLong(a[8]);
+  const double scale = a[10] == Py_None ? 1.0 / sqrt((double)h->head_dim) : PyFloat_AsDouble(a[10]);
+  if (PyErr_Occurred()) return NULL;
+  mdw_stream_t s;
+  int elsewhere;
+  if (!stream_of(&c, a[12], &s, &elsewhere)) return elsewhere ? result(&c, 1, MDW_OK) : NULL;
+  if (!fits32(in.size[0]) || !fits32(t) || !fits32(q.size[1]) || !fits32(most)) return result(&c, 0, MDW_ERR_INVALID_ARG);
+  mdw_status st;
+  Py_BEGIN_ALLOW_THREADS;
+  st = g_linear_tree(h, (int)in.size[0], (int)t, (int)q.size[1], (int)most, q.p, ldq, k.p, ldk, v.p, ldv, g.p, ldd, out.p, ldo, start.p,
+                     in.p, mask.p, (float)scale, status.p, s);
+  Py_END_ALLOW_THREADS;
+  return result(&c, 0, st);
+}
+
+/* linear_state_advance(handle, k, v, log_decay, row_start, accepted, slot_in, slot_out, max_new, status, stream) */
+static PyObject* b_linear_advance(PyObject* self, PyObject* const* a, Py_ssize_t n) {
+  Call c = {"mdw_linear_state_advance", -1};
+  Tensor k, v, g, start, take, in, to, status;
+  int64_t ldk, ldv, ldd;
+  const mdw_linear_state* h;
+  if (!arguments(c.fn, n, 11) || !(h = handle(&c, a[0], MDW_FMT_LINEAR_STATE))) return NULL;
+  if (!rows(&c, a[1], "k", T_BF16, 0, 3, -1, -1, h->head_dim, &k, &ldk)) return NULL;
+  const int64_t t = k.size[0];
+  if (!rows(&c, a[2], "v", T_BF16, 0, 3, t, h->heads, h->head_dim, &v, &ldv) || !decays(&c, a[3], t, h->heads, &g, &ldd) ||
+      !array(&c, a[6], "slot_in", T_I32, 0, 1, -1, 0, &in) || !array(&c, a[4], "row_start", T_I32, 0, 1, in.size[0] + 1, 0, &start) ||
+      !array(&c, a[5], "accepted", T_I64 | T_U64, 0, 1, in.size[0], 0, &take) || !array(&c, a[7], "slot_out", T_I32, 0, 1, in.size[0], 0, &to) ||
+      !array(&c, a[9], "status", T_I32, 1, 1, 1, 0, &status))
+    return NULL;
+  const int64_t most = PyLong_AsLongLong(a[8]);
+  if (PyErr_Occurred()) return NULL;
+  mdw_stream_t s;
+  int elsewhere;
+  if (!stream_of(&c, a[10], &s, &elsewhere)) return elsewhere ? result(&c, 1, MDW_OK) : NULL;
+  if (!fits32(in.size[0]) || !fits32(t) || !fits32(k.size[1]) || !fits32(most)) return result(&c, 0, MDW_ERR_INVALID_ARG);
+  mdw_status st;
+  Py_BEGIN_ALLOW_THREADS;
+  st = g_advance(h, (int)in.size[0], (int)t, (int)k.size[1], (int)most, k.p, ldk, v.p, ldv, g.p, ldd, start.p, take.p, in.p, to.p, status.p, s);
+  Py_END_ALLOW_THREADS;
+  return result(&c, 0, st);
+}
+
+/* block_norm(y, sum, post_weight, group, gate, gate kind, residual, pre_weight, x, branch_scale, residual_scale, eps, stream) */
+static PyObject* b_block_norm(PyObject* self, PyObject* const* a, Py_ssize_t n) {
+  Call c = {"mdw_block_norm", -1};
+  Tensor y, sum, post, gate, res, pre, x;
+  int64_t ldy, lds, ldr, ldx, ldg = 0;
+  if (!arguments(c.fn, n, 13) || !rows(&c, a[0], "y", T_BF16 | T_F16 | T_F32, 0, 2, -1, -1, 0, &y, &ldy)) return NULL;
+  const int64_t t = y.size[0], w = y.size[1];
+  const int64_t group = a[3] == Py_None ? w : PyLong_AsLongLong(a[3]), kind = PyLong_AsLongLong(a[5]);
+  const double fb = PyFloat_AsDouble(a[9]), fr = PyFloat_AsDouble(a[10]), eps = PyFloat_AsDouble(a[11]);
+  if (PyErr_Occurred()) return NULL;
+  const int any = T_BF16 | T_F16;
+  if (!tensor(&c, a[4], "gate", any, 1, 1, &gate) || !array(&c, a[2], "post_weight", any, 1, 1, group, 0, &post) ||
+      !rows(&c, a[8], "x", any, 1, 2, t, w, 0, &x, &ldx) || !array(&c, a[7], "pre_weight", any, 1, 1, w, 0, &pre) ||
+      !rows(&c, a[1], "sum", any | T_F32, 1, 2, t, w, 0, &sum, &lds) || !rows(&c, a[6], "residual", any | T_F32, 1, 2, t, w, 0, &res, &ldr))
+    return NULL;
+  if (gate.p || gate.dims) {
+    const int last = gate.dims - 1;
+    if (gate.dims < 1 || gate.dims > 2 || gate.size[last] != w || (w > 1 && gate.stride[last] != 1) || (gate.dims == 2 && gate.size[0] != t)) {
+      refuse(&c, MDW_ERR_INVALID_ARG, "gate", "has another shape, or rows whose elements are not contiguous");
+      return NULL;
+    }
+    if (gate.dims == 2) ldg = t == 1 ? (w + 7) / 8 * 8 : gate.stride[0];
+  }
+  /* the 16-bit type: that of the first tensor that has one; the others have to be of it */
+  const int types[6] = {y.type, post.type, gate.type, pre.type, x.type, sum.type};
+  int type = 0;
+  for (int i = 0; i < 6 && !type; ++i) type = types[i] & any;
+  if (!type) type = res.type & any ? res.type : T_BF16;
+  const int all16 = post.type | gate.type | pre.type | x.type | ((y.type | sum.type | res.type) & any);
+  if (all16 & ~type) {
+    refuse(&c, MDW_ERR_FORMAT_MISMATCH, "the tensors", "are of two 16-bit types");
     return NULL;
   }
-  void* f[4];
-  for (int i = 0; i < 4; ++i) f[i] = PyLong_AsVoidPtr(PyTuple_GET_ITEM(a[4], i));
+  const int sums = sum.type ? sum.type : res.type ? res.type : type;
+  if (res.type && res.type != sums) {
+    refuse(&c, MDW_ERR_FORMAT_MISMATCH, "residual", "has another type than sum");
+    return NULL;
+  }
+  mdw_stream_t s;
+  int elsewhere;
+  if (!stream_of(&c, a[12], &s, &elsewhere)) return elsewhere ? result(&c, 1, MDW_OK) : NULL;
+  if (!fits32(t) || !fits32(w) || !fits32(group)) return result(&c, 0, MDW_ERR_INVALID_ARG);
+  mdw_status st;
+  Py_BEGIN_ALLOW_THREADS;
+  st = g_norm((int)t, (int)w, dtype_code(type), y.p, ldy, dtype_code(y.type), post.p, (int)group, gate.p, ldg, (int)kind, (float)fb, res.p, ldr,
+              (float)fr, sum.p, lds, dtype_code(sums), pre.p, x.p, ldx, (float)eps, s);
+  Py_END_ALLOW_THREADS;
+  return result(&c, 0, st);
+}
+
+/* setup(types, refuse, current device, current stream, addresses of the eight entry points) */
+static PyObject* b_setup(PyObject* self, PyObject* const* a, Py_ssize_t n) {
+  if (!arguments("setup", n, 5)) return NULL;
+  if (!PyTuple_Check(a[0]) || PyTuple_GET_SIZE(a[0]) != T_KINDS || !PyTuple_Check(a[4]) || PyTuple_GET_SIZE(a[4]) != 8) {
+    PyErr_SetString(PyExc_TypeError, "setup: types and addresses are tuples of 8 each");
+    return NULL;
+  }
+  void* f[8];
+  for (int i = 0; i < 8; ++i) f[i] = PyLong_AsVoidPtr(PyTuple_GET_ITEM(a[4], i));
   if (PyErr_Occurred()) return NULL;
   for (int i = 0; i < T_KINDS; ++i) Py_XSETREF(g_types[i], Py_NewRef(PyTuple_GET_ITEM(a[0], i)));
   Py_XSETREF(g_refuse, Py_NewRef(a[1]));
@@ -308,6 +474,10 @@ static PyObject* b_setup(PyObject* self, PyObject* const* a, Py_ssize_t n) {
   g_plan = (plan_fn)f[1];
   g_write = (write_fn)f[2];
   g_attention = (attention_fn)f[3];
+  g_linear = (linear_fn)f[4];
+  g_linear_tree = (linear_tree_fn)f[5];
+  g_advance = (advance_fn)f[6];
+  g_norm = (norm_fn)f[7];
   Py_RETURN_NONE;
 }
 
@@ -316,6 +486,10 @@ static PyMethodDef methods[] = {{"setup", (PyCFunction)(void (*)(void))b_setup, 
                                 {"kv_plan", (PyCFunction)(void (*)(void))b_kv_plan, METH_FASTCALL, NULL},
                                 {"kv_write", (PyCFunction)(void (*)(void))b_kv_write, METH_FASTCALL, NULL},
                                 {"tree_attention", (PyCFunction)(void (*)(void))b_tree_attention, METH_FASTCALL, NULL},
+                                {"linear_attention", (PyCFunction)(void (*)(void))b_linear_attention, METH_FASTCALL, NULL},
+                                {"linear_tree_attention", (PyCFunction)(void (*)(void))b_linear_tree, METH_FASTCALL, NULL},
+                                {"linear_state_advance", (PyCFunction)(void (*)(void))b_linear_advance, METH_FASTCALL, NULL},
+                                {"block_norm", (PyCFunction)(void (*)(void))b_block_norm, METH_FASTCALL, NULL},
                                 {NULL, NULL, 0, NULL}};
 static struct PyModuleDef module = {PyModuleDef_HEAD_INIT, "_binding", NULL, -1, methods, NULL, NULL, NULL, NULL};
 

@@ -1,0 +1,69 @@
+// Shared by the linear-attention kernels (linear_step.cu, linear_tree.cu): parameters, a request's rows and slots.
+#pragma once
+
+#include "mdw_attn.cuh"
+
+namespace mdw {
+
+struct LinearParams {
+  const __nv_bfloat16* q;          // [T][Hqk][D]
+  const __nv_bfloat16* k;
+  const __nv_bfloat16* v;          // [T][H][D]
+  const float* decay;              // [T][H] (row stride ldd), or [H] with ldd = 0
+  __nv_bfloat16* out;
+  int64_t ldq, ldk, ldv, ldd, ldo, slot_stride;
+  float* s;
+  const int32_t* row_start;
+  const int32_t* slot_in;
+  const int32_t* slot_out;         // null: nothing is stored
+  const uint64_t* bits;            // per row the nodes it comes after (trees), per request the accepted rows
+  uint32_t* status;
+  float scale;
+  int B, T, H, share, max_new, num_slots;
+};
+
+// Rows [row0, row0 + n) and slots of a request.
+struct LinearRequest {
+  int row0, n, in, out;
+};
+
+// Request b, read by all threads of a block together; false (for all) if it has to be skipped. A slot that is
+// stored to by one request and read or stored to by another one would make results depend on timing, so every
+// block looks through the list of slots: B loads of 4 bytes from L2.
+__device__ __forceinline__ bool linear_request(const LinearParams& p, int b, LinearRequest& r) {
+  r.row0 = p.row_start[b];
+  const int end = p.row_start[b + 1];
+  r.in = p.slot_in[b];
+  r.out = p.slot_out ? p.slot_out[b] : -1;
+  int bad = 0;
+  if (p.slot_out)
+    for (int i = threadIdx.x; i < p.B; i += blockDim.x) {
+      const int other = p.slot_out[i];
+      bad |= i != b && other >= 0 && (other == r.in || other == r.out);
+    }
+  bad |= r.row0 < 0 || end < r.row0 || end > p.T || r.in < -1 || r.in >= p.num_slots || r.out < -1 || r.out >= p.num_slots;
+  r.n = bad ? 0 : end - r.row0;
+  bad |= r.n > p.max_new;
+  bad = __syncthreads_or(bad);
+  if (bad && threadIdx.x == 0) raise_status(p.status, MDW_ERR_DEVICE_BOUNDS);
+  return !bad;
+}
+
+__device__ __forceinline__ float log_decay_of(const LinearParams& p, int row, int h) { return p.decay[(int64_t)row * p.ldd + h]; }
+
+// S <- e^g S, with e^g - 1 where e^g is near 1: over a thousand tokens the rounding of e^g itself would add up.
+struct Decay {
+  float f;
+  bool near;
+  __device__ __forceinline__ explicit Decay(float g) : near(g > -0.5f && g < 0.5f) { f = near ? expm1f(g) : expf(g); }
+};
+
+// ------------------------------------------------------------------ host
+
+mdw_status check_linear_state(const mdw_linear_state* s);
+// Sizes and pointers that the three calls share.
+mdw_status check_linear_call(const mdw_linear_state* s, int32_t B, int32_t T, int32_t qk_heads, int32_t max_new, const void* k, int64_t ldk,
+                             const void* v, int64_t ldv, const float* log_decay, int64_t ldd, const int32_t* row_start,
+                             const int32_t* slot_in, const uint32_t* status);
+
+}  // namespace mdw

@@ -1,0 +1,229 @@
+// mdw_linear_attention and mdw_linear_state_advance: one row after the other.
+//
+// Mathematics. S <- e^g S + k v^T, o = scale S^T q, for a request's rows in order. The block of a request and value
+// head holds S in registers, so the state is read and written once whatever the number of rows.
+//
+// What bounds it is the state's 64 KB (heads of 128) in and out of memory: D rows of it lie on the
+// warps, four columns on a lane, and all loads are requested before the first is used.
+#include <algorithm>
+#include <cmath>
+
+#include "linear.cuh"
+
+namespace mdw {
+
+mdw_status check_linear_state(const mdw_linear_state* s) {
+  if (!s) return MDW_ERR_INVALID_ARG;
+  if (s->magic != MDW_MAGIC || s->fmt != MDW_FMT_LINEAR_STATE) return MDW_ERR_FORMAT_MISMATCH;
+  if (s->num_slots < 1 || s->heads < 1 || s->heads > 1024 || (s->head_dim != 64 && s->head_dim != 128)) return MDW_ERR_UNSUPPORTED_SHAPE;
+  if (!aligned_to(s->s, 16) || s->slot_stride < (int64_t)s->heads * s->head_dim * s->head_dim || s->slot_stride % 4 != 0 ||
+      s->slot_stride > (int64_t)1 << 32)
+    return MDW_ERR_INVALID_ARG;
+  return MDW_OK;
+}
+
+mdw_status check_linear_call(const mdw_linear_state* s, int32_t B, int32_t T, int32_t qk_heads, int32_t max_new, const void* k, int64_t ldk,
+                             const void* v, int64_t ldv, const float* log_decay, int64_t ldd, const int32_t* row_start,
+                             const int32_t* slot_in, const uint32_t* status) {
+  const mdw_status st = check_linear_state(s);
+  if (st != MDW_OK) return st;
+  if (B < 1 || B > MDW_MAX_REQUESTS || T < 1 || max_new < 1 || qk_heads < 1 || s->heads % qk_heads != 0 ||
+      s->heads / qk_heads > MDW_MAX_GROUP)
+    return MDW_ERR_INVALID_ARG;
+  if (T > 0x7fff0000) return MDW_ERR_UNSUPPORTED_SHAPE;          // rows of a chunk past the last are int32
+  const int64_t narrow = (int64_t)qk_heads * s->head_dim, wide = (int64_t)s->heads * s->head_dim;
+  if (!aligned_to(k, 16) || !row_stride_ok(ldk, narrow) || !aligned_to(v, 16) || !row_stride_ok(ldv, wide) || !aligned_to(log_decay, 4) ||
+      (ldd != 0 && ldd < s->heads) || !aligned_to(row_start, 4) || !aligned_to(slot_in, 4) || !null_or_aligned(status, 4))
+    return MDW_ERR_INVALID_ARG;
+  return MDW_OK;
+}
+
+namespace {
+
+constexpr int kThreads = 256, kWarps = kThreads / 32;
+constexpr int kRows = 8;                                        // rows whose elements are in shared memory at a time
+
+// One block: request blockIdx.z, value head blockIdx.y, kCols of the columns. kOut: outputs of all rows; else the rows
+// whose bits are set change the state only.
+template <int D, int kCols, bool kOut>
+__global__ void __launch_bounds__(kThreads) step_kernel(const LinearParams p) {
+  constexpr int kLanes = kCols / 4, kGroups = kThreads / kLanes, kPer = D / kGroups;   // lanes of a row, rows at once, rows of a thread
+  static_assert(kPer * kGroups == D && kPer >= 1, "");
+  __shared__ __align__(16) float qs[kRows][D], ks[kRows][D], vs[kRows][kCols];
+  __shared__ __align__(16) float parts[kOut ? kRows : 1][kWarps][kCols];
+  __shared__ float gs[kRows];
+  const int b = blockIdx.z, h = blockIdx.y, col0 = blockIdx.x * kCols, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  LinearRequest r;
+  if (!linear_request(p, b, r)) return;
+  if (r.out < 0 && !(kOut && r.n > 0)) return;
+  const int c = tid % kLanes * 4, a0 = tid / kLanes * kPer;
+  float4 s[kPer];
+#pragma unroll
+  for (int i = 0; i < kPer; ++i) {
+    s[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (r.in >= 0) s[i] = __ldcs(reinterpret_cast<const float4*>(p.s + r.in * p.slot_stride + ((int64_t)h * D + a0 + i) * D + col0 + c));
+  }
+  uint64_t left = 0;                                            // accepted rows that are still to come
+  if (!kOut) left = p.bits[b] & (r.n < 64 ? (1ull << r.n) - 1 : ~0ull);
+  int next = 0;
+  for (;;) {
+    int rows[kRows], count = 0;
+    if (kOut) {
+      count = min(r.n - next, kRows);
+    } else {
+#pragma unroll
+      for (int i = 0; i < kRows; ++i)
+        if (left) {
+          rows[i] = r.row0 + __ffsll((long long)left) - 1;
+          left &= left - 1;
+          count = i + 1;
+        }
+    }
+    if (count <= 0) break;
+    auto row_of = [&](int i) {
+      if (kOut) return r.row0 + next + i;
+      int at = 0;
+#pragma unroll
+      for (int j = 0; j < kRows; ++j) at = j == i ? rows[j] : at;
+      return at;
+    };
+    // pieces of 8 elements: k, then v's columns of the block, then q
+    constexpr int kOfRow = D / 8 + kCols / 8 + (kOut ? D / 8 : 0);
+    for (int i = tid; i < count * kOfRow; i += kThreads) {
+      const int t = i / kOfRow, at = i % kOfRow, row = row_of(t);
+      const __nv_bfloat16* src;
+      float* dst;
+      if (at < D / 8) {
+        src = p.k + row * p.ldk + (int64_t)(h / p.share) * D + 8 * at;
+        dst = &ks[t][8 * at];
+      } else if (at < D / 8 + kCols / 8) {
+        src = p.v + row * p.ldv + (int64_t)h * D + col0 + 8 * (at - D / 8);
+        dst = &vs[t][8 * (at - D / 8)];
+      } else {
+        src = p.q + row * p.ldq + (int64_t)(h / p.share) * D + 8 * (at - D / 8 - kCols / 8);
+        dst = &qs[t][8 * (at - D / 8 - kCols / 8)];
+      }
+      const uint4 x = *reinterpret_cast<const uint4*>(src);
+      const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        dst[2 * e] = __uint_as_float(w[e] << 16);
+        dst[2 * e + 1] = __uint_as_float(w[e] & 0xffff0000u);
+      }
+    }
+    if (tid < count) gs[tid] = log_decay_of(p, row_of(tid), h);
+    __syncthreads();
+    for (int t = 0; t < count; ++t) {
+      const Decay decay(gs[t]);
+      const float4 v = *reinterpret_cast<const float4*>(&vs[t][c]);
+      float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+      for (int i = 0; i < kPer; ++i) {
+        const float k = ks[t][a0 + i];
+        const float4 was = s[i];
+        float4 x;
+        x.x = fmaf(was.x, decay.f, decay.near ? was.x : 0.f);
+        x.y = fmaf(was.y, decay.f, decay.near ? was.y : 0.f);
+        x.z = fmaf(was.z, decay.f, decay.near ? was.z : 0.f);
+        x.w = fmaf(was.w, decay.f, decay.near ? was.w : 0.f);
+        s[i] = make_float4(fmaf(k, v.x, x.x), fmaf(k, v.y, x.y), fmaf(k, v.z, x.z), fmaf(k, v.w, x.w));
+        if (kOut) {
+          const float q = qs[t][a0 + i];
+          o = make_float4(fmaf(q, s[i].x, o.x), fmaf(q, s[i].y, o.y), fmaf(q, s[i].z, o.z), fmaf(q, s[i].w, o.w));
+        }
+      }
+      if (kOut) {
+#pragma unroll
+        for (int m = kLanes; m < 32; m <<= 1) {
+          o.x += __shfl_xor_sync(0xffffffffu, o.x, m);
+          o.y += __shfl_xor_sync(0xffffffffu, o.y, m);
+          o.z += __shfl_xor_sync(0xffffffffu, o.z, m);
+          o.w += __shfl_xor_sync(0xffffffffu, o.w, m);
+        }
+        if (lane < kLanes) *reinterpret_cast<float4*>(&parts[t][warp][c]) = o;
+      }
+    }
+    __syncthreads();
+    if (kOut)
+      for (int i = tid; i < count * kCols; i += kThreads) {
+        const int t = i / kCols, at = i % kCols;
+        float o = 0.f;
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) o += parts[t][w][at];
+        p.out[(int64_t)(r.row0 + next + t) * p.ldo + (int64_t)h * D + col0 + at] = __float2bfloat16_rn(o * p.scale);
+      }
+    next += count;
+  }
+  if (r.out >= 0)
+#pragma unroll
+    for (int i = 0; i < kPer; ++i)
+      __stcs(reinterpret_cast<float4*>(p.s + r.out * p.slot_stride + ((int64_t)h * D + a0 + i) * D + col0 + c), s[i]);
+}
+
+template <int D, int kCols, bool kOut>
+void launch_cols(const LinearParams& p, cudaStream_t s) {
+  step_kernel<D, kCols, kOut><<<dim3(D / kCols, p.H, p.B), kThreads, 0, s>>>(p);
+}
+template <bool kOut>
+cudaError_t launch_step(const LinearParams& p, int D, int sms, cudaStream_t s) {
+  // columns are split where few requests and heads leave SMs without a block
+  const int64_t units = (int64_t)p.B * p.H;
+  if (D == 128) {
+    if (units * 2 <= sms) launch_cols<128, 32, kOut>(p, s);
+    else launch_cols<128, 128, kOut>(p, s);
+  } else {
+    if (units * 2 <= sms) launch_cols<64, 32, kOut>(p, s);
+    else launch_cols<64, 64, kOut>(p, s);
+  }
+  return cudaGetLastError();
+}
+
+}  // namespace
+}  // namespace mdw
+
+using namespace mdw;
+
+extern "C" size_t mdw_linear_attention_workspace_bytes(const mdw_linear_state* state, int32_t B, int32_t T,
+                                                       int32_t qk_heads, int32_t max_new) {
+  if (check_linear_state(state) != MDW_OK || B < 1 || B > MDW_MAX_REQUESTS || T < 1 || T > 0x7fff0000 || max_new < 1 || qk_heads < 1 ||
+      state->heads % qk_heads != 0 || state->heads / qk_heads > MDW_MAX_GROUP)
+    return 0;
+  return 16;
+}
+
+extern "C" mdw_status mdw_linear_attention(const mdw_linear_state* state, int32_t B, int32_t T, int32_t qk_heads,
+                                           int32_t max_new, const void* q, int64_t ldq, const void* k, int64_t ldk,
+                                           const void* v, int64_t ldv, const float* log_decay, int64_t ldd, void* out,
+                                           int64_t ldo, const int32_t* row_start, const int32_t* slot_in,
+                                           const int32_t* slot_out, float scale, uint32_t* status, void* ws,
+                                           size_t ws_bytes, mdw_stream_t stream) {
+  const mdw_status st = check_linear_call(state, B, T, qk_heads, max_new, k, ldk, v, ldv, log_decay, ldd, row_start, slot_in, status);
+  if (st != MDW_OK) return st;
+  const int D = state->head_dim;
+  if (!aligned_to(q, 16) || !row_stride_ok(ldq, (int64_t)qk_heads * D) || !aligned_to(out, 16) || !row_stride_ok(ldo, (int64_t)state->heads * D) ||
+      !aligned_to(slot_out, 4) || !std::isfinite(scale) || !aligned_to(ws, 16))
+    return MDW_ERR_INVALID_ARG;
+  if (ws_bytes < mdw_linear_attention_workspace_bytes(state, B, T, qk_heads, max_new)) return MDW_ERR_WORKSPACE_TOO_SMALL;
+  const int sms = sm_count(current_device());
+  if (sms <= 0) return MDW_ERR_CUDA;
+  const LinearParams p{static_cast<const __nv_bfloat16*>(q), static_cast<const __nv_bfloat16*>(k), static_cast<const __nv_bfloat16*>(v),
+                       log_decay, static_cast<__nv_bfloat16*>(out), ldq, ldk, ldv, ldd, ldo, state->slot_stride, state->s, row_start, slot_in,
+                       slot_out, nullptr, status, scale, B, T, state->heads, state->heads / qk_heads, max_new, state->num_slots};
+  return launch_step<true>(p, D, sms, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess ? MDW_OK : MDW_ERR_CUDA;
+}
+
+extern "C" mdw_status mdw_linear_state_advance(const mdw_linear_state* state, int32_t B, int32_t T, int32_t qk_heads,
+                                               int32_t max_new, const void* k, int64_t ldk, const void* v, int64_t ldv,
+                                               const float* log_decay, int64_t ldd, const int32_t* row_start,
+                                               const uint64_t* accepted, const int32_t* slot_in,
+                                               const int32_t* slot_out, uint32_t* status, mdw_stream_t stream) {
+  const mdw_status st = check_linear_call(state, B, T, qk_heads, max_new, k, ldk, v, ldv, log_decay, ldd, row_start, slot_in, status);
+  if (st != MDW_OK) return st;
+  if (max_new > MDW_MAX_TREE || !aligned_to(accepted, 8) || !aligned_to(slot_out, 4)) return MDW_ERR_INVALID_ARG;
+  const int sms = sm_count(current_device());
+  if (sms <= 0) return MDW_ERR_CUDA;
+  const LinearParams p{nullptr, static_cast<const __nv_bfloat16*>(k), static_cast<const __nv_bfloat16*>(v), log_decay, nullptr, 0, ldk, ldv,
+                       ldd, 0, state->slot_stride, state->s, row_start, slot_in, slot_out, accepted, status, 0.f, B, T, state->heads,
+                       state->heads / qk_heads, max_new, state->num_slots};
+  return launch_step<false>(p, state->head_dim, sms, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess ? MDW_OK : MDW_ERR_CUDA;
+}
