@@ -1,4 +1,5 @@
-// Shared by the linear-attention kernels (linear_step.cu, linear_tree.cu): parameters, a request's rows and slots.
+// Shared by the linear-attention kernels (linear_step.cu: single rows, linear_prompt.cu: chunks of rows, linear_tree.cu):
+// parameters, a request's rows and slots.
 #pragma once
 
 #include "mdw_attn.cuh"
@@ -20,7 +21,31 @@ struct LinearParams {
   uint32_t* status;
   float scale;
   int B, T, H, share, max_new, num_slots;
+  int short_rows;                  // requests of more rows are left to the other kernel
+  int32_t* ok;                     // [B] whether a request is sound, for the kernels that follow; or null
+  long long spin_budget;
 };
+
+// Rows of a chunk; requests of up to kLinearShort rows take them one by one; least chunks of a segment.
+constexpr int kLinearChunk = 128, kLinearShort = 16, kLinearSegment = 4;
+
+// A part of a request's rows, for all value heads, in the workspace.
+struct LinearEntry {
+  int row0, rows, slot_in, slot_out;
+  int seg, segs;                   // segment of how many
+  int set, pad;                    // first set of states of the request: the one before it, then what each segment adds
+};
+
+// The workspace of mdw_linear_attention.
+struct LinearPlan {
+  int32_t* head;                   // units; units of the first pass; whether that was cut short
+  int32_t* ok;
+  LinearEntry* all;                // [B + blocks] every segment, longest first
+  LinearEntry* first;              // [blocks] those whose state others start from
+  float* logs;                     // [blocks] log decay of a segment, by set and head
+  float* states;                   // [blocks][D][D] by set and head
+};
+cudaError_t launch_prompts(const LinearParams& p, const LinearPlan& w, int D, int grid, int dev, cudaStream_t s);
 
 // Rows [row0, row0 + n) and slots of a request.
 struct LinearRequest {

@@ -1,0 +1,689 @@
+// mdw_linear_attention for requests of more rows than linear_step.cu takes one by one: chunks of 128 rows on tcgen05.
+//
+// Mathematics. With c_t the sum of the log decays from the chunk's first row to row t, and S the state before the chunk,
+//   o_i = scale ( sum_{j <= i} e^{c_i - c_j} (q_i . k_j) v_j + e^{c_i} S^T q_i ),
+//   S'  = e^{c_last} S + sum_j k_j (e^{c_last - c_j} v_j)^T.
+// Four products of a chunk: scores Q K^T (128 x 128), weighted by the decays, times V; Q times the state; K^T times
+// the decayed values. Sums of log decays are in 64 bits and only differences leave them, so none of their digits
+// are lost; no factor is above 1, so nothing overflows and what underflows would have underflown.
+//
+// Roundings to bf16, the operands' type: the weighted scores and the state as the outputs read it (outputs are off by 0.0022 of
+// their norm instead of the 0.0017 of their own rounding). The decayed values enter the state's product as
+// three bf16 numbers that hold 24 bits together, so a state carries the error of fp32 sums only; it is kept in registers.
+//
+// Split. A unit is a value head of a request; where these are fewer than the SMs, or one is far longer than the others, a
+// request's rows are cut into segments: a first pass computes what each segment adds to the state, and a
+// segment then starts from the sums before it. plan_kernel lays the units out, longest first, from the lengths on the
+// device; block i takes units i, 2 G - 1 - i, 2 G + i, ... of G blocks, one on each SM.
+//
+// What bounds it: 4 rows of D 16-bit elements in and out for each row, and as floor of a chunk the chain of the state
+// (values decayed, three products, state scaled and rounded). Roles of a block:
+//   warp 0       requests the tiles of q, k and v by TMA (swizzled, 128 rows x 128 bytes)
+//   warp 1       issues the products
+//   warp 2       sums the decays of the next chunk
+//   warps 4-7    weights the scores, one thread a row
+//   warps 8-11   the outputs, one thread a row; stored by TMA from the place of the values
+//   warps 12-27  the decayed values and the state, four threads a row of the state
+#include <cuda.h>
+
+#include <algorithm>
+
+#include "linear.cuh"
+#include "mdw_tcgen05.cuh"
+
+namespace mdw {
+namespace {
+
+constexpr int kChunk = kLinearChunk, kStateWarps = 16, kThreads = 32 * (12 + kStateWarps);
+constexpr float kLn2 = 0.6931471805599453f;
+
+__device__ __forceinline__ void tma_load(uint32_t dst, const CUtensorMap* map, uint32_t bar, int x, int head, int row) {
+  asm volatile("cp.async.bulk.tensor.3d.shared::cta.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];"
+               :: "r"(dst), "l"(map), "r"(x), "r"(head), "r"(row), "r"(bar) : "memory");
+}
+__device__ __forceinline__ void tma_store(const CUtensorMap* map, uint32_t src, int x, int head, int row) {
+  asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.tile.bulk_group [%0, {%1, %2, %3}], [%4];"
+               :: "l"(map), "r"(x), "r"(head), "r"(row), "r"(src) : "memory");
+}
+__device__ __forceinline__ uint4 lds16(uint32_t a) {
+  uint4 v;
+  asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a) : "memory");
+  return v;
+}
+__device__ __forceinline__ void sts16(uint32_t a, uint4 v) {
+  asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" :: "r"(a), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
+}
+__device__ __forceinline__ float exp2_fast(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+// Two fp32 numbers as bf16 (low half: a), and back.
+__device__ __forceinline__ uint32_t pack(float a, float b) {
+  uint32_t r;
+  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(b), "f"(a));
+  return r;
+}
+__device__ __forceinline__ float low(uint32_t v) { return __uint_as_float(v << 16); }
+__device__ __forceinline__ float high(uint32_t v) { return __uint_as_float(v & 0xffff0000u); }
+
+// ------------------------------------------------------------------ the units
+
+__global__ void __launch_bounds__(1024) plan_kernel(const LinearParams p, const LinearPlan w, int blocks) {
+  constexpr int kBuckets = 1024;                                // units of so many chunks (the last: and more)
+  __shared__ int at[kBuckets], sums[32], sets, extra;
+  __shared__ unsigned long long total;
+  const int tid = threadIdx.x;
+  if (tid == 0) total = 0, sets = 0, extra = 0;
+  at[tid] = 0;
+  __syncthreads();
+  auto chunks_of = [&](int b) {
+    const int n = p.row_start[b + 1] - p.row_start[b];
+    return w.ok[b] && n > kLinearShort ? (n + kChunk - 1) / kChunk : 0;
+  };
+  unsigned long long mine = 0;
+  for (int b = tid; b < p.B; b += blockDim.x) mine += chunks_of(b);
+  if (mine) atomicAdd(&total, mine);
+  __syncthreads();
+  // A segment is at least an SM's share of all work, and four chunks: its start costs about one.
+  const long long share = max((long long)kLinearSegment, ((long long)total * p.H + blocks - 1) / blocks);
+  auto cut = [&](int chunks, int& n) {                          // segments and the chunks of one
+    n = (int)max(1ll, chunks / share);
+    const int each = (chunks + n - 1) / n;
+    n = (chunks + each - 1) / each;
+    return each;
+  };
+  for (int b = tid; b < p.B; b += blockDim.x) {
+    int n;
+    const int chunks = chunks_of(b);
+    if (chunks) atomicAdd(&at[min(cut(chunks, n), kBuckets - 1)], n);
+  }
+  __syncthreads();
+  // first place of each bucket, the longest first (sums of all buckets above)
+  const int own = at[kBuckets - 1 - tid];
+  int sum = own;
+  for (int m = 1; m < 32; m <<= 1) {
+    const int up = __shfl_up_sync(0xffffffffu, sum, m);
+    if ((tid & 31) >= m) sum += up;
+  }
+  if ((tid & 31) == 31) sums[tid >> 5] = sum;
+  __syncthreads();
+  int before = 0, all = 0;
+  for (int i = 0; i < 32; ++i) {
+    if (i < tid >> 5) before += sums[i];
+    all += sums[i];
+  }
+  __syncthreads();
+  at[kBuckets - 1 - tid] = before + sum - own;
+  __syncthreads();
+  for (int b = tid; b < p.B; b += blockDim.x) {
+    const int chunks = chunks_of(b);
+    if (!chunks) continue;
+    int n;
+    const int each = cut(chunks, n), rows = p.row_start[b + 1] - p.row_start[b];
+    LinearEntry e{p.row_start[b], 0, p.slot_in[b], p.slot_out[b], 0, n, 0, 0};
+    if (n > 1) e.set = atomicAdd(&sets, n);
+    const int to = atomicAdd(&at[min(each, kBuckets - 1)], n);
+    for (int s = 0; s < n; ++s) {
+      e.seg = s;
+      e.row0 = p.row_start[b] + s * each * kChunk;
+      e.rows = min(rows - s * each * kChunk, each * kChunk);
+      w.all[to + s] = e;
+      if (s + 1 < n) w.first[atomicAdd(&extra, 1)] = e;
+    }
+  }
+  __syncthreads();
+  if (tid == 0) {
+    w.head[0] = all * p.H;
+    w.head[1] = extra * p.H;
+    w.head[2] = 0;
+  }
+}
+
+// ------------------------------------------------------------------ the kernel
+
+template <int D>
+struct Shape {
+  static constexpr int kTile = kChunk * D * 2, kHalves = D / 64;
+  static constexpr int kQ = 0, kK = kTile, kV = 3 * kTile, kW = 5 * kTile, kS = 6 * kTile;
+  static constexpr int kSmall = kS + D * D * 2;
+  static constexpr int kSmem = kSmall + 3 * kChunk * 4 + 22 * 4 + 2 * kChunk * 4 + 24 * 8 + 16;   // sums, rows, barriers, words
+  // tensor memory columns; the weighted scores take the scores' first half when D = 128
+  static constexpr int kOut = 128, kRead = 128 + D, kAdd = 128 + 2 * D, kProb = D == 128 ? 0 : 320;
+  static constexpr int kCols = D / 4;                           // of the state, a thread
+};
+
+// What the warps of a block take from the sums of a chunk's decays (in log2).
+struct Sums {
+  float d[kChunk];                 // from the start of the row's 32 rows to the row
+  float after[kChunk];             // factor from the row to the end of its 32 rows
+  float rest[kChunk];              // factor from the row to the end of the chunk
+  float gap[16];                   // [block][earlier block]: from the end of the earlier one to the start of the block
+  float base[4];                   // from the start of the chunk to the start of the block
+  float all, pad;                  // log decay of the chunk, natural
+};
+
+template <int D, bool kRows>
+__global__ void __launch_bounds__(kThreads, 1)
+prompt_kernel(const LinearParams p, const LinearPlan w, const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CUtensorMap kmap,
+              const __grid_constant__ CUtensorMap vmap, const __grid_constant__ CUtensorMap omap) {
+  using S = Shape<D>;
+  extern __shared__ __align__(1024) uint8_t smem[];
+  const uint32_t base = smem_u32(smem);
+  const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31, blocks = gridDim.x;
+  Sums& sums = *reinterpret_cast<Sums*>(smem + S::kSmall);
+  int* first_bad = reinterpret_cast<int*>(smem + S::kSmall + sizeof(Sums));   // [2][D]: first row whose value is not finite
+  uint32_t bar = smem_u32(first_bad + 2 * kChunk);
+  auto take = [&](int n) { const uint32_t r = bar; bar += 8 * n; return r; };
+  const uint32_t q_full = take(1), q_free = take(1), k_full = take(2), k_free = take(2), v_full = take(2), v_free = take(2), v_done = take(2);
+  const uint32_t sums_full = take(1), sums_free = take(1), s_full = take(1), p_full = take(1), o_full = take(1), o_free = take(1);
+  const uint32_t w_full = take(1), w_free = take(1), state_full = take(1), state_read = take(1), add_full = take(1), end = take(1);
+  uint32_t* words = reinterpret_cast<uint32_t*>(smem + (bar - base));
+  volatile int* dead = reinterpret_cast<volatile int*>(words);
+  volatile int* any_bad = reinterpret_cast<volatile int*>(words + 2);
+  const int units = w.head[kRows ? 0 : 1];
+  const bool failed = kRows && w.head[2] != 0;
+  if ((int)blockIdx.x >= units) return;                         // the whole block
+  if (base & 1023) {
+    if (threadIdx.x == 0) {
+      raise_status(p.status, MDW_ERR_UNSUPPORTED_SHAPE);
+      if (!kRows) w.head[2] = 1;
+    }
+    return;
+  }
+  if (threadIdx.x == 0) {
+    prefetch_map(&kmap);
+    prefetch_map(&vmap);
+    if (kRows) {
+      prefetch_map(&qmap);
+      prefetch_map(&omap);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(k_full + 8 * i, 1);
+      mbar_init(k_free + 8 * i, 1);
+      mbar_init(v_full + 8 * i, 1);
+      mbar_init(v_free + 8 * i, kRows ? 1 : kStateWarps);
+      mbar_init(v_done + 8 * i, kStateWarps);
+      any_bad[i] = 0;
+    }
+    for (const uint32_t b : {q_full, q_free, s_full, o_full, w_free, state_read, add_full, end, sums_full}) mbar_init(b, 1);
+    mbar_init(sums_free, kStateWarps + (kRows ? 8 : 0));
+    mbar_init(p_full, 4);
+    mbar_init(o_free, 4);
+    mbar_init(w_full, kStateWarps);
+    mbar_init(state_full, kStateWarps);
+    *dead = 0;
+    mbar_init_fence();
+  }
+  for (int i = threadIdx.x; i < 2 * kChunk; i += kThreads) first_bad[i] = kChunk;
+  if (warp == 1) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" :: "r"(smem_u32(words + 1)) : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    tc_fence_before();
+  }
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = __shfl_sync(0xffffffffu, words[1], 0);
+  auto wait = [&](uint32_t b, uint32_t parity) { mbar_wait(b, parity, p.spin_budget, p.status, dead); };
+  auto arrive = [&](uint32_t b) {                               // of the warp
+    __syncwarp();
+    if (lane == 0) mbar_arrive(b);
+  };
+  // Every role goes over the block's units and their chunks in the same order; g counts the chunks.
+  auto each_unit = [&](auto&& unit) {
+    int g = 0;
+    for (int k = 0; k * blocks < units; ++k) {
+      const int u = k * blocks + (k & 1 ? blocks - 1 - (int)blockIdx.x : (int)blockIdx.x);
+      if (u >= units) break;
+      const LinearEntry e = (kRows ? w.all : w.first)[u / p.H];
+      if (failed && e.segs > 1) continue;
+      const int chunks = (e.rows + kChunk - 1) / kChunk;
+      unit(e, u % p.H, chunks, g);
+      g += chunks;
+    }
+    return g;
+  };
+
+  if (warp == 0) {
+    // ---- copies
+    int asked[3] = {0, 0, 0};                                   // tiles of k, v and q
+    each_unit([&](const LinearEntry& e, int h, int chunks, int g0) {
+      for (int c = 0; c < chunks; ++c) {
+        const int g = g0 + c, slot = g & 1, row = e.row0 + c * kChunk;
+        const uint32_t again = (g >> 1 & 1) ^ 1;
+        auto load = [&](int which, uint32_t to, const CUtensorMap* map, uint32_t full, uint32_t free, uint32_t parity, int head) {
+          wait(free, parity);
+          if (__any_sync(0xffffffffu, *dead)) return;
+          if (lane == 0) {
+            mbar_arrive_tx(full, S::kTile);
+#pragma unroll
+            for (int i = 0; i < S::kHalves; ++i) tma_load(to + i * (kChunk * 128), map, full, 64 * i, head, row);
+          }
+          __syncwarp();
+          ++asked[which];
+        };
+        load(0, base + S::kK + slot * S::kTile, &kmap, k_full + 8 * slot, k_free + 8 * slot, again, h / p.share);
+        load(1, base + S::kV + slot * S::kTile, &vmap, v_full + 8 * slot, v_free + 8 * slot, again, h);
+        if (kRows) load(2, base + S::kQ, &qmap, q_full, q_free, (g & 1) ^ 1, h / p.share);
+      }
+    });
+    // every copy arrives before the block ends, also where a wait ran out
+    for (int i = 0; i < 2; ++i) {
+      const int k = (asked[0] + 1 - i) >> 1, v = (asked[1] + 1 - i) >> 1;
+      if (k > 0) mbar_drain(k_full + 8 * i, (k - 1) & 1);
+      if (v > 0) mbar_drain(v_full + 8 * i, (v - 1) & 1);
+    }
+    if (asked[2] > 0) mbar_drain(q_full, (asked[2] - 1) & 1);
+  } else if (warp == 1) {
+    // ---- products
+    each_unit([&](const LinearEntry& e, int h, int chunks, int g0) {
+      for (int c = 0; c < chunks; ++c) {
+        const int g = g0 + c, slot = g & 1;
+        const uint32_t q_at = base + S::kQ, k_at = base + S::kK + slot * S::kTile, v_at = base + S::kV + slot * S::kTile;
+        wait(k_full + 8 * slot, g >> 1 & 1);
+        if (kRows) {
+          wait(q_full, g & 1);
+          if (g > 0) wait(o_full, (g - 1) & 1);                 // (the weighted scores lie in the scores' columns)
+          tc_fence_after();
+          if (elect_one()) {
+            const uint32_t ql = operand_low(q_at, 16), kl = operand_low(k_at, 16);
+#pragma unroll
+            for (int t = 0; t < D / 16; ++t) {
+              const uint32_t off = ((t >> 2) * (kChunk * 128) + (t & 3) * 32) >> 4;
+              tc_mma(tmem, ql + off, kl + off, mma_shape(true, false, kChunk), t > 0);
+            }
+            tc_commit(s_full);
+          }
+          __syncwarp();
+          wait(state_full, g & 1);
+          wait(o_free, (g & 1) ^ 1);
+          tc_fence_after();
+          if (elect_one()) {
+            const uint32_t ql = operand_low(q_at, 16), sl = operand_low(base + S::kS, D * 128);
+#pragma unroll
+            for (int t = 0; t < D / 16; ++t)
+              tc_mma(tmem + S::kRead, ql + (((t >> 2) * (kChunk * 128) + (t & 3) * 32) >> 4), sl + t * (2048 >> 4), mma_shape(true, true, D), t > 0);
+            tc_commit(state_read);
+            tc_commit(q_free);
+          }
+          __syncwarp();
+        }
+#pragma unroll
+        for (int part = 0; part < 3; ++part) {
+          wait(w_full, (3 * g + part) & 1);
+          tc_fence_after();
+          if (elect_one()) {
+            // k is the first operand transposed: 64 of its columns at a time (heads of 64: the second 64 lie behind the tile, and what they
+            // hold only reaches lanes that are not read)
+            const uint32_t kl = operand_low(k_at, kChunk * 128), wl = operand_low(base + S::kW, kChunk * 128);
+#pragma unroll
+            for (int t = 0; t < kChunk / 16; ++t)
+              tc_mma(tmem + S::kAdd, kl + t * (2048 >> 4), wl + t * (2048 >> 4), mma_shape(true, true, D) | 1u << 15, part > 0 || t > 0);
+            tc_commit(w_free);
+            if (part == 2) {
+              tc_commit(add_full);
+              tc_commit(k_free + 8 * slot);
+            }
+          }
+          __syncwarp();
+          if (kRows && part == 1) {
+            wait(p_full, g & 1);
+            tc_fence_after();
+            if (elect_one()) {
+              const uint32_t vl = operand_low(v_at, kChunk * 128);
+#pragma unroll
+              for (int t = 0; t < kChunk / 16; ++t)
+                tc_mma_tmem(tmem + S::kOut, tmem + S::kProb + 8 * t, vl + t * (2048 >> 4), mma_shape(true, true, D), t > 0);
+              tc_commit(o_full);
+            }
+            __syncwarp();
+          }
+        }
+      }
+    });
+    if (lane == 0) tc_commit(end);
+    __syncwarp();
+    mbar_drain(end, 0);                                         // nothing is in flight when the columns are given back
+  } else if (warp == 2) {
+    // ---- sums of the decays: a lane has four rows
+    each_unit([&](const LinearEntry& e, int h, int chunks, int g0) {
+      double unit = 0.0;
+      for (int c = 0; c < chunks; ++c) {
+        const int g = g0 + c;
+        double x[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int row = c * kChunk + 4 * lane + i;
+          float v = row < e.rows ? log_decay_of(p, e.row0 + row, h) : 0.f;
+          if (v < -200.f) v = -200.f;                           // below every fp32 number, and sums stay finite
+          x[i] = (double)v * 1.4426950408889634074;
+        }
+#pragma unroll
+        for (int i = 1; i < 4; ++i) x[i] += x[i - 1];
+        double sum = x[3];
+#pragma unroll
+        for (int m = 1; m < 32; m <<= 1) {
+          const double up = __shfl_up_sync(0xffffffffu, sum, m);
+          if (lane >= m) sum += up;
+        }
+        double before = __shfl_up_sync(0xffffffffu, sum, 1);
+        if (lane == 0) before = 0.0;
+        const double last = __shfl_sync(0xffffffffu, sum, 31), stop = __shfl_sync(0xffffffffu, sum, lane | 7);
+        const double start = __shfl_sync(0xffffffffu, before, lane & ~7);
+        float d[4], after[4], rest[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const double c_t = before + x[i], left = last - c_t;
+          d[i] = (float)(c_t - start);
+          after[i] = exp2f((float)(stop - c_t));
+          const float l = (float)left;
+          rest[i] = exp2f(l) * fmaf((float)(left - (double)l), kLn2, 1.f);
+        }
+        // [lane >> 2][lane & 3], lanes below 16
+        const double start_a = __shfl_sync(0xffffffffu, before, (lane >> 2 & 3) * 8), stop_b = __shfl_sync(0xffffffffu, sum, (lane & 3) * 8 + 7);
+        wait(sums_free, (g & 1) ^ 1);
+        *reinterpret_cast<float4*>(&sums.d[4 * lane]) = make_float4(d[0], d[1], d[2], d[3]);
+        *reinterpret_cast<float4*>(&sums.after[4 * lane]) = make_float4(after[0], after[1], after[2], after[3]);
+        *reinterpret_cast<float4*>(&sums.rest[4 * lane]) = make_float4(rest[0], rest[1], rest[2], rest[3]);
+        if (lane < 16) sums.gap[lane] = (float)(start_a - stop_b);
+        if ((lane & 7) == 0) sums.base[lane >> 3] = (float)start;
+        if (lane == 0) sums.all = (float)(last * 0.69314718055994530942);
+        unit += last;
+        arrive(sums_full);
+      }
+      if (!kRows && lane == 0) w.logs[(size_t)(e.set + e.seg + 1) * p.H + h] = (float)(unit * 0.69314718055994530942);
+    });
+  } else if (warp >= 4 && warp < 8) {
+    // ---- weights of the scores: thread = row; 32 columns at a time, none above the diagonal
+    if (kRows) {
+      const int own = warp & 3;
+      const uint32_t lanes = (uint32_t)own * 32 << 16;
+      each_unit([&](const LinearEntry& e, int h, int chunks, int g0) {
+        for (int c = 0; c < chunks; ++c) {
+          const int g = g0 + c;
+          wait(sums_full, g & 1);
+          wait(s_full, g & 1);
+          tc_fence_after();
+          const float d = sums.d[own * 32 + lane];
+#pragma unroll 1
+          for (int b = 0; b < 4; ++b) {
+            uint32_t packed[16];
+            if (b <= own) {
+              float v[32];
+              tc_ld32(v, tmem + lanes + 32 * b);
+              tc_wait_ld();
+              if (b < own) {
+                const float f = exp2_fast(d + sums.gap[4 * own + b]);
+#pragma unroll
+                for (int i = 0; i < 32; i += 4) {
+                  const float4 a = *reinterpret_cast<const float4*>(&sums.after[32 * b + i]);
+                  packed[i / 2] = pack(v[i] * (a.x * f), v[i + 1] * (a.y * f));
+                  packed[i / 2 + 1] = pack(v[i + 2] * (a.z * f), v[i + 3] * (a.w * f));
+                }
+              } else {
+#pragma unroll
+                for (int i = 0; i < 32; i += 4) {
+                  const float4 a = *reinterpret_cast<const float4*>(&sums.d[32 * b + i]);
+                  packed[i / 2] = pack(i <= lane ? v[i] * exp2_fast(d - a.x) : 0.f, i + 1 <= lane ? v[i + 1] * exp2_fast(d - a.y) : 0.f);
+                  packed[i / 2 + 1] = pack(i + 2 <= lane ? v[i + 2] * exp2_fast(d - a.z) : 0.f, i + 3 <= lane ? v[i + 3] * exp2_fast(d - a.w) : 0.f);
+                }
+              }
+            } else {
+#pragma unroll
+              for (int i = 0; i < 16; ++i) packed[i] = 0;
+            }
+            tc_st16(tmem + lanes + S::kProb + 16 * b, packed);
+          }
+          tc_wait_st();
+          tc_fence_before();
+          arrive(p_full);
+          arrive(sums_free);
+        }
+      });
+    }
+  } else if (warp >= 8 && warp < 12) {
+    // ---- outputs: thread = row
+    if (kRows) {
+      const int own = warp & 3, row = own * 32 + lane;
+      const uint32_t lanes = (uint32_t)own * 32 << 16;
+      each_unit([&](const LinearEntry& e, int h, int chunks, int g0) {
+        for (int c = 0; c < chunks; ++c) {
+          const int g = g0 + c, slot = g & 1, valid = min(e.rows - c * kChunk, kChunk);
+          const uint32_t stage = base + S::kV + slot * S::kTile;
+          wait(sums_full, g & 1);
+          const float f = exp2_fast(sums.d[row] + sums.base[own]);
+          arrive(sums_free);
+          wait(v_done + 8 * slot, g >> 1 & 1);
+          wait(o_full, g & 1);
+          tc_fence_after();
+          const bool bad = any_bad[slot] != 0;
+          const bool whole = valid == kChunk;
+          const bool store = row < valid && !*dead;
+          __nv_bfloat16* dst = p.out + (int64_t)(e.row0 + c * kChunk + min(row, valid - 1)) * p.ldo + (int64_t)h * D;
+#pragma unroll 1
+          for (int i = 0; i < D; i += 16) {
+            float o[16], u[16];
+            tc_ld16(o, tmem + lanes + S::kOut + i);
+            tc_ld16(u, tmem + lanes + S::kRead + i);
+            tc_wait_ld();
+#pragma unroll
+            for (int j = 0; j < 16; ++j) o[j] = p.scale * fmaf(f, u[j], o[j]);
+            if (bad)
+#pragma unroll
+              for (int j = 0; j < 16; ++j) o[j] = first_bad[slot * kChunk + i + j] <= row ? __int_as_float(0x7fffffff) : o[j];
+#pragma unroll
+            for (int j = 0; j < 16; j += 8) {
+              const uint4 x = make_uint4(pack(o[j], o[j + 1]), pack(o[j + 2], o[j + 3]), pack(o[j + 4], o[j + 5]), pack(o[j + 6], o[j + 7]));
+              const int piece = (i + j) >> 3;
+              if (whole) sts16(stage + (piece >> 3) * (kChunk * 128) + row * 128 + (((piece & 7) ^ (row & 7)) << 4), x);
+              else if (store) *reinterpret_cast<uint4*>(dst + i + j) = x;
+            }
+          }
+          tc_fence_before();
+          arrive(o_free);
+          if (whole) fence_async_proxy();
+          asm volatile("bar.sync 1, 128;" ::: "memory");
+          if (bad) {
+            for (int i = row; i < kChunk; i += 128) first_bad[slot * kChunk + i] = kChunk;
+            if (row == 0) any_bad[slot] = 0;
+            asm volatile("bar.sync 1, 128;" ::: "memory");
+          }
+          if (row == 0) {
+            if (whole && !*dead) {
+#pragma unroll
+              for (int i = 0; i < S::kHalves; ++i) tma_store(&omap, stage + i * (kChunk * 128), 64 * i, h, e.row0 + c * kChunk);
+              asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+              asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+            }
+            mbar_arrive(v_free + 8 * slot);
+          }
+          __syncwarp();
+        }
+      });
+      if (row == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
+    }
+  } else if (warp >= 12) {
+    // ---- the state: thread = row of it, a quarter of the columns; values: a 16-byte piece of every 64th row
+    const int quad = warp & 3, a = quad * 32 + lane, col0 = ((warp - 12) >> 2) * S::kCols;
+    const bool holds = quad * 32 < D;
+    const uint32_t lanes = (uint32_t)quad * 32 << 16;
+    const int id = threadIdx.x - 384, piece = id & 7, row0 = id >> 3;
+    const uint32_t place = row0 * 128 + ((piece ^ (row0 & 7)) << 4);
+    float s[S::kCols];
+    auto at_state = [&](float* pool, int64_t first) { return pool + first + ((int64_t)a * D + col0); };
+    auto load_state = [&](const float* src) {
+#pragma unroll
+      for (int i = 0; i < S::kCols; i += 4) {
+        const float4 x = *reinterpret_cast<const float4*>(src + i);
+        s[i] = x.x, s[i + 1] = x.y, s[i + 2] = x.z, s[i + 3] = x.w;
+      }
+    };
+    auto store_state = [&](float* dst) {
+#pragma unroll
+      for (int i = 0; i < S::kCols; i += 4) *reinterpret_cast<float4*>(dst + i) = make_float4(s[i], s[i + 1], s[i + 2], s[i + 3]);
+    };
+    auto set_at = [&](int set, int h) { return at_state(w.states, ((int64_t)set * p.H + h) * D * D); };
+    auto publish = [&](int g) {                                 // the state as the outputs of chunk g read it
+      if (g > 0) wait(state_read, (g - 1) & 1);
+      if (holds)
+#pragma unroll
+        for (int i = 0; i < S::kCols; i += 8) {
+          const int at = (col0 + i) >> 3;
+          sts16(base + S::kS + (at >> 3) * (D * 128) + a * 128 + (((at & 7) ^ (a & 7)) << 4),
+                make_uint4(pack(s[i], s[i + 1]), pack(s[i + 2], s[i + 3]), pack(s[i + 4], s[i + 5]), pack(s[i + 6], s[i + 7])));
+        }
+      fence_async_proxy();
+      arrive(state_full);
+    };
+    each_unit([&](const LinearEntry& e, int h, int chunks, int g0) {
+#pragma unroll
+      for (int i = 0; i < S::kCols; ++i) s[i] = 0.f;
+      if (holds) {
+        const int64_t own = (int64_t)h * D * D;
+        if (e.seg == 0 && (!kRows || e.segs == 1)) {
+          if (e.slot_in >= 0) load_state(at_state(p.s, e.slot_in * p.slot_stride + own));
+          // (the last segment may store to the slot before the first one reads it)
+          if (!kRows) store_state(set_at(e.set, h));
+        } else if (kRows) {
+          load_state(set_at(e.set + min(e.seg, 1), h));
+          for (int i = 2; i <= e.seg; ++i) {
+            const Decay f(w.logs[(size_t)(e.set + i) * p.H + h]);
+            const float* add = set_at(e.set + i, h);
+#pragma unroll
+            for (int j = 0; j < S::kCols; j += 4) {
+              const float4 x = *reinterpret_cast<const float4*>(add + j);
+              s[j] = fmaf(s[j], f.f, f.near ? s[j] : 0.f) + x.x;
+              s[j + 1] = fmaf(s[j + 1], f.f, f.near ? s[j + 1] : 0.f) + x.y;
+              s[j + 2] = fmaf(s[j + 2], f.f, f.near ? s[j + 2] : 0.f) + x.z;
+              s[j + 3] = fmaf(s[j + 3], f.f, f.near ? s[j + 3] : 0.f) + x.w;
+            }
+          }
+        }
+      }
+      if (kRows) publish(g0);
+      for (int c = 0; c < chunks; ++c) {
+        const int g = g0 + c, slot = g & 1, valid = min(e.rows - c * kChunk, kChunk);
+        const uint32_t v_at = base + S::kV + slot * S::kTile + place, w_at = base + S::kW + place, k_at = base + S::kK + slot * S::kTile + place;
+        wait(sums_full, g & 1);
+        const float rest[2] = {sums.rest[row0], sums.rest[row0 + 64]};
+        const Decay f(sums.all);
+        arrive(sums_free);
+        wait(v_full + 8 * slot, g >> 1 & 1);
+        if (valid < kChunk) wait(k_full + 8 * slot, g >> 1 & 1);
+        // the decayed values as three bf16 numbers, the smallest first
+#pragma unroll
+        for (int part = 0; part < 3; ++part) {
+          const int use = 3 * g + part;
+          wait(w_free, (use & 1) ^ 1);
+#pragma unroll
+          for (int n = 0; n < S::kHalves * 2; ++n) {
+            const uint32_t off = (n >> 1) * (kChunk * 128) + (n & 1) * (64 * 128);
+            const int row = row0 + 64 * (n & 1);
+            uint4 v = lds16(v_at + off), non = make_uint4(0u, 0u, 0u, 0u);
+            if (part == 0) {
+              const uint32_t m = 0x7f807f80u;
+              non = make_uint4(__vcmpeq2(v.x & m, m), __vcmpeq2(v.y & m, m), __vcmpeq2(v.z & m, m), __vcmpeq2(v.w & m, m));
+              if (row >= valid) {
+                // rows behind the last are another request's, or nobody's
+                v = non = make_uint4(0u, 0u, 0u, 0u);
+                sts16(v_at + off, v);
+                sts16(k_at + off, v);
+              } else if (non.x | non.y | non.z | non.w) {
+                // values that are not finite leave the product with the scores, where they would reach earlier rows too
+                v = make_uint4(v.x & ~non.x, v.y & ~non.y, v.z & ~non.z, v.w & ~non.w);
+                if (kRows) {
+                  sts16(v_at + off, v);
+                  const uint32_t word[4] = {non.x, non.y, non.z, non.w};
+#pragma unroll
+                  for (int i = 0; i < 8; ++i)
+                    if (word[i >> 1] >> (16 * (i & 1)) & 1) atomicMin(&first_bad[slot * kChunk + (n >> 1) * 64 + piece * 8 + i], row);
+                  any_bad[slot] = 1;
+                }
+              }
+            }
+            const uint32_t word[4] = {v.x, v.y, v.z, v.w}, odd[4] = {non.x, non.y, non.z, non.w};
+            uint32_t to[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              float x = low(word[i]) * rest[n & 1], y = high(word[i]) * rest[n & 1];
+              uint32_t r = pack(x, y);
+#pragma unroll
+              for (int more = part; more < 2; ++more) {
+                x -= low(r);
+                y -= high(r);
+                r = pack(x, y);
+              }
+              to[i] = r | (odd[i] & 0x7fff7fffu);
+            }
+            sts16(w_at + off, make_uint4(to[0], to[1], to[2], to[3]));
+          }
+          fence_async_proxy();
+          arrive(w_full);
+        }
+        arrive(v_done + 8 * slot);
+        if (!kRows) arrive(v_free + 8 * slot);
+        wait(add_full, g & 1);
+        tc_fence_after();
+        if (holds)
+#pragma unroll
+          for (int i = 0; i < S::kCols; i += 16) {
+            float x[16];
+            tc_ld16(x, tmem + lanes + S::kAdd + col0 + i);
+            tc_wait_ld();
+#pragma unroll
+            for (int j = 0; j < 16; ++j) s[i + j] = fmaf(s[i + j], f.f, f.near ? s[i + j] : 0.f) + x[j];
+          }
+        tc_fence_before();
+        if (kRows && c + 1 < chunks) publish(g + 1);
+      }
+      if (holds && !*dead) {
+        if (!kRows) store_state(set_at(e.set + e.seg + 1, h));
+        else if (e.seg == e.segs - 1 && e.slot_out >= 0) store_state(at_state(p.s, e.slot_out * p.slot_stride + (int64_t)h * D * D));
+      }
+    });
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (!kRows && threadIdx.x == 0 && *dead) w.head[2] = 1;
+  if (warp == 1) {
+    tc_fence_after();
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" :: "r"(tmem) : "memory");
+  }
+}
+
+// ------------------------------------------------------------------ host
+
+// Rows [heads][d] as [T][heads][d]; a box is 128 rows of 64 elements of a head, swizzled.
+bool encode_rows(CUtensorMap* map, const void* data, int64_t ld, int heads, int d, int T) {
+  const cuuint64_t dims[3] = {(cuuint64_t)d, (cuuint64_t)heads, (cuuint64_t)T}, strides[2] = {(cuuint64_t)d * 2, (cuuint64_t)ld * 2};
+  const cuuint32_t box[3] = {64, 1, kChunk}, ones[3] = {1, 1, 1};
+  const EncodeTiledFn fn = encode_tiled();
+  return fn && fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT16, 3, const_cast<void*>(data), dims, strides, box, ones, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                  CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <int D>
+cudaError_t launch(const LinearParams& p, const LinearPlan& w, const CUtensorMap (&m)[4], int grid, int dev, bool segments, cudaStream_t s) {
+  cudaError_t e = allow_shared_memory<prompt_kernel<D, true>>(dev);
+  if (e == cudaSuccess) e = allow_shared_memory<prompt_kernel<D, false>>(dev);
+  if (e != cudaSuccess) return e;
+  plan_kernel<<<1, 1024, 0, s>>>(p, w, grid);
+  if (segments) prompt_kernel<D, false><<<grid, kThreads, Shape<D>::kSmem, s>>>(p, w, m[0], m[1], m[2], m[3]);
+  prompt_kernel<D, true><<<grid, kThreads, Shape<D>::kSmem, s>>>(p, w, m[0], m[1], m[2], m[3]);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_prompts(const LinearParams& p, const LinearPlan& w, int D, int grid, int dev, cudaStream_t s) {
+  static_assert(sizeof(Sums) == 3 * kChunk * 4 + 22 * 4 && Shape<128>::kSmem <= 227 * 1024, "");
+  CUtensorMap m[4];
+  if (!encode_rows(&m[0], p.q, p.ldq, p.H / p.share, D, p.T) || !encode_rows(&m[1], p.k, p.ldk, p.H / p.share, D, p.T) ||
+      !encode_rows(&m[2], p.v, p.ldv, p.H, D, p.T) || !encode_rows(&m[3], p.out, p.ldo, p.H, D, p.T))
+    return cudaErrorInvalidValue;
+  // a request has two segments only where its chunks are two shares, a share being the chunks of all units over the SMs
+  const bool segments = p.H <= grid / 2 && p.max_new > (2 * kLinearSegment - 1) * kChunk;
+  return D == 128 ? launch<128>(p, w, m, grid, dev, segments, s) : launch<64>(p, w, m, grid, dev, segments, s);
+}
+
+}  // namespace mdw

@@ -7,8 +7,10 @@
 // warps, four columns on a lane, and all loads are requested before the first is used.
 #include <algorithm>
 #include <cmath>
+#include <utility>
 
 #include "linear.cuh"
+#include "mdw_internal.h"
 
 namespace mdw {
 
@@ -31,6 +33,7 @@ mdw_status check_linear_call(const mdw_linear_state* s, int32_t B, int32_t T, in
       s->heads / qk_heads > MDW_MAX_GROUP)
     return MDW_ERR_INVALID_ARG;
   if (T > 0x7fff0000) return MDW_ERR_UNSUPPORTED_SHAPE;          // rows of a chunk past the last are int32
+  if (ldk > (int64_t)1 << 36 || ldv > (int64_t)1 << 36) return MDW_ERR_UNSUPPORTED_SHAPE;   // (strides of a tensor map)
   const int64_t narrow = (int64_t)qk_heads * s->head_dim, wide = (int64_t)s->heads * s->head_dim;
   if (!aligned_to(k, 16) || !row_stride_ok(ldk, narrow) || !aligned_to(v, 16) || !row_stride_ok(ldv, wide) || !aligned_to(log_decay, 4) ||
       (ldd != 0 && ldd < s->heads) || !aligned_to(row_start, 4) || !aligned_to(slot_in, 4) || !null_or_aligned(status, 4))
@@ -54,7 +57,9 @@ __global__ void __launch_bounds__(kThreads) step_kernel(const LinearParams p) {
   __shared__ float gs[kRows];
   const int b = blockIdx.z, h = blockIdx.y, col0 = blockIdx.x * kCols, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   LinearRequest r;
-  if (!linear_request(p, b, r)) return;
+  const bool sound = linear_request(p, b, r);
+  if (kOut && p.ok && blockIdx.x == 0 && h == 0 && tid == 0) p.ok[b] = sound;
+  if (!sound || (kOut && r.n > p.short_rows)) return;
   if (r.out < 0 && !(kOut && r.n > 0)) return;
   const int c = tid % kLanes * 4, a0 = tid / kLanes * kPer;
   float4 s[kPer];
@@ -178,6 +183,25 @@ cudaError_t launch_step(const LinearParams& p, int D, int sms, cudaStream_t s) {
   return cudaGetLastError();
 }
 
+// The parts of the workspace, and its bytes. Segments: their number times the heads is at most the number of blocks (a segment is at
+// least a block's share of all chunks and heads).
+std::pair<LinearPlan, size_t> plan_of(uint8_t* ws, int B, int D, int grid) {
+  size_t at = 0;
+  auto take = [&](size_t bytes) {
+    uint8_t* r = ws + at;
+    at += (bytes + 255) / 256 * 256;
+    return r;
+  };
+  LinearPlan w;
+  w.head = reinterpret_cast<int32_t*>(take(256));
+  w.ok = reinterpret_cast<int32_t*>(take((size_t)B * 4));
+  w.all = reinterpret_cast<LinearEntry*>(take((size_t)(B + grid) * sizeof(LinearEntry)));
+  w.first = reinterpret_cast<LinearEntry*>(take((size_t)grid * sizeof(LinearEntry)));
+  w.logs = reinterpret_cast<float*>(take((size_t)grid * 4));
+  w.states = reinterpret_cast<float*>(take((size_t)grid * D * D * 4));
+  return {w, at};
+}
+
 }  // namespace
 }  // namespace mdw
 
@@ -188,7 +212,8 @@ extern "C" size_t mdw_linear_attention_workspace_bytes(const mdw_linear_state* s
   if (check_linear_state(state) != MDW_OK || B < 1 || B > MDW_MAX_REQUESTS || T < 1 || T > 0x7fff0000 || max_new < 1 || qk_heads < 1 ||
       state->heads % qk_heads != 0 || state->heads / qk_heads > MDW_MAX_GROUP)
     return 0;
-  return 16;
+  const int grid = sm_count(current_device());
+  return plan_of(nullptr, B, state->head_dim, std::max(grid, 1)).second;
 }
 
 extern "C" mdw_status mdw_linear_attention(const mdw_linear_state* state, int32_t B, int32_t T, int32_t qk_heads,
@@ -203,13 +228,20 @@ extern "C" mdw_status mdw_linear_attention(const mdw_linear_state* state, int32_
   if (!aligned_to(q, 16) || !row_stride_ok(ldq, (int64_t)qk_heads * D) || !aligned_to(out, 16) || !row_stride_ok(ldo, (int64_t)state->heads * D) ||
       !aligned_to(slot_out, 4) || !std::isfinite(scale) || !aligned_to(ws, 16))
     return MDW_ERR_INVALID_ARG;
+  if (ldq > (int64_t)1 << 36 || ldo > (int64_t)1 << 36) return MDW_ERR_UNSUPPORTED_SHAPE;
   if (ws_bytes < mdw_linear_attention_workspace_bytes(state, B, T, qk_heads, max_new)) return MDW_ERR_WORKSPACE_TOO_SMALL;
   const int sms = sm_count(current_device());
   if (sms <= 0) return MDW_ERR_CUDA;
+  const LinearPlan w = plan_of(static_cast<uint8_t*>(ws), B, D, sms).first;
+  const bool chunks = max_new > kLinearShort;
   const LinearParams p{static_cast<const __nv_bfloat16*>(q), static_cast<const __nv_bfloat16*>(k), static_cast<const __nv_bfloat16*>(v),
                        log_decay, static_cast<__nv_bfloat16*>(out), ldq, ldk, ldv, ldd, ldo, state->slot_stride, state->s, row_start, slot_in,
-                       slot_out, nullptr, status, scale, B, T, state->heads, state->heads / qk_heads, max_new, state->num_slots};
-  return launch_step<true>(p, D, sms, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess ? MDW_OK : MDW_ERR_CUDA;
+                       slot_out, nullptr, status, scale, B, T, state->heads, state->heads / qk_heads, max_new, state->num_slots,
+                       kLinearShort, chunks ? w.ok : nullptr, mdw_spin_budget()};
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  cudaError_t e = launch_step<true>(p, D, sms, s);
+  if (e == cudaSuccess && chunks) e = launch_prompts(p, w, D, sms, current_device(), s);
+  return e == cudaSuccess ? MDW_OK : MDW_ERR_CUDA;
 }
 
 extern "C" mdw_status mdw_linear_state_advance(const mdw_linear_state* state, int32_t B, int32_t T, int32_t qk_heads,
@@ -224,6 +256,6 @@ extern "C" mdw_status mdw_linear_state_advance(const mdw_linear_state* state, in
   if (sms <= 0) return MDW_ERR_CUDA;
   const LinearParams p{nullptr, static_cast<const __nv_bfloat16*>(k), static_cast<const __nv_bfloat16*>(v), log_decay, nullptr, 0, ldk, ldv,
                        ldd, 0, state->slot_stride, state->s, row_start, slot_in, slot_out, accepted, status, 0.f, B, T, state->heads,
-                       state->heads / qk_heads, max_new, state->num_slots};
+                       state->heads / qk_heads, max_new, state->num_slots, 0, nullptr, 0};
   return launch_step<false>(p, state->head_dim, sms, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess ? MDW_OK : MDW_ERR_CUDA;
 }

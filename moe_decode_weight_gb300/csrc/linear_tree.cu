@@ -109,7 +109,7 @@ extern "C" mdw_status mdw_linear_tree_attention(const mdw_linear_state* state, i
     return MDW_ERR_INVALID_ARG;
   const LinearParams p{static_cast<const __nv_bfloat16*>(q), static_cast<const __nv_bfloat16*>(k), static_cast<const __nv_bfloat16*>(v),
                        log_decay, static_cast<__nv_bfloat16*>(out), ldq, ldk, ldv, ldd, ldo, state->slot_stride, state->s, row_start, slot_in,
-                       nullptr, tree_mask, status, scale, B, T, state->heads, state->heads / qk_heads, max_new, state->num_slots};
+                       nullptr, tree_mask, status, scale, B, T, state->heads, state->heads / qk_heads, max_new, state->num_slots, 0, nullptr, 0};
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   const dim3 grid(1, p.H, p.B);
   if (D == 128) tree_kernel<128><<<grid, kThreads, 0, s>>>(p);
