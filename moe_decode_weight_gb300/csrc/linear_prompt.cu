@@ -21,8 +21,9 @@
 //   warp 0       requests the tiles of q, k and v by TMA (swizzled, 128 rows x 128 bytes)
 //   warp 1       issues the products
 //   warp 2       sums the decays of the next chunk
+//   warp 3       stores the outputs of whole chunks by TMA, from the place of their values
 //   warps 4-7    weights the scores, one thread a row
-//   warps 8-11   the outputs, one thread a row; stored by TMA from the place of the values
+//   warps 8-11   the outputs, one thread a row
 //   warps 12-27  the decayed values and the state, four threads a row of the state
 #include <cuda.h>
 
@@ -64,8 +65,33 @@ __device__ __forceinline__ uint32_t pack(float a, float b) {
   asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(b), "f"(a));
   return r;
 }
-__device__ __forceinline__ float low(uint32_t v) { return __uint_as_float(v << 16); }
-__device__ __forceinline__ float high(uint32_t v) { return __uint_as_float(v & 0xffff0000u); }
+// Pairs of fp32 numbers, which one instruction takes together.
+struct Pair {
+  uint64_t v;
+  __device__ __forceinline__ Pair(float a, float b) { asm("mov.b64 %0, {%1, %2};" : "=l"(v) : "f"(a), "f"(b)); }
+  __device__ __forceinline__ float2 floats() const {
+    float2 r;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+    return r;
+  }
+};
+__device__ __forceinline__ Pair operator*(Pair a, Pair b) {
+  asm("mul.rn.f32x2 %0, %0, %1;" : "+l"(a.v) : "l"(b.v));
+  return a;
+}
+__device__ __forceinline__ Pair operator+(Pair a, Pair b) {
+  asm("add.rn.f32x2 %0, %0, %1;" : "+l"(a.v) : "l"(b.v));
+  return a;
+}
+__device__ __forceinline__ Pair fma(Pair a, Pair b, Pair c) {
+  asm("fma.rn.f32x2 %0, %1, %2, %0;" : "+l"(c.v) : "l"(a.v), "l"(b.v));
+  return c;
+}
+__device__ __forceinline__ Pair unpack(uint32_t v) { return Pair(__uint_as_float(v << 16), __uint_as_float(v & 0xffff0000u)); }
+__device__ __forceinline__ uint32_t pack(Pair a) {
+  const float2 f = a.floats();
+  return pack(f.x, f.y);
+}
 
 // ------------------------------------------------------------------ the units
 
@@ -142,24 +168,26 @@ __global__ void __launch_bounds__(1024) plan_kernel(const LinearParams p, const 
 
 // ------------------------------------------------------------------ the kernel
 
-template <int D>
+// Tiles in shared memory: q, k, two of v (in which the outputs of the chunk wait for their copy), two of decayed values, the state. k has
+// two where there is room: heads of 64, and the first pass, which takes q's place for it.
+template <int D, bool kRows>
 struct Shape {
   static constexpr int kTile = kChunk * D * 2, kHalves = D / 64;
-  static constexpr int kQ = 0, kK = kTile, kV = 3 * kTile, kW = 5 * kTile, kS = 6 * kTile;
-  static constexpr int kSmall = kS + D * D * 2;
-  static constexpr int kSmem = kSmall + 3 * kChunk * 4 + 22 * 4 + 2 * kChunk * 4 + 24 * 8 + 16;   // sums, rows, barriers, words
+  static constexpr int kKeys = D == 64 || !kRows ? 2 : 1;
+  static constexpr int kQ = 0, kK = kRows ? kTile : 0, kV = kTile * (kRows ? 1 + kKeys : 2), kW = kV + 2 * kTile, kS = kW + 2 * kTile;
+  static constexpr int kSmall = kS + D * D * 2, kBarriers = 26;
+  static constexpr int kSmem = kSmall + 3 * kChunk * 4 + 18 * 4 + 2 * kChunk * 4 + kBarriers * 8 + 16;   // sums, rows, barriers, words
   // tensor memory columns; the weighted scores take the scores' first half when D = 128
   static constexpr int kOut = 128, kRead = 128 + D, kAdd = 128 + 2 * D, kProb = D == 128 ? 0 : 320;
   static constexpr int kCols = D / 4;                           // of the state, a thread
 };
 
 // What the warps of a block take from the sums of a chunk's decays (in log2).
-struct Sums {
+struct alignas(8) Sums {
   float d[kChunk];                 // from the start of the row's 32 rows to the row
   float after[kChunk];             // factor from the row to the end of its 32 rows
   float rest[kChunk];              // factor from the row to the end of the chunk
   float gap[16];                   // [block][earlier block]: from the end of the earlier one to the start of the block
-  float base[4];                   // from the start of the chunk to the start of the block
   float all, pad;                  // log decay of the chunk, natural
 };
 
@@ -167,17 +195,18 @@ template <int D, bool kRows>
 __global__ void __launch_bounds__(kThreads, 1)
 prompt_kernel(const LinearParams p, const LinearPlan w, const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CUtensorMap kmap,
               const __grid_constant__ CUtensorMap vmap, const __grid_constant__ CUtensorMap omap) {
-  using S = Shape<D>;
+  using S = Shape<D, kRows>;
   extern __shared__ __align__(1024) uint8_t smem[];
   const uint32_t base = smem_u32(smem);
   const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31, blocks = gridDim.x;
-  Sums& sums = *reinterpret_cast<Sums*>(smem + S::kSmall);
-  int* first_bad = reinterpret_cast<int*>(smem + S::kSmall + sizeof(Sums));   // [2][D]: first row whose value is not finite
-  uint32_t bar = smem_u32(first_bad + 2 * kChunk);
+  // (both on 16-byte boundaries, for rows by four)
+  float* from_start = reinterpret_cast<float*>(smem + S::kSmall);   // [2][kChunk]: factor from the chunk's start to the row
+  Sums& sums = *reinterpret_cast<Sums*>(from_start + 2 * kChunk);
+  uint32_t bar = smem_u32(&sums + 1);
   auto take = [&](int n) { const uint32_t r = bar; bar += 8 * n; return r; };
   const uint32_t q_full = take(1), q_free = take(1), k_full = take(2), k_free = take(2), v_full = take(2), v_free = take(2), v_done = take(2);
   const uint32_t sums_full = take(1), sums_free = take(1), s_full = take(1), p_full = take(1), o_full = take(1), o_free = take(1);
-  const uint32_t w_full = take(1), w_free = take(1), state_full = take(1), state_read = take(1), add_full = take(1), end = take(1);
+  const uint32_t w_full = take(1), w_free = take(1), staged = take(2), state_full = take(1), state_read = take(1), add_full = take(1), end = take(1);
   uint32_t* words = reinterpret_cast<uint32_t*>(smem + (bar - base));
   volatile int* dead = reinterpret_cast<volatile int*>(words);
   volatile int* any_bad = reinterpret_cast<volatile int*>(words + 2);
@@ -204,10 +233,11 @@ prompt_kernel(const LinearParams p, const LinearPlan w, const __grid_constant__ 
       mbar_init(v_full + 8 * i, 1);
       mbar_init(v_free + 8 * i, kRows ? 1 : kStateWarps);
       mbar_init(v_done + 8 * i, kStateWarps);
+      mbar_init(staged + 8 * i, 4);
       any_bad[i] = 0;
     }
     for (const uint32_t b : {q_full, q_free, s_full, o_full, w_free, state_read, add_full, end, sums_full}) mbar_init(b, 1);
-    mbar_init(sums_free, kStateWarps + (kRows ? 8 : 0));
+    mbar_init(sums_free, kStateWarps + (kRows ? 4 : 0));
     mbar_init(p_full, 4);
     mbar_init(o_free, 4);
     mbar_init(w_full, kStateWarps);
@@ -215,7 +245,6 @@ prompt_kernel(const LinearParams p, const LinearPlan w, const __grid_constant__ 
     *dead = 0;
     mbar_init_fence();
   }
-  for (int i = threadIdx.x; i < 2 * kChunk; i += kThreads) first_bad[i] = kChunk;
   if (warp == 1) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" :: "r"(smem_u32(words + 1)) : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
@@ -249,8 +278,7 @@ prompt_kernel(const LinearParams p, const LinearPlan w, const __grid_constant__ 
     int asked[3] = {0, 0, 0};                                   // tiles of k, v and q
     each_unit([&](const LinearEntry& e, int h, int chunks, int g0) {
       for (int c = 0; c < chunks; ++c) {
-        const int g = g0 + c, slot = g & 1, row = e.row0 + c * kChunk;
-        const uint32_t again = (g >> 1 & 1) ^ 1;
+        const int g = g0 + c, slot = g & 1, ks = g % S::kKeys, row = e.row0 + c * kChunk;
         auto load = [&](int which, uint32_t to, const CUtensorMap* map, uint32_t full, uint32_t free, uint32_t parity, int head) {
           wait(free, parity);
           if (__any_sync(0xffffffffu, *dead)) return;
@@ -262,14 +290,14 @@ prompt_kernel(const LinearParams p, const LinearPlan w, const __grid_constant__ 
           __syncwarp();
           ++asked[which];
         };
-        load(0, base + S::kK + slot * S::kTile, &kmap, k_full + 8 * slot, k_free + 8 * slot, again, h / p.share);
-        load(1, base + S::kV + slot * S::kTile, &vmap, v_full + 8 * slot, v_free + 8 * slot, again, h);
+        load(1, base + S::kV + slot * S::kTile, &vmap, v_full + 8 * slot, v_free + 8 * slot, (g >> 1 & 1) ^ 1, h);
+        load(0, base + S::kK + ks * S::kTile, &kmap, k_full + 8 * ks, k_free + 8 * ks, (g / S::kKeys & 1) ^ 1, h / p.share);
         if (kRows) load(2, base + S::kQ, &qmap, q_full, q_free, (g & 1) ^ 1, h / p.share);
       }
     });
     // every copy arrives before the block ends, also where a wait ran out
     for (int i = 0; i < 2; ++i) {
-      const int k = (asked[0] + 1 - i) >> 1, v = (asked[1] + 1 - i) >> 1;
+      const int k = S::kKeys == 2 ? (asked[0] + 1 - i) >> 1 : i == 0 ? asked[0] : 0, v = (asked[1] + 1 - i) >> 1;
       if (k > 0) mbar_drain(k_full + 8 * i, (k - 1) & 1);
       if (v > 0) mbar_drain(v_full + 8 * i, (v - 1) & 1);
     }
@@ -278,9 +306,9 @@ prompt_kernel(const LinearParams p, const LinearPlan w, const __grid_constant__ 
     // ---- products
     each_unit([&](const LinearEntry& e, int h, int chunks, int g0) {
       for (int c = 0; c < chunks; ++c) {
-        const int g = g0 + c, slot = g & 1;
-        const uint32_t q_at = base + S::kQ, k_at = base + S::kK + slot * S::kTile, v_at = base + S::kV + slot * S::kTile;
-        wait(k_full + 8 * slot, g >> 1 & 1);
+        const int g = g0 + c, ks = g % S::kKeys;
+        const uint32_t q_at = base + S::kQ, k_at = base + S::kK + ks * S::kTile, v_at = base + S::kV + (g & 1) * S::kTile;
+        wait(k_full + 8 * ks, g / S::kKeys & 1);
         if (kRows) {
           wait(q_full, g & 1);
           if (g > 0) wait(o_full, (g - 1) & 1);                 // (the weighted scores lie in the scores' columns)
@@ -310,19 +338,21 @@ prompt_kernel(const LinearParams p, const LinearPlan w, const __grid_constant__ 
         }
 #pragma unroll
         for (int part = 0; part < 3; ++part) {
-          wait(w_full, (3 * g + part) & 1);
-          tc_fence_after();
+          if (part != 1) {
+            wait(w_full, part >> 1);
+            tc_fence_after();
+          }
           if (elect_one()) {
             // k is the first operand transposed: 64 of its columns at a time (heads of 64: the second 64 lie behind the tile, and what they
             // hold only reaches lanes that are not read)
-            const uint32_t kl = operand_low(k_at, kChunk * 128), wl = operand_low(base + S::kW, kChunk * 128);
+            const uint32_t kl = operand_low(k_at, kChunk * 128), wl = operand_low(base + S::kW + (part & 1) * S::kTile, kChunk * 128);
 #pragma unroll
             for (int t = 0; t < kChunk / 16; ++t)
               tc_mma(tmem + S::kAdd, kl + t * (2048 >> 4), wl + t * (2048 >> 4), mma_shape(true, true, D) | 1u << 15, part > 0 || t > 0);
-            tc_commit(w_free);
+            if (part == 0) tc_commit(w_free);
             if (part == 2) {
               tc_commit(add_full);
-              tc_commit(k_free + 8 * slot);
+              tc_commit(k_free + 8 * ks);
             }
           }
           __syncwarp();
@@ -370,7 +400,7 @@ prompt_kernel(const LinearParams p, const LinearPlan w, const __grid_constant__ 
         if (lane == 0) before = 0.0;
         const double last = __shfl_sync(0xffffffffu, sum, 31), stop = __shfl_sync(0xffffffffu, sum, lane | 7);
         const double start = __shfl_sync(0xffffffffu, before, lane & ~7);
-        float d[4], after[4], rest[4];
+        float d[4], after[4], rest[4], from[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           const double c_t = before + x[i], left = last - c_t;
@@ -378,21 +408,48 @@ prompt_kernel(const LinearParams p, const LinearPlan w, const __grid_constant__ 
           after[i] = exp2f((float)(stop - c_t));
           const float l = (float)left;
           rest[i] = exp2f(l) * fmaf((float)(left - (double)l), kLn2, 1.f);
+          from[i] = exp2f((float)c_t);
         }
         // [lane >> 2][lane & 3], lanes below 16
         const double start_a = __shfl_sync(0xffffffffu, before, (lane >> 2 & 3) * 8), stop_b = __shfl_sync(0xffffffffu, sum, (lane & 3) * 8 + 7);
+        if (kRows) {
+          wait(staged + 8 * (g & 1), (g >> 1 & 1) ^ 1);         // the outputs of the chunk before the last have read theirs
+          *reinterpret_cast<float4*>(&from_start[(g & 1) * kChunk + 4 * lane]) = make_float4(from[0], from[1], from[2], from[3]);
+        }
         wait(sums_free, (g & 1) ^ 1);
         *reinterpret_cast<float4*>(&sums.d[4 * lane]) = make_float4(d[0], d[1], d[2], d[3]);
         *reinterpret_cast<float4*>(&sums.after[4 * lane]) = make_float4(after[0], after[1], after[2], after[3]);
         *reinterpret_cast<float4*>(&sums.rest[4 * lane]) = make_float4(rest[0], rest[1], rest[2], rest[3]);
         if (lane < 16) sums.gap[lane] = (float)(start_a - stop_b);
-        if ((lane & 7) == 0) sums.base[lane >> 3] = (float)start;
         if (lane == 0) sums.all = (float)(last * 0.69314718055994530942);
         unit += last;
         arrive(sums_full);
       }
       if (!kRows && lane == 0) w.logs[(size_t)(e.set + e.seg + 1) * p.H + h] = (float)(unit * 0.69314718055994530942);
     });
+  } else if (warp == 3) {
+    // ---- outputs of whole chunks to memory, and the place of the values free again
+    if (kRows) {
+      each_unit([&](const LinearEntry& e, int h, int chunks, int g0) {
+        for (int c = 0; c < chunks; ++c) {
+          const int g = g0 + c, slot = g & 1;
+          wait(staged + 8 * slot, g >> 1 & 1);
+          if (lane == 0) {
+            any_bad[slot] = 0;
+            if (e.rows - c * kChunk >= kChunk && !*dead) {
+#pragma unroll
+              for (int i = 0; i < S::kHalves; ++i)
+                tma_store(&omap, base + S::kV + slot * S::kTile + i * (kChunk * 128), 64 * i, h, e.row0 + c * kChunk);
+              asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+              asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+            }
+            mbar_arrive(v_free + 8 * slot);
+          }
+          __syncwarp();
+        }
+      });
+      if (lane == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
+    }
   } else if (warp >= 4 && warp < 8) {
     // ---- weights of the scores: thread = row; 32 columns at a time, none above the diagonal
     if (kRows) {
@@ -417,8 +474,8 @@ prompt_kernel(const LinearParams p, const LinearPlan w, const __grid_constant__ 
 #pragma unroll
                 for (int i = 0; i < 32; i += 4) {
                   const float4 a = *reinterpret_cast<const float4*>(&sums.after[32 * b + i]);
-                  packed[i / 2] = pack(v[i] * (a.x * f), v[i + 1] * (a.y * f));
-                  packed[i / 2 + 1] = pack(v[i + 2] * (a.z * f), v[i + 3] * (a.w * f));
+                  packed[i / 2] = pack(Pair(v[i], v[i + 1]) * (Pair(a.x, a.y) * Pair(f, f)));
+                  packed[i / 2 + 1] = pack(Pair(v[i + 2], v[i + 3]) * (Pair(a.z, a.w) * Pair(f, f)));
                 }
               } else {
 #pragma unroll
@@ -448,59 +505,46 @@ prompt_kernel(const LinearParams p, const LinearPlan w, const __grid_constant__ 
       const uint32_t lanes = (uint32_t)own * 32 << 16;
       each_unit([&](const LinearEntry& e, int h, int chunks, int g0) {
         for (int c = 0; c < chunks; ++c) {
-          const int g = g0 + c, slot = g & 1, valid = min(e.rows - c * kChunk, kChunk);
+          const int g = g0 + c, slot = g & 1, valid = min(e.rows - c * kChunk, kChunk), first = e.row0 + c * kChunk;
           const uint32_t stage = base + S::kV + slot * S::kTile;
-          wait(sums_full, g & 1);
-          const float f = exp2_fast(sums.d[row] + sums.base[own]);
-          arrive(sums_free);
           wait(v_done + 8 * slot, g >> 1 & 1);
           wait(o_full, g & 1);
           tc_fence_after();
-          const bool bad = any_bad[slot] != 0;
-          const bool whole = valid == kChunk;
-          const bool store = row < valid && !*dead;
-          __nv_bfloat16* dst = p.out + (int64_t)(e.row0 + c * kChunk + min(row, valid - 1)) * p.ldo + (int64_t)h * D;
+          const float f = p.scale * from_start[slot * kChunk + row];
+          const bool whole = valid == kChunk, store = row < valid && !*dead;
+          __nv_bfloat16* dst = p.out + (int64_t)(first + min(row, valid - 1)) * p.ldo + (int64_t)h * D;
 #pragma unroll 1
           for (int i = 0; i < D; i += 16) {
             float o[16], u[16];
             tc_ld16(o, tmem + lanes + S::kOut + i);
             tc_ld16(u, tmem + lanes + S::kRead + i);
             tc_wait_ld();
+            uint32_t x[8];
 #pragma unroll
-            for (int j = 0; j < 16; ++j) o[j] = p.scale * fmaf(f, u[j], o[j]);
-            if (bad)
+            for (int j = 0; j < 16; j += 2) x[j / 2] = pack(fma(Pair(u[j], u[j + 1]), Pair(f, f), Pair(o[j], o[j + 1]) * Pair(p.scale, p.scale)));
+            if (any_bad[slot]) {
+              // rare: values that are not finite, which were left out; they make what comes after them in their column so
 #pragma unroll
-              for (int j = 0; j < 16; ++j) o[j] = first_bad[slot * kChunk + i + j] <= row ? __int_as_float(0x7fffffff) : o[j];
+              for (int j = 0; j < 16; ++j) {
+                const __nv_bfloat16* v = p.v + (int64_t)first * p.ldv + (int64_t)h * D + i + j;
+                for (int k = 0; k <= min(row, valid - 1); ++k)
+                  if (!isfinite(__bfloat162float(v[(int64_t)k * p.ldv]))) x[j / 2] |= j & 1 ? 0x7fff0000u : 0x7fffu;
+              }
+            }
 #pragma unroll
-            for (int j = 0; j < 16; j += 8) {
-              const uint4 x = make_uint4(pack(o[j], o[j + 1]), pack(o[j + 2], o[j + 3]), pack(o[j + 4], o[j + 5]), pack(o[j + 6], o[j + 7]));
-              const int piece = (i + j) >> 3;
-              if (whole) sts16(stage + (piece >> 3) * (kChunk * 128) + row * 128 + (((piece & 7) ^ (row & 7)) << 4), x);
-              else if (store) *reinterpret_cast<uint4*>(dst + i + j) = x;
+            for (int j = 0; j < 2; ++j) {
+              const int piece = (i >> 3) + j;
+              const uint4 y = make_uint4(x[4 * j], x[4 * j + 1], x[4 * j + 2], x[4 * j + 3]);
+              if (whole) sts16(stage + (piece >> 3) * (kChunk * 128) + row * 128 + (((piece & 7) ^ (row & 7)) << 4), y);
+              else if (store) *reinterpret_cast<uint4*>(dst + i + 8 * j) = y;
             }
           }
           tc_fence_before();
           arrive(o_free);
-          if (whole) fence_async_proxy();
-          asm volatile("bar.sync 1, 128;" ::: "memory");
-          if (bad) {
-            for (int i = row; i < kChunk; i += 128) first_bad[slot * kChunk + i] = kChunk;
-            if (row == 0) any_bad[slot] = 0;
-            asm volatile("bar.sync 1, 128;" ::: "memory");
-          }
-          if (row == 0) {
-            if (whole && !*dead) {
-#pragma unroll
-              for (int i = 0; i < S::kHalves; ++i) tma_store(&omap, stage + i * (kChunk * 128), 64 * i, h, e.row0 + c * kChunk);
-              asm volatile("cp.async.bulk.commit_group;" ::: "memory");
-              asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
-            }
-            mbar_arrive(v_free + 8 * slot);
-          }
-          __syncwarp();
+          fence_async_proxy();
+          arrive(staged + 8 * slot);
         }
       });
-      if (row == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
     }
   } else if (warp >= 12) {
     // ---- the state: thread = row of it, a quarter of the columns; values: a 16-byte piece of every 64th row
@@ -563,65 +607,59 @@ prompt_kernel(const LinearParams p, const LinearPlan w, const __grid_constant__ 
       if (kRows) publish(g0);
       for (int c = 0; c < chunks; ++c) {
         const int g = g0 + c, slot = g & 1, valid = min(e.rows - c * kChunk, kChunk);
-        const uint32_t v_at = base + S::kV + slot * S::kTile + place, w_at = base + S::kW + place, k_at = base + S::kK + slot * S::kTile + place;
+        const uint32_t v_at = base + S::kV + slot * S::kTile + place, w_at = base + S::kW + place, k_at = base + S::kK + g % S::kKeys * S::kTile + place;
         wait(sums_full, g & 1);
         const float rest[2] = {sums.rest[row0], sums.rest[row0 + 64]};
         const Decay f(sums.all);
         arrive(sums_free);
         wait(v_full + 8 * slot, g >> 1 & 1);
-        if (valid < kChunk) wait(k_full + 8 * slot, g >> 1 & 1);
-        // the decayed values as three bf16 numbers, the smallest first
+        if (valid < kChunk) wait(k_full + 8 * (g % S::kKeys), g / S::kKeys & 1);
+        // The decayed values as three bf16 numbers. The smallest part is summed first; the largest takes its place then.
+        uint4 largest[S::kHalves * 2];
 #pragma unroll
-        for (int part = 0; part < 3; ++part) {
-          const int use = 3 * g + part;
-          wait(w_free, (use & 1) ^ 1);
-#pragma unroll
-          for (int n = 0; n < S::kHalves * 2; ++n) {
-            const uint32_t off = (n >> 1) * (kChunk * 128) + (n & 1) * (64 * 128);
-            const int row = row0 + 64 * (n & 1);
-            uint4 v = lds16(v_at + off), non = make_uint4(0u, 0u, 0u, 0u);
-            if (part == 0) {
-              const uint32_t m = 0x7f807f80u;
-              non = make_uint4(__vcmpeq2(v.x & m, m), __vcmpeq2(v.y & m, m), __vcmpeq2(v.z & m, m), __vcmpeq2(v.w & m, m));
-              if (row >= valid) {
-                // rows behind the last are another request's, or nobody's
-                v = non = make_uint4(0u, 0u, 0u, 0u);
-                sts16(v_at + off, v);
-                sts16(k_at + off, v);
-              } else if (non.x | non.y | non.z | non.w) {
-                // values that are not finite leave the product with the scores, where they would reach earlier rows too
-                v = make_uint4(v.x & ~non.x, v.y & ~non.y, v.z & ~non.z, v.w & ~non.w);
-                if (kRows) {
-                  sts16(v_at + off, v);
-                  const uint32_t word[4] = {non.x, non.y, non.z, non.w};
-#pragma unroll
-                  for (int i = 0; i < 8; ++i)
-                    if (word[i >> 1] >> (16 * (i & 1)) & 1) atomicMin(&first_bad[slot * kChunk + (n >> 1) * 64 + piece * 8 + i], row);
-                  any_bad[slot] = 1;
-                }
-              }
+        for (int n = 0; n < S::kHalves * 2; ++n) {
+          const uint32_t off = (n >> 1) * (kChunk * 128) + (n & 1) * (64 * 128);
+          uint4 v = lds16(v_at + off);
+          const uint32_t m = 0x7f807f80u;
+          uint4 non = make_uint4(__vcmpeq2(v.x & m, m), __vcmpeq2(v.y & m, m), __vcmpeq2(v.z & m, m), __vcmpeq2(v.w & m, m));
+          if (row0 + 64 * (n & 1) >= valid) {
+            // rows behind the last are another request's, or nobody's
+            v = non = make_uint4(0u, 0u, 0u, 0u);
+            sts16(v_at + off, v);
+            sts16(k_at + off, v);
+          } else if (non.x | non.y | non.z | non.w) {
+            // values that are not finite leave the product with the scores, where they would reach earlier rows too
+            v = make_uint4(v.x & ~non.x, v.y & ~non.y, v.z & ~non.z, v.w & ~non.w);
+            if (kRows) {
+              sts16(v_at + off, v);
+              any_bad[slot] = 1;
             }
-            const uint32_t word[4] = {v.x, v.y, v.z, v.w}, odd[4] = {non.x, non.y, non.z, non.w};
-            uint32_t to[4];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              float x = low(word[i]) * rest[n & 1], y = high(word[i]) * rest[n & 1];
-              uint32_t r = pack(x, y);
-#pragma unroll
-              for (int more = part; more < 2; ++more) {
-                x -= low(r);
-                y -= high(r);
-                r = pack(x, y);
-              }
-              to[i] = r | (odd[i] & 0x7fff7fffu);
-            }
-            sts16(w_at + off, make_uint4(to[0], to[1], to[2], to[3]));
           }
-          fence_async_proxy();
-          arrive(w_full);
+          const uint32_t word[4] = {v.x, v.y, v.z, v.w}, odd[4] = {non.x, non.y, non.z, non.w};
+          uint32_t part[3][4];
+          const Pair by(rest[n & 1], rest[n & 1]), minus(-1.f, -1.f);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            Pair x = unpack(word[i]) * by;
+            part[2][i] = pack(x);
+            x = fma(unpack(part[2][i]), minus, x);
+            part[1][i] = pack(x);
+            x = fma(unpack(part[1][i]), minus, x);
+            part[0][i] = pack(x) | (odd[i] & 0x7fff7fffu);
+          }
+          sts16(w_at + off, make_uint4(part[0][0], part[0][1], part[0][2], part[0][3]));
+          sts16(w_at + S::kTile + off, make_uint4(part[1][0], part[1][1], part[1][2], part[1][3]));
+          largest[n] = make_uint4(part[2][0], part[2][1], part[2][2], part[2][3]);
         }
+        fence_async_proxy();
+        arrive(w_full);
         arrive(v_done + 8 * slot);
         if (!kRows) arrive(v_free + 8 * slot);
+        wait(w_free, g & 1);
+#pragma unroll
+        for (int n = 0; n < S::kHalves * 2; ++n) sts16(w_at + (n >> 1) * (kChunk * 128) + (n & 1) * (64 * 128), largest[n]);
+        fence_async_proxy();
+        arrive(w_full);
         wait(add_full, g & 1);
         tc_fence_after();
         if (holds)
@@ -631,7 +669,13 @@ prompt_kernel(const LinearParams p, const LinearPlan w, const __grid_constant__ 
             tc_ld16(x, tmem + lanes + S::kAdd + col0 + i);
             tc_wait_ld();
 #pragma unroll
-            for (int j = 0; j < 16; ++j) s[i + j] = fmaf(s[i + j], f.f, f.near ? s[i + j] : 0.f) + x[j];
+            for (int j = 0; j < 16; j += 2) {
+              const Pair was(s[i + j], s[i + j + 1]);
+              Pair now = fma(was, Pair(f.f, f.f), Pair(x[j], x[j + 1]));
+              if (f.near) now = now + was;
+              s[i + j] = now.floats().x;
+              s[i + j + 1] = now.floats().y;
+            }
           }
         tc_fence_before();
         if (kRows && c + 1 < chunks) publish(g + 1);
@@ -668,15 +712,15 @@ cudaError_t launch(const LinearParams& p, const LinearPlan& w, const CUtensorMap
   if (e == cudaSuccess) e = allow_shared_memory<prompt_kernel<D, false>>(dev);
   if (e != cudaSuccess) return e;
   plan_kernel<<<1, 1024, 0, s>>>(p, w, grid);
-  if (segments) prompt_kernel<D, false><<<grid, kThreads, Shape<D>::kSmem, s>>>(p, w, m[0], m[1], m[2], m[3]);
-  prompt_kernel<D, true><<<grid, kThreads, Shape<D>::kSmem, s>>>(p, w, m[0], m[1], m[2], m[3]);
+  if (segments) prompt_kernel<D, false><<<grid, kThreads, Shape<D, false>::kSmem, s>>>(p, w, m[0], m[1], m[2], m[3]);
+  prompt_kernel<D, true><<<grid, kThreads, Shape<D, true>::kSmem, s>>>(p, w, m[0], m[1], m[2], m[3]);
   return cudaGetLastError();
 }
 
 }  // namespace
 
 cudaError_t launch_prompts(const LinearParams& p, const LinearPlan& w, int D, int grid, int dev, cudaStream_t s) {
-  static_assert(sizeof(Sums) == 3 * kChunk * 4 + 22 * 4 && Shape<128>::kSmem <= 227 * 1024, "");
+  static_assert(sizeof(Sums) == 3 * kChunk * 4 + 18 * 4 && Shape<128, true>::kSmem <= 227 * 1024, "");
   CUtensorMap m[4];
   if (!encode_rows(&m[0], p.q, p.ldq, p.H / p.share, D, p.T) || !encode_rows(&m[1], p.k, p.ldk, p.H / p.share, D, p.T) ||
       !encode_rows(&m[2], p.v, p.ldv, p.H, D, p.T) || !encode_rows(&m[3], p.out, p.ldo, p.H, D, p.T))
