@@ -24,6 +24,7 @@ struct LinearParams {
   int short_rows;                  // requests of more rows are left to the other kernel
   int32_t* ok;                     // [B] whether a request is sound, for the kernels that follow; or null
   long long spin_budget;
+  int wide;                        // rows of out lie on 32-byte boundaries
 };
 
 // Rows of a chunk; requests of up to kLinearShort rows take them one by one; least chunks of a segment.

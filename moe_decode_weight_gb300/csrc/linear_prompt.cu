@@ -21,7 +21,6 @@
 //   warp 0       requests the tiles of q, k and v by TMA (swizzled, 128 rows x 128 bytes)
 //   warp 1       issues the products
 //   warp 2       sums the decays of the next chunk
-//   warp 3       stores the outputs of whole chunks by TMA, from the place of their values
 //   warps 4-7    weights the scores, one thread a row
 //   warps 8-11   the outputs, one thread a row
 //   warps 12-27  the decayed values and the state, four threads a row of the state
@@ -41,10 +40,6 @@ constexpr float kLn2 = 0.6931471805599453f;
 __device__ __forceinline__ void tma_load(uint32_t dst, const CUtensorMap* map, uint32_t bar, int x, int head, int row) {
   asm volatile("cp.async.bulk.tensor.3d.shared::cta.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];"
                :: "r"(dst), "l"(map), "r"(x), "r"(head), "r"(row), "r"(bar) : "memory");
-}
-__device__ __forceinline__ void tma_store(const CUtensorMap* map, uint32_t src, int x, int head, int row) {
-  asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.tile.bulk_group [%0, {%1, %2, %3}], [%4];"
-               :: "l"(map), "r"(x), "r"(head), "r"(row), "r"(src) : "memory");
 }
 __device__ __forceinline__ uint4 lds16(uint32_t a) {
   uint4 v;
@@ -77,10 +72,6 @@ struct Pair {
 };
 __device__ __forceinline__ Pair operator*(Pair a, Pair b) {
   asm("mul.rn.f32x2 %0, %0, %1;" : "+l"(a.v) : "l"(b.v));
-  return a;
-}
-__device__ __forceinline__ Pair operator+(Pair a, Pair b) {
-  asm("add.rn.f32x2 %0, %0, %1;" : "+l"(a.v) : "l"(b.v));
   return a;
 }
 __device__ __forceinline__ Pair fma(Pair a, Pair b, Pair c) {
@@ -166,53 +157,76 @@ __global__ void __launch_bounds__(1024) plan_kernel(const LinearParams p, const 
   }
 }
 
+// The states at the starts of a request's segments from what each segment adds: block (set of the first segment, head).
+__global__ void __launch_bounds__(256) sums_kernel(const LinearPlan w, int H, int elements) {
+  if ((int)blockIdx.x >= w.head[1]) return;
+  const LinearEntry e = w.first[blockIdx.x / H];
+  const int h = blockIdx.x % H;
+  if (e.seg != 0) return;
+  for (int i = threadIdx.x * 4; i < elements; i += blockDim.x * 4) {
+    float4* at = reinterpret_cast<float4*>(w.states + ((int64_t)(e.set + 1) * H + h) * elements + i);
+    float4 s = *at;
+    for (int k = 2; k < e.segs; ++k) {
+      at += (int64_t)H * elements / 4;
+      const Decay f(w.logs[(size_t)(e.set + k) * H + h]);
+      const float4 x = *at;
+      s.x = fmaf(s.x, f.f, f.near ? s.x : 0.f) + x.x;
+      s.y = fmaf(s.y, f.f, f.near ? s.y : 0.f) + x.y;
+      s.z = fmaf(s.z, f.f, f.near ? s.z : 0.f) + x.z;
+      s.w = fmaf(s.w, f.f, f.near ? s.w : 0.f) + x.w;
+      *at = s;
+    }
+  }
+}
+
 // ------------------------------------------------------------------ the kernel
 
-// Tiles in shared memory: q, k, two of v (in which the outputs of the chunk wait for their copy), two of decayed values, the state. k has
-// two where there is room: heads of 64, and the first pass, which takes q's place for it.
+// Shared memory: a tile of q, two of k and of v, a ring of two steps of decayed values (three parts of kStep rows), the state.
 template <int D, bool kRows>
 struct Shape {
   static constexpr int kTile = kChunk * D * 2, kHalves = D / 64;
-  static constexpr int kKeys = D == 64 || !kRows ? 2 : 1;
-  static constexpr int kQ = 0, kK = kRows ? kTile : 0, kV = kTile * (kRows ? 1 + kKeys : 2), kW = kV + 2 * kTile, kS = kW + 2 * kTile;
-  static constexpr int kSmall = kS + D * D * 2, kBarriers = 26;
-  static constexpr int kSmem = kSmall + 3 * kChunk * 4 + 18 * 4 + 2 * kChunk * 4 + kBarriers * 8 + 16;   // sums, rows, barriers, words
+  static constexpr int kStep = 32 / kHalves, kSteps = kChunk / kStep, kPart = kStep * D * 2;
+  static constexpr int kQ = 0, kK = kTile, kV = 3 * kTile, kW = 5 * kTile, kS = kW + 6 * kPart;
+  static constexpr int kSmall = kS + D * D * 2, kBarriers = 29;
+  static constexpr int kSmem = kSmall + 2 * (4 * kChunk * 4 + 24 * 4) + kBarriers * 8 + 16;   // sums, barriers, words
   // tensor memory columns; the weighted scores take the scores' first half when D = 128
   static constexpr int kOut = 128, kRead = 128 + D, kAdd = 128 + 2 * D, kProb = D == 128 ? 0 : 320;
   static constexpr int kCols = D / 4;                           // of the state, a thread
 };
 
-// What the warps of a block take from the sums of a chunk's decays (in log2).
-struct alignas(8) Sums {
+// What the warps of a block take from the sums of a chunk's decays (in log2), and how the chunk lies.
+struct alignas(16) Sums {
   float d[kChunk];                 // from the start of the row's 32 rows to the row
   float after[kChunk];             // factor from the row to the end of its 32 rows
   float rest[kChunk];              // factor from the row to the end of the chunk
+  float from[kChunk];              // factor from the start of the chunk to the row
   float gap[16];                   // [block][earlier block]: from the end of the earlier one to the start of the block
-  float all, pad;                  // log decay of the chunk, natural
+  float factor;                    // of the chunk, less 1 if near
+  int near, valid, more;           // valid rows; whether the block has another chunk
+  int bad, pad[3];                 // whether values that are not finite were taken out
 };
 
 template <int D, bool kRows>
 __global__ void __launch_bounds__(kThreads, 1)
 prompt_kernel(const LinearParams p, const LinearPlan w, const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CUtensorMap kmap,
-              const __grid_constant__ CUtensorMap vmap, const __grid_constant__ CUtensorMap omap) {
+              const __grid_constant__ CUtensorMap vmap) {
   using S = Shape<D, kRows>;
   extern __shared__ __align__(1024) uint8_t smem[];
   const uint32_t base = smem_u32(smem);
   const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31, blocks = gridDim.x;
-  // (both on 16-byte boundaries, for rows by four)
-  float* from_start = reinterpret_cast<float*>(smem + S::kSmall);   // [2][kChunk]: factor from the chunk's start to the row
-  Sums& sums = *reinterpret_cast<Sums*>(from_start + 2 * kChunk);
-  uint32_t bar = smem_u32(&sums + 1);
+  Sums* sums_at = reinterpret_cast<Sums*>(smem + S::kSmall);   // [2]
+  uint32_t bar = smem_u32(sums_at + 2);
   auto take = [&](int n) { const uint32_t r = bar; bar += 8 * n; return r; };
   const uint32_t q_full = take(1), q_free = take(1), k_full = take(2), k_free = take(2), v_full = take(2), v_free = take(2), v_done = take(2);
-  const uint32_t sums_full = take(1), sums_free = take(1), s_full = take(1), p_full = take(1), o_full = take(1), o_free = take(1);
-  const uint32_t w_full = take(1), w_free = take(1), staged = take(2), state_full = take(1), state_read = take(1), add_full = take(1), end = take(1);
+  const uint32_t sums_full = take(2), sums_free = take(2), s_full = take(1), p_full = take(1), o_full = take(1), o_free = take(1);
+  const uint32_t w_full = take(2), w_free = take(2), state_full = take(1), state_read = take(1);
+  const uint32_t add_full = take(1), add_read = take(1), end = take(1);
   uint32_t* words = reinterpret_cast<uint32_t*>(smem + (bar - base));
   volatile int* dead = reinterpret_cast<volatile int*>(words);
-  volatile int* any_bad = reinterpret_cast<volatile int*>(words + 2);
   const int units = w.head[kRows ? 0 : 1];
+  // a first pass that gave up leaves the whole call without the outputs of this one
   const bool failed = kRows && w.head[2] != 0;
-  if ((int)blockIdx.x >= units) return;                         // the whole block
+  if ((int)blockIdx.x >= units || failed) return;               // the whole block
   if (base & 1023) {
     if (threadIdx.x == 0) {
       raise_status(p.status, MDW_ERR_UNSUPPORTED_SHAPE);
@@ -223,25 +237,23 @@ prompt_kernel(const LinearParams p, const LinearPlan w, const __grid_constant__ 
   if (threadIdx.x == 0) {
     prefetch_map(&kmap);
     prefetch_map(&vmap);
-    if (kRows) {
-      prefetch_map(&qmap);
-      prefetch_map(&omap);
-    }
+    if (kRows) prefetch_map(&qmap);
     for (int i = 0; i < 2; ++i) {
       mbar_init(k_full + 8 * i, 1);
       mbar_init(k_free + 8 * i, 1);
       mbar_init(v_full + 8 * i, 1);
-      mbar_init(v_free + 8 * i, kRows ? 1 : kStateWarps);
+      mbar_init(v_free + 8 * i, kStateWarps + (kRows ? 1 : 0));
       mbar_init(v_done + 8 * i, kStateWarps);
-      mbar_init(staged + 8 * i, 4);
-      any_bad[i] = 0;
+      mbar_init(w_full + 8 * i, kStateWarps / 2);
+      mbar_init(w_free + 8 * i, 1);
+      mbar_init(sums_full + 8 * i, 1);
+      mbar_init(sums_free + 8 * i, kStateWarps + (kRows ? 8 : 0));
     }
-    for (const uint32_t b : {q_full, q_free, s_full, o_full, w_free, state_read, add_full, end, sums_full}) mbar_init(b, 1);
-    mbar_init(sums_free, kStateWarps + (kRows ? 4 : 0));
+    for (const uint32_t b : {q_full, q_free, s_full, o_full, state_read, add_full, end}) mbar_init(b, 1);
     mbar_init(p_full, 4);
     mbar_init(o_free, 4);
-    mbar_init(w_full, kStateWarps);
     mbar_init(state_full, kStateWarps);
+    mbar_init(add_read, kStateWarps);
     *dead = 0;
     mbar_init_fence();
   }
@@ -253,32 +265,45 @@ prompt_kernel(const LinearParams p, const LinearPlan w, const __grid_constant__ 
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = __shfl_sync(0xffffffffu, words[1], 0);
-  auto wait = [&](uint32_t b, uint32_t parity) { mbar_wait(b, parity, p.spin_budget, p.status, dead); };
+  // As mbar_wait(), in line: around a call the state's registers would go to memory and come back.
+  auto wait = [&](uint32_t b, uint32_t parity) {
+    if (mbar_test(b, parity)) return;
+    const long long t0 = clock64();
+    while (!mbar_try(b, parity)) {
+      if (*dead) return;
+      if (clock64() - t0 > p.spin_budget) {
+        *dead = 1;
+        raise_status(p.status, MDW_ERR_TIMEOUT);
+        return;
+      }
+    }
+  };
   auto arrive = [&](uint32_t b) {                               // of the warp
     __syncwarp();
     if (lane == 0) mbar_arrive(b);
   };
   // Every role goes over the block's units and their chunks in the same order; g counts the chunks.
+  auto unit_of = [&](int k) {                                   // the block's k-th unit; `units` or more: none
+    return k * blocks + (k & 1 ? blocks - 1 - (int)blockIdx.x : (int)blockIdx.x);
+  };
+  auto entry_of = [&](int u) -> const LinearEntry& { return (kRows ? w.all : w.first)[u / p.H]; };
   auto each_unit = [&](auto&& unit) {
     int g = 0;
-    for (int k = 0; k * blocks < units; ++k) {
-      const int u = k * blocks + (k & 1 ? blocks - 1 - (int)blockIdx.x : (int)blockIdx.x);
-      if (u >= units) break;
-      const LinearEntry e = (kRows ? w.all : w.first)[u / p.H];
-      if (failed && e.segs > 1) continue;
-      const int chunks = (e.rows + kChunk - 1) / kChunk;
-      unit(e, u % p.H, chunks, g);
+    for (int k = 0; unit_of(k) < units; ++k) {
+      const int chunks = (entry_of(unit_of(k)).rows + kChunk - 1) / kChunk;
+      unit(unit_of(k), chunks, g, k);
       g += chunks;
     }
-    return g;
   };
 
   if (warp == 0) {
     // ---- copies
     int asked[3] = {0, 0, 0};                                   // tiles of k, v and q
-    each_unit([&](const LinearEntry& e, int h, int chunks, int g0) {
+    each_unit([&](int u, int chunks, int g0, int k) {
+      const int h = u % p.H, row0 = entry_of(u).row0;
       for (int c = 0; c < chunks; ++c) {
-        const int g = g0 + c, slot = g & 1, ks = g % S::kKeys, row = e.row0 + c * kChunk;
+        const int g = g0 + c, slot = g & 1, row = row0 + c * kChunk;
+        const uint32_t again = (g >> 1 & 1) ^ 1;
         auto load = [&](int which, uint32_t to, const CUtensorMap* map, uint32_t full, uint32_t free, uint32_t parity, int head) {
           wait(free, parity);
           if (__any_sync(0xffffffffu, *dead)) return;
@@ -290,25 +315,25 @@ prompt_kernel(const LinearParams p, const LinearPlan w, const __grid_constant__ 
           __syncwarp();
           ++asked[which];
         };
-        load(1, base + S::kV + slot * S::kTile, &vmap, v_full + 8 * slot, v_free + 8 * slot, (g >> 1 & 1) ^ 1, h);
-        load(0, base + S::kK + ks * S::kTile, &kmap, k_full + 8 * ks, k_free + 8 * ks, (g / S::kKeys & 1) ^ 1, h / p.share);
+        load(1, base + S::kV + slot * S::kTile, &vmap, v_full + 8 * slot, v_free + 8 * slot, again, h);
+        load(0, base + S::kK + slot * S::kTile, &kmap, k_full + 8 * slot, k_free + 8 * slot, again, h / p.share);
         if (kRows) load(2, base + S::kQ, &qmap, q_full, q_free, (g & 1) ^ 1, h / p.share);
       }
     });
     // every copy arrives before the block ends, also where a wait ran out
     for (int i = 0; i < 2; ++i) {
-      const int k = S::kKeys == 2 ? (asked[0] + 1 - i) >> 1 : i == 0 ? asked[0] : 0, v = (asked[1] + 1 - i) >> 1;
-      if (k > 0) mbar_drain(k_full + 8 * i, (k - 1) & 1);
-      if (v > 0) mbar_drain(v_full + 8 * i, (v - 1) & 1);
+      const int k = (asked[0] + 1 - i) >> 1, v = (asked[1] + 1 - i) >> 1;
+      if (k > 0) mbar_drain_inline(k_full + 8 * i, (k - 1) & 1);
+      if (v > 0) mbar_drain_inline(v_full + 8 * i, (v - 1) & 1);
     }
-    if (asked[2] > 0) mbar_drain(q_full, (asked[2] - 1) & 1);
+    if (asked[2] > 0) mbar_drain_inline(q_full, (asked[2] - 1) & 1);
   } else if (warp == 1) {
     // ---- products
-    each_unit([&](const LinearEntry& e, int h, int chunks, int g0) {
+    each_unit([&](int u, int chunks, int g0, int k) {
       for (int c = 0; c < chunks; ++c) {
-        const int g = g0 + c, ks = g % S::kKeys;
-        const uint32_t q_at = base + S::kQ, k_at = base + S::kK + ks * S::kTile, v_at = base + S::kV + (g & 1) * S::kTile;
-        wait(k_full + 8 * ks, g / S::kKeys & 1);
+        const int g = g0 + c, slot = g & 1;
+        const uint32_t q_at = base + S::kQ, k_at = base + S::kK + slot * S::kTile, v_at = base + S::kV + slot * S::kTile;
+        wait(k_full + 8 * slot, g >> 1 & 1);
         if (kRows) {
           wait(q_full, g & 1);
           if (g > 0) wait(o_full, (g - 1) & 1);                 // (the weighted scores lie in the scores' columns)
@@ -323,60 +348,71 @@ prompt_kernel(const LinearParams p, const LinearPlan w, const __grid_constant__ 
             tc_commit(s_full);
           }
           __syncwarp();
-          wait(state_full, g & 1);
-          wait(o_free, (g & 1) ^ 1);
+        }
+        if (g > 0) wait(add_read, (g - 1) & 1);                 // (and the sums of the last chunk out of their columns)
+#pragma unroll 1
+        for (int step = 0; step < S::kSteps; ++step) {
+          const int use = g * S::kSteps + step, at = use & 1;
+          wait(w_full + 8 * at, use >> 1 & 1);
           tc_fence_after();
           if (elect_one()) {
-            const uint32_t ql = operand_low(q_at, 16), sl = operand_low(base + S::kS, D * 128);
-#pragma unroll
-            for (int t = 0; t < D / 16; ++t)
-              tc_mma(tmem + S::kRead, ql + (((t >> 2) * (kChunk * 128) + (t & 3) * 32) >> 4), sl + t * (2048 >> 4), mma_shape(true, true, D), t > 0);
-            tc_commit(state_read);
-            tc_commit(q_free);
-          }
-          __syncwarp();
-        }
-#pragma unroll
-        for (int part = 0; part < 3; ++part) {
-          if (part != 1) {
-            wait(w_full, part >> 1);
-            tc_fence_after();
-          }
-          if (elect_one()) {
             // k is the first operand transposed: 64 of its columns at a time (heads of 64: the second 64 lie behind the tile, and what they
-            // hold only reaches lanes that are not read)
-            const uint32_t kl = operand_low(k_at, kChunk * 128), wl = operand_low(base + S::kW + (part & 1) * S::kTile, kChunk * 128);
+            // hold only reaches lanes that are not read). The smallest part of the values is summed first.
+            const uint32_t kl = operand_low(k_at + step * (S::kStep * 128), kChunk * 128);
 #pragma unroll
-            for (int t = 0; t < kChunk / 16; ++t)
-              tc_mma(tmem + S::kAdd, kl + t * (2048 >> 4), wl + t * (2048 >> 4), mma_shape(true, true, D) | 1u << 15, part > 0 || t > 0);
-            if (part == 0) tc_commit(w_free);
-            if (part == 2) {
+            for (int part = 0; part < 3; ++part) {
+              const uint32_t wl = operand_low(base + S::kW + (3 * at + part) * S::kPart, S::kStep * 128);
+#pragma unroll
+              for (int i = 0; i < S::kStep / 16; ++i)
+                tc_mma(tmem + S::kAdd, kl + i * (2048 >> 4), wl + i * (2048 >> 4), mma_shape(true, true, D) | 1u << 15, step > 0 || part > 0 || i > 0);
+            }
+            tc_commit(w_free + 8 * at);
+            if (step == S::kSteps - 1) {
               tc_commit(add_full);
-              tc_commit(k_free + 8 * ks);
+              tc_commit(k_free + 8 * slot);
             }
           }
           __syncwarp();
-          if (kRows && part == 1) {
-            wait(p_full, g & 1);
+          if (kRows && step == 1) {
+            // what the rows read of the state, while the other steps are converted
+            wait(state_full, g & 1);
+            wait(o_free, (g & 1) ^ 1);
             tc_fence_after();
             if (elect_one()) {
-              const uint32_t vl = operand_low(v_at, kChunk * 128);
+              const uint32_t ql = operand_low(q_at, 16), sl = operand_low(base + S::kS, D * 128);
 #pragma unroll
-              for (int t = 0; t < kChunk / 16; ++t)
-                tc_mma_tmem(tmem + S::kOut, tmem + S::kProb + 8 * t, vl + t * (2048 >> 4), mma_shape(true, true, D), t > 0);
-              tc_commit(o_full);
+              for (int i = 0; i < D / 16; ++i)
+                tc_mma(tmem + S::kRead, ql + (((i >> 2) * (kChunk * 128) + (i & 3) * 32) >> 4), sl + i * (2048 >> 4), mma_shape(true, true, D), i > 0);
+              tc_commit(state_read);
+              tc_commit(q_free);
             }
             __syncwarp();
           }
+        }
+        if (kRows) {
+          wait(p_full, g & 1);
+          tc_fence_after();
+          if (elect_one()) {
+            const uint32_t vl = operand_low(v_at, kChunk * 128);
+#pragma unroll
+            for (int i = 0; i < kChunk / 16; ++i)
+              tc_mma_tmem(tmem + S::kOut, tmem + S::kProb + 8 * i, vl + i * (2048 >> 4), mma_shape(true, true, D), i > 0);
+            tc_commit(o_full);
+            tc_commit(v_free + 8 * slot);
+          }
+          __syncwarp();
         }
       }
     });
     if (lane == 0) tc_commit(end);
     __syncwarp();
-    mbar_drain(end, 0);                                         // nothing is in flight when the columns are given back
+    mbar_drain_inline(end, 0);                                         // nothing is in flight when the columns are given back
   } else if (warp == 2) {
     // ---- sums of the decays: a lane has four rows
-    each_unit([&](const LinearEntry& e, int h, int chunks, int g0) {
+    each_unit([&](int u, int chunks, int g0, int k) {
+      const int h = u % p.H;
+      const LinearEntry e = entry_of(u);
+      const bool others = unit_of(k + 1) < units;
       double unit = 0.0;
       for (int c = 0; c < chunks; ++c) {
         const int g = g0 + c;
@@ -412,53 +448,37 @@ prompt_kernel(const LinearParams p, const LinearPlan w, const __grid_constant__ 
         }
         // [lane >> 2][lane & 3], lanes below 16
         const double start_a = __shfl_sync(0xffffffffu, before, (lane >> 2 & 3) * 8), stop_b = __shfl_sync(0xffffffffu, sum, (lane & 3) * 8 + 7);
-        if (kRows) {
-          wait(staged + 8 * (g & 1), (g >> 1 & 1) ^ 1);         // the outputs of the chunk before the last have read theirs
-          *reinterpret_cast<float4*>(&from_start[(g & 1) * kChunk + 4 * lane]) = make_float4(from[0], from[1], from[2], from[3]);
-        }
-        wait(sums_free, (g & 1) ^ 1);
+        const Decay whole((float)(last * 0.69314718055994530942));
+        const bool more = c + 1 < chunks || others;
+        wait(sums_free + 8 * (g & 1), (g >> 1 & 1) ^ 1);
+        Sums& sums = sums_at[g & 1];
         *reinterpret_cast<float4*>(&sums.d[4 * lane]) = make_float4(d[0], d[1], d[2], d[3]);
         *reinterpret_cast<float4*>(&sums.after[4 * lane]) = make_float4(after[0], after[1], after[2], after[3]);
         *reinterpret_cast<float4*>(&sums.rest[4 * lane]) = make_float4(rest[0], rest[1], rest[2], rest[3]);
+        *reinterpret_cast<float4*>(&sums.from[4 * lane]) = make_float4(from[0], from[1], from[2], from[3]);
         if (lane < 16) sums.gap[lane] = (float)(start_a - stop_b);
-        if (lane == 0) sums.all = (float)(last * 0.69314718055994530942);
+        if (lane == 0) {
+          sums.factor = whole.f;
+          sums.near = whole.near;
+          sums.valid = min(e.rows - c * kChunk, kChunk);
+          sums.more = more;
+          sums.bad = 0;
+        }
         unit += last;
-        arrive(sums_full);
+        arrive(sums_full + 8 * (g & 1));
       }
       if (!kRows && lane == 0) w.logs[(size_t)(e.set + e.seg + 1) * p.H + h] = (float)(unit * 0.69314718055994530942);
     });
-  } else if (warp == 3) {
-    // ---- outputs of whole chunks to memory, and the place of the values free again
-    if (kRows) {
-      each_unit([&](const LinearEntry& e, int h, int chunks, int g0) {
-        for (int c = 0; c < chunks; ++c) {
-          const int g = g0 + c, slot = g & 1;
-          wait(staged + 8 * slot, g >> 1 & 1);
-          if (lane == 0) {
-            any_bad[slot] = 0;
-            if (e.rows - c * kChunk >= kChunk && !*dead) {
-#pragma unroll
-              for (int i = 0; i < S::kHalves; ++i)
-                tma_store(&omap, base + S::kV + slot * S::kTile + i * (kChunk * 128), 64 * i, h, e.row0 + c * kChunk);
-              asm volatile("cp.async.bulk.commit_group;" ::: "memory");
-              asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
-            }
-            mbar_arrive(v_free + 8 * slot);
-          }
-          __syncwarp();
-        }
-      });
-      if (lane == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
-    }
   } else if (warp >= 4 && warp < 8) {
     // ---- weights of the scores: thread = row; 32 columns at a time, none above the diagonal
     if (kRows) {
       const int own = warp & 3;
       const uint32_t lanes = (uint32_t)own * 32 << 16;
-      each_unit([&](const LinearEntry& e, int h, int chunks, int g0) {
+      each_unit([&](int u, int chunks, int g0, int k) {
         for (int c = 0; c < chunks; ++c) {
           const int g = g0 + c;
-          wait(sums_full, g & 1);
+          wait(sums_full + 8 * (g & 1), g >> 1 & 1);
+          const Sums& sums = sums_at[g & 1];
           wait(s_full, g & 1);
           tc_fence_after();
           const float d = sums.d[own * 32 + lane];
@@ -494,7 +514,7 @@ prompt_kernel(const LinearParams p, const LinearPlan w, const __grid_constant__ 
           tc_wait_st();
           tc_fence_before();
           arrive(p_full);
-          arrive(sums_free);
+          arrive(sums_free + 8 * (g & 1));
         }
       });
     }
@@ -503,15 +523,17 @@ prompt_kernel(const LinearParams p, const LinearPlan w, const __grid_constant__ 
     if (kRows) {
       const int own = warp & 3, row = own * 32 + lane;
       const uint32_t lanes = (uint32_t)own * 32 << 16;
-      each_unit([&](const LinearEntry& e, int h, int chunks, int g0) {
+      each_unit([&](int u, int chunks, int g0, int k) {
+        const int h = u % p.H, row0 = entry_of(u).row0;
         for (int c = 0; c < chunks; ++c) {
-          const int g = g0 + c, slot = g & 1, valid = min(e.rows - c * kChunk, kChunk), first = e.row0 + c * kChunk;
-          const uint32_t stage = base + S::kV + slot * S::kTile;
+          const int g = g0 + c, slot = g & 1, first = row0 + c * kChunk;
+          wait(sums_full + 8 * slot, g >> 1 & 1);
+          const float f = p.scale * sums_at[slot].from[row];
+          const int valid = sums_at[slot].valid;
           wait(v_done + 8 * slot, g >> 1 & 1);
           wait(o_full, g & 1);
           tc_fence_after();
-          const float f = p.scale * from_start[slot * kChunk + row];
-          const bool whole = valid == kChunk, store = row < valid && !*dead;
+          const bool bad = sums_at[slot].bad, store = row < valid && !*dead;
           __nv_bfloat16* dst = p.out + (int64_t)(first + min(row, valid - 1)) * p.ldo + (int64_t)h * D;
 #pragma unroll 1
           for (int i = 0; i < D; i += 16) {
@@ -522,27 +544,28 @@ prompt_kernel(const LinearParams p, const LinearPlan w, const __grid_constant__ 
             uint32_t x[8];
 #pragma unroll
             for (int j = 0; j < 16; j += 2) x[j / 2] = pack(fma(Pair(u[j], u[j + 1]), Pair(f, f), Pair(o[j], o[j + 1]) * Pair(p.scale, p.scale)));
-            if (any_bad[slot]) {
+            if (bad) {
               // rare: values that are not finite, which were left out; they make what comes after them in their column so
 #pragma unroll
               for (int j = 0; j < 16; ++j) {
                 const __nv_bfloat16* v = p.v + (int64_t)first * p.ldv + (int64_t)h * D + i + j;
-                for (int k = 0; k <= min(row, valid - 1); ++k)
-                  if (!isfinite(__bfloat162float(v[(int64_t)k * p.ldv]))) x[j / 2] |= j & 1 ? 0x7fff0000u : 0x7fffu;
+                for (int before = 0; before <= min(row, valid - 1); ++before)
+                  if (!isfinite(__bfloat162float(v[(int64_t)before * p.ldv]))) x[j / 2] |= j & 1 ? 0x7fff0000u : 0x7fffu;
               }
             }
-#pragma unroll
-            for (int j = 0; j < 2; ++j) {
-              const int piece = (i >> 3) + j;
-              const uint4 y = make_uint4(x[4 * j], x[4 * j + 1], x[4 * j + 2], x[4 * j + 3]);
-              if (whole) sts16(stage + (piece >> 3) * (kChunk * 128) + row * 128 + (((piece & 7) ^ (row & 7)) << 4), y);
-              else if (store) *reinterpret_cast<uint4*>(dst + i + 8 * j) = y;
+            if (store) {
+              if (p.wide) {                                     // rows on 32-byte boundaries
+                asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};"
+                             :: "l"(dst + i), "r"(x[0]), "r"(x[1]), "r"(x[2]), "r"(x[3]), "r"(x[4]), "r"(x[5]), "r"(x[6]), "r"(x[7]) : "memory");
+              } else {
+                *reinterpret_cast<uint4*>(dst + i) = make_uint4(x[0], x[1], x[2], x[3]);
+                *reinterpret_cast<uint4*>(dst + i + 8) = make_uint4(x[4], x[5], x[6], x[7]);
+              }
             }
           }
           tc_fence_before();
           arrive(o_free);
-          fence_async_proxy();
-          arrive(staged + 8 * slot);
+          arrive(sums_free + 8 * slot);
         }
       });
     }
@@ -551,8 +574,8 @@ prompt_kernel(const LinearParams p, const LinearPlan w, const __grid_constant__ 
     const int quad = warp & 3, a = quad * 32 + lane, col0 = ((warp - 12) >> 2) * S::kCols;
     const bool holds = quad * 32 < D;
     const uint32_t lanes = (uint32_t)quad * 32 << 16;
-    const int id = threadIdx.x - 384, piece = id & 7, row0 = id >> 3;
-    const uint32_t place = row0 * 128 + ((piece ^ (row0 & 7)) << 4);
+    const int group = (warp - 12) >> 3, id = threadIdx.x - 384 & 255, piece = id & 7, row0 = (id >> 3) & (S::kStep - 1), part0 = (id >> 3) / S::kStep;
+    const uint32_t swizzled = row0 * 128 + ((piece ^ (row0 & 7)) << 4);
     float s[S::kCols];
     auto at_state = [&](float* pool, int64_t first) { return pool + first + ((int64_t)a * D + col0); };
     auto load_state = [&](const float* src) {
@@ -579,87 +602,88 @@ prompt_kernel(const LinearParams p, const LinearPlan w, const __grid_constant__ 
       fence_async_proxy();
       arrive(state_full);
     };
-    each_unit([&](const LinearEntry& e, int h, int chunks, int g0) {
+    // The decayed values of a step of rows as three bf16 numbers, by 8 of the warps; two steps ahead of the state.
+    auto convert = [&](int g, int step) {
+      const int slot = g & 1, use = g * S::kSteps + step, at = group;
+      if (step == group) {
+        wait(sums_full + 8 * slot, g >> 1 & 1);
+        wait(v_full + 8 * slot, g >> 1 & 1);
+      }
+      const Sums& sums = sums_at[slot];
+      const int row = step * S::kStep + row0;
+      const uint32_t off = part0 * (kChunk * 128) + step * (S::kStep * 128) + swizzled, v_at = base + S::kV + slot * S::kTile + off;
+      const uint32_t to = base + S::kW + 3 * at * S::kPart + part0 * (S::kStep * 128) + swizzled;
+      uint4 v = lds16(v_at);
+      if (row >= sums.valid) {
+        // rows behind the last are another request's, or nobody's
+        v = make_uint4(0u, 0u, 0u, 0u);
+        wait(k_full + 8 * slot, g >> 1 & 1);
+        sts16(v_at, v);
+        sts16(base + S::kK + slot * S::kTile + off, v);
+      }
+      const float rest = sums.rest[row];
+      const Pair by(rest, rest), minus(-1.f, -1.f);
+      Pair x[4] = {unpack(v.x) * by, unpack(v.y) * by, unpack(v.z) * by, unpack(v.w) * by}, none(0.f, 0.f);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) none = fma(x[i], Pair(0.f, 0.f), none);
+      const bool odd = !(none.floats().x == 0.f && none.floats().y == 0.f);
+      uint4 non = make_uint4(0u, 0u, 0u, 0u);
+      if (odd) {
+        // values that are not finite leave the product with the scores, where they would reach earlier rows too
+        const uint32_t m = 0x7f807f80u;
+        non = make_uint4(__vcmpeq2(v.x & m, m), __vcmpeq2(v.y & m, m), __vcmpeq2(v.z & m, m), __vcmpeq2(v.w & m, m));
+        v = make_uint4(v.x & ~non.x, v.y & ~non.y, v.z & ~non.z, v.w & ~non.w);
+        if (kRows) {
+          sts16(v_at, v);
+          sums_at[slot].bad = 1;
+        }
+        x[0] = unpack(v.x) * by, x[1] = unpack(v.y) * by, x[2] = unpack(v.z) * by, x[3] = unpack(v.w) * by;
+      }
+      wait(w_free + 8 * at, (use >> 1 & 1) ^ 1);
+      // 8 leading bits at a time: the three parts are the whole number
+#pragma unroll
+      for (int part = 2; part >= 0; --part) {
+        uint32_t word[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const float2 f = x[i].floats();
+          word[i] = __byte_perm(__float_as_uint(f.x), __float_as_uint(f.y), 0x7632);
+          if (part > 0) x[i] = fma(Pair(__uint_as_float(__float_as_uint(f.x) & 0xffff0000u), __uint_as_float(__float_as_uint(f.y) & 0xffff0000u)), minus, x[i]);
+        }
+        if (part == 0 && odd) word[0] |= non.x & 0x7fff7fffu, word[1] |= non.y & 0x7fff7fffu, word[2] |= non.z & 0x7fff7fffu, word[3] |= non.w & 0x7fff7fffu;
+        sts16(to + part * S::kPart, make_uint4(word[0], word[1], word[2], word[3]));
+      }
+      fence_async_proxy();
+      arrive(w_full + 8 * at);
+    };
+    convert(0, group);
+    each_unit([&](int u, int chunks, int g0, int k) {
 #pragma unroll
       for (int i = 0; i < S::kCols; ++i) s[i] = 0.f;
       if (holds) {
+        const int h = u % p.H;
+        const LinearEntry e = entry_of(u);
         const int64_t own = (int64_t)h * D * D;
         if (e.seg == 0 && (!kRows || e.segs == 1)) {
           if (e.slot_in >= 0) load_state(at_state(p.s, e.slot_in * p.slot_stride + own));
           // (the last segment may store to the slot before the first one reads it)
           if (!kRows) store_state(set_at(e.set, h));
         } else if (kRows) {
-          load_state(set_at(e.set + min(e.seg, 1), h));
-          for (int i = 2; i <= e.seg; ++i) {
-            const Decay f(w.logs[(size_t)(e.set + i) * p.H + h]);
-            const float* add = set_at(e.set + i, h);
-#pragma unroll
-            for (int j = 0; j < S::kCols; j += 4) {
-              const float4 x = *reinterpret_cast<const float4*>(add + j);
-              s[j] = fmaf(s[j], f.f, f.near ? s[j] : 0.f) + x.x;
-              s[j + 1] = fmaf(s[j + 1], f.f, f.near ? s[j + 1] : 0.f) + x.y;
-              s[j + 2] = fmaf(s[j + 2], f.f, f.near ? s[j + 2] : 0.f) + x.z;
-              s[j + 3] = fmaf(s[j + 3], f.f, f.near ? s[j + 3] : 0.f) + x.w;
-            }
-          }
+          load_state(set_at(e.set + e.seg, h));
         }
       }
       if (kRows) publish(g0);
       for (int c = 0; c < chunks; ++c) {
-        const int g = g0 + c, slot = g & 1, valid = min(e.rows - c * kChunk, kChunk);
-        const uint32_t v_at = base + S::kV + slot * S::kTile + place, w_at = base + S::kW + place, k_at = base + S::kK + g % S::kKeys * S::kTile + place;
-        wait(sums_full, g & 1);
-        const float rest[2] = {sums.rest[row0], sums.rest[row0 + 64]};
-        const Decay f(sums.all);
-        arrive(sums_free);
-        wait(v_full + 8 * slot, g >> 1 & 1);
-        if (valid < kChunk) wait(k_full + 8 * (g % S::kKeys), g / S::kKeys & 1);
-        // The decayed values as three bf16 numbers. The smallest part is summed first; the largest takes its place then.
-        uint4 largest[S::kHalves * 2];
-#pragma unroll
-        for (int n = 0; n < S::kHalves * 2; ++n) {
-          const uint32_t off = (n >> 1) * (kChunk * 128) + (n & 1) * (64 * 128);
-          uint4 v = lds16(v_at + off);
-          const uint32_t m = 0x7f807f80u;
-          uint4 non = make_uint4(__vcmpeq2(v.x & m, m), __vcmpeq2(v.y & m, m), __vcmpeq2(v.z & m, m), __vcmpeq2(v.w & m, m));
-          if (row0 + 64 * (n & 1) >= valid) {
-            // rows behind the last are another request's, or nobody's
-            v = non = make_uint4(0u, 0u, 0u, 0u);
-            sts16(v_at + off, v);
-            sts16(k_at + off, v);
-          } else if (non.x | non.y | non.z | non.w) {
-            // values that are not finite leave the product with the scores, where they would reach earlier rows too
-            v = make_uint4(v.x & ~non.x, v.y & ~non.y, v.z & ~non.z, v.w & ~non.w);
-            if (kRows) {
-              sts16(v_at + off, v);
-              any_bad[slot] = 1;
-            }
-          }
-          const uint32_t word[4] = {v.x, v.y, v.z, v.w}, odd[4] = {non.x, non.y, non.z, non.w};
-          uint32_t part[3][4];
-          const Pair by(rest[n & 1], rest[n & 1]), minus(-1.f, -1.f);
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            Pair x = unpack(word[i]) * by;
-            part[2][i] = pack(x);
-            x = fma(unpack(part[2][i]), minus, x);
-            part[1][i] = pack(x);
-            x = fma(unpack(part[1][i]), minus, x);
-            part[0][i] = pack(x) | (odd[i] & 0x7fff7fffu);
-          }
-          sts16(w_at + off, make_uint4(part[0][0], part[0][1], part[0][2], part[0][3]));
-          sts16(w_at + S::kTile + off, make_uint4(part[1][0], part[1][1], part[1][2], part[1][3]));
-          largest[n] = make_uint4(part[2][0], part[2][1], part[2][2], part[2][3]);
-        }
-        fence_async_proxy();
-        arrive(w_full);
-        arrive(v_done + 8 * slot);
-        if (!kRows) arrive(v_free + 8 * slot);
-        wait(w_free, g & 1);
-#pragma unroll
-        for (int n = 0; n < S::kHalves * 2; ++n) sts16(w_at + (n >> 1) * (kChunk * 128) + (n & 1) * (64 * 128), largest[n]);
-        fence_async_proxy();
-        arrive(w_full);
+        const int g = g0 + c;
+        for (int step = 2 + group; step < S::kSteps; step += 2) convert(g, step);
+        const Sums& sums = sums_at[g & 1];
+        const float f = sums.factor;
+        const float keep = sums.near ? 1.f : 0.f;
+        const bool more = sums.more;
+        arrive(sums_free + 8 * (g & 1));
+        arrive(v_done + 8 * (g & 1));
+        arrive(v_free + 8 * (g & 1));
+        if (more) convert(g + 1, group);
         wait(add_full, g & 1);
         tc_fence_after();
         if (holds)
@@ -670,17 +694,19 @@ prompt_kernel(const LinearParams p, const LinearPlan w, const __grid_constant__ 
             tc_wait_ld();
 #pragma unroll
             for (int j = 0; j < 16; j += 2) {
-              const Pair was(s[i + j], s[i + j + 1]);
-              Pair now = fma(was, Pair(f.f, f.f), Pair(x[j], x[j + 1]));
-              if (f.near) now = now + was;
+              // (keep: 1 where the factor is given less 1; a branch would cost the registers of both ways)
+              const Pair was(s[i + j], s[i + j + 1]), now = fma(was, Pair(keep, keep), fma(was, Pair(f, f), Pair(x[j], x[j + 1])));
               s[i + j] = now.floats().x;
               s[i + j + 1] = now.floats().y;
             }
           }
         tc_fence_before();
+        arrive(add_read);
         if (kRows && c + 1 < chunks) publish(g + 1);
       }
       if (holds && !*dead) {
+        const int h = u % p.H;
+        const LinearEntry e = entry_of(u);
         if (!kRows) store_state(set_at(e.set + e.seg + 1, h));
         else if (e.seg == e.segs - 1 && e.slot_out >= 0) store_state(at_state(p.s, e.slot_out * p.slot_stride + (int64_t)h * D * D));
       }
@@ -707,23 +733,28 @@ bool encode_rows(CUtensorMap* map, const void* data, int64_t ld, int heads, int 
 }
 
 template <int D>
-cudaError_t launch(const LinearParams& p, const LinearPlan& w, const CUtensorMap (&m)[4], int grid, int dev, bool segments, cudaStream_t s) {
+cudaError_t launch(const LinearParams& p, const LinearPlan& w, const CUtensorMap (&m)[3], int grid, int dev, bool segments, cudaStream_t s) {
   cudaError_t e = allow_shared_memory<prompt_kernel<D, true>>(dev);
   if (e == cudaSuccess) e = allow_shared_memory<prompt_kernel<D, false>>(dev);
   if (e != cudaSuccess) return e;
   plan_kernel<<<1, 1024, 0, s>>>(p, w, grid);
-  if (segments) prompt_kernel<D, false><<<grid, kThreads, Shape<D, false>::kSmem, s>>>(p, w, m[0], m[1], m[2], m[3]);
-  prompt_kernel<D, true><<<grid, kThreads, Shape<D, true>::kSmem, s>>>(p, w, m[0], m[1], m[2], m[3]);
+  if (segments) {
+    prompt_kernel<D, false><<<grid, kThreads, Shape<D, false>::kSmem, s>>>(p, w, m[0], m[1], m[2]);
+    sums_kernel<<<grid, 256, 0, s>>>(w, p.H, D * D);
+  }
+  prompt_kernel<D, true><<<grid, kThreads, Shape<D, true>::kSmem, s>>>(p, w, m[0], m[1], m[2]);
   return cudaGetLastError();
 }
 
 }  // namespace
 
-cudaError_t launch_prompts(const LinearParams& p, const LinearPlan& w, int D, int grid, int dev, cudaStream_t s) {
-  static_assert(sizeof(Sums) == 3 * kChunk * 4 + 18 * 4 && Shape<128, true>::kSmem <= 227 * 1024, "");
-  CUtensorMap m[4];
+cudaError_t launch_prompts(const LinearParams& p0, const LinearPlan& w, int D, int grid, int dev, cudaStream_t s) {
+  static_assert(sizeof(Sums) == 4 * kChunk * 4 + 24 * 4 && Shape<128, true>::kSmem <= 227 * 1024, "");
+  LinearParams p = p0;
+  p.wide = (reinterpret_cast<uintptr_t>(p.out) | (uintptr_t)p.ldo * 2) % 32 == 0;
+  CUtensorMap m[3];
   if (!encode_rows(&m[0], p.q, p.ldq, p.H / p.share, D, p.T) || !encode_rows(&m[1], p.k, p.ldk, p.H / p.share, D, p.T) ||
-      !encode_rows(&m[2], p.v, p.ldv, p.H, D, p.T) || !encode_rows(&m[3], p.out, p.ldo, p.H, D, p.T))
+      !encode_rows(&m[2], p.v, p.ldv, p.H, D, p.T))
     return cudaErrorInvalidValue;
   // a request has two segments only where its chunks are two shares, a share being the chunks of all units over the SMs
   const bool segments = p.H <= grid / 2 && p.max_new > (2 * kLinearSegment - 1) * kChunk;
