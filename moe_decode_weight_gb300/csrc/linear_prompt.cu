@@ -4,7 +4,7 @@
 //   o_i = scale ( sum_{j <= i} e^{c_i - c_j} (q_i . k_j) v_j + e^{c_i} S^T q_i ),
 //   S'  = e^{c_last} S + sum_j k_j (e^{c_last - c_j} v_j)^T.
 // Four products of a chunk: scores Q K^T (128 x 128), weighted by the decays, times V; Q times the state; K^T times
-// the decayed values. Sums of log decays are in 64 bits and only differences leave them, so none of their digits
+// the decayed values. Sums of log decays have 48 bits and only differences leave them, so none of their digits
 // are lost; no factor is above 1, so nothing overflows and what underflows would have underflown.
 //
 // Roundings to bf16, the operands' type: the weighted scores and the state as the outputs read it (outputs are off by 0.0022 of
@@ -19,8 +19,9 @@
 // What bounds it: 4 rows of D 16-bit elements in and out for each row, and as floor of a chunk the chain of the state
 // (values decayed, three products, state scaled and rounded). Roles of a block:
 //   warp 0       requests the tiles of q, k and v by TMA (swizzled, 128 rows x 128 bytes)
-//   warp 1       issues the products
+//   warp 1       issues the products for the state
 //   warp 2       sums the decays of the next chunk
+//   warp 3       issues the products for the outputs
 //   warps 4-7    weights the scores, one thread a row
 //   warps 8-11   the outputs, one thread a row
 //   warps 12-27  the decayed values and the state, four threads a row of the state
@@ -83,6 +84,25 @@ __device__ __forceinline__ uint32_t pack(Pair a) {
   const float2 f = a.floats();
   return pack(f.x, f.y);
 }
+
+// A sum of log decays in two fp32 numbers, 48 bits: only differences of sums are used, and those of long ones would lose their digits.
+// (64-bit additions take 16 cycles of issue each here, and the sums of a chunk took longer than all else.)
+struct Sum {
+  float hi, lo;
+  // v * log2(e)
+  static __device__ __forceinline__ Sum log2_of_e_to(float v) {
+    const float h = v * 1.44269502162933349609375f;             // log2(e) = this + 1.9259629...e-8
+    return {h, fmaf(v, 1.44269502162933349609375f, -h) + v * 1.92596303339e-8f};
+  }
+  __device__ __forceinline__ Sum operator+(Sum b) const {
+    const float s = __fadd_rn(hi, b.hi), t = __fsub_rn(s, hi);
+    const float e = __fadd_rn(__fadd_rn(__fsub_rn(hi, __fsub_rn(s, t)), __fsub_rn(b.hi, t)), __fadd_rn(lo, b.lo));
+    const float h = __fadd_rn(s, e);
+    return {h, __fsub_rn(e, __fsub_rn(h, s))};
+  }
+  __device__ __forceinline__ float less(Sum b) const { return __fadd_rn(__fsub_rn(hi, b.hi), __fsub_rn(lo, b.lo)); }
+  __device__ __forceinline__ float natural() const { return fmaf(hi, kLn2, lo * kLn2) + hi * -1.9046542e-9f; }
+};
 
 // ------------------------------------------------------------------ the units
 
@@ -187,10 +207,10 @@ struct Shape {
   static constexpr int kTile = kChunk * D * 2, kHalves = D / 64;
   static constexpr int kStep = 32 / kHalves, kSteps = kChunk / kStep, kPart = kStep * D * 2;
   static constexpr int kQ = 0, kK = kTile, kV = 3 * kTile, kW = 5 * kTile, kS = kW + 6 * kPart;
-  static constexpr int kSmall = kS + D * D * 2, kBarriers = 29;
-  static constexpr int kSmem = kSmall + 2 * (4 * kChunk * 4 + 24 * 4) + kBarriers * 8 + 16;   // sums, barriers, words
-  // tensor memory columns; the weighted scores take the scores' first half when D = 128
-  static constexpr int kOut = 128, kRead = 128 + D, kAdd = 128 + 2 * D, kProb = D == 128 ? 0 : 320;
+  static constexpr int kSmall = kS + D * D * 2, kBarriers = 32;
+  static constexpr int kSmem = kSmall + 2 * (5 * kChunk * 4 + 28 * 4) + kBarriers * 8 + 16;   // sums, barriers, words
+  // tensor memory columns: scores (the weighted ones take their first half when D = 128), two outputs, what a chunk adds to the state
+  static constexpr int kOut = 128, kAdd = 128 + 2 * D, kProb = D == 128 ? 0 : 320;
   static constexpr int kCols = D / 4;                           // of the state, a thread
 };
 
@@ -199,11 +219,16 @@ struct alignas(16) Sums {
   float d[kChunk];                 // from the start of the row's 32 rows to the row
   float after[kChunk];             // factor from the row to the end of its 32 rows
   float rest[kChunk];              // factor from the row to the end of the chunk
-  float from[kChunk];              // factor from the start of the chunk to the row
+  // A row's outputs are summed without its factor from the chunk's start, 2^c: scores count 2^(-c), what the row reads of the state
+  // 1, and the sum is scaled. Where c is below -60 a power of two of it, 2^down, is left to the row of q instead.
+  float lift[kChunk];              // down - c
+  float from[kChunk];              // 2^(c - down)
   float gap[16];                   // [block][earlier block]: from the end of the earlier one to the start of the block
+  float base[4];                   // from the start of the chunk to the start of the block
   float factor;                    // of the chunk, less 1 if near
   int near, valid, more;           // valid rows; whether the block has another chunk
-  int bad, pad[3];                 // whether values that are not finite were taken out
+  int bad;                         // whether values that are not finite were taken out
+  int strong, pad[2];              // whether any row's power of two is not 1
 };
 
 template <int D, bool kRows>
@@ -217,8 +242,8 @@ prompt_kernel(const LinearParams p, const LinearPlan w, const __grid_constant__ 
   Sums* sums_at = reinterpret_cast<Sums*>(smem + S::kSmall);   // [2]
   uint32_t bar = smem_u32(sums_at + 2);
   auto take = [&](int n) { const uint32_t r = bar; bar += 8 * n; return r; };
-  const uint32_t q_full = take(1), q_free = take(1), k_full = take(2), k_free = take(2), v_full = take(2), v_free = take(2), v_done = take(2);
-  const uint32_t sums_full = take(2), sums_free = take(2), s_full = take(1), p_full = take(1), o_full = take(1), o_free = take(1);
+  const uint32_t q_full = take(1), q_free = take(1), q_ok = take(1), k_full = take(2), k_free = take(2), v_full = take(2), v_free = take(2), v_done = take(2);
+  const uint32_t sums_full = take(2), sums_free = take(2), s_full = take(1), p_full = take(1), o_full = take(2), o_free = take(2);
   const uint32_t w_full = take(2), w_free = take(2), state_full = take(1), state_read = take(1);
   const uint32_t add_full = take(1), add_read = take(1), end = take(1);
   uint32_t* words = reinterpret_cast<uint32_t*>(smem + (bar - base));
@@ -240,7 +265,7 @@ prompt_kernel(const LinearParams p, const LinearPlan w, const __grid_constant__ 
     if (kRows) prefetch_map(&qmap);
     for (int i = 0; i < 2; ++i) {
       mbar_init(k_full + 8 * i, 1);
-      mbar_init(k_free + 8 * i, 1);
+      mbar_init(k_free + 8 * i, kRows ? 2 : 1);
       mbar_init(v_full + 8 * i, 1);
       mbar_init(v_free + 8 * i, kStateWarps + (kRows ? 1 : 0));
       mbar_init(v_done + 8 * i, kStateWarps);
@@ -249,9 +274,12 @@ prompt_kernel(const LinearParams p, const LinearPlan w, const __grid_constant__ 
       mbar_init(sums_full + 8 * i, 1);
       mbar_init(sums_free + 8 * i, kStateWarps + (kRows ? 8 : 0));
     }
-    for (const uint32_t b : {q_full, q_free, s_full, o_full, state_read, add_full, end}) mbar_init(b, 1);
+    for (const uint32_t b : {q_full, q_free, s_full, o_full, o_full + 8, state_read, add_full}) mbar_init(b, 1);
+    mbar_init(end, kRows ? 2 : 1);
     mbar_init(p_full, 4);
+    mbar_init(q_ok, 4);
     mbar_init(o_free, 4);
+    mbar_init(o_free + 8, 4);
     mbar_init(state_full, kStateWarps);
     mbar_init(add_read, kStateWarps);
     *dead = 0;
@@ -328,28 +356,13 @@ prompt_kernel(const LinearParams p, const LinearPlan w, const __grid_constant__ 
     }
     if (asked[2] > 0) mbar_drain_inline(q_full, (asked[2] - 1) & 1);
   } else if (warp == 1) {
-    // ---- products
+    // ---- products for the state
     each_unit([&](int u, int chunks, int g0, int k) {
       for (int c = 0; c < chunks; ++c) {
         const int g = g0 + c, slot = g & 1;
-        const uint32_t q_at = base + S::kQ, k_at = base + S::kK + slot * S::kTile, v_at = base + S::kV + slot * S::kTile;
+        const uint32_t k_at = base + S::kK + slot * S::kTile;
         wait(k_full + 8 * slot, g >> 1 & 1);
-        if (kRows) {
-          wait(q_full, g & 1);
-          if (g > 0) wait(o_full, (g - 1) & 1);                 // (the weighted scores lie in the scores' columns)
-          tc_fence_after();
-          if (elect_one()) {
-            const uint32_t ql = operand_low(q_at, 16), kl = operand_low(k_at, 16);
-#pragma unroll
-            for (int t = 0; t < D / 16; ++t) {
-              const uint32_t off = ((t >> 2) * (kChunk * 128) + (t & 3) * 32) >> 4;
-              tc_mma(tmem, ql + off, kl + off, mma_shape(true, false, kChunk), t > 0);
-            }
-            tc_commit(s_full);
-          }
-          __syncwarp();
-        }
-        if (g > 0) wait(add_read, (g - 1) & 1);                 // (and the sums of the last chunk out of their columns)
+        if (g > 0) wait(add_read, (g - 1) & 1);                 // the sums of the last chunk are out of their columns
 #pragma unroll 1
         for (int step = 0; step < S::kSteps; ++step) {
           const int use = g * S::kSteps + step, at = use & 1;
@@ -373,82 +386,118 @@ prompt_kernel(const LinearParams p, const LinearPlan w, const __grid_constant__ 
             }
           }
           __syncwarp();
-          if (kRows && step == 1) {
-            // what the rows read of the state, while the other steps are converted
-            wait(state_full, g & 1);
-            wait(o_free, (g & 1) ^ 1);
-            tc_fence_after();
-            if (elect_one()) {
-              const uint32_t ql = operand_low(q_at, 16), sl = operand_low(base + S::kS, D * 128);
-#pragma unroll
-              for (int i = 0; i < D / 16; ++i)
-                tc_mma(tmem + S::kRead, ql + (((i >> 2) * (kChunk * 128) + (i & 3) * 32) >> 4), sl + i * (2048 >> 4), mma_shape(true, true, D), i > 0);
-              tc_commit(state_read);
-              tc_commit(q_free);
-            }
-            __syncwarp();
-          }
-        }
-        if (kRows) {
-          wait(p_full, g & 1);
-          tc_fence_after();
-          if (elect_one()) {
-            const uint32_t vl = operand_low(v_at, kChunk * 128);
-#pragma unroll
-            for (int i = 0; i < kChunk / 16; ++i)
-              tc_mma_tmem(tmem + S::kOut, tmem + S::kProb + 8 * i, vl + i * (2048 >> 4), mma_shape(true, true, D), i > 0);
-            tc_commit(o_full);
-            tc_commit(v_free + 8 * slot);
-          }
-          __syncwarp();
         }
       }
     });
     if (lane == 0) tc_commit(end);
     __syncwarp();
-    mbar_drain_inline(end, 0);                                         // nothing is in flight when the columns are given back
+    mbar_drain_inline(end, 0);                                  // nothing is in flight when the columns are given back
+  } else if (warp == 3) {
+    // ---- products for the outputs
+    if (kRows) {
+      each_unit([&](int u, int chunks, int g0, int k) {
+        for (int c = 0; c < chunks; ++c) {
+          const int g = g0 + c, slot = g & 1;
+          const uint32_t ql = operand_low(base + S::kQ, 16), out = tmem + S::kOut + slot * D;
+          wait(k_full + 8 * slot, g >> 1 & 1);
+          wait(q_full, g & 1);
+          if (g > 0) wait(o_full + 8 * (slot ^ 1), (g - 1) >> 1 & 1);   // (the weighted scores lie in the scores' columns)
+          tc_fence_after();
+          if (elect_one()) {
+            const uint32_t kl = operand_low(base + S::kK + slot * S::kTile, 16);
+#pragma unroll
+            for (int i = 0; i < D / 16; ++i) {
+              const uint32_t off = ((i >> 2) * (kChunk * 128) + (i & 3) * 32) >> 4;
+              tc_mma(tmem, ql + off, kl + off, mma_shape(true, false, kChunk), i > 0);
+            }
+            tc_commit(s_full);
+            tc_commit(k_free + 8 * slot);
+          }
+          __syncwarp();
+          wait(q_ok, g & 1);
+          wait(state_full, g & 1);
+          wait(o_free + 8 * slot, (g >> 1 & 1) ^ 1);
+          tc_fence_after();
+          if (elect_one()) {
+            const uint32_t sl = operand_low(base + S::kS, D * 128);
+#pragma unroll
+            for (int i = 0; i < D / 16; ++i)
+              tc_mma(out, ql + (((i >> 2) * (kChunk * 128) + (i & 3) * 32) >> 4), sl + i * (2048 >> 4), mma_shape(true, true, D), i > 0);
+            tc_commit(state_read);
+            tc_commit(q_free);
+          }
+          __syncwarp();
+          wait(p_full, g & 1);
+          wait(v_done + 8 * slot, g >> 1 & 1);                  // values that are not finite, and rows behind the last, are out of the tile
+          tc_fence_after();
+          if (elect_one()) {
+            const uint32_t vl = operand_low(base + S::kV + slot * S::kTile, kChunk * 128);
+#pragma unroll
+            for (int i = 0; i < kChunk / 16; ++i)
+              tc_mma_tmem(out, tmem + S::kProb + 8 * i, vl + i * (2048 >> 4), mma_shape(true, true, D), true);
+            tc_commit(o_full + 8 * slot);
+            tc_commit(v_free + 8 * slot);
+          }
+          __syncwarp();
+        }
+      });
+      if (lane == 0) tc_commit(end);
+      __syncwarp();
+      mbar_drain_inline(end, 0);
+    }
   } else if (warp == 2) {
     // ---- sums of the decays: a lane has four rows
     each_unit([&](int u, int chunks, int g0, int k) {
       const int h = u % p.H;
       const LinearEntry e = entry_of(u);
       const bool others = unit_of(k + 1) < units;
-      double unit = 0.0;
+      Sum unit{0.f, 0.f};
+      auto ask = [&](int c, int i) {
+        const int row = c * kChunk + 4 * lane + i;
+        return row < e.rows ? log_decay_of(p, e.row0 + row, h) : 0.f;
+      };
+      float next[4] = {ask(0, 0), ask(0, 1), ask(0, 2), ask(0, 3)};
       for (int c = 0; c < chunks; ++c) {
         const int g = g0 + c;
-        double x[4];
+        Sum x[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          const int row = c * kChunk + 4 * lane + i;
-          float v = row < e.rows ? log_decay_of(p, e.row0 + row, h) : 0.f;
+          float v = next[i];
           if (v < -200.f) v = -200.f;                           // below every fp32 number, and sums stay finite
-          x[i] = (double)v * 1.4426950408889634074;
+          x[i] = Sum::log2_of_e_to(v);
         }
+        if (c + 1 < chunks)
 #pragma unroll
-        for (int i = 1; i < 4; ++i) x[i] += x[i - 1];
-        double sum = x[3];
+          for (int i = 0; i < 4; ++i) next[i] = ask(c + 1, i);
+#pragma unroll
+        for (int i = 1; i < 4; ++i) x[i] = x[i - 1] + x[i];
+        Sum sum = x[3];
 #pragma unroll
         for (int m = 1; m < 32; m <<= 1) {
-          const double up = __shfl_up_sync(0xffffffffu, sum, m);
-          if (lane >= m) sum += up;
+          const Sum more = Sum{__shfl_up_sync(0xffffffffu, sum.hi, m), __shfl_up_sync(0xffffffffu, sum.lo, m)} + sum;
+          if (lane >= m) sum = more;
         }
-        double before = __shfl_up_sync(0xffffffffu, sum, 1);
-        if (lane == 0) before = 0.0;
-        const double last = __shfl_sync(0xffffffffu, sum, 31), stop = __shfl_sync(0xffffffffu, sum, lane | 7);
-        const double start = __shfl_sync(0xffffffffu, before, lane & ~7);
-        float d[4], after[4], rest[4], from[4];
+        auto of_lane = [&](Sum v, int l) { return Sum{__shfl_sync(0xffffffffu, v.hi, l), __shfl_sync(0xffffffffu, v.lo, l)}; };
+        Sum before = of_lane(sum, lane - 1 & 31);
+        if (lane == 0) before = Sum{0.f, 0.f};
+        const Sum last = of_lane(sum, 31), stop = of_lane(sum, lane | 7), start = of_lane(before, lane & ~7);
+        float d[4], after[4], rest[4], from[4], lift[4];
+        bool strong = false;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          const double c_t = before + x[i], left = last - c_t;
-          d[i] = (float)(c_t - start);
-          after[i] = exp2f((float)(stop - c_t));
-          const float l = (float)left;
-          rest[i] = exp2f(l) * fmaf((float)(left - (double)l), kLn2, 1.f);
-          from[i] = exp2f((float)c_t);
+          const Sum c_t = before + x[i];
+          d[i] = c_t.less(start);
+          after[i] = exp2f(stop.less(c_t));
+          rest[i] = exp2f(last.less(c_t));
+          const float down = c_t.hi < -60.f ? floorf(c_t.hi) + 60.f : 0.f;
+          strong |= down != 0.f;
+          lift[i] = Sum{down, 0.f}.less(c_t);
+          from[i] = exp2f(-lift[i]);
         }
         // [lane >> 2][lane & 3], lanes below 16
-        const double start_a = __shfl_sync(0xffffffffu, before, (lane >> 2 & 3) * 8), stop_b = __shfl_sync(0xffffffffu, sum, (lane & 3) * 8 + 7);
-        const Decay whole((float)(last * 0.69314718055994530942));
+        const float gap = of_lane(before, (lane >> 2 & 3) * 8).less(of_lane(sum, (lane & 3) * 8 + 7));
+        strong = __any_sync(0xffffffffu, strong);
+        const Decay whole(last.natural());
         const bool more = c + 1 < chunks || others;
         wait(sums_free + 8 * (g & 1), (g >> 1 & 1) ^ 1);
         Sums& sums = sums_at[g & 1];
@@ -456,18 +505,21 @@ prompt_kernel(const LinearParams p, const LinearPlan w, const __grid_constant__ 
         *reinterpret_cast<float4*>(&sums.after[4 * lane]) = make_float4(after[0], after[1], after[2], after[3]);
         *reinterpret_cast<float4*>(&sums.rest[4 * lane]) = make_float4(rest[0], rest[1], rest[2], rest[3]);
         *reinterpret_cast<float4*>(&sums.from[4 * lane]) = make_float4(from[0], from[1], from[2], from[3]);
-        if (lane < 16) sums.gap[lane] = (float)(start_a - stop_b);
+        *reinterpret_cast<float4*>(&sums.lift[4 * lane]) = make_float4(lift[0], lift[1], lift[2], lift[3]);
+        if ((lane & 7) == 0) sums.base[lane >> 3] = start.hi;
+        if (lane < 16) sums.gap[lane] = gap;
         if (lane == 0) {
           sums.factor = whole.f;
           sums.near = whole.near;
           sums.valid = min(e.rows - c * kChunk, kChunk);
           sums.more = more;
           sums.bad = 0;
+          sums.strong = strong;
         }
-        unit += last;
+        if (!kRows) unit = unit + last;
         arrive(sums_full + 8 * (g & 1));
       }
-      if (!kRows && lane == 0) w.logs[(size_t)(e.set + e.seg + 1) * p.H + h] = (float)(unit * 0.69314718055994530942);
+      if (!kRows && lane == 0) w.logs[(size_t)(e.set + e.seg + 1) * p.H + h] = unit.natural();
     });
   } else if (warp >= 4 && warp < 8) {
     // ---- weights of the scores: thread = row; 32 columns at a time, none above the diagonal
@@ -479,9 +531,24 @@ prompt_kernel(const LinearParams p, const LinearPlan w, const __grid_constant__ 
           const int g = g0 + c;
           wait(sums_full + 8 * (g & 1), g >> 1 & 1);
           const Sums& sums = sums_at[g & 1];
+          const int row = own * 32 + lane;
+          if (!sums.strong) arrive(q_ok);
           wait(s_full, g & 1);
           tc_fence_after();
-          const float d = sums.d[own * 32 + lane];
+          if (sums.strong) {
+            const float down = rintf(sums.base[own] + sums.d[row] + sums.lift[row]);
+            if (down < 0.f) {
+              const float f = exp2f(down);
+              for (int i = 0; i < D / 8; ++i) {
+                const uint32_t at = base + S::kQ + (i >> 3) * (kChunk * 128) + row * 128 + (((i & 7) ^ (row & 7)) << 4);
+                const uint4 x = lds16(at);
+                sts16(at, make_uint4(pack(unpack(x.x) * Pair(f, f)), pack(unpack(x.y) * Pair(f, f)), pack(unpack(x.z) * Pair(f, f)), pack(unpack(x.w) * Pair(f, f))));
+              }
+            }
+            fence_async_proxy();
+            arrive(q_ok);
+          }
+          const float d = sums.d[row] + sums.lift[row];
 #pragma unroll 1
           for (int b = 0; b < 4; ++b) {
             uint32_t packed[16];
@@ -531,19 +598,18 @@ prompt_kernel(const LinearParams p, const LinearPlan w, const __grid_constant__ 
           const float f = p.scale * sums_at[slot].from[row];
           const int valid = sums_at[slot].valid;
           wait(v_done + 8 * slot, g >> 1 & 1);
-          wait(o_full, g & 1);
+          wait(o_full + 8 * slot, g >> 1 & 1);
           tc_fence_after();
           const bool bad = sums_at[slot].bad, store = row < valid && !*dead;
           __nv_bfloat16* dst = p.out + (int64_t)(first + min(row, valid - 1)) * p.ldo + (int64_t)h * D;
 #pragma unroll 1
           for (int i = 0; i < D; i += 16) {
-            float o[16], u[16];
-            tc_ld16(o, tmem + lanes + S::kOut + i);
-            tc_ld16(u, tmem + lanes + S::kRead + i);
+            float o[16];
+            tc_ld16(o, tmem + lanes + S::kOut + slot * D + i);
             tc_wait_ld();
             uint32_t x[8];
 #pragma unroll
-            for (int j = 0; j < 16; j += 2) x[j / 2] = pack(fma(Pair(u[j], u[j + 1]), Pair(f, f), Pair(o[j], o[j + 1]) * Pair(p.scale, p.scale)));
+            for (int j = 0; j < 16; j += 2) x[j / 2] = pack(Pair(o[j], o[j + 1]) * Pair(f, f));
             if (bad) {
               // rare: values that are not finite, which were left out; they make what comes after them in their column so
 #pragma unroll
@@ -564,7 +630,7 @@ prompt_kernel(const LinearParams p, const LinearPlan w, const __grid_constant__ 
             }
           }
           tc_fence_before();
-          arrive(o_free);
+          arrive(o_free + 8 * slot);
           arrive(sums_free + 8 * slot);
         }
       });
@@ -749,7 +815,7 @@ cudaError_t launch(const LinearParams& p, const LinearPlan& w, const CUtensorMap
 }  // namespace
 
 cudaError_t launch_prompts(const LinearParams& p0, const LinearPlan& w, int D, int grid, int dev, cudaStream_t s) {
-  static_assert(sizeof(Sums) == 4 * kChunk * 4 + 24 * 4 && Shape<128, true>::kSmem <= 227 * 1024, "");
+  static_assert(sizeof(Sums) == 5 * kChunk * 4 + 28 * 4 && Shape<128, true>::kSmem <= 227 * 1024, "");
   LinearParams p = p0;
   p.wide = (reinterpret_cast<uintptr_t>(p.out) | (uintptr_t)p.ldo * 2) % 32 == 0;
   CUtensorMap m[3];
