@@ -55,6 +55,13 @@ __device__ __forceinline__ float exp2_fast(float x) {
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
+// As mbar_try(), for up to 10 us before it answers: few instructions are spent on waiting.
+__device__ __forceinline__ bool mbar_try_long(uint32_t bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile("{ .reg .pred p; mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3; selp.u32 %0, 1, 0, p; }"
+               : "=r"(ok) : "r"(bar), "r"(parity), "r"(10000u) : "memory");
+  return ok != 0;
+}
 // Two fp32 numbers as bf16 (low half: a), and back.
 __device__ __forceinline__ uint32_t pack(float a, float b) {
   uint32_t r;
@@ -104,6 +111,12 @@ struct Sum {
   __device__ __forceinline__ float natural() const { return fmaf(hi, kLn2, lo * kLn2) + hi * -1.9046542e-9f; }
 };
 
+// The kernels of a call start while the one before them ends, and wait here for its results.
+__device__ __forceinline__ void after_previous() {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+}
+
 // ------------------------------------------------------------------ the units
 
 __global__ void __launch_bounds__(1024) plan_kernel(const LinearParams p, const LinearPlan w, int blocks) {
@@ -113,6 +126,7 @@ __global__ void __launch_bounds__(1024) plan_kernel(const LinearParams p, const 
   const int tid = threadIdx.x;
   if (tid == 0) total = 0, sets = 0, extra = 0;
   at[tid] = 0;
+  after_previous();
   __syncthreads();
   auto chunks_of = [&](int b) {
     const int n = p.row_start[b + 1] - p.row_start[b];
@@ -177,13 +191,15 @@ __global__ void __launch_bounds__(1024) plan_kernel(const LinearParams p, const 
   }
 }
 
-// The states at the starts of a request's segments from what each segment adds: block (set of the first segment, head).
+// The states at the starts of a request's segments from what each segment adds: block (first segment and head, part of the elements).
+constexpr int kSumsParts = 16;
 __global__ void __launch_bounds__(256) sums_kernel(const LinearPlan w, int H, int elements) {
+  after_previous();
   if ((int)blockIdx.x >= w.head[1]) return;
   const LinearEntry e = w.first[blockIdx.x / H];
   const int h = blockIdx.x % H;
   if (e.seg != 0) return;
-  for (int i = threadIdx.x * 4; i < elements; i += blockDim.x * 4) {
+  for (int i = (blockIdx.y * blockDim.x + threadIdx.x) * 4; i < elements; i += gridDim.y * blockDim.x * 4) {
     float4* at = reinterpret_cast<float4*>(w.states + ((int64_t)(e.set + 1) * H + h) * elements + i);
     float4 s = *at;
     for (int k = 2; k < e.segs; ++k) {
@@ -207,7 +223,7 @@ struct Shape {
   static constexpr int kTile = kChunk * D * 2, kHalves = D / 64;
   static constexpr int kStep = 32 / kHalves, kSteps = kChunk / kStep, kPart = kStep * D * 2;
   static constexpr int kQ = 0, kK = kTile, kV = 3 * kTile, kW = 5 * kTile, kS = kW + 6 * kPart;
-  static constexpr int kSmall = kS + D * D * 2, kBarriers = 32;
+  static constexpr int kSmall = kS + D * D * 2, kBarriers = 34;
   static constexpr int kSmem = kSmall + 2 * (5 * kChunk * 4 + 28 * 4) + kBarriers * 8 + 16;   // sums, barriers, words
   // tensor memory columns: scores (the weighted ones take their first half when D = 128), two outputs, what a chunk adds to the state
   static constexpr int kOut = 128, kAdd = 128 + 2 * D, kProb = D == 128 ? 0 : 320;
@@ -244,10 +260,11 @@ prompt_kernel(const LinearParams p, const LinearPlan w, const __grid_constant__ 
   auto take = [&](int n) { const uint32_t r = bar; bar += 8 * n; return r; };
   const uint32_t q_full = take(1), q_free = take(1), q_ok = take(1), k_full = take(2), k_free = take(2), v_full = take(2), v_free = take(2), v_done = take(2);
   const uint32_t sums_full = take(2), sums_free = take(2), s_full = take(1), p_full = take(1), o_full = take(2), o_free = take(2);
-  const uint32_t w_full = take(2), w_free = take(2), state_full = take(1), state_read = take(1);
+  const uint32_t w_full = take(2), w_free = take(4), state_full = take(1), state_read = take(1);
   const uint32_t add_full = take(1), add_read = take(1), end = take(1);
   uint32_t* words = reinterpret_cast<uint32_t*>(smem + (bar - base));
   volatile int* dead = reinterpret_cast<volatile int*>(words);
+  after_previous();
   const int units = w.head[kRows ? 0 : 1];
   // a first pass that gave up leaves the whole call without the outputs of this one
   const bool failed = kRows && w.head[2] != 0;
@@ -269,8 +286,9 @@ prompt_kernel(const LinearParams p, const LinearPlan w, const __grid_constant__ 
       mbar_init(v_full + 8 * i, 1);
       mbar_init(v_free + 8 * i, kStateWarps + (kRows ? 1 : 0));
       mbar_init(v_done + 8 * i, kStateWarps);
-      mbar_init(w_full + 8 * i, kStateWarps / 2);
+      mbar_init(w_full + 8 * i, kStateWarps / 4);
       mbar_init(w_free + 8 * i, 1);
+      mbar_init(w_free + 16 + 8 * i, 1);
       mbar_init(sums_full + 8 * i, 1);
       mbar_init(sums_free + 8 * i, kStateWarps + (kRows ? 8 : 0));
     }
@@ -297,7 +315,7 @@ prompt_kernel(const LinearParams p, const LinearPlan w, const __grid_constant__ 
   auto wait = [&](uint32_t b, uint32_t parity) {
     if (mbar_test(b, parity)) return;
     const long long t0 = clock64();
-    while (!mbar_try(b, parity)) {
+    while (!mbar_try_long(b, parity)) {
       if (*dead) return;
       if (clock64() - t0 > p.spin_budget) {
         *dead = 1;
@@ -379,7 +397,7 @@ prompt_kernel(const LinearParams p, const LinearPlan w, const __grid_constant__ 
               for (int i = 0; i < S::kStep / 16; ++i)
                 tc_mma(tmem + S::kAdd, kl + i * (2048 >> 4), wl + i * (2048 >> 4), mma_shape(true, true, D) | 1u << 15, step > 0 || part > 0 || i > 0);
             }
-            tc_commit(w_free + 8 * at);
+            tc_commit(w_free + 8 * (use & 3));
             if (step == S::kSteps - 1) {
               tc_commit(add_full);
               tc_commit(k_free + 8 * slot);
@@ -640,7 +658,7 @@ prompt_kernel(const LinearParams p, const LinearPlan w, const __grid_constant__ 
     const int quad = warp & 3, a = quad * 32 + lane, col0 = ((warp - 12) >> 2) * S::kCols;
     const bool holds = quad * 32 < D;
     const uint32_t lanes = (uint32_t)quad * 32 << 16;
-    const int group = (warp - 12) >> 3, id = threadIdx.x - 384 & 255, piece = id & 7, row0 = (id >> 3) & (S::kStep - 1), part0 = (id >> 3) / S::kStep;
+    const int group = (warp - 12) >> 2, id = threadIdx.x & 127, piece = id & 7, row0 = id >> 3;
     const uint32_t swizzled = row0 * 128 + ((piece ^ (row0 & 7)) << 4);
     float s[S::kCols];
     auto at_state = [&](float* pool, int64_t first) { return pool + first + ((int64_t)a * D + col0); };
@@ -668,61 +686,71 @@ prompt_kernel(const LinearParams p, const LinearPlan w, const __grid_constant__ 
       fence_async_proxy();
       arrive(state_full);
     };
-    // The decayed values of a step of rows as three bf16 numbers, by 8 of the warps; two steps ahead of the state.
+    // The decayed values of a step of rows as three bf16 numbers, by 4 of the warps; two steps ahead of the state. Each thread: two
+    // pieces, of one row (heads of 128) or of rows 16 apart.
     auto convert = [&](int g, int step) {
-      const int slot = g & 1, use = g * S::kSteps + step, at = group;
+      const int slot = g & 1, use = g * S::kSteps + step, at = group & 1;
       if (step == group) {
         wait(sums_full + 8 * slot, g >> 1 & 1);
         wait(v_full + 8 * slot, g >> 1 & 1);
       }
       const Sums& sums = sums_at[slot];
-      const int row = step * S::kStep + row0;
-      const uint32_t off = part0 * (kChunk * 128) + step * (S::kStep * 128) + swizzled, v_at = base + S::kV + slot * S::kTile + off;
-      const uint32_t to = base + S::kW + 3 * at * S::kPart + part0 * (S::kStep * 128) + swizzled;
-      uint4 v = lds16(v_at);
-      if (row >= sums.valid) {
-        // rows behind the last are another request's, or nobody's
-        v = make_uint4(0u, 0u, 0u, 0u);
-        wait(k_full + 8 * slot, g >> 1 & 1);
-        sts16(v_at, v);
-        sts16(base + S::kK + slot * S::kTile + off, v);
-      }
-      const float rest = sums.rest[row];
-      const Pair by(rest, rest), minus(-1.f, -1.f);
-      Pair x[4] = {unpack(v.x) * by, unpack(v.y) * by, unpack(v.z) * by, unpack(v.w) * by}, none(0.f, 0.f);
+      constexpr uint32_t kNext = D == 128 ? kChunk * 128 : 16 * 128, kNextPart = D == 128 ? S::kStep * 128 : 16 * 128;
+      const uint32_t off = step * (S::kStep * 128) + swizzled, v_at = base + S::kV + slot * S::kTile + off;
+      const uint32_t to = base + S::kW + 3 * at * S::kPart + swizzled;
+      const int row = step * S::kStep + row0, valid = sums.valid;
+      uint4 v[2] = {lds16(v_at), lds16(v_at + kNext)};
 #pragma unroll
-      for (int i = 0; i < 4; ++i) none = fma(x[i], Pair(0.f, 0.f), none);
+      for (int n = 0; n < 2; ++n)
+        if (row + (D == 128 ? 0 : 16 * n) >= valid) {
+          // rows behind the last are another request's, or nobody's
+          v[n] = make_uint4(0u, 0u, 0u, 0u);
+          wait(k_full + 8 * slot, g >> 1 & 1);
+          sts16(v_at + n * kNext, v[n]);
+          sts16(base + S::kK + slot * S::kTile + off + n * kNext, v[n]);
+        }
+      const float rest[2] = {sums.rest[row], sums.rest[row + (D == 128 ? 0 : 16)]};
+      Pair x[8] = {unpack(v[0].x), unpack(v[0].y), unpack(v[0].z), unpack(v[0].w), unpack(v[1].x), unpack(v[1].y), unpack(v[1].z), unpack(v[1].w)};
+      Pair none(0.f, 0.f);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        x[i] = x[i] * Pair(rest[i >> 2], rest[i >> 2]);
+        none = fma(x[i], Pair(0.f, 0.f), none);
+      }
       const bool odd = !(none.floats().x == 0.f && none.floats().y == 0.f);
-      uint4 non = make_uint4(0u, 0u, 0u, 0u);
       if (odd) {
         // values that are not finite leave the product with the scores, where they would reach earlier rows too
         const uint32_t m = 0x7f807f80u;
-        non = make_uint4(__vcmpeq2(v.x & m, m), __vcmpeq2(v.y & m, m), __vcmpeq2(v.z & m, m), __vcmpeq2(v.w & m, m));
-        v = make_uint4(v.x & ~non.x, v.y & ~non.y, v.z & ~non.z, v.w & ~non.w);
-        if (kRows) {
-          sts16(v_at, v);
-          sums_at[slot].bad = 1;
+#pragma unroll 1
+        for (int n = 0; n < 2; ++n) {
+          uint4 y = lds16(v_at + n * kNext);
+          y = make_uint4(y.x & ~__vcmpeq2(y.x & m, m), y.y & ~__vcmpeq2(y.y & m, m), y.z & ~__vcmpeq2(y.z & m, m), y.w & ~__vcmpeq2(y.w & m, m));
+          if (kRows) {
+            sts16(v_at + n * kNext, y);
+            sums_at[slot].bad = 1;
+          }
         }
-        x[0] = unpack(v.x) * by, x[1] = unpack(v.y) * by, x[2] = unpack(v.z) * by, x[3] = unpack(v.w) * by;
       }
-      wait(w_free + 8 * at, (use >> 1 & 1) ^ 1);
-      // 8 leading bits at a time: the three parts are the whole number
+      // The place of the step before the last. Each group's steps have a barrier of their own: one for a place could be two phases away
+      // from the one that is waited for, where parities say nothing.
+      if (use >= 2) wait(w_free + 8 * (group ^ 2), (use - 2) >> 2 & 1);
+      // 8 leading bits at a time: the three parts are the whole number (infinities are themselves three times, or nothing)
 #pragma unroll
       for (int part = 2; part >= 0; --part) {
-        uint32_t word[4];
+        uint32_t word[8];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
+        for (int i = 0; i < 8; ++i) {
           const float2 f = x[i].floats();
           word[i] = __byte_perm(__float_as_uint(f.x), __float_as_uint(f.y), 0x7632);
-          if (part > 0) x[i] = fma(Pair(__uint_as_float(__float_as_uint(f.x) & 0xffff0000u), __uint_as_float(__float_as_uint(f.y) & 0xffff0000u)), minus, x[i]);
+          if (part > 0) x[i] = fma(Pair(__uint_as_float(__float_as_uint(f.x) & 0xffff0000u), __uint_as_float(__float_as_uint(f.y) & 0xffff0000u)), Pair(-1.f, -1.f), x[i]);
         }
-        if (part == 0 && odd) word[0] |= non.x & 0x7fff7fffu, word[1] |= non.y & 0x7fff7fffu, word[2] |= non.z & 0x7fff7fffu, word[3] |= non.w & 0x7fff7fffu;
         sts16(to + part * S::kPart, make_uint4(word[0], word[1], word[2], word[3]));
+        sts16(to + part * S::kPart + kNextPart, make_uint4(word[4], word[5], word[6], word[7]));
       }
       fence_async_proxy();
       arrive(w_full + 8 * at);
     };
-    convert(0, group);
+    if (group < 2) convert(0, group);
     each_unit([&](int u, int chunks, int g0, int k) {
 #pragma unroll
       for (int i = 0; i < S::kCols; ++i) s[i] = 0.f;
@@ -741,7 +769,7 @@ prompt_kernel(const LinearParams p, const LinearPlan w, const __grid_constant__ 
       if (kRows) publish(g0);
       for (int c = 0; c < chunks; ++c) {
         const int g = g0 + c;
-        for (int step = 2 + group; step < S::kSteps; step += 2) convert(g, step);
+        for (int step = group < 2 ? 4 + group : group; step < S::kSteps; step += 4) convert(g, step);
         const Sums& sums = sums_at[g & 1];
         const float f = sums.factor;
         const float keep = sums.near ? 1.f : 0.f;
@@ -749,7 +777,7 @@ prompt_kernel(const LinearParams p, const LinearPlan w, const __grid_constant__ 
         arrive(sums_free + 8 * (g & 1));
         arrive(v_done + 8 * (g & 1));
         arrive(v_free + 8 * (g & 1));
-        if (more) convert(g + 1, group);
+        if (more && group < 2) convert(g + 1, group);
         wait(add_full, g & 1);
         tc_fence_after();
         if (holds)
@@ -798,18 +826,32 @@ bool encode_rows(CUtensorMap* map, const void* data, int64_t ld, int heads, int 
                   CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+template <typename... Args>
+cudaError_t launch_next(void (*kernel)(Args...), dim3 grid, int threads, size_t smem, cudaStream_t s, Args... args) {
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3((unsigned)threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute a{};
+  a.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  a.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &a;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
 template <int D>
 cudaError_t launch(const LinearParams& p, const LinearPlan& w, const CUtensorMap (&m)[3], int grid, int dev, bool segments, cudaStream_t s) {
   cudaError_t e = allow_shared_memory<prompt_kernel<D, true>>(dev);
   if (e == cudaSuccess) e = allow_shared_memory<prompt_kernel<D, false>>(dev);
-  if (e != cudaSuccess) return e;
-  plan_kernel<<<1, 1024, 0, s>>>(p, w, grid);
+  if (e == cudaSuccess) e = launch_next(plan_kernel, dim3(1), 1024, 0, s, p, w, grid);
   if (segments) {
-    prompt_kernel<D, false><<<grid, kThreads, Shape<D, false>::kSmem, s>>>(p, w, m[0], m[1], m[2]);
-    sums_kernel<<<grid, 256, 0, s>>>(w, p.H, D * D);
+    if (e == cudaSuccess) e = launch_next(prompt_kernel<D, false>, dim3(grid), kThreads, Shape<D, false>::kSmem, s, p, w, m[0], m[1], m[2]);
+    if (e == cudaSuccess) e = launch_next(sums_kernel, dim3(grid, kSumsParts), 256, 0, s, w, (int)p.H, D * D);
   }
-  prompt_kernel<D, true><<<grid, kThreads, Shape<D, true>::kSmem, s>>>(p, w, m[0], m[1], m[2]);
-  return cudaGetLastError();
+  if (e == cudaSuccess) e = launch_next(prompt_kernel<D, true>, dim3(grid), kThreads, Shape<D, true>::kSmem, s, p, w, m[0], m[1], m[2]);
+  return e;
 }
 
 }  // namespace
