@@ -84,6 +84,26 @@ struct Decay {
   __device__ __forceinline__ explicit Decay(float g) : near(g > -0.5f && g < 0.5f) { f = near ? expm1f(g) : expf(g); }
 };
 
+// Pairs of fp32 numbers, which one instruction takes together.
+struct Pair {
+  uint64_t v;
+  __device__ __forceinline__ Pair() {}
+  __device__ __forceinline__ Pair(float a, float b) { asm("mov.b64 %0, {%1, %2};" : "=l"(v) : "f"(a), "f"(b)); }
+  __device__ __forceinline__ float2 floats() const {
+    float2 r;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+    return r;
+  }
+};
+__device__ __forceinline__ Pair operator*(Pair a, Pair b) {
+  asm("mul.rn.f32x2 %0, %0, %1;" : "+l"(a.v) : "l"(b.v));
+  return a;
+}
+__device__ __forceinline__ Pair fma(Pair a, Pair b, Pair c) {
+  asm("fma.rn.f32x2 %0, %1, %2, %0;" : "+l"(c.v) : "l"(a.v), "l"(b.v));
+  return c;
+}
+
 // ------------------------------------------------------------------ host
 
 mdw_status check_linear_state(const mdw_linear_state* s);

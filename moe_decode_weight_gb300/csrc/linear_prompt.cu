@@ -68,24 +68,6 @@ __device__ __forceinline__ uint32_t pack(float a, float b) {
   asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(b), "f"(a));
   return r;
 }
-// Pairs of fp32 numbers, which one instruction takes together.
-struct Pair {
-  uint64_t v;
-  __device__ __forceinline__ Pair(float a, float b) { asm("mov.b64 %0, {%1, %2};" : "=l"(v) : "f"(a), "f"(b)); }
-  __device__ __forceinline__ float2 floats() const {
-    float2 r;
-    asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
-    return r;
-  }
-};
-__device__ __forceinline__ Pair operator*(Pair a, Pair b) {
-  asm("mul.rn.f32x2 %0, %0, %1;" : "+l"(a.v) : "l"(b.v));
-  return a;
-}
-__device__ __forceinline__ Pair fma(Pair a, Pair b, Pair c) {
-  asm("fma.rn.f32x2 %0, %1, %2, %0;" : "+l"(c.v) : "l"(a.v), "l"(b.v));
-  return c;
-}
 __device__ __forceinline__ Pair unpack(uint32_t v) { return Pair(__uint_as_float(v << 16), __uint_as_float(v & 0xffff0000u)); }
 __device__ __forceinline__ uint32_t pack(Pair a) {
   const float2 f = a.floats();

@@ -49,12 +49,12 @@ constexpr int kRows = 8;                                        // rows whose el
 // One block: request blockIdx.z, value head blockIdx.y, kCols of the columns. kOut: outputs of all rows; else the rows
 // whose bits are set change the state only.
 template <int D, int kCols, bool kOut>
-__global__ void __launch_bounds__(kThreads) step_kernel(const LinearParams p) {
+__global__ void __launch_bounds__(kThreads, D * kCols > 64 * 64 ? 2 : 4) step_kernel(const LinearParams p) {
   constexpr int kLanes = kCols / 4, kGroups = kThreads / kLanes, kPer = D / kGroups;   // lanes of a row, rows at once, rows of a thread
-  static_assert(kPer * kGroups == D && kPer >= 1, "");
-  __shared__ __align__(16) float qs[kRows][D], ks[kRows][D], vs[kRows][kCols];
+  static_assert(kPer * kGroups == D && kPer % 2 == 0, "");
+  __shared__ __align__(16) float qs[kOut ? kRows : 1][D], ks[kRows][D], vs[kRows][kCols];
   __shared__ __align__(16) float parts[kOut ? kRows : 1][kWarps][kCols];
-  __shared__ float gs[kRows];
+  __shared__ float factor[kRows], keep[kRows];
   const int b = blockIdx.z, h = blockIdx.y, col0 = blockIdx.x * kCols, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   if (kOut) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");   // (plan_kernel of longer requests waits for this one's end)
   LinearRequest r;
@@ -63,11 +63,14 @@ __global__ void __launch_bounds__(kThreads) step_kernel(const LinearParams p) {
   if (!sound || (kOut && r.n > p.short_rows)) return;
   if (r.out < 0 && !(kOut && r.n > 0)) return;
   const int c = tid % kLanes * 4, a0 = tid / kLanes * kPer;
-  float4 s[kPer];
+  const int64_t at = ((int64_t)h * D + a0) * D + col0 + c;
+  Pair s[kPer][2];
 #pragma unroll
   for (int i = 0; i < kPer; ++i) {
-    s[i] = make_float4(0.f, 0.f, 0.f, 0.f);
-    if (r.in >= 0) s[i] = __ldcs(reinterpret_cast<const float4*>(p.s + r.in * p.slot_stride + ((int64_t)h * D + a0 + i) * D + col0 + c));
+    float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (r.in >= 0) x = __ldcs(reinterpret_cast<const float4*>(p.s + r.in * p.slot_stride + at + i * D));
+    s[i][0] = Pair(x.x, x.y);
+    s[i][1] = Pair(x.z, x.w);
   }
   uint64_t left = 0;                                            // accepted rows that are still to come
   if (!kOut) left = p.bits[b] & (r.n < 64 ? (1ull << r.n) - 1 : ~0ull);
@@ -88,82 +91,94 @@ __global__ void __launch_bounds__(kThreads) step_kernel(const LinearParams p) {
     if (count <= 0) break;
     auto row_of = [&](int i) {
       if (kOut) return r.row0 + next + i;
-      int at = 0;
+      int row = 0;
 #pragma unroll
-      for (int j = 0; j < kRows; ++j) at = j == i ? rows[j] : at;
-      return at;
+      for (int j = 0; j < kRows; ++j) row = j == i ? rows[j] : row;
+      return row;
     };
     // pieces of 8 elements: k, then v's columns of the block, then q
     constexpr int kOfRow = D / 8 + kCols / 8 + (kOut ? D / 8 : 0);
     for (int i = tid; i < count * kOfRow; i += kThreads) {
-      const int t = i / kOfRow, at = i % kOfRow, row = row_of(t);
+      const int t = i / kOfRow, piece = i % kOfRow, row = row_of(t);
       const __nv_bfloat16* src;
       float* dst;
-      if (at < D / 8) {
-        src = p.k + row * p.ldk + (int64_t)(h / p.share) * D + 8 * at;
-        dst = &ks[t][8 * at];
-      } else if (at < D / 8 + kCols / 8) {
-        src = p.v + row * p.ldv + (int64_t)h * D + col0 + 8 * (at - D / 8);
-        dst = &vs[t][8 * (at - D / 8)];
+      if (piece < D / 8) {
+        src = p.k + row * p.ldk + (int64_t)(h / p.share) * D + 8 * piece;
+        dst = &ks[t][8 * piece];
+      } else if (piece < D / 8 + kCols / 8) {
+        src = p.v + row * p.ldv + (int64_t)h * D + col0 + 8 * (piece - D / 8);
+        dst = &vs[t][8 * (piece - D / 8)];
       } else {
-        src = p.q + row * p.ldq + (int64_t)(h / p.share) * D + 8 * (at - D / 8 - kCols / 8);
-        dst = &qs[t][8 * (at - D / 8 - kCols / 8)];
+        src = p.q + row * p.ldq + (int64_t)(h / p.share) * D + 8 * (piece - D / 8 - kCols / 8);
+        dst = &qs[t][8 * (piece - D / 8 - kCols / 8)];
       }
       const uint4 x = *reinterpret_cast<const uint4*>(src);
-      const uint32_t w[4] = {x.x, x.y, x.z, x.w};
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        dst[2 * e] = __uint_as_float(w[e] << 16);
-        dst[2 * e + 1] = __uint_as_float(w[e] & 0xffff0000u);
-      }
+      reinterpret_cast<float4*>(dst)[0] = make_float4(__uint_as_float(x.x << 16), __uint_as_float(x.x & 0xffff0000u),
+                                                      __uint_as_float(x.y << 16), __uint_as_float(x.y & 0xffff0000u));
+      reinterpret_cast<float4*>(dst)[1] = make_float4(__uint_as_float(x.z << 16), __uint_as_float(x.z & 0xffff0000u),
+                                                      __uint_as_float(x.w << 16), __uint_as_float(x.w & 0xffff0000u));
     }
-    if (tid < count) gs[tid] = log_decay_of(p, row_of(tid), h);
+    if (tid < count) {
+      const Decay decay(log_decay_of(p, row_of(tid), h));
+      factor[tid] = decay.f;
+      keep[tid] = decay.near ? 1.f : 0.f;
+    }
     __syncthreads();
     for (int t = 0; t < count; ++t) {
-      const Decay decay(gs[t]);
-      const float4 v = *reinterpret_cast<const float4*>(&vs[t][c]);
-      float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+      const Pair f(factor[t], factor[t]), same(keep[t], keep[t]);
+      const float4 v4 = *reinterpret_cast<const float4*>(&vs[t][c]);
+      const Pair v[2] = {Pair(v4.x, v4.y), Pair(v4.z, v4.w)};
+      Pair o[2] = {Pair(0.f, 0.f), Pair(0.f, 0.f)};
 #pragma unroll
-      for (int i = 0; i < kPer; ++i) {
-        const float k = ks[t][a0 + i];
-        const float4 was = s[i];
-        float4 x;
-        x.x = fmaf(was.x, decay.f, decay.near ? was.x : 0.f);
-        x.y = fmaf(was.y, decay.f, decay.near ? was.y : 0.f);
-        x.z = fmaf(was.z, decay.f, decay.near ? was.z : 0.f);
-        x.w = fmaf(was.w, decay.f, decay.near ? was.w : 0.f);
-        s[i] = make_float4(fmaf(k, v.x, x.x), fmaf(k, v.y, x.y), fmaf(k, v.z, x.z), fmaf(k, v.w, x.w));
-        if (kOut) {
-          const float q = qs[t][a0 + i];
-          o = make_float4(fmaf(q, s[i].x, o.x), fmaf(q, s[i].y, o.y), fmaf(q, s[i].z, o.z), fmaf(q, s[i].w, o.w));
+      for (int i = 0; i < kPer; i += 2) {
+        const float2 k = *reinterpret_cast<const float2*>(&ks[t][a0 + i]);
+        float2 q = make_float2(0.f, 0.f);
+        if (kOut) q = *reinterpret_cast<const float2*>(&qs[t][a0 + i]);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const float kk = j < 2 ? k.x : k.y;
+          Pair& x = s[i + (j >> 1)][j & 1];
+          x = fma(x, same, fma(x, f, Pair(kk, kk) * v[j & 1]));  // (the product of two bf16 numbers is exact)
+          if (kOut) {
+            const float qq = j < 2 ? q.x : q.y;
+            o[j & 1] = fma(Pair(qq, qq), x, o[j & 1]);
+          }
         }
       }
       if (kOut) {
+        float4 sum = make_float4(o[0].floats().x, o[0].floats().y, o[1].floats().x, o[1].floats().y);
 #pragma unroll
         for (int m = kLanes; m < 32; m <<= 1) {
-          o.x += __shfl_xor_sync(0xffffffffu, o.x, m);
-          o.y += __shfl_xor_sync(0xffffffffu, o.y, m);
-          o.z += __shfl_xor_sync(0xffffffffu, o.z, m);
-          o.w += __shfl_xor_sync(0xffffffffu, o.w, m);
+          sum.x += __shfl_xor_sync(0xffffffffu, sum.x, m);
+          sum.y += __shfl_xor_sync(0xffffffffu, sum.y, m);
+          sum.z += __shfl_xor_sync(0xffffffffu, sum.z, m);
+          sum.w += __shfl_xor_sync(0xffffffffu, sum.w, m);
         }
-        if (lane < kLanes) *reinterpret_cast<float4*>(&parts[t][warp][c]) = o;
+        if (lane < kLanes) *reinterpret_cast<float4*>(&parts[t][warp][c]) = sum;
       }
     }
     __syncthreads();
     if (kOut)
-      for (int i = tid; i < count * kCols; i += kThreads) {
-        const int t = i / kCols, at = i % kCols;
-        float o = 0.f;
+      for (int i = tid; i < count * (kCols / 2); i += kThreads) {
+        const int t = i / (kCols / 2), col = i % (kCols / 2) * 2;
+        float x = 0.f, y = 0.f;
 #pragma unroll
-        for (int w = 0; w < kWarps; ++w) o += parts[t][w][at];
-        p.out[(int64_t)(r.row0 + next + t) * p.ldo + (int64_t)h * D + col0 + at] = __float2bfloat16_rn(o * p.scale);
+        for (int w = 0; w < kWarps; ++w) {
+          const float2 part = *reinterpret_cast<const float2*>(&parts[t][w][col]);
+          x += part.x;
+          y += part.y;
+        }
+        *reinterpret_cast<__nv_bfloat162*>(p.out + (int64_t)(r.row0 + next + t) * p.ldo + (int64_t)h * D + col0 + col) =
+            __floats2bfloat162_rn(x * p.scale, y * p.scale);
       }
     next += count;
   }
   if (r.out >= 0)
 #pragma unroll
-    for (int i = 0; i < kPer; ++i)
-      __stcs(reinterpret_cast<float4*>(p.s + r.out * p.slot_stride + ((int64_t)h * D + a0 + i) * D + col0 + c), s[i]);
+    for (int i = 0; i < kPer; ++i) {
+      const float2 x = s[i][0].floats(), y = s[i][1].floats();
+      __stcs(reinterpret_cast<float4*>(p.s + r.out * p.slot_stride + at + i * D), make_float4(x.x, x.y, y.x, y.y));
+    }
 }
 
 template <int D, int kCols, bool kOut>
@@ -172,13 +187,13 @@ void launch_cols(const LinearParams& p, cudaStream_t s) {
 }
 template <bool kOut>
 cudaError_t launch_step(const LinearParams& p, int D, int sms, cudaStream_t s) {
-  // columns are split where few requests and heads leave SMs without a block
-  const int64_t units = (int64_t)p.B * p.H;
+  // columns are split further where few requests and heads leave SMs without a block
+  const bool few = (int64_t)p.B * p.H * (D / 64) <= sms;
   if (D == 128) {
-    if (units * 2 <= sms) launch_cols<128, 32, kOut>(p, s);
-    else launch_cols<128, 128, kOut>(p, s);
+    if (few) launch_cols<128, 32, kOut>(p, s);
+    else launch_cols<128, 64, kOut>(p, s);
   } else {
-    if (units * 2 <= sms) launch_cols<64, 32, kOut>(p, s);
+    if (few) launch_cols<64, 32, kOut>(p, s);
     else launch_cols<64, 64, kOut>(p, s);
   }
   return cudaGetLastError();
