@@ -52,6 +52,15 @@ template <typename T> __device__ __forceinline__ void store8(void* p, int64_t at
   }
 }
 
+// Off by a few 2^-22: the exponential and the reciprocal take one instruction each (with the exact ones the gated norm of 4,099
+// rows of 32 heads took 39 us).
+__device__ __forceinline__ float sigmoid(float x) {
+  float e, r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(x * -1.4426950408889634f));
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.f + e));
+  return r;
+}
+
 constexpr int kMaxThreads = 512;
 
 // T: the 16-bit type; Y, S: types of y and of residual and sum. kPieces of eight elements a thread. kVector: by 16 bytes.
@@ -157,7 +166,7 @@ __global__ void __launch_bounds__(kMaxThreads) norm_kernel(const NormParams p) {
       get(T(), p.gate, row * p.ldg, i, g);
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
-        const float act = p.gate_kind == MDW_GATE_MUL ? 1.f : 1.f / (1.f + expf(-g[j]));
+        const float act = p.gate_kind == MDW_GATE_MUL ? 1.f : sigmoid(g[j]);
         z[i][j] *= p.gate_kind == MDW_GATE_SIGMOID ? act : g[j] * act;
       }
     }

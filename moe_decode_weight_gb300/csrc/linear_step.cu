@@ -49,12 +49,13 @@ constexpr int kRows = 8;                                        // rows whose el
 // One block: request blockIdx.z, value head blockIdx.y, kCols of the columns. kOut: outputs of all rows; else the rows
 // whose bits are set change the state only.
 template <int D, int kCols, bool kOut>
-__global__ void __launch_bounds__(kThreads, D * kCols > 64 * 64 ? 2 : 4) step_kernel(const LinearParams p) {
+__global__ void __launch_bounds__(kThreads, D * kCols > 64 * 64 ? 3 : 4) step_kernel(const LinearParams p) {
   constexpr int kLanes = kCols / 4, kGroups = kThreads / kLanes, kPer = D / kGroups;   // lanes of a row, rows at once, rows of a thread
   static_assert(kPer * kGroups == D && kPer % 2 == 0, "");
   __shared__ __align__(16) float qs[kOut ? kRows : 1][D], ks[kRows][D], vs[kRows][kCols];
   __shared__ __align__(16) float parts[kOut ? kRows : 1][kWarps][kCols];
   __shared__ float factor[kRows], keep[kRows];
+  __shared__ int taken[kRows];
   const int b = blockIdx.z, h = blockIdx.y, col0 = blockIdx.x * kCols, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   if (kOut) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");   // (plan_kernel of longer requests waits for this one's end)
   LinearRequest r;
@@ -76,26 +77,21 @@ __global__ void __launch_bounds__(kThreads, D * kCols > 64 * 64 ? 2 : 4) step_ke
   if (!kOut) left = p.bits[b] & (r.n < 64 ? (1ull << r.n) - 1 : ~0ull);
   int next = 0;
   for (;;) {
-    int rows[kRows], count = 0;
+    int count;
     if (kOut) {
       count = min(r.n - next, kRows);
     } else {
-#pragma unroll
-      for (int i = 0; i < kRows; ++i)
-        if (left) {
-          rows[i] = r.row0 + __ffsll((long long)left) - 1;
-          left &= left - 1;
-          count = i + 1;
-        }
+      count = min(__popcll(left), kRows);
+      if (tid < count) {
+        uint64_t from = left;                                   // without its first tid bits
+        for (int i = 0; i < tid; ++i) from &= from - 1;
+        taken[tid] = r.row0 + __ffsll((long long)from) - 1;
+      }
+      for (int i = 0; i < count; ++i) left &= left - 1;
+      __syncthreads();
     }
     if (count <= 0) break;
-    auto row_of = [&](int i) {
-      if (kOut) return r.row0 + next + i;
-      int row = 0;
-#pragma unroll
-      for (int j = 0; j < kRows; ++j) row = j == i ? rows[j] : row;
-      return row;
-    };
+    auto row_of = [&](int i) { return kOut ? r.row0 + next + i : taken[i]; };
     // pieces of 8 elements: k, then v's columns of the block, then q
     constexpr int kOfRow = D / 8 + kCols / 8 + (kOut ? D / 8 : 0);
     for (int i = tid; i < count * kOfRow; i += kThreads) {
