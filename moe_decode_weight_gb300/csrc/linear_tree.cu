@@ -18,6 +18,8 @@
 namespace mdw {
 namespace {
 
+constexpr float kLog2e = 1.4426950408889634f;
+
 __device__ __forceinline__ void mma(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
   asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
                : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3]) : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
@@ -27,11 +29,15 @@ __device__ __forceinline__ uint32_t pack(float a, float b) {
   asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(b), "f"(a));
   return r;
 }
-// Two numbers as the sum of two bf16 numbers each; what is not finite is itself and nothing.
+// Two numbers as the sum of two bf16 numbers each: 8 leading bits, and the rest rounded to 8 (a number that is not finite: itself and NaN).
 __device__ __forceinline__ void split(float a, float b, uint32_t& high, uint32_t& low) {
-  high = pack(a, b);
-  const float x = a - __uint_as_float(high << 16), y = b - __uint_as_float(high & 0xffff0000u);
-  low = pack(isfinite(a) ? x : 0.f, isfinite(b) ? y : 0.f);
+  high = __byte_perm(__float_as_uint(a), __float_as_uint(b), 0x7632);
+  low = pack(a - __uint_as_float(__float_as_uint(a) & 0xffff0000u), b - __uint_as_float(__float_as_uint(b) & 0xffff0000u));
+}
+__device__ __forceinline__ float exp2_fast(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
 }
 __device__ __forceinline__ uint32_t lds(const __nv_bfloat16* p) { return *reinterpret_cast<const uint32_t*>(p); }
 __device__ __forceinline__ uint32_t smem_at(const void* p) { return (uint32_t)__cvta_generic_to_shared(p); }
@@ -42,79 +48,111 @@ __device__ __forceinline__ void ldmatrix_trans(uint32_t (&r)[4], uint32_t at) {
 // kTiles tiles of 16 nodes.
 template <int D, int kTiles>
 struct Shape {
-  static constexpr int kThreads = 2 * D, kWarps = kThreads / 32, kNodes = 16 * kTiles;
+  static constexpr int kWarps = D == 128 || kTiles == 4 ? 8 : 4, kThreads = 32 * kWarps, kNodes = 16 * kTiles;
+  static constexpr int kResident = kWarps == 4 ? 4 : D == 128 && kTiles == 4 ? 1 : 2;   // blocks an SM
+  static constexpr int kColumns = D / 32, kSplits = kWarps / kColumns;   // groups of 32 columns, parts of the state's rows
   static constexpr int kRow = D + 8;                            // elements from one row to the next in shared memory: no bank twice
   static constexpr int kWeights = kNodes + 4, kSums = D + 4;
-  static constexpr int kSmem = 3 * kNodes * kRow * 2 + kNodes * kWeights * 4 + kNodes * kSums * 4 + kNodes * (4 + 8) + D * 8 + 16;
+  // q and k, whose place the sums take later; v; weights; per node mask and e^{e_i}; per column a mask
+  static constexpr int kV = (2 * kRow * 2 > kSums * 4 ? 2 * kRow * 2 : kSums * 4) * kNodes, kWeightsAt = kV + kNodes * kRow * 2;
+  static constexpr int kBits = kWeightsAt + kNodes * kWeights * 4, kSmem = kBits + kNodes * 12 + D * 8 + 16;
 };
 
 template <int D, int kTiles>
-__global__ void __launch_bounds__(2 * D, kTiles == 4 ? 1 : 2) tree_kernel(const LinearParams p) {
+__global__ void __launch_bounds__(Shape<D, kTiles>::kThreads, Shape<D, kTiles>::kResident) tree_kernel(const LinearParams p) {
   using S = Shape<D, kTiles>;
   extern __shared__ __align__(16) uint8_t smem[];
   __nv_bfloat16* qs = reinterpret_cast<__nv_bfloat16*>(smem);
   __nv_bfloat16* ks = qs + S::kNodes * S::kRow;
-  __nv_bfloat16* vs = ks + S::kNodes * S::kRow;
-  uint64_t* bits = reinterpret_cast<uint64_t*>(vs + S::kNodes * S::kRow);
+  __nv_bfloat16* vs = reinterpret_cast<__nv_bfloat16*>(smem + S::kV);
+  float* sums = reinterpret_cast<float*>(smem);                 // [node][D]
+  float* weights = reinterpret_cast<float*>(smem + S::kWeightsAt);   // [node][node] e^{e_ij}, -1 where j is not seen; then weighted scores
+  uint64_t* bits = reinterpret_cast<uint64_t*>(smem + S::kBits);
   uint64_t* odd = bits + S::kNodes;                             // per column the nodes whose value is not finite
-  float* weights = reinterpret_cast<float*>(odd + D);           // [node][node] e^{e_ij}; -1 where j is not seen
-  float* from_state = weights + S::kNodes * S::kWeights;        // [node][D]
-  float* whole = from_state + S::kNodes * S::kSums;             // e^{e_i}
+  float* whole = reinterpret_cast<float*>(odd + D);             // e^{e_i}
   int* any_odd = reinterpret_cast<int*>(whole + S::kNodes);
-  const int b = blockIdx.y, h = blockIdx.x, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
-  LinearRequest r;
-  if (!linear_request(p, b, r) || r.n == 0) return;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3, units = p.B * p.H;
 
-  // ---- the state: warp = 32 columns and half of the rows
-  constexpr int kColumns = D / 32, kSteps = D / 32;             // groups of columns; 16 rows of half the state
-  const int col0 = warp % kColumns * 32, half = warp / kColumns, row0 = half * (D / 2);
+  // ---- requests: a block has several units (request, head), and asks for the next one's data as soon as it has room for it
+  struct Unit {
+    int row0, n, in, h;                                         // n = 0: nothing to do
+  };
+  auto look = [&](int u) {
+    Unit r{0, 0, -1, 0};
+    if (u >= units) return r;
+    const int b = u / p.H, end = p.row_start[b + 1];
+    r.row0 = p.row_start[b];
+    r.in = p.slot_in[b];
+    r.h = u - b * p.H;
+    const bool bad = r.row0 < 0 || end < r.row0 || end > p.T || r.in < -1 || r.in >= p.num_slots || end - r.row0 > p.max_new;
+    r.n = bad ? 0 : end - r.row0;
+    if (bad && tid == 0) raise_status(p.status, MDW_ERR_DEVICE_BOUNDS);
+    return r;
+  };
+  // the state: warp = 32 columns and a part of the rows
+  constexpr int kSteps = D / 16 / S::kSplits;                   // of 16 rows
+  const int col0 = warp % S::kColumns * 32, part = warp / S::kColumns, row0 = part * (D / S::kSplits);
   float4 state[kSteps][4];
-  if (r.in >= 0) {
-    const float* src = p.s + r.in * p.slot_stride + (int64_t)h * D * D + (int64_t)(row0 + 2 * t) * D + col0 + 4 * g;
+  auto ask_state = [&](const Unit& r) {
+    if (r.n == 0 || r.in < 0) return;
+    const float* src = p.s + r.in * p.slot_stride + (int64_t)r.h * D * D + (int64_t)(row0 + 2 * t) * D + col0 + 4 * g;
 #pragma unroll
     for (int k = 0; k < kSteps; ++k)
 #pragma unroll
       for (int i = 0; i < 4; ++i) state[k][i] = __ldg(reinterpret_cast<const float4*>(src + (16 * k + (i & 1) + 8 * (i >> 1)) * D));
-  }
+  };
+  // rows of q, k and v, zeros behind the last; two decays a lane; masks of a warp's rows, one a lane
+  constexpr int kPieces = (S::kNodes * D / 8 + S::kThreads - 1) / S::kThreads, kMasks = S::kNodes / S::kWarps;   // of 8 elements, a thread
+  constexpr bool kEarly = D == 64 || kTiles != 2;               // (else there are no registers for it before)
+  uint4 piece[3][kPieces];
+  float g0 = 0.f, g1 = 0.f;
+  uint64_t mask = ~0ull;
+  auto ask_rows = [&](const Unit& r) {
+    if (r.n == 0) return;
+    const int64_t qk = (int64_t)(r.h / p.share) * D;
+#pragma unroll
+    for (int i = 0; i < kPieces; ++i) {
+      const int at = i * S::kThreads + tid, node = at / (D / 8), e = at % (D / 8) * 8;
+      piece[0][i] = piece[1][i] = piece[2][i] = make_uint4(0u, 0u, 0u, 0u);
+      if (node < r.n) {
+        const int64_t row = r.row0 + node;
+        piece[0][i] = *reinterpret_cast<const uint4*>(p.q + row * p.ldq + qk + e);
+        piece[1][i] = *reinterpret_cast<const uint4*>(p.k + row * p.ldk + qk + e);
+        piece[2][i] = *reinterpret_cast<const uint4*>(p.v + row * p.ldv + (int64_t)r.h * D + e);
+      }
+    }
+    g0 = 2 * lane < r.n ? log_decay_of(p, r.row0 + 2 * lane, r.h) * kLog2e : 0.f;
+    g1 = 2 * lane + 1 < r.n ? log_decay_of(p, r.row0 + 2 * lane + 1, r.h) * kLog2e : 0.f;
+    if (p.bits && lane < kMasks && lane * S::kWarps + warp < r.n) mask = p.bits[r.row0 + lane * S::kWarps + warp];
+  };
 
-  // ---- rows of q, k and v; zeros behind the last
-  const int64_t qk = (int64_t)(h / p.share) * D;
+  Unit r = look(blockIdx.x);
+  ask_state(r);
+  ask_rows(r);
+  for (int u = blockIdx.x; u < units; u += gridDim.x) {
+  const Unit next = look(u + gridDim.x);
+  if (r.n > 0) {
   for (int i = tid; i < D; i += S::kThreads) odd[i] = 0;
   if (tid == 0) *any_odd = 0;
-  constexpr int kPieces = S::kNodes * D / 8 / S::kThreads;      // of 8 elements, a thread
-  uint4 piece[3][kPieces];
-#pragma unroll
-  for (int i = 0; i < kPieces; ++i) {
-    const int at = i * S::kThreads + tid, node = at / (D / 8), e = at % (D / 8) * 8;
-    piece[0][i] = piece[1][i] = piece[2][i] = make_uint4(0u, 0u, 0u, 0u);
-    if (node < r.n) {
-      const int64_t row = r.row0 + node;
-      piece[0][i] = *reinterpret_cast<const uint4*>(p.q + row * p.ldq + qk + e);
-      piece[1][i] = *reinterpret_cast<const uint4*>(p.k + row * p.ldk + qk + e);
-      piece[2][i] = *reinterpret_cast<const uint4*>(p.v + row * p.ldv + (int64_t)h * D + e);
-    }
-  }
-  // ---- weights: a warp's rows, two nodes a lane, sums from the row downwards
-  const float g0 = 2 * lane < r.n ? log_decay_of(p, r.row0 + 2 * lane, h) : 0.f;
-  const float g1 = 2 * lane + 1 < r.n ? log_decay_of(p, r.row0 + 2 * lane + 1, h) : 0.f;
+  // ---- weights: a warp's rows, sums from the row downwards
 #pragma unroll 4
-  for (int j = 0; j < S::kNodes / S::kWarps; ++j) {
+  for (int j = 0; j < kMasks; ++j) {
     const int i = j * S::kWarps + warp;
-    uint64_t seen = 0;
-    if (i < r.n) seen = ((p.bits ? p.bits[r.row0 + i] : ~0ull) & ((1ull << i) - 1)) | 1ull << i;
+    const uint64_t own = __shfl_sync(0xffffffffu, mask, j);
+    const uint64_t seen = i < r.n ? (own & ((1ull << i) - 1)) | 1ull << i : 0;
     const bool s0 = seen >> (2 * lane) & 1, s1 = seen >> (2 * lane + 1) & 1;
     const float x1 = s1 ? g1 : 0.f;
     float sum = (s0 ? g0 : 0.f) + x1;
 #pragma unroll
-    for (int m = 1; m < 32; m <<= 1) {
+    for (int m = 1; m < S::kNodes / 2; m <<= 1) {
       const float down = __shfl_down_sync(0xffffffffu, sum, m);
       if (lane + m < 32) sum += down;
     }
     float after = __shfl_down_sync(0xffffffffu, sum, 1);        // of all nodes after the lane's
     if (lane == 31) after = 0.f;
-    if (2 * lane < S::kNodes) *reinterpret_cast<float2*>(&weights[i * S::kWeights + 2 * lane]) = make_float2(s0 ? expf(after + x1) : -1.f, s1 ? expf(after) : -1.f);
+    if (2 * lane < S::kNodes) *reinterpret_cast<float2*>(&weights[i * S::kWeights + 2 * lane]) = make_float2(s0 ? exp2_fast(after + x1) : -1.f, s1 ? exp2_fast(after) : -1.f);
     if (lane == 0) {
-      whole[i] = expf(sum);
+      whole[i] = exp2_fast(sum);
       bits[i] = seen;
     }
   }
@@ -122,35 +160,64 @@ __global__ void __launch_bounds__(2 * D, kTiles == 4 ? 1 : 2) tree_kernel(const 
 #pragma unroll
   for (int i = 0; i < kPieces; ++i) {
     const int at = i * S::kThreads + tid, node = at / (D / 8), e = at % (D / 8) * 8;
-    uint4 v = piece[2][i];
+    if (S::kNodes * D / 8 % S::kThreads != 0 && node >= S::kNodes) break;
+    uint32_t v[4] = {piece[2][i].x, piece[2][i].y, piece[2][i].z, piece[2][i].w};
     const uint32_t m = 0x7f807f80u, one = 0x00800080u;          // (an exponent of ones and one more carry into the sign's place)
-    if ((((v.x & m) + one) | ((v.y & m) + one) | ((v.z & m) + one) | ((v.w & m) + one)) & 0x80008000u) {
+    if ((((v[0] & m) + one) | ((v[1] & m) + one) | ((v[2] & m) + one) | ((v[3] & m) + one)) & 0x80008000u) {
       // values that are not finite stay out of the product, where they would reach nodes that do not see them
-      uint32_t word[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
       for (int j = 0; j < 8; ++j)
-        if (uint32_t x = word[j >> 1] >> (16 * (j & 1)); (x & 0x7f80u) == 0x7f80u) {
-          word[j >> 1] &= j & 1 ? 0x0000ffffu : 0xffff0000u;
+        if (const uint32_t x = v[j >> 1] >> (16 * (j & 1)); (x & 0x7f80u) == 0x7f80u) {
+          v[j >> 1] &= j & 1 ? 0x0000ffffu : 0xffff0000u;
           atomicOr(reinterpret_cast<unsigned long long*>(&odd[e + j]), 1ull << node);
         }
-      v = make_uint4(word[0], word[1], word[2], word[3]);
       *any_odd = 1;
     }
     *reinterpret_cast<uint4*>(qs + node * S::kRow + e) = piece[0][i];
     *reinterpret_cast<uint4*>(ks + node * S::kRow + e) = piece[1][i];
-    *reinterpret_cast<uint4*>(vs + node * S::kRow + e) = v;
+    // column 32 a + 4 x + j at 32 a + 8 j + x, the order of the state's columns
+    __nv_bfloat16* to = vs + node * S::kRow + (e & ~31) + (e >> 2 & 7);
+    *reinterpret_cast<uint32_t*>(to) = __byte_perm(v[0], v[2], 0x5410);
+    *reinterpret_cast<uint32_t*>(to + 8) = __byte_perm(v[0], v[2], 0x7632);
+    *reinterpret_cast<uint32_t*>(to + 16) = __byte_perm(v[1], v[3], 0x5410);
+    *reinterpret_cast<uint32_t*>(to + 24) = __byte_perm(v[1], v[3], 0x7632);
   }
   __syncthreads();
+  if (kTiles == 1) ask_rows(next);
 
-  // ---- what the nodes read of the state: halves of the rows one after the other
+  // ---- weighted scores, 16 nodes x 8 earlier ones at a time, as two bf16 numbers in the weights' place
+  constexpr int kPairs = kTiles * (kTiles + 1);
+  for (int u = warp; u < kPairs; u += S::kWarps) {
+    int tile = 0;
+    while ((tile + 1) * (tile + 2) <= u) ++tile;
+    const int first = (u - tile * (tile + 1)) * 8;
+    if (16 * tile >= r.n) break;
+    float s[4] = {0.f, 0.f, 0.f, 0.f};
+    const __nv_bfloat16 *q = qs + (16 * tile + g) * S::kRow + 2 * t, *k_at = ks + (first + g) * S::kRow + 2 * t;
+#pragma unroll
+    for (int k = 0; k < D; k += 16) {
+      const uint32_t a[4] = {lds(q + k), lds(q + k + 8 * S::kRow), lds(q + k + 8), lds(q + k + 8 * S::kRow + 8)};
+      mma(s, a, lds(k_at + k), lds(k_at + k + 8));
+    }
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      float2* at = reinterpret_cast<float2*>(&weights[(16 * tile + g + 8 * e) * S::kWeights + first + 2 * t]);
+      const float2 w = *at;
+      uint32_t high, low;
+      split(w.x < 0.f ? 0.f : s[2 * e] * w.x, w.y < 0.f ? 0.f : s[2 * e + 1] * w.y, high, low);
+      *at = make_float2(__uint_as_float(high), __uint_as_float(low));
+    }
+  }
+
+  // ---- what the nodes read of the state
+  float acc[kTiles][4][4];
+#pragma unroll
+  for (int i = 0; i < kTiles; ++i)
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) acc[i][j][e] = 0.f;
   if (r.in >= 0) {
-    float acc[kTiles][4][4];
-#pragma unroll
-    for (int i = 0; i < kTiles; ++i)
-#pragma unroll
-      for (int j = 0; j < 4; ++j)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) acc[i][j][e] = 0.f;
 #pragma unroll
     for (int k = 0; k < kSteps; ++k) {
       uint32_t high[4][2], low[4][2];
@@ -167,90 +234,85 @@ __global__ void __launch_bounds__(2 * D, kTiles == 4 ? 1 : 2) tree_kernel(const 
         const __nv_bfloat16* q = qs + (16 * i + g) * S::kRow + row0 + 16 * k + 2 * t;
         const uint32_t a[4] = {lds(q), lds(q + 8 * S::kRow), lds(q + 8), lds(q + 8 * S::kRow + 8)};
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          mma(acc[i][j], a, low[j][0], low[j][1]);
-          mma(acc[i][j], a, high[j][0], high[j][1]);
-        }
+        for (int j = 0; j < 4; ++j) mma(acc[i][j], a, low[j][0], low[j][1]);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) mma(acc[i][j], a, high[j][0], high[j][1]);
       }
     }
-    // a thread's columns: col0 + 8 t .. + 7 of rows g and g + 8 of each tile
 #pragma unroll
-    for (int turn = 1; turn >= 0; --turn) {
-      if (half == turn)
+    for (int i = 0; i < kTiles; ++i) {
+      const float f0 = whole[16 * i + g], f1 = whole[16 * i + g + 8];
 #pragma unroll
-        for (int i = 0; i < kTiles; ++i)
+      for (int j = 0; j < 4; ++j) acc[i][j][0] *= f0, acc[i][j][1] *= f0, acc[i][j][2] *= f1, acc[i][j][3] *= f1;
+    }
+  }
+  if (kEarly) ask_state(next);
+  __syncthreads();
+
+  // ---- weighted scores x values, 16 earlier nodes at a time, taken in turns by the warps of the same columns
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            float4* to = reinterpret_cast<float4*>(&from_state[(16 * i + g + 8 * (e >> 1)) * S::kSums + col0 + 8 * t + 4 * (e & 1)]);
-            float4 x = make_float4(acc[i][0][e], acc[i][1][e], acc[i][2][e], acc[i][3][e]);
-            if (turn == 0) {
-              const float4 y = *to;
-              x = make_float4(x.x + y.x, x.y + y.y, x.z + y.z, x.w + y.w);
-            }
-            *to = x;
-          }
-      __syncthreads();
+  for (int from = 0; from < kTiles; ++from) {
+    if ((from & 1 ? from ^ 2 : from) % S::kSplits != part && kTiles > 1) continue;
+    if (kTiles == 1 && part != 0) continue;
+    if (16 * from >= r.n) continue;
+    uint32_t v[2][4];                                           // each: two tiles of 8 columns
+#pragma unroll
+    for (int j = 0; j < 2; ++j) ldmatrix_trans(v[j], smem_at(vs + (16 * from + (lane & 15)) * S::kRow + col0 + 16 * j + 8 * (lane >> 4)));
+#pragma unroll
+    for (int i = from; i < kTiles; ++i) {
+      uint2 w[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        w[e] = *reinterpret_cast<const uint2*>(&weights[(16 * i + g + 8 * (e & 1)) * S::kWeights + 16 * from + 2 * t + 8 * (e >> 1)]);
+      const uint32_t high[4] = {w[0].x, w[1].x, w[2].x, w[3].x}, low[4] = {w[0].y, w[1].y, w[2].y, w[3].y};
+#pragma unroll
+      for (int j = 0; j < 4; ++j) mma(acc[i][j], low, v[j >> 1][2 * (j & 1)], v[j >> 1][2 * (j & 1) + 1]);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) mma(acc[i][j], high, v[j >> 1][2 * (j & 1)], v[j >> 1][2 * (j & 1) + 1]);
     }
   }
 
-  // ---- scores, their weights, values: warp = a tile of nodes and 16 kTiles columns
-  const int tile = warp % kTiles, first = warp / kTiles * S::kNodes, rows = min(r.n - 16 * tile, 16);
-  if (rows <= 0) return;
-  float out[2 * kTiles][4];
+  if (!kEarly) ask_state(next);
+
+  // ---- the parts together; a thread's columns: col0 + 8 t .. + 7 of rows g and g + 8 of each tile
+  const bool bad = *any_odd;
 #pragma unroll
-  for (int j = 0; j < 2 * kTiles; ++j)
+  for (int turn = S::kSplits - 1; turn >= 0; --turn) {
+    if (part == turn)
 #pragma unroll
-    for (int e = 0; e < 4; ++e) out[j][e] = 0.f;
-  uint32_t q[D / 16][4];
+      for (int i = 0; i < kTiles; ++i)
 #pragma unroll
-  for (int k = 0; k < D / 16; ++k) {
-    const __nv_bfloat16* at = qs + (16 * tile + g) * S::kRow + 16 * k + 2 * t;
-    q[k][0] = lds(at), q[k][1] = lds(at + 8 * S::kRow), q[k][2] = lds(at + 8), q[k][3] = lds(at + 8 * S::kRow + 8);
+        for (int e = 0; e < 2; ++e) {
+          const int node = 16 * i + g + 8 * e, col = col0 + 8 * t;
+          float4* at = reinterpret_cast<float4*>(&sums[node * S::kSums + col]);
+          float x[8] = {acc[i][0][2 * e], acc[i][1][2 * e], acc[i][2][2 * e], acc[i][3][2 * e],
+                        acc[i][0][2 * e + 1], acc[i][1][2 * e + 1], acc[i][2][2 * e + 1], acc[i][3][2 * e + 1]};
+          if (turn < S::kSplits - 1) {
+            const float4 a = at[0], c = at[1];
+            x[0] += a.x, x[1] += a.y, x[2] += a.z, x[3] += a.w, x[4] += c.x, x[5] += c.y, x[6] += c.z, x[7] += c.w;
+          }
+          if (turn > 0) {
+            at[0] = make_float4(x[0], x[1], x[2], x[3]);
+            at[1] = make_float4(x[4], x[5], x[6], x[7]);
+          } else if (node < r.n) {
+            if (bad)
+#pragma unroll
+              for (int j = 0; j < 8; ++j)
+                if (odd[col + j] & bits[node]) x[j] = __int_as_float(0x7fffffff);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) x[j] *= p.scale;
+            *reinterpret_cast<uint4*>(p.out + (int64_t)(r.row0 + node) * p.ldo + (int64_t)r.h * D + col) =
+                make_uint4(pack(x[0], x[1]), pack(x[2], x[3]), pack(x[4], x[5]), pack(x[6], x[7]));
+          }
+        }
+    __syncthreads();
   }
-#pragma unroll 1
-  for (int from = 0; from <= tile; ++from) {                    // 16 nodes that come before (or are the tile's own)
-    uint32_t high[4], low[4];
-#pragma unroll
-    for (int j = 0; j < 2; ++j) {
-      float s[4] = {0.f, 0.f, 0.f, 0.f};
-      const __nv_bfloat16* k_at = ks + (16 * from + 8 * j + g) * S::kRow + 2 * t;
-#pragma unroll
-      for (int k = 0; k < D / 16; ++k) mma(s, q[k], lds(k_at + 16 * k), lds(k_at + 16 * k + 8));
-      const float2 w0 = *reinterpret_cast<const float2*>(&weights[(16 * tile + g) * S::kWeights + 16 * from + 8 * j + 2 * t]);
-      const float2 w1 = *reinterpret_cast<const float2*>(&weights[(16 * tile + g + 8) * S::kWeights + 16 * from + 8 * j + 2 * t]);
-      split(w0.x < 0.f ? 0.f : s[0] * w0.x, w0.y < 0.f ? 0.f : s[1] * w0.y, high[2 * j], low[2 * j]);
-      split(w1.x < 0.f ? 0.f : s[2] * w1.x, w1.y < 0.f ? 0.f : s[3] * w1.y, high[2 * j + 1], low[2 * j + 1]);
-    }
-#pragma unroll
-    for (int j = 0; j < kTiles; ++j) {
-      uint32_t v[4];                                            // two tiles of 8 columns
-      ldmatrix_trans(v, smem_at(vs + (16 * from + (lane & 15)) * S::kRow + first + 16 * j + 8 * (lane >> 4)));
-      mma(out[2 * j], low, v[0], v[1]);
-      mma(out[2 * j], high, v[0], v[1]);
-      mma(out[2 * j + 1], low, v[2], v[3]);
-      mma(out[2 * j + 1], high, v[2], v[3]);
-    }
+  if (kTiles > 1) ask_rows(next);
+  } else {
+    ask_state(next);
+    ask_rows(next);
   }
-#pragma unroll
-  for (int e = 0; e < 2; ++e) {
-    const int node = 16 * tile + g + 8 * e;
-    if (g + 8 * e >= rows) continue;
-    const float f = whole[node];
-    __nv_bfloat16* dst = p.out + (int64_t)(r.row0 + node) * p.ldo + (int64_t)h * D + first + 2 * t;
-#pragma unroll
-    for (int j = 0; j < 2 * kTiles; ++j) {
-      float x = out[j][2 * e], y = out[j][2 * e + 1];
-      if (r.in >= 0) {
-        const float2 s = *reinterpret_cast<const float2*>(&from_state[node * S::kSums + first + 8 * j + 2 * t]);
-        x = fmaf(s.x, f, x);
-        y = fmaf(s.y, f, y);
-      }
-      if (*any_odd) {
-        if (odd[first + 8 * j + 2 * t] & bits[node]) x = __int_as_float(0x7fffffff);
-        if (odd[first + 8 * j + 2 * t + 1] & bits[node]) y = __int_as_float(0x7fffffff);
-      }
-      *reinterpret_cast<uint32_t*>(dst + 8 * j) = pack(x * p.scale, y * p.scale);
-    }
+  r = next;
   }
 }
 
@@ -259,7 +321,8 @@ cudaError_t launch(const LinearParams& p, int dev, cudaStream_t s) {
   using S = Shape<D, kTiles>;
   const cudaError_t e = allow_shared_memory<tree_kernel<D, kTiles>>(dev);
   if (e != cudaSuccess) return e;
-  tree_kernel<D, kTiles><<<dim3(p.H, p.B), S::kThreads, S::kSmem, s>>>(p);
+  const int64_t units = (int64_t)p.H * p.B, most = (int64_t)S::kResident * sm_count(dev);
+  tree_kernel<D, kTiles><<<(unsigned)(units < most ? units : most), S::kThreads, S::kSmem, s>>>(p);
   return cudaGetLastError();
 }
 template <int D>
