@@ -32,7 +32,8 @@ __device__ __forceinline__ uint32_t pack(float a, float b) {
 // Two numbers as the sum of two bf16 numbers each: 8 leading bits, and the rest rounded to 8 (a number that is not finite: itself and NaN).
 __device__ __forceinline__ void split(float a, float b, uint32_t& high, uint32_t& low) {
   high = __byte_perm(__float_as_uint(a), __float_as_uint(b), 0x7632);
-  low = pack(a - __uint_as_float(__float_as_uint(a) & 0xffff0000u), b - __uint_as_float(__float_as_uint(b) & 0xffff0000u));
+  const Pair rest = fma(Pair(__uint_as_float(__float_as_uint(a) & 0xffff0000u), __uint_as_float(__float_as_uint(b) & 0xffff0000u)), Pair(-1.f, -1.f), Pair(a, b));
+  low = pack(rest.floats().x, rest.floats().y);
 }
 __device__ __forceinline__ float exp2_fast(float x) {
   float y;
@@ -53,8 +54,11 @@ struct Shape {
   static constexpr int kColumns = D / 32, kSplits = kWarps / kColumns;   // groups of 32 columns, parts of the state's rows
   static constexpr int kRow = D + 8;                            // elements from one row to the next in shared memory: no bank twice
   static constexpr int kWeights = kNodes + 4, kSums = D + 4;
-  // q and k, whose place the sums take later; v; weights; per node mask and e^{e_i}; per column a mask
-  static constexpr int kV = (2 * kRow * 2 > kSums * 4 ? 2 * kRow * 2 : kSums * 4) * kNodes, kWeightsAt = kV + kNodes * kRow * 2;
+  // q, k and v; weights; sums (4 tiles: in q's and k's place); per node mask and e^{e_i}; per column a mask
+  static constexpr bool kApart = kTiles < 4;
+  static constexpr int kV = 2 * kRow * 2 * kNodes, kSumsAt = kApart ? kV + kNodes * kRow * 2 : 0;
+  static constexpr int kWeightsAt = kV + kNodes * kRow * 2 + (kApart ? kNodes * kSums * 4 : 0);
+  static_assert(kApart || kSums * 4 <= 2 * kRow * 2, "");
   static constexpr int kBits = kWeightsAt + kNodes * kWeights * 4, kSmem = kBits + kNodes * 12 + D * 8 + 16;
 };
 
@@ -65,7 +69,7 @@ __global__ void __launch_bounds__(Shape<D, kTiles>::kThreads, Shape<D, kTiles>::
   __nv_bfloat16* qs = reinterpret_cast<__nv_bfloat16*>(smem);
   __nv_bfloat16* ks = qs + S::kNodes * S::kRow;
   __nv_bfloat16* vs = reinterpret_cast<__nv_bfloat16*>(smem + S::kV);
-  float* sums = reinterpret_cast<float*>(smem);                 // [node][D]
+  float* sums = reinterpret_cast<float*>(smem + S::kSumsAt);    // [node][D]
   float* weights = reinterpret_cast<float*>(smem + S::kWeightsAt);   // [node][node] e^{e_ij}, -1 where j is not seen; then weighted scores
   uint64_t* bits = reinterpret_cast<uint64_t*>(smem + S::kBits);
   uint64_t* odd = bits + S::kNodes;                             // per column the nodes whose value is not finite
@@ -126,14 +130,15 @@ __global__ void __launch_bounds__(Shape<D, kTiles>::kThreads, Shape<D, kTiles>::
     if (p.bits && lane < kMasks && lane * S::kWarps + warp < r.n) mask = p.bits[r.row0 + lane * S::kWarps + warp];
   };
 
+  for (int i = tid; i < D; i += S::kThreads) odd[i] = 0;
+  if (tid == 0) *any_odd = 0;
   Unit r = look(blockIdx.x);
   ask_state(r);
   ask_rows(r);
+  __syncthreads();                                              // (odd is cleared)
   for (int u = blockIdx.x; u < units; u += gridDim.x) {
   const Unit next = look(u + gridDim.x);
   if (r.n > 0) {
-  for (int i = tid; i < D; i += S::kThreads) odd[i] = 0;
-  if (tid == 0) *any_odd = 0;
   // ---- weights: a warp's rows, sums from the row downwards
 #pragma unroll 4
   for (int j = 0; j < kMasks; ++j) {
@@ -156,7 +161,6 @@ __global__ void __launch_bounds__(Shape<D, kTiles>::kThreads, Shape<D, kTiles>::
       bits[i] = seen;
     }
   }
-  __syncthreads();                                              // (odd is cleared)
 #pragma unroll
   for (int i = 0; i < kPieces; ++i) {
     const int at = i * S::kThreads + tid, node = at / (D / 8), e = at % (D / 8) * 8;
@@ -192,13 +196,15 @@ __global__ void __launch_bounds__(Shape<D, kTiles>::kThreads, Shape<D, kTiles>::
     while ((tile + 1) * (tile + 2) <= u) ++tile;
     const int first = (u - tile * (tile + 1)) * 8;
     if (16 * tile >= r.n) break;
-    float s[4] = {0.f, 0.f, 0.f, 0.f};
+    float s[4] = {0.f, 0.f, 0.f, 0.f}, s2[4] = {0.f, 0.f, 0.f, 0.f};   // two chains of products
     const __nv_bfloat16 *q = qs + (16 * tile + g) * S::kRow + 2 * t, *k_at = ks + (first + g) * S::kRow + 2 * t;
 #pragma unroll
     for (int k = 0; k < D; k += 16) {
       const uint32_t a[4] = {lds(q + k), lds(q + k + 8 * S::kRow), lds(q + k + 8), lds(q + k + 8 * S::kRow + 8)};
-      mma(s, a, lds(k_at + k), lds(k_at + k + 8));
+      mma(k & 16 ? s2 : s, a, lds(k_at + k), lds(k_at + k + 8));
     }
+#pragma unroll
+    for (int e = 0; e < 4; ++e) s[e] += s2[e];
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
       float2* at = reinterpret_cast<float2*>(&weights[(16 * tile + g + 8 * e) * S::kWeights + first + 2 * t]);
@@ -305,6 +311,12 @@ __global__ void __launch_bounds__(Shape<D, kTiles>::kThreads, Shape<D, kTiles>::
                 make_uint4(pack(x[0], x[1]), pack(x[2], x[3]), pack(x[4], x[5]), pack(x[6], x[7]));
           }
         }
+    if (turn > 0 || !S::kApart) __syncthreads();
+  }
+  if (bad) {                                                    // (of all threads)
+    __syncthreads();
+    for (int i = tid; i < D; i += S::kThreads) odd[i] = 0;
+    if (tid == 0) *any_odd = 0;
     __syncthreads();
   }
   if (kTiles > 1) ask_rows(next);
