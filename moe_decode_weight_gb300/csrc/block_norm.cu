@@ -24,6 +24,23 @@ struct NormParams {
   int scattered;                                                // by elements, neighbouring threads at neighbouring ones
 };
 
+// Eight elements as they lie in memory, zeros where they are not asked for.
+template <typename T> struct Raw {
+  uint4 v[sizeof(T) / 2];
+  __device__ __forceinline__ void ask(const void* p, int64_t at, bool wanted) {
+    const T* src = static_cast<const T*>(p) + at;
+#pragma unroll
+    for (int i = 0; i < (int)sizeof(T) / 2; ++i)
+      asm volatile("{ .reg .pred p; setp.ne.b32 p, %5, 0; mov.b32 %0, 0; mov.b32 %1, 0; mov.b32 %2, 0; mov.b32 %3, 0; @p ld.global.v4.b32 {%0,%1,%2,%3}, [%4]; }"
+                   : "=&r"(v[i].x), "=&r"(v[i].y), "=&r"(v[i].z), "=&r"(v[i].w) : "l"(reinterpret_cast<const uint4*>(src) + i), "r"((int)wanted));
+  }
+  __device__ __forceinline__ void get(float (&f)[8]) const {
+    T e[8];
+    memcpy(e, v, sizeof e);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) f[i] = Elem<T>::to_float(e[i]);
+  }
+};
 template <typename T> __device__ __forceinline__ void load8(const void* p, int64_t at, float (&v)[8]) {
   const T* src = static_cast<const T*>(p) + at;
   if constexpr (sizeof(T) == 4) {
@@ -108,16 +125,32 @@ __global__ void __launch_bounds__(kMaxThreads) norm_kernel(const NormParams p) {
     return v;
   };
 
-  float z[kPieces][8], r[kPieces][8];
+  // Everything a row needs is asked for at once, by loads under a predicate (a branch around some of them would wait for the others), and
+  // unpacked when it is used.
+  float z[kPieces][8];
+  Raw<Y> y_raw[kVector ? kPieces : 1];
+  Raw<S> r_raw[kVector ? kPieces : 1];
+  Raw<T> gate[kVector ? kPieces : 1], weight[kVector ? kPieces : 1];
+  if constexpr (kVector) {
 #pragma unroll
-  for (int i = 0; i < kPieces; ++i) {
+    for (int i = 0; i < kPieces; ++i) {
+      const int at = place(i, 0);
+      const bool in = has(i, 0);
+      y_raw[i].ask(p.y, row * p.ldy + at, in);
+      r_raw[i].ask(p.residual, row * p.ldr + at, in && p.residual);
+      gate[i].ask(p.gate, row * p.ldg + at, in && p.gate);
+      weight[i].ask(p.post_w, p.group == p.width ? at : at & (p.group - 1), in && p.post_w);
+    }
 #pragma unroll
-    for (int j = 0; j < 8; ++j) z[i][j] = r[i][j] = 0.f;
-    get(Y(), p.y, row * p.ldy, i, z[i]);
+    for (int i = 0; i < kPieces; ++i) y_raw[i].get(z[i]);
+  } else {
+#pragma unroll
+    for (int i = 0; i < kPieces; ++i) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) z[i][j] = 0.f;
+      get(Y(), p.y, row * p.ldy, i, z[i]);
+    }
   }
-  if (p.residual)
-#pragma unroll
-    for (int i = 0; i < kPieces; ++i) get(S(), p.residual, row * p.ldr, i, r[i]);
   if (p.post_w) {
     float f[kPieces];
     if (p.group == p.width) {
@@ -144,14 +177,13 @@ __global__ void __launch_bounds__(kMaxThreads) norm_kernel(const NormParams p) {
       float w[8];
 #pragma unroll
       for (int j = 0; j < 8; ++j) w[j] = 0.f;
-      if (p.group == p.width) {
+      if constexpr (kVector) {
+        weight[i].get(w);
+      } else if (p.group == p.width) {
         get(T(), p.post_w, 0, i, w);
       } else if (has(i, 0)) {
-        const int at = place(i, 0) & (p.group - 1);
-        if constexpr (kVector) load8<T>(p.post_w, at, w);
-        else
 #pragma unroll
-          for (int j = 0; j < 8; ++j) w[j] = Elem<T>::to_float(static_cast<const T*>(p.post_w)[at + j]);
+        for (int j = 0; j < 8; ++j) w[j] = Elem<T>::to_float(static_cast<const T*>(p.post_w)[(place(i, 0) & (p.group - 1)) + j]);
       }
 #pragma unroll
       for (int j = 0; j < 8; ++j) z[i][j] *= f[i] * w[j];
@@ -163,7 +195,8 @@ __global__ void __launch_bounds__(kMaxThreads) norm_kernel(const NormParams p) {
       float g[8];
 #pragma unroll
       for (int j = 0; j < 8; ++j) g[j] = 0.f;
-      get(T(), p.gate, row * p.ldg, i, g);
+      if constexpr (kVector) gate[i].get(g);
+      else get(T(), p.gate, row * p.ldg, i, g);
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
         const float act = p.gate_kind == MDW_GATE_MUL ? 1.f : sigmoid(g[j]);
@@ -173,11 +206,16 @@ __global__ void __launch_bounds__(kMaxThreads) norm_kernel(const NormParams p) {
   float ss = 0.f;
 #pragma unroll
   for (int i = 0; i < kPieces; ++i) {
+    float r[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) r[j] = 0.f;
+    if constexpr (kVector) r_raw[i].get(r);
+    else if (p.residual) get(S(), p.residual, row * p.ldr, i, r);
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
       float s = p.branch_scale * z[i][j];
-      if (p.residual) s = fmaf(p.residual_scale, r[i][j], s);
-      z[i][j] = Elem<S>::to_float(Elem<S>::from_float(s));
+      if (p.residual) s = fmaf(p.residual_scale, r[j], s);
+      z[i][j] = p.x ? Elem<S>::to_float(Elem<S>::from_float(s)) : s;
       ss = fmaf(z[i][j], z[i][j], ss);
     }
     if (p.sum) put(S(), p.sum, row * p.lds, i, z[i]);
