@@ -5,8 +5,7 @@
 //
 // What bounds it is memory for many rows and the two chains load - sum - exchange for few. A row lies in the
 // registers of its threads, eight neighbouring elements (16 or 32 bytes of a load) at a time, so it is read once; the norms are
-// sums over the row's warps. Rows that are not on 16-byte boundaries are read and written by elements, neighbouring threads at
-// neighbouring ones.
+// sums over the row's warps. Rows that are not on 16-byte boundaries are read by the aligned pieces around them and shifted in registers.
 #include <cmath>
 #include <type_traits>
 
@@ -15,57 +14,114 @@
 namespace mdw {
 namespace {
 
+static_assert(MDW_MAX_NORM_WIDTH <= 2 * 8 * 1024, "");
+
 struct NormParams {
   const void *y, *post_w, *gate, *residual, *pre_w;
   void *sum, *x;
   int64_t ldy, ldg, ldr, lds, ldx;
   float branch_scale, residual_scale, eps, inv_group, inv_width;
   int T, width, group, gate_kind, threads;                      // threads of a row
-  int scattered;                                                // by elements, neighbouring threads at neighbouring ones
 };
 
-// Eight elements as they lie in memory, zeros where they are not asked for.
-template <typename T> struct Raw {
-  uint4 v[sizeof(T) / 2];
-  __device__ __forceinline__ void ask(const void* p, int64_t at, bool wanted) {
-    const T* src = static_cast<const T*>(p) + at;
+__device__ __forceinline__ void load16_if(uint4& v, const void* src, bool wanted) {
+  asm volatile("{ .reg .pred p; setp.ne.b32 p, %5, 0; mov.b32 %0, 0; mov.b32 %1, 0; mov.b32 %2, 0; mov.b32 %3, 0; @p ld.global.v4.b32 {%0,%1,%2,%3}, [%4]; }"
+               : "=&r"(v.x), "=&r"(v.y), "=&r"(v.z), "=&r"(v.w) : "l"(src), "r"((int)wanted));
+}
+// Words moved towards the first one, by `halves` half words (below 16).
+template <int kWords> __device__ __forceinline__ void shift_words(uint32_t (&w)[kWords], int halves) {
 #pragma unroll
-    for (int i = 0; i < (int)sizeof(T) / 2; ++i)
-      asm volatile("{ .reg .pred p; setp.ne.b32 p, %5, 0; mov.b32 %0, 0; mov.b32 %1, 0; mov.b32 %2, 0; mov.b32 %3, 0; @p ld.global.v4.b32 {%0,%1,%2,%3}, [%4]; }"
-                   : "=&r"(v[i].x), "=&r"(v[i].y), "=&r"(v[i].z), "=&r"(v[i].w) : "l"(reinterpret_cast<const uint4*>(src) + i), "r"((int)wanted));
+  for (int n = 4; n >= 1; n >>= 1)
+    if (halves & 2 * n)
+#pragma unroll
+      for (int i = 0; i + n < kWords; ++i) w[i] = w[i + n];
+  if (halves & 1)
+#pragma unroll
+    for (int i = 0; i + 1 < kWords; ++i) w[i] = __funnelshift_r(w[i], w[i + 1], 16);
+}
+
+// Eight elements of a row, element `at` (a multiple of 8) and on, as they lie in memory; zeros where there are none. Rows that do not lie on
+// 16-byte boundaries are read by the 16-byte pieces around the elements, which may reach into the rows beside them, and shifted. Only the
+// ends of the whole array (`total` elements) are read by elements: waiting for those of every row took three times as long.
+template <typename T, bool kAligned> struct Raw {
+  static constexpr int kLoads = sizeof(T) / 2 + (kAligned ? 0 : 1), kPer = 16 / sizeof(T);
+  uint4 v[kLoads];
+  int off, left;                                                // elements before the first one, and of the row from it on
+  __device__ __forceinline__ void ask(const void* p, int64_t base, int at, int width, int64_t total, bool wanted) {
+    const T* src = static_cast<const T*>(p) + base + at;
+    off = 0;
+    if constexpr (kAligned) {
+#pragma unroll
+      for (int i = 0; i < kLoads; ++i) load16_if(v[i], src + i * kPer, wanted);
+    } else {
+      if (wanted) off = (int)(reinterpret_cast<uintptr_t>(src) & 15) / (int)sizeof(T);
+      const int reach = off ? kLoads * kPer - off : 8;
+      const bool inside = wanted && base + at >= off && base + at + reach <= total;
+      left = wanted ? width - at : 0;
+#pragma unroll
+      for (int i = 0; i < kLoads; ++i) load16_if(v[i], src - off + i * kPer, inside && (i + 1 < kLoads || off));
+      if (wanted && !inside) {
+        T e[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) e[j] = at + j < width ? src[j] : T(0.f);
+        memcpy(v, e, sizeof e);
+        off = 0;
+      }
+    }
   }
   __device__ __forceinline__ void get(float (&f)[8]) const {
+    uint32_t w[4 * kLoads];
+    memcpy(w, v, sizeof w);
+    if constexpr (!kAligned)
+      if (off) shift_words(w, off * (int)sizeof(T) / 2);
     T e[8];
-    memcpy(e, v, sizeof e);
+    memcpy(e, w, sizeof e);
 #pragma unroll
     for (int i = 0; i < 8; ++i) f[i] = Elem<T>::to_float(e[i]);
+    if constexpr (!kAligned)
+      if (left < 8)
+#pragma unroll
+        for (int i = 0; i < 8; ++i) f[i] = i < left ? f[i] : 0.f;
   }
 };
-template <typename T> __device__ __forceinline__ void load8(const void* p, int64_t at, float (&v)[8]) {
-  const T* src = static_cast<const T*>(p) + at;
-  if constexpr (sizeof(T) == 4) {
-    const float4 a = reinterpret_cast<const float4*>(src)[0], b = reinterpret_cast<const float4*>(src)[1];
-    v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
-  } else {
-    const uint4 x = *reinterpret_cast<const uint4*>(src);
-    T e[8];
-    memcpy(e, &x, 16);
+
+// Stores the row's elements at .. at + 7 (those below width) of every lane of a warp; neighbouring lanes have neighbouring ones. Rows that do not
+// lie on 16-byte boundaries: a lane takes over the last elements of the lane before it and writes whole 16-byte pieces; what no lane
+// takes over is written by elements.
+template <typename T, bool kAligned> __device__ __forceinline__ void store_row(void* p, int64_t base, int at, int width, bool wanted, const float (&f)[8]) {
+  T e[8];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = Elem<T>::to_float(e[i]);
-  }
-}
-template <typename T> __device__ __forceinline__ void store8(void* p, int64_t at, const float (&v)[8]) {
-  T* dst = static_cast<T*>(p) + at;
-  if constexpr (sizeof(T) == 4) {
-    reinterpret_cast<float4*>(dst)[0] = make_float4(v[0], v[1], v[2], v[3]);
-    reinterpret_cast<float4*>(dst)[1] = make_float4(v[4], v[5], v[6], v[7]);
-  } else {
-    T e[8];
+  for (int i = 0; i < 8; ++i) e[i] = Elem<T>::from_float(f[i]);
+  T* dst = static_cast<T*>(p) + base + at;
+  constexpr int kPer = 16 / sizeof(T), kPiecesOf8 = 8 / kPer, kWords = 2 * sizeof(T);
+  if constexpr (kAligned) {
+    uint4 x[kPiecesOf8];
+    memcpy(x, e, sizeof e);
+    if (wanted)
 #pragma unroll
-    for (int i = 0; i < 8; ++i) e[i] = Elem<T>::from_float(v[i]);
-    uint4 x;
-    memcpy(&x, e, 16);
-    *reinterpret_cast<uint4*>(dst) = x;
+      for (int i = 0; i < kPiecesOf8; ++i) reinterpret_cast<uint4*>(dst)[i] = x[i];
+  } else {
+    const int off = (int)(reinterpret_cast<uintptr_t>(dst) & 15) / (int)sizeof(T), lane = threadIdx.x & 31, count = wanted ? min(width - at, 8) : 0;
+    uint32_t w[4 + kWords];                                     // the last 16 bytes of the lane before, then the lane's own
+    memcpy(w + 4, e, sizeof e);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) w[i] = __shfl_up_sync(0xffffffffu, w[kWords + i], 1);
+    shift_words(w, (kPer - off) * (int)sizeof(T) / 2);          // (off = 0: by 16 bytes, so that only the lane's own are left)
+#pragma unroll
+    for (int i = 0; i < kPiecesOf8; ++i) {
+      // elements i kPer - off .. + kPer - 1 of the lane's
+      const bool whole = count >= (i + 1) * kPer - off && (i > 0 || off == 0 || (lane > 0 && at > 0));
+      if (whole) reinterpret_cast<uint4*>(dst - off)[i] = make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
+      else
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+          if (j < count && j >= i * kPer - off && j < (i + 1) * kPer - off) dst[j] = e[j];
+    }
+    // the last ones, if the next lane does not take them over
+    if (off != 0 && !(lane < 31 && width - at - 8 >= kPer - off))
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        if (j < count && j >= 8 - off) dst[j] = e[j];
   }
 }
 
@@ -78,38 +134,19 @@ __device__ __forceinline__ float sigmoid(float x) {
   return r;
 }
 
-constexpr int kMaxThreads = 512;
+// Pieces of a thread: two, as more rows are on their way then; rows off 16-byte boundaries take more registers a piece and are spread over
+// more threads, up to 8,192 elements one piece each (16,000 rows of 2,563 elements: two pieces a thread 278 us, one 160).
+constexpr int kMaxThreads = 1024;
 
-// T: the 16-bit type; Y, S: types of y and of residual and sum. kPieces of eight elements a thread. kVector: by 16 bytes.
+// T: the 16-bit type; Y, S: types of y and of residual and sum. kPieces of eight elements a thread. kVector: all rows on 16-byte
+// boundaries, and whole pieces.
 template <typename T, typename Y, typename S, int kPieces, bool kVector>
 __global__ void __launch_bounds__(kMaxThreads) norm_kernel(const NormParams p) {
   __shared__ float part[2][32];
   const int row = blockIdx.x * (blockDim.x / p.threads) + threadIdx.x / p.threads, tid = threadIdx.x % p.threads;
   const bool live = row < p.T;                                  // (rows share a block only where a row is a warp's)
-  auto place = [&](int i, int j) {                              // of element j of piece i
-    return kVector || !p.scattered ? (i * p.threads + tid) * 8 + j : (i * 8 + j) * p.threads + tid;
-  };
-  auto has = [&](int i, int j) { return live && (kVector ? (i * p.threads + tid) * 8 < p.width : place(i, j) < p.width); };
-  auto get = [&](auto type, const void* src, int64_t base, int i, float (&v)[8]) {
-    using E = decltype(type);
-    if constexpr (kVector) {
-      if (has(i, 0)) load8<E>(src, base + place(i, 0), v);
-    } else {
-#pragma unroll
-      for (int j = 0; j < 8; ++j)
-        if (has(i, j)) v[j] = Elem<E>::to_float(static_cast<const E*>(src)[base + place(i, j)]);
-    }
-  };
-  auto put = [&](auto type, void* dst, int64_t base, int i, const float (&v)[8]) {
-    using E = decltype(type);
-    if constexpr (kVector) {
-      if (has(i, 0)) store8<E>(dst, base + place(i, 0), v);
-    } else {
-#pragma unroll
-      for (int j = 0; j < 8; ++j)
-        if (has(i, j)) static_cast<E*>(dst)[base + place(i, j)] = Elem<E>::from_float(v[j]);
-    }
-  };
+  auto place = [&](int i) { return (i * p.threads + tid) * 8; };   // first element of piece i
+  auto has = [&](int i) { return live && place(i) < p.width; };
   // sum over the threads of a row
   auto over_row = [&](float v, int which) {
 #pragma unroll
@@ -128,29 +165,21 @@ __global__ void __launch_bounds__(kMaxThreads) norm_kernel(const NormParams p) {
   // Everything a row needs is asked for at once, by loads under a predicate (a branch around some of them would wait for the others), and
   // unpacked when it is used.
   float z[kPieces][8];
-  Raw<Y> y_raw[kVector ? kPieces : 1];
-  Raw<S> r_raw[kVector ? kPieces : 1];
-  Raw<T> gate[kVector ? kPieces : 1], weight[kVector ? kPieces : 1];
-  if constexpr (kVector) {
+  Raw<Y, kVector> y[kPieces];
+  Raw<S, kVector> r[kPieces];
+  Raw<T, kVector> gate[kPieces], weight[kPieces];
 #pragma unroll
-    for (int i = 0; i < kPieces; ++i) {
-      const int at = place(i, 0);
-      const bool in = has(i, 0);
-      y_raw[i].ask(p.y, row * p.ldy + at, in);
-      r_raw[i].ask(p.residual, row * p.ldr + at, in && p.residual);
-      gate[i].ask(p.gate, row * p.ldg + at, in && p.gate);
-      weight[i].ask(p.post_w, p.group == p.width ? at : at & (p.group - 1), in && p.post_w);
-    }
-#pragma unroll
-    for (int i = 0; i < kPieces; ++i) y_raw[i].get(z[i]);
-  } else {
-#pragma unroll
-    for (int i = 0; i < kPieces; ++i) {
-#pragma unroll
-      for (int j = 0; j < 8; ++j) z[i][j] = 0.f;
-      get(Y(), p.y, row * p.ldy, i, z[i]);
-    }
+  for (int i = 0; i < kPieces; ++i) {
+    const int at = place(i);
+    const bool in = has(i);
+    y[i].ask(p.y, row * p.ldy, at, p.width, (p.T - 1) * p.ldy + p.width, in);
+    r[i].ask(p.residual, row * p.ldr, at, p.width, (p.T - 1) * p.ldr + p.width, in && p.residual != nullptr);
+    gate[i].ask(p.gate, row * p.ldg, at, p.width, (p.T - 1) * p.ldg + p.width, in && p.gate != nullptr);
+    if (p.group == p.width) weight[i].ask(p.post_w, 0, at, p.width, p.width, in && p.post_w != nullptr);
+    else weight[i].ask(p.post_w, 0, at & (p.group - 1), p.group, p.group, in && p.post_w != nullptr);
   }
+#pragma unroll
+  for (int i = 0; i < kPieces; ++i) y[i].get(z[i]);
   if (p.post_w) {
     float f[kPieces];
     if (p.group == p.width) {
@@ -175,16 +204,7 @@ __global__ void __launch_bounds__(kMaxThreads) norm_kernel(const NormParams p) {
 #pragma unroll
     for (int i = 0; i < kPieces; ++i) {
       float w[8];
-#pragma unroll
-      for (int j = 0; j < 8; ++j) w[j] = 0.f;
-      if constexpr (kVector) {
-        weight[i].get(w);
-      } else if (p.group == p.width) {
-        get(T(), p.post_w, 0, i, w);
-      } else if (has(i, 0)) {
-#pragma unroll
-        for (int j = 0; j < 8; ++j) w[j] = Elem<T>::to_float(static_cast<const T*>(p.post_w)[(place(i, 0) & (p.group - 1)) + j]);
-      }
+      weight[i].get(w);
 #pragma unroll
       for (int j = 0; j < 8; ++j) z[i][j] *= f[i] * w[j];
     }
@@ -193,10 +213,7 @@ __global__ void __launch_bounds__(kMaxThreads) norm_kernel(const NormParams p) {
 #pragma unroll
     for (int i = 0; i < kPieces; ++i) {
       float g[8];
-#pragma unroll
-      for (int j = 0; j < 8; ++j) g[j] = 0.f;
-      if constexpr (kVector) gate[i].get(g);
-      else get(T(), p.gate, row * p.ldg, i, g);
+      gate[i].get(g);
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
         const float act = p.gate_kind == MDW_GATE_MUL ? 1.f : sigmoid(g[j]);
@@ -206,31 +223,29 @@ __global__ void __launch_bounds__(kMaxThreads) norm_kernel(const NormParams p) {
   float ss = 0.f;
 #pragma unroll
   for (int i = 0; i < kPieces; ++i) {
-    float r[8];
-#pragma unroll
-    for (int j = 0; j < 8; ++j) r[j] = 0.f;
-    if constexpr (kVector) r_raw[i].get(r);
-    else if (p.residual) get(S(), p.residual, row * p.ldr, i, r);
+    float old[8];
+    r[i].get(old);
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
       float s = p.branch_scale * z[i][j];
-      if (p.residual) s = fmaf(p.residual_scale, r[j], s);
+      if (p.residual) s = fmaf(p.residual_scale, old[j], s);
       z[i][j] = p.x ? Elem<S>::to_float(Elem<S>::from_float(s)) : s;
       ss = fmaf(z[i][j], z[i][j], ss);
     }
-    if (p.sum) put(S(), p.sum, row * p.lds, i, z[i]);
+    if (p.sum) store_row<S, kVector>(p.sum, row * p.lds, place(i), p.width, has(i), z[i]);
   }
   if (!p.x) return;
+  Raw<T, kVector> pre[kPieces];
+#pragma unroll
+  for (int i = 0; i < kPieces; ++i) pre[i].ask(p.pre_w, 0, place(i), p.width, p.width, has(i));
   const float f = rsqrtf(over_row(ss, 1) * p.inv_width + p.eps);
 #pragma unroll
   for (int i = 0; i < kPieces; ++i) {
     float w[8];
-#pragma unroll
-    for (int j = 0; j < 8; ++j) w[j] = 0.f;
-    get(T(), p.pre_w, 0, i, w);
+    pre[i].get(w);
 #pragma unroll
     for (int j = 0; j < 8; ++j) w[j] *= z[i][j] * f;
-    put(T(), p.x, row * p.ldx, i, w);
+    store_row<T, kVector>(p.x, row * p.ldx, place(i), p.width, has(i), w);
   }
 }
 
@@ -238,14 +253,13 @@ template <typename T, typename Y, typename S, bool kVector>
 cudaError_t launch(const NormParams& p0, cudaStream_t s) {
   NormParams p = p0;
   const int vectors = (p.width + 7) / 8;
-  const int pieces = vectors <= 32 ? 1 : vectors <= 2 * kMaxThreads ? 2 : 4;
+  const int pieces = vectors <= (kVector ? 32 : kMaxThreads) ? 1 : 2;
   p.threads = ((vectors + pieces - 1) / pieces + 31) / 32 * 32;
   const int rows = p.threads == 32 ? 4 : 1;
   const unsigned blocks = (unsigned)((p.T + rows - 1) / rows);
   const int threads = p.threads * rows;
   if (pieces == 1) norm_kernel<T, Y, S, 1, kVector><<<blocks, threads, 0, s>>>(p);
-  else if (pieces == 2) norm_kernel<T, Y, S, 2, kVector><<<blocks, threads, 0, s>>>(p);
-  else norm_kernel<T, Y, S, 4, kVector><<<blocks, threads, 0, s>>>(p);
+  else norm_kernel<T, Y, S, 2, kVector><<<blocks, threads, 0, s>>>(p);
   return cudaGetLastError();
 }
 template <typename T>
@@ -283,8 +297,8 @@ extern "C" mdw_status mdw_block_norm(int32_t T, int32_t width, int32_t dtype, co
   auto row_ok = [](const void* q, int64_t ld, uintptr_t e) { return q == nullptr || (aligned_to(q, 16) && ld * e % 16 == 0); };
   const bool vector = width % 8 == 0 && row_ok(y, ldy, ye) && row_ok(post_w, 0, 2) && row_ok(gate, ldg, 2) && row_ok(residual, ldr, se) &&
                       row_ok(sum, lds, se) && row_ok(pre_w, 0, 2) && row_ok(x, ldx, 2);
-  NormParams p{y, post_w, gate, residual, pre_w, sum, x, ldy, ldg, ldr, lds, ldx, branch_scale, residual_scale, eps, 1.f / (float)group,
-               1.f / (float)width, T, width, group, gate_kind, 0, group == width || !post_w};
+  const NormParams p{y, post_w, gate, residual, pre_w, sum, x, ldy, ldg, ldr, lds, ldx, branch_scale, residual_scale, eps, 1.f / (float)group,
+               1.f / (float)width, T, width, group, gate_kind, 0};
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   const cudaError_t e = dtype == MDW_DT_BF16 ? launch<__nv_bfloat16>(p, y_dtype == MDW_DT_F32, sum_dtype == MDW_DT_F32, vector, s)
                                              : launch<__half>(p, y_dtype == MDW_DT_F32, sum_dtype == MDW_DT_F32, vector, s);
