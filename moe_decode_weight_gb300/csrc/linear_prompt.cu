@@ -22,8 +22,7 @@
 //   warp 1       issues the products for the state
 //   warp 2       sums the decays of the next chunk
 //   warp 3       issues the products for the outputs
-//   warps 4-7    weights the scores, one thread a row
-//   warps 8-11   the outputs, one thread a row
+//   warps 4-11   weight the scores and take the outputs, two threads a row
 //   warps 12-27  the decayed values and the state, four threads a row of the state
 #include <cuda.h>
 
@@ -35,7 +34,7 @@
 namespace mdw {
 namespace {
 
-constexpr int kChunk = kLinearChunk, kStateWarps = 16, kThreads = 32 * (12 + kStateWarps);
+constexpr int kChunk = kLinearChunk, kRowWarps = 8, kStateWarps = 16, kThreads = 32 * (12 + kStateWarps);
 constexpr float kLn2 = 0.6931471805599453f;
 
 __device__ __forceinline__ void tma_load(uint32_t dst, const CUtensorMap* map, uint32_t bar, int x, int head, int row) {
@@ -61,6 +60,13 @@ __device__ __forceinline__ bool mbar_try_long(uint32_t bar, uint32_t parity) {
   asm volatile("{ .reg .pred p; mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3; selp.u32 %0, 1, 0, p; }"
                : "=r"(ok) : "r"(bar), "r"(parity), "r"(10000u) : "memory");
   return ok != 0;
+}
+// 16 lanes x 8 columns of tensor memory: a thread has columns lane % 4 and lane % 4 + 4 of lanes lane / 4 and lane / 4 + 8.
+__device__ __forceinline__ void tc_st_16x128(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+  asm volatile("tcgen05.st.sync.aligned.16x128b.x2.b32 [%0], {%1,%2,%3,%4};" :: "r"(addr), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
+}
+__device__ __forceinline__ void ldmatrix_trans(uint32_t (&r)[4], uint32_t at) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];" : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(at) : "memory");
 }
 // Two fp32 numbers as bf16 (low half: a), and back.
 __device__ __forceinline__ uint32_t pack(float a, float b) {
@@ -199,16 +205,17 @@ __global__ void __launch_bounds__(256) sums_kernel(const LinearPlan w, int H, in
 
 // ------------------------------------------------------------------ the kernel
 
-// Shared memory: a tile of q, two of k and of v, a ring of two steps of decayed values (three parts of kStep rows), the state.
+// Shared memory: a tile of q, two of k and of v, the state as the outputs read it (rows: columns of the state).
 template <int D, bool kRows>
 struct Shape {
   static constexpr int kTile = kChunk * D * 2, kHalves = D / 64;
-  static constexpr int kStep = 32 / kHalves, kSteps = kChunk / kStep, kPart = kStep * D * 2;
-  static constexpr int kQ = 0, kK = kTile, kV = 3 * kTile, kW = 5 * kTile, kS = kW + 6 * kPart;
-  static constexpr int kSmall = kS + D * D * 2, kBarriers = 34;
-  static constexpr int kSmem = kSmall + 2 * (5 * kChunk * 4 + 28 * 4) + kBarriers * 8 + 16;   // sums, barriers, words
-  // tensor memory columns: scores (the weighted ones take their first half when D = 128), two outputs, what a chunk adds to the state
-  static constexpr int kOut = 128, kAdd = 128 + 2 * D, kProb = D == 128 ? 0 : 320;
+  static constexpr int kStep = 16, kSteps = kChunk / kStep;     // rows of a step of the state's product
+  static constexpr int kQ = 0, kK = kTile, kV = 3 * kTile, kS = 5 * kTile;
+  static constexpr int kSmall = kS + D * D * 2, kBarriers = 35;
+  static constexpr int kSmem = kSmall + 2 * (5 * kChunk * 4 + 28 * 4) + kBarriers * 8 + 32;   // sums, barriers, words
+  // Tensor memory columns: scores (the weighted ones take their first half when D = 128), outputs, what a chunk adds to the state (a lane is a
+  // column of the state), and four steps of decayed values, each in three parts.
+  static constexpr int kOut = 256 - D, kAdd = 256, kParts = 384, kProb = D == 128 ? 0 : 128;
   static constexpr int kCols = D / 4;                           // of the state, a thread
 };
 
@@ -225,8 +232,7 @@ struct alignas(16) Sums {
   float base[4];                   // from the start of the chunk to the start of the block
   float factor;                    // of the chunk, less 1 if near
   int near, valid, more;           // valid rows; whether the block has another chunk
-  int bad;                         // whether values that are not finite were taken out
-  int strong, pad[2];              // whether any row's power of two is not 1
+  int strong, pad[3];              // whether any row's power of two is not 1
 };
 
 template <int D, bool kRows>
@@ -241,10 +247,11 @@ prompt_kernel(const LinearParams p, const LinearPlan w, const __grid_constant__ 
   uint32_t bar = smem_u32(sums_at + 2);
   auto take = [&](int n) { const uint32_t r = bar; bar += 8 * n; return r; };
   const uint32_t q_full = take(1), q_free = take(1), q_ok = take(1), k_full = take(2), k_free = take(2), v_full = take(2), v_free = take(2), v_done = take(2);
-  const uint32_t sums_full = take(2), sums_free = take(2), s_full = take(1), p_full = take(1), o_full = take(2), o_free = take(2);
-  const uint32_t w_full = take(2), w_free = take(4), state_full = take(1), state_read = take(1);
+  const uint32_t sums_full = take(2), sums_free = take(2), s_full = take(1), p_full = take(1), o_full = take(2), o_free = take(1);
+  const uint32_t w_full = take(4), w_free = take(4), state_full = take(1), state_read = take(1);
   const uint32_t add_full = take(1), add_read = take(1), end = take(1);
   uint32_t* words = reinterpret_cast<uint32_t*>(smem + (bar - base));
+  volatile uint32_t* bad_values = words + 4;                    // [4], by chunk: whether values that are not finite were taken out
   volatile int* dead = reinterpret_cast<volatile int*>(words);
   after_previous();
   const int units = w.head[kRows ? 0 : 1];
@@ -268,18 +275,16 @@ prompt_kernel(const LinearParams p, const LinearPlan w, const __grid_constant__ 
       mbar_init(v_full + 8 * i, 1);
       mbar_init(v_free + 8 * i, kStateWarps + (kRows ? 1 : 0));
       mbar_init(v_done + 8 * i, kStateWarps);
-      mbar_init(w_full + 8 * i, kStateWarps / 4);
-      mbar_init(w_free + 8 * i, 1);
-      mbar_init(w_free + 16 + 8 * i, 1);
+      for (int j = i; j < 4; j += 2) {
+        mbar_init(w_full + 8 * j, kStateWarps / 4);
+        mbar_init(w_free + 8 * j, 1);
+      }
       mbar_init(sums_full + 8 * i, 1);
-      mbar_init(sums_free + 8 * i, kStateWarps + (kRows ? 8 : 0));
+      mbar_init(sums_free + 8 * i, kStateWarps + (kRows ? kRowWarps : 0));
     }
     for (const uint32_t b : {q_full, q_free, s_full, o_full, o_full + 8, state_read, add_full}) mbar_init(b, 1);
     mbar_init(end, kRows ? 2 : 1);
-    mbar_init(p_full, 4);
-    mbar_init(q_ok, 4);
-    mbar_init(o_free, 4);
-    mbar_init(o_free + 8, 4);
+    for (const uint32_t b : {p_full, q_ok, o_free}) mbar_init(b, kRowWarps);
     mbar_init(state_full, kStateWarps);
     mbar_init(add_read, kStateWarps);
     *dead = 0;
@@ -365,21 +370,16 @@ prompt_kernel(const LinearParams p, const LinearPlan w, const __grid_constant__ 
         if (g > 0) wait(add_read, (g - 1) & 1);                 // the sums of the last chunk are out of their columns
 #pragma unroll 1
         for (int step = 0; step < S::kSteps; ++step) {
-          const int use = g * S::kSteps + step, at = use & 1;
-          wait(w_full + 8 * at, use >> 1 & 1);
+          const int use = g * S::kSteps + step, at = use & 3;
+          wait(w_full + 8 * at, use >> 2 & 1);
           tc_fence_after();
           if (elect_one()) {
-            // k is the first operand transposed: 64 of its columns at a time (heads of 64: the second 64 lie behind the tile, and what they
-            // hold only reaches lanes that are not read). The smallest part of the values is summed first.
+            // the smallest part of the values is summed first
             const uint32_t kl = operand_low(k_at + step * (S::kStep * 128), kChunk * 128);
 #pragma unroll
-            for (int part = 0; part < 3; ++part) {
-              const uint32_t wl = operand_low(base + S::kW + (3 * at + part) * S::kPart, S::kStep * 128);
-#pragma unroll
-              for (int i = 0; i < S::kStep / 16; ++i)
-                tc_mma(tmem + S::kAdd, kl + i * (2048 >> 4), wl + i * (2048 >> 4), mma_shape(true, true, D) | 1u << 15, step > 0 || part > 0 || i > 0);
-            }
-            tc_commit(w_free + 8 * (use & 3));
+            for (int part = 0; part < 3; ++part)
+              tc_mma_tmem(tmem + S::kAdd, tmem + S::kParts + 8 * (3 * at + part), kl, mma_shape(true, true, D), step > 0 || part > 0);
+            tc_commit(w_free + 8 * at);
             if (step == S::kSteps - 1) {
               tc_commit(add_full);
               tc_commit(k_free + 8 * slot);
@@ -398,7 +398,7 @@ prompt_kernel(const LinearParams p, const LinearPlan w, const __grid_constant__ 
       each_unit([&](int u, int chunks, int g0, int k) {
         for (int c = 0; c < chunks; ++c) {
           const int g = g0 + c, slot = g & 1;
-          const uint32_t ql = operand_low(base + S::kQ, 16), out = tmem + S::kOut + slot * D;
+          const uint32_t ql = operand_low(base + S::kQ, 16), out = tmem + S::kOut;
           wait(k_full + 8 * slot, g >> 1 & 1);
           wait(q_full, g & 1);
           if (g > 0) wait(o_full + 8 * (slot ^ 1), (g - 1) >> 1 & 1);   // (the weighted scores lie in the scores' columns)
@@ -416,13 +416,13 @@ prompt_kernel(const LinearParams p, const LinearPlan w, const __grid_constant__ 
           __syncwarp();
           wait(q_ok, g & 1);
           wait(state_full, g & 1);
-          wait(o_free + 8 * slot, (g >> 1 & 1) ^ 1);
+          wait(o_free, (g & 1) ^ 1);
           tc_fence_after();
           if (elect_one()) {
-            const uint32_t sl = operand_low(base + S::kS, D * 128);
+            const uint32_t sl = operand_low(base + S::kS, 16);
 #pragma unroll
             for (int i = 0; i < D / 16; ++i)
-              tc_mma(out, ql + (((i >> 2) * (kChunk * 128) + (i & 3) * 32) >> 4), sl + i * (2048 >> 4), mma_shape(true, true, D), i > 0);
+              tc_mma(out, ql + (((i >> 2) * (kChunk * 128) + (i & 3) * 32) >> 4), sl + (((i >> 2) * (D * 128) + (i & 3) * 32) >> 4), mma_shape(true, false, D), i > 0);
             tc_commit(state_read);
             tc_commit(q_free);
           }
@@ -513,7 +513,7 @@ prompt_kernel(const LinearParams p, const LinearPlan w, const __grid_constant__ 
           sums.near = whole.near;
           sums.valid = min(e.rows - c * kChunk, kChunk);
           sums.more = more;
-          sums.bad = 0;
+          bad_values[g & 3] = 0;                                // (the outputs of the chunk four before were taken before the weights of the one after)
           sums.strong = strong;
         }
         if (!kRows) unit = unit + last;
@@ -521,23 +521,65 @@ prompt_kernel(const LinearParams p, const LinearPlan w, const __grid_constant__ 
       }
       if (!kRows && lane == 0) w.logs[(size_t)(e.set + e.seg + 1) * p.H + h] = unit.natural();
     });
-  } else if (warp >= 4 && warp < 8) {
-    // ---- weights of the scores: thread = row; 32 columns at a time, none above the diagonal
+  } else if (warp >= 4 && warp < 12) {
+    // ---- rows: two threads each. Weights of the scores, 32 columns at a time and none above the diagonal; then the outputs, half of the
+    // columns each
     if (kRows) {
-      const int own = warp & 3;
+      const int own = warp & 3, side = (warp - 4) >> 2, row = own * 32 + lane;
       const uint32_t lanes = (uint32_t)own * 32 << 16;
+      // A row's blocks of 32 columns, by thread (those on the diagonal take half as long again): up to two to be weighted, and zeros above
+      // the diagonal (a bit each).
+      const int block[2] = {side == 0 ? (own == 3 ? 0 : own) : own == 3 ? 1 : own == 0 ? -1 : 0, side == 0 ? (own == 3 ? 3 : -1) : own == 3 ? 2 : own == 2 ? 1 : -1};
+      const uint32_t zeros = side == 0 ? (own == 1 || own == 2 ? 8u : 0u) : own == 1 ? 4u : own == 0 ? 14u : 0u;
+      auto outputs = [&](int g, int first, int h, int valid, float f) {
+        const int slot = g & 1;
+        wait(v_done + 8 * slot, g >> 1 & 1);
+        wait(o_full + 8 * slot, g >> 1 & 1);
+        tc_fence_after();
+        const bool bad = bad_values[g & 3] != 0, store = row < valid && !*dead;
+        __nv_bfloat16* dst = p.out + (int64_t)(first + min(row, valid - 1)) * p.ldo + (int64_t)h * D;
+#pragma unroll 1
+        for (int i = side * (D / 2); i < (side + 1) * (D / 2); i += 16) {
+          float o[16];
+          tc_ld16(o, tmem + lanes + S::kOut + i);
+          tc_wait_ld();
+          uint32_t x[8];
+#pragma unroll
+          for (int j = 0; j < 16; j += 2) x[j / 2] = pack(Pair(o[j], o[j + 1]) * Pair(f, f));
+          if (bad) {
+            // rare: values that are not finite, which were left out; they make what comes after them in their column so
+#pragma unroll
+            for (int j = 0; j < 16; ++j) {
+              const __nv_bfloat16* v = p.v + (int64_t)first * p.ldv + (int64_t)h * D + i + j;
+              for (int before = 0; before <= min(row, valid - 1); ++before)
+                if (!isfinite(__bfloat162float(v[(int64_t)before * p.ldv]))) x[j / 2] |= j & 1 ? 0x7fff0000u : 0x7fffu;
+            }
+          }
+          if (store) {
+            if (p.wide) {                                       // rows on 32-byte boundaries
+              asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};"
+                           :: "l"(dst + i), "r"(x[0]), "r"(x[1]), "r"(x[2]), "r"(x[3]), "r"(x[4]), "r"(x[5]), "r"(x[6]), "r"(x[7]) : "memory");
+            } else {
+              *reinterpret_cast<uint4*>(dst + i) = make_uint4(x[0], x[1], x[2], x[3]);
+              *reinterpret_cast<uint4*>(dst + i + 8) = make_uint4(x[4], x[5], x[6], x[7]);
+            }
+          }
+        }
+        tc_fence_before();
+        arrive(o_free);
+      };
       each_unit([&](int u, int chunks, int g0, int k) {
+        const int h = u % p.H, row0 = entry_of(u).row0;
         for (int c = 0; c < chunks; ++c) {
           const int g = g0 + c;
           wait(sums_full + 8 * (g & 1), g >> 1 & 1);
           const Sums& sums = sums_at[g & 1];
-          const int row = own * 32 + lane;
           if (!sums.strong) arrive(q_ok);
           wait(s_full, g & 1);
           tc_fence_after();
           if (sums.strong) {
             const float down = rintf(sums.base[own] + sums.d[row] + sums.lift[row]);
-            if (down < 0.f) {
+            if (down < 0.f && side == 0) {
               const float f = exp2f(down);
               for (int i = 0; i < D / 8; ++i) {
                 const uint32_t at = base + S::kQ + (i >> 3) * (kChunk * 128) + row * 128 + (((i & 7) ^ (row & 7)) << 4);
@@ -548,112 +590,65 @@ prompt_kernel(const LinearParams p, const LinearPlan w, const __grid_constant__ 
             fence_async_proxy();
             arrive(q_ok);
           }
-          const float d = sums.d[row] + sums.lift[row];
-#pragma unroll 1
-          for (int b = 0; b < 4; ++b) {
-            uint32_t packed[16];
-            if (b <= own) {
-              float v[32];
-              tc_ld32(v, tmem + lanes + 32 * b);
-              tc_wait_ld();
-              if (b < own) {
-                const float f = exp2_fast(d + sums.gap[4 * own + b]);
+          const float d = sums.d[row] + sums.lift[row], f_out = p.scale * sums.from[row];
+          const int valid = sums.valid;
+          uint32_t packed[2][16];
 #pragma unroll
-                for (int i = 0; i < 32; i += 4) {
-                  const float4 a = *reinterpret_cast<const float4*>(&sums.after[32 * b + i]);
-                  packed[i / 2] = pack(Pair(v[i], v[i + 1]) * (Pair(a.x, a.y) * Pair(f, f)));
-                  packed[i / 2 + 1] = pack(Pair(v[i + 2], v[i + 3]) * (Pair(a.z, a.w) * Pair(f, f)));
-                }
-              } else {
+          for (int n = 0; n < 2; ++n) {
+            const int b = block[n];
+            if (b < 0) continue;
+            float v[32];
+            tc_ld32(v, tmem + lanes + 32 * b);
+            tc_wait_ld();
+            if (b < own) {
+              const float f = exp2_fast(d + sums.gap[4 * own + b]);
 #pragma unroll
-                for (int i = 0; i < 32; i += 4) {
-                  const float4 a = *reinterpret_cast<const float4*>(&sums.d[32 * b + i]);
-                  packed[i / 2] = pack(i <= lane ? v[i] * exp2_fast(d - a.x) : 0.f, i + 1 <= lane ? v[i + 1] * exp2_fast(d - a.y) : 0.f);
-                  packed[i / 2 + 1] = pack(i + 2 <= lane ? v[i + 2] * exp2_fast(d - a.z) : 0.f, i + 3 <= lane ? v[i + 3] * exp2_fast(d - a.w) : 0.f);
-                }
+              for (int i = 0; i < 32; i += 4) {
+                const float4 a = *reinterpret_cast<const float4*>(&sums.after[32 * b + i]);
+                packed[n][i / 2] = pack(Pair(v[i], v[i + 1]) * (Pair(a.x, a.y) * Pair(f, f)));
+                packed[n][i / 2 + 1] = pack(Pair(v[i + 2], v[i + 3]) * (Pair(a.z, a.w) * Pair(f, f)));
               }
             } else {
 #pragma unroll
-              for (int i = 0; i < 16; ++i) packed[i] = 0;
+              for (int i = 0; i < 32; i += 4) {
+                const float4 a = *reinterpret_cast<const float4*>(&sums.d[32 * b + i]);
+                packed[n][i / 2] = pack(i <= lane ? v[i] * exp2_fast(d - a.x) : 0.f, i + 1 <= lane ? v[i + 1] * exp2_fast(d - a.y) : 0.f);
+                packed[n][i / 2 + 1] = pack(i + 2 <= lane ? v[i + 2] * exp2_fast(d - a.z) : 0.f, i + 3 <= lane ? v[i + 3] * exp2_fast(d - a.w) : 0.f);
+              }
             }
-            tc_st16(tmem + lanes + S::kProb + 16 * b, packed);
           }
+          // (heads of 128: in the place of the first scores, which both threads of the row have read by then)
+          if (D == 128) asm volatile("bar.sync %0, 64;" :: "r"(1 + own) : "memory");
+#pragma unroll
+          for (int n = 0; n < 2; ++n)
+            if (block[n] >= 0) tc_st16(tmem + lanes + S::kProb + 16 * block[n], packed[n]);
+          const uint32_t none[16] = {0u, 0u, 0u, 0u, 0u, 0u, 0u, 0u, 0u, 0u, 0u, 0u, 0u, 0u, 0u, 0u};
+#pragma unroll
+          for (int b = 1; b < 4; ++b)
+            if (zeros >> b & 1) tc_st16(tmem + lanes + S::kProb + 16 * b, none);
           tc_wait_st();
           tc_fence_before();
           arrive(p_full);
           arrive(sums_free + 8 * (g & 1));
-        }
-      });
-    }
-  } else if (warp >= 8 && warp < 12) {
-    // ---- outputs: thread = row
-    if (kRows) {
-      const int own = warp & 3, row = own * 32 + lane;
-      const uint32_t lanes = (uint32_t)own * 32 << 16;
-      each_unit([&](int u, int chunks, int g0, int k) {
-        const int h = u % p.H, row0 = entry_of(u).row0;
-        for (int c = 0; c < chunks; ++c) {
-          const int g = g0 + c, slot = g & 1, first = row0 + c * kChunk;
-          wait(sums_full + 8 * slot, g >> 1 & 1);
-          const float f = p.scale * sums_at[slot].from[row];
-          const int valid = sums_at[slot].valid;
-          wait(v_done + 8 * slot, g >> 1 & 1);
-          wait(o_full + 8 * slot, g >> 1 & 1);
-          tc_fence_after();
-          const bool bad = sums_at[slot].bad, store = row < valid && !*dead;
-          __nv_bfloat16* dst = p.out + (int64_t)(first + min(row, valid - 1)) * p.ldo + (int64_t)h * D;
-#pragma unroll 1
-          for (int i = 0; i < D; i += 16) {
-            float o[16];
-            tc_ld16(o, tmem + lanes + S::kOut + slot * D + i);
-            tc_wait_ld();
-            uint32_t x[8];
-#pragma unroll
-            for (int j = 0; j < 16; j += 2) x[j / 2] = pack(Pair(o[j], o[j + 1]) * Pair(f, f));
-            if (bad) {
-              // rare: values that are not finite, which were left out; they make what comes after them in their column so
-#pragma unroll
-              for (int j = 0; j < 16; ++j) {
-                const __nv_bfloat16* v = p.v + (int64_t)first * p.ldv + (int64_t)h * D + i + j;
-                for (int before = 0; before <= min(row, valid - 1); ++before)
-                  if (!isfinite(__bfloat162float(v[(int64_t)before * p.ldv]))) x[j / 2] |= j & 1 ? 0x7fff0000u : 0x7fffu;
-              }
-            }
-            if (store) {
-              if (p.wide) {                                     // rows on 32-byte boundaries
-                asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};"
-                             :: "l"(dst + i), "r"(x[0]), "r"(x[1]), "r"(x[2]), "r"(x[3]), "r"(x[4]), "r"(x[5]), "r"(x[6]), "r"(x[7]) : "memory");
-              } else {
-                *reinterpret_cast<uint4*>(dst + i) = make_uint4(x[0], x[1], x[2], x[3]);
-                *reinterpret_cast<uint4*>(dst + i + 8) = make_uint4(x[4], x[5], x[6], x[7]);
-              }
-            }
-          }
-          tc_fence_before();
-          arrive(o_free + 8 * slot);
-          arrive(sums_free + 8 * slot);
+          outputs(g, row0 + c * kChunk, h, valid, f_out);
         }
       });
     }
   } else if (warp >= 12) {
-    // ---- the state: thread = row of it, a quarter of the columns; values: a 16-byte piece of every 64th row
+    // ---- the state: thread = column of it (lane of tensor memory), a quarter of the rows; values: 16 columns x 16 rows at a time
     const int quad = warp & 3, a = quad * 32 + lane, col0 = ((warp - 12) >> 2) * S::kCols;
     const bool holds = quad * 32 < D;
     const uint32_t lanes = (uint32_t)quad * 32 << 16;
-    const int group = (warp - 12) >> 2, id = threadIdx.x & 127, piece = id & 7, row0 = id >> 3;
-    const uint32_t swizzled = row0 * 128 + ((piece ^ (row0 & 7)) << 4);
+    const int group = (warp - 12) >> 2, id = threadIdx.x & 127;
     float s[S::kCols];
-    auto at_state = [&](float* pool, int64_t first) { return pool + first + ((int64_t)a * D + col0); };
+    auto at_state = [&](float* pool, int64_t first) { return pool + first + ((int64_t)col0 * D + a); };
     auto load_state = [&](const float* src) {
 #pragma unroll
-      for (int i = 0; i < S::kCols; i += 4) {
-        const float4 x = *reinterpret_cast<const float4*>(src + i);
-        s[i] = x.x, s[i + 1] = x.y, s[i + 2] = x.z, s[i + 3] = x.w;
-      }
+      for (int i = 0; i < S::kCols; ++i) s[i] = src[i * D];
     };
     auto store_state = [&](float* dst) {
 #pragma unroll
-      for (int i = 0; i < S::kCols; i += 4) *reinterpret_cast<float4*>(dst + i) = make_float4(s[i], s[i + 1], s[i + 2], s[i + 3]);
+      for (int i = 0; i < S::kCols; ++i) dst[i * D] = s[i];
     };
     auto set_at = [&](int set, int h) { return at_state(w.states, ((int64_t)set * p.H + h) * D * D); };
     auto publish = [&](int g) {                                 // the state as the outputs of chunk g read it
@@ -668,71 +663,79 @@ prompt_kernel(const LinearParams p, const LinearPlan w, const __grid_constant__ 
       fence_async_proxy();
       arrive(state_full);
     };
-    // The decayed values of a step of rows as three bf16 numbers, by 4 of the warps; two steps ahead of the state. Each thread: two
-    // pieces, of one row (heads of 128) or of rows 16 apart.
+    // The decayed values of a step of rows as three bf16 numbers, by 4 of the warps, into tensor memory: a lane is a column of the values,
+    // which the transposing loads from shared memory give. A thread has two neighbouring rows of 8 and two of the other 8.
     auto convert = [&](int g, int step) {
-      const int slot = g & 1, use = g * S::kSteps + step, at = group & 1;
+      const int slot = g & 1, use = g * S::kSteps + step;
       if (step == group) {
         wait(sums_full + 8 * slot, g >> 1 & 1);
         wait(v_full + 8 * slot, g >> 1 & 1);
       }
       const Sums& sums = sums_at[slot];
-      constexpr uint32_t kNext = D == 128 ? kChunk * 128 : 16 * 128, kNextPart = D == 128 ? S::kStep * 128 : 16 * 128;
-      const uint32_t off = step * (S::kStep * 128) + swizzled, v_at = base + S::kV + slot * S::kTile + off;
-      const uint32_t to = base + S::kW + 3 * at * S::kPart + swizzled;
-      const int row = step * S::kStep + row0, valid = sums.valid;
-      uint4 v[2] = {lds16(v_at), lds16(v_at + kNext)};
+      const int row = step * S::kStep, valid = sums.valid;
+      const uint32_t v_at = base + S::kV + slot * S::kTile, k_at = base + S::kK + slot * S::kTile;
+      // of a row and a column's piece of 8
+      auto place = [&](int r, int piece) { return (uint32_t)((piece >> 3) * (kChunk * 128) + r * 128 + (((piece & 7) ^ (r & 7)) << 4)); };
+      uint32_t word[2][4];                                      // [16 columns][rows 0-7: columns 0-7, 8-15; rows 8-15: the same]
+      if (holds)
 #pragma unroll
-      for (int n = 0; n < 2; ++n)
-        if (row + (D == 128 ? 0 : 16 * n) >= valid) {
-          // rows behind the last are another request's, or nobody's
-          v[n] = make_uint4(0u, 0u, 0u, 0u);
-          wait(k_full + 8 * slot, g >> 1 & 1);
-          sts16(v_at + n * kNext, v[n]);
-          sts16(base + S::kK + slot * S::kTile + off + n * kNext, v[n]);
-        }
-      const float rest[2] = {sums.rest[row], sums.rest[row + (D == 128 ? 0 : 16)]};
-      Pair x[8] = {unpack(v[0].x), unpack(v[0].y), unpack(v[0].z), unpack(v[0].w), unpack(v[1].x), unpack(v[1].y), unpack(v[1].z), unpack(v[1].w)};
-      Pair none(0.f, 0.f);
+        for (int n = 0; n < 2; ++n)
+          ldmatrix_trans(word[n], v_at + place(row + (lane & 7) + (lane >> 4) * 8, quad * 4 + 2 * n + (lane >> 3 & 1)));
+      const float2 r0 = *reinterpret_cast<const float2*>(&sums.rest[row + 2 * (lane & 3)]), r1 = *reinterpret_cast<const float2*>(&sums.rest[row + 8 + 2 * (lane & 3)]);
+      if (row + S::kStep > valid) {
+        // rows behind the last are another request's, or nobody's
+        wait(k_full + 8 * slot, g >> 1 & 1);
+        for (int i = id; i < S::kStep * (D / 8); i += 128)
+          if (row + i / (D / 8) >= valid) {
+            const uint32_t at = place(row + i / (D / 8), i % (D / 8));
+            sts16(v_at + at, make_uint4(0u, 0u, 0u, 0u));
+            sts16(k_at + at, make_uint4(0u, 0u, 0u, 0u));
+          }
+        fence_async_proxy();
+        const int t = row + 2 * (lane & 3);
+        const uint32_t keep0 = t + 1 < valid ? ~0u : t < valid ? 0xffffu : 0u, keep1 = t + 9 < valid ? ~0u : t + 8 < valid ? 0xffffu : 0u;
+#pragma unroll
+        for (int n = 0; n < 2; ++n) word[n][0] &= keep0, word[n][1] &= keep0, word[n][2] &= keep1, word[n][3] &= keep1;
+      }
+      Pair x[8], none(0.f, 0.f);
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
-        x[i] = x[i] * Pair(rest[i >> 2], rest[i >> 2]);
+        x[i] = unpack(word[i >> 2][i & 3]) * (i & 2 ? Pair(r1.x, r1.y) : Pair(r0.x, r0.y));
         none = fma(x[i], Pair(0.f, 0.f), none);
       }
-      const bool odd = !(none.floats().x == 0.f && none.floats().y == 0.f);
-      if (odd) {
+      if (kRows && holds && !(none.floats().x == 0.f && none.floats().y == 0.f)) {
         // values that are not finite leave the product with the scores, where they would reach earlier rows too
-        const uint32_t m = 0x7f807f80u;
 #pragma unroll 1
-        for (int n = 0; n < 2; ++n) {
-          uint4 y = lds16(v_at + n * kNext);
-          y = make_uint4(y.x & ~__vcmpeq2(y.x & m, m), y.y & ~__vcmpeq2(y.y & m, m), y.z & ~__vcmpeq2(y.z & m, m), y.w & ~__vcmpeq2(y.w & m, m));
-          if (kRows) {
-            sts16(v_at + n * kNext, y);
-            sums_at[slot].bad = 1;
+        for (int i = 0; i < 16; ++i) {
+          const int r = row + 2 * (lane & 3) + (i & 1) + (i >> 2 & 1) * 8, c = quad * 32 + (i >> 3) * 16 + (i >> 1 & 1) * 8 + (lane >> 2);
+          uint16_t* at = reinterpret_cast<uint16_t*>(smem + S::kV + slot * S::kTile + place(r, c >> 3)) + (c & 7);
+          if ((*at & 0x7f80) == 0x7f80) *at = 0;
+        }
+        bad_values[g & 3] = 1;
+        fence_async_proxy();
+      }
+      if (use >= 4) wait(w_free + 8 * group, (use >> 2 & 1) ^ 1);
+      tc_fence_after();
+      // 8 leading bits at a time: the three parts are the whole number (infinities are themselves, and NaN)
+      if (holds)
+#pragma unroll
+        for (int part = 2; part >= 0; --part) {
+          uint32_t to[8];
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const float2 f = x[i].floats();
+            to[i] = __byte_perm(__float_as_uint(f.x), __float_as_uint(f.y), 0x7632);
+            if (part > 0) x[i] = fma(Pair(__uint_as_float(__float_as_uint(f.x) & 0xffff0000u), __uint_as_float(__float_as_uint(f.y) & 0xffff0000u)), Pair(-1.f, -1.f), x[i]);
           }
-        }
-      }
-      // The place of the step before the last. Each group's steps have a barrier of their own: one for a place could be two phases away
-      // from the one that is waited for, where parities say nothing.
-      if (use >= 2) wait(w_free + 8 * (group ^ 2), (use - 2) >> 2 & 1);
-      // 8 leading bits at a time: the three parts are the whole number (infinities are themselves three times, or nothing)
 #pragma unroll
-      for (int part = 2; part >= 0; --part) {
-        uint32_t word[8];
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const float2 f = x[i].floats();
-          word[i] = __byte_perm(__float_as_uint(f.x), __float_as_uint(f.y), 0x7632);
-          if (part > 0) x[i] = fma(Pair(__uint_as_float(__float_as_uint(f.x) & 0xffff0000u), __uint_as_float(__float_as_uint(f.y) & 0xffff0000u)), Pair(-1.f, -1.f), x[i]);
+          for (int n = 0; n < 2; ++n)
+            tc_st_16x128(tmem + lanes + ((uint32_t)n * 16 << 16) + S::kParts + 8 * (3 * group + part), to[4 * n], to[4 * n + 1], to[4 * n + 2], to[4 * n + 3]);
         }
-        sts16(to + part * S::kPart, make_uint4(word[0], word[1], word[2], word[3]));
-        sts16(to + part * S::kPart + kNextPart, make_uint4(word[4], word[5], word[6], word[7]));
-      }
-      fence_async_proxy();
-      arrive(w_full + 8 * at);
+      tc_wait_st();
+      tc_fence_before();
+      arrive(w_full + 8 * group);
     };
-    if (group < 2) convert(0, group);
+    convert(0, group);
     each_unit([&](int u, int chunks, int g0, int k) {
 #pragma unroll
       for (int i = 0; i < S::kCols; ++i) s[i] = 0.f;
@@ -751,7 +754,7 @@ prompt_kernel(const LinearParams p, const LinearPlan w, const __grid_constant__ 
       if (kRows) publish(g0);
       for (int c = 0; c < chunks; ++c) {
         const int g = g0 + c;
-        for (int step = group < 2 ? 4 + group : group; step < S::kSteps; step += 4) convert(g, step);
+        convert(g, group + 4);
         const Sums& sums = sums_at[g & 1];
         const float f = sums.factor;
         const float keep = sums.near ? 1.f : 0.f;
@@ -759,7 +762,7 @@ prompt_kernel(const LinearParams p, const LinearPlan w, const __grid_constant__ 
         arrive(sums_free + 8 * (g & 1));
         arrive(v_done + 8 * (g & 1));
         arrive(v_free + 8 * (g & 1));
-        if (more && group < 2) convert(g + 1, group);
+        if (more) convert(g + 1, group);
         wait(add_full, g & 1);
         tc_fence_after();
         if (holds)
