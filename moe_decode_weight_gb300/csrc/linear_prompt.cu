@@ -22,8 +22,10 @@
 //   warp 1       issues the products for the state
 //   warp 2       sums the decays of the next chunk
 //   warp 3       issues the products for the outputs
-//   warps 4-11   weight the scores and take the outputs, two threads a row
-//   warps 12-27  the decayed values and the state, four threads a row of the state
+//   warps 4-7    weight the scores, one thread a row
+//   warps 8-11   the outputs, one thread a row
+//   warps 12-19  the decayed values
+//   warps 20-27  the state, two threads a column of it
 #include <cuda.h>
 
 #include <algorithm>
@@ -34,7 +36,7 @@
 namespace mdw {
 namespace {
 
-constexpr int kChunk = kLinearChunk, kRowWarps = 8, kStateWarps = 16, kThreads = 32 * (12 + kStateWarps);
+constexpr int kChunk = kLinearChunk, kConvertWarps = 8, kStateWarps = 8, kThreads = 32 * (12 + kConvertWarps + kStateWarps);
 constexpr float kLn2 = 0.6931471805599453f;
 
 __device__ __forceinline__ void tma_load(uint32_t dst, const CUtensorMap* map, uint32_t bar, int x, int head, int row) {
@@ -98,6 +100,11 @@ struct Sum {
   __device__ __forceinline__ float less(Sum b) const { return __fadd_rn(__fsub_rn(hi, b.hi), __fsub_rn(lo, b.lo)); }
   __device__ __forceinline__ float natural() const { return fmaf(hi, kLn2, lo * kLn2) + hi * -1.9046542e-9f; }
 };
+
+// Registers of a thread. A block starts with 72 for each of its seven groups of four warps, 504 together; the two groups that hold the
+// state take more from what the others give up: 56 + 88 + 56 + 2 * 56 + 2 * 96 = 504.
+template <int kCount> __device__ __forceinline__ void fewer_registers() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" :: "n"(kCount)); }
+template <int kCount> __device__ __forceinline__ void more_registers() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" :: "n"(kCount)); }
 
 // The kernels of a call start while the one before them ends, and wait here for its results.
 __device__ __forceinline__ void after_previous() {
@@ -216,7 +223,7 @@ struct Shape {
   // Tensor memory columns: scores (the weighted ones take their first half when D = 128), outputs, what a chunk adds to the state (a lane is a
   // column of the state), and four steps of decayed values, each in three parts.
   static constexpr int kOut = 256 - D, kAdd = 256, kParts = 384, kProb = D == 128 ? 0 : 128;
-  static constexpr int kCols = D / 4;                           // of the state, a thread
+  static constexpr int kCols = D / 2;                           // rows of the state, a thread
 };
 
 // What the warps of a block take from the sums of a chunk's decays (in log2), and how the chunk lies.
@@ -273,18 +280,18 @@ prompt_kernel(const LinearParams p, const LinearPlan w, const __grid_constant__ 
       mbar_init(k_full + 8 * i, 1);
       mbar_init(k_free + 8 * i, kRows ? 2 : 1);
       mbar_init(v_full + 8 * i, 1);
-      mbar_init(v_free + 8 * i, kStateWarps + (kRows ? 1 : 0));
-      mbar_init(v_done + 8 * i, kStateWarps);
+      mbar_init(v_free + 8 * i, kConvertWarps + (kRows ? 1 : 0));
+      mbar_init(v_done + 8 * i, kConvertWarps);
       for (int j = i; j < 4; j += 2) {
-        mbar_init(w_full + 8 * j, kStateWarps / 4);
+        mbar_init(w_full + 8 * j, 4);
         mbar_init(w_free + 8 * j, 1);
       }
       mbar_init(sums_full + 8 * i, 1);
-      mbar_init(sums_free + 8 * i, kStateWarps + (kRows ? kRowWarps : 0));
+      mbar_init(sums_free + 8 * i, kConvertWarps + kStateWarps + (kRows ? 8 : 0));
     }
     for (const uint32_t b : {q_full, q_free, s_full, o_full, o_full + 8, state_read, add_full}) mbar_init(b, 1);
     mbar_init(end, kRows ? 2 : 1);
-    for (const uint32_t b : {p_full, q_ok, o_free}) mbar_init(b, kRowWarps);
+    for (const uint32_t b : {p_full, q_ok, o_free}) mbar_init(b, 4);
     mbar_init(state_full, kStateWarps);
     mbar_init(add_read, kStateWarps);
     *dead = 0;
@@ -331,6 +338,7 @@ prompt_kernel(const LinearParams p, const LinearPlan w, const __grid_constant__ 
 
   if (warp == 0) {
     // ---- copies
+    fewer_registers<56>();
     int asked[3] = {0, 0, 0};                                   // tiles of k, v and q
     each_unit([&](int u, int chunks, int g0, int k) {
       const int h = u % p.H, row0 = entry_of(u).row0;
@@ -362,6 +370,7 @@ prompt_kernel(const LinearParams p, const LinearPlan w, const __grid_constant__ 
     if (asked[2] > 0) mbar_drain_inline(q_full, (asked[2] - 1) & 1);
   } else if (warp == 1) {
     // ---- products for the state
+    fewer_registers<56>();
     each_unit([&](int u, int chunks, int g0, int k) {
       for (int c = 0; c < chunks; ++c) {
         const int g = g0 + c, slot = g & 1;
@@ -394,6 +403,7 @@ prompt_kernel(const LinearParams p, const LinearPlan w, const __grid_constant__ 
     mbar_drain_inline(end, 0);                                  // nothing is in flight when the columns are given back
   } else if (warp == 3) {
     // ---- products for the outputs
+    fewer_registers<56>();
     if (kRows) {
       each_unit([&](int u, int chunks, int g0, int k) {
         for (int c = 0; c < chunks; ++c) {
@@ -447,6 +457,7 @@ prompt_kernel(const LinearParams p, const LinearPlan w, const __grid_constant__ 
     }
   } else if (warp == 2) {
     // ---- sums of the decays: a lane has four rows
+    fewer_registers<56>();
     each_unit([&](int u, int chunks, int g0, int k) {
       const int h = u % p.H;
       const LinearEntry e = entry_of(u);
@@ -521,55 +532,13 @@ prompt_kernel(const LinearParams p, const LinearPlan w, const __grid_constant__ 
       }
       if (!kRows && lane == 0) w.logs[(size_t)(e.set + e.seg + 1) * p.H + h] = unit.natural();
     });
-  } else if (warp >= 4 && warp < 12) {
-    // ---- rows: two threads each. Weights of the scores, 32 columns at a time and none above the diagonal; then the outputs, half of the
-    // columns each
+  } else if (warp >= 4 && warp < 8) {
+    // ---- weights of the scores: thread = row; 32 columns at a time, none above the diagonal
+    more_registers<88>();
     if (kRows) {
-      const int own = warp & 3, side = (warp - 4) >> 2, row = own * 32 + lane;
+      const int own = warp & 3, row = own * 32 + lane;
       const uint32_t lanes = (uint32_t)own * 32 << 16;
-      // A row's blocks of 32 columns, by thread (those on the diagonal take half as long again): up to two to be weighted, and zeros above
-      // the diagonal (a bit each).
-      const int block[2] = {side == 0 ? (own == 3 ? 0 : own) : own == 3 ? 1 : own == 0 ? -1 : 0, side == 0 ? (own == 3 ? 3 : -1) : own == 3 ? 2 : own == 2 ? 1 : -1};
-      const uint32_t zeros = side == 0 ? (own == 1 || own == 2 ? 8u : 0u) : own == 1 ? 4u : own == 0 ? 14u : 0u;
-      auto outputs = [&](int g, int first, int h, int valid, float f) {
-        const int slot = g & 1;
-        wait(v_done + 8 * slot, g >> 1 & 1);
-        wait(o_full + 8 * slot, g >> 1 & 1);
-        tc_fence_after();
-        const bool bad = bad_values[g & 3] != 0, store = row < valid && !*dead;
-        __nv_bfloat16* dst = p.out + (int64_t)(first + min(row, valid - 1)) * p.ldo + (int64_t)h * D;
-#pragma unroll 1
-        for (int i = side * (D / 2); i < (side + 1) * (D / 2); i += 16) {
-          float o[16];
-          tc_ld16(o, tmem + lanes + S::kOut + i);
-          tc_wait_ld();
-          uint32_t x[8];
-#pragma unroll
-          for (int j = 0; j < 16; j += 2) x[j / 2] = pack(Pair(o[j], o[j + 1]) * Pair(f, f));
-          if (bad) {
-            // rare: values that are not finite, which were left out; they make what comes after them in their column so
-#pragma unroll
-            for (int j = 0; j < 16; ++j) {
-              const __nv_bfloat16* v = p.v + (int64_t)first * p.ldv + (int64_t)h * D + i + j;
-              for (int before = 0; before <= min(row, valid - 1); ++before)
-                if (!isfinite(__bfloat162float(v[(int64_t)before * p.ldv]))) x[j / 2] |= j & 1 ? 0x7fff0000u : 0x7fffu;
-            }
-          }
-          if (store) {
-            if (p.wide) {                                       // rows on 32-byte boundaries
-              asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};"
-                           :: "l"(dst + i), "r"(x[0]), "r"(x[1]), "r"(x[2]), "r"(x[3]), "r"(x[4]), "r"(x[5]), "r"(x[6]), "r"(x[7]) : "memory");
-            } else {
-              *reinterpret_cast<uint4*>(dst + i) = make_uint4(x[0], x[1], x[2], x[3]);
-              *reinterpret_cast<uint4*>(dst + i + 8) = make_uint4(x[4], x[5], x[6], x[7]);
-            }
-          }
-        }
-        tc_fence_before();
-        arrive(o_free);
-      };
       each_unit([&](int u, int chunks, int g0, int k) {
-        const int h = u % p.H, row0 = entry_of(u).row0;
         for (int c = 0; c < chunks; ++c) {
           const int g = g0 + c;
           wait(sums_full + 8 * (g & 1), g >> 1 & 1);
@@ -577,10 +546,13 @@ prompt_kernel(const LinearParams p, const LinearPlan w, const __grid_constant__ 
           if (!sums.strong) arrive(q_ok);
           wait(s_full, g & 1);
           tc_fence_after();
+          float v[32];
+          tc_ld32(v, tmem + lanes);
           if (sums.strong) {
             const float down = rintf(sums.base[own] + sums.d[row] + sums.lift[row]);
-            if (down < 0.f && side == 0) {
+            if (down < 0.f) {
               const float f = exp2f(down);
+#pragma unroll 1
               for (int i = 0; i < D / 8; ++i) {
                 const uint32_t at = base + S::kQ + (i >> 3) * (kChunk * 128) + row * 128 + (((i & 7) ^ (row & 7)) << 4);
                 const uint4 x = lds16(at);
@@ -590,83 +562,105 @@ prompt_kernel(const LinearParams p, const LinearPlan w, const __grid_constant__ 
             fence_async_proxy();
             arrive(q_ok);
           }
-          const float d = sums.d[row] + sums.lift[row], f_out = p.scale * sums.from[row];
-          const int valid = sums.valid;
-          uint32_t packed[2][16];
-#pragma unroll
-          for (int n = 0; n < 2; ++n) {
-            const int b = block[n];
-            if (b < 0) continue;
-            float v[32];
-            tc_ld32(v, tmem + lanes + 32 * b);
-            tc_wait_ld();
+          const float d = sums.d[row] + sums.lift[row];
+          tc_wait_ld();
+#pragma unroll 1
+          for (int b = 0; b < 4; ++b) {
+            uint32_t packed[16];
             if (b < own) {
               const float f = exp2_fast(d + sums.gap[4 * own + b]);
 #pragma unroll
               for (int i = 0; i < 32; i += 4) {
                 const float4 a = *reinterpret_cast<const float4*>(&sums.after[32 * b + i]);
-                packed[n][i / 2] = pack(Pair(v[i], v[i + 1]) * (Pair(a.x, a.y) * Pair(f, f)));
-                packed[n][i / 2 + 1] = pack(Pair(v[i + 2], v[i + 3]) * (Pair(a.z, a.w) * Pair(f, f)));
+                packed[i / 2] = pack(Pair(v[i], v[i + 1]) * (Pair(a.x, a.y) * Pair(f, f)));
+                packed[i / 2 + 1] = pack(Pair(v[i + 2], v[i + 3]) * (Pair(a.z, a.w) * Pair(f, f)));
               }
-            } else {
+              tc_ld32(v, tmem + lanes + 32 * (b + 1));          // (the next ones while these are stored)
+            } else if (b == own) {
 #pragma unroll
               for (int i = 0; i < 32; i += 4) {
                 const float4 a = *reinterpret_cast<const float4*>(&sums.d[32 * b + i]);
-                packed[n][i / 2] = pack(i <= lane ? v[i] * exp2_fast(d - a.x) : 0.f, i + 1 <= lane ? v[i + 1] * exp2_fast(d - a.y) : 0.f);
-                packed[n][i / 2 + 1] = pack(i + 2 <= lane ? v[i + 2] * exp2_fast(d - a.z) : 0.f, i + 3 <= lane ? v[i + 3] * exp2_fast(d - a.w) : 0.f);
+                packed[i / 2] = pack(i <= lane ? v[i] * exp2_fast(d - a.x) : 0.f, i + 1 <= lane ? v[i + 1] * exp2_fast(d - a.y) : 0.f);
+                packed[i / 2 + 1] = pack(i + 2 <= lane ? v[i + 2] * exp2_fast(d - a.z) : 0.f, i + 3 <= lane ? v[i + 3] * exp2_fast(d - a.w) : 0.f);
               }
+            } else {
+#pragma unroll
+              for (int i = 0; i < 16; ++i) packed[i] = 0;
             }
+            tc_wait_ld();                                       // (before these go to where they came from)
+            tc_st16(tmem + lanes + S::kProb + 16 * b, packed);
           }
-          // (heads of 128: in the place of the first scores, which both threads of the row have read by then)
-          if (D == 128) asm volatile("bar.sync %0, 64;" :: "r"(1 + own) : "memory");
-#pragma unroll
-          for (int n = 0; n < 2; ++n)
-            if (block[n] >= 0) tc_st16(tmem + lanes + S::kProb + 16 * block[n], packed[n]);
-          const uint32_t none[16] = {0u, 0u, 0u, 0u, 0u, 0u, 0u, 0u, 0u, 0u, 0u, 0u, 0u, 0u, 0u, 0u};
-#pragma unroll
-          for (int b = 1; b < 4; ++b)
-            if (zeros >> b & 1) tc_st16(tmem + lanes + S::kProb + 16 * b, none);
           tc_wait_st();
           tc_fence_before();
           arrive(p_full);
           arrive(sums_free + 8 * (g & 1));
-          outputs(g, row0 + c * kChunk, h, valid, f_out);
         }
       });
     }
-  } else if (warp >= 12) {
-    // ---- the state: thread = column of it (lane of tensor memory), a quarter of the rows; values: 16 columns x 16 rows at a time
-    const int quad = warp & 3, a = quad * 32 + lane, col0 = ((warp - 12) >> 2) * S::kCols;
+  } else if (warp >= 8 && warp < 12) {
+    // ---- outputs: thread = row
+    fewer_registers<56>();
+    if (kRows) {
+      const int own = warp & 3, row = own * 32 + lane;
+      const uint32_t lanes = (uint32_t)own * 32 << 16;
+      each_unit([&](int u, int chunks, int g0, int k) {
+        const int h = u % p.H, row0 = entry_of(u).row0;
+        for (int c = 0; c < chunks; ++c) {
+          const int g = g0 + c, slot = g & 1, first = row0 + c * kChunk;
+          wait(sums_full + 8 * slot, g >> 1 & 1);
+          const float f = p.scale * sums_at[slot].from[row];
+          const int valid = sums_at[slot].valid;
+          arrive(sums_free + 8 * slot);
+          wait(v_done + 8 * slot, g >> 1 & 1);
+          wait(o_full + 8 * slot, g >> 1 & 1);
+          tc_fence_after();
+          const bool bad = bad_values[g & 3] != 0, store = row < valid && !*dead;
+          __nv_bfloat16* dst = p.out + (int64_t)(first + min(row, valid - 1)) * p.ldo + (int64_t)h * D;
+          float o[16];
+          tc_ld16(o, tmem + lanes + S::kOut);
+#pragma unroll 1
+          for (int i = 0; i < D; i += 16) {
+            uint32_t x[8];
+            tc_wait_ld();
+#pragma unroll
+            for (int j = 0; j < 16; j += 2) x[j / 2] = pack(Pair(o[j], o[j + 1]) * Pair(f, f));
+            if (i + 16 < D) tc_ld16(o, tmem + lanes + S::kOut + i + 16);   // (the next ones while these are stored)
+            if (bad) {
+              // rare: values that are not finite, which were left out; they make what comes after them in their column so
+#pragma unroll
+              for (int j = 0; j < 16; ++j) {
+                const __nv_bfloat16* v = p.v + (int64_t)first * p.ldv + (int64_t)h * D + i + j;
+#pragma unroll 1
+                for (int before = 0; before <= min(row, valid - 1); ++before)
+                  if (!isfinite(__bfloat162float(v[(int64_t)before * p.ldv]))) x[j / 2] |= j & 1 ? 0x7fff0000u : 0x7fffu;
+              }
+            }
+            if (store) {
+              if (p.wide) {                                     // rows on 32-byte boundaries
+                asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};"
+                             :: "l"(dst + i), "r"(x[0]), "r"(x[1]), "r"(x[2]), "r"(x[3]), "r"(x[4]), "r"(x[5]), "r"(x[6]), "r"(x[7]) : "memory");
+              } else {
+                *reinterpret_cast<uint4*>(dst + i) = make_uint4(x[0], x[1], x[2], x[3]);
+                *reinterpret_cast<uint4*>(dst + i + 8) = make_uint4(x[4], x[5], x[6], x[7]);
+              }
+            }
+          }
+          tc_fence_before();
+          arrive(o_free);
+        }
+      });
+    }
+  } else if (warp < 20) {
+    // ---- values: 16 columns x 16 rows at a time
+    fewer_registers<56>();
+    const int quad = warp & 3, group = (warp - 12) >> 2, id = threadIdx.x & 127;
     const bool holds = quad * 32 < D;
     const uint32_t lanes = (uint32_t)quad * 32 << 16;
-    const int group = (warp - 12) >> 2, id = threadIdx.x & 127;
-    float s[S::kCols];
-    auto at_state = [&](float* pool, int64_t first) { return pool + first + ((int64_t)col0 * D + a); };
-    auto load_state = [&](const float* src) {
-#pragma unroll
-      for (int i = 0; i < S::kCols; ++i) s[i] = src[i * D];
-    };
-    auto store_state = [&](float* dst) {
-#pragma unroll
-      for (int i = 0; i < S::kCols; ++i) dst[i * D] = s[i];
-    };
-    auto set_at = [&](int set, int h) { return at_state(w.states, ((int64_t)set * p.H + h) * D * D); };
-    auto publish = [&](int g) {                                 // the state as the outputs of chunk g read it
-      if (g > 0) wait(state_read, (g - 1) & 1);
-      if (holds)
-#pragma unroll
-        for (int i = 0; i < S::kCols; i += 8) {
-          const int at = (col0 + i) >> 3;
-          sts16(base + S::kS + (at >> 3) * (D * 128) + a * 128 + (((at & 7) ^ (a & 7)) << 4),
-                make_uint4(pack(s[i], s[i + 1]), pack(s[i + 2], s[i + 3]), pack(s[i + 4], s[i + 5]), pack(s[i + 6], s[i + 7])));
-        }
-      fence_async_proxy();
-      arrive(state_full);
-    };
-    // The decayed values of a step of rows as three bf16 numbers, by 4 of the warps, into tensor memory: a lane is a column of the values,
+    // The decayed values of a step of rows as three bf16 numbers, by 4 of the warps (the others have the next step), into tensor memory: a lane is a column of the values,
     // which the transposing loads from shared memory give. A thread has two neighbouring rows of 8 and two of the other 8.
     auto convert = [&](int g, int step) {
       const int slot = g & 1, use = g * S::kSteps + step;
+      const int at_slot = step & 3;
       if (step == group) {
         wait(sums_full + 8 * slot, g >> 1 & 1);
         wait(v_full + 8 * slot, g >> 1 & 1);
@@ -714,7 +708,7 @@ prompt_kernel(const LinearParams p, const LinearPlan w, const __grid_constant__ 
         bad_values[g & 3] = 1;
         fence_async_proxy();
       }
-      if (use >= 4) wait(w_free + 8 * group, (use >> 2 & 1) ^ 1);
+      if (use >= 4) wait(w_free + 8 * at_slot, (use >> 2 & 1) ^ 1);
       tc_fence_after();
       // 8 leading bits at a time: the three parts are the whole number (infinities are themselves, and NaN)
       if (holds)
@@ -729,13 +723,51 @@ prompt_kernel(const LinearParams p, const LinearPlan w, const __grid_constant__ 
           }
 #pragma unroll
           for (int n = 0; n < 2; ++n)
-            tc_st_16x128(tmem + lanes + ((uint32_t)n * 16 << 16) + S::kParts + 8 * (3 * group + part), to[4 * n], to[4 * n + 1], to[4 * n + 2], to[4 * n + 3]);
+            tc_st_16x128(tmem + lanes + ((uint32_t)n * 16 << 16) + S::kParts + 8 * (3 * at_slot + part), to[4 * n], to[4 * n + 1], to[4 * n + 2], to[4 * n + 3]);
         }
       tc_wait_st();
       tc_fence_before();
-      arrive(w_full + 8 * group);
+      arrive(w_full + 8 * at_slot);
     };
-    convert(0, group);
+    bool more = true;
+    for (int g = 0; more; ++g) {
+#pragma unroll 1
+      for (int step = group; step < S::kSteps; step += 2) convert(g, step);
+      more = sums_at[g & 1].more;
+      arrive(sums_free + 8 * (g & 1));
+      arrive(v_done + 8 * (g & 1));
+      arrive(v_free + 8 * (g & 1));
+      if (*dead && g > 1 << 24) break;
+    }
+  } else {
+    // ---- the state: thread = column of it (lane of tensor memory), half of the rows
+    more_registers<96>();
+    const int quad = warp & 3, a = quad * 32 + lane, col0 = ((warp - 20) >> 2) * S::kCols;
+    const bool holds = quad * 32 < D;
+    const uint32_t lanes = (uint32_t)quad * 32 << 16;
+    float s[S::kCols];
+    auto at_state = [&](float* pool, int64_t first) { return pool + first + ((int64_t)col0 * D + a); };
+    auto load_state = [&](const float* src) {
+#pragma unroll
+      for (int i = 0; i < S::kCols; ++i) s[i] = src[i * D];
+    };
+    auto store_state = [&](float* dst) {
+#pragma unroll
+      for (int i = 0; i < S::kCols; ++i) dst[i * D] = s[i];
+    };
+    auto set_at = [&](int set, int h) { return at_state(w.states, ((int64_t)set * p.H + h) * D * D); };
+    auto publish = [&](int g) {                                 // the state as the outputs of chunk g read it
+      if (g > 0) wait(state_read, (g - 1) & 1);
+      if (holds)
+#pragma unroll
+        for (int i = 0; i < S::kCols; i += 8) {
+          const int at = (col0 + i) >> 3;
+          sts16(base + S::kS + (at >> 3) * (D * 128) + a * 128 + (((at & 7) ^ (a & 7)) << 4),
+                make_uint4(pack(s[i], s[i + 1]), pack(s[i + 2], s[i + 3]), pack(s[i + 4], s[i + 5]), pack(s[i + 6], s[i + 7])));
+        }
+      fence_async_proxy();
+      arrive(state_full);
+    };
     each_unit([&](int u, int chunks, int g0, int k) {
 #pragma unroll
       for (int i = 0; i < S::kCols; ++i) s[i] = 0.f;
@@ -754,15 +786,11 @@ prompt_kernel(const LinearParams p, const LinearPlan w, const __grid_constant__ 
       if (kRows) publish(g0);
       for (int c = 0; c < chunks; ++c) {
         const int g = g0 + c;
-        convert(g, group + 4);
+        wait(sums_full + 8 * (g & 1), g >> 1 & 1);
         const Sums& sums = sums_at[g & 1];
         const float f = sums.factor;
         const float keep = sums.near ? 1.f : 0.f;
-        const bool more = sums.more;
         arrive(sums_free + 8 * (g & 1));
-        arrive(v_done + 8 * (g & 1));
-        arrive(v_free + 8 * (g & 1));
-        if (more) convert(g + 1, group);
         wait(add_full, g & 1);
         tc_fence_after();
         if (holds)
