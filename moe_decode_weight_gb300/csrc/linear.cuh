@@ -27,24 +27,25 @@ struct LinearParams {
   int wide;                        // rows of out lie on 32-byte boundaries
 };
 
-// Rows of a chunk; requests of up to kLinearShort rows take them one by one; least chunks of a segment.
-constexpr int kLinearChunk = 128, kLinearShort = 16, kLinearSegment = 4;
+// Rows of a chunk; requests of up to kLinearShort rows take them one by one; least chunks of a segment, and its pieces in the first pass.
+constexpr int kLinearChunk = 128, kLinearShort = 16, kLinearSegment = 4, kLinearPieces = 3;
 
 // A part of a request's rows, for all value heads, in the workspace.
 struct LinearEntry {
   int row0, rows, slot_in, slot_out;
-  int seg, segs;                   // segment of how many
-  int set, pad;                    // first set of states of the request: the one before it, then what each segment adds
+  int seg, segs;                   // segment of how many; in the first pass piece of how many, and one
+  int set, pad;                    // set of states before the request; those after each of its pieces follow
 };
 
 // The workspace of mdw_linear_attention.
 struct LinearPlan {
-  int32_t* head;                   // units; units of the first pass; whether that was cut short
+  int32_t* head;                   // units; units of the first pass; whether that was cut short; requests of several segments and heads
   int32_t* ok;
   LinearEntry* all;                // [B + blocks] every segment, longest first
-  LinearEntry* first;              // [blocks] those whose state others start from
-  float* logs;                     // [blocks] log decay of a segment, by set and head
-  float* states;                   // [blocks][D][D] by set and head
+  LinearEntry* first;              // [3 blocks] pieces of segments whose state others start from
+  LinearEntry* joins;              // [blocks] requests of several segments
+  float* logs;                     // [3 blocks] log decay of a piece, by set and head
+  float* states;                   // [3 blocks][D][D] by set and head
 };
 cudaError_t launch_prompts(const LinearParams& p, const LinearPlan& w, int D, int grid, int dev, cudaStream_t s);
 

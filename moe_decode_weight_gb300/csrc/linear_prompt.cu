@@ -56,13 +56,6 @@ __device__ __forceinline__ float exp2_fast(float x) {
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
-// As mbar_try(), for up to 10 us before it answers: few instructions are spent on waiting.
-__device__ __forceinline__ bool mbar_try_long(uint32_t bar, uint32_t parity) {
-  uint32_t ok;
-  asm volatile("{ .reg .pred p; mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3; selp.u32 %0, 1, 0, p; }"
-               : "=r"(ok) : "r"(bar), "r"(parity), "r"(10000u) : "memory");
-  return ok != 0;
-}
 // 16 lanes x 8 columns of tensor memory: a thread has columns lane % 4 and lane % 4 + 4 of lanes lane / 4 and lane / 4 + 8.
 __device__ __forceinline__ void tc_st_16x128(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
   asm volatile("tcgen05.st.sync.aligned.16x128b.x2.b32 [%0], {%1,%2,%3,%4};" :: "r"(addr), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
@@ -116,10 +109,10 @@ __device__ __forceinline__ void after_previous() {
 
 __global__ void __launch_bounds__(1024) plan_kernel(const LinearParams p, const LinearPlan w, int blocks) {
   constexpr int kBuckets = 1024;                                // units of so many chunks (the last: and more)
-  __shared__ int at[kBuckets], sums[32], sets, extra;
+  __shared__ int at[kBuckets], sums[32], sets, extra, joins;
   __shared__ unsigned long long total;
   const int tid = threadIdx.x;
-  if (tid == 0) total = 0, sets = 0, extra = 0;
+  if (tid == 0) total = 0, sets = 0, extra = 0, joins = 0;
   at[tid] = 0;
   after_previous();
   __syncthreads();
@@ -131,7 +124,9 @@ __global__ void __launch_bounds__(1024) plan_kernel(const LinearParams p, const 
   for (int b = tid; b < p.B; b += blockDim.x) mine += chunks_of(b);
   if (mine) atomicAdd(&total, mine);
   __syncthreads();
-  // A segment is at least an SM's share of all work, and four chunks: its start costs about one.
+  // A segment is at least an SM's share of all work, and four chunks: its start costs about one. The first pass has all segments but each
+  // request's last, in three pieces each, so that it fills the SMs too (16,301 rows of 32 heads: 4 segments, so 96 units of 32 chunks there or
+  // 288 of about 11 on 152 SMs: 90 and 45 us, the whole call 223 and 216).
   const long long share = max((long long)kLinearSegment, ((long long)total * p.H + blocks - 1) / blocks);
   auto cut = [&](int chunks, int& n) {                          // segments and the chunks of one
     n = (int)max(1ll, chunks / share);
@@ -168,14 +163,22 @@ __global__ void __launch_bounds__(1024) plan_kernel(const LinearParams p, const 
     int n;
     const int each = cut(chunks, n), rows = p.row_start[b + 1] - p.row_start[b];
     LinearEntry e{p.row_start[b], 0, p.slot_in[b], p.slot_out[b], 0, n, 0, 0};
-    if (n > 1) e.set = atomicAdd(&sets, n);
+    // sets of states: the one before the request, then what each piece of all segments but the last adds
+    const int pieces = (n - 1) * kLinearPieces;
+    if (n > 1) {
+      e.set = atomicAdd(&sets, pieces + 1);
+      w.joins[atomicAdd(&joins, 1)] = e;
+    }
     const int to = atomicAdd(&at[min(each, kBuckets - 1)], n);
     for (int s = 0; s < n; ++s) {
       e.seg = s;
       e.row0 = p.row_start[b] + s * each * kChunk;
       e.rows = min(rows - s * each * kChunk, each * kChunk);
       w.all[to + s] = e;
-      if (s + 1 < n) w.first[atomicAdd(&extra, 1)] = e;
+    }
+    for (int s = 0; s < pieces; ++s) {
+      auto start = [&](int s) { return s / kLinearPieces * each + s % kLinearPieces * each / kLinearPieces; };
+      w.first[atomicAdd(&extra, 1)] = LinearEntry{p.row_start[b] + start(s) * kChunk, (start(s + 1) - start(s)) * kChunk, p.slot_in[b], -1, s, pieces + 1, e.set, 0};
     }
   }
   __syncthreads();
@@ -183,30 +186,50 @@ __global__ void __launch_bounds__(1024) plan_kernel(const LinearParams p, const 
     w.head[0] = all * p.H;
     w.head[1] = extra * p.H;
     w.head[2] = 0;
+    w.head[3] = joins * p.H;
   }
 }
 
-// The states at the starts of a request's segments from what each segment adds: block (first segment and head, part of the elements).
+// The states at the starts of a request's segments from what each piece adds: block (request and head, part of the elements). A segment's pieces
+// are asked for at once, those of the next one before these are summed.
 constexpr int kSumsParts = 16;
 __global__ void __launch_bounds__(256) sums_kernel(const LinearPlan w, int H, int elements) {
   after_previous();
-  if ((int)blockIdx.x >= w.head[1]) return;
-  const LinearEntry e = w.first[blockIdx.x / H];
-  const int h = blockIdx.x % H;
-  if (e.seg != 0) return;
-  for (int i = (blockIdx.y * blockDim.x + threadIdx.x) * 4; i < elements; i += gridDim.y * blockDim.x * 4) {
-    float4* at = reinterpret_cast<float4*>(w.states + ((int64_t)(e.set + 1) * H + h) * elements + i);
-    float4 s = *at;
-    for (int k = 2; k < e.segs; ++k) {
-      at += (int64_t)H * elements / 4;
-      const Decay f(w.logs[(size_t)(e.set + k) * H + h]);
-      const float4 x = *at;
-      s.x = fmaf(s.x, f.f, f.near ? s.x : 0.f) + x.x;
-      s.y = fmaf(s.y, f.f, f.near ? s.y : 0.f) + x.y;
-      s.z = fmaf(s.z, f.f, f.near ? s.z : 0.f) + x.z;
-      s.w = fmaf(s.w, f.f, f.near ? s.w : 0.f) + x.w;
-      *at = s;
+  if ((int)blockIdx.x >= w.head[3]) return;
+  const LinearEntry e = w.joins[blockIdx.x / H];
+  const int h = blockIdx.x % H, i = (blockIdx.y * blockDim.x + threadIdx.x) * 4;
+  if (i >= elements) return;
+  auto at = [&](int set) { return reinterpret_cast<float4*>(w.states + ((int64_t)(e.set + set) * H + h) * elements + i); };
+  float4 x[kLinearPieces], s = make_float4(0.f, 0.f, 0.f, 0.f);
+  float logs[kLinearPieces];
+  auto ask = [&](int seg) {
+#pragma unroll
+    for (int k = 0; k < kLinearPieces; ++k) {
+      const int set = seg * kLinearPieces + k + 1;
+      x[k] = *at(set);
+      logs[k] = w.logs[(size_t)(e.set + set) * H + h];
     }
+  };
+  ask(0);
+  for (int seg = 0; seg + 1 < e.segs; ++seg) {
+    float4 now[kLinearPieces];
+    float decays[kLinearPieces];
+#pragma unroll
+    for (int k = 0; k < kLinearPieces; ++k) now[k] = x[k], decays[k] = logs[k];
+    if (seg + 2 < e.segs) ask(seg + 1);
+#pragma unroll
+    for (int k = 0; k < kLinearPieces; ++k) {
+      if (seg == 0 && k == 0) {                                 // holds the request's own state
+        s = now[0];
+        continue;
+      }
+      const Decay f(decays[k]);
+      s.x = fmaf(s.x, f.f, f.near ? s.x : 0.f) + now[k].x;
+      s.y = fmaf(s.y, f.f, f.near ? s.y : 0.f) + now[k].y;
+      s.z = fmaf(s.z, f.f, f.near ? s.z : 0.f) + now[k].z;
+      s.w = fmaf(s.w, f.f, f.near ? s.w : 0.f) + now[k].w;
+    }
+    *at((seg + 1) * kLinearPieces) = s;
   }
 }
 
@@ -309,7 +332,7 @@ prompt_kernel(const LinearParams p, const LinearPlan w, const __grid_constant__ 
   auto wait = [&](uint32_t b, uint32_t parity) {
     if (mbar_test(b, parity)) return;
     const long long t0 = clock64();
-    while (!mbar_try_long(b, parity)) {
+    while (!mbar_try(b, parity)) {
       if (*dead) return;
       if (clock64() - t0 > p.spin_budget) {
         *dead = 1;
@@ -780,7 +803,7 @@ prompt_kernel(const LinearParams p, const LinearPlan w, const __grid_constant__ 
           // (the last segment may store to the slot before the first one reads it)
           if (!kRows) store_state(set_at(e.set, h));
         } else if (kRows) {
-          load_state(set_at(e.set + e.seg, h));
+          load_state(set_at(e.set + e.seg * kLinearPieces, h));
         }
       }
       if (kRows) publish(g0);

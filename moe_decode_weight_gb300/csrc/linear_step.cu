@@ -195,8 +195,8 @@ cudaError_t launch_step(const LinearParams& p, int D, int sms, cudaStream_t s) {
   return cudaGetLastError();
 }
 
-// The parts of the workspace, and its bytes. Segments: their number times the heads is at most the number of blocks (a segment is at
-// least a block's share of all chunks and heads).
+// The parts of the workspace, and its bytes. Segments of requests that have several: their number times the heads is at most the number of
+// blocks (a segment is at least a block's share of all chunks and heads); each has three pieces, and a set of states for a piece.
 std::pair<LinearPlan, size_t> plan_of(uint8_t* ws, int B, int D, int grid) {
   size_t at = 0;
   auto take = [&](size_t bytes) {
@@ -208,9 +208,10 @@ std::pair<LinearPlan, size_t> plan_of(uint8_t* ws, int B, int D, int grid) {
   w.head = reinterpret_cast<int32_t*>(take(256));
   w.ok = reinterpret_cast<int32_t*>(take((size_t)B * 4));
   w.all = reinterpret_cast<LinearEntry*>(take((size_t)(B + grid) * sizeof(LinearEntry)));
-  w.first = reinterpret_cast<LinearEntry*>(take((size_t)grid * sizeof(LinearEntry)));
-  w.logs = reinterpret_cast<float*>(take((size_t)grid * 4));
-  w.states = reinterpret_cast<float*>(take((size_t)grid * D * D * 4));
+  w.first = reinterpret_cast<LinearEntry*>(take((size_t)kLinearPieces * grid * sizeof(LinearEntry)));
+  w.joins = reinterpret_cast<LinearEntry*>(take((size_t)grid * sizeof(LinearEntry)));
+  w.logs = reinterpret_cast<float*>(take((size_t)kLinearPieces * grid * 4));
+  w.states = reinterpret_cast<float*>(take((size_t)kLinearPieces * grid * D * D * 4));
   return {w, at};
 }
 
