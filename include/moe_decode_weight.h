@@ -486,14 +486,16 @@ mdw_status mdw_tree_attention(const mdw_kv_cache* cache, int32_t B, int32_t T, i
  * The conventions of the attention sub-layer above hold (row strides, status words), and these:
  *   - q and k are rows [qk_heads][head_dim], v and out rows [heads][head_dim] of bf16; value head h uses query and
  *     key head h / (heads / qk_heads) (at most MDW_MAX_GROUP value heads to one).
- *   - log_decay: fp32 [T][heads] (row stride ldd), or [heads] for all rows with ldd = 0; 4-byte aligned. -inf forgets what
- *     was before.
+ *   - log_decay: fp32 [T][heads] (row stride ldd), or [heads] for all rows with ldd = 0; 4-byte aligned; at most 0 (what
+ *     growing states give is not defined). -inf forgets what was before.
  *   - Rows row_start[b] .. row_start[b+1] - 1 are those of request b, in order. Rows before row_start[0] or from
  *     row_start[B] on are left as they were.
  *   - slot_in[b] (-1: zeros) is the slot of the state before, slot_out[b] (-1: not stored) of the one after; they
  *     may be the same. A request is skipped, with MDW_ERR_DEVICE_BOUNDS, if its rows or slots are bad (outside
  *     [0, T), more than max_new rows, slots from num_slots on) or if another request stores to the slot that it
  *     reads or stores to.
+ *   - Row strides are at most 2^36 elements. Outputs overlap no input. Where a wait inside a kernel runs out
+ *     (MDW_ERR_TIMEOUT), outputs and stored states of the call's requests of more than 16 rows are not defined.
  *   - States and sums are fp32, in a fixed order, which depends on the lengths and the call's sizes and not on timing.
  *   - Values that are not finite make results of their own row and later ones of the request NaN or infinite (which,
  *     is not defined), and reach no earlier row and no other request. */

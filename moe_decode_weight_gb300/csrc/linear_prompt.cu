@@ -7,7 +7,7 @@
 // the decayed values. Sums of log decays have 48 bits and only differences leave them, so none of their digits
 // are lost; no factor is above 1, so nothing overflows and what underflows would have underflown.
 //
-// Roundings to bf16, the operands' type: the weighted scores and the state as the outputs read it (outputs are off by 0.0022 of
+// Roundings to bf16, the operands' type: the weighted scores and the state as the outputs read it (outputs are off by 0.0023 of
 // their norm instead of the 0.0017 of their own rounding). The decayed values enter the state's product as
 // three bf16 numbers that hold 24 bits together, so a state carries the error of fp32 sums only; it is kept in registers.
 //
@@ -16,8 +16,11 @@
 // segment then starts from the sums before it. plan_kernel lays the units out, longest first, from the lengths on the
 // device; block i takes units i, 2 G - 1 - i, 2 G + i, ... of G blocks, one on each SM.
 //
-// What bounds it: 4 rows of D 16-bit elements in and out for each row, and as floor of a chunk the chain of the state
-// (values decayed, three products, state scaled and rounded). Roles of a block:
+// What bounds it: neither memory (42 to 50 % of the copy rate) nor the matrix unit (33 %) nor the issue of instructions (39 %), but
+// the chain of a chunk: the outputs of the last one read the state, the state takes its products and is rounded, the tile of q is
+// free and filled again, scores, weights, products with the values. It takes 6,000 to 7,000 cycles and only parts of two chunks overlap;
+// heads whose decays pass 2^-60 within a chunk pay 2,400 more to scale q. Measured: 16,301 rows of 32 heads from an empty state 216 us
+// (first pass 45, sums 9, outputs 150), 24 requests of up to 2,100 rows of 20 heads 148 us. Roles of a block:
 //   warp 0       requests the tiles of q, k and v by TMA (swizzled, 128 rows x 128 bytes)
 //   warp 1       issues the products for the state
 //   warp 2       sums the decays of the next chunk
@@ -124,9 +127,10 @@ __global__ void __launch_bounds__(1024) plan_kernel(const LinearParams p, const 
   for (int b = tid; b < p.B; b += blockDim.x) mine += chunks_of(b);
   if (mine) atomicAdd(&total, mine);
   __syncthreads();
-  // A segment is at least an SM's share of all work, and four chunks: its start costs about one. The first pass has all segments but each
-  // request's last, in three pieces each, so that it fills the SMs too (16,301 rows of 32 heads: 4 segments, so 96 units of 32 chunks there or
-  // 288 of about 11 on 152 SMs: 90 and 45 us, the whole call 223 and 216).
+  // A segment is at least an SM's share of all work, and four chunks: its start costs about one. (32 heads, one request with and without
+  // segments: 1,000 rows 45 and 47 us, 2,000 54 and 77, 4,000 79 and 135, 16,301 218 and 507; four of 1,000 rows 58 and 53. At least eight
+  // chunks: 2,000 rows 64, four of 1,000 rows 53.) The first pass has all segments but each request's last, in three pieces each, so that it
+  // fills the SMs too (16,301 rows: 4 segments, so 96 units of 32 chunks there or 288 of about 11 on 152 SMs: 90 and 45 us).
   const long long share = max((long long)kLinearSegment, ((long long)total * p.H + blocks - 1) / blocks);
   auto cut = [&](int chunks, int& n) {                          // segments and the chunks of one
     n = (int)max(1ll, chunks / share);
@@ -332,14 +336,14 @@ prompt_kernel(const LinearParams p, const LinearPlan w, const __grid_constant__ 
   auto wait = [&](uint32_t b, uint32_t parity) {
     if (mbar_test(b, parity)) return;
     const long long t0 = clock64();
-    while (!mbar_try(b, parity)) {
+    do {
       if (*dead) return;
       if (clock64() - t0 > p.spin_budget) {
         *dead = 1;
         raise_status(p.status, MDW_ERR_TIMEOUT);
         return;
       }
-    }
+    } while (!mbar_try(b, parity));
   };
   auto arrive = [&](uint32_t b) {                               // of the warp
     __syncwarp();
@@ -421,7 +425,7 @@ prompt_kernel(const LinearParams p, const LinearPlan w, const __grid_constant__ 
         }
       }
     });
-    if (lane == 0) tc_commit(end);
+    if (elect_one()) tc_commit(end);                            // (by the thread that issued the products)
     __syncwarp();
     mbar_drain_inline(end, 0);                                  // nothing is in flight when the columns are given back
   } else if (warp == 3) {
@@ -474,7 +478,7 @@ prompt_kernel(const LinearParams p, const LinearPlan w, const __grid_constant__ 
           __syncwarp();
         }
       });
-      if (lane == 0) tc_commit(end);
+      if (elect_one()) tc_commit(end);                            // (by the thread that issued the products)
       __syncwarp();
       mbar_drain_inline(end, 0);
     }
@@ -637,7 +641,7 @@ prompt_kernel(const LinearParams p, const LinearPlan w, const __grid_constant__ 
           wait(v_done + 8 * slot, g >> 1 & 1);
           wait(o_full + 8 * slot, g >> 1 & 1);
           tc_fence_after();
-          const bool bad = bad_values[g & 3] != 0, store = row < valid && !*dead;
+          const bool alive = !*dead, bad = alive && bad_values[g & 3] != 0, store = alive && row < valid;   // (not alive: valid may be anything)
           __nv_bfloat16* dst = p.out + (int64_t)(first + min(row, valid - 1)) * p.ldo + (int64_t)h * D;
           float o[16];
           tc_ld16(o, tmem + lanes + S::kOut);
@@ -679,8 +683,9 @@ prompt_kernel(const LinearParams p, const LinearPlan w, const __grid_constant__ 
     const int quad = warp & 3, group = (warp - 12) >> 2, id = threadIdx.x & 127;
     const bool holds = quad * 32 < D;
     const uint32_t lanes = (uint32_t)quad * 32 << 16;
-    // The decayed values of a step of rows as three bf16 numbers, by 4 of the warps (the others have the next step), into tensor memory: a lane is a column of the values,
-    // which the transposing loads from shared memory give. A thread has two neighbouring rows of 8 and two of the other 8.
+    // The decayed values of a step of rows as three bf16 numbers, by 4 of the warps (the others have the next step), into tensor
+    // memory: a lane is a column of the values, which the transposing loads from shared memory give. A thread has two neighbouring
+    // rows of 8 and two of the other 8.
     auto convert = [&](int g, int step) {
       const int slot = g & 1, use = g * S::kSteps + step;
       const int at_slot = step & 3;
@@ -760,7 +765,7 @@ prompt_kernel(const LinearParams p, const LinearPlan w, const __grid_constant__ 
       arrive(sums_free + 8 * (g & 1));
       arrive(v_done + 8 * (g & 1));
       arrive(v_free + 8 * (g & 1));
-      if (*dead && g > 1 << 24) break;
+      if (__any_sync(0xffffffffu, *dead)) break;                // (more may be anything)
     }
   } else {
     // ---- the state: thread = column of it (lane of tensor memory), half of the rows
@@ -893,6 +898,7 @@ cudaError_t launch(const LinearParams& p, const LinearPlan& w, const CUtensorMap
 }  // namespace
 
 cudaError_t launch_prompts(const LinearParams& p0, const LinearPlan& w, int D, int grid, int dev, cudaStream_t s) {
+  static_assert(kLinearPieces <= kLinearSegment, "a piece has a chunk at least");
   static_assert(sizeof(Sums) == 5 * kChunk * 4 + 28 * 4 && Shape<128, true>::kSmem <= 227 * 1024, "");
   LinearParams p = p0;
   p.wide = (reinterpret_cast<uintptr_t>(p.out) | (uintptr_t)p.ldo * 2) % 32 == 0;

@@ -364,6 +364,78 @@ def test_slots_beyond_4_gigabytes():
         assert_close(host(pool[c.slot_out[b]]), s, 2.0 ** -18 * size + 4 * U * chain)
 
 
+@pytest.mark.parametrize("lens", [[1024], [1025, 3], [1500, 0, 1200], [13 * 128 + 1, 17], [2 * 2048 + 77]], ids=str)
+@pytest.mark.parametrize("h,d", [(1, 128), (2, 64)])
+def test_segments_of_every_length(lens, h, d):
+    """Requests long enough to be cut into segments, of 4 chunks and on, stored to the slots that they were read from."""
+    c = Case(sum(lens), lens, h, h, d, True, rate=0.01)
+    before = host(c.pool)
+    c.call()
+    check_rows(c, before)
+
+
+@pytest.mark.parametrize("lens", [[5, 200], [130, 1]], ids=str)
+def test_outputs_off_32_byte_boundaries(lens):
+    c = Case(18, lens, 2, 2, 128)
+    buf = torch.full((c.t, 2 * 128 + 24), 7.0, dtype=BF, device="cuda")
+    c.out = buf[:, 8:8 + 256].unflatten(1, (2, 128))
+    before = host(c.pool)
+    c.call()
+    check_rows(c, before)
+    assert (buf[:, :8] == 7).all() and (buf[:, 264:] == 7).all()
+
+
+@pytest.mark.parametrize("b", [300, 4096])
+def test_many_requests(b):
+    lens = [(1, 0, 2, 17, 1, 16, 130, 1)[i * 5 % 8] if i < 300 else i % 2 for i in range(b)]
+    c = Case(19, lens, 1, 1, 64)
+    before = host(c.pool)
+    c.call()
+    check_rows(c, before)
+    assert int(c.status) == 0
+
+
+def test_workspace_of_two_captured_calls():
+    """One workspace serves captured calls that replay one after the other, in either order."""
+    a, b = Case(20, [1300, 2, 140], 2, 2, 64), Case(21, [200, 40], 2, 2, 64, inplace=False)
+    ws = torch.empty(max(api.mdw_linear_attention_workspace_bytes(api.LinearState(c.pool), c.b, c.t, c.hk, c.new) for c in (a, b)),
+                     dtype=torch.uint8, device="cuda")
+    saved = [c.pool.clone() for c in (a, b)]
+    args = [(api.LinearState(c.pool), c.q, c.k, c.v, c.g, c.out, i32(c.start.tolist()), i32(c.slot_in), i32(c.slot_out), c.new, ws) for c in (a, b)]
+    torch.cuda.synchronize()
+    graphs = []
+    for x in args:
+        graphs.append(torch.cuda.CUDAGraph())
+        with torch.cuda.graph(graphs[-1]):
+            api.mdw_linear_attention(*x)
+    for order in ((0, 1), (1, 0), (0, 0)):
+        for i in order:
+            c = (a, b)[i]
+            c.pool.copy_(saved[i])
+            c.out.fill_(7)
+            graphs[i].replay()
+            torch.cuda.synchronize()
+            check_rows(c, host(saved[i]))
+
+
+@pytest.mark.parametrize("lens", [[300, 2], [1500]], ids=str)
+def test_a_wait_that_runs_out(lens):
+    """With a budget of one cycle the first wait of a block gives up: a status word, no fault, and the next call is right."""
+    c = Case(22, lens, 2, 2, 128)
+    previous = api.mdw_debug_set_spin_budget(1)
+    try:
+        c.call()
+    finally:
+        api.mdw_debug_set_spin_budget(previous)
+    torch.cuda.synchronize()
+    assert int(c.status) == 6                                  # MDW_ERR_TIMEOUT
+    c = Case(22, lens, 2, 2, 128)
+    before = host(c.pool)
+    c.call()
+    check_rows(c, before)
+    assert int(c.status) == 0
+
+
 # ------------------------------------------------------------------------------ trees
 
 
