@@ -6,6 +6,7 @@
 // What bounds it is memory for many rows and the two chains load - sum - exchange for few. A row lies in the
 // registers of its threads, eight neighbouring elements (16 or 32 bytes of a load) at a time, so it is read once; the norms are
 // sums over the row's warps. Rows that are not on 16-byte boundaries are read by the aligned pieces around them and shifted in registers.
+// Measured: 16,381 rows of 2,560 elements with an fp32 residual 76 us (6.6 TB/s), gated norms of 4,099 rows of 32 heads 24 us (4.1 TB/s).
 #include <cmath>
 #include <type_traits>
 
@@ -134,8 +135,9 @@ __device__ __forceinline__ float sigmoid(float x) {
   return r;
 }
 
-// Pieces of a thread: two, as more rows are on their way then; rows off 16-byte boundaries take more registers a piece and are spread over
-// more threads, up to 8,192 elements one piece each (16,000 rows of 2,563 elements: two pieces a thread 278 us, one 160).
+// Pieces of a thread: two above 256 elements, as more rows are on their way then (16,381 rows of 2,560 elements: 69 us, one piece 83; 256
+// elements: 18 and 16). Rows off 16-byte boundaries take more registers a piece and are spread over more threads, up to 8,192 elements one
+// piece each (16,381 rows of 2,563 elements: two pieces 195 us, one 144).
 constexpr int kMaxThreads = 1024;
 
 // T: the 16-bit type; Y, S: types of y and of residual and sum. kPieces of eight elements a thread. kVector: all rows on 16-byte

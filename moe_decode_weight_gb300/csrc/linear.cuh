@@ -27,7 +27,9 @@ struct LinearParams {
   int wide;                        // rows of out lie on 32-byte boundaries
 };
 
-// Rows of a chunk; requests of up to kLinearShort rows take them one by one; least chunks of a segment, and its pieces in the first pass.
+// Rows of a chunk; least chunks of a segment, and its pieces in the first pass. Requests of up to kLinearShort rows take them one by one: rows
+// then cost 0.5 us (3 requests of 32 heads) to 5 us (48) each, and chunks of 128 rows as much for one row as for all: the two are even at
+// 20 rows of 3 requests (both 22 us), 16 of 8 (30 us), 11 of 48 (87 us; 16 rows one by one 110). A call of few rows is one launch then.
 constexpr int kLinearChunk = 128, kLinearShort = 16, kLinearSegment = 4, kLinearPieces = 3;
 
 // A part of a request's rows, for all value heads, in the workspace.
@@ -54,10 +56,10 @@ struct LinearRequest {
   int row0, n, in, out;
 };
 
-// Request b, read by all threads of a block together; false (for all) if it has to be skipped. A slot that is
+// Request b, read by all threads of a block together; not 0 (for some of them) if it has to be skipped. A slot that is
 // stored to by one request and read or stored to by another one would make results depend on timing, so every
 // block looks through the list of slots: B loads of 4 bytes from L2.
-__device__ __forceinline__ bool linear_request(const LinearParams& p, int b, LinearRequest& r) {
+__device__ __forceinline__ int look_at_request(const LinearParams& p, int b, LinearRequest& r) {
   r.row0 = p.row_start[b];
   const int end = p.row_start[b + 1];
   r.in = p.slot_in[b];
@@ -70,11 +72,15 @@ __device__ __forceinline__ bool linear_request(const LinearParams& p, int b, Lin
     }
   bad |= r.row0 < 0 || end < r.row0 || end > p.T || r.in < -1 || r.in >= p.num_slots || r.out < -1 || r.out >= p.num_slots;
   r.n = bad ? 0 : end - r.row0;
-  bad |= r.n > p.max_new;
+  return bad | (r.n > p.max_new);
+}
+// What the block's threads make of it: false if the request has to be skipped.
+__device__ __forceinline__ bool settle_request(const LinearParams& p, int bad) {
   bad = __syncthreads_or(bad);
   if (bad && threadIdx.x == 0) raise_status(p.status, MDW_ERR_DEVICE_BOUNDS);
   return !bad;
 }
+__device__ __forceinline__ bool linear_request(const LinearParams& p, int b, LinearRequest& r) { return settle_request(p, look_at_request(p, b, r)); }
 
 __device__ __forceinline__ float log_decay_of(const LinearParams& p, int row, int h) { return p.decay[(int64_t)row * p.ldd + h]; }
 

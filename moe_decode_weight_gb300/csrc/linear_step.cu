@@ -3,8 +3,10 @@
 // Mathematics. S <- e^g S + k v^T, o = scale S^T q, for a request's rows in order. The block of a request and value
 // head holds S in registers, so the state is read and written once whatever the number of rows.
 //
-// What bounds it is the state's 64 KB (heads of 128) in and out of memory: D rows of it lie on the
-// warps, four columns on a lane, and all loads are requested before the first is used.
+// What bounds it is the state's 64 KB (heads of 128) in and out of memory: D rows of it lie on the warps, four columns on a lane, and all
+// loads are requested before the first is used. Measured: 61 requests of 1 to 4 rows and 32 heads 50 us, where a plain copy of
+// their states takes 43 (a quarter of a warp's time goes to waiting for memory, as much to the barriers around the rows); one row of 20 heads 6
+// us with its launch. Blocks that stay and copy the next state to shared memory meanwhile took 57: two of them an SM, with the same barriers.
 #include <algorithm>
 #include <cmath>
 #include <utility>
@@ -48,6 +50,7 @@ constexpr int kRows = 8;                                        // rows whose el
 
 // One block: request blockIdx.z, value head blockIdx.y, kCols of the columns. kOut: outputs of all rows; else the rows
 // whose bits are set change the state only.
+// Blocks of an SM, 64 of 128 columns: three with 80 registers (two or four: 59 and 52 us for the 61 requests instead of 50).
 template <int D, int kCols, bool kOut>
 __global__ void __launch_bounds__(kThreads, D * kCols > 64 * 64 ? 3 : 4) step_kernel(const LinearParams p) {
   constexpr int kLanes = kCols / 4, kGroups = kThreads / kLanes, kPer = D / kGroups;   // lanes of a row, rows at once, rows of a thread
@@ -58,21 +61,24 @@ __global__ void __launch_bounds__(kThreads, D * kCols > 64 * 64 ? 3 : 4) step_ke
   __shared__ int taken[kRows];
   const int b = blockIdx.z, h = blockIdx.y, col0 = blockIdx.x * kCols, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   if (kOut) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");   // (plan_kernel of longer requests waits for this one's end)
-  LinearRequest r;
-  const bool sound = linear_request(p, b, r);
-  if (kOut && p.ok && blockIdx.x == 0 && h == 0 && tid == 0) p.ok[b] = sound;
-  if (!sound || (kOut && r.n > p.short_rows)) return;
-  if (r.out < 0 && !(kOut && r.n > 0)) return;
   const int c = tid % kLanes * 4, a0 = tid / kLanes * kPer;
   const int64_t at = ((int64_t)h * D + a0) * D + col0 + c;
+  // the state is asked for before the request is known to be sound, as soon as its slot is known to exist
+  LinearRequest r;
+  const int bad = look_at_request(p, b, r);
+  const bool holds = r.in >= 0 && r.in < p.num_slots && (r.out >= 0 || kOut) && !(kOut && r.n > p.short_rows);
   Pair s[kPer][2];
 #pragma unroll
   for (int i = 0; i < kPer; ++i) {
     float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
-    if (r.in >= 0) x = __ldcs(reinterpret_cast<const float4*>(p.s + r.in * p.slot_stride + at + i * D));
+    if (holds) x = __ldcs(reinterpret_cast<const float4*>(p.s + r.in * p.slot_stride + at + i * D));
     s[i][0] = Pair(x.x, x.y);
     s[i][1] = Pair(x.z, x.w);
   }
+  const bool sound = settle_request(p, bad);
+  if (kOut && p.ok && blockIdx.x == 0 && h == 0 && tid == 0) p.ok[b] = sound;
+  if (!sound || (kOut && r.n > p.short_rows)) return;
+  if (r.out < 0 && !(kOut && r.n > 0)) return;
   uint64_t left = 0;                                            // accepted rows that are still to come
   if (!kOut) left = p.bits[b] & (r.n < 64 ? (1ull << r.n) - 1 : ~0ull);
   int next = 0;
@@ -183,7 +189,8 @@ void launch_cols(const LinearParams& p, cudaStream_t s) {
 }
 template <bool kOut>
 cudaError_t launch_step(const LinearParams& p, int D, int sms, cudaStream_t s) {
-  // columns are split further where few requests and heads leave SMs without a block
+  // columns are split further where few requests and heads leave SMs without a block (20 heads, 4 rows: one request 9.4 us instead of 11.4,
+  // 4 the same, 8 15.5 instead of 14.4, 16 21.6 instead of 19.6)
   const bool few = (int64_t)p.B * p.H * (D / 64) <= sms;
   if (D == 128) {
     if (few) launch_cols<128, 32, kOut>(p, s);

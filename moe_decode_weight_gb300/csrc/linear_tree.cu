@@ -8,9 +8,9 @@
 // What bounds it up to 16 nodes is the state's 64 KB (heads of 128) from memory, so a block requests all of it before
 // anything else: a thread's loads are whole operands of m16n8k16 products (four columns of it are four tiles' column, which
 // only changes the order of the columns), turned into two bf16 numbers that hold 16 bits together. The scores and weights are
-// products of the same kind, the weights as two bf16 numbers too. 16 rows a block, or 32 or 64.
-//
-// 64 nodes: three quarters of the products are with the state.
+// products of the same kind, the weights as two bf16 numbers too. A block asks for its next unit's state as soon as it has used up the
+// one before. Measured: 48 requests of up to 16 nodes and 32 heads 32 us, half of the copy rate; 12 requests of 64 nodes and 64 heads of 64 25 us,
+// where the split states, two products each, and the barriers between the steps of a unit bound it (16 warps an SM).
 #include <cmath>
 
 #include "linear.cuh"
@@ -137,194 +137,194 @@ __global__ void __launch_bounds__(Shape<D, kTiles>::kThreads, Shape<D, kTiles>::
   ask_rows(r);
   __syncthreads();                                              // (odd is cleared)
   for (int u = blockIdx.x; u < units; u += gridDim.x) {
-  const Unit next = look(u + gridDim.x);
-  if (r.n > 0) {
-  // ---- weights: a warp's rows, sums from the row downwards
+    const Unit next = look(u + gridDim.x);
+    if (r.n > 0) {
+      // ---- weights: a warp's rows, sums from the row downwards
 #pragma unroll 4
-  for (int j = 0; j < kMasks; ++j) {
-    const int i = j * S::kWarps + warp;
-    const uint64_t own = __shfl_sync(0xffffffffu, mask, j);
-    const uint64_t seen = i < r.n ? (own & ((1ull << i) - 1)) | 1ull << i : 0;
-    const bool s0 = seen >> (2 * lane) & 1, s1 = seen >> (2 * lane + 1) & 1;
-    const float x1 = s1 ? g1 : 0.f;
-    float sum = (s0 ? g0 : 0.f) + x1;
+      for (int j = 0; j < kMasks; ++j) {
+        const int i = j * S::kWarps + warp;
+        const uint64_t own = __shfl_sync(0xffffffffu, mask, j);
+        const uint64_t seen = i < r.n ? (own & ((1ull << i) - 1)) | 1ull << i : 0;
+        const bool s0 = seen >> (2 * lane) & 1, s1 = seen >> (2 * lane + 1) & 1;
+        const float x1 = s1 ? g1 : 0.f;
+        float sum = (s0 ? g0 : 0.f) + x1;
 #pragma unroll
-    for (int m = 1; m < S::kNodes / 2; m <<= 1) {
-      const float down = __shfl_down_sync(0xffffffffu, sum, m);
-      if (lane + m < 32) sum += down;
-    }
-    float after = __shfl_down_sync(0xffffffffu, sum, 1);        // of all nodes after the lane's
-    if (lane == 31) after = 0.f;
-    if (2 * lane < S::kNodes) *reinterpret_cast<float2*>(&weights[i * S::kWeights + 2 * lane]) = make_float2(s0 ? exp2_fast(after + x1) : -1.f, s1 ? exp2_fast(after) : -1.f);
-    if (lane == 0) {
-      whole[i] = exp2_fast(sum);
-      bits[i] = seen;
-    }
-  }
-#pragma unroll
-  for (int i = 0; i < kPieces; ++i) {
-    const int at = i * S::kThreads + tid, node = at / (D / 8), e = at % (D / 8) * 8;
-    if (S::kNodes * D / 8 % S::kThreads != 0 && node >= S::kNodes) break;
-    uint32_t v[4] = {piece[2][i].x, piece[2][i].y, piece[2][i].z, piece[2][i].w};
-    const uint32_t m = 0x7f807f80u, one = 0x00800080u;          // (an exponent of ones and one more carry into the sign's place)
-    if ((((v[0] & m) + one) | ((v[1] & m) + one) | ((v[2] & m) + one) | ((v[3] & m) + one)) & 0x80008000u) {
-      // values that are not finite stay out of the product, where they would reach nodes that do not see them
-#pragma unroll
-      for (int j = 0; j < 8; ++j)
-        if (const uint32_t x = v[j >> 1] >> (16 * (j & 1)); (x & 0x7f80u) == 0x7f80u) {
-          v[j >> 1] &= j & 1 ? 0x0000ffffu : 0xffff0000u;
-          atomicOr(reinterpret_cast<unsigned long long*>(&odd[e + j]), 1ull << node);
+        for (int m = 1; m < S::kNodes / 2; m <<= 1) {
+          const float down = __shfl_down_sync(0xffffffffu, sum, m);
+          if (lane + m < 32) sum += down;
         }
-      *any_odd = 1;
-    }
-    *reinterpret_cast<uint4*>(qs + node * S::kRow + e) = piece[0][i];
-    *reinterpret_cast<uint4*>(ks + node * S::kRow + e) = piece[1][i];
-    // column 32 a + 4 x + j at 32 a + 8 j + x, the order of the state's columns
-    __nv_bfloat16* to = vs + node * S::kRow + (e & ~31) + (e >> 2 & 7);
-    *reinterpret_cast<uint32_t*>(to) = __byte_perm(v[0], v[2], 0x5410);
-    *reinterpret_cast<uint32_t*>(to + 8) = __byte_perm(v[0], v[2], 0x7632);
-    *reinterpret_cast<uint32_t*>(to + 16) = __byte_perm(v[1], v[3], 0x5410);
-    *reinterpret_cast<uint32_t*>(to + 24) = __byte_perm(v[1], v[3], 0x7632);
-  }
-  __syncthreads();
-  if (kTiles == 1) ask_rows(next);
-
-  // ---- weighted scores, 16 nodes x 8 earlier ones at a time, as two bf16 numbers in the weights' place
-  constexpr int kPairs = kTiles * (kTiles + 1);
-  for (int u = warp; u < kPairs; u += S::kWarps) {
-    int tile = 0;
-    while ((tile + 1) * (tile + 2) <= u) ++tile;
-    const int first = (u - tile * (tile + 1)) * 8;
-    if (16 * tile >= r.n) break;
-    float s[4] = {0.f, 0.f, 0.f, 0.f}, s2[4] = {0.f, 0.f, 0.f, 0.f};   // two chains of products
-    const __nv_bfloat16 *q = qs + (16 * tile + g) * S::kRow + 2 * t, *k_at = ks + (first + g) * S::kRow + 2 * t;
-#pragma unroll
-    for (int k = 0; k < D; k += 16) {
-      const uint32_t a[4] = {lds(q + k), lds(q + k + 8 * S::kRow), lds(q + k + 8), lds(q + k + 8 * S::kRow + 8)};
-      mma(k & 16 ? s2 : s, a, lds(k_at + k), lds(k_at + k + 8));
-    }
-#pragma unroll
-    for (int e = 0; e < 4; ++e) s[e] += s2[e];
-#pragma unroll
-    for (int e = 0; e < 2; ++e) {
-      float2* at = reinterpret_cast<float2*>(&weights[(16 * tile + g + 8 * e) * S::kWeights + first + 2 * t]);
-      const float2 w = *at;
-      uint32_t high, low;
-      split(w.x < 0.f ? 0.f : s[2 * e] * w.x, w.y < 0.f ? 0.f : s[2 * e + 1] * w.y, high, low);
-      *at = make_float2(__uint_as_float(high), __uint_as_float(low));
-    }
-  }
-
-  // ---- what the nodes read of the state
-  float acc[kTiles][4][4];
-#pragma unroll
-  for (int i = 0; i < kTiles; ++i)
-#pragma unroll
-    for (int j = 0; j < 4; ++j)
-#pragma unroll
-      for (int e = 0; e < 4; ++e) acc[i][j][e] = 0.f;
-  if (r.in >= 0) {
-#pragma unroll
-    for (int k = 0; k < kSteps; ++k) {
-      uint32_t high[4][2], low[4][2];
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const float4 x = state[k][2 * i], y = state[k][2 * i + 1];
-        split(x.x, y.x, high[0][i], low[0][i]);
-        split(x.y, y.y, high[1][i], low[1][i]);
-        split(x.z, y.z, high[2][i], low[2][i]);
-        split(x.w, y.w, high[3][i], low[3][i]);
+        float after = __shfl_down_sync(0xffffffffu, sum, 1);        // of all nodes after the lane's
+        if (lane == 31) after = 0.f;
+        if (2 * lane < S::kNodes) *reinterpret_cast<float2*>(&weights[i * S::kWeights + 2 * lane]) = make_float2(s0 ? exp2_fast(after + x1) : -1.f, s1 ? exp2_fast(after) : -1.f);
+        if (lane == 0) {
+          whole[i] = exp2_fast(sum);
+          bits[i] = seen;
+        }
       }
 #pragma unroll
-      for (int i = 0; i < kTiles; ++i) {
-        const __nv_bfloat16* q = qs + (16 * i + g) * S::kRow + row0 + 16 * k + 2 * t;
-        const uint32_t a[4] = {lds(q), lds(q + 8 * S::kRow), lds(q + 8), lds(q + 8 * S::kRow + 8)};
+      for (int i = 0; i < kPieces; ++i) {
+        const int at = i * S::kThreads + tid, node = at / (D / 8), e = at % (D / 8) * 8;
+        if (S::kNodes * D / 8 % S::kThreads != 0 && node >= S::kNodes) break;
+        uint32_t v[4] = {piece[2][i].x, piece[2][i].y, piece[2][i].z, piece[2][i].w};
+        const uint32_t m = 0x7f807f80u, one = 0x00800080u;          // (an exponent of ones and one more carry into the sign's place)
+        if ((((v[0] & m) + one) | ((v[1] & m) + one) | ((v[2] & m) + one) | ((v[3] & m) + one)) & 0x80008000u) {
+          // values that are not finite stay out of the product, where they would reach nodes that do not see them
 #pragma unroll
-        for (int j = 0; j < 4; ++j) mma(acc[i][j], a, low[j][0], low[j][1]);
-#pragma unroll
-        for (int j = 0; j < 4; ++j) mma(acc[i][j], a, high[j][0], high[j][1]);
+          for (int j = 0; j < 8; ++j)
+            if (const uint32_t x = v[j >> 1] >> (16 * (j & 1)); (x & 0x7f80u) == 0x7f80u) {
+              v[j >> 1] &= j & 1 ? 0x0000ffffu : 0xffff0000u;
+              atomicOr(reinterpret_cast<unsigned long long*>(&odd[e + j]), 1ull << node);
+            }
+          *any_odd = 1;
+        }
+        *reinterpret_cast<uint4*>(qs + node * S::kRow + e) = piece[0][i];
+        *reinterpret_cast<uint4*>(ks + node * S::kRow + e) = piece[1][i];
+        // column 32 a + 4 x + j at 32 a + 8 j + x, the order of the state's columns
+        __nv_bfloat16* to = vs + node * S::kRow + (e & ~31) + (e >> 2 & 7);
+        *reinterpret_cast<uint32_t*>(to) = __byte_perm(v[0], v[2], 0x5410);
+        *reinterpret_cast<uint32_t*>(to + 8) = __byte_perm(v[0], v[2], 0x7632);
+        *reinterpret_cast<uint32_t*>(to + 16) = __byte_perm(v[1], v[3], 0x5410);
+        *reinterpret_cast<uint32_t*>(to + 24) = __byte_perm(v[1], v[3], 0x7632);
       }
-    }
-#pragma unroll
-    for (int i = 0; i < kTiles; ++i) {
-      const float f0 = whole[16 * i + g], f1 = whole[16 * i + g + 8];
-#pragma unroll
-      for (int j = 0; j < 4; ++j) acc[i][j][0] *= f0, acc[i][j][1] *= f0, acc[i][j][2] *= f1, acc[i][j][3] *= f1;
-    }
-  }
-  if (kEarly) ask_state(next);
-  __syncthreads();
+      __syncthreads();
+      if (kTiles == 1) ask_rows(next);
 
-  // ---- weighted scores x values, 16 earlier nodes at a time, taken in turns by the warps of the same columns
+      // ---- weighted scores, 16 nodes x 8 earlier ones at a time, as two bf16 numbers in the weights' place
+      constexpr int kPairs = kTiles * (kTiles + 1);
+      for (int u = warp; u < kPairs; u += S::kWarps) {
+        int tile = 0;
+        while ((tile + 1) * (tile + 2) <= u) ++tile;
+        const int first = (u - tile * (tile + 1)) * 8;
+        if (16 * tile >= r.n) break;
+        float s[4] = {0.f, 0.f, 0.f, 0.f}, s2[4] = {0.f, 0.f, 0.f, 0.f};   // two chains of products
+        const __nv_bfloat16 *q = qs + (16 * tile + g) * S::kRow + 2 * t, *k_at = ks + (first + g) * S::kRow + 2 * t;
 #pragma unroll
-  for (int from = 0; from < kTiles; ++from) {
-    if ((from & 1 ? from ^ 2 : from) % S::kSplits != part && kTiles > 1) continue;
-    if (kTiles == 1 && part != 0) continue;
-    if (16 * from >= r.n) continue;
-    uint32_t v[2][4];                                           // each: two tiles of 8 columns
+        for (int k = 0; k < D; k += 16) {
+          const uint32_t a[4] = {lds(q + k), lds(q + k + 8 * S::kRow), lds(q + k + 8), lds(q + k + 8 * S::kRow + 8)};
+          mma(k & 16 ? s2 : s, a, lds(k_at + k), lds(k_at + k + 8));
+        }
 #pragma unroll
-    for (int j = 0; j < 2; ++j) ldmatrix_trans(v[j], smem_at(vs + (16 * from + (lane & 15)) * S::kRow + col0 + 16 * j + 8 * (lane >> 4)));
+        for (int e = 0; e < 4; ++e) s[e] += s2[e];
 #pragma unroll
-    for (int i = from; i < kTiles; ++i) {
-      uint2 w[4];
-#pragma unroll
-      for (int e = 0; e < 4; ++e)
-        w[e] = *reinterpret_cast<const uint2*>(&weights[(16 * i + g + 8 * (e & 1)) * S::kWeights + 16 * from + 2 * t + 8 * (e >> 1)]);
-      const uint32_t high[4] = {w[0].x, w[1].x, w[2].x, w[3].x}, low[4] = {w[0].y, w[1].y, w[2].y, w[3].y};
-#pragma unroll
-      for (int j = 0; j < 4; ++j) mma(acc[i][j], low, v[j >> 1][2 * (j & 1)], v[j >> 1][2 * (j & 1) + 1]);
-#pragma unroll
-      for (int j = 0; j < 4; ++j) mma(acc[i][j], high, v[j >> 1][2 * (j & 1)], v[j >> 1][2 * (j & 1) + 1]);
-    }
-  }
+        for (int e = 0; e < 2; ++e) {
+          float2* at = reinterpret_cast<float2*>(&weights[(16 * tile + g + 8 * e) * S::kWeights + first + 2 * t]);
+          const float2 w = *at;
+          uint32_t high, low;
+          split(w.x < 0.f ? 0.f : s[2 * e] * w.x, w.y < 0.f ? 0.f : s[2 * e + 1] * w.y, high, low);
+          *at = make_float2(__uint_as_float(high), __uint_as_float(low));
+        }
+      }
 
-  if (!kEarly) ask_state(next);
-
-  // ---- the parts together; a thread's columns: col0 + 8 t .. + 7 of rows g and g + 8 of each tile
-  const bool bad = *any_odd;
-#pragma unroll
-  for (int turn = S::kSplits - 1; turn >= 0; --turn) {
-    if (part == turn)
+      // ---- what the nodes read of the state
+      float acc[kTiles][4][4];
 #pragma unroll
       for (int i = 0; i < kTiles; ++i)
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          const int node = 16 * i + g + 8 * e, col = col0 + 8 * t;
-          float4* at = reinterpret_cast<float4*>(&sums[node * S::kSums + col]);
-          float x[8] = {acc[i][0][2 * e], acc[i][1][2 * e], acc[i][2][2 * e], acc[i][3][2 * e],
-                        acc[i][0][2 * e + 1], acc[i][1][2 * e + 1], acc[i][2][2 * e + 1], acc[i][3][2 * e + 1]};
-          if (turn < S::kSplits - 1) {
-            const float4 a = at[0], c = at[1];
-            x[0] += a.x, x[1] += a.y, x[2] += a.z, x[3] += a.w, x[4] += c.x, x[5] += c.y, x[6] += c.z, x[7] += c.w;
+        for (int j = 0; j < 4; ++j)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) acc[i][j][e] = 0.f;
+      if (r.in >= 0) {
+#pragma unroll
+        for (int k = 0; k < kSteps; ++k) {
+          uint32_t high[4][2], low[4][2];
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            const float4 x = state[k][2 * i], y = state[k][2 * i + 1];
+            split(x.x, y.x, high[0][i], low[0][i]);
+            split(x.y, y.y, high[1][i], low[1][i]);
+            split(x.z, y.z, high[2][i], low[2][i]);
+            split(x.w, y.w, high[3][i], low[3][i]);
           }
-          if (turn > 0) {
-            at[0] = make_float4(x[0], x[1], x[2], x[3]);
-            at[1] = make_float4(x[4], x[5], x[6], x[7]);
-          } else if (node < r.n) {
-            if (bad)
 #pragma unroll
-              for (int j = 0; j < 8; ++j)
-                if (odd[col + j] & bits[node]) x[j] = __int_as_float(0x7fffffff);
+          for (int i = 0; i < kTiles; ++i) {
+            const __nv_bfloat16* q = qs + (16 * i + g) * S::kRow + row0 + 16 * k + 2 * t;
+            const uint32_t a[4] = {lds(q), lds(q + 8 * S::kRow), lds(q + 8), lds(q + 8 * S::kRow + 8)};
 #pragma unroll
-            for (int j = 0; j < 8; ++j) x[j] *= p.scale;
-            *reinterpret_cast<uint4*>(p.out + (int64_t)(r.row0 + node) * p.ldo + (int64_t)r.h * D + col) =
-                make_uint4(pack(x[0], x[1]), pack(x[2], x[3]), pack(x[4], x[5]), pack(x[6], x[7]));
+            for (int j = 0; j < 4; ++j) mma(acc[i][j], a, low[j][0], low[j][1]);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) mma(acc[i][j], a, high[j][0], high[j][1]);
           }
         }
-    if (turn > 0 || !S::kApart) __syncthreads();
-  }
-  if (bad) {                                                    // (of all threads)
-    __syncthreads();
-    for (int i = tid; i < D; i += S::kThreads) odd[i] = 0;
-    if (tid == 0) *any_odd = 0;
-    __syncthreads();
-  }
-  if (kTiles > 1) ask_rows(next);
-  } else {
-    ask_state(next);
-    ask_rows(next);
-  }
-  r = next;
+#pragma unroll
+        for (int i = 0; i < kTiles; ++i) {
+          const float f0 = whole[16 * i + g], f1 = whole[16 * i + g + 8];
+#pragma unroll
+          for (int j = 0; j < 4; ++j) acc[i][j][0] *= f0, acc[i][j][1] *= f0, acc[i][j][2] *= f1, acc[i][j][3] *= f1;
+        }
+      }
+      if (kEarly) ask_state(next);
+      __syncthreads();
+
+      // ---- weighted scores x values, 16 earlier nodes at a time, taken in turns by the warps of the same columns
+#pragma unroll
+      for (int from = 0; from < kTiles; ++from) {
+        if ((from & 1 ? from ^ 2 : from) % S::kSplits != part && kTiles > 1) continue;
+        if (kTiles == 1 && part != 0) continue;
+        if (16 * from >= r.n) continue;
+        uint32_t v[2][4];                                           // each: two tiles of 8 columns
+#pragma unroll
+        for (int j = 0; j < 2; ++j) ldmatrix_trans(v[j], smem_at(vs + (16 * from + (lane & 15)) * S::kRow + col0 + 16 * j + 8 * (lane >> 4)));
+#pragma unroll
+        for (int i = from; i < kTiles; ++i) {
+          uint2 w[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            w[e] = *reinterpret_cast<const uint2*>(&weights[(16 * i + g + 8 * (e & 1)) * S::kWeights + 16 * from + 2 * t + 8 * (e >> 1)]);
+          const uint32_t high[4] = {w[0].x, w[1].x, w[2].x, w[3].x}, low[4] = {w[0].y, w[1].y, w[2].y, w[3].y};
+#pragma unroll
+          for (int j = 0; j < 4; ++j) mma(acc[i][j], low, v[j >> 1][2 * (j & 1)], v[j >> 1][2 * (j & 1) + 1]);
+#pragma unroll
+          for (int j = 0; j < 4; ++j) mma(acc[i][j], high, v[j >> 1][2 * (j & 1)], v[j >> 1][2 * (j & 1) + 1]);
+        }
+      }
+
+      if (!kEarly) ask_state(next);
+
+      // ---- the parts together; a thread's columns: col0 + 8 t .. + 7 of rows g and g + 8 of each tile
+      const bool bad = *any_odd;
+#pragma unroll
+      for (int turn = S::kSplits - 1; turn >= 0; --turn) {
+        if (part == turn)
+#pragma unroll
+          for (int i = 0; i < kTiles; ++i)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              const int node = 16 * i + g + 8 * e, col = col0 + 8 * t;
+              float4* at = reinterpret_cast<float4*>(&sums[node * S::kSums + col]);
+              float x[8] = {acc[i][0][2 * e], acc[i][1][2 * e], acc[i][2][2 * e], acc[i][3][2 * e],
+                            acc[i][0][2 * e + 1], acc[i][1][2 * e + 1], acc[i][2][2 * e + 1], acc[i][3][2 * e + 1]};
+              if (turn < S::kSplits - 1) {
+                const float4 a = at[0], c = at[1];
+                x[0] += a.x, x[1] += a.y, x[2] += a.z, x[3] += a.w, x[4] += c.x, x[5] += c.y, x[6] += c.z, x[7] += c.w;
+              }
+              if (turn > 0) {
+                at[0] = make_float4(x[0], x[1], x[2], x[3]);
+                at[1] = make_float4(x[4], x[5], x[6], x[7]);
+              } else if (node < r.n) {
+                if (bad)
+#pragma unroll
+                  for (int j = 0; j < 8; ++j)
+                    if (odd[col + j] & bits[node]) x[j] = __int_as_float(0x7fffffff);
+#pragma unroll
+                for (int j = 0; j < 8; ++j) x[j] *= p.scale;
+                *reinterpret_cast<uint4*>(p.out + (int64_t)(r.row0 + node) * p.ldo + (int64_t)r.h * D + col) =
+                    make_uint4(pack(x[0], x[1]), pack(x[2], x[3]), pack(x[4], x[5]), pack(x[6], x[7]));
+              }
+            }
+        if (turn > 0 || !S::kApart) __syncthreads();
+      }
+      if (bad) {                                                // (of all threads)
+        __syncthreads();
+        for (int i = tid; i < D; i += S::kThreads) odd[i] = 0;
+        if (tid == 0) *any_odd = 0;
+        __syncthreads();
+      }
+      if (kTiles > 1) ask_rows(next);
+    } else {
+      ask_state(next);
+      ask_rows(next);
+    }
+    r = next;
   }
 }
 
@@ -339,6 +339,7 @@ cudaError_t launch(const LinearParams& p, int dev, cudaStream_t s) {
 }
 template <int D>
 cudaError_t launch(const LinearParams& p, int dev, cudaStream_t s) {
+  // as few tiles as the nodes need (48 requests of 32 heads, 16 nodes: one tile 40 us, two 53, four 71; 32 nodes: two 61, four 77)
   if (p.max_new <= 16) return launch<D, 1>(p, dev, s);
   return p.max_new <= 32 ? launch<D, 2>(p, dev, s) : launch<D, 4>(p, dev, s);
 }
