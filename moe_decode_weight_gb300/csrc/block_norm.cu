@@ -6,7 +6,8 @@
 // What bounds it is memory for many rows and the two chains load - sum - exchange for few. A row lies in the
 // registers of its threads, eight neighbouring elements (16 or 32 bytes of a load) at a time, so it is read once; the norms are
 // sums over the row's warps. Rows that are not on 16-byte boundaries are read by the aligned pieces around them and shifted in registers.
-// Measured: 16,381 rows of 2,560 elements with an fp32 residual 76 us (6.6 TB/s), gated norms of 4,099 rows of 32 heads 24 us (4.1 TB/s).
+// Measured: 16,381 rows of 2,560 elements with an fp32 residual 76 us (6.6 TB/s), gated norms of 4,099 rows of 32 heads 23 us (4.4
+// TB/s: there the conversions and sigmoids take 70 % of the issue slots).
 #include <cmath>
 #include <type_traits>
 
@@ -126,8 +127,8 @@ template <typename T, bool kAligned> __device__ __forceinline__ void store_row(v
   }
 }
 
-// Off by a few 2^-22: the exponential and the reciprocal take one instruction each (with the exact ones the gated norm of 4,099
-// rows of 32 heads took 39 us).
+// Off by a few 2^-22, and 0 below 2^-126: the exponential and the reciprocal take one instruction each (with the exact ones the
+// gated norm of 4,099 rows of 32 heads took 39 us).
 __device__ __forceinline__ float sigmoid(float x) {
   float e, r;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(x * -1.4426950408889634f));
@@ -216,24 +217,30 @@ __global__ void __launch_bounds__(kMaxThreads) norm_kernel(const NormParams p) {
     for (int i = 0; i < kPieces; ++i) {
       float g[8];
       gate[i].get(g);
+      if (p.gate_kind != MDW_GATE_MUL)                          // (first: times the gate alone could overflow)
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const float act = p.gate_kind == MDW_GATE_MUL ? 1.f : sigmoid(g[j]);
-        z[i][j] *= p.gate_kind == MDW_GATE_SIGMOID ? act : g[j] * act;
-      }
+        for (int j = 0; j < 8; ++j) z[i][j] *= sigmoid(g[j]);
+      if (p.gate_kind != MDW_GATE_SIGMOID)
+#pragma unroll
+        for (int j = 0; j < 8; ++j) z[i][j] *= g[j];
     }
   float ss = 0.f;
 #pragma unroll
   for (int i = 0; i < kPieces; ++i) {
-    float old[8];
-    r[i].get(old);
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      float s = p.branch_scale * z[i][j];
-      if (p.residual) s = fmaf(p.residual_scale, old[j], s);
-      z[i][j] = p.x ? Elem<S>::to_float(Elem<S>::from_float(s)) : s;
-      ss = fmaf(z[i][j], z[i][j], ss);
+    for (int j = 0; j < 8; ++j) z[i][j] *= p.branch_scale;
+    if (p.residual) {
+      float old[8];
+      r[i].get(old);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) z[i][j] = fmaf(p.residual_scale, old[j], z[i][j]);
     }
+    if (p.x)
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        z[i][j] = Elem<S>::to_float(Elem<S>::from_float(z[i][j]));
+        ss = fmaf(z[i][j], z[i][j], ss);
+      }
     if (p.sum) store_row<S, kVector>(p.sum, row * p.lds, place(i), p.width, has(i), z[i]);
   }
   if (!p.x) return;

@@ -625,6 +625,25 @@ def test_norm_parts(post, kind, res, pre):
     check_norm(a, branch_scale=2.0)
 
 
+@pytest.mark.parametrize("kind", ["mul", "sigmoid", "silu"])
+def test_norm_gates_of_all_sizes(kind):
+    """Gates whose exponentials overflow or vanish: a product with the gate alone would be infinite times zero."""
+    values = [-3e38, -1e5, -200.0, -89.0, -88.0, -30.0, -1e-30, 0.0, 1e-30, 30.0, 88.0, 200.0, 1e5, 3e38]
+    a = norm_case(2, 3, 16 * len(values), post=False, kind=kind, pre=False)
+    a["y"].clamp_(-0.5, 0.5)
+    a["y"][:, ::2] *= 1.0 if kind == "mul" else -1.0
+    a["gate"].copy_(torch.tensor(values, device="cuda").repeat_interleave(16).to(BF).expand(3, -1))
+    with np.errstate(over="ignore"):
+        api.mdw_block_norm(**a)
+        check_norm(a)
+    if kind == "silu":
+        b = norm_case(2, 1, 16, post=False, kind=kind, pre=False)
+        b["y"].fill_(2.0 ** 100)
+        b["gate"].fill_(-2.0 ** 100)
+        api.mdw_block_norm(**b)
+        assert (b["sum"] == 0).all()
+
+
 def test_norm_without_the_sum():
     a = norm_case(2, 3, 640, BF, None, None, True, "none", True, BF, True)
     b = dict(a)
