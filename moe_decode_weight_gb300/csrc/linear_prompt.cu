@@ -19,8 +19,8 @@
 // What bounds it: neither memory (42 to 50 % of the copy rate) nor the matrix unit (33 %) nor the issue of instructions (39 %), but
 // the chain of a chunk: the outputs of the last one read the state, the state takes its products and is rounded, the tile of q is
 // free and filled again, scores, weights, products with the values. It takes 6,000 to 7,000 cycles and only parts of two chunks overlap;
-// heads whose decays pass 2^-60 within a chunk pay 2,400 more to scale q. Measured: 16,301 rows of 32 heads from an empty state 216 us
-// (first pass 45, sums 9, outputs 150), 24 requests of up to 2,100 rows of 20 heads 148 us. Roles of a block:
+// heads whose decays pass 2^-60 within a chunk wait for q to be scaled too. Measured: 16,301 rows of 32 heads from an empty state 190 us
+// (of them the first pass 45, its sums 9), 24 requests of up to 2,100 rows of 20 heads 131 us. Roles of a block:
 //   warp 0       requests the tiles of q, k and v by TMA (swizzled, 128 rows x 128 bytes)
 //   warp 1       issues the products for the state
 //   warp 2       sums the decays of the next chunk
@@ -76,6 +76,13 @@ __device__ __forceinline__ Pair unpack(uint32_t v) { return Pair(__uint_as_float
 __device__ __forceinline__ uint32_t pack(Pair a) {
   const float2 f = a.floats();
   return pack(f.x, f.y);
+}
+
+// Products of two pairs of bf16 numbers.
+__device__ __forceinline__ uint32_t times(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
 }
 
 // A sum of log decays in two fp32 numbers, 48 bits: only differences of sums are used, and those of long ones would lose their digits.
@@ -573,22 +580,26 @@ prompt_kernel(const LinearParams p, const LinearPlan w, const __grid_constant__ 
           if (!sums.strong) arrive(q_ok);
           wait(s_full, g & 1);
           tc_fence_after();
-          float v[32];
-          tc_ld32(v, tmem + lanes);
           if (sums.strong) {
+            // (before the scores take their registers, four loads at a time: one, four, eight at a time 216, 190, 198 us for 16,301 rows)
             const float down = rintf(sums.base[own] + sums.d[row] + sums.lift[row]);
             if (down < 0.f) {
-              const float f = exp2f(down);
+              const uint32_t f = pack(exp2f(down), exp2f(down));
 #pragma unroll 1
-              for (int i = 0; i < D / 8; ++i) {
-                const uint32_t at = base + S::kQ + (i >> 3) * (kChunk * 128) + row * 128 + (((i & 7) ^ (row & 7)) << 4);
-                const uint4 x = lds16(at);
-                sts16(at, make_uint4(pack(unpack(x.x) * Pair(f, f)), pack(unpack(x.y) * Pair(f, f)), pack(unpack(x.z) * Pair(f, f)), pack(unpack(x.w) * Pair(f, f))));
+              for (int i = 0; i < D / 8; i += 4) {
+                auto at = [&](int i) { return base + S::kQ + (i >> 3) * (kChunk * 128) + row * 128 + (((i & 7) ^ (row & 7)) << 4); };
+                uint4 x[4];
+#pragma unroll
+                for (int j = 0; j < 4; ++j) x[j] = lds16(at(i + j));
+#pragma unroll
+                for (int j = 0; j < 4; ++j) sts16(at(i + j), make_uint4(times(x[j].x, f), times(x[j].y, f), times(x[j].z, f), times(x[j].w, f)));
               }
             }
             fence_async_proxy();
             arrive(q_ok);
           }
+          float v[32];
+          tc_ld32(v, tmem + lanes);
           const float d = sums.d[row] + sums.lift[row];
           tc_wait_ld();
 #pragma unroll 1
