@@ -140,11 +140,14 @@ __device__ __forceinline__ float sigmoid(float x) {
 // elements: 18 and 16). Rows off 16-byte boundaries take more registers a piece and are spread over more threads, up to 8,192 elements one
 // piece each (16,381 rows of 2,563 elements: two pieces 195 us, one 144).
 constexpr int kMaxThreads = 1024;
+// Registers: 64, or 56 for one piece off 16-byte boundaries, so that one more block fits an SM (fp32 y, f16 residual: 4,617 rows of 4,374 elements 105
+// and 75 us, 16,381 of 2,563 204 and 173, 7,000 of 6,001 214 and 222; with 48 they spill: 77, 179, 235).
+constexpr int registers_of(bool vector, int pieces) { return vector || pieces == 2 ? 64 : 56; }
 
 // T: the 16-bit type; Y, S: types of y and of residual and sum. kPieces of eight elements a thread. kVector: all rows on 16-byte
 // boundaries, and whole pieces.
 template <typename T, typename Y, typename S, int kPieces, bool kVector>
-__global__ void __launch_bounds__(kMaxThreads) norm_kernel(const NormParams p) {
+__global__ void __maxnreg__(registers_of(kVector, kPieces)) norm_kernel(const NormParams p) {
   __shared__ float part[2][32];
   const int row = blockIdx.x * (blockDim.x / p.threads) + threadIdx.x / p.threads, tid = threadIdx.x % p.threads;
   const bool live = row < p.T;                                  // (rows share a block only where a row is a warp's)
