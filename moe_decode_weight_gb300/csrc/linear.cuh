@@ -31,6 +31,10 @@ struct LinearParams {
 // then cost 0.5 us (3 requests of 32 heads) to 5 us (48) each, and chunks of 128 rows as much for one row as for all: the two are even at
 // 20 rows of 3 requests (both 22 us), 16 of 8 (30 us), 11 of 48 (87 us; 16 rows one by one 110). A call of few rows is one launch then.
 constexpr int kLinearChunk = 128, kLinearShort = 16, kLinearSegment = 4, kLinearPieces = 3;
+// Calls of at most 16 rows a request, and possibly of so many, take the products on mma.sync instead of row by row: whatever the rows, 48 requests
+// of 32 heads 67 to 71 us (row by row 4 rows 52, 8 67, 12 87, 16 109), 10 26 (20, 26, 30, 35), one of 20 heads 13.5 (10, 11, 13, 15.5).
+// max_new is a bound only, and where the rows are fewer, row by row is as fast or faster; so not from 9 on.
+constexpr int kLinearWindow = 12;
 
 // A part of a request's rows, for all value heads, in the workspace.
 struct LinearEntry {
@@ -49,6 +53,8 @@ struct LinearPlan {
   float* logs;                     // [3 blocks] log decay of a piece, by set and head
   float* states;                   // [3 blocks][D][D] by set and head
 };
+// Requests of up to kLinearShort rows, by the kernel of linear_tree.cu.
+cudaError_t launch_windows(const LinearParams& p, int D, int dev, cudaStream_t s);
 cudaError_t launch_prompts(const LinearParams& p, const LinearPlan& w, int D, int grid, int dev, cudaStream_t s);
 
 // Rows [row0, row0 + n) and slots of a request.

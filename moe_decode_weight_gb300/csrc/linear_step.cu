@@ -1,4 +1,4 @@
-// mdw_linear_attention and mdw_linear_state_advance: one row after the other.
+// mdw_linear_attention (requests of few rows) and mdw_linear_state_advance: one row after the other.
 //
 // Mathematics. S <- e^g S + k v^T, o = scale S^T q, for a request's rows in order. The block of a request and value
 // head holds S in registers, so the state is read and written once whatever the number of rows.
@@ -259,7 +259,8 @@ extern "C" mdw_status mdw_linear_attention(const mdw_linear_state* state, int32_
                        slot_out, nullptr, status, scale, B, T, state->heads, state->heads / qk_heads, max_new, state->num_slots,
                        kLinearShort, chunks ? w.ok : nullptr, mdw_spin_budget()};
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  cudaError_t e = launch_step<true>(p, D, sms, s);
+  const bool windows = !chunks && max_new >= kLinearWindow;     // (linear.cuh)
+  cudaError_t e = windows ? launch_windows(p, D, current_device(), s) : launch_step<true>(p, D, sms, s);
   if (e == cudaSuccess && chunks) e = launch_prompts(p, w, D, sms, current_device(), s);
   return e == cudaSuccess ? MDW_OK : MDW_ERR_CUDA;
 }

@@ -1,4 +1,5 @@
-// mdw_linear_tree_attention: the nodes of trees of drafted tokens against a state that stays as it is.
+// mdw_linear_tree_attention: the nodes of trees of drafted tokens against a state that stays as it is; and mdw_linear_attention for
+// windows of 12 to 16 rows, as chains whose state is stored.
 //
 // Mathematics. Node i comes after the nodes j of its mask (itself among them). With e_ij the sum of the log decays of those of
 // them that come after j, and e_i that of all,
@@ -11,6 +12,7 @@
 // products of the same kind, the weights as two bf16 numbers too. A block asks for its next unit's state as soon as it has used up the
 // one before. Measured: 48 requests of up to 16 nodes and 32 heads 32 us, half of the copy rate; 12 requests of 64 nodes and 64 heads of 64 25 us,
 // where the split states, two products each, and the barriers between the steps of a unit bound it (16 warps an SM).
+// Windows of 16 rows, the same 48 requests: 71 us; the products for the state come between its use and the next one's loads.
 #include <cmath>
 
 #include "linear.cuh"
@@ -59,10 +61,11 @@ struct Shape {
   static constexpr int kV = 2 * kRow * 2 * kNodes, kSumsAt = kApart ? kV + kNodes * kRow * 2 : 0;
   static constexpr int kWeightsAt = kV + kNodes * kRow * 2 + (kApart ? kNodes * kSums * 4 : 0);
   static_assert(kApart || kSums * 4 <= 2 * kRow * 2, "");
-  static constexpr int kBits = kWeightsAt + kNodes * kWeights * 4, kSmem = kBits + kNodes * 12 + D * 8 + 16;
+  static constexpr int kBits = kWeightsAt + kNodes * kWeights * 4, kSmem = kBits + kNodes * 12 + D * 8 + 32 + kNodes * 4;
 };
 
-template <int D, int kTiles>
+// kStore: the nodes are a chain, and the state after them goes to slot_out.
+template <int D, int kTiles, bool kStore>
 __global__ void __launch_bounds__(Shape<D, kTiles>::kThreads, Shape<D, kTiles>::kResident) tree_kernel(const LinearParams p) {
   using S = Shape<D, kTiles>;
   extern __shared__ __align__(16) uint8_t smem[];
@@ -75,19 +78,27 @@ __global__ void __launch_bounds__(Shape<D, kTiles>::kThreads, Shape<D, kTiles>::
   uint64_t* odd = bits + S::kNodes;                             // per column the nodes whose value is not finite
   float* whole = reinterpret_cast<float*>(odd + D);             // e^{e_i}
   int* any_odd = reinterpret_cast<int*>(whole + S::kNodes);
+  float* decay = reinterpret_cast<float*>(any_odd + 4);         // of all rows: factor, and 1 if it is given less 1
+  float* rest = decay + 4;                                      // from a row to the end
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3, units = p.B * p.H;
 
   // ---- requests: a block has several units (request, head), and asks for the next one's data as soon as it has room for it
   struct Unit {
-    int row0, n, in, h;                                         // n = 0: nothing to do
+    int row0, n, in, h, out;                                    // n = 0 and out < 0: nothing to do
   };
   auto look = [&](int u) {
-    Unit r{0, 0, -1, 0};
+    Unit r{0, 0, -1, 0, -1};
     if (u >= units) return r;
-    const int b = u / p.H, end = p.row_start[b + 1];
+    const int b = u / p.H;
+    r.h = u - b * p.H;
+    if (kStore) {
+      LinearRequest x;
+      if (linear_request(p, b, x) && (x.n > 0 || x.out >= 0)) r.row0 = x.row0, r.n = x.n, r.in = x.in, r.out = x.out;
+      return r;
+    }
+    const int end = p.row_start[b + 1];
     r.row0 = p.row_start[b];
     r.in = p.slot_in[b];
-    r.h = u - b * p.H;
     const bool bad = r.row0 < 0 || end < r.row0 || end > p.T || r.in < -1 || r.in >= p.num_slots || end - r.row0 > p.max_new;
     r.n = bad ? 0 : end - r.row0;
     if (bad && tid == 0) raise_status(p.status, MDW_ERR_DEVICE_BOUNDS);
@@ -98,12 +109,24 @@ __global__ void __launch_bounds__(Shape<D, kTiles>::kThreads, Shape<D, kTiles>::
   const int col0 = warp % S::kColumns * 32, part = warp / S::kColumns, row0 = part * (D / S::kSplits);
   float4 state[kSteps][4];
   auto ask_state = [&](const Unit& r) {
-    if (r.n == 0 || r.in < 0) return;
+    if (kStore && r.in < 0)
+#pragma unroll
+      for (int k = 0; k < kSteps; ++k)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) state[k][i] = make_float4(0.f, 0.f, 0.f, 0.f);
+    if ((r.n == 0 && r.out < 0) || r.in < 0) return;
     const float* src = p.s + r.in * p.slot_stride + (int64_t)r.h * D * D + (int64_t)(row0 + 2 * t) * D + col0 + 4 * g;
 #pragma unroll
     for (int k = 0; k < kSteps; ++k)
 #pragma unroll
       for (int i = 0; i < 4; ++i) state[k][i] = __ldg(reinterpret_cast<const float4*>(src + (16 * k + (i & 1) + 8 * (i >> 1)) * D));
+  };
+  auto store_state = [&](const Unit& r) {
+    float* dst = p.s + r.out * p.slot_stride + (int64_t)r.h * D * D + (int64_t)(row0 + 2 * t) * D + col0 + 4 * g;
+#pragma unroll
+    for (int k = 0; k < kSteps; ++k)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) __stcs(reinterpret_cast<float4*>(dst + (16 * k + (i & 1) + 8 * (i >> 1)) * D), state[k][i]);
   };
   // rows of q, k and v, zeros behind the last; two decays a lane; masks of a warp's rows, one a lane
   constexpr int kPieces = (S::kNodes * D / 8 + S::kThreads - 1) / S::kThreads, kMasks = S::kNodes / S::kWarps;   // of 8 elements, a thread
@@ -159,6 +182,14 @@ __global__ void __launch_bounds__(Shape<D, kTiles>::kThreads, Shape<D, kTiles>::
         if (lane == 0) {
           whole[i] = exp2_fast(sum);
           bits[i] = seen;
+        }
+        if (kStore && i == r.n - 1) {
+          if (2 * lane < S::kNodes) *reinterpret_cast<float2*>(&rest[2 * lane]) = make_float2(exp2f(after + x1), exp2f(after));
+          if (lane == 0) {
+            const Decay all(sum * 0.6931471805599453f);
+            decay[0] = all.f;
+            decay[1] = all.near ? 1.f : 0.f;
+          }
         }
       }
 #pragma unroll
@@ -252,6 +283,53 @@ __global__ void __launch_bounds__(Shape<D, kTiles>::kThreads, Shape<D, kTiles>::
           for (int j = 0; j < 4; ++j) acc[i][j][0] *= f0, acc[i][j][1] *= f0, acc[i][j][2] *= f1, acc[i][j][3] *= f1;
         }
       }
+      if (kStore && r.out >= 0) {
+        // ---- the state after the rows, columns x rows: a thread's numbers of the state are those of its sums, and the values that the
+        // outputs take as second operand are the first one here, times their decays in three bf16 numbers that hold all 24 bits
+        const float2 r0 = *reinterpret_cast<const float2*>(&rest[2 * t]), r1 = *reinterpret_cast<const float2*>(&rest[2 * t + 8]);
+        const float f = decay[0], same = decay[1];
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          uint32_t v[4], a[3][4];
+          ldmatrix_trans(v, smem_at(vs + (lane & 15) * S::kRow + col0 + 16 * j + 8 * (lane >> 4)));
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {                         // 8 columns and 8 rows: v[column half * 2 + row half], a[row half * 2 + column half]
+            Pair x = Pair(__uint_as_float(v[i] << 16), __uint_as_float(v[i] & 0xffff0000u)) * (i & 1 ? Pair(r1.x, r1.y) : Pair(r0.x, r0.y));
+#pragma unroll
+            for (int part = 0; part < 3; ++part) {
+              const uint32_t lo = __float_as_uint(x.floats().x), hi = __float_as_uint(x.floats().y);
+              a[part][(i & 1) * 2 + (i >> 1)] = __byte_perm(lo, hi, 0x7632);
+              x = fma(Pair(__uint_as_float(lo & 0xffff0000u), __uint_as_float(hi & 0xffff0000u)), Pair(-1.f, -1.f), x);
+            }
+          }
+#pragma unroll
+          for (int k = 0; k < kSteps; ++k) {
+            uint32_t b[4];                                      // 16 rows of the state: the first 8 of them, the others
+            ldmatrix_trans(b, smem_at(ks + (lane & 15) * S::kRow + row0 + 16 * k + 8 * (lane >> 4)));
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+              float add[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+              for (int part = 2; part >= 0; --part) mma(add, a[part], b[2 * i], b[2 * i + 1]);
+              auto next_of = [&](float& s, float x) { s = fmaf(s, same, fmaf(s, f, x)); };
+              float4 &s0 = state[k][2 * i], &s1 = state[k][2 * i + 1];
+              next_of(j ? s0.z : s0.x, add[0]);
+              next_of(j ? s1.z : s1.x, add[1]);
+              next_of(j ? s0.w : s0.y, add[2]);
+              next_of(j ? s1.w : s1.y, add[3]);
+            }
+          }
+        }
+        if (*any_odd)
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            if (odd[col0 + 4 * g + j])
+#pragma unroll
+              for (int k = 0; k < kSteps; ++k)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) (&state[k][i].x)[j] = __int_as_float(0x7fffffff);
+        store_state(r);
+      }
       if (kEarly) ask_state(next);
       __syncthreads();
 
@@ -321,6 +399,7 @@ __global__ void __launch_bounds__(Shape<D, kTiles>::kThreads, Shape<D, kTiles>::
       }
       if (kTiles > 1) ask_rows(next);
     } else {
+      if (kStore && r.out >= 0) store_state(r);
       ask_state(next);
       ask_rows(next);
     }
@@ -328,23 +407,28 @@ __global__ void __launch_bounds__(Shape<D, kTiles>::kThreads, Shape<D, kTiles>::
   }
 }
 
-template <int D, int kTiles>
+template <int D, int kTiles, bool kStore>
 cudaError_t launch(const LinearParams& p, int dev, cudaStream_t s) {
   using S = Shape<D, kTiles>;
-  const cudaError_t e = allow_shared_memory<tree_kernel<D, kTiles>>(dev);
+  const cudaError_t e = allow_shared_memory<tree_kernel<D, kTiles, kStore>>(dev);
   if (e != cudaSuccess) return e;
   const int64_t units = (int64_t)p.H * p.B, most = (int64_t)S::kResident * sm_count(dev);
-  tree_kernel<D, kTiles><<<(unsigned)(units < most ? units : most), S::kThreads, S::kSmem, s>>>(p);
+  tree_kernel<D, kTiles, kStore><<<(unsigned)(units < most ? units : most), S::kThreads, S::kSmem, s>>>(p);
   return cudaGetLastError();
 }
 template <int D>
 cudaError_t launch(const LinearParams& p, int dev, cudaStream_t s) {
   // as few tiles as the nodes need (48 requests of 32 heads, 16 nodes: one tile 40 us, two 53, four 71; 32 nodes: two 61, four 77)
-  if (p.max_new <= 16) return launch<D, 1>(p, dev, s);
-  return p.max_new <= 32 ? launch<D, 2>(p, dev, s) : launch<D, 4>(p, dev, s);
+  if (p.max_new <= 16) return launch<D, 1, false>(p, dev, s);
+  return p.max_new <= 32 ? launch<D, 2, false>(p, dev, s) : launch<D, 4, false>(p, dev, s);
 }
 
 }  // namespace
+
+cudaError_t launch_windows(const LinearParams& p, int D, int dev, cudaStream_t s) {
+  return D == 128 ? launch<128, 1, true>(p, dev, s) : launch<64, 1, true>(p, dev, s);
+}
+
 }  // namespace mdw
 
 using namespace mdw;

@@ -121,7 +121,7 @@ def check_rows(c, pool0, scale=None, skip=()):
 
 
 LENS = [[1], [1, 1, 1, 1, 1], [4, 0, 1, 7], [8, 9, 16, 17], [15, 31, 33, 1, 63], [64, 65, 127, 1], [128, 129, 0, 2], [255, 256, 257],
-        [300, 5, 700]]
+        [300, 5, 700], [16, 1, 0, 12], [13, 15, 2, 9, 0, 16, 14]]
 
 
 @pytest.mark.parametrize("lens", LENS, ids=str)
@@ -152,7 +152,7 @@ def test_a_bound_above_the_rows_changes_no_result_beyond_rounding(new):
     check_rows(c, before)
 
 
-@pytest.mark.parametrize("lens", [[5, 2, 30], [200, 140]], ids=str)
+@pytest.mark.parametrize("lens", [[5, 2, 30], [200, 140], [16, 12]], ids=str)
 def test_decays_that_forget(lens):
     """A decay of 0 forgets what was before, and the rows after it count on."""
     c = Case(3, lens, 2, 2, 128)
@@ -174,7 +174,7 @@ def test_scale(scale):
     check_rows(c, before, scale)
 
 
-@pytest.mark.parametrize("lens", [[2, 0, 3], [140, 0, 1, 200]], ids=str)
+@pytest.mark.parametrize("lens", [[2, 0, 3], [140, 0, 1, 200], [14, 0, 3]], ids=str)
 def test_states_not_stored_copied_and_elsewhere(lens):
     c = Case(6, lens, 1, 2, 128, inplace=False, fresh=(0,))
     c.slot_out[0] = -1
@@ -199,7 +199,7 @@ def test_two_requests_may_read_one_slot():
         check_rows(c, before)
 
 
-@pytest.mark.parametrize("lens", [[4, 3, 2, 5], [140, 3, 200, 150]], ids=str)
+@pytest.mark.parametrize("lens", [[4, 3, 2, 5], [140, 3, 200, 150], [14, 3, 12, 5]], ids=str)
 @pytest.mark.parametrize("fault,skip", [("out", (0, 2)), ("in", (0,)), ("high", (1,)), ("low", (2,)), ("rows", (3,)), ("back", (1, 2))])
 def test_bad_requests_are_skipped(lens, fault, skip):
     c = Case(8, lens, 2, 2, 64, inplace=False)
@@ -247,7 +247,7 @@ def test_too_many_rows_are_refused_on_the_device():
 
 @pytest.mark.parametrize("what", ["q", "k", "v"])
 @pytest.mark.parametrize("value", [float("inf"), float("nan")])
-@pytest.mark.parametrize("lens,row", [([6, 3], 4), ([6, 3], 0), ([300, 140], 190), ([140, 20], 0), ([129, 3], 128)], ids=str)
+@pytest.mark.parametrize("lens,row", [([6, 3], 4), ([6, 3], 0), ([16, 3], 4), ([13, 5], 12), ([300, 140], 190), ([140, 20], 0), ([129, 3], 128)], ids=str)
 def test_values_that_are_not_finite_reach_no_earlier_row(what, value, lens, row):
     c = Case(10, lens, 2, 2, 128, lead=2)
     clean = Case(10, lens, 2, 2, 128, lead=2)
@@ -284,7 +284,7 @@ def test_values_that_are_not_finite_reach_no_earlier_row(what, value, lens, row)
     assert np.isfinite(before).all()
 
 
-@pytest.mark.parametrize("lens", [[1, 3], [700, 1, 130]], ids=str)
+@pytest.mark.parametrize("lens", [[1, 3], [700, 1, 130], [16, 2, 13]], ids=str)
 def test_calls_repeat_bit_for_bit(lens):
     results = []
     for _ in range(3):
@@ -294,7 +294,7 @@ def test_calls_repeat_bit_for_bit(lens):
     assert all(torch.equal(a, b) for r in results[1:] for a, b in zip(r, results[0]))
 
 
-@pytest.mark.parametrize("lens", [[2, 3], [400, 1, 130]], ids=str)
+@pytest.mark.parametrize("lens", [[2, 3], [400, 1, 130], [12, 0, 15]], ids=str)
 def test_captured_calls_on_a_stream_of_their_own(lens):
     """Two captured calls with workspaces of their own replay on new inputs, as eager calls give them."""
     a, b = Case(12, lens, 2, 2, 128), Case(13, lens, 2, 2, 128)
@@ -434,6 +434,29 @@ def test_a_wait_that_runs_out(lens):
     c.call()
     check_rows(c, before)
     assert int(c.status) == 0
+
+
+@pytest.mark.parametrize("h,d,lens", [(40, 64, [16, 3, 12, 0] * 5), (32, 128, [1, 14, 15] * 4)], ids=str)
+def test_windows_of_many_heads(h, d, lens):
+    """More units than blocks, with requests without rows and from empty states among them."""
+    c = Case(23, lens, h // 2, h, d, fresh=(0, 3, 4), inplace=False)
+    before = host(c.pool)
+    c.call(new=16)
+    check_rows(c, before)
+    assert int(c.status) == 0
+
+
+def test_a_state_of_many_windows():
+    """Errors of 80 windows of 16 rows, with decays so slow that all of them count."""
+    n, d = 80, 64
+    c = Case(24, [16 * n], 1, 1, d, rate=0.0005, tail=0)
+    first = host(c.pool)
+    for i in range(n):
+        at = slice(16 * i, 16 * i + 16)
+        st = api.LinearState(c.pool)
+        ws = torch.empty(api.mdw_linear_attention_workspace_bytes(st, 1, 16, 1, 16), dtype=torch.uint8, device="cuda")
+        api.mdw_linear_attention(st, c.q[at], c.k[at], c.v[at], c.g[at], c.out[at], i32([0, 16]), i32(c.slot_in), i32(c.slot_out), 16, ws)
+    check_rows(c, first)
 
 
 # ------------------------------------------------------------------------------ trees
