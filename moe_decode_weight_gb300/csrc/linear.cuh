@@ -62,10 +62,10 @@ struct LinearRequest {
   int row0, n, in, out;
 };
 
-// Request b, read by all threads of a block together; not 0 (for some of them) if it has to be skipped. A slot that is
+// Request b, read by all threads of a block together; false (for all) if it has to be skipped. A slot that is
 // stored to by one request and read or stored to by another one would make results depend on timing, so every
 // block looks through the list of slots: B loads of 4 bytes from L2.
-__device__ __forceinline__ int look_at_request(const LinearParams& p, int b, LinearRequest& r) {
+__device__ __forceinline__ bool linear_request(const LinearParams& p, int b, LinearRequest& r) {
   r.row0 = p.row_start[b];
   const int end = p.row_start[b + 1];
   r.in = p.slot_in[b];
@@ -78,15 +78,11 @@ __device__ __forceinline__ int look_at_request(const LinearParams& p, int b, Lin
     }
   bad |= r.row0 < 0 || end < r.row0 || end > p.T || r.in < -1 || r.in >= p.num_slots || r.out < -1 || r.out >= p.num_slots;
   r.n = bad ? 0 : end - r.row0;
-  return bad | (r.n > p.max_new);
-}
-// What the block's threads make of it: false if the request has to be skipped.
-__device__ __forceinline__ bool settle_request(const LinearParams& p, int bad) {
+  bad |= r.n > p.max_new;
   bad = __syncthreads_or(bad);
   if (bad && threadIdx.x == 0) raise_status(p.status, MDW_ERR_DEVICE_BOUNDS);
   return !bad;
 }
-__device__ __forceinline__ bool linear_request(const LinearParams& p, int b, LinearRequest& r) { return settle_request(p, look_at_request(p, b, r)); }
 
 __device__ __forceinline__ float log_decay_of(const LinearParams& p, int row, int h) { return p.decay[(int64_t)row * p.ldd + h]; }
 

@@ -5,8 +5,8 @@
 //
 // What bounds it is the state's 64 KB (heads of 128) in and out of memory: D rows of it lie on the warps, four columns on a lane, and all
 // loads are requested before the first is used. Measured: 61 requests of 1 to 4 rows and 32 heads 50 us, where a plain copy of
-// their states takes 43 (a quarter of a warp's time goes to waiting for memory, as much to the barriers around the rows); one row of 20 heads 6
-// us with its launch. Blocks that stay and copy the next state to shared memory meanwhile took 57: two of them an SM, with the same barriers.
+// their states takes 43 (a quarter of a warp's time goes to waiting for memory, as much to the barriers around the rows; asking for the state before the
+// request is checked changed nothing); one row of 20 heads 6 us with its launch. Blocks that stay and copy the next state to shared memory meanwhile took 57: two of them an SM, with the same barriers.
 #include <algorithm>
 #include <cmath>
 #include <utility>
@@ -63,22 +63,19 @@ __global__ void __launch_bounds__(kThreads, D * kCols > 64 * 64 ? 3 : 4) step_ke
   if (kOut) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");   // (plan_kernel of longer requests waits for this one's end)
   const int c = tid % kLanes * 4, a0 = tid / kLanes * kPer;
   const int64_t at = ((int64_t)h * D + a0) * D + col0 + c;
-  // the state is asked for before the request is known to be sound, as soon as its slot is known to exist
   LinearRequest r;
-  const int bad = look_at_request(p, b, r);
-  const bool holds = r.in >= 0 && r.in < p.num_slots && (r.out >= 0 || kOut) && !(kOut && r.n > p.short_rows);
+  const bool sound = linear_request(p, b, r);
+  if (kOut && p.ok && blockIdx.x == 0 && h == 0 && tid == 0) p.ok[b] = sound;
+  if (!sound || (kOut && r.n > p.short_rows)) return;
+  if (r.out < 0 && !(kOut && r.n > 0)) return;
   Pair s[kPer][2];
 #pragma unroll
   for (int i = 0; i < kPer; ++i) {
     float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
-    if (holds) x = __ldcs(reinterpret_cast<const float4*>(p.s + r.in * p.slot_stride + at + i * D));
+    if (r.in >= 0) x = __ldcs(reinterpret_cast<const float4*>(p.s + r.in * p.slot_stride + at + i * D));
     s[i][0] = Pair(x.x, x.y);
     s[i][1] = Pair(x.z, x.w);
   }
-  const bool sound = settle_request(p, bad);
-  if (kOut && p.ok && blockIdx.x == 0 && h == 0 && tid == 0) p.ok[b] = sound;
-  if (!sound || (kOut && r.n > p.short_rows)) return;
-  if (r.out < 0 && !(kOut && r.n > 0)) return;
   uint64_t left = 0;                                            // accepted rows that are still to come
   if (!kOut) left = p.bits[b] & (r.n < 64 ? (1ull << r.n) - 1 : ~0ull);
   int next = 0;
