@@ -4,9 +4,10 @@
 // head holds S in registers, so the state is read and written once whatever the number of rows.
 //
 // What bounds it is the state's 64 KB (heads of 128) in and out of memory: D rows of it lie on the warps, four columns on a lane, and all
-// loads are requested before the first is used. Measured: 61 requests of 1 to 4 rows and 32 heads 50 us, where a plain copy of
-// their states takes 43 (a quarter of a warp's time goes to waiting for memory, as much to the barriers around the rows; asking for the state before the
-// request is checked changed nothing); one row of 20 heads 6 us with its launch. Blocks that stay and copy the next state to shared memory meanwhile took 57: two of them an SM, with the same barriers.
+// loads are requested before the first is used. Measured: 61 requests of 1 to 4 rows and 32 heads 51 us, where a plain copy of
+// their states takes 43 (a quarter of a warp's time goes to waiting for memory, as much to the barriers around the rows); one row of
+// 20 heads 6 us with its launch. Asking for the state before the request is checked changed nothing; blocks that stay and copy the next state
+// to shared memory meanwhile took 57: two of them an SM, with the same barriers.
 #include <algorithm>
 #include <cmath>
 #include <utility>

@@ -4,7 +4,7 @@
 // Mathematics. Node i comes after the nodes j of its mask (itself among them). With e_ij the sum of the log decays of those of
 // them that come after j, and e_i that of all,
 //   o_i = scale ( e^{e_i} S^T q_i + sum_{j in mask_i} e^{e_ij} (q_i . k_j) v_j ).
-// e_ij is summed from node i downwards, so a large sum never leaves a small difference.
+// e_ij is summed from node i downwards, so a large sum never leaves a small difference. Windows: S <- e^{e_n} S + sum_j k_j (e^{e_nj} v_j)^T too.
 //
 // What bounds it up to 16 nodes is the state's 64 KB (heads of 128) from memory, so a block requests all of it before
 // anything else: a thread's loads are whole operands of m16n8k16 products (four columns of it are four tiles' column, which
@@ -119,7 +119,10 @@ __global__ void __launch_bounds__(Shape<D, kTiles>::kThreads, Shape<D, kTiles>::
 #pragma unroll
     for (int k = 0; k < kSteps; ++k)
 #pragma unroll
-      for (int i = 0; i < 4; ++i) state[k][i] = __ldg(reinterpret_cast<const float4*>(src + (16 * k + (i & 1) + 8 * (i >> 1)) * D));
+      for (int i = 0; i < 4; ++i) {
+        const float4* at = reinterpret_cast<const float4*>(src + (16 * k + (i & 1) + 8 * (i >> 1)) * D);
+        state[k][i] = kStore ? __ldcs(at) : __ldg(at);          // (what is stored to is not read-only)
+      }
   };
   auto store_state = [&](const Unit& r) {
     float* dst = p.s + r.out * p.slot_stride + (int64_t)r.h * D * D + (int64_t)(row0 + 2 * t) * D + col0 + 4 * g;
