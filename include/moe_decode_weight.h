@@ -496,6 +496,8 @@ mdw_status mdw_tree_attention(const mdw_kv_cache* cache, int32_t B, int32_t T, i
  *     reads or stores to.
  *   - Row strides are at most 2^36 elements. Outputs overlap no input. Where a wait inside a kernel runs out
  *     (MDW_ERR_TIMEOUT), outputs and stored states of the call's requests of more than 16 rows are not defined.
+ *   - Range of requests of more than 16 rows: sums of the magnitudes |q_a k_a|, |q_a k_a v| and |q_a S| stay below 2^96; what such sums
+ *     have below 2^-96 may be lost. (Shorter ones, trees: what fp32 holds.)
  *   - States and sums are fp32, in a fixed order, which depends on the lengths and the call's sizes and not on timing.
  *   - Values that are not finite make results of their own row and later ones of the request NaN or infinite (which,
  *     is not defined), and reach no earlier row and no other request. */

@@ -4,8 +4,8 @@
 //   o_i = scale ( sum_{j <= i} e^{c_i - c_j} (q_i . k_j) v_j + e^{c_i} S^T q_i ),
 //   S'  = e^{c_last} S + sum_j k_j (e^{c_last - c_j} v_j)^T.
 // Four products of a chunk: scores Q K^T (128 x 128), weighted by the decays, times V; Q times the state; K^T times
-// the decayed values. Sums of log decays have 48 bits and only differences leave them, so none of their digits
-// are lost; no factor is above 1, so nothing overflows and what underflows would have underflown.
+// the decayed values. Sums of log decays have 48 bits and only differences leave them. A row's outputs are summed before its factor
+// e^{c_i} comes, in units of 2^-30 (the state as it is read) to 2^30, so that terms from 2^-96 to 2^96 keep their digits.
 //
 // Roundings to bf16, the operands' type: the weighted scores and the state as the outputs read it (outputs are off by 0.0023 of
 // their norm instead of the 0.0017 of their own rounding). The decayed values enter the state's product as
@@ -41,6 +41,8 @@ namespace {
 
 constexpr int kChunk = kLinearChunk, kConvertWarps = 8, kStateWarps = 8, kThreads = 32 * (12 + kConvertWarps + kStateWarps);
 constexpr float kLn2 = 0.6931471805599453f;
+constexpr float kCentre = 30.f;                                 // (see Sums)
+constexpr uint32_t kStateUnit = 0x30803080u;                    // 2^-kCentre, two bf16 numbers
 
 __device__ __forceinline__ void tma_load(uint32_t dst, const CUtensorMap* map, uint32_t bar, int x, int head, int row) {
   asm volatile("cp.async.bulk.tensor.3d.shared::cta.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];"
@@ -265,10 +267,11 @@ struct alignas(16) Sums {
   float d[kChunk];                 // from the start of the row's 32 rows to the row
   float after[kChunk];             // factor from the row to the end of its 32 rows
   float rest[kChunk];              // factor from the row to the end of the chunk
-  // A row's outputs are summed without its factor from the chunk's start, 2^c: scores count 2^(-c), what the row reads of the state
-  // 1, and the sum is scaled. Where c is below -60 a power of two of it, 2^down, is left to the row of q instead.
-  float lift[kChunk];              // down - c
-  float from[kChunk];              // 2^(c - down)
+  // A row's outputs are summed without its factor from the chunk's start, 2^c: what the row reads of the state counts 2^-30 (the state is
+  // stored so), scores 2^(-c - 30), and the sum is scaled. Where c is below -60 a power of two of it, 2^down, is left to the row of q
+  // instead. So no row's sum is off its outputs by more than 2^30 either way: without the 2^-30, scores would count up to 2^60.
+  float lift[kChunk];              // down - c - 30
+  float from[kChunk];              // 2^(c - down + 30)
   float gap[16];                   // [block][earlier block]: from the end of the earlier one to the start of the block
   float base[4];                   // from the start of the chunk to the start of the block
   float factor;                    // of the chunk, less 1 if near
@@ -536,7 +539,7 @@ prompt_kernel(const LinearParams p, const LinearPlan w, const __grid_constant__ 
           rest[i] = exp2f(last.less(c_t));
           const float down = c_t.hi < -60.f ? floorf(c_t.hi) + 60.f : 0.f;
           strong |= down != 0.f;
-          lift[i] = Sum{down, 0.f}.less(c_t);
+          lift[i] = Sum{down - kCentre, 0.f}.less(c_t);
           from[i] = exp2f(-lift[i]);
         }
         // [lane >> 2][lane & 3], lanes below 16
@@ -582,7 +585,7 @@ prompt_kernel(const LinearParams p, const LinearPlan w, const __grid_constant__ 
           tc_fence_after();
           if (sums.strong) {
             // (before the scores take their registers, four loads at a time: one, four, eight at a time 216, 190, 198 us for 16,301 rows)
-            const float down = rintf(sums.base[own] + sums.d[row] + sums.lift[row]);
+            const float down = rintf(sums.base[own] + sums.d[row] + sums.lift[row]) + kCentre;
             if (down < 0.f) {
               const uint32_t f = pack(exp2f(down), exp2f(down));
 #pragma unroll 1
@@ -641,12 +644,15 @@ prompt_kernel(const LinearParams p, const LinearPlan w, const __grid_constant__ 
     if (kRows) {
       const int own = warp & 3, row = own * 32 + lane;
       const uint32_t lanes = (uint32_t)own * 32 << 16;
+      // (a scale whose product with the row's factor could leave fp32 comes after it)
+      const float size = fabsf(p.scale);
+      const bool apart = size > 0x1p60f || (size < 0x1p-60f && size > 0.f);
       each_unit([&](int u, int chunks, int g0, int k) {
         const int h = u % p.H, row0 = entry_of(u).row0;
         for (int c = 0; c < chunks; ++c) {
           const int g = g0 + c, slot = g & 1, first = row0 + c * kChunk;
           wait(sums_full + 8 * slot, g >> 1 & 1);
-          const float f = p.scale * sums_at[slot].from[row];
+          const float f = (apart ? 1.f : p.scale) * sums_at[slot].from[row];
           const int valid = sums_at[slot].valid;
           arrive(sums_free + 8 * slot);
           wait(v_done + 8 * slot, g >> 1 & 1);
@@ -662,6 +668,9 @@ prompt_kernel(const LinearParams p, const LinearPlan w, const __grid_constant__ 
             tc_wait_ld();
 #pragma unroll
             for (int j = 0; j < 16; j += 2) x[j / 2] = pack(Pair(o[j], o[j + 1]) * Pair(f, f));
+            if (apart)
+#pragma unroll
+              for (int j = 0; j < 16; j += 2) x[j / 2] = pack(Pair(o[j], o[j + 1]) * Pair(f, f) * Pair(p.scale, p.scale));
             if (i + 16 < D) tc_ld16(o, tmem + lanes + S::kOut + i + 16);   // (the next ones while these are stored)
             if (bad) {
               // rare: values that are not finite, which were left out; they make what comes after them in their column so
@@ -802,7 +811,8 @@ prompt_kernel(const LinearParams p, const LinearPlan w, const __grid_constant__ 
         for (int i = 0; i < S::kCols; i += 8) {
           const int at = (col0 + i) >> 3;
           sts16(base + S::kS + (at >> 3) * (D * 128) + a * 128 + (((at & 7) ^ (a & 7)) << 4),
-                make_uint4(pack(s[i], s[i + 1]), pack(s[i + 2], s[i + 3]), pack(s[i + 4], s[i + 5]), pack(s[i + 6], s[i + 7])));
+                make_uint4(times(pack(s[i], s[i + 1]), kStateUnit), times(pack(s[i + 2], s[i + 3]), kStateUnit), times(pack(s[i + 4], s[i + 5]), kStateUnit),
+                           times(pack(s[i + 6], s[i + 7]), kStateUnit)));
         }
       fence_async_proxy();
       arrive(state_full);

@@ -799,3 +799,26 @@ def test_a_window_with_trees_as_a_program_runs_it():
         assert_close(host(o[i:i + 1]), want, 2.0 ** -7 * np.abs(want) + 2.0 ** -7 * bound)
         assert_close(host(pool)[int(slots[i])], s, 2.0 ** -18 * size)
     assert int(status) == 0
+
+
+@pytest.mark.parametrize("power", [-28, 20, 28])
+@pytest.mark.parametrize("d", [64, 128])
+def test_prompts_of_large_and_small_values(power, d):
+    """q, k and v of 2^power each, and decays that pass 2^-60 within a chunk: the terms are of 2^(3 power), which the range at the
+    declaration allows, and the tolerances are relative to them."""
+    c = Case(26, [300, 17, 128], 2, 2, d, True, rate=0.8)
+    for t in (c.q, c.k, c.v):
+        t.mul_(2.0 ** power)
+    c.pool.mul_(2.0 ** (2 * power))
+    before = host(c.pool)
+    c.call()
+    check_rows(c, before)
+
+
+@pytest.mark.parametrize("scale", [2.0 ** -110, -2.0 ** -70, 2.0 ** 100])
+def test_scales_of_all_sizes(scale):
+    """The factor that is left for a row's outputs and a small or large scale: neither product may leave fp32."""
+    c = Case(27, [150, 3, 40], 2, 2, 64, True, rate=0.8)
+    before = host(c.pool)
+    c.call(scale=scale)
+    check_rows(c, before, scale)
