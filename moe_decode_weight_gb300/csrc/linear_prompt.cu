@@ -148,9 +148,11 @@ __global__ void __launch_bounds__(1024) plan_kernel(const LinearParams p, const 
     return each;
   };
   for (int b = tid; b < p.B; b += blockDim.x) {
-    int n;
     const int chunks = chunks_of(b);
-    if (chunks) atomicAdd(&at[min(cut(chunks, n), kBuckets - 1)], n);
+    if (!chunks) continue;
+    int n;
+    const int each = cut(chunks, n);                            // (in a statement of its own: it gives n)
+    atomicAdd(&at[min(each, kBuckets - 1)], n);
   }
   __syncthreads();
   // first place of each bucket, the longest first (sums of all buckets above)

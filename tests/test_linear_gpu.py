@@ -822,3 +822,22 @@ def test_scales_of_all_sizes(scale):
     before = host(c.pool)
     c.call(scale=scale)
     check_rows(c, before, scale)
+
+
+# ------------------------------------------------------------------------------ more units than blocks
+
+
+def sms():
+    return torch.cuda.get_device_properties(0).multi_processor_count
+
+
+def test_segments_of_more_units_than_blocks():
+    """Pieces and segments whose number passes the blocks'."""
+    h, lens = 32, [3000, 1100, 40, 300]
+    c = Case(30, lens, 8, h, 64, True, rate=0.02)
+    chunks = [-(-n // 128) for n in lens]
+    segments = chunks[0] // max(4, -(-sum(chunks) * h // sms()))
+    assert segments > 1 and 3 * (segments - 1) * h > sms() and (segments + 3) * h > sms()
+    before = host(c.pool)
+    c.call()
+    check_rows(c, before)
