@@ -375,331 +375,89 @@ prompt_kernel(const LinearParams p, const LinearPlan w, const __grid_constant__ 
     }
   };
 
-  if (warp == 0) {
-    // ---- copies
-    fewer_registers<56>();
-    int asked[3] = {0, 0, 0};                                   // tiles of k, v and q
-    each_unit([&](int u, int chunks, int g0, int k) {
-      const int h = u % p.H, row0 = entry_of(u).row0;
-      for (int c = 0; c < chunks; ++c) {
-        const int g = g0 + c, slot = g & 1, row = row0 + c * kChunk;
-        const uint32_t again = (g >> 1 & 1) ^ 1;
-        auto load = [&](int which, uint32_t to, const CUtensorMap* map, uint32_t full, uint32_t free, uint32_t parity, int head) {
-          wait(free, parity);
-          if (__any_sync(0xffffffffu, *dead)) return;
-          if (lane == 0) {
-            mbar_arrive_tx(full, S::kTile);
+  // The roles; their order is that of the code, whose instructions seven warps a scheduler fetch in turn: of seven orders 189 us (this one) to
+  // 199 for 16,301 rows, 132 to 138 for the 24 requests.
+  if (warp >= 20) {
+    // ---- the state: thread = column of it (lane of tensor memory), half of the rows
+    more_registers<96>();
+    const int quad = warp & 3, a = quad * 32 + lane, col0 = ((warp - 20) >> 2) * S::kCols;
+    const bool holds = quad * 32 < D;
+    const uint32_t lanes = (uint32_t)quad * 32 << 16;
+    float s[S::kCols];
+    auto at_state = [&](float* pool, int64_t first) { return pool + first + ((int64_t)col0 * D + a); };
+    auto load_state = [&](const float* src) {
 #pragma unroll
-            for (int i = 0; i < S::kHalves; ++i) tma_load(to + i * (kChunk * 128), map, full, 64 * i, head, row);
-          }
-          __syncwarp();
-          ++asked[which];
-        };
-        load(1, base + S::kV + slot * S::kTile, &vmap, v_full + 8 * slot, v_free + 8 * slot, again, h);
-        load(0, base + S::kK + slot * S::kTile, &kmap, k_full + 8 * slot, k_free + 8 * slot, again, h / p.share);
-        if (kRows) load(2, base + S::kQ, &qmap, q_full, q_free, (g & 1) ^ 1, h / p.share);
-      }
-    });
-    // every copy arrives before the block ends, also where a wait ran out
-    for (int i = 0; i < 2; ++i) {
-      const int k = (asked[0] + 1 - i) >> 1, v = (asked[1] + 1 - i) >> 1;
-      if (k > 0) mbar_drain_inline(k_full + 8 * i, (k - 1) & 1);
-      if (v > 0) mbar_drain_inline(v_full + 8 * i, (v - 1) & 1);
-    }
-    if (asked[2] > 0) mbar_drain_inline(q_full, (asked[2] - 1) & 1);
-  } else if (warp == 1) {
-    // ---- products for the state
-    fewer_registers<56>();
-    each_unit([&](int u, int chunks, int g0, int k) {
-      for (int c = 0; c < chunks; ++c) {
-        const int g = g0 + c, slot = g & 1;
-        const uint32_t k_at = base + S::kK + slot * S::kTile;
-        wait(k_full + 8 * slot, g >> 1 & 1);
-        if (g > 0) wait(add_read, (g - 1) & 1);                 // the sums of the last chunk are out of their columns
-#pragma unroll 1
-        for (int step = 0; step < S::kSteps; ++step) {
-          const int use = g * S::kSteps + step, at = use & 3;
-          wait(w_full + 8 * at, use >> 2 & 1);
-          tc_fence_after();
-          if (elect_one()) {
-            // the smallest part of the values is summed first
-            const uint32_t kl = operand_low(k_at + step * (S::kStep * 128), kChunk * 128);
+      for (int i = 0; i < S::kCols; ++i) s[i] = src[i * D];
+    };
+    auto store_state = [&](float* dst) {
 #pragma unroll
-            for (int part = 0; part < 3; ++part)
-              tc_mma_tmem(tmem + S::kAdd, tmem + S::kParts + 8 * (3 * at + part), kl, mma_shape(true, true, D), step > 0 || part > 0);
-            tc_commit(w_free + 8 * at);
-            if (step == S::kSteps - 1) {
-              tc_commit(add_full);
-              tc_commit(k_free + 8 * slot);
-            }
-          }
-          __syncwarp();
+      for (int i = 0; i < S::kCols; ++i) dst[i * D] = s[i];
+    };
+    auto set_at = [&](int set, int h) { return at_state(w.states, ((int64_t)set * p.H + h) * D * D); };
+    auto publish = [&](int g) {                                 // the state as the outputs of chunk g read it
+      if (g > 0) wait(state_read, (g - 1) & 1);
+      if (holds)
+#pragma unroll
+        for (int i = 0; i < S::kCols; i += 8) {
+          const int at = (col0 + i) >> 3;
+          sts16(base + S::kS + (at >> 3) * (D * 128) + a * 128 + (((at & 7) ^ (a & 7)) << 4),
+                make_uint4(times(pack(s[i], s[i + 1]), kStateUnit), times(pack(s[i + 2], s[i + 3]), kStateUnit), times(pack(s[i + 4], s[i + 5]), kStateUnit),
+                           times(pack(s[i + 6], s[i + 7]), kStateUnit)));
+        }
+      fence_async_proxy();
+      arrive(state_full);
+    };
+    each_unit([&](int u, int chunks, int g0, int k) {
+#pragma unroll
+      for (int i = 0; i < S::kCols; ++i) s[i] = 0.f;
+      if (holds) {
+        const int h = u % p.H;
+        const LinearEntry e = entry_of(u);
+        const int64_t own = (int64_t)h * D * D;
+        if (e.seg == 0 && (!kRows || e.segs == 1)) {
+          if (e.slot_in >= 0) load_state(at_state(p.s, e.slot_in * p.slot_stride + own));
+          // (the last segment may store to the slot before the first one reads it)
+          if (!kRows) store_state(set_at(e.set, h));
+        } else if (kRows) {
+          load_state(set_at(e.set + e.seg * kLinearPieces, h));
         }
       }
-    });
-    if (elect_one()) tc_commit(end);                            // (by the thread that issued the products)
-    __syncwarp();
-    mbar_drain_inline(end, 0);                                  // nothing is in flight when the columns are given back
-  } else if (warp == 3) {
-    // ---- products for the outputs
-    fewer_registers<56>();
-    if (kRows) {
-      each_unit([&](int u, int chunks, int g0, int k) {
-        for (int c = 0; c < chunks; ++c) {
-          const int g = g0 + c, slot = g & 1;
-          const uint32_t ql = operand_low(base + S::kQ, 16), out = tmem + S::kOut;
-          wait(k_full + 8 * slot, g >> 1 & 1);
-          wait(q_full, g & 1);
-          if (g > 0) wait(o_full + 8 * (slot ^ 1), (g - 1) >> 1 & 1);   // (the weighted scores lie in the scores' columns)
-          tc_fence_after();
-          if (elect_one()) {
-            const uint32_t kl = operand_low(base + S::kK + slot * S::kTile, 16);
-#pragma unroll
-            for (int i = 0; i < D / 16; ++i) {
-              const uint32_t off = ((i >> 2) * (kChunk * 128) + (i & 3) * 32) >> 4;
-              tc_mma(tmem, ql + off, kl + off, mma_shape(true, false, kChunk), i > 0);
-            }
-            tc_commit(s_full);
-            tc_commit(k_free + 8 * slot);
-          }
-          __syncwarp();
-          wait(q_ok, g & 1);
-          wait(state_full, g & 1);
-          wait(o_free, (g & 1) ^ 1);
-          tc_fence_after();
-          if (elect_one()) {
-            const uint32_t sl = operand_low(base + S::kS, 16);
-#pragma unroll
-            for (int i = 0; i < D / 16; ++i)
-              tc_mma(out, ql + (((i >> 2) * (kChunk * 128) + (i & 3) * 32) >> 4), sl + (((i >> 2) * (D * 128) + (i & 3) * 32) >> 4), mma_shape(true, false, D), i > 0);
-            tc_commit(state_read);
-            tc_commit(q_free);
-          }
-          __syncwarp();
-          wait(p_full, g & 1);
-          wait(v_done + 8 * slot, g >> 1 & 1);                  // values that are not finite, and rows behind the last, are out of the tile
-          tc_fence_after();
-          if (elect_one()) {
-            const uint32_t vl = operand_low(base + S::kV + slot * S::kTile, kChunk * 128);
-#pragma unroll
-            for (int i = 0; i < kChunk / 16; ++i)
-              tc_mma_tmem(out, tmem + S::kProb + 8 * i, vl + i * (2048 >> 4), mma_shape(true, true, D), true);
-            tc_commit(o_full + 8 * slot);
-            tc_commit(v_free + 8 * slot);
-          }
-          __syncwarp();
-        }
-      });
-      if (elect_one()) tc_commit(end);                            // (by the thread that issued the products)
-      __syncwarp();
-      mbar_drain_inline(end, 0);
-    }
-  } else if (warp == 2) {
-    // ---- sums of the decays: a lane has four rows
-    fewer_registers<56>();
-    each_unit([&](int u, int chunks, int g0, int k) {
-      const int h = u % p.H;
-      const LinearEntry e = entry_of(u);
-      const bool others = unit_of(k + 1) < units;
-      Sum unit{0.f, 0.f};
-      auto ask = [&](int c, int i) {
-        const int row = c * kChunk + 4 * lane + i;
-        return row < e.rows ? log_decay_of(p, e.row0 + row, h) : 0.f;
-      };
-      float next[4] = {ask(0, 0), ask(0, 1), ask(0, 2), ask(0, 3)};
+      if (kRows) publish(g0);
       for (int c = 0; c < chunks; ++c) {
         const int g = g0 + c;
-        Sum x[4];
+        wait(sums_full + 8 * (g & 1), g >> 1 & 1);
+        const Sums& sums = sums_at[g & 1];
+        const float f = sums.factor;
+        const float keep = sums.near ? 1.f : 0.f;
+        arrive(sums_free + 8 * (g & 1));
+        wait(add_full, g & 1);
+        tc_fence_after();
+        if (holds)
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          float v = next[i];
-          if (v < -200.f) v = -200.f;                           // below every fp32 number, and sums stay finite
-          x[i] = Sum::log2_of_e_to(v);
-        }
-        if (c + 1 < chunks)
-#pragma unroll
-          for (int i = 0; i < 4; ++i) next[i] = ask(c + 1, i);
-#pragma unroll
-        for (int i = 1; i < 4; ++i) x[i] = x[i - 1] + x[i];
-        Sum sum = x[3];
-#pragma unroll
-        for (int m = 1; m < 32; m <<= 1) {
-          const Sum more = Sum{__shfl_up_sync(0xffffffffu, sum.hi, m), __shfl_up_sync(0xffffffffu, sum.lo, m)} + sum;
-          if (lane >= m) sum = more;
-        }
-        auto of_lane = [&](Sum v, int l) { return Sum{__shfl_sync(0xffffffffu, v.hi, l), __shfl_sync(0xffffffffu, v.lo, l)}; };
-        Sum before = of_lane(sum, lane - 1 & 31);
-        if (lane == 0) before = Sum{0.f, 0.f};
-        const Sum last = of_lane(sum, 31), stop = of_lane(sum, lane | 7), start = of_lane(before, lane & ~7);
-        float d[4], after[4], rest[4], from[4], lift[4];
-        bool strong = false;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const Sum c_t = before + x[i];
-          d[i] = c_t.less(start);
-          after[i] = exp2f(stop.less(c_t));
-          rest[i] = exp2f(last.less(c_t));
-          const float down = c_t.hi < -60.f ? floorf(c_t.hi) + 60.f : 0.f;
-          strong |= down != 0.f;
-          lift[i] = Sum{down - kCentre, 0.f}.less(c_t);
-          from[i] = exp2f(-lift[i]);
-        }
-        // [lane >> 2][lane & 3], lanes below 16
-        const float gap = of_lane(before, (lane >> 2 & 3) * 8).less(of_lane(sum, (lane & 3) * 8 + 7));
-        strong = __any_sync(0xffffffffu, strong);
-        const Decay whole(last.natural());
-        const bool more = c + 1 < chunks || others;
-        wait(sums_free + 8 * (g & 1), (g >> 1 & 1) ^ 1);
-        Sums& sums = sums_at[g & 1];
-        *reinterpret_cast<float4*>(&sums.d[4 * lane]) = make_float4(d[0], d[1], d[2], d[3]);
-        *reinterpret_cast<float4*>(&sums.after[4 * lane]) = make_float4(after[0], after[1], after[2], after[3]);
-        *reinterpret_cast<float4*>(&sums.rest[4 * lane]) = make_float4(rest[0], rest[1], rest[2], rest[3]);
-        *reinterpret_cast<float4*>(&sums.from[4 * lane]) = make_float4(from[0], from[1], from[2], from[3]);
-        *reinterpret_cast<float4*>(&sums.lift[4 * lane]) = make_float4(lift[0], lift[1], lift[2], lift[3]);
-        if ((lane & 7) == 0) sums.base[lane >> 3] = start.hi;
-        if (lane < 16) sums.gap[lane] = gap;
-        if (lane == 0) {
-          sums.factor = whole.f;
-          sums.near = whole.near;
-          sums.valid = min(e.rows - c * kChunk, kChunk);
-          sums.more = more;
-          bad_values[g & 3] = 0;                                // (the outputs of the chunk four before were taken before the weights of the one after)
-          sums.strong = strong;
-        }
-        if (!kRows) unit = unit + last;
-        arrive(sums_full + 8 * (g & 1));
-      }
-      if (!kRows && lane == 0) w.logs[(size_t)(e.set + e.seg + 1) * p.H + h] = unit.natural();
-    });
-  } else if (warp >= 4 && warp < 8) {
-    // ---- weights of the scores: thread = row; 32 columns at a time, none above the diagonal
-    more_registers<88>();
-    if (kRows) {
-      const int own = warp & 3, row = own * 32 + lane;
-      const uint32_t lanes = (uint32_t)own * 32 << 16;
-      each_unit([&](int u, int chunks, int g0, int k) {
-        for (int c = 0; c < chunks; ++c) {
-          const int g = g0 + c;
-          wait(sums_full + 8 * (g & 1), g >> 1 & 1);
-          const Sums& sums = sums_at[g & 1];
-          if (!sums.strong) arrive(q_ok);
-          wait(s_full, g & 1);
-          tc_fence_after();
-          if (sums.strong) {
-            // (before the scores take their registers, four loads at a time: one, four, eight at a time 216, 190, 198 us for 16,301 rows)
-            const float down = rintf(sums.base[own] + sums.d[row] + sums.lift[row]) + kCentre;
-            if (down < 0.f) {
-              const uint32_t f = pack(exp2f(down), exp2f(down));
-#pragma unroll 1
-              for (int i = 0; i < D / 8; i += 4) {
-                auto at = [&](int i) { return base + S::kQ + (i >> 3) * (kChunk * 128) + row * 128 + (((i & 7) ^ (row & 7)) << 4); };
-                uint4 x[4];
-#pragma unroll
-                for (int j = 0; j < 4; ++j) x[j] = lds16(at(i + j));
-#pragma unroll
-                for (int j = 0; j < 4; ++j) sts16(at(i + j), make_uint4(times(x[j].x, f), times(x[j].y, f), times(x[j].z, f), times(x[j].w, f)));
-              }
-            }
-            fence_async_proxy();
-            arrive(q_ok);
-          }
-          float v[32];
-          tc_ld32(v, tmem + lanes);
-          const float d = sums.d[row] + sums.lift[row];
-          tc_wait_ld();
-#pragma unroll 1
-          for (int b = 0; b < 4; ++b) {
-            uint32_t packed[16];
-            if (b < own) {
-              const float f = exp2_fast(d + sums.gap[4 * own + b]);
-#pragma unroll
-              for (int i = 0; i < 32; i += 4) {
-                const float4 a = *reinterpret_cast<const float4*>(&sums.after[32 * b + i]);
-                packed[i / 2] = pack(Pair(v[i], v[i + 1]) * (Pair(a.x, a.y) * Pair(f, f)));
-                packed[i / 2 + 1] = pack(Pair(v[i + 2], v[i + 3]) * (Pair(a.z, a.w) * Pair(f, f)));
-              }
-              tc_ld32(v, tmem + lanes + 32 * (b + 1));          // (the next ones while these are stored)
-            } else if (b == own) {
-#pragma unroll
-              for (int i = 0; i < 32; i += 4) {
-                const float4 a = *reinterpret_cast<const float4*>(&sums.d[32 * b + i]);
-                packed[i / 2] = pack(i <= lane ? v[i] * exp2_fast(d - a.x) : 0.f, i + 1 <= lane ? v[i + 1] * exp2_fast(d - a.y) : 0.f);
-                packed[i / 2 + 1] = pack(i + 2 <= lane ? v[i + 2] * exp2_fast(d - a.z) : 0.f, i + 3 <= lane ? v[i + 3] * exp2_fast(d - a.w) : 0.f);
-              }
-            } else {
-#pragma unroll
-              for (int i = 0; i < 16; ++i) packed[i] = 0;
-            }
-            tc_wait_ld();                                       // (before these go to where they came from)
-            tc_st16(tmem + lanes + S::kProb + 16 * b, packed);
-          }
-          tc_wait_st();
-          tc_fence_before();
-          arrive(p_full);
-          arrive(sums_free + 8 * (g & 1));
-        }
-      });
-    }
-  } else if (warp >= 8 && warp < 12) {
-    // ---- outputs: thread = row
-    fewer_registers<56>();
-    if (kRows) {
-      const int own = warp & 3, row = own * 32 + lane;
-      const uint32_t lanes = (uint32_t)own * 32 << 16;
-      // (a scale whose product with the row's factor could leave fp32 comes after it)
-      const float size = fabsf(p.scale);
-      const bool apart = size > 0x1p60f || (size < 0x1p-60f && size > 0.f);
-      each_unit([&](int u, int chunks, int g0, int k) {
-        const int h = u % p.H, row0 = entry_of(u).row0;
-        for (int c = 0; c < chunks; ++c) {
-          const int g = g0 + c, slot = g & 1, first = row0 + c * kChunk;
-          wait(sums_full + 8 * slot, g >> 1 & 1);
-          const float f = (apart ? 1.f : p.scale) * sums_at[slot].from[row];
-          const int valid = sums_at[slot].valid;
-          arrive(sums_free + 8 * slot);
-          wait(v_done + 8 * slot, g >> 1 & 1);
-          wait(o_full + 8 * slot, g >> 1 & 1);
-          tc_fence_after();
-          const bool alive = !*dead, bad = alive && bad_values[g & 3] != 0, store = alive && row < valid;   // (not alive: valid may be anything)
-          __nv_bfloat16* dst = p.out + (int64_t)(first + min(row, valid - 1)) * p.ldo + (int64_t)h * D;
-          float o[16];
-          tc_ld16(o, tmem + lanes + S::kOut);
-#pragma unroll 1
-          for (int i = 0; i < D; i += 16) {
-            uint32_t x[8];
+          for (int i = 0; i < S::kCols; i += 16) {
+            float x[16];
+            tc_ld16(x, tmem + lanes + S::kAdd + col0 + i);
             tc_wait_ld();
 #pragma unroll
-            for (int j = 0; j < 16; j += 2) x[j / 2] = pack(Pair(o[j], o[j + 1]) * Pair(f, f));
-            if (apart)
-#pragma unroll
-              for (int j = 0; j < 16; j += 2) x[j / 2] = pack(Pair(o[j], o[j + 1]) * Pair(f, f) * Pair(p.scale, p.scale));
-            if (i + 16 < D) tc_ld16(o, tmem + lanes + S::kOut + i + 16);   // (the next ones while these are stored)
-            if (bad) {
-              // rare: values that are not finite, which were left out; they make what comes after them in their column so
-#pragma unroll
-              for (int j = 0; j < 16; ++j) {
-                const __nv_bfloat16* v = p.v + (int64_t)first * p.ldv + (int64_t)h * D + i + j;
-#pragma unroll 1
-                for (int before = 0; before <= min(row, valid - 1); ++before)
-                  if (!isfinite(__bfloat162float(v[(int64_t)before * p.ldv]))) x[j / 2] |= j & 1 ? 0x7fff0000u : 0x7fffu;
-              }
-            }
-            if (store) {
-              if (p.wide) {                                     // rows on 32-byte boundaries
-                asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};"
-                             :: "l"(dst + i), "r"(x[0]), "r"(x[1]), "r"(x[2]), "r"(x[3]), "r"(x[4]), "r"(x[5]), "r"(x[6]), "r"(x[7]) : "memory");
-              } else {
-                *reinterpret_cast<uint4*>(dst + i) = make_uint4(x[0], x[1], x[2], x[3]);
-                *reinterpret_cast<uint4*>(dst + i + 8) = make_uint4(x[4], x[5], x[6], x[7]);
-              }
+            for (int j = 0; j < 16; j += 2) {
+              // (keep: 1 where the factor is given less 1; a branch would cost the registers of both ways)
+              const Pair was(s[i + j], s[i + j + 1]), now = fma(was, Pair(keep, keep), fma(was, Pair(f, f), Pair(x[j], x[j + 1])));
+              s[i + j] = now.floats().x;
+              s[i + j + 1] = now.floats().y;
             }
           }
-          tc_fence_before();
-          arrive(o_free);
-        }
-      });
-    }
-  } else if (warp < 20) {
+        tc_fence_before();
+        arrive(add_read);
+        if (kRows && c + 1 < chunks) publish(g + 1);
+      }
+      if (holds && !*dead) {
+        const int h = u % p.H;
+        const LinearEntry e = entry_of(u);
+        if (!kRows) store_state(set_at(e.set + e.seg + 1, h));
+        else if (e.seg == e.segs - 1 && e.slot_out >= 0) store_state(at_state(p.s, e.slot_out * p.slot_stride + (int64_t)h * D * D));
+      }
+    });
+  } else if (warp >= 12 && warp < 20) {
     // ---- values: 16 columns x 16 rows at a time
     fewer_registers<56>();
     const int quad = warp & 3, group = (warp - 12) >> 2, id = threadIdx.x & 127;
@@ -789,86 +547,329 @@ prompt_kernel(const LinearParams p, const LinearPlan w, const __grid_constant__ 
       arrive(v_free + 8 * (g & 1));
       if (__any_sync(0xffffffffu, *dead)) break;                // (more may be anything)
     }
-  } else {
-    // ---- the state: thread = column of it (lane of tensor memory), half of the rows
-    more_registers<96>();
-    const int quad = warp & 3, a = quad * 32 + lane, col0 = ((warp - 20) >> 2) * S::kCols;
-    const bool holds = quad * 32 < D;
-    const uint32_t lanes = (uint32_t)quad * 32 << 16;
-    float s[S::kCols];
-    auto at_state = [&](float* pool, int64_t first) { return pool + first + ((int64_t)col0 * D + a); };
-    auto load_state = [&](const float* src) {
-#pragma unroll
-      for (int i = 0; i < S::kCols; ++i) s[i] = src[i * D];
-    };
-    auto store_state = [&](float* dst) {
-#pragma unroll
-      for (int i = 0; i < S::kCols; ++i) dst[i * D] = s[i];
-    };
-    auto set_at = [&](int set, int h) { return at_state(w.states, ((int64_t)set * p.H + h) * D * D); };
-    auto publish = [&](int g) {                                 // the state as the outputs of chunk g read it
-      if (g > 0) wait(state_read, (g - 1) & 1);
-      if (holds)
-#pragma unroll
-        for (int i = 0; i < S::kCols; i += 8) {
-          const int at = (col0 + i) >> 3;
-          sts16(base + S::kS + (at >> 3) * (D * 128) + a * 128 + (((at & 7) ^ (a & 7)) << 4),
-                make_uint4(times(pack(s[i], s[i + 1]), kStateUnit), times(pack(s[i + 2], s[i + 3]), kStateUnit), times(pack(s[i + 4], s[i + 5]), kStateUnit),
-                           times(pack(s[i + 6], s[i + 7]), kStateUnit)));
-        }
-      fence_async_proxy();
-      arrive(state_full);
-    };
-    each_unit([&](int u, int chunks, int g0, int k) {
-#pragma unroll
-      for (int i = 0; i < S::kCols; ++i) s[i] = 0.f;
-      if (holds) {
-        const int h = u % p.H;
-        const LinearEntry e = entry_of(u);
-        const int64_t own = (int64_t)h * D * D;
-        if (e.seg == 0 && (!kRows || e.segs == 1)) {
-          if (e.slot_in >= 0) load_state(at_state(p.s, e.slot_in * p.slot_stride + own));
-          // (the last segment may store to the slot before the first one reads it)
-          if (!kRows) store_state(set_at(e.set, h));
-        } else if (kRows) {
-          load_state(set_at(e.set + e.seg * kLinearPieces, h));
-        }
-      }
-      if (kRows) publish(g0);
-      for (int c = 0; c < chunks; ++c) {
-        const int g = g0 + c;
-        wait(sums_full + 8 * (g & 1), g >> 1 & 1);
-        const Sums& sums = sums_at[g & 1];
-        const float f = sums.factor;
-        const float keep = sums.near ? 1.f : 0.f;
-        arrive(sums_free + 8 * (g & 1));
-        wait(add_full, g & 1);
-        tc_fence_after();
-        if (holds)
-#pragma unroll
-          for (int i = 0; i < S::kCols; i += 16) {
-            float x[16];
-            tc_ld16(x, tmem + lanes + S::kAdd + col0 + i);
+  } else if (warp >= 8 && warp < 12) {
+    // ---- outputs: thread = row
+    fewer_registers<56>();
+    if (kRows) {
+      const int own = warp & 3, row = own * 32 + lane;
+      const uint32_t lanes = (uint32_t)own * 32 << 16;
+      // (a scale whose product with the row's factor could leave fp32 comes after it)
+      const float size = fabsf(p.scale);
+      const bool apart = size > 0x1p60f || (size < 0x1p-60f && size > 0.f);
+      each_unit([&](int u, int chunks, int g0, int k) {
+        const int h = u % p.H, row0 = entry_of(u).row0;
+        for (int c = 0; c < chunks; ++c) {
+          const int g = g0 + c, slot = g & 1, first = row0 + c * kChunk;
+          wait(sums_full + 8 * slot, g >> 1 & 1);
+          const float f = (apart ? 1.f : p.scale) * sums_at[slot].from[row];
+          const int valid = sums_at[slot].valid;
+          arrive(sums_free + 8 * slot);
+          wait(v_done + 8 * slot, g >> 1 & 1);
+          wait(o_full + 8 * slot, g >> 1 & 1);
+          tc_fence_after();
+          const bool alive = !*dead, bad = alive && bad_values[g & 3] != 0, store = alive && row < valid;   // (not alive: valid may be anything)
+          __nv_bfloat16* dst = p.out + (int64_t)(first + min(row, valid - 1)) * p.ldo + (int64_t)h * D;
+          float o[16];
+          tc_ld16(o, tmem + lanes + S::kOut);
+#pragma unroll 1
+          for (int i = 0; i < D; i += 16) {
+            uint32_t x[8];
             tc_wait_ld();
 #pragma unroll
-            for (int j = 0; j < 16; j += 2) {
-              // (keep: 1 where the factor is given less 1; a branch would cost the registers of both ways)
-              const Pair was(s[i + j], s[i + j + 1]), now = fma(was, Pair(keep, keep), fma(was, Pair(f, f), Pair(x[j], x[j + 1])));
-              s[i + j] = now.floats().x;
-              s[i + j + 1] = now.floats().y;
+            for (int j = 0; j < 16; j += 2) x[j / 2] = pack(Pair(o[j], o[j + 1]) * Pair(f, f));
+            if (apart)
+#pragma unroll
+              for (int j = 0; j < 16; j += 2) x[j / 2] = pack(Pair(o[j], o[j + 1]) * Pair(f, f) * Pair(p.scale, p.scale));
+            if (i + 16 < D) tc_ld16(o, tmem + lanes + S::kOut + i + 16);   // (the next ones while these are stored)
+            if (bad) {
+              // rare: values that are not finite, which were left out; they make what comes after them in their column so
+#pragma unroll
+              for (int j = 0; j < 16; ++j) {
+                const __nv_bfloat16* v = p.v + (int64_t)first * p.ldv + (int64_t)h * D + i + j;
+#pragma unroll 1
+                for (int before = 0; before <= min(row, valid - 1); ++before)
+                  if (!isfinite(__bfloat162float(v[(int64_t)before * p.ldv]))) x[j / 2] |= j & 1 ? 0x7fff0000u : 0x7fffu;
+              }
+            }
+            if (store) {
+              if (p.wide) {                                     // rows on 32-byte boundaries
+                asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};"
+                             :: "l"(dst + i), "r"(x[0]), "r"(x[1]), "r"(x[2]), "r"(x[3]), "r"(x[4]), "r"(x[5]), "r"(x[6]), "r"(x[7]) : "memory");
+              } else {
+                *reinterpret_cast<uint4*>(dst + i) = make_uint4(x[0], x[1], x[2], x[3]);
+                *reinterpret_cast<uint4*>(dst + i + 8) = make_uint4(x[4], x[5], x[6], x[7]);
+              }
             }
           }
-        tc_fence_before();
-        arrive(add_read);
-        if (kRows && c + 1 < chunks) publish(g + 1);
+          tc_fence_before();
+          arrive(o_free);
+        }
+      });
+    }
+  } else if (warp >= 4 && warp < 8) {
+    // ---- weights of the scores: thread = row; 32 columns at a time, none above the diagonal
+    more_registers<88>();
+    if (kRows) {
+      const int own = warp & 3, row = own * 32 + lane;
+      const uint32_t lanes = (uint32_t)own * 32 << 16;
+      each_unit([&](int u, int chunks, int g0, int k) {
+        for (int c = 0; c < chunks; ++c) {
+          const int g = g0 + c;
+          wait(sums_full + 8 * (g & 1), g >> 1 & 1);
+          const Sums& sums = sums_at[g & 1];
+          if (!sums.strong) arrive(q_ok);
+          wait(s_full, g & 1);
+          tc_fence_after();
+          if (sums.strong) {
+            // (before the scores take their registers, four loads at a time: one, four, eight at a time 216, 190, 198 us for 16,301 rows)
+            const float down = rintf(sums.base[own] + sums.d[row] + sums.lift[row]) + kCentre;
+            if (down < 0.f) {
+              const uint32_t f = pack(exp2f(down), exp2f(down));
+#pragma unroll 1
+              for (int i = 0; i < D / 8; i += 4) {
+                auto at = [&](int i) { return base + S::kQ + (i >> 3) * (kChunk * 128) + row * 128 + (((i & 7) ^ (row & 7)) << 4); };
+                uint4 x[4];
+#pragma unroll
+                for (int j = 0; j < 4; ++j) x[j] = lds16(at(i + j));
+#pragma unroll
+                for (int j = 0; j < 4; ++j) sts16(at(i + j), make_uint4(times(x[j].x, f), times(x[j].y, f), times(x[j].z, f), times(x[j].w, f)));
+              }
+            }
+            fence_async_proxy();
+            arrive(q_ok);
+          }
+          float v[32];
+          tc_ld32(v, tmem + lanes);
+          const float d = sums.d[row] + sums.lift[row];
+          tc_wait_ld();
+#pragma unroll 1
+          for (int b = 0; b < 4; ++b) {
+            uint32_t packed[16];
+            if (b < own) {
+              const float f = exp2_fast(d + sums.gap[4 * own + b]);
+#pragma unroll
+              for (int i = 0; i < 32; i += 4) {
+                const float4 a = *reinterpret_cast<const float4*>(&sums.after[32 * b + i]);
+                packed[i / 2] = pack(Pair(v[i], v[i + 1]) * (Pair(a.x, a.y) * Pair(f, f)));
+                packed[i / 2 + 1] = pack(Pair(v[i + 2], v[i + 3]) * (Pair(a.z, a.w) * Pair(f, f)));
+              }
+              tc_ld32(v, tmem + lanes + 32 * (b + 1));          // (the next ones while these are stored)
+            } else if (b == own) {
+#pragma unroll
+              for (int i = 0; i < 32; i += 4) {
+                const float4 a = *reinterpret_cast<const float4*>(&sums.d[32 * b + i]);
+                packed[i / 2] = pack(i <= lane ? v[i] * exp2_fast(d - a.x) : 0.f, i + 1 <= lane ? v[i + 1] * exp2_fast(d - a.y) : 0.f);
+                packed[i / 2 + 1] = pack(i + 2 <= lane ? v[i + 2] * exp2_fast(d - a.z) : 0.f, i + 3 <= lane ? v[i + 3] * exp2_fast(d - a.w) : 0.f);
+              }
+            } else {
+#pragma unroll
+              for (int i = 0; i < 16; ++i) packed[i] = 0;
+            }
+            tc_wait_ld();                                       // (before these go to where they came from)
+            tc_st16(tmem + lanes + S::kProb + 16 * b, packed);
+          }
+          tc_wait_st();
+          tc_fence_before();
+          arrive(p_full);
+          arrive(sums_free + 8 * (g & 1));
+        }
+      });
+    }
+  } else {
+    fewer_registers<56>();                                      // (one instruction, of the four warps together)
+    if (warp == 0) {
+      // ---- copies
+      int asked[3] = {0, 0, 0};                                   // tiles of k, v and q
+      each_unit([&](int u, int chunks, int g0, int k) {
+        const int h = u % p.H, row0 = entry_of(u).row0;
+        for (int c = 0; c < chunks; ++c) {
+          const int g = g0 + c, slot = g & 1, row = row0 + c * kChunk;
+          const uint32_t again = (g >> 1 & 1) ^ 1;
+          auto load = [&](int which, uint32_t to, const CUtensorMap* map, uint32_t full, uint32_t free, uint32_t parity, int head) {
+            wait(free, parity);
+            if (__any_sync(0xffffffffu, *dead)) return;
+            if (lane == 0) {
+              mbar_arrive_tx(full, S::kTile);
+#pragma unroll
+              for (int i = 0; i < S::kHalves; ++i) tma_load(to + i * (kChunk * 128), map, full, 64 * i, head, row);
+            }
+            __syncwarp();
+            ++asked[which];
+          };
+          load(1, base + S::kV + slot * S::kTile, &vmap, v_full + 8 * slot, v_free + 8 * slot, again, h);
+          load(0, base + S::kK + slot * S::kTile, &kmap, k_full + 8 * slot, k_free + 8 * slot, again, h / p.share);
+          if (kRows) load(2, base + S::kQ, &qmap, q_full, q_free, (g & 1) ^ 1, h / p.share);
+        }
+      });
+      // every copy arrives before the block ends, also where a wait ran out
+      for (int i = 0; i < 2; ++i) {
+        const int k = (asked[0] + 1 - i) >> 1, v = (asked[1] + 1 - i) >> 1;
+        if (k > 0) mbar_drain_inline(k_full + 8 * i, (k - 1) & 1);
+        if (v > 0) mbar_drain_inline(v_full + 8 * i, (v - 1) & 1);
       }
-      if (holds && !*dead) {
+      if (asked[2] > 0) mbar_drain_inline(q_full, (asked[2] - 1) & 1);
+    } else if (warp == 1) {
+      // ---- products for the state
+      each_unit([&](int u, int chunks, int g0, int k) {
+        for (int c = 0; c < chunks; ++c) {
+          const int g = g0 + c, slot = g & 1;
+          const uint32_t k_at = base + S::kK + slot * S::kTile;
+          wait(k_full + 8 * slot, g >> 1 & 1);
+          if (g > 0) wait(add_read, (g - 1) & 1);                 // the sums of the last chunk are out of their columns
+#pragma unroll 1
+          for (int step = 0; step < S::kSteps; ++step) {
+            const int use = g * S::kSteps + step, at = use & 3;
+            wait(w_full + 8 * at, use >> 2 & 1);
+            tc_fence_after();
+            if (elect_one()) {
+              // the smallest part of the values is summed first
+              const uint32_t kl = operand_low(k_at + step * (S::kStep * 128), kChunk * 128);
+#pragma unroll
+              for (int part = 0; part < 3; ++part)
+                tc_mma_tmem(tmem + S::kAdd, tmem + S::kParts + 8 * (3 * at + part), kl, mma_shape(true, true, D), step > 0 || part > 0);
+              tc_commit(w_free + 8 * at);
+              if (step == S::kSteps - 1) {
+                tc_commit(add_full);
+                tc_commit(k_free + 8 * slot);
+              }
+            }
+            __syncwarp();
+          }
+        }
+      });
+      if (elect_one()) tc_commit(end);                            // (by the thread that issued the products)
+      __syncwarp();
+      mbar_drain_inline(end, 0);                                  // nothing is in flight when the columns are given back
+    } else if (warp == 3) {
+      // ---- products for the outputs
+      if (kRows) {
+        each_unit([&](int u, int chunks, int g0, int k) {
+          for (int c = 0; c < chunks; ++c) {
+            const int g = g0 + c, slot = g & 1;
+            const uint32_t ql = operand_low(base + S::kQ, 16), out = tmem + S::kOut;
+            wait(k_full + 8 * slot, g >> 1 & 1);
+            wait(q_full, g & 1);
+            if (g > 0) wait(o_full + 8 * (slot ^ 1), (g - 1) >> 1 & 1);   // (the weighted scores lie in the scores' columns)
+            tc_fence_after();
+            if (elect_one()) {
+              const uint32_t kl = operand_low(base + S::kK + slot * S::kTile, 16);
+#pragma unroll
+              for (int i = 0; i < D / 16; ++i) {
+                const uint32_t off = ((i >> 2) * (kChunk * 128) + (i & 3) * 32) >> 4;
+                tc_mma(tmem, ql + off, kl + off, mma_shape(true, false, kChunk), i > 0);
+              }
+              tc_commit(s_full);
+              tc_commit(k_free + 8 * slot);
+            }
+            __syncwarp();
+            wait(q_ok, g & 1);
+            wait(state_full, g & 1);
+            wait(o_free, (g & 1) ^ 1);
+            tc_fence_after();
+            if (elect_one()) {
+              const uint32_t sl = operand_low(base + S::kS, 16);
+#pragma unroll
+              for (int i = 0; i < D / 16; ++i)
+                tc_mma(out, ql + (((i >> 2) * (kChunk * 128) + (i & 3) * 32) >> 4), sl + (((i >> 2) * (D * 128) + (i & 3) * 32) >> 4), mma_shape(true, false, D), i > 0);
+              tc_commit(state_read);
+              tc_commit(q_free);
+            }
+            __syncwarp();
+            wait(p_full, g & 1);
+            wait(v_done + 8 * slot, g >> 1 & 1);                  // values that are not finite, and rows behind the last, are out of the tile
+            tc_fence_after();
+            if (elect_one()) {
+              const uint32_t vl = operand_low(base + S::kV + slot * S::kTile, kChunk * 128);
+#pragma unroll
+              for (int i = 0; i < kChunk / 16; ++i)
+                tc_mma_tmem(out, tmem + S::kProb + 8 * i, vl + i * (2048 >> 4), mma_shape(true, true, D), true);
+              tc_commit(o_full + 8 * slot);
+              tc_commit(v_free + 8 * slot);
+            }
+            __syncwarp();
+          }
+        });
+        if (elect_one()) tc_commit(end);                            // (by the thread that issued the products)
+        __syncwarp();
+        mbar_drain_inline(end, 0);
+      }
+    } else {
+      // ---- sums of the decays: a lane has four rows
+      each_unit([&](int u, int chunks, int g0, int k) {
         const int h = u % p.H;
         const LinearEntry e = entry_of(u);
-        if (!kRows) store_state(set_at(e.set + e.seg + 1, h));
-        else if (e.seg == e.segs - 1 && e.slot_out >= 0) store_state(at_state(p.s, e.slot_out * p.slot_stride + (int64_t)h * D * D));
-      }
-    });
+        const bool others = unit_of(k + 1) < units;
+        Sum unit{0.f, 0.f};
+        auto ask = [&](int c, int i) {
+          const int row = c * kChunk + 4 * lane + i;
+          return row < e.rows ? log_decay_of(p, e.row0 + row, h) : 0.f;
+        };
+        float next[4] = {ask(0, 0), ask(0, 1), ask(0, 2), ask(0, 3)};
+        for (int c = 0; c < chunks; ++c) {
+          const int g = g0 + c;
+          Sum x[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            float v = next[i];
+            if (v < -200.f) v = -200.f;                           // below every fp32 number, and sums stay finite
+            x[i] = Sum::log2_of_e_to(v);
+          }
+          if (c + 1 < chunks)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) next[i] = ask(c + 1, i);
+#pragma unroll
+          for (int i = 1; i < 4; ++i) x[i] = x[i - 1] + x[i];
+          Sum sum = x[3];
+#pragma unroll
+          for (int m = 1; m < 32; m <<= 1) {
+            const Sum more = Sum{__shfl_up_sync(0xffffffffu, sum.hi, m), __shfl_up_sync(0xffffffffu, sum.lo, m)} + sum;
+            if (lane >= m) sum = more;
+          }
+          auto of_lane = [&](Sum v, int l) { return Sum{__shfl_sync(0xffffffffu, v.hi, l), __shfl_sync(0xffffffffu, v.lo, l)}; };
+          Sum before = of_lane(sum, lane - 1 & 31);
+          if (lane == 0) before = Sum{0.f, 0.f};
+          const Sum last = of_lane(sum, 31), stop = of_lane(sum, lane | 7), start = of_lane(before, lane & ~7);
+          float d[4], after[4], rest[4], from[4], lift[4];
+          bool strong = false;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const Sum c_t = before + x[i];
+            d[i] = c_t.less(start);
+            after[i] = exp2f(stop.less(c_t));
+            rest[i] = exp2f(last.less(c_t));
+            const float down = c_t.hi < -60.f ? floorf(c_t.hi) + 60.f : 0.f;
+            strong |= down != 0.f;
+            lift[i] = Sum{down - kCentre, 0.f}.less(c_t);
+            from[i] = exp2f(-lift[i]);
+          }
+          // [lane >> 2][lane & 3], lanes below 16
+          const float gap = of_lane(before, (lane >> 2 & 3) * 8).less(of_lane(sum, (lane & 3) * 8 + 7));
+          strong = __any_sync(0xffffffffu, strong);
+          const Decay whole(last.natural());
+          const bool more = c + 1 < chunks || others;
+          wait(sums_free + 8 * (g & 1), (g >> 1 & 1) ^ 1);
+          Sums& sums = sums_at[g & 1];
+          *reinterpret_cast<float4*>(&sums.d[4 * lane]) = make_float4(d[0], d[1], d[2], d[3]);
+          *reinterpret_cast<float4*>(&sums.after[4 * lane]) = make_float4(after[0], after[1], after[2], after[3]);
+          *reinterpret_cast<float4*>(&sums.rest[4 * lane]) = make_float4(rest[0], rest[1], rest[2], rest[3]);
+          *reinterpret_cast<float4*>(&sums.from[4 * lane]) = make_float4(from[0], from[1], from[2], from[3]);
+          *reinterpret_cast<float4*>(&sums.lift[4 * lane]) = make_float4(lift[0], lift[1], lift[2], lift[3]);
+          if ((lane & 7) == 0) sums.base[lane >> 3] = start.hi;
+          if (lane < 16) sums.gap[lane] = gap;
+          if (lane == 0) {
+            sums.factor = whole.f;
+            sums.near = whole.near;
+            sums.valid = min(e.rows - c * kChunk, kChunk);
+            sums.more = more;
+            bad_values[g & 3] = 0;                                // (the outputs of the chunk four before were taken before the weights of the one after)
+            sums.strong = strong;
+          }
+          if (!kRows) unit = unit + last;
+          arrive(sums_full + 8 * (g & 1));
+        }
+        if (!kRows && lane == 0) w.logs[(size_t)(e.set + e.seg + 1) * p.H + h] = unit.natural();
+      });
+    }
   }
   tc_fence_before();
   __syncthreads();
