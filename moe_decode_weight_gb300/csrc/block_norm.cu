@@ -268,7 +268,7 @@ cudaError_t launch(const NormParams& p0, cudaStream_t s) {
   const int pieces = vectors <= (kVector ? 32 : kMaxThreads) ? 1 : 2;
   p.threads = ((vectors + pieces - 1) / pieces + 31) / 32 * 32;
   const int rows = p.threads == 32 ? 4 : 1;
-  const unsigned blocks = (unsigned)((p.T + rows - 1) / rows);
+  const unsigned blocks = ((unsigned)p.T + rows - 1) / rows;
   const int threads = p.threads * rows;
   if (pieces == 1) norm_kernel<T, Y, S, 1, kVector><<<blocks, threads, 0, s>>>(p);
   else norm_kernel<T, Y, S, 2, kVector><<<blocks, threads, 0, s>>>(p);

@@ -841,3 +841,11 @@ def test_segments_of_more_units_than_blocks():
     before = host(c.pool)
     c.call()
     check_rows(c, before)
+
+
+@pytest.mark.parametrize("t", [(1 << 31) - 1, (1 << 31) - 3])
+def test_norm_of_as_many_rows_as_an_int32_holds(t):
+    y = torch.empty((t, 1), dtype=BF, device="cuda").normal_()
+    out = torch.empty_like(y)
+    api.mdw_block_norm(y, out)
+    assert torch.equal(y, out)
