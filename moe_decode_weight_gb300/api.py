@@ -586,7 +586,8 @@ def mdw_block_norm(y: torch.Tensor, sum: torch.Tensor | None, post_weight=None, 
                    gate_kind: str = "none", residual=None, pre_weight=None, x=None, branch_scale: float = 1.0,
                    residual_scale: float = 1.0, eps: float = 1e-6, stream=None) -> None:
     """Norm after a sub-layer, gate, scaled residual and norm before the next (see the C declaration): y [T, W];
-    sum = residual_scale * residual + branch_scale * act(gate) * norm(y) and x = norm(sum) * pre_weight, both [T, W];
+    sum = residual_scale * residual + branch_scale * act(gate) * norm(y) and x = norm(sum) * pre_weight, both [T, W], x of the
+    sum as rounded to sum's type (without sum to residual's, without either to float32);
     post_weight [group] (W by default), gate [T, W] or [W], gate_kind "none", "mul", "sigmoid" or "silu"."""
     if gate_kind not in GATES:
         raise MdwError("mdw_block_norm", 1, f"gate_kind {gate_kind!r} is none of {sorted(GATES)}")

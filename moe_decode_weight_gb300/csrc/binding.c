@@ -439,7 +439,8 @@ static PyObject* b_block_norm(PyObject* self, PyObject* const* a, Py_ssize_t n) 
     refuse(&c, MDW_ERR_FORMAT_MISMATCH, "the tensors", "are of two 16-bit types");
     return NULL;
   }
-  const int sums = sum.type ? sum.type : res.type ? res.type : type;
+  /* (a sum that nothing stores is not rounded before x) */
+  const int sums = sum.type ? sum.type : res.type ? res.type : x.type ? T_F32 : type;
   if (res.type && res.type != sums) {
     refuse(&c, MDW_ERR_FORMAT_MISMATCH, "residual", "has another type than sum");
     return NULL;

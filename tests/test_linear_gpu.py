@@ -849,3 +849,16 @@ def test_norm_of_as_many_rows_as_an_int32_holds(t):
     out = torch.empty_like(y)
     api.mdw_block_norm(y, out)
     assert torch.equal(y, out)
+
+
+@pytest.mark.parametrize("y", [BF, F32])
+@pytest.mark.parametrize("w", [640, 1003])
+def test_norm_of_a_sum_that_is_not_stored(y, w):
+    """Without sum and residual nothing is rounded before x."""
+    a = norm_case(8, 5, w, BF, y, None, True, "sigmoid", True, None, True)
+    a["sum"] = None
+    api.mdw_block_norm(**a)
+    s, _ = OL.block_sum(host(a["y"]), host(a["post_weight"]), None, host(a["gate"]), "sigmoid")
+    x = OL.rmsnorm(s, host(a["pre_weight"]), 1e-6)
+    # s is off by 128 u of its magnitude, its root mean square by as much, and x is rounded once
+    assert_close(host(a["x"]), x, (half_step(BF) + 256 * U) * np.abs(x) + 2.0 ** -24)
