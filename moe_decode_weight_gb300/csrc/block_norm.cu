@@ -127,11 +127,19 @@ template <typename T, bool kAligned> __device__ __forceinline__ void store_row(v
   }
 }
 
-// Off by a few 2^-22, and 0 below 2^-126: the exponential and the reciprocal take one instruction each (with the exact ones the
-// gated norm of 4,099 rows of 32 heads took 39 us).
-__device__ __forceinline__ float sigmoid(float x) {
+// 0 below 2^-126. The exponential and the reciprocal take one instruction each (with the library's the gated norm of 4,099 rows of 32
+// heads took 39 us) and are off by 2^-22 and 2^-23; the rounding of x log2(e) adds |x| 2^-25, 2^-18.5 at -80, to what is stored in 16 bits. Sums
+// in fp32 (kFine) take what it left along: e^(-x) = 2^h e^(rest), rest below 2^-17.
+template <bool kFine> __device__ __forceinline__ float sigmoid(float x) {
+  constexpr float kLog2e = 1.44269502162933349609375f, kLn2 = 0.6931471805599453f;   // log2(e) = this + 1.9259629...e-8
   float e, r;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(x * -1.4426950408889634f));
+  if (kFine) {                                                  // (so that the exponential is finite; the sigmoid is 0 or 1 there; NaN stays)
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(x) : "f"(x), "f"(-88.f));
+    asm("min.NaN.f32 %0, %1, %2;" : "=f"(x) : "f"(x), "f"(88.f));
+  }
+  const float h = x * -kLog2e;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(h));
+  if (kFine) e = fmaf(e, fmaf(fmaf(x, -kLog2e, -h), kLn2, x * (-1.92596303339e-8f * kLn2)), e);
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.f + e));
   return r;
 }
@@ -222,7 +230,7 @@ __global__ void __maxnreg__(registers_of(kVector, kPieces)) norm_kernel(const No
       gate[i].get(g);
       if (p.gate_kind != MDW_GATE_MUL)                          // (first: times the gate alone could overflow)
 #pragma unroll
-        for (int j = 0; j < 8; ++j) z[i][j] *= sigmoid(g[j]);
+        for (int j = 0; j < 8; ++j) z[i][j] *= sigmoid<sizeof(S) == 4>(g[j]);
       if (p.gate_kind != MDW_GATE_SIGMOID)
 #pragma unroll
         for (int j = 0; j < 8; ++j) z[i][j] *= g[j];

@@ -862,3 +862,15 @@ def test_norm_of_a_sum_that_is_not_stored(y, w):
     x = OL.rmsnorm(s, host(a["pre_weight"]), 1e-6)
     # s is off by 128 u of its magnitude, its root mean square by as much, and x is rounded once
     assert_close(host(a["x"]), x, (half_step(BF) + 256 * U) * np.abs(x) + 2.0 ** -24)
+
+
+@pytest.mark.parametrize("kind", ["sigmoid", "silu"])
+def test_norm_gates_far_below_zero_in_an_fp32_sum(kind):
+    """In units of u = 2^-24: the exponential 4, what is left of its argument 1, one plus it 1, the reciprocal 2, the products with y, the gate
+    and the scale 3, the store 1: 12."""
+    n = 4096
+    a = dict(y=norm_case(9, 2, n, F32)["y"], sum=torch.empty((2, n), device="cuda"), gate_kind=kind,
+             gate=torch.linspace(-80, 10, n, device="cuda").to(BF).expand(2, n).contiguous())
+    api.mdw_block_norm(**a, branch_scale=0.7)
+    s, _ = OL.block_sum(host(a["y"]), None, None, host(a["gate"]), kind, branch_scale=np.float64(np.float32(0.7)))
+    assert_close(host(a["sum"]), s, 12 * U * np.abs(s))
