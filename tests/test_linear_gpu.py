@@ -874,3 +874,132 @@ def test_norm_gates_far_below_zero_in_an_fp32_sum(kind):
     api.mdw_block_norm(**a, branch_scale=0.7)
     s, _ = OL.block_sum(host(a["y"]), None, None, host(a["gate"]), kind, branch_scale=np.float64(np.float32(0.7)))
     assert_close(host(a["sum"]), s, 12 * U * np.abs(s))
+
+
+# ------------------------------------------------------------------------------ each kernel at its own precision
+
+
+def check_precision(c, pool0, rows_of_norm=64):
+    """Outputs by the kernel that a call takes (see the end of the first docstring):
+    * rows one by one (a bound below 12; requests of up to 16 rows of a call with longer ones): fp32. The sum over a column of the state has at most
+      8 additions of a thread, 2 between lanes and 8 between warps, and the scale: 20 u `bound`, beside what the state itself is off by.
+    * a bound of 12 to 16: scores and state as two bf16 numbers, off by 2^-7 (what the first one leaves) times 2^-8: 2^-15, doubled for the
+      exponentials and sums.
+    * chunks: an output's own rounding, and one of its terms to bf16 each. A rounding is uniform within half a step, so its root mean square is at
+      most 2^-8 / sqrt(3) of the value; terms and output are independent of each other: sqrt(2) of that, 0.0032, of the norm. 0.004, of the
+      norm over some rows of a head, among which those that start a segment."""
+    out, scale = host(c.out), c.d ** -0.5
+    for b in range(c.b):
+        at, q, k, v, g = c.rows(b)
+        if not len(q):
+            continue
+        o, s, bound, size, chain = OL.linear_attention(c.before(b, pool0), q, k, v, g, scale)
+        if len(q) > 16:
+            for h in range(c.h):
+                for first in range(0, max(len(q) - rows_of_norm + 1, 1), rows_of_norm):
+                    part = slice(first, first + rows_of_norm)
+                    norm = np.linalg.norm(o[part, h])
+                    assert np.linalg.norm(out[at][part, h] - o[part, h]) <= 0.004 * norm, (b, h, first)
+            continue
+        tol = 2.0 ** -14 * bound if 12 <= c.new <= 16 else 20 * U * bound + scale * 4 * U * np.einsum("nhi,hij->nhj", np.repeat(np.abs(q), c.h // c.hk, 1), chain)
+        assert_close(out[at], o, half_step(BF) * np.abs(o) + 1.01 * tol, b)
+
+
+@pytest.mark.parametrize("lens", [[1], [1, 5, 11, 8], [16, 3, 12, 0, 9], [300, 16, 5, 17], [1025, 3], [1500, 0, 1200]], ids=str)
+@pytest.mark.parametrize("h,d,rate", [(2, 64, 0.3), (2, 128, 0.02), (1, 128, 2.0)])
+def test_precision_of_each_kernel(lens, h, d, rate):
+    c = Case(sum(lens) + 1, lens, 1, h, d, True, rate=rate)
+    before = host(c.pool)
+    c.call()
+    check_precision(c, before)
+
+
+@pytest.mark.parametrize("lens", [[4, 3, 2, 5], [140, 3, 200, 150], [14, 3, 12, 5]], ids=str)
+@pytest.mark.parametrize("fault,skip", [("out", (0, 2)), ("in", (0,)), ("high", (1,)), ("low", (2,)), ("rows", (3,))])
+def test_a_bad_request_changes_nothing_of_the_others(lens, fault, skip):
+    """The others' rows and states are those of a call without the fault, bit for bit; a skipped one's rows and slot stay."""
+    c, clean = Case(28, lens, 2, 2, 64, inplace=False), Case(28, lens, 2, 2, 64, inplace=False)
+    start, to = c.start.copy(), list(c.slot_out)
+    if fault == "out":
+        c.slot_out[2] = c.slot_out[0]
+    elif fault == "in":
+        c.slot_in[0] = c.slot_out[2]
+    elif fault == "high":
+        c.slot_in[1] = len(c.pool)
+    elif fault == "low":
+        c.slot_out[2] = -2
+    else:
+        start[-1] = c.t + 1
+    before = c.pool.clone()
+    c.call(start=i32(start.tolist()))
+    clean.call()
+    assert int(c.status) == 7 and int(clean.status) == 0
+    want, pool = clean.out.clone(), clean.pool.clone()
+    for b in skip:
+        want[int(c.start[b]):int(c.start[b + 1])] = 7
+        pool[to[b]] = before[to[b]]
+    assert torch.equal(c.out, want) and torch.equal(c.pool, pool)
+
+
+def bits(t):
+    return t.contiguous().view(torch.int16 if t.element_size() == 2 else torch.int32)
+
+
+def alone(c, b, run):
+    """The outputs and the pool of a call with request b only, whose bound, rows and state are the same."""
+    at = slice(int(c.start[b]), int(c.start[b + 1]))
+    one = Case(0, [at.stop - at.start], c.hk, c.h, c.d, tail=0)
+    one.q, one.k, one.v, one.g = c.q[at], c.k[at], c.v[at], c.g[at]
+    one.pool, one.slot_in, one.slot_out, one.new = c.pool.clone(), [c.slot_in[b]], [c.slot_out[b]], c.new
+    run(one)
+    return one.out, one.pool
+
+
+@pytest.mark.parametrize("h,d,lens", [(64, 64, [130, 17, 300, 1, 256, 40, 129]), (40, 128, [150, 260, 20, 0, 129, 33, 128])], ids=str)
+@pytest.mark.parametrize("odd", [False, True])
+def test_prompts_of_more_units_than_blocks(h, d, lens, odd):
+    """Blocks of the chunk kernel that take several units: as each request alone gives them, values that are not finite among them."""
+    c = Case(29, lens, h // 2, h, d, True, fresh=(2,), inplace=False, lead=1)
+    assert sum(n > 16 for n in lens) * h > sms()
+    if odd:
+        c.v[int(c.start[0]) + 60, 3, 7] = float("inf")
+        c.k[int(c.start[1]) + 2, 2, 1] = float("nan")
+        c.v[int(c.start[5]) + 1, :, 9] = float("nan")
+    before = c.pool.clone()
+    whole = Case(29, lens, h // 2, h, d, True, fresh=(2,), inplace=False, lead=1)
+    whole.q, whole.k, whole.v, whole.pool = c.q, c.k, c.v, c.pool.clone()
+    whole.call()
+    for b, n in enumerate(lens):
+        if n:
+            out, pool = alone(c, b, lambda one: one.call(new=c.new))
+            assert torch.equal(bits(whole.out[int(c.start[b]):int(c.start[b + 1])]), bits(out)), b
+            assert torch.equal(bits(whole.pool[c.slot_out[b]]), bits(pool[c.slot_out[b]])), b
+    if not odd:
+        check_rows(whole, host(before))
+        check_precision(whole, host(before))
+
+
+@pytest.mark.parametrize("h,d,most,each", [(32, 128, 16, 2), (64, 64, 16, 4), (32, 128, 32, 2), (64, 64, 32, 4), (20, 128, 64, 1), (32, 64, 64, 2)])
+def test_trees_of_more_units_than_blocks(h, d, most, each):
+    """The same for each number of tiles of the trees' kernel, `each` of whose blocks fit an SM."""
+    rng = np.random.default_rng(most + d)
+    b = each * sms() // h + 3
+    lens = [most] + [int(rng.integers(0, most + 1)) for _ in range(b - 1)]
+    assert b * h > each * sms()
+    c = Case(31, lens, h // 2, h, d, True, fresh=(3,), rate=1.0, lead=1)
+    masks = [[1] * c.start[0]] + [random_masks(rng, n) for n in lens]
+    for i in (1, b // 2, b - 1):
+        if lens[i]:
+            c.v[int(c.start[i]) + lens[i] // 2, ::3, 5] = float("inf")
+    before = c.pool.clone()
+    c.tree([m for r in masks for m in r] + [0] * 3)
+    assert torch.equal(c.pool, before) and int(c.status) == 0
+    assert (c.out[:1] == 7).all() and (c.out[int(c.start[-1]):] == 7).all()
+    for i, n in enumerate(lens):
+        if n:
+            out, _ = alone(c, i, lambda one: one.tree(masks[i + 1], new=most))
+            assert torch.equal(bits(c.out[int(c.start[i]):int(c.start[i + 1])]), bits(out)), i
+    rows, q, k, v, g = c.rows(0)
+    few = min(lens[0], 16)
+    o, bound = OL.tree_attention(c.before(0, host(before)), q[:few], k[:few], v[:few], g[:few], masks[1][:few], d ** -0.5)
+    assert_close(host(c.out)[rows][:few], o, half_step(BF) * np.abs(o) + 2.0 ** -14 * bound)
