@@ -498,7 +498,11 @@ mdw_status mdw_tree_attention(const mdw_kv_cache* cache, int32_t B, int32_t T, i
  *     (MDW_ERR_TIMEOUT), outputs and stored states of the call's requests of more than 16 rows are not defined.
  *   - Range of requests of more than 16 rows: sums of the magnitudes |q_a k_a|, |q_a k_a v| and |q_a S| stay below 2^96; what such sums
  *     have below 2^-96 may be lost. (Shorter ones, trees: what fp32 holds.)
- *   - States and sums are fp32, in a fixed order, which depends on the lengths and the call's sizes and not on timing.
+ *   - States are fp32, and so are the sums, in a fixed order, which depends on the lengths and the call's sizes and not on timing. What the
+ *     outputs read of a state and their scores beside the values are fp32 for requests of up to 16 rows, but two bf16 numbers each, off by
+ *     2^-15, for trees and where max_new is 12 to 16; requests of more than 16 rows round both to bf16, which puts
+ *     outputs off by 0.0024 of their norm instead of the 0.0017 of their own rounding. So the same rows' outputs differ in
+ *     their last bits with max_new.
  *   - Values that are not finite make results of their own row and later ones of the request NaN or infinite (which,
  *     is not defined), and reach no earlier row and no other request. */
 

@@ -149,7 +149,8 @@ template <bool kFine> __device__ __forceinline__ float sigmoid(float x) {
 // piece each (16,381 rows of 2,563 elements: two pieces 195 us, one 144).
 constexpr int kMaxThreads = 1024;
 // Registers: 64, or 56 for one piece off 16-byte boundaries, so that one more block fits an SM (fp32 y, f16 residual: 4,617 rows of 4,374 elements 105
-// and 75 us, 16,381 of 2,563 204 and 173, 7,000 of 6,001 214 and 222; with 48 they spill: 77, 179, 235).
+// and 75 us, 16,381 of 2,563 204 and 173, 7,000 of 6,001 214 and 222; with 48: 77, 179, 235). 56 spill 60 bytes a thread where y and the sum are
+// fp32, and two pieces off boundaries, above 8,192 elements, spill 340 to 720.
 constexpr int registers_of(bool vector, int pieces) { return vector || pieces == 2 ? 64 : 56; }
 
 // T: the 16-bit type; Y, S: types of y and of residual and sum. kPieces of eight elements a thread. kVector: all rows on 16-byte

@@ -27,12 +27,14 @@ struct LinearParams {
   int wide;                        // rows of out lie on 32-byte boundaries
 };
 
-// Rows of a chunk; least chunks of a segment, and its pieces in the first pass. Requests of up to kLinearShort rows take them one by one: rows
-// then cost 0.5 us (3 requests of 32 heads) to 5 us (48) each, and chunks of 128 rows as much for one row as for all: the two are even at
-// 20 rows of 3 requests (both 22 us), 16 of 8 (30 us), 11 of 48 (87 us; 16 rows one by one 110). A call of few rows is one launch then.
+// Rows of a chunk; least chunks of a segment, and its pieces in the first pass. Requests of up to kLinearShort rows take them one by one (in calls
+// with longer ones; else see below): rows then cost 0.5 us (3 requests of 32 heads) to 5 us (48) each, and chunks of 128 rows as much for one row
+// as for all: the two are even at 20 rows of 3 requests (both 22 us), 16 of 8 (30 us), 11 of 48 (86 us; 16 rows one by one 110). A call of
+// few rows is one launch then.
 constexpr int kLinearChunk = 128, kLinearShort = 16, kLinearSegment = 4, kLinearPieces = 3;
 // Calls of at most 16 rows a request, and possibly of so many, take the products on mma.sync instead of row by row: whatever the rows, 48 requests
-// of 32 heads 67 to 71 us (row by row 4 rows 52, 8 67, 12 87, 16 109), 10 26 (20, 26, 30, 35), one of 20 heads 13.5 (10, 11, 13, 15.5).
+// of 32 heads 69 to 71 us (row by row 4 rows 54, 8 69, 12 89, 16 110), 10 26 (20, 25, 30, 34), 3 14 (13, 16, 18, 20), one of 20 heads 13.5 (9,
+// 11, 13, 15.5).
 // max_new is a bound only, and where the rows are fewer, row by row is as fast or faster; so not from 9 on.
 constexpr int kLinearWindow = 12;
 

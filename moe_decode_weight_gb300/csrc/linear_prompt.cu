@@ -4,10 +4,11 @@
 //   o_i = scale ( sum_{j <= i} e^{c_i - c_j} (q_i . k_j) v_j + e^{c_i} S^T q_i ),
 //   S'  = e^{c_last} S + sum_j k_j (e^{c_last - c_j} v_j)^T.
 // Four products of a chunk: scores Q K^T (128 x 128), weighted by the decays, times V; Q times the state; K^T times
-// the decayed values. Sums of log decays have 48 bits and only differences leave them. A row's outputs are summed before its factor
+// the decayed values. Sums of log decays have 48 bits and only differences leave them; those within 32 rows are of fp32 sums from the start of
+// the 32, so that weights are off by less than their rounding to bf16 even where each row's decay is e^-200. A row's outputs are summed before its factor
 // e^{c_i} comes, in units of 2^-30 (the state as it is read) to 2^30, so that terms from 2^-96 to 2^96 keep their digits.
 //
-// Roundings to bf16, the operands' type: the weighted scores and the state as the outputs read it (outputs are off by 0.0023 of
+// Roundings to bf16, the operands' type: the weighted scores and the state as the outputs read it (outputs are off by 0.0024 of
 // their norm instead of the 0.0017 of their own rounding). The decayed values enter the state's product as
 // three bf16 numbers that hold 24 bits together, so a state carries the error of fp32 sums only; it is kept in registers.
 //
@@ -16,11 +17,11 @@
 // segment then starts from the sums before it. plan_kernel lays the units out, longest first, from the lengths on the
 // device; block i takes units i, 2 G - 1 - i, 2 G + i, ... of G blocks, one on each SM.
 //
-// What bounds it: neither memory (42 to 50 % of the copy rate) nor the matrix unit (33 %) nor the issue of instructions (39 %), but
+// What bounds it: neither memory (50 to 58 % of its peak) nor the matrix unit (41 to 44 %) nor the issue of instructions (45 to 52 %), but
 // the chain of a chunk: the outputs of the last one read the state, the state takes its products and is rounded, the tile of q is
 // free and filled again, scores, weights, products with the values. It takes 6,000 to 7,000 cycles and only parts of two chunks overlap;
-// heads whose decays pass 2^-60 within a chunk wait for q to be scaled too. Measured: 16,301 rows of 32 heads from an empty state 190 us
-// (of them the first pass 45, its sums 9), 24 requests of up to 2,100 rows of 20 heads 131 us. Roles of a block:
+// heads whose decays pass 2^-60 within a chunk wait for q to be scaled too. Measured: 16,301 rows of 32 heads from an empty state 189 us
+// (of them the first pass 46, its sums 10), 24 requests of up to 2,100 rows of 20 heads 131 us. Roles of a block:
 //   warp 0       requests the tiles of q, k and v by TMA (swizzled, 128 rows x 128 bytes)
 //   warp 1       issues the products for the state
 //   warp 2       sums the decays of the next chunk
@@ -137,9 +138,10 @@ __global__ void __launch_bounds__(1024) plan_kernel(const LinearParams p, const 
   if (mine) atomicAdd(&total, mine);
   __syncthreads();
   // A segment is at least an SM's share of all work, and four chunks: its start costs about one. (32 heads, one request with and without
-  // segments: 1,000 rows 45 and 47 us, 2,000 54 and 77, 4,000 79 and 135, 16,301 218 and 507; four of 1,000 rows 58 and 53. At least eight
-  // chunks: 2,000 rows 64, four of 1,000 rows 53.) The first pass has all segments but each request's last, in three pieces each, so that it
-  // fills the SMs too (16,301 rows: 4 segments, so 96 units of 32 chunks there or 288 of about 11 on 152 SMs: 90 and 45 us).
+  // segments: 1,000 rows 44 and 43 us, 1,500 47 and 56, 2,000 52 and 71, 4,000 73 and 126, 16,301 194 and 469; four of 1,000 rows 54
+  // and 48, of 2,000 84 and 79, of 4,000 145 and 138: they fill the SMs without. At least eight chunks: 1,500 rows 59, 2,000 61, four of 1,000
+  // rows 50; at least three: 46, 52, 54.) The first pass has all segments but each request's last, in three pieces each, so that it
+  // fills the SMs too (16,301 rows: 4 segments, so 96 units of 32 chunks there or 288 of about 11 on 152 SMs: 202 us with one piece, 194).
   const long long share = max((long long)kLinearSegment, ((long long)total * p.H + blocks - 1) / blocks);
   auto cut = [&](int chunks, int& n) {                          // segments and the chunks of one
     n = (int)max(1ll, chunks / share);

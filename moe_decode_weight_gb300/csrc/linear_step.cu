@@ -51,7 +51,7 @@ constexpr int kRows = 8;                                        // rows whose el
 
 // One block: request blockIdx.z, value head blockIdx.y, kCols of the columns. kOut: outputs of all rows; else the rows
 // whose bits are set change the state only.
-// Blocks of an SM, 64 of 128 columns: three with 80 registers (two or four: 59 and 52 us for the 61 requests instead of 50).
+// Blocks of an SM, 64 of 128 columns: three with 80 registers, 12 bytes of them spilled (two or four: 59 and 52 us for the 61 requests instead of 50).
 template <int D, int kCols, bool kOut>
 __global__ void __launch_bounds__(kThreads, D * kCols > 64 * 64 ? 3 : 4) step_kernel(const LinearParams p) {
   constexpr int kLanes = kCols / 4, kGroups = kThreads / kLanes, kPer = D / kGroups;   // lanes of a row, rows at once, rows of a thread

@@ -10,7 +10,7 @@
 // anything else: a thread's loads are whole operands of m16n8k16 products (four columns of it are four tiles' column, which
 // only changes the order of the columns), turned into two bf16 numbers that hold 16 bits together. The scores and weights are
 // products of the same kind, the weights as two bf16 numbers too. A block asks for its next unit's state as soon as it has used up the
-// one before. Measured: 48 requests of up to 16 nodes and 32 heads 32 us, half of the copy rate; 12 requests of 64 nodes and 64 heads of 64 25 us,
+// one before. Measured: 48 requests of up to 16 nodes and 32 heads 31 to 33 us, half of the copy rate; 12 requests of 64 nodes and 64 heads of 64 25 us,
 // where the split states, two products each, and the barriers between the steps of a unit bound it (16 warps an SM).
 // Windows of 16 rows, the same 48 requests: 71 us; the products for the state come between its use and the next one's loads.
 #include <cmath>
@@ -48,7 +48,7 @@ __device__ __forceinline__ void ldmatrix_trans(uint32_t (&r)[4], uint32_t at) {
   asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];" : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(at));
 }
 
-// kTiles tiles of 16 nodes.
+// kTiles tiles of 16 nodes. 128 registers spill 456 bytes a thread with two tiles of 128, 256 where a state of 128 is stored, 192 with four tiles of 64.
 template <int D, int kTiles>
 struct Shape {
   static constexpr int kWarps = D == 128 || kTiles == 4 ? 8 : 4, kThreads = 32 * kWarps, kNodes = 16 * kTiles;
